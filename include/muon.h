@@ -420,6 +420,99 @@ int muon_spectral_diag_timed(const void* A, int dtype, int m, int n, long long b
                              float* sigma_max, float* sigma_min, void* workspace, size_t workspace_bytes,
                              void* stream, void** events, int nevents);
 
+/* An operand of a sequence operator, [batch][tokens][heads or groups][width]:
+ * token t of sequence b, head h starts at element b sb + t st + h sh of p
+ * (strides in elements, >= 0; the width elements themselves are adjacent), so
+ * a column range of a wider tensor needs no copy. */
+typedef struct {
+  const void* p;
+  long long sb, st, sh;
+} muon_seq;
+
+/* The gated scan: the linear recurrence between the two projections that "Muon
+ * Meets Mamba" trains (Mamba-2 130M: 24 heads of P = 64, N = 128, one group),
+ * and MuonSSM's memory update with undisturbed injections.  For every sequence
+ * and head, t = 1..tokens:
+ *   S_t = e^{g_t} S_{t-1} + b_t v_t k_t^T   (P x N, float32),   y_t = S_t q_t
+ *   v          [batch][tokens][heads][P]   of dtype (MUON_BF16 or MUON_F32)
+ *   k, q       [batch][tokens][groups][N]  of dtype; head h reads group
+ *              h / (heads / groups), groups divides heads
+ *   log_decay  g: [batch][tokens][heads] float32 (sh: stride of the heads).
+ *              -inf starts a new sequence at t: nothing before it is read
+ *              after it (values below -10000 are taken as that)
+ *   gate       b, as log_decay; gate.p NULL: 1
+ *   S0         NULL (zero), or [batch][heads][P][N] float32, contiguous
+ * Supported: N <= 128 (else MUON_EUNSUPPORTED), any P; batch or tokens may be
+ * 0.  v, k, q and the states must be finite (a NaN or Inf reaches the whole
+ * chunk of 64 tokens that holds it, earlier tokens included).  Rows that are
+ * 16-byte aligned and a multiple of 16 bytes wide take vectorised loads.
+ * States, sums and gates are float32 (decays summed in float64); with
+ * MUON_BF16 the products that give y and the gradients of v, k, q have
+ * bfloat16 operands and float32 sums, those that give states and gate
+ * gradients carry float32 accuracy.  Results are deterministic and do not
+ * depend on the device. */
+typedef struct {
+  int batch, tokens, heads, groups, P, N;
+  int dtype;
+  muon_seq v, k, q;
+  muon_seq log_decay, gate;
+  const float* S0;
+} muon_scan_args;
+
+/* Bytes of device workspace (0 for invalid or unsupported sizes; reads only
+ * the sizes and dtype). */
+size_t muon_gated_scan_workspace_size(const muon_scan_args* args);
+/* Y: [batch][tokens][heads][P] of dtype, contiguous.  S_out: NULL, or
+ * [batch][heads][P][N] float32 receiving the last state (S0, or zero, when
+ * tokens is 0).  Outputs and the workspace (16-byte aligned) must not overlap
+ * inputs or each other. */
+int muon_gated_scan(const muon_scan_args* args, void* Y, float* S_out, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* Gradients of a loss through muon_gated_scan: args as in the forward call
+ * (nothing that it computed is needed), dY the gradient of Y (same shape, own
+ * strides), dS that of S_out or NULL (zero).  Written, contiguous:
+ *   dV [batch][tokens][heads][P], dK, dQ [batch][tokens][groups][N] of dtype
+ *   (dK and dQ summed over a group's heads), dlog_decay and dgate
+ *   [batch][tokens][heads] float32 (dgate may be NULL), dS0 NULL or
+ *   [batch][heads][P][N] float32.
+ * The gradient of a log decay whose e^g is 0 in float32 is 0. */
+size_t muon_gated_scan_backward_workspace_size(const muon_scan_args* args);
+int muon_gated_scan_backward(const muon_scan_args* args, const muon_seq* dY, const float* dS, void* dV, void* dK,
+                             void* dQ, float* dlog_decay, float* dgate, float* dS0, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* The single-token form (decoding): args->tokens must be 1, S0 is required and
+ * S_out receives the state after the token (may be S0: in place; otherwise the
+ * two must not overlap).  Both are 16-byte aligned when N % 4 == 0.  Y:
+ * [batch][heads][P], contiguous.  One launch, no workspace; everything but the
+ * rounding of Y is float32. */
+int muon_gated_scan_step(const muon_scan_args* args, void* Y, float* S_out, void* stream);
+
+/* Layer norm of each of `rows` rows of n elements:
+ *   Y = (X - mu) r weight + bias,  mu = mean(X),  r = 1 / sqrt(mean((X - mu)^2) + eps)
+ * or with center 0 the same with mu = 0 (the root-mean-square norm of the
+ * Mamba-2 block).
+ *   X, Y        rows of dtype (MUON_BF16 or MUON_F32), ldx and ldy elements
+ *               apart (>= n); Y must not overlap X
+ *   weight, bias  NULL (1 and 0), or float32[n]
+ *   mean, rstd  NULL, or float32[rows] receiving mu and r
+ * Statistics are float32, the variance taken around the mean.  rows < 2^31. */
+int muon_layer_norm(const void* X, long long ldx, int dtype, long long rows, int n, const float* weight,
+                    const float* bias, float eps, int center, void* Y, long long ldy, float* mean, float* rstd,
+                    void* stream);
+
+/* Gradients of muon_layer_norm, from its inputs and the mu (mean NULL: center
+ * was 0) and r that it gave: dX (rows lddx apart) of dtype, dweight and dbias
+ * float32[n] or NULL (not wanted; written as 0 when rows is 0).  The sums over
+ * the rows are float32 in a fixed order; the workspace (16-byte aligned) holds
+ * their parts.  Outputs must not overlap inputs or each other. */
+size_t muon_layer_norm_backward_workspace_size(long long rows, int n, int dtype);
+int muon_layer_norm_backward(const void* dY, long long lddy, const void* X, long long ldx, int dtype, long long rows,
+                             int n, const float* weight, const float* mean, const float* rstd, void* dX,
+                             long long lddx, float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
 /* Human-readable name of a muon_status. */
 const char* muon_status_string(int status);
 

@@ -48,11 +48,24 @@ class GroupC(ctypes.Structure):
                 ("cap_sigma", ctypes.c_void_p), ("cap", ctypes.c_float)]
 
 
+class SeqC(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("sb", ctypes.c_longlong), ("st", ctypes.c_longlong), ("sh", ctypes.c_longlong)]
+
+
+class ScanArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("heads", ctypes.c_int), ("groups", ctypes.c_int),
+                ("P", ctypes.c_int), ("N", ctypes.c_int), ("dtype", ctypes.c_int), ("v", SeqC), ("k", SeqC), ("q", SeqC),
+                ("log_decay", SeqC), ("gate", SeqC), ("S0", ctypes.c_void_p)]
+
+
 EXPORTS = ("muon_step_workspace_size", "muon_step", "muon_step_phases", "muon_step_timed", "muon_ns_workspace_size",
            "muon_ns_orthogonalize", "muon_ns_noalloc_max_bytes", "muon_ns_orthogonalize_noalloc", "muon_query_flags",
            "muon_ns_batched_small", "muon_ns_factored", "muon_ssm_momentum_workspace_size", "muon_ssm_momentum",
            "muon_ssm_momentum_timed", "muon_adamw",
            "muon_spectral_diag_workspace_size", "muon_spectral_diag", "muon_spectral_diag_timed",
+           "muon_gated_scan_workspace_size", "muon_gated_scan", "muon_gated_scan_backward_workspace_size",
+           "muon_gated_scan_backward", "muon_gated_scan_step", "muon_layer_norm",
+           "muon_layer_norm_backward_workspace_size", "muon_layer_norm_backward",
            "muon_status_string", "muon_version")
 
 
@@ -110,6 +123,23 @@ def lib():
     L.muon_spectral_diag_timed.argtypes = [vp, i, i, i, ctypes.c_longlong, i, vp, vp, vp, vp, sz, vp,
                                            ctypes.POINTER(ctypes.c_void_p), i]
     L.muon_spectral_diag_timed.restype = i
+    ll, sa = ctypes.c_longlong, ctypes.POINTER(ScanArgs)
+    L.muon_gated_scan_workspace_size.argtypes = [sa]
+    L.muon_gated_scan_workspace_size.restype = sz
+    L.muon_gated_scan.argtypes = [sa, vp, vp, vp, sz, vp]
+    L.muon_gated_scan.restype = i
+    L.muon_gated_scan_backward_workspace_size.argtypes = [sa]
+    L.muon_gated_scan_backward_workspace_size.restype = sz
+    L.muon_gated_scan_backward.argtypes = [sa, ctypes.POINTER(SeqC), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.muon_gated_scan_backward.restype = i
+    L.muon_gated_scan_step.argtypes = [sa, vp, vp, vp]
+    L.muon_gated_scan_step.restype = i
+    L.muon_layer_norm.argtypes = [vp, ll, i, ll, i, vp, vp, f, i, vp, ll, vp, vp, vp]
+    L.muon_layer_norm.restype = i
+    L.muon_layer_norm_backward_workspace_size.argtypes = [ll, i, i]
+    L.muon_layer_norm_backward_workspace_size.restype = sz
+    L.muon_layer_norm_backward.argtypes = [vp, ll, vp, ll, i, ll, i, vp, vp, vp, vp, ll, vp, vp, vp, sz, vp]
+    L.muon_layer_norm_backward.restype = i
     L.muon_status_string.argtypes = [i]
     L.muon_status_string.restype = ctypes.c_char_p
     L.muon_version.argtypes = []
@@ -614,3 +644,254 @@ def muon_spectral_diag(A, iters=32, orth_err=True, sigma_max=True, sigma_min=Tru
         rc = L.muon_spectral_diag_timed(*args, arr, len(events))
     _check(rc, "muon_spectral_diag")
     return outs
+
+
+# ----------------------------------------------------------------------------
+# sequence operators
+# ----------------------------------------------------------------------------
+def _seq(t) -> SeqC:
+    """A [batch, tokens, heads, width] (or, for gates, [batch, tokens, heads])
+    tensor as a muon_seq (the stride of a dimension of one is never used)."""
+    sb, st, sh = (int(t.stride(d)) if t.shape[d] > 1 else 0 for d in range(3))
+    return SeqC(t.data_ptr(), sb, st, sh)
+
+
+def _scan_args(V, K, Q, log_decay, gate, S0, device):
+    """The muon_scan_args of a call, checked."""
+    import torch
+    if V.dim() != 4 or K.dim() != 4 or K.shape != Q.shape or V.shape[:2] != K.shape[:2]:
+        raise ValueError("V must be [batch, tokens, heads, P]; K and Q [batch, tokens, groups, N]")
+    b, t, h, p = (int(x) for x in V.shape)
+    g, n = int(K.shape[2]), int(K.shape[3])
+    if h == 0 or g == 0 or h % g != 0:
+        raise ValueError(f"the groups ({g}) must divide the heads ({h})")
+    for name, x in (("V", V), ("K", K), ("Q", Q)):
+        if x.numel() > 0 and x.shape[3] > 1 and x.stride(3) != 1:
+            raise ValueError(f"{name} must have adjacent elements in its last dimension")
+    for name, x in (("log_decay", log_decay), ("gate", gate)):
+        if x is not None and tuple(x.shape) != (b, t, h):
+            raise ValueError(f"{name} must be a [{b}, {t}, {h}] float32 tensor")
+    _check_tensors([V, K, Q], "V, K and Q", (torch.bfloat16, torch.float32), device)
+    _check_tensors([x for x in (log_decay, gate) if x is not None], "log_decay and gate", (torch.float32,), device)
+    if S0 is not None:
+        _check_state(S0, "S0", (b, h, p, n), device)
+    return ScanArgs(b, t, h, g, p, n, _dtype_code(V), _seq(V), _seq(K), _seq(Q), _seq(log_decay),
+                    SeqC() if gate is None else _seq(gate), None if S0 is None else S0.data_ptr())
+
+
+def _check_state(S, name, shape, device):
+    import torch
+    if not S.is_contiguous() or tuple(S.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous [{', '.join(map(str, shape))}] float32 tensor")
+    _check_tensors([S], name, (torch.float32,), device)
+
+
+def _out(t, name, shape, dtype, device):
+    """The caller's output tensor when given (checked), else a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous [{', '.join(map(str, shape))}] tensor")
+    _check_tensors([t], name, (dtype,), device)
+    return t
+
+
+def _ptr(t):
+    return None if t is None or t.numel() == 0 else t.data_ptr()
+
+
+def _used_on(stream, *tensors):
+    """Tensors made on torch's current stream for a call on another one: their
+    memory is not given out again before that stream is past the call."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def muon_gated_scan(V, K, Q, log_decay, gate=None, S0=None, Y=None, S_out=None, workspace=None, stream=None):
+    """The gated scan S_t = exp(log_decay_t) S_{t-1} + gate_t v_t k_t^T,
+    y_t = S_t q_t of every sequence and head: V [batch, tokens, heads, P], K and
+    Q [batch, tokens, groups, N] of one dtype (bf16 or float32), log_decay and
+    gate [batch, tokens, heads] float32 (any strides, but adjacent elements in
+    the last dimension of V, K and Q), S0 [batch, heads, P, N] float32.  A
+    log decay of -inf starts a new sequence.  Returns (Y, S_out): the outputs,
+    of V's dtype and float32, and the last state, in the tensors given or in
+    new ones.  workspace: a uint8 tensor of at least
+    muon_gated_scan_workspace_size bytes to use instead of a new one."""
+    import torch
+    L = lib()
+    dev = _current_device()
+    a = _scan_args(V, K, Q, log_decay, gate, S0, dev)
+    need = int(L.muon_gated_scan_workspace_size(ctypes.byref(a)))
+    if need == 0:
+        raise MuonError(MUON_EUNSUPPORTED, "muon_gated_scan_workspace_size")
+    Y = _out(Y, "Y", (a.batch, a.tokens, a.heads, a.P), V.dtype, dev)
+    S_out = _out(S_out, "S_out", (a.batch, a.heads, a.P, a.N), torch.float32, dev)
+    ws = _workspace(workspace, need, dev)
+    _check(L.muon_gated_scan(ctypes.byref(a), _ptr(Y), _ptr(S_out), ws.data_ptr(), ws.numel(), _stream_handle(stream)),
+           "muon_gated_scan")
+    _used_on(stream, Y, S_out, ws)
+    return Y, S_out
+
+
+def muon_gated_scan_workspace_size(V, K, backward=False) -> int:
+    """Workspace bytes of muon_gated_scan (backward: of
+    muon_gated_scan_backward) for V and K of these shapes and dtype."""
+    b, t, h, p = (int(x) for x in V.shape)
+    a = ScanArgs(b, t, h, int(K.shape[2]), p, int(K.shape[3]), _dtype_code(V))
+    L = lib()
+    fn = L.muon_gated_scan_backward_workspace_size if backward else L.muon_gated_scan_workspace_size
+    return int(fn(ctypes.byref(a)))
+
+
+def muon_gated_scan_backward(V, K, Q, log_decay, dY, gate=None, S0=None, dS=None, dV=None, dK=None, dQ=None,
+                             dlog_decay=None, dgate=None, dS0=None, workspace=None, stream=None):
+    """Gradients through muon_gated_scan: the forward call's inputs, dY the
+    gradient of Y and dS that of S_out (None: zero).  Returns (dV, dK, dQ,
+    dlog_decay, dgate, dS0), of the shapes and dtypes of what they are the
+    gradients of, in the tensors given or in new ones; dgate is None without a
+    gate, dS0 without S0."""
+    import torch
+    L = lib()
+    dev = _current_device()
+    a = _scan_args(V, K, Q, log_decay, gate, S0, dev)
+    state = (a.batch, a.heads, a.P, a.N)
+    if tuple(dY.shape) != tuple(V.shape) or (dY.numel() > 0 and dY.shape[3] > 1 and dY.stride(3) != 1):
+        raise ValueError("dY must have V's shape and adjacent elements in its last dimension")
+    _check_tensors([dY], "dY", (V.dtype,), dev)
+    if dS is not None:
+        _check_state(dS, "dS", state, dev)
+    need = int(L.muon_gated_scan_backward_workspace_size(ctypes.byref(a)))
+    if need == 0:
+        raise MuonError(MUON_EUNSUPPORTED, "muon_gated_scan_backward_workspace_size")
+    dV = _out(dV, "dV", tuple(V.shape), V.dtype, dev)
+    dK = _out(dK, "dK", tuple(K.shape), V.dtype, dev)
+    dQ = _out(dQ, "dQ", tuple(K.shape), V.dtype, dev)
+    dlog_decay = _out(dlog_decay, "dlog_decay", tuple(V.shape[:3]), torch.float32, dev)
+    if dgate is not None or gate is not None:
+        dgate = _out(dgate, "dgate", tuple(V.shape[:3]), torch.float32, dev)
+    if dS0 is not None or S0 is not None:
+        dS0 = _out(dS0, "dS0", state, torch.float32, dev)
+    ws = _workspace(workspace, need, dev)
+    dy = _seq(dY)
+    _check(L.muon_gated_scan_backward(ctypes.byref(a), ctypes.byref(dy), _ptr(dS), _ptr(dV), _ptr(dK), _ptr(dQ),
+                                      _ptr(dlog_decay), _ptr(dgate), _ptr(dS0), ws.data_ptr(), ws.numel(),
+                                      _stream_handle(stream)), "muon_gated_scan_backward")
+    _used_on(stream, dV, dK, dQ, dlog_decay, dgate, dS0, ws)
+    return dV, dK, dQ, dlog_decay, dgate, dS0
+
+
+def muon_gated_scan_step(V, K, Q, log_decay, S, gate=None, Y=None, S_out=None, stream=None):
+    """One token of the gated scan (decoding): V [batch, heads, P], K and Q
+    [batch, groups, N], log_decay and gate [batch, heads], S [batch, heads, P,
+    N] float32, updated in place unless S_out is given.  Returns (Y, S_out or
+    S)."""
+    L = lib()
+    dev = _current_device()
+    if V.dim() != 3 or K.dim() != 3 or Q.dim() != 3:
+        raise ValueError("V must be [batch, heads, P]; K and Q [batch, groups, N]")
+    one = lambda x: None if x is None else x.unsqueeze(1)  # noqa: E731
+    a = _scan_args(one(V), one(K), one(Q), one(log_decay), one(gate), S, dev)
+    Y = _out(Y, "Y", tuple(V.shape), V.dtype, dev)
+    if S_out is None:
+        S_out = S
+    else:
+        _check_state(S_out, "S_out", tuple(S.shape), dev)
+    _check(L.muon_gated_scan_step(ctypes.byref(a), _ptr(Y), _ptr(S_out), _stream_handle(stream)), "muon_gated_scan_step")
+    _used_on(stream, Y)
+    return Y, S_out
+
+
+def _rows(t, name):
+    """(rows, n, row stride) of a tensor whose last dimension is adjacent and
+    whose other dimensions fold into one row stride."""
+    n = int(t.shape[-1])
+    rows = t.numel() // n if n else 0
+    if n > 1 and t.numel() > 0 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have adjacent elements in its last dimension")
+    ld, expect = n, None
+    for d in range(t.dim() - 2, -1, -1):
+        if t.shape[d] == 1:
+            continue
+        if expect is None:
+            ld = int(t.stride(d))
+        elif int(t.stride(d)) != expect:
+            raise ValueError(f"the rows of {name} must be one stride apart")
+        expect = int(t.stride(d)) * int(t.shape[d])
+    return rows, n, ld
+
+
+def _check_row_params(n, device, **params):
+    import torch
+    for name, t in params.items():
+        if t is None:
+            continue
+        if not t.is_contiguous() or tuple(t.shape) != (n,):
+            raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
+        _check_tensors([t], name, (torch.float32,), device)
+
+
+def muon_layer_norm(X, weight=None, bias=None, eps=1e-5, center=True, Y=None, stream=None):
+    """Layer norm over the last dimension of X (bf16 or float32, rows one stride
+    apart): Y = (X - mean) / sqrt(var + eps) * weight + bias; center=False: the
+    root-mean-square norm (mean 0).  weight and bias are float32.  Returns (Y,
+    mean, rstd): Y of X's dtype, the float32 statistics of the rows for the
+    backward pass (mean None without centering)."""
+    import torch
+    L = lib()
+    dev = _current_device()
+    _check_tensors([X], "X", (torch.bfloat16, torch.float32), dev)
+    rows, n, ldx = _rows(X, "X")
+    _check_row_params(n, dev, weight=weight, bias=bias)
+    if Y is None:
+        Y = torch.empty(X.shape, dtype=X.dtype, device=dev)
+    if Y.shape != X.shape:
+        raise ValueError("Y must have X's shape")
+    _check_tensors([Y], "Y", (X.dtype,), dev)
+    ldy = _rows(Y, "Y")[2]
+    lead = tuple(X.shape[:-1])
+    mean = torch.empty(lead, dtype=torch.float32, device=dev) if center else None
+    rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+    _check(L.muon_layer_norm(_ptr(X), ldx, _dtype_code(X), rows, n, _ptr(weight), _ptr(bias), float(eps), int(bool(center)),
+                             _ptr(Y), ldy, _ptr(mean), _ptr(rstd), _stream_handle(stream)), "muon_layer_norm")
+    _used_on(stream, Y, mean, rstd)
+    return Y, mean, rstd
+
+
+def muon_layer_norm_backward(dY, X, weight, mean, rstd, center=True, bias_grad=True, workspace=None, stream=None):
+    """Gradients through muon_layer_norm from its input, weight and the
+    statistics that it returned: (dX, dweight, dbias), dweight None without a
+    weight, dbias None unless bias_grad."""
+    import torch
+    L = lib()
+    dev = _current_device()
+    _check_tensors([X], "X", (torch.bfloat16, torch.float32), dev)
+    _check_tensors([dY], "dY", (X.dtype,), dev)
+    if dY.shape != X.shape:
+        raise ValueError("dY must have X's shape")
+    rows, n, ldx = _rows(X, "X")
+    lddy = _rows(dY, "dY")[2]
+    _check_row_params(n, dev, weight=weight)
+    if center and mean is None:
+        raise ValueError("mean is needed with centering")
+    for name, t in (("mean", mean if center else None), ("rstd", rstd)):
+        if t is None:
+            continue
+        if not t.is_contiguous() or t.numel() != rows:
+            raise ValueError(f"{name} must be a contiguous float32 tensor with one entry per row")
+        _check_tensors([t], name, (torch.float32,), dev)
+    dt = _dtype_code(X)
+    need = int(L.muon_layer_norm_backward_workspace_size(rows, n, dt))
+    if need == 0:
+        raise MuonError(MUON_EUNSUPPORTED, "muon_layer_norm_backward_workspace_size")
+    dX = torch.empty(X.shape, dtype=X.dtype, device=dev)
+    dweight = torch.empty(n, dtype=torch.float32, device=dev) if weight is not None else None
+    dbias = torch.empty(n, dtype=torch.float32, device=dev) if bias_grad else None
+    ws = _workspace(workspace, need, dev)
+    _check(L.muon_layer_norm_backward(_ptr(dY), lddy, _ptr(X), ldx, dt, rows, n, _ptr(weight), _ptr(mean) if center else None,
+                                      _ptr(rstd), _ptr(dX), n, _ptr(dweight), _ptr(dbias), ws.data_ptr(), ws.numel(),
+                                      _stream_handle(stream)), "muon_layer_norm_backward")
+    _used_on(stream, dX, dweight, dbias, ws)
+    return dX, dweight, dbias

@@ -1,0 +1,429 @@
+// The gated scan: for every sequence and head
+//   S_t = e^{g_t} S_{t-1} + b_t v_t k_t^T   (P x N),   y_t = S_t q_t.
+// With c the inclusive sums of g inside a chunk of kQ tokens that starts from
+// S_in, the chunk is
+//   y_i   = sum_{j <= i} e^{c_i - c_j} b_j (q_i . k_j) v_j + e^{c_i} S_in q_i
+//   S_out = e^{c_end} S_in + sum_j e^{c_end - c_j} b_j v_j k_j^T,
+// matrix products all.  One workgroup walks the chunks of a sequence, head and
+// block of kPB state rows with the state in its registers (float32, so it
+// crosses HBM only at the ends): each of its four waves holds 16 rows of S.
+// Held as S^T with n along the accumulator rows, the state is the operand of
+// S_in q without leaving the registers.
+//
+// Rounding, bfloat16 operands: the weights e^{c_i - c_j} b_j (q_i . k_j) and
+// the copy of S_in that is read are rounded to bfloat16 once, which leaves y
+// within its own rounding; the weighted values that enter the state are split
+// into three bfloat16 pieces, so the state keeps float32 accuracy.
+//
+// In reversed time the same walk with (dy, q) for (v, k), weights e^{c_i} and
+// no reads gives the gradients of the states (muon_gated_scan_backward).
+#include "scan_tiles.cuh"
+
+namespace muon {
+namespace {
+
+using namespace scan;
+
+template <typename T, int NT>
+struct WalkLds {
+  static constexpr int kLdN = NT + Ops<T>::kPad;
+  static constexpr int kLdP = kPB + Ops<T>::kPad;
+  static constexpr int kLdM = kQ + Ops<T>::kPad;
+  static constexpr int k = 0;                                   // k [kQ][NT]
+  static constexpr int x = k + kQ * kLdN * (int)sizeof(T);      // x [kQ][kPB]
+  static constexpr int gates = x + kQ * kLdP * (int)sizeof(T);  // Gates[2]
+  static constexpr int states_bytes = gates + 2 * (int)sizeof(Gates);
+  static constexpr int q = states_bytes;                        // q [kQ][NT]
+  static constexpr int m = q + kQ * kLdN * (int)sizeof(T);      // weights M [i][j]
+  static constexpr int read_bytes = m + kQ * kLdM * (int)sizeof(T);
+};
+
+struct WalkPair {
+  ScanWalk w[2];
+};
+
+// READ: y is computed (q is read); else only states move.
+template <typename T, int NT, bool READ>
+__global__ void __launch_bounds__(kThreads, 2) scan_walk_kernel(WalkPair W) {
+  typedef Ops<T> O;
+  typedef typename O::Frag Frag;
+  typedef WalkLds<T, NT> L;
+  constexpr int kT = NT / 16;       // state tiles of a wave
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const ScanWalk& A = W.w[blockIdx.y];
+  T* lk = reinterpret_cast<T*>(lds + L::k);
+  T* lx = reinterpret_cast<T*>(lds + L::x);
+  T* lq = reinterpret_cast<T*>(lds + L::q);
+  T* lm = reinterpret_cast<T*>(lds + L::m);
+  Gates* gates = reinterpret_cast<Gates*>(lds + L::gates);
+
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l16 = lane & 15, g4 = lane >> 4;
+  const int vheads = A.heads * A.pblocks;
+  const long long item = blockIdx.x;
+  const int seg = static_cast<int>(item % A.nseg);
+  const int vh = static_cast<int>(item / A.nseg % vheads);
+  const long long bi = item / A.nseg / vheads;
+  const int h = vh / A.pblocks, pb = vh - h * A.pblocks, grp = h / (A.heads / A.groups);
+  const int rows_p = A.P - pb * kPB < kPB ? A.P - pb * kPB : kPB;
+  if (A.totals && seg + 1 == A.nseg) return;   // nothing starts after the last segment
+  const long long vrow = bi * vheads + vh;
+  const int cc0 = seg * A.seg_chunks;
+  const int cc1 = cc0 + A.seg_chunks < A.nchunks ? cc0 + A.seg_chunks : A.nchunks;
+
+  const T* xp = static_cast<const T*>(A.x.p) + bi * A.x.sb + h * A.x.sh + pb * kPB;
+  const T* kp = static_cast<const T*>(A.k.p) + bi * A.k.sb + grp * A.k.sh;
+  const T* qp = READ ? static_cast<const T*>(A.q.p) + bi * A.q.sb + grp * A.q.sh : nullptr;
+  const float* gp = static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh;
+  const float* bp = A.b.p == nullptr ? nullptr : static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh;
+
+  // token of a lane in the cc-th chunk visited; its gates (past the end: no decay, no input)
+  const auto chunk_of = [&](int cc) { return A.reverse ? A.nchunks - 1 - cc : cc; };
+  const auto load_gates = [&](int cc, float& gv, float& bv) {
+    const long long t = static_cast<long long>(chunk_of(cc)) * kQ + lane;
+    gv = 0.0f;
+    bv = 0.0f;
+    if (t < A.tokens) {
+      gv = gp[t * A.g.st];
+      bv = bp == nullptr ? 1.0f : bp[t * A.b.st];
+    }
+  };
+
+  TileLoad<T, NT> tk, tq;
+  TileLoad<T, kPB> tx;
+  const auto load_tiles = [&](int cc) {
+    const long long t0 = static_cast<long long>(chunk_of(cc)) * kQ;
+    const int rows = A.tokens - t0 < kQ ? static_cast<int>(A.tokens - t0) : kQ;
+    tk.load(kp + t0 * A.k.st, A.k.st, rows, A.N, A.k.vec);
+    tx.load(xp + t0 * A.x.st, A.x.st, rows, rows_p, A.x.vec && rows_p % O::kVec == 0);
+    if constexpr (READ) tq.load(qp + t0 * A.q.st, A.q.st, rows, A.N, A.q.vec);
+  };
+
+  // the state: tile t holds S^T rows n = 16 t + 4 g4 + 0..3, column p = 16 w + l16
+  f32x4_t st[kT];
+  const int prow = pb * kPB + 16 * w + l16;
+  if (A.seg_state != nullptr && !A.totals) {
+    const float* sp = A.seg_state + ((vrow * A.nseg + seg) * kPB + 16 * w + l16) * NT + 4 * g4;
+#pragma unroll
+    for (int t = 0; t < kT; ++t) st[t] = *reinterpret_cast<const f32x4_t*>(sp + 16 * t);
+  } else {
+    const bool init = A.init != nullptr && !A.totals;
+    const float* sp = A.init + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int n = 16 * t + 4 * g4 + r;
+        st[t][r] = init && prow < A.P && n < A.N ? sp[n] : 0.0f;
+      }
+  }
+
+  if constexpr (READ) {
+    // tiles (0, 1) and (2, 3) of M lie above the diagonal inside the 32-wide
+    // steps that are multiplied: zero for good
+    if (w < 2) {
+      const int r0 = 32 * w, c0 = 32 * w + 16;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) lm[(r0 + l16) * L::kLdM + c0 + 4 * g4 + e] = O::from_f32(0.0f);
+    }
+  }
+  float gv = 0.0f, bv = 0.0f;
+  double seg_log = 0.0;
+  load_tiles(cc0);
+  if (w == 3) {
+    load_gates(cc0, gv, bv);
+    seg_log += write_gates(gates[cc0 & 1], gv, bv, lane);
+    if (cc0 + 1 < cc1) load_gates(cc0 + 1, gv, bv);
+  }
+  for (int cc = cc0; cc < cc1; ++cc) {
+    __syncthreads();   // the last chunk's tiles are done with
+    tk.store(lk);
+    tx.store(lx);
+    if constexpr (READ) tq.store(lq);
+    __syncthreads();
+    const Gates& G = gates[cc & 1];
+    if (cc + 1 < cc1) {
+      load_tiles(cc + 1);
+      if (w == 3) {
+        seg_log += write_gates(gates[(cc + 1) & 1], gv, bv, lane);
+        if (cc + 2 < cc1) load_gates(cc + 2, gv, bv);
+      }
+    }
+    const long long t0 = static_cast<long long>(chunk_of(cc)) * kQ;
+
+    f32x4_t y[4];   // y^T: rows p = 16 w + 4 g4 + 0..3, column i = 16 it + l16
+    if constexpr (READ) {
+      // M^T tiles: rows j, columns i, so a lane's four values are neighbours in M
+      const int nt = tile_count(w);
+#pragma unroll
+      for (int t = 0; t < kMaxTiles; ++t) {
+        if (t < nt) {
+          const int it = tile_row(w, t), jt = tile_col(w, t);
+          f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int s = 0; s < NT / 32; ++s)
+            a = O::mma(O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4),
+                       O::row(lq + (16 * it + l16) * L::kLdN + 32 * s + 8 * g4), a);
+          const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
+          const float hi = G.hi[i], lo = G.lo[i];
+          const f32x4_t jh = *reinterpret_cast<const f32x4_t*>(G.hi + j0), jl = *reinterpret_cast<const f32x4_t*>(G.lo + j0);
+          const f32x4_t jb = *reinterpret_cast<const f32x4_t*>(G.b + j0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) a[r] = j0 + r <= i ? a[r] * between(hi, lo, jh[r], jl[r]) * jb[r] : 0.0f;
+          O::store4(lm + i * L::kLdM + j0, a);
+        }
+      }
+      // what S_in gives: e^{c_i} S_in q_i
+#pragma unroll
+      for (int it = 0; it < 4; ++it) y[it] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int s = 0; s < NT / 32; ++s) {
+        const Frag f = frag_from_acc<T>(st[2 * s], st[2 * s + 1]);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const T* qr = lq + (16 * it + l16) * L::kLdN + 32 * s + 4 * g4;
+          y[it] = O::mma(f, O::row2(qr, qr + 16), y[it]);
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < 4; ++it) y[it] *= G.first[16 * it + l16];
+    }
+    if (A.states != nullptr) {
+      // the state that the chunk starts from (in reversed time: ends with)
+      float* sp = A.states + ((vrow * A.nchunks + chunk_of(cc)) * kPB + 16 * w + l16) * NT + 4 * g4;
+#pragma unroll
+      for (int t = 0; t < kT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
+    }
+
+    // the chunk's own part of the state
+    const float end = G.end[0];
+#pragma unroll
+    for (int t = 0; t < kT; ++t) st[t] *= end;
+#pragma unroll
+    for (int s = 0; s < kQ / 32; ++s) {
+      float xv[8];
+      O::widen(O::col(lx, L::kLdP, 32 * s, 16 * w, lane), xv);
+      const int j0 = 32 * s + 8 * g4;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xv[e] *= A.reverse ? G.first[j0 + e] : G.last[j0 + e] * G.b[j0 + e];
+      Frag f[O::kSplit];
+      O::split(xv, f);
+#pragma unroll
+      for (int t = 0; t < kT; ++t) {
+        const Frag kf = O::col(lk, L::kLdN, 32 * s, 16 * t, lane);
+#pragma unroll
+        for (int u = O::kSplit - 1; u >= 0; --u) st[t] = O::mma(kf, f[u], st[t]);
+      }
+    }
+
+    if constexpr (READ) {
+      __syncthreads();   // M is written
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const Frag vf = O::col(lx, L::kLdP, 32 * s, 16 * w, lane);
+#pragma unroll
+        for (int it = 2 * s; it < 4; ++it)
+          y[it] = O::mma(vf, O::row(lm + (16 * it + l16) * L::kLdM + 32 * s + 8 * g4), y[it]);
+      }
+      const int p0 = 16 * w + 4 * g4;
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const long long t = t0 + 16 * it + l16;
+        if (t < A.tokens && p0 < rows_p) {
+          T* yp = static_cast<T*>(A.y) + ((bi * A.tokens + t) * A.heads + h) * A.P + pb * kPB + p0;
+          if (A.yvec) {
+            O::store4(yp, y[it]);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (p0 + r < rows_p) yp[r] = O::from_f32(y[it][r]);
+          }
+        }
+      }
+    }
+  }
+
+  if (A.totals) {
+    float* sp = A.seg_state + ((vrow * A.nseg + seg) * kPB + 16 * w + l16) * NT + 4 * g4;
+#pragma unroll
+    for (int t = 0; t < kT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
+    if (w == 3 && lane == 0) A.seg_decay[vrow * A.nseg + seg] = __builtin_amdgcn_exp2f(static_cast<float>(seg_log));
+  } else if (A.fin != nullptr && cc1 == A.nchunks) {
+    float* sp = A.fin + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
+#pragma unroll
+    for (int t = 0; t < kT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int n = 16 * t + 4 * g4 + r;
+        if (prow < A.P && n < A.N) sp[n] = st[t][r];
+      }
+  }
+}
+
+// The state that each segment starts from, out of the segments' own totals
+// (in place: a total is read before its slot is overwritten).
+__global__ void __launch_bounds__(kThreads) scan_segments_kernel(WalkPair W, int nt) {
+  const ScanWalk& A = W.w[blockIdx.z];
+  const int e = static_cast<int>(blockIdx.y) * kThreads + static_cast<int>(threadIdx.x);   // of kPB * nt
+  const long long vrow = blockIdx.x;
+  const int vheads = A.heads * A.pblocks;
+  const int vh = static_cast<int>(vrow % vheads);
+  const long long bi = vrow / vheads;
+  const int h = vh / A.pblocks, p = (vh - h * A.pblocks) * kPB + e / nt, n = e % nt;
+  float cur = A.init != nullptr && p < A.P && n < A.N ? A.init[((bi * A.heads + h) * A.P + p) * static_cast<long long>(A.N) + n]
+                                                      : 0.0f;
+  float* sp = A.seg_state + vrow * A.nseg * kPB * nt + e;
+  const float* dp = A.seg_decay + vrow * A.nseg;
+  for (int s = 0; s + 1 < A.nseg; ++s) {
+    const float own = sp[static_cast<long long>(s) * kPB * nt];
+    sp[static_cast<long long>(s) * kPB * nt] = cur;
+    cur = fmaf(dp[s], cur, own);
+  }
+  sp[static_cast<long long>(A.nseg - 1) * kPB * nt] = cur;
+}
+
+template <typename T, int NT, bool READ>
+hipError_t walk(const WalkPair& W, int dirs, hipStream_t st) {
+  const ScanWalk& a = W.w[0];
+  const int bytes = READ ? WalkLds<T, NT>::read_bytes : WalkLds<T, NT>::states_bytes;
+  const void* fn = reinterpret_cast<const void*>(scan_walk_kernel<T, NT, READ>);
+  const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != hipSuccess) return e;
+  const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg;
+  hipLaunchKernelGGL((scan_walk_kernel<T, NT, READ>), dim3(static_cast<unsigned>(items), dirs), dim3(kThreads), bytes, st,
+                     W);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t walk_any(const WalkPair& W, int dirs, bool read, hipStream_t st) {
+  if (W.w[0].N <= 64) return read ? walk<T, 64, true>(W, dirs, st) : walk<T, 64, false>(W, dirs, st);
+  return read ? walk<T, 128, true>(W, dirs, st) : walk<T, 128, false>(W, dirs, st);
+}
+
+}  // namespace
+
+hipError_t launch_scan_walk(const ScanWalk* walks, int dirs, bool read, bool bf16, hipStream_t st) {
+  WalkPair W{{walks[0], walks[dirs - 1]}};
+  const ScanWalk& a = walks[0];
+  if (a.nseg > 1) {
+    WalkPair S = W;
+    for (ScanWalk& x : S.w) {
+      x.totals = 1;
+      x.states = nullptr;
+    }
+    hipError_t e = bf16 ? walk_any<bf16_t>(S, dirs, false, st) : walk_any<float>(S, dirs, false, st);
+    if (e != hipSuccess) return e;
+    const int nt = scan_padded_n(a.N);
+    const long long vrows = static_cast<long long>(a.batch) * a.heads * a.pblocks;
+    hipLaunchKernelGGL(scan_segments_kernel, dim3(static_cast<unsigned>(vrows), kScanRows * nt / kThreads, dirs),
+                       dim3(kThreads), 0, st, W, nt);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return bf16 ? walk_any<bf16_t>(W, dirs, read, st) : walk_any<float>(W, dirs, read, st);
+}
+
+// ---------------------------------------------------------------------------
+// one token: S' = e^g S + b v k^T, y = S' q.  Reads and writes the state once;
+// a half-wave holds a row's N <= 128 elements, 4 consecutive ones a lane.
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kStepRows = 16;   // state rows per workgroup: 8 half-waves, 2 rows each
+
+template <typename T>
+__device__ __forceinline__ float load1(const T* p);
+template <>
+__device__ __forceinline__ float load1<bf16_t>(const bf16_t* p) { return bf16_to_f32(*p); }
+template <>
+__device__ __forceinline__ float load1<float>(const float* p) { return *p; }
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanStep A) {
+  const int half = threadIdx.x >> 5, l = threadIdx.x & 31, n0 = 4 * l;
+  const int pblocks = (A.P + kStepRows - 1) / kStepRows;
+  const int pb = static_cast<int>(blockIdx.x) % pblocks;
+  const long long bh = blockIdx.x / pblocks;
+  const int h = static_cast<int>(bh % A.heads), grp = h / (A.heads / A.groups);
+  const long long bi = bh / A.heads;
+  const T* vp = static_cast<const T*>(A.v.p) + bi * A.v.sb + h * A.v.sh;
+  const T* kp = static_cast<const T*>(A.k.p) + bi * A.k.sb + grp * A.k.sh;
+  const T* qp = static_cast<const T*>(A.q.p) + bi * A.q.sb + grp * A.q.sh;
+  const bool vec = A.N % 4 == 0;   // rows of the state stay 16-byte aligned
+  f32x4_t s[2];
+  bool live[2];
+  const float* sp[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int p = pb * kStepRows + 8 * u + half;
+    live[u] = p < A.P;
+    sp[u] = A.S + (bh * A.P + p) * A.N + n0;
+    s[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (live[u] && n0 < A.N) {
+      if (vec) {
+        s[u] = *reinterpret_cast<const f32x4_t*>(sp[u]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n0 + r < A.N) s[u][r] = sp[u][r];
+      }
+    }
+  }
+  f32x4_t k, q;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    k[r] = n0 + r < A.N ? load1<T>(kp + n0 + r) : 0.0f;
+    q[r] = n0 + r < A.N ? load1<T>(qp + n0 + r) : 0.0f;
+  }
+  const float decay = expf(static_cast<const float*>(A.g.p)[bi * A.g.sb + h * A.g.sh]);
+  const float gate = A.b.p == nullptr ? 1.0f : static_cast<const float*>(A.b.p)[bi * A.b.sb + h * A.b.sh];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int p = pb * kStepRows + 8 * u + half;
+    const float v = live[u] ? gate * load1<T>(vp + p) : 0.0f;
+    float y = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      s[u][r] = fmaf(decay, s[u][r], v * k[r]);
+      y = fmaf(s[u][r], q[r], y);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) y += __shfl_xor(y, off, kWave);
+    if (!live[u]) continue;
+    float* op = A.S_out + (bh * A.P + p) * A.N + n0;
+    if (n0 < A.N) {
+      if (vec) {
+        *reinterpret_cast<f32x4_t*>(op) = s[u];
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n0 + r < A.N) op[r] = s[u][r];
+      }
+    }
+    if (l == 0) static_cast<T*>(A.y)[bh * A.P + p] = Ops<T>::from_f32(y);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_scan_step(const ScanStep& A, bool bf16, hipStream_t st) {
+  const long long blocks = static_cast<long long>(A.batch) * A.heads * ((A.P + kStepRows - 1) / kStepRows);
+  if (bf16) hipLaunchKernelGGL(scan_step_kernel<bf16_t>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, A);
+  else hipLaunchKernelGGL(scan_step_kernel<float>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, A);
+  return hipGetLastError();
+}
+
+namespace {
+__global__ void __launch_bounds__(kThreads) scan_copy_kernel(const float* src, float* dst, long long n) {
+  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += static_cast<long long>(gridDim.x) * kThreads)
+    dst[i] = src == nullptr ? 0.0f : src[i];
+}
+}  // namespace
+
+hipError_t launch_copy_f32(const float* src, float* dst, long long n, hipStream_t st) {
+  const long long blocks = (n + kThreads - 1) / kThreads;
+  hipLaunchKernelGGL(scan_copy_kernel, dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048)), dim3(kThreads), 0, st, src, dst, n);
+  return hipGetLastError();
+}
+
+}  // namespace muon

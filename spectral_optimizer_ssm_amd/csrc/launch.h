@@ -302,4 +302,83 @@ struct AdamwLaunch {
 };
 hipError_t launch_adamw(const AdamwLaunch& A, bool grad_bf16, int blocks, hipStream_t st);
 
+// Gated scan (gated_scan.hip, gated_scan_backward.hip).
+constexpr int kScanChunk = 64;     // tokens per chunk
+constexpr int kScanRows = 64;      // state rows (value components) per workgroup
+constexpr int kScanMaxN = 128;     // largest key length
+inline int scan_padded_n(int n) { return n <= 64 ? 64 : 128; }
+struct SeqOperand {    // [batch][tokens][heads or groups][width], innermost stride 1
+  const void* p;
+  long long sb, st, sh;   // strides in elements
+  int vec;             // every row is 16-byte aligned and a multiple of 16 bytes wide
+};
+struct ScanWalk {
+  SeqOperand x, k, q;  // values, keys, queries; in reversed time dy and queries (q unused)
+  SeqOperand g, b;     // float32 log decays and input gates (b.p null: 1); st, sh per token, head
+  int batch, tokens, heads, groups, P, N;
+  int pblocks, nchunks;       // ceil(P / kScanRows), ceil(tokens / kScanChunk)
+  int nseg, seg_chunks;       // segments of the time axis and their chunks
+  int reverse;                // chunks from the last to the first, weights e^{c_i}
+  int totals;                 // set by the launcher: segments from a zero state, into seg_state
+  int yvec;                   // rows of y take 4-element stores
+  void* y;                    // [batch][tokens][heads][P]
+  const float* init;          // null, or [batch][heads][P][N]: the state before the first chunk visited
+  float* fin;                 // null, or the state after the last
+  float* states;              // null, or [batch][heads * pblocks][nchunks][kScanRows][padded N]: the
+                              // state that each chunk is visited with
+  float* seg_state;           // nseg > 1: [batch][heads * pblocks][nseg][kScanRows][padded N]
+  float* seg_decay;           //           [batch][heads * pblocks][nseg]
+};
+// One walk, or two (dirs = 2, of equal sizes) in one launch.
+hipError_t launch_scan_walk(const ScanWalk* W, int dirs, bool read, bool bf16, hipStream_t st);
+struct ScanGrad {
+  SeqOperand v, k, q, dy, g, b;
+  int batch, tokens, heads, groups, P, N, pblocks, nchunks;
+  int nsplit;                 // workgroups that share a chunk's heads
+  int dvvec, dkvec;           // rows of dv; of dq and dk: 4-element stores
+  const float* states;        // as ScanWalk.states: before each chunk
+  const float* dstates;       // gradients of the states after each chunk
+  void *dv, *dk, *dq;
+  float *dg, *db;             // [batch][tokens][heads]; db may be null
+  float* parts;               // nsplit > 1: [nsplit][2][batch * tokens * groups * N]
+};
+hipError_t launch_scan_grad(const ScanGrad& A, bool bf16, hipStream_t st);
+struct ScanStep {
+  SeqOperand v, k, q, g, b;
+  int batch, heads, groups, P, N;
+  void* y;                    // [batch][heads][P]
+  const float* S;             // [batch][heads][P][N]
+  float* S_out;               // may be S
+};
+hipError_t launch_scan_step(const ScanStep& A, bool bf16, hipStream_t st);
+
+// dst = src, or 0 where src is null (the final state of a scan without tokens).
+hipError_t launch_copy_f32(const float* src, float* dst, long long n, hipStream_t st);
+
+// Layer norm (layer_norm.hip).
+struct NormLaunch {
+  const void* x;
+  void* y;
+  long long ldx, ldy, rows;
+  int n, center;
+  int vec, pvec;       // rows of x and y, w and bias: 16-byte aligned, n a multiple of a piece
+  const float *w, *bias;   // may be null
+  float eps;
+  float *mean, *rstd;      // [rows], may be null
+};
+hipError_t launch_norm(const NormLaunch& A, bool bf16, hipStream_t st);
+struct NormGradLaunch {
+  const void *dy, *x;
+  void* dx;
+  long long lddy, ldx, lddx, rows;
+  int n, vec;
+  const float* w;          // may be null
+  const float *mean, *rstd;   // mean null: no centering
+  float *dw, *dbias;       // may be null
+  float* part;             // [parts][2][n]
+  int parts;
+};
+int norm_grad_parts(long long rows, int n, bool bf16);
+hipError_t launch_norm_grad(const NormGradLaunch& A, bool bf16, hipStream_t st);
+
 }  // namespace muon

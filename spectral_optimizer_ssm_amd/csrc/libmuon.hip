@@ -19,6 +19,7 @@
 #include <vector>
 
 #include "../../include/muon.h"
+#include "host.h"
 #include "launch.h"
 
 using namespace muon;
@@ -26,17 +27,12 @@ using namespace muon;
 namespace {
 
 constexpr int kMaxSteps = 64;
-constexpr size_t kAlign = 256;
 // Every muon_step / muon_ns_orthogonalize workspace opens with this header:
 // word 0 is the non-finite flag of the last call (muon_query_flags); the
 // per-block partial sums of squares of all groups follow it, contiguous.
 constexpr size_t kHeader = 256;
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int round_up(int x, int a) { return (x + a - 1) / a * a; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-size_t dtype_size(int dt) { return dt == MUON_BF16 ? 2 : 4; }
 
 struct NsCoefs {
   int steps;
@@ -969,8 +965,6 @@ int factored_launch(int m, int n, int r, long long batch, const NsCoefs& C, floa
   for (int k = 0; k < C.steps; ++k) { F->a[k] = C.a[k]; F->b[k] = C.b[k]; F->c[k] = C.c[k]; }
   return MUON_OK;
 }
-
-bool overlaps(const char* a, size_t na, const char* b, size_t nb) { return a < b + nb && b < a + na; }
 
 // Workspace of the momentum pathway: the per-chunk partial sums (two 64 x 128
 // float32 tiles each) and the chunk coefficients.

@@ -1,0 +1,371 @@
+// libmuon C ABI of the sequence operators (the gated scan and the layer norm;
+// declared in include/muon.h): argument validation, workspace planning and
+// launches.  Nothing is allocated and nothing synchronises.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "host.h"
+#include "launch.h"
+
+using namespace muon;
+
+namespace {
+
+// Bytes an operand spans.
+struct Span {
+  const char* p;
+  size_t n;
+};
+Span span(const void* p, size_t bytes) { return {static_cast<const char*>(p), bytes}; }
+Span span(const muon_seq& s, int batch, int tokens, int heads, int width, size_t es) {
+  const long long last = (batch - 1) * s.sb + (tokens - 1) * s.st + (heads - 1) * s.sh + width;
+  return {static_cast<const char*>(s.p), static_cast<size_t>(last) * es};
+}
+// No output may overlap an input or another output (null operands overlap nothing).
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* a = outs.begin(); a != outs.end(); ++a) {
+    if (a->p == nullptr) continue;
+    for (const Span& b : ins)
+      if (b.p != nullptr && overlaps(a->p, a->n, b.p, b.n)) return true;
+    for (const Span* b = a + 1; b != outs.end(); ++b)
+      if (b->p != nullptr && overlaps(a->p, a->n, b->p, b->n)) return true;
+  }
+  return false;
+}
+
+bool seq_ok(const muon_seq& s, size_t es) {
+  return s.p != nullptr && aligned_to(s.p, es) && s.sb >= 0 && s.st >= 0 && s.sh >= 0;
+}
+// 16-byte loads of whole rows: every row starts aligned and holds a multiple of 16 bytes.
+SeqOperand operand(const muon_seq& s, int width, size_t es) {
+  const long long q = 16 / static_cast<long long>(es);
+  const bool vec = aligned16(s.p) && s.sb % q == 0 && s.st % q == 0 && s.sh % q == 0 && width % q == 0;
+  return {s.p, s.sb, s.st, s.sh, vec ? 1 : 0};
+}
+
+int check_dims(const muon_scan_args* a) {
+  if (a == nullptr) return MUON_EINVAL;
+  if (a->dtype != MUON_F32 && a->dtype != MUON_BF16) return MUON_EINVAL;
+  if (a->batch < 0 || a->tokens < 0 || a->heads <= 0 || a->groups <= 0 || a->heads % a->groups != 0 || a->P <= 0 || a->N <= 0)
+    return MUON_EINVAL;
+  if (a->N > kScanMaxN) return MUON_EUNSUPPORTED;
+  return MUON_OK;
+}
+int check_operands(const muon_scan_args* a) {
+  const size_t es = dtype_size(a->dtype);
+  if (!seq_ok(a->v, es) || !seq_ok(a->k, es) || !seq_ok(a->q, es) || !seq_ok(a->log_decay, 4)) return MUON_EINVAL;
+  if (a->gate.p != nullptr && !seq_ok(a->gate, 4)) return MUON_EINVAL;
+  if (a->S0 != nullptr && !aligned_to(a->S0, 4)) return MUON_EINVAL;
+  return MUON_OK;
+}
+
+// Workgroups that fill the chip: two on each of 256 compute units.
+constexpr long long kFill = 512;
+
+struct ScanPlan {
+  int pblocks, nchunks, nseg, seg_chunks, nsplit;
+  size_t states, dstates, seg, seg2, decay, decay2, parts, end;   // workspace offsets
+};
+// The walk of one sequence is serial, so with few sequences and heads the time
+// axis is cut into segments (their totals first, then all of them at once):
+// worth its second reading of the inputs only where segments of at least
+// kSegChunks chunks fill idle compute units.
+constexpr int kSegChunks = 4;
+
+int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
+  p->pblocks = (a->P + kScanRows - 1) / kScanRows;
+  p->nchunks = static_cast<int>((static_cast<long long>(a->tokens) + kScanChunk - 1) / kScanChunk);
+  const long long vrows = static_cast<long long>(a->batch) * a->heads * p->pblocks;
+  const long long walks = backward ? 2 * vrows : vrows;
+  if (a->batch == 0 || a->tokens == 0) {
+    p->nseg = p->nsplit = 1;
+    p->seg_chunks = 0;
+    p->end = kAlign;
+    return MUON_OK;
+  }
+  long long nseg = std::min<long long>(kFill / walks, p->nchunks / kSegChunks);
+  if (nseg < 1) nseg = 1;
+  p->seg_chunks = static_cast<int>((p->nchunks + nseg - 1) / nseg);
+  p->nseg = (p->nchunks + p->seg_chunks - 1) / p->seg_chunks;
+  const long long groups = static_cast<long long>(a->batch) * p->nchunks * a->groups;
+  p->nsplit = static_cast<int>(std::min<long long>(a->heads / a->groups, std::max<long long>(1, (kFill + groups - 1) / groups)));
+  const int per_split = (a->heads / a->groups + p->nsplit - 1) / p->nsplit;
+  p->nsplit = (a->heads / a->groups + per_split - 1) / per_split;   // none without heads
+  if (vrows * p->nseg > INT_MAX || groups * p->nsplit > INT_MAX) return MUON_EUNSUPPORTED;
+  const size_t tile = static_cast<size_t>(kScanRows) * scan_padded_n(a->N) * sizeof(float);
+  size_t off = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes, kAlign);
+    return at;
+  };
+  const size_t seg_bytes = p->nseg > 1 ? vrows * p->nseg * tile : 0, decay_bytes = p->nseg > 1 ? vrows * p->nseg * 4 : 0;
+  p->seg = take(seg_bytes);
+  p->decay = take(decay_bytes);
+  if (backward) {
+    p->seg2 = take(seg_bytes);
+    p->decay2 = take(decay_bytes);
+    p->states = take(vrows * p->nchunks * tile);
+    p->dstates = take(vrows * p->nchunks * tile);
+    const size_t half = static_cast<size_t>(a->batch) * a->tokens * a->groups * a->N;
+    if (p->nsplit > 1 && 2 * half / 256 + 1 > static_cast<size_t>(INT_MAX)) return MUON_EUNSUPPORTED;
+    p->parts = take(p->nsplit > 1 ? static_cast<size_t>(p->nsplit) * 2 * half * 4 : 0);
+  }
+  p->end = std::max(off, kAlign);
+  return MUON_OK;
+}
+
+size_t scan_bytes(const muon_scan_args* a, bool backward) {
+  ScanPlan p;
+  return check_dims(a) == MUON_OK && plan_scan(a, backward, &p) == MUON_OK ? p.end : 0;
+}
+
+ScanWalk walk_of(const muon_scan_args* a, const ScanPlan& p) {
+  ScanWalk w{};
+  const size_t es = dtype_size(a->dtype);
+  w.x = operand(a->v, a->P, es);
+  w.k = operand(a->k, a->N, es);
+  w.q = operand(a->q, a->N, es);
+  w.g = operand(a->log_decay, 1, 4);
+  if (a->gate.p != nullptr) w.b = operand(a->gate, 1, 4);
+  w.batch = a->batch; w.tokens = a->tokens; w.heads = a->heads; w.groups = a->groups;
+  w.P = a->P; w.N = a->N;
+  w.pblocks = p.pblocks; w.nchunks = p.nchunks; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
+  w.init = a->S0;
+  return w;
+}
+
+size_t state_bytes(const muon_scan_args* a) { return static_cast<size_t>(a->batch) * a->heads * a->P * a->N * 4; }
+size_t value_bytes(const muon_scan_args* a) {
+  return static_cast<size_t>(a->batch) * a->tokens * a->heads * a->P * dtype_size(a->dtype);
+}
+Span gate_span(const muon_scan_args* a) {
+  return a->gate.p == nullptr ? Span{nullptr, 0} : span(a->gate, a->batch, a->tokens, a->heads, 1, 4);
+}
+
+// S_out of a call without tokens is S0 (or zero).
+int copy_state(const muon_scan_args* a, float* dst, const float* src, hipStream_t st) {
+  const size_t n = state_bytes(a);
+  if (dst == nullptr || n == 0) return MUON_OK;
+  return launch_copy_f32(src, dst, static_cast<long long>(n / 4), st) == hipSuccess ? MUON_OK : MUON_EHIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t muon_gated_scan_workspace_size(const muon_scan_args* args) { return scan_bytes(args, false); }
+
+int muon_gated_scan(const muon_scan_args* a, void* Y, float* S_out, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_dims(a);
+  if (rc != MUON_OK) return rc;
+  ScanPlan p;
+  rc = plan_scan(a, false, &p);
+  if (rc != MUON_OK) return rc;
+  const size_t es = dtype_size(a->dtype);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (S_out != nullptr && !aligned_to(S_out, 4)) return MUON_EINVAL;
+  if (a->batch == 0) return MUON_OK;
+  const Span s0 = span(a->S0, state_bytes(a)), so = span(S_out, state_bytes(a));
+  if (a->tokens == 0) {
+    if ((a->S0 != nullptr && !aligned_to(a->S0, 4)) || clash({so}, {s0})) return MUON_EINVAL;
+    return copy_state(a, S_out, a->S0, st);
+  }
+  rc = check_operands(a);
+  if (rc != MUON_OK) return rc;
+  if (Y == nullptr || !aligned_to(Y, es)) return MUON_EINVAL;
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < p.end) return MUON_EWORKSPACE;
+  const Span v = span(a->v, a->batch, a->tokens, a->heads, a->P, es), k = span(a->k, a->batch, a->tokens, a->groups, a->N, es),
+             q = span(a->q, a->batch, a->tokens, a->groups, a->N, es),
+             g = span(a->log_decay, a->batch, a->tokens, a->heads, 1, 4);
+  if (clash({span(Y, value_bytes(a)), so, span(workspace, p.end)}, {v, k, q, g, gate_span(a), s0})) return MUON_EINVAL;
+  ScanWalk w = walk_of(a, p);
+  char* ws = static_cast<char*>(workspace);
+  w.y = Y;
+  w.yvec = a->P % 4 == 0 && aligned_to(Y, 4 * es);
+  w.fin = S_out;
+  w.seg_state = p.nseg > 1 ? reinterpret_cast<float*>(ws + p.seg) : nullptr;
+  w.seg_decay = p.nseg > 1 ? reinterpret_cast<float*>(ws + p.decay) : nullptr;
+  return launch_scan_walk(&w, 1, true, a->dtype == MUON_BF16, st) == hipSuccess ? MUON_OK : MUON_EHIP;
+}
+
+size_t muon_gated_scan_backward_workspace_size(const muon_scan_args* args) { return scan_bytes(args, true); }
+
+int muon_gated_scan_backward(const muon_scan_args* a, const muon_seq* dY, const float* dS, void* dV, void* dK, void* dQ,
+                             float* dlog_decay, float* dgate, float* dS0, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  int rc = check_dims(a);
+  if (rc != MUON_OK) return rc;
+  ScanPlan p;
+  rc = plan_scan(a, true, &p);
+  if (rc != MUON_OK) return rc;
+  const size_t es = dtype_size(a->dtype);
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  if ((dS != nullptr && !aligned_to(dS, 4)) || (dS0 != nullptr && !aligned_to(dS0, 4))) return MUON_EINVAL;
+  if (a->batch == 0) return MUON_OK;
+  const Span ds = span(dS, state_bytes(a)), ds0 = span(dS0, state_bytes(a)), s0 = span(a->S0, state_bytes(a));
+  if (a->tokens == 0) {
+    if (clash({ds0}, {ds, s0})) return MUON_EINVAL;
+    return copy_state(a, dS0, dS, st);
+  }
+  rc = check_operands(a);
+  if (rc != MUON_OK) return rc;
+  if (dY == nullptr || !seq_ok(*dY, es) || dV == nullptr || dK == nullptr || dQ == nullptr || dlog_decay == nullptr ||
+      !aligned_to(dV, es) || !aligned_to(dK, es) || !aligned_to(dQ, es) || !aligned_to(dlog_decay, 4) ||
+      (dgate != nullptr && !aligned_to(dgate, 4)))
+    return MUON_EINVAL;
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < p.end) return MUON_EWORKSPACE;
+  const Span v = span(a->v, a->batch, a->tokens, a->heads, a->P, es), k = span(a->k, a->batch, a->tokens, a->groups, a->N, es),
+             q = span(a->q, a->batch, a->tokens, a->groups, a->N, es),
+             g = span(a->log_decay, a->batch, a->tokens, a->heads, 1, 4),
+             dy = span(*dY, a->batch, a->tokens, a->heads, a->P, es);
+  const size_t keys = static_cast<size_t>(a->batch) * a->tokens * a->groups * a->N * es;
+  const size_t gates = static_cast<size_t>(a->batch) * a->tokens * a->heads * 4;
+  if (clash({span(dV, value_bytes(a)), span(dK, keys), span(dQ, keys), span(dlog_decay, gates), span(dgate, gates), ds0,
+             span(workspace, p.end)},
+            {v, k, q, g, gate_span(a), s0, dy, ds}))
+    return MUON_EINVAL;
+  const bool bf16 = a->dtype == MUON_BF16;
+  char* ws = static_cast<char*>(workspace);
+  const auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  // 1. the states before every chunk and the gradients of the states after it
+  ScanWalk w[2] = {walk_of(a, p), walk_of(a, p)};
+  w[0].states = at(p.states);
+  w[1].x = operand(*dY, a->P, es);
+  w[1].k = w[1].q;
+  w[1].reverse = 1;
+  w[1].init = dS;
+  w[1].fin = dS0;
+  w[1].states = at(p.dstates);
+  if (p.nseg > 1) {
+    w[0].seg_state = at(p.seg);
+    w[0].seg_decay = at(p.decay);
+    w[1].seg_state = at(p.seg2);
+    w[1].seg_decay = at(p.decay2);
+  }
+  if (launch_scan_walk(w, 2, false, bf16, st) != hipSuccess) return MUON_EHIP;
+  // 2. the gradients, chunk by chunk
+  ScanGrad r{};
+  r.v = w[0].x; r.k = w[0].k; r.q = w[0].q; r.dy = w[1].x; r.g = w[0].g; r.b = w[0].b;
+  r.batch = a->batch; r.tokens = a->tokens; r.heads = a->heads; r.groups = a->groups; r.P = a->P; r.N = a->N;
+  r.pblocks = p.pblocks; r.nchunks = p.nchunks; r.nsplit = p.nsplit;
+  r.dvvec = a->P % 4 == 0 && aligned_to(dV, 4 * es);
+  r.dkvec = a->N % 4 == 0 && aligned_to(dK, 4 * es) && aligned_to(dQ, 4 * es);
+  r.states = at(p.states);
+  r.dstates = at(p.dstates);
+  r.dv = dV; r.dk = dK; r.dq = dQ; r.dg = dlog_decay; r.db = dgate;
+  r.parts = at(p.parts);
+  return launch_scan_grad(r, bf16, st) == hipSuccess ? MUON_OK : MUON_EHIP;
+}
+
+int muon_gated_scan_step(const muon_scan_args* a, void* Y, float* S_out, void* stream) {
+  int rc = check_dims(a);
+  if (rc != MUON_OK) return rc;
+  if (a->tokens != 1) return MUON_EINVAL;
+  if (a->batch == 0) return MUON_OK;
+  rc = check_operands(a);
+  if (rc != MUON_OK) return rc;
+  const size_t es = dtype_size(a->dtype);
+  // whole 16-byte accesses of the states where their rows are
+  const size_t sa = a->N % 4 == 0 ? 16 : 4;
+  if (Y == nullptr || !aligned_to(Y, es) || a->S0 == nullptr || S_out == nullptr || !aligned_to(a->S0, sa) || !aligned_to(S_out, sa))
+    return MUON_EINVAL;
+  const Span v = span(a->v, a->batch, 1, a->heads, a->P, es), k = span(a->k, a->batch, 1, a->groups, a->N, es),
+             q = span(a->q, a->batch, 1, a->groups, a->N, es), g = span(a->log_decay, a->batch, 1, a->heads, 1, 4);
+  const Span s0 = span(a->S0, state_bytes(a)), so = span(S_out, state_bytes(a));
+  const bool in_place = a->S0 == S_out;
+  if (clash({span(Y, value_bytes(a)), so}, {v, k, q, g, gate_span(a), in_place ? Span{nullptr, 0} : s0})) return MUON_EINVAL;
+  if (static_cast<long long>(a->batch) * a->heads * ((a->P + 15) / 16) > INT_MAX) return MUON_EUNSUPPORTED;
+  ScanStep s{};
+  s.v = operand(a->v, a->P, es);
+  s.k = operand(a->k, a->N, es);
+  s.q = operand(a->q, a->N, es);
+  s.g = operand(a->log_decay, 1, 4);
+  if (a->gate.p != nullptr) s.b = operand(a->gate, 1, 4);
+  s.batch = a->batch; s.heads = a->heads; s.groups = a->groups; s.P = a->P; s.N = a->N;
+  s.y = Y;
+  s.S = a->S0;
+  s.S_out = S_out;
+  return launch_scan_step(s, a->dtype == MUON_BF16, static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_EHIP;
+}
+
+// ---------------------------------------------------------------------------
+// layer norm
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_norm(int dtype, long long rows, int n) {
+  if (dtype != MUON_F32 && dtype != MUON_BF16) return MUON_EINVAL;
+  if (rows < 0 || n <= 0) return MUON_EINVAL;
+  return rows > INT_MAX ? MUON_EUNSUPPORTED : MUON_OK;
+}
+Span rows_span(const void* p, long long rows, int n, long long ld, size_t es) {
+  return span(p, rows == 0 ? 0 : static_cast<size_t>((rows - 1) * ld + n) * es);
+}
+bool rows_vec(const void* p, long long ld, int n, size_t es) {
+  const long long q = 16 / static_cast<long long>(es);
+  return aligned16(p) && ld % q == 0 && n % q == 0;
+}
+
+}  // namespace
+
+int muon_layer_norm(const void* X, long long ldx, int dtype, long long rows, int n, const float* weight, const float* bias,
+                    float eps, int center, void* Y, long long ldy, float* mean, float* rstd, void* stream) {
+  const int rc = check_norm(dtype, rows, n);
+  if (rc != MUON_OK) return rc;
+  if (!(eps >= 0.0f) || !std::isfinite(eps) || (center != 0 && center != 1) || ldx < n || ldy < n) return MUON_EINVAL;
+  if (rows == 0) return MUON_OK;
+  const size_t es = dtype_size(dtype);
+  if (X == nullptr || Y == nullptr || !aligned_to(X, es) || !aligned_to(Y, es) || !aligned_to(weight, 4) ||
+      !aligned_to(bias, 4) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return MUON_EINVAL;
+  const size_t params = static_cast<size_t>(n) * 4, stats = static_cast<size_t>(rows) * 4;
+  if (clash({rows_span(Y, rows, n, ldy, es), span(mean, stats), span(rstd, stats)},
+            {rows_span(X, rows, n, ldx, es), span(weight, params), span(bias, params)}))
+    return MUON_EINVAL;
+  NormLaunch A{};
+  A.x = X; A.y = Y; A.ldx = ldx; A.ldy = ldy; A.rows = rows; A.n = n; A.center = center;
+  A.vec = rows_vec(X, ldx, n, es) && rows_vec(Y, ldy, n, es);
+  A.pvec = aligned16(weight) && aligned16(bias) && n % 4 == 0;
+  A.w = weight; A.bias = bias; A.eps = eps; A.mean = mean; A.rstd = rstd;
+  return launch_norm(A, dtype == MUON_BF16, static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_EHIP;
+}
+
+size_t muon_layer_norm_backward_workspace_size(long long rows, int n, int dtype) {
+  if (check_norm(dtype, rows, n) != MUON_OK) return 0;
+  return align_up(static_cast<size_t>(norm_grad_parts(rows, n, dtype == MUON_BF16)) * 2 * n * 4, kAlign);
+}
+
+int muon_layer_norm_backward(const void* dY, long long lddy, const void* X, long long ldx, int dtype, long long rows, int n,
+                             const float* weight, const float* mean, const float* rstd, void* dX, long long lddx,
+                             float* dweight, float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_norm(dtype, rows, n);
+  if (rc != MUON_OK) return rc;
+  if (lddy < n || ldx < n || lddx < n) return MUON_EINVAL;
+  const size_t es = dtype_size(dtype), need = muon_layer_norm_backward_workspace_size(rows, n, dtype);
+  if (!aligned_to(dweight, 4) || !aligned_to(dbias, 4) || !aligned_to(weight, 4)) return MUON_EINVAL;
+  if (rows == 0 && dweight == nullptr && dbias == nullptr) return MUON_OK;
+  if (rows > 0 && (dY == nullptr || X == nullptr || dX == nullptr || rstd == nullptr || !aligned_to(dY, es) || !aligned_to(X, es) ||
+                   !aligned_to(dX, es) || !aligned_to(mean, 4) || !aligned_to(rstd, 4)))
+    return MUON_EINVAL;
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < need) return MUON_EWORKSPACE;
+  const size_t params = static_cast<size_t>(n) * 4, stats = static_cast<size_t>(rows) * 4;
+  if (clash({rows_span(dX, rows, n, lddx, es), span(dweight, params), span(dbias, params), span(workspace, need)},
+            {rows_span(dY, rows, n, lddy, es), rows_span(X, rows, n, ldx, es), span(weight, params), span(mean, stats),
+             span(rstd, stats)}))
+    return MUON_EINVAL;
+  NormGradLaunch A{};
+  A.dy = dY; A.x = X; A.dx = dX; A.lddy = lddy; A.ldx = ldx; A.lddx = lddx; A.rows = rows; A.n = n;
+  A.vec = rows_vec(dY, lddy, n, es) && rows_vec(X, ldx, n, es) && rows_vec(dX, lddx, n, es);
+  A.w = weight; A.mean = mean; A.rstd = rstd; A.dw = dweight; A.dbias = dbias;
+  A.part = static_cast<float*>(workspace);
+  A.parts = norm_grad_parts(rows, n, dtype == MUON_BF16);
+  return launch_norm_grad(A, dtype == MUON_BF16, static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_EHIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,258 @@
+// Tiles, fragments and gates of the gated scan kernels (gated_scan.hip,
+// gated_scan_backward.hip).
+//
+// Products run on 16 x 16 matrix-core tiles with 32 contraction terms a step.
+// Lane l of the wave (g = l / 16) holds, of either operand, row l % 16 at the
+// 8 contraction indices 8 g + 0..7, and of the result column l % 16 (the
+// second operand's row), rows 4 g + 0..3 (the first operand's).  Any
+// permutation of the contraction indices that both operands share gives the
+// same product, so a result kept in registers can be the next product's
+// operand without a trip through LDS (Frag::from_acc).  bfloat16 operands
+// take one v_mfma_f32_16x16x32_bf16 per step, float32 ones eight
+// v_mfma_f32_16x16x4f32.
+#pragma once
+#include "launch.h"
+
+namespace muon {
+namespace scan {
+
+constexpr int kQ = kScanChunk;   // tokens per chunk
+constexpr int kPB = kScanRows;   // state rows (value components) per workgroup
+constexpr int kThreads = 256;
+constexpr float kLog2e = 1.44269504088896340736f;
+// log decays below this are taken as this: e^-10000 is 0 in float32 and in
+// float64 alike, and sums of 64 of them stay finite
+constexpr float kMinLogDecay = -1.0e4f;
+
+struct FragF32 {
+  float v[8];
+};
+
+template <typename T>
+struct Ops;
+
+template <>
+struct Ops<bf16_t> {
+  typedef bf16x8_t Frag;
+  static constexpr int kVec = 8;      // elements per 16 bytes
+  static constexpr int kPad = 8;      // elements appended to an LDS row
+  static constexpr int kSplit = 3;    // bf16 pieces that carry a float32's 24 bits
+  __device__ static __forceinline__ f32x4_t mma(Frag a, Frag b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  // 8 consecutive elements
+  __device__ static __forceinline__ Frag row(const bf16_t* p) {
+    return __builtin_bit_cast(Frag, *reinterpret_cast<const u32x4_t*>(p));
+  }
+  // two runs of 4 consecutive elements
+  __device__ static __forceinline__ Frag row2(const bf16_t* p, const bf16_t* q) {
+    const u32x2_t a = *reinterpret_cast<const u32x2_t*>(p), b = *reinterpret_cast<const u32x2_t*>(q);
+    return __builtin_bit_cast(Frag, u32x4_t{a[0], a[1], b[0], b[1]});
+  }
+  // column col0 + l % 16 of rows row0 + 8 g + 0..7 (ds_read_b64_tr_b16: in
+  // each 16-lane group the lanes address a 4 x 16 block, 4 elements each, and
+  // receive one column)
+  __device__ static __forceinline__ Frag col(const bf16_t* tile, int ld, int row0, int col0, int lane) {
+    const bf16_t* p = tile + (row0 + 8 * (lane >> 4) + ((lane & 15) >> 2)) * ld + col0 + 4 * (lane & 3);
+    const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
+    const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(p + 4 * ld));
+    const u32x2_t ua = __builtin_bit_cast(u32x2_t, a), ub = __builtin_bit_cast(u32x2_t, b);
+    return __builtin_bit_cast(Frag, u32x4_t{ua[0], ua[1], ub[0], ub[1]});
+  }
+  __device__ static __forceinline__ void widen(Frag f, float (&o)[8]) {
+    const u32x4_t w = __builtin_bit_cast(u32x4_t, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = lo_bf16(w[i]);
+      o[2 * i + 1] = hi_bf16(w[i]);
+    }
+  }
+  __device__ static __forceinline__ Frag narrow(const float (&v)[8]) {
+    return __builtin_bit_cast(Frag, u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                            pack_bf16x2(v[6], v[7])});
+  }
+  // acc += (float32 operand) b: the operand as three bfloat16 pieces (rounded,
+  // then the remainder, then its remainder), so its 24 bits all count
+  __device__ static __forceinline__ void split(const float (&v)[8], Frag (&f)[kSplit]) {
+    float r[8], w[8];
+    f[0] = narrow(v);
+    widen(f[0], w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = v[i] - w[i];
+    f[1] = narrow(r);
+    widen(f[1], w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = r[i] - w[i];
+    f[2] = narrow(r);
+  }
+  __device__ static __forceinline__ void store4(bf16_t* p, f32x4_t v) {
+    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  }
+  __device__ static __forceinline__ f32x4_t load4(const bf16_t* p) {
+    const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
+    return f32x4_t{lo_bf16(w[0]), hi_bf16(w[0]), lo_bf16(w[1]), hi_bf16(w[1])};
+  }
+  __device__ static __forceinline__ bf16_t from_f32(float v) { return f32_to_bf16(v); }
+};
+
+template <>
+struct Ops<float> {
+  typedef FragF32 Frag;
+  static constexpr int kVec = 4;
+  static constexpr int kPad = 4;
+  static constexpr int kSplit = 1;
+  __device__ static __forceinline__ f32x4_t mma(const Frag& a, const Frag& b, f32x4_t c) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
+    return c;
+  }
+  __device__ static __forceinline__ Frag row2(const float* p, const float* q) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(q);
+    return Frag{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+  }
+  __device__ static __forceinline__ Frag row(const float* p) { return row2(p, p + 4); }
+  __device__ static __forceinline__ Frag col(const float* tile, int ld, int row0, int col0, int lane) {
+    const float* p = tile + (row0 + 8 * (lane >> 4)) * ld + col0 + (lane & 15);
+    Frag f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f.v[e] = p[e * ld];
+    return f;
+  }
+  __device__ static __forceinline__ void widen(const Frag& f, float (&o)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = f.v[i];
+  }
+  __device__ static __forceinline__ Frag narrow(const float (&v)[8]) {
+    Frag f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f.v[i] = v[i];
+    return f;
+  }
+  __device__ static __forceinline__ void split(const float (&v)[8], Frag (&f)[kSplit]) { f[0] = narrow(v); }
+  __device__ static __forceinline__ void store4(float* p, f32x4_t v) { *reinterpret_cast<f32x4_t*>(p) = v; }
+  __device__ static __forceinline__ f32x4_t load4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
+  __device__ static __forceinline__ float from_f32(float v) { return v; }
+};
+
+// Fragment of a float32 result held in two accumulator tiles (rows 0..15 and
+// 16..31 of a 32-row block): contraction indices 4 g + 0..3 of each.
+template <typename T>
+__device__ __forceinline__ typename Ops<T>::Frag frag_from_acc(f32x4_t a, f32x4_t b) {
+  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return Ops<T>::narrow(v);
+}
+
+// A [kQ][WIDTH] tile of a sequence operand on its way into LDS: 16-byte pieces
+// held in registers.  Rows past `rows` and columns past `width` are zero.
+template <typename T, int WIDTH>
+struct TileLoad {
+  static constexpr int kVec = Ops<T>::kVec;
+  static constexpr int kRowPieces = WIDTH / kVec;
+  static constexpr int kPieces = kQ * kRowPieces / kThreads;
+  static constexpr int kLd = WIDTH + Ops<T>::kPad;
+  u32x4_t r[kPieces];
+
+  // p: element (token 0, column 0); vec: 16-byte loads are aligned and width
+  // is a multiple of a piece
+  __device__ __forceinline__ void load(const T* p, long long st, int rows, int width, bool vec) {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int idx = i * kThreads + static_cast<int>(threadIdx.x);
+      const int row = idx / kRowPieces, col = (idx % kRowPieces) * kVec;
+      r[i] = u32x4_t{0u, 0u, 0u, 0u};
+      if (row < rows && col < width) {
+        const T* e = p + row * st + col;
+        if (vec) {
+          r[i] = *reinterpret_cast<const u32x4_t*>(e);
+        } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (col + j < width) r[i][j / 2] |= static_cast<uint32_t>(e[j]) << (16 * (j & 1));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col + j < width) r[i][j] = __float_as_uint(e[j]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* lds) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int idx = i * kThreads + static_cast<int>(threadIdx.x);
+      const int row = idx / kRowPieces, col = (idx % kRowPieces) * kVec;
+      *reinterpret_cast<u32x4_t*>(lds + row * kLd + col) = r[i];
+    }
+  }
+};
+
+// Inclusive sums over the lanes of a wave, in float64.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_rows_d(double v) {
+  const long long b = __double_as_longlong(v);
+  const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROWS, 0xf, false);
+  return __longlong_as_double((static_cast<long long>(hi) << 32) | static_cast<unsigned>(lo));
+}
+__device__ __forceinline__ double wave_prefix_d(double v) {
+  v += dpp_rows_d<kDppShr1, 0xf>(v);
+  v += dpp_rows_d<kDppShr2, 0xf>(v);
+  v += dpp_rows_d<kDppShr4, 0xf>(v);
+  v += dpp_rows_d<kDppShr8, 0xf>(v);
+  v += dpp_rows_d<kDppBcast15, 0xa>(v);
+  v += dpp_rows_d<kDppBcast31, 0xc>(v);
+  return v;
+}
+__device__ __forceinline__ double read_lane_d(double v, int lane) {
+  const long long b = __double_as_longlong(v);
+  const int lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
+  const int hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
+  return __longlong_as_double((static_cast<long long>(hi) << 32) | static_cast<unsigned>(lo));
+}
+
+// One chunk's gates.  c is the inclusive prefix sum of the log2 decays, summed
+// in float64 and kept as two floats, so that e^{c_i - c_j} keeps float32
+// accuracy after a reset (log decay -inf) has made both sums large.
+struct Gates {
+  float hi[kQ], lo[kQ];   // c
+  float b[kQ];            // input gates
+  float first[kQ];        // e^{c_i}
+  float last[kQ];         // e^{c_end - c_j}
+  float own[kQ];          // e^{g_t}
+  float end[4];           // e^{c_end}
+};
+
+// lane = token; by one wave.  Returns c_end.
+__device__ __forceinline__ double write_gates(Gates& G, float log_decay, float gate, int lane) {
+  const float ld = log_decay < kMinLogDecay ? kMinLogDecay : log_decay;   // keeps NaN
+  const double c = wave_prefix_d(static_cast<double>(ld) * static_cast<double>(1.44269504088896340736));
+  const double e = read_lane_d(c, 63);
+  const float hi = static_cast<float>(c);
+  G.hi[lane] = hi;
+  G.lo[lane] = static_cast<float>(c - static_cast<double>(hi));
+  G.b[lane] = gate;
+  G.own[lane] = __builtin_amdgcn_exp2f(ld * kLog2e);
+  G.first[lane] = __builtin_amdgcn_exp2f(static_cast<float>(c));
+  G.last[lane] = __builtin_amdgcn_exp2f(static_cast<float>(e - c));
+  if (lane == 0) G.end[0] = __builtin_amdgcn_exp2f(static_cast<float>(e));
+  return e;
+}
+
+__device__ __forceinline__ float between(float hi_i, float lo_i, float hi_j, float lo_j) {
+  return __builtin_amdgcn_exp2f((hi_i - hi_j) + (lo_i - lo_j));
+}
+
+// The ten 16 x 16 tiles on and below the diagonal of a kQ x kQ matrix, dealt
+// to four waves (three at most each): tile t of wave w is (row, column) block
+// (tile_row(w, t), tile_col(w, t)).
+constexpr int kMaxTiles = 3;
+__device__ __forceinline__ int tile_count(int w) { return w == 3 ? 1 : 3; }
+__device__ __forceinline__ int tile_row(int w, int t) {
+  return t < 2 ? (w < 2 ? 3 : 2) : (w == 0 ? 0 : 1);
+}
+__device__ __forceinline__ int tile_col(int w, int t) {
+  return t == 2 ? (w == 2 ? 1 : 0) : (w == 1 || w == 3 ? 2 + t : t);
+}
+
+}  // namespace scan
+}  // namespace muon
