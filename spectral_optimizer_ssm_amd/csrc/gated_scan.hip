@@ -24,6 +24,9 @@ namespace {
 
 using namespace scan;
 
+constexpr int kWalkThreads = 512;
+constexpr int kStepThreads = 256;
+
 template <typename T, int NT>
 struct WalkLds {
   static constexpr int kLdN = NT + Ops<T>::kPad;
@@ -32,10 +35,11 @@ struct WalkLds {
   static constexpr int k = 0;                                   // k [kQ][NT]
   static constexpr int x = k + kQ * kLdN * (int)sizeof(T);      // x [kQ][kPB]
   static constexpr int gates = x + kQ * kLdP * (int)sizeof(T);  // Gates[2]
-  static constexpr int states_bytes = gates + 2 * (int)sizeof(Gates);
+  static constexpr int states_bytes = gates + 2 * (int)sizeof(Gates<kQ>);
   static constexpr int q = states_bytes;                        // q [kQ][NT]
   static constexpr int m = q + kQ * kLdN * (int)sizeof(T);      // weights M [i][j]
-  static constexpr int read_bytes = m + kQ * kLdM * (int)sizeof(T);
+  static constexpr int y = m + kQ * kLdM * (int)sizeof(T);      // halves of y that waves hand over [8][2][64] float4
+  static constexpr int read_bytes = y + 8 * 2 * 64 * 16;
 };
 
 struct WalkPair {
@@ -43,21 +47,28 @@ struct WalkPair {
 };
 
 // READ: y is computed (q is read); else only states move.
+//
+// Wave w holds rows p = 16 (w % 4) + 0..15 of S and columns n of half w / 4:
+// the tokens' products with the halves are partial sums of y, which the two
+// waves of the same rows exchange through LDS, each finishing half of the
+// tokens.  Eight waves a workgroup rather than four (160 -> ... us).
 template <typename T, int NT, bool READ>
-__global__ void __launch_bounds__(kThreads, 2) scan_walk_kernel(WalkPair W) {
+__global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_walk_kernel(WalkPair W) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
   typedef WalkLds<T, NT> L;
-  constexpr int kT = NT / 16;       // state tiles of a wave
+  constexpr int kT = NT / 32;       // state tiles of a wave
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const ScanWalk& A = W.w[blockIdx.y];
   T* lk = reinterpret_cast<T*>(lds + L::k);
   T* lx = reinterpret_cast<T*>(lds + L::x);
   T* lq = reinterpret_cast<T*>(lds + L::q);
   T* lm = reinterpret_cast<T*>(lds + L::m);
-  Gates* gates = reinterpret_cast<Gates*>(lds + L::gates);
+  f32x4_t* ly = reinterpret_cast<f32x4_t*>(lds + L::y);
+  Gates<kQ>* gates = reinterpret_cast<Gates<kQ>*>(lds + L::gates);
 
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, l16 = lane & 15, g4 = lane >> 4;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, g4 = lane >> 4;
+  const int pw = w & 3, nh = w >> 2, nbase = nh * (NT / 2);
   const int vheads = A.heads * A.pblocks;
   const long long item = blockIdx.x;
   const int seg = static_cast<int>(item % A.nseg);
@@ -78,31 +89,33 @@ __global__ void __launch_bounds__(kThreads, 2) scan_walk_kernel(WalkPair W) {
 
   // token of a lane in the cc-th chunk visited; its gates (past the end: no decay, no input)
   const auto chunk_of = [&](int cc) { return A.reverse ? A.nchunks - 1 - cc : cc; };
-  const auto load_gates = [&](int cc, float& gv, float& bv) {
+  float gv[1] = {0.0f}, bv[1] = {0.0f};
+  const auto load_gates = [&](int cc) {
     const long long t = static_cast<long long>(chunk_of(cc)) * kQ + lane;
-    gv = 0.0f;
-    bv = 0.0f;
+    gv[0] = 0.0f;
+    bv[0] = 0.0f;
     if (t < A.tokens) {
-      gv = gp[t * A.g.st];
-      bv = bp == nullptr ? 1.0f : bp[t * A.b.st];
+      gv[0] = gp[t * A.g.st];
+      bv[0] = bp == nullptr ? 1.0f : bp[t * A.b.st];
     }
   };
 
-  TileLoad<T, NT> tk, tq;
-  TileLoad<T, kPB> tx;
-  const auto load_tiles = [&](int cc) {
+  TileLoad<T, NT, kQ, kWalkThreads> tk, tq;
+  TileLoad<T, kPB, kQ, kWalkThreads> tx;
+  const auto load_tiles = [&](int cc, int tid) {
     const long long t0 = static_cast<long long>(chunk_of(cc)) * kQ;
     const int rows = A.tokens - t0 < kQ ? static_cast<int>(A.tokens - t0) : kQ;
-    tk.load(kp + t0 * A.k.st, A.k.st, rows, A.N, A.k.vec);
-    tx.load(xp + t0 * A.x.st, A.x.st, rows, rows_p, A.x.vec && rows_p % O::kVec == 0);
-    if constexpr (READ) tq.load(qp + t0 * A.q.st, A.q.st, rows, A.N, A.q.vec);
+    tk.load(kp + t0 * A.k.st, A.k.st, rows, A.N, A.k.vec, tid);
+    tx.load(xp + t0 * A.x.st, A.x.st, rows, rows_p, A.x.vec && rows_p % O::kVec == 0, tid);
+    if constexpr (READ) tq.load(qp + t0 * A.q.st, A.q.st, rows, A.N, A.q.vec, tid);
   };
 
-  // the state: tile t holds S^T rows n = 16 t + 4 g4 + 0..3, column p = 16 w + l16
+  // the state: tile t holds S^T rows n = nbase + 16 t + 4 g4 + 0..3, column p = 16 pw + l16
   f32x4_t st[kT];
-  const int prow = pb * kPB + 16 * w + l16;
+  const int prow = pb * kPB + 16 * pw + l16;
+  const long long tile_off = static_cast<long long>(16 * pw + l16) * NT + nbase + 4 * g4;
   if (A.seg_state != nullptr && !A.totals) {
-    const float* sp = A.seg_state + ((vrow * A.nseg + seg) * kPB + 16 * w + l16) * NT + 4 * g4;
+    const float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off;
 #pragma unroll
     for (int t = 0; t < kT; ++t) st[t] = *reinterpret_cast<const f32x4_t*>(sp + 16 * t);
   } else {
@@ -112,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_walk_kernel(WalkPair W) {
     for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int n = 16 * t + 4 * g4 + r;
+        const int n = nbase + 16 * t + 4 * g4 + r;
         st[t][r] = init && prow < A.P && n < A.N ? sp[n] : 0.0f;
       }
   }
@@ -126,72 +139,71 @@ __global__ void __launch_bounds__(kThreads, 2) scan_walk_kernel(WalkPair W) {
       for (int e = 0; e < 4; ++e) lm[(r0 + l16) * L::kLdM + c0 + 4 * g4 + e] = O::from_f32(0.0f);
     }
   }
-  float gv = 0.0f, bv = 0.0f;
   double seg_log = 0.0;
-  load_tiles(cc0);
-  if (w == 3) {
-    load_gates(cc0, gv, bv);
+  load_tiles(cc0, threadIdx.x);
+  if (w == 7) {
+    load_gates(cc0);
     seg_log += write_gates(gates[cc0 & 1], gv, bv, lane);
-    if (cc0 + 1 < cc1) load_gates(cc0 + 1, gv, bv);
+    if (cc0 + 1 < cc1) load_gates(cc0 + 1);
   }
   for (int cc = cc0; cc < cc1; ++cc) {
     __syncthreads();   // the last chunk's tiles are done with
-    tk.store(lk);
-    tx.store(lx);
-    if constexpr (READ) tq.store(lq);
+    tk.store(lk, threadIdx.x);
+    tx.store(lx, threadIdx.x);
+    if constexpr (READ) tq.store(lq, threadIdx.x);
     __syncthreads();
-    const Gates& G = gates[cc & 1];
-    if (cc + 1 < cc1) {
-      load_tiles(cc + 1);
-      if (w == 3) {
-        seg_log += write_gates(gates[(cc + 1) & 1], gv, bv, lane);
-        if (cc + 2 < cc1) load_gates(cc + 2, gv, bv);
-      }
-    }
-    const long long t0 = static_cast<long long>(chunk_of(cc)) * kQ;
+    const Gates<kQ>& G = gates[cc & 1];
+    if (cc + 1 < cc1) load_tiles(cc + 1, threadIdx.x);
+    const int chunk = chunk_of(cc);
+    const long long t0 = static_cast<long long>(chunk) * kQ;
 
-    f32x4_t y[4];   // y^T: rows p = 16 w + 4 g4 + 0..3, column i = 16 it + l16
+    f32x4_t y[4];   // y^T: rows p = 16 pw + 4 g4 + 0..3, column i = 16 it + l16
     if constexpr (READ) {
       // M^T tiles: rows j, columns i, so a lane's four values are neighbours in M
-      const int nt = tile_count(w);
+      for (int e = w; e < 10; e += 8) {
+        const int it = tile_row(e), jt = tile_col(e, it);
+        f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int t = 0; t < kMaxTiles; ++t) {
-        if (t < nt) {
-          const int it = tile_row(w, t), jt = tile_col(w, t);
-          f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < NT / 32; ++s)
+          a = O::mma(O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4),
+                     O::row(lq + (16 * it + l16) * L::kLdN + 32 * s + 8 * g4), a);
+        const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
+        const float hi = G.hi[i], lo = G.lo[i];
+        const f32x4_t jh = *reinterpret_cast<const f32x4_t*>(G.hi + j0), jl = *reinterpret_cast<const f32x4_t*>(G.lo + j0);
+        const f32x4_t jb = *reinterpret_cast<const f32x4_t*>(G.b + j0);
 #pragma unroll
-          for (int s = 0; s < NT / 32; ++s)
-            a = O::mma(O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4),
-                       O::row(lq + (16 * it + l16) * L::kLdN + 32 * s + 8 * g4), a);
-          const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
-          const float hi = G.hi[i], lo = G.lo[i];
-          const f32x4_t jh = *reinterpret_cast<const f32x4_t*>(G.hi + j0), jl = *reinterpret_cast<const f32x4_t*>(G.lo + j0);
-          const f32x4_t jb = *reinterpret_cast<const f32x4_t*>(G.b + j0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) a[r] = j0 + r <= i ? a[r] * between(hi, lo, jh[r], jl[r]) * jb[r] : 0.0f;
-          O::store4(lm + i * L::kLdM + j0, a);
-        }
+        for (int r = 0; r < 4; ++r) a[r] = j0 + r <= i ? a[r] * between(hi, lo, jh[r], jl[r]) * jb[r] : 0.0f;
+        O::store4(lm + i * L::kLdM + j0, a);
       }
-      // what S_in gives: e^{c_i} S_in q_i
+      // what this half of S_in gives: S_in q_i
 #pragma unroll
       for (int it = 0; it < 4; ++it) y[it] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int s = 0; s < NT / 32; ++s) {
+      for (int s = 0; s < kT / 2; ++s) {
         const Frag f = frag_from_acc<T>(st[2 * s], st[2 * s + 1]);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-          const T* qr = lq + (16 * it + l16) * L::kLdN + 32 * s + 4 * g4;
+          const T* qr = lq + (16 * it + l16) * L::kLdN + nbase + 32 * s + 4 * g4;
           y[it] = O::mma(f, O::row2(qr, qr + 16), y[it]);
         }
       }
+      // token tiles 2 nh and 2 nh + 1 stay, the others go to the other half's wave
 #pragma unroll
-      for (int it = 0; it < 4; ++it) y[it] *= G.first[16 * it + l16];
+      for (int u = 0; u < 2; ++u) {
+        ly[(w * 2 + u) * 64 + lane] = nh == 0 ? y[2 + u] : y[u];
+        y[u] = nh == 0 ? y[u] : y[2 + u];
+      }
     }
-    if (A.states != nullptr) {
-      // the state that the chunk starts from (in reversed time: ends with)
-      float* sp = A.states + ((vrow * A.nchunks + chunk_of(cc)) * kPB + 16 * w + l16) * NT + 4 * g4;
+    // the state that a block of `keep` chunks starts from (in reversed time: ends with)
+    if (A.states != nullptr &&
+        (A.reverse ? chunk % A.keep == A.keep - 1 || chunk == A.nchunks - 1 : chunk % A.keep == 0)) {
+      float* sp = A.states + (vrow * A.nblocks + chunk / A.keep) * (kPB * NT) + tile_off;
 #pragma unroll
       for (int t = 0; t < kT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
+    }
+    if (w == 7 && cc + 1 < cc1) {
+      seg_log += write_gates(gates[(cc + 1) & 1], gv, bv, lane);
+      if (cc + 2 < cc1) load_gates(cc + 2);
     }
 
     // the chunk's own part of the state
@@ -200,42 +212,54 @@ __global__ void __launch_bounds__(kThreads, 2) scan_walk_kernel(WalkPair W) {
     for (int t = 0; t < kT; ++t) st[t] *= end;
 #pragma unroll
     for (int s = 0; s < kQ / 32; ++s) {
-      float xv[8];
-      O::widen(O::col(lx, L::kLdP, 32 * s, 16 * w, lane), xv);
+      float xv[8], wv[8];
+      O::widen(O::col(lx, L::kLdP, 32 * s, 16 * pw, lane), xv);
       const int j0 = 32 * s + 8 * g4;
+      if (A.reverse) {
+        load8(G.first + j0, wv);
+      } else {
+        float bw[8];
+        load8(G.last + j0, wv);
+        load8(G.b + j0, bw);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) xv[e] *= A.reverse ? G.first[j0 + e] : G.last[j0 + e] * G.b[j0 + e];
-      Frag f[O::kSplit];
+        for (int e = 0; e < 8; ++e) wv[e] *= bw[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xv[e] *= wv[e];
+      Frag f[O::kSplit], kf[kT];
       O::split(xv, f);
 #pragma unroll
-      for (int t = 0; t < kT; ++t) {
-        const Frag kf = O::col(lk, L::kLdN, 32 * s, 16 * t, lane);
+      for (int t = 0; t < kT; ++t) kf[t] = O::col(lk, L::kLdN, 32 * s, nbase + 16 * t, lane);
 #pragma unroll
-        for (int u = O::kSplit - 1; u >= 0; --u) st[t] = O::mma(kf, f[u], st[t]);
-      }
+      for (int u = O::kSplit - 1; u >= 0; --u)
+#pragma unroll
+        for (int t = 0; t < kT; ++t) st[t] = O::mma(kf[t], f[u], st[t]);
     }
 
     if constexpr (READ) {
-      __syncthreads();   // M is written
+      __syncthreads();   // M and the halves of y are written
+      const int p0 = 16 * pw + 4 * g4;
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Frag vf = O::col(lx, L::kLdP, 32 * s, 16 * w, lane);
+      for (int u = 0; u < 2; ++u) y[u] = (y[u] + ly[((w ^ 4) * 2 + u) * 64 + lane]) * G.first[32 * nh + 16 * u + l16];
 #pragma unroll
-        for (int it = 2 * s; it < 4; ++it)
-          y[it] = O::mma(vf, O::row(lm + (16 * it + l16) * L::kLdM + 32 * s + 8 * g4), y[it]);
-      }
-      const int p0 = 16 * w + 4 * g4;
+      for (int s = 0; s < 2; ++s)
+        if (s <= nh) {
+          const Frag vf = O::col(lx, L::kLdP, 32 * s, 16 * pw, lane);
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const long long t = t0 + 16 * it + l16;
+          for (int u = 0; u < 2; ++u)
+            y[u] = O::mma(vf, O::row(lm + (32 * nh + 16 * u + l16) * L::kLdM + 32 * s + 8 * g4), y[u]);
+        }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const long long t = t0 + 32 * nh + 16 * u + l16;
         if (t < A.tokens && p0 < rows_p) {
           T* yp = static_cast<T*>(A.y) + ((bi * A.tokens + t) * A.heads + h) * A.P + pb * kPB + p0;
           if (A.yvec) {
-            O::store4(yp, y[it]);
+            O::store4(yp, y[u]);
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              if (p0 + r < rows_p) yp[r] = O::from_f32(y[it][r]);
+              if (p0 + r < rows_p) yp[r] = O::from_f32(y[u][r]);
           }
         }
       }
@@ -243,17 +267,17 @@ __global__ void __launch_bounds__(kThreads, 2) scan_walk_kernel(WalkPair W) {
   }
 
   if (A.totals) {
-    float* sp = A.seg_state + ((vrow * A.nseg + seg) * kPB + 16 * w + l16) * NT + 4 * g4;
+    float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off;
 #pragma unroll
     for (int t = 0; t < kT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
-    if (w == 3 && lane == 0) A.seg_decay[vrow * A.nseg + seg] = __builtin_amdgcn_exp2f(static_cast<float>(seg_log));
+    if (w == 7 && lane == 0) A.seg_decay[vrow * A.nseg + seg] = __builtin_amdgcn_exp2f(static_cast<float>(seg_log));
   } else if (A.fin != nullptr && cc1 == A.nchunks) {
     float* sp = A.fin + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
 #pragma unroll
     for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int n = 16 * t + 4 * g4 + r;
+        const int n = nbase + 16 * t + 4 * g4 + r;
         if (prow < A.P && n < A.N) sp[n] = st[t][r];
       }
   }
@@ -261,9 +285,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_walk_kernel(WalkPair W) {
 
 // The state that each segment starts from, out of the segments' own totals
 // (in place: a total is read before its slot is overwritten).
-__global__ void __launch_bounds__(kThreads) scan_segments_kernel(WalkPair W, int nt) {
+__global__ void __launch_bounds__(kStepThreads) scan_segments_kernel(WalkPair W, int nt) {
   const ScanWalk& A = W.w[blockIdx.z];
-  const int e = static_cast<int>(blockIdx.y) * kThreads + static_cast<int>(threadIdx.x);   // of kPB * nt
+  const int e = static_cast<int>(blockIdx.y) * kStepThreads + static_cast<int>(threadIdx.x);   // of kPB * nt
   const long long vrow = blockIdx.x;
   const int vheads = A.heads * A.pblocks;
   const int vh = static_cast<int>(vrow % vheads);
@@ -289,7 +313,7 @@ hipError_t walk(const WalkPair& W, int dirs, hipStream_t st) {
   const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
   const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg;
-  hipLaunchKernelGGL((scan_walk_kernel<T, NT, READ>), dim3(static_cast<unsigned>(items), dirs), dim3(kThreads), bytes, st,
+  hipLaunchKernelGGL((scan_walk_kernel<T, NT, READ>), dim3(static_cast<unsigned>(items), dirs), dim3(kWalkThreads), bytes, st,
                      W);
   return hipGetLastError();
 }
@@ -315,8 +339,8 @@ hipError_t launch_scan_walk(const ScanWalk* walks, int dirs, bool read, bool bf1
     if (e != hipSuccess) return e;
     const int nt = scan_padded_n(a.N);
     const long long vrows = static_cast<long long>(a.batch) * a.heads * a.pblocks;
-    hipLaunchKernelGGL(scan_segments_kernel, dim3(static_cast<unsigned>(vrows), kScanRows * nt / kThreads, dirs),
-                       dim3(kThreads), 0, st, W, nt);
+    hipLaunchKernelGGL(scan_segments_kernel, dim3(static_cast<unsigned>(vrows), kScanRows * nt / kStepThreads, dirs),
+                       dim3(kStepThreads), 0, st, W, nt);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -339,7 +363,7 @@ template <>
 __device__ __forceinline__ float load1<float>(const float* p) { return *p; }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanStep A) {
+__global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanStep A) {
   const int half = threadIdx.x >> 5, l = threadIdx.x & 31, n0 = 4 * l;
   const int pblocks = (A.P + kStepRows - 1) / kStepRows;
   const int pb = static_cast<int>(blockIdx.x) % pblocks;
@@ -408,21 +432,21 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanStep A) {
 
 hipError_t launch_scan_step(const ScanStep& A, bool bf16, hipStream_t st) {
   const long long blocks = static_cast<long long>(A.batch) * A.heads * ((A.P + kStepRows - 1) / kStepRows);
-  if (bf16) hipLaunchKernelGGL(scan_step_kernel<bf16_t>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, A);
-  else hipLaunchKernelGGL(scan_step_kernel<float>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, A);
+  if (bf16) hipLaunchKernelGGL(scan_step_kernel<bf16_t>, dim3(static_cast<unsigned>(blocks)), dim3(kStepThreads), 0, st, A);
+  else hipLaunchKernelGGL(scan_step_kernel<float>, dim3(static_cast<unsigned>(blocks)), dim3(kStepThreads), 0, st, A);
   return hipGetLastError();
 }
 
 namespace {
-__global__ void __launch_bounds__(kThreads) scan_copy_kernel(const float* src, float* dst, long long n) {
-  for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < n; i += static_cast<long long>(gridDim.x) * kThreads)
+__global__ void __launch_bounds__(kStepThreads) scan_copy_kernel(const float* src, float* dst, long long n) {
+  for (long long i = static_cast<long long>(blockIdx.x) * kStepThreads + threadIdx.x; i < n; i += static_cast<long long>(gridDim.x) * kStepThreads)
     dst[i] = src == nullptr ? 0.0f : src[i];
 }
 }  // namespace
 
 hipError_t launch_copy_f32(const float* src, float* dst, long long n, hipStream_t st) {
-  const long long blocks = (n + kThreads - 1) / kThreads;
-  hipLaunchKernelGGL(scan_copy_kernel, dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048)), dim3(kThreads), 0, st, src, dst, n);
+  const long long blocks = (n + kStepThreads - 1) / kStepThreads;
+  hipLaunchKernelGGL(scan_copy_kernel, dim3(static_cast<unsigned>(blocks < 2048 ? blocks : 2048)), dim3(kStepThreads), 0, st, src, dst, n);
   return hipGetLastError();
 }
 

@@ -29,23 +29,28 @@ namespace {
 
 using namespace scan;
 
-template <typename T, int NT>
+// A block of Q tokens by 4 Q threads: 128 tokens with bfloat16 operands, 64
+// with float32 ones, whose tiles fill the LDS of a compute unit.
+template <typename T, int NT, int Q>
 struct GradLds {
   static constexpr int kLdN = NT + Ops<T>::kPad;
   static constexpr int kLdP = kPB + Ops<T>::kPad;
-  static constexpr int kLdM = kQ + Ops<T>::kPad;
-  static constexpr int q = 0;                                     // [kQ][NT]
-  static constexpr int k = q + kQ * kLdN * (int)sizeof(T);        // [kQ][NT]
-  static constexpr int v = k + kQ * kLdN * (int)sizeof(T);        // [kQ][kPB]; at the end D [i][j]
-  static constexpr int dy = v + kQ * kLdP * (int)sizeof(T);       // [kQ][kPB]; at the end D^T [j][i]
-  static constexpr int m = dy + kQ * kLdP * (int)sizeof(T);       // (L A)^T [j][i]
-  static constexpr int gates = m + kQ * kLdM * (int)sizeof(T);    // Gates
-  static constexpr int rows = gates + (int)sizeof(Gates);         // row sums of W by column block [4][kQ]
-  static constexpr int cols = rows + 4 * kQ * 4;                  // column sums of L A E by row block [4][kQ]
-  static constexpr int qs = cols + 4 * kQ * 4;                    // e^{c_i} q_i . S_in^T dy_i by wave [4][kQ]
-  static constexpr int ks = qs + 4 * kQ * 4;                      // e^{c_end - c_j} k_j . dS_out^T v_j by wave [4][kQ]
-  static constexpr int through = ks + 4 * kQ * 4;                 // <S_in, dS_out> by wave [4]
-  static constexpr int bytes = through + 16;
+  static constexpr int kLdM = Q + Ops<T>::kPad;
+  static constexpr int kTiles = Q / 16;                           // token tiles, and waves
+  static constexpr int q = 0;                                     // [Q][NT]
+  static constexpr int k = q + Q * kLdN * (int)sizeof(T);         // [Q][NT]
+  static constexpr int v = k + Q * kLdN * (int)sizeof(T);         // [Q][kPB]
+  static constexpr int dy = v + Q * kLdP * (int)sizeof(T);        // [Q][kPB]; v and dy at the end: D [i][j]
+  static constexpr int m = dy + Q * kLdP * (int)sizeof(T);        // (L A)^T [j][i]; at the end D^T
+  static constexpr int gates = m + Q * kLdM * (int)sizeof(T);     // Gates
+  static constexpr int rows = gates + (int)sizeof(Gates<Q>);      // row sums of W by the first column tile of a run
+  static constexpr int cols = rows + kTiles * Q * 4;              // column sums of L A E by row tile
+  static constexpr int qs = cols + kTiles * Q * 4;                // e^{c_i} q_i . S_in^T dy_i by block of n
+  static constexpr int ks = qs + kTiles * Q * 4;                  // e^{c_end - c_j} k_j . dS_out^T v_j by block of n
+  static constexpr int through = ks + kTiles * Q * 4;             // <S_in, dS_out> by wave
+  static constexpr int bytes = through + kTiles * 4;
+  static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
+  static_assert(kLdM <= 2 * kLdP, "D fits where v and dy were");
 };
 
 // Sum over the 16 lanes of a row.
@@ -57,110 +62,144 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-template <typename T, int NT>
-__global__ void __launch_bounds__(kThreads, 2) scan_grad_kernel(ScanGrad A) {
+template <typename T, int NT, int Q>
+__global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
-  typedef GradLds<T, NT> L;
-  constexpr int kNW = NT / 64;   // 16-wide blocks of n per wave
+  typedef GradLds<T, NT, Q> L;
+  constexpr int kThreads = 4 * Q, kTiles = L::kTiles, kU = Q / 64;
+  // the tiles on and below the diagonal, dealt to the waves in runs
+  constexpr int kAll = kTiles * (kTiles + 1) / 2, kMaxTiles = (kAll + kTiles - 1) / kTiles;
+  // dq and dk: 16-wide blocks of n per wave, groups of waves that share a block's tokens
+  constexpr int kBlocks = NT / 16, kNW = kBlocks > kTiles ? kBlocks / kTiles : 1;
+  constexpr int kTG = kTiles > kBlocks ? kTiles / kBlocks : 1, kTT = kTiles / kTG;
+  // dv: four blocks of value rows, the tokens dealt to kTiles / 4 groups of waves
+  constexpr int kZG = kTiles / 4;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   T* lq = reinterpret_cast<T*>(lds + L::q);
   T* lk = reinterpret_cast<T*>(lds + L::k);
   T* lv = reinterpret_cast<T*>(lds + L::v);
   T* ldy = reinterpret_cast<T*>(lds + L::dy);
   T* lm = reinterpret_cast<T*>(lds + L::m);
-  Gates& G = *reinterpret_cast<Gates*>(lds + L::gates);
+  Gates<Q>& G = *reinterpret_cast<Gates<Q>*>(lds + L::gates);
   float* lrow = reinterpret_cast<float*>(lds + L::rows);
   float* lcol = reinterpret_cast<float*>(lds + L::cols);
   float* lqs = reinterpret_cast<float*>(lds + L::qs);
   float* lks = reinterpret_cast<float*>(lds + L::ks);
   float* lthrough = reinterpret_cast<float*>(lds + L::through);
 
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, l16 = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g4 = lane >> 4;
   const int split = static_cast<int>(blockIdx.x % A.nsplit);
   const long long rest = blockIdx.x / A.nsplit;
   const int grp = static_cast<int>(rest % A.groups);
-  const int c = static_cast<int>(rest / A.groups % A.nchunks);
-  const long long bi = rest / A.groups / A.nchunks;
-  const long long t0 = static_cast<long long>(c) * kQ;
-  const int rows = A.tokens - t0 < kQ ? static_cast<int>(A.tokens - t0) : kQ;
+  const int c = static_cast<int>(rest / A.groups % A.nblocks);
+  const long long bi = rest / A.groups / A.nblocks;
+  const long long t0 = static_cast<long long>(c) * Q;
+  const int rows = A.tokens - t0 < Q ? static_cast<int>(A.tokens - t0) : Q;
   const int per_group = A.heads / A.groups;
   const int per_split = (per_group + A.nsplit - 1) / A.nsplit;
   const int h0 = grp * per_group + split * per_split;
   const int h1 = grp * per_group + (split * per_split + per_split < per_group ? split * per_split + per_split : per_group);
   const int nvirt = (h1 - h0) * A.pblocks;   // (head, block of kPB value components), heads outermost
   const int vheads = A.heads * A.pblocks;
-
   const auto rows_p_of = [&](int pb) { return A.P - pb * kPB < kPB ? A.P - pb * kPB : kPB; };
-  TileLoad<T, kPB> tv, tdy;
-  float gv = 0.0f, bv = 0.0f;
-  const auto load_head = [&](int i) {
+  const auto state_at = [&](int i) {
+    const int h = h0 + i / A.pblocks, pb = i % A.pblocks;
+    return ((bi * vheads + h * A.pblocks + pb) * A.nblocks + c) * static_cast<long long>(kPB * NT);
+  };
+
+  TileLoad<T, kPB, Q, kThreads> tv, tdy;
+  float gv[kU], bv[kU];
+  const auto load_head = [&](int i, int tid) {
+    const int lane = tid & 63;
     const int h = h0 + i / A.pblocks, pb = i % A.pblocks, rp = rows_p_of(pb);
     const T* vp = static_cast<const T*>(A.v.p) + bi * A.v.sb + h * A.v.sh + t0 * A.v.st + pb * kPB;
     const T* dp = static_cast<const T*>(A.dy.p) + bi * A.dy.sb + h * A.dy.sh + t0 * A.dy.st + pb * kPB;
-    tv.load(vp, A.v.st, rows, rp, A.v.vec && rp % O::kVec == 0);
-    tdy.load(dp, A.dy.st, rows, rp, A.dy.vec && rp % O::kVec == 0);
-    if (w == 3) {
-      gv = 0.0f;
-      bv = 0.0f;
-      if (lane < rows) {
-        gv = (static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh)[(t0 + lane) * A.g.st];
-        bv = A.b.p == nullptr ? 1.0f : (static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh)[(t0 + lane) * A.b.st];
+    tv.load(vp, A.v.st, rows, rp, A.v.vec && rp % O::kVec == 0, tid);
+    tdy.load(dp, A.dy.st, rows, rp, A.dy.vec && rp % O::kVec == 0, tid);
+    if (w == kTiles - 1) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int t = 64 * u + lane;
+        gv[u] = 0.0f;
+        bv[u] = 0.0f;
+        if (t < rows) {
+          gv[u] = (static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh)[(t0 + t) * A.g.st];
+          bv[u] = A.b.p == nullptr ? 1.0f : (static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh)[(t0 + t) * A.b.st];
+        }
       }
     }
   };
+  // the states as operands [n][p]: row n = n0 + l16, 8 components p = 32 s + 8 g4 + 0..7
+  const int nw0 = (w % (kBlocks / kNW)) * kNW, tg = w / (kBlocks / kNW);
+  const auto load_columns = [&](const float* base, int l16, int g4, float (&x)[kNW][kPB / 32][8]) {
+#pragma unroll
+    for (int b = 0; b < kNW; ++b)
+#pragma unroll
+      for (int s = 0; s < kPB / 32; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[b][s][e] = base[(32 * s + 8 * g4 + e) * NT + 16 * (nw0 + b) + l16];
+  };
 
   {
-    TileLoad<T, NT> tq, tk;
-    tq.load(static_cast<const T*>(A.q.p) + bi * A.q.sb + grp * A.q.sh + t0 * A.q.st, A.q.st, rows, A.N, A.q.vec);
-    tk.load(static_cast<const T*>(A.k.p) + bi * A.k.sb + grp * A.k.sh + t0 * A.k.st, A.k.st, rows, A.N, A.k.vec);
-    if (nvirt > 0) load_head(0);
-    tq.store(lq);
-    tk.store(lk);
+    TileLoad<T, NT, Q, kThreads> tq, tk;
+    tq.load(static_cast<const T*>(A.q.p) + bi * A.q.sb + grp * A.q.sh + t0 * A.q.st, A.q.st, rows, A.N, A.q.vec, tid);
+    tk.load(static_cast<const T*>(A.k.p) + bi * A.k.sb + grp * A.k.sh + t0 * A.k.st, A.k.st, rows, A.N, A.k.vec, tid);
+    tq.store(lq, tid);
+    tk.store(lk, tid);
   }
-  // tiles of (L A)^T and of the sums that no wave writes
-  for (int i = tid; i < kQ * L::kLdM; i += kThreads) lm[i] = O::from_f32(0.0f);
-  for (int i = tid; i < 4 * kQ; i += kThreads) {
+  if (nvirt > 0) load_head(0, tid);
+  // tiles of (L A)^T and slots of the sums that no wave writes
+  for (int i = tid; i < Q * L::kLdM; i += kThreads) lm[i] = O::from_f32(0.0f);
+  for (int i = tid; i < kTiles * Q; i += kThreads) {
     lrow[i] = 0.0f;
     lcol[i] = 0.0f;
   }
   __syncthreads();
 
-  // A and the sum of L b E: tiles on and below the diagonal, rows i, columns j
-  const int ntile = tile_count(w);
+  // A and the sum of L b E, by tile: rows i, columns j
+  const int tile0 = w * kAll / kTiles, ntile = (w + 1) * kAll / kTiles - tile0;
+  int trow[kMaxTiles], tcol[kMaxTiles];
   f32x4_t sc[kMaxTiles], dsum[kMaxTiles];
 #pragma unroll
   for (int t = 0; t < kMaxTiles; ++t) {
+    trow[t] = tile_row(tile0 + t);
+    tcol[t] = tile_col(tile0 + t, trow[t]);
     sc[t] = dsum[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     if (t < ntile)
 #pragma unroll
       for (int s = 0; s < NT / 32; ++s)
-        sc[t] = O::mma(O::row(lq + (16 * tile_row(w, t) + l16) * L::kLdN + 32 * s + 8 * g4),
-                       O::row(lk + (16 * tile_col(w, t) + l16) * L::kLdN + 32 * s + 8 * g4), sc[t]);
+        sc[t] = O::mma(O::row(lq + (16 * trow[t] + l16) * L::kLdN + 32 * s + 8 * g4),
+                       O::row(lk + (16 * tcol[t] + l16) * L::kLdN + 32 * s + 8 * g4), sc[t]);
   }
-  // dq^T and dk^T: rows n = 16 (w kNW + b) + 4 g4 + 0..3, column i (j) = 16 it + l16
-  f32x4_t dq[kNW][4], dk[kNW][4];
+  // dq^T and dk^T: rows n = 16 (nw0 + b) + 4 g4 + 0..3, column i (j) = 16 (u kTG + tg) + l16
+  f32x4_t dq[kNW][kTT], dk[kNW][kTT];
 #pragma unroll
   for (int b = 0; b < kNW; ++b)
 #pragma unroll
-    for (int it = 0; it < 4; ++it) dq[b][it] = dk[b][it] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int u = 0; u < kTT; ++u) dq[b][u] = dk[b][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  float acc_in = 0.0f, acc_leave = 0.0f, acc_db = 0.0f, acc_z = 0.0f;   // wave 0: token = lane, over a head's blocks
+  float acc_in[kU] = {}, acc_leave[kU] = {}, acc_db[kU] = {}, acc_z = 0.0f;   // wave 0, over a head's blocks
   for (int i = 0; i < nvirt; ++i) {
+    const int tid = fresh(threadIdx.x), lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
     const int h = h0 + i / A.pblocks, pb = i % A.pblocks;
-    const long long srow = ((bi * vheads + h * A.pblocks + pb) * A.nchunks + c) * static_cast<long long>(kPB * NT);
-    const float* sp = A.states + srow;
-    const float* dsp = A.dstates + srow;
-    tv.store(lv);
-    tdy.store(ldy);
-    if (w == 3) write_gates(G, gv, bv, lane);
+    const float* dsp = A.dstates + state_at(i);
+    float x[kNW][kPB / 32][8], y[kNW][kPB / 32][8];
+    load_columns(A.states + state_at(i), l16, g4, x);
+    load_columns(dsp, l16, g4, y);
+    tv.store(lv, tid);
+    tdy.store(ldy, tid);
+    if (w == kTiles - 1) write_gates(G, gv, bv, lane);
     __syncthreads();
-    if (i + 1 < nvirt) load_head(i + 1);
+    if (i + 1 < nvirt) load_head(i + 1, tid);
+    __builtin_amdgcn_sched_barrier(0);
 
+    float racc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int run = 0;
 #pragma unroll
     for (int t = 0; t < kMaxTiles; ++t) {
       if (t < ntile) {
-        const int it = tile_row(w, t), jt = tile_col(w, t);
+        const int it = trow[t], jt = tcol[t];
         f32x4_t e = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < kPB / 32; ++s)
@@ -171,184 +210,229 @@ __global__ void __launch_bounds__(kThreads, 2) scan_grad_kernel(ScanGrad A) {
         const f32x4_t ih = *reinterpret_cast<const f32x4_t*>(G.hi + i0), il = *reinterpret_cast<const f32x4_t*>(G.lo + i0);
         f32x4_t mm;
         float col = 0.0f;
-        float rsum[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float d = i0 + r >= j ? between(ih[r], il[r], hi, lo) : 0.0f;
           mm[r] = d * sc[t][r];
-          const float le = d * e[r];
-          dsum[t][r] = fmaf(le, b, dsum[t][r]);
+          dsum[t][r] = fmaf(d * e[r], b, dsum[t][r]);
           const float we = mm[r] * e[r];
           col += we;
-          rsum[r] = row_sum(we * b);
+          racc[r] = fmaf(we, b, racc[r]);
         }
         O::store4(lm + j * L::kLdM + i0, mm);
         col += __shfl_xor(col, 16, kWave);
         col += __shfl_xor(col, 32, kWave);
-        if (g4 == 0) lcol[it * kQ + j] = col;
-        if (l16 == 0) *reinterpret_cast<f32x4_t*>(lrow + jt * kQ + i0) = f32x4_t{rsum[0], rsum[1], rsum[2], rsum[3]};
-      }
-    }
-
-    // the states' part of dq and dk, and the states' product
-    float qs[4] = {0.0f, 0.0f, 0.0f, 0.0f}, ks[4] = {0.0f, 0.0f, 0.0f, 0.0f}, through = 0.0f;
+        if (g4 == 0) lcol[it * Q + j] = col;
+        if (t + 1 == ntile || trow[t + 1 < kMaxTiles ? t + 1 : t] != it) {   // the run in this row of tiles ends
+          f32x4_t rs;
 #pragma unroll
-    for (int b = 0; b < kNW; ++b) {
-      const int n0 = 16 * (w * kNW + b);
-      f32x4_t aq[4], ak[4];
-#pragma unroll
-      for (int it = 0; it < 4; ++it) aq[it] = ak[it] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int s = 0; s < kPB / 32; ++s) {
-        float x[8], y[8];
-        const long long off = static_cast<long long>(32 * s + 8 * g4) * NT + n0 + l16;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = sp[off + e * NT];
-          y[e] = dsp[off + e * NT];
+          for (int r = 0; r < 4; ++r) {
+            rs[r] = row_sum(racc[r]);
+            racc[r] = 0.0f;
+          }
+          if (l16 == 0) *reinterpret_cast<f32x4_t*>(lrow + tcol[run] * Q + i0) = rs;
+          run = t + 1;
         }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
+    // the states' part of dq, then of dk, and the states' product
+    float through = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) through = fmaf(x[e], y[e], through);
-        Frag fx[O::kSplit], fy[O::kSplit];
-        O::split(x, fx);
-        O::split(y, fy);
+    for (int b = 0; b < kNW; ++b)
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const Frag d = O::row(ldy + (16 * it + l16) * L::kLdP + 32 * s + 8 * g4);
-          const Frag v = O::row(lv + (16 * it + l16) * L::kLdP + 32 * s + 8 * g4);
+      for (int s = 0; s < kPB / 32; ++s)
 #pragma unroll
-          for (int u = O::kSplit - 1; u >= 0; --u) {
-            aq[it] = O::mma(fx[u], d, aq[it]);
-            ak[it] = O::mma(fy[u], v, ak[it]);
+        for (int e = 0; e < 8; ++e) through = fmaf(x[b][s][e], y[b][s][e], through);
+    through = wave_total(through);
+    if (lane == 0) lthrough[w] = tg == 0 ? through : 0.0f;
+    float sums[kTT];
+    const auto products = [&](const float (&xs)[kNW][kPB / 32][8], const T* tile, const T* other, const float* scale,
+                              const float* gate, f32x4_t (&out)[kNW][kTT], float* slot) {
+      const int lane = fresh(threadIdx.x) & 63, l16 = lane & 15, g4 = lane >> 4;
+#pragma unroll
+      for (int u = 0; u < kTT; ++u) sums[u] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < kNW; ++b) {
+        f32x4_t acc[kTT];
+#pragma unroll
+        for (int u = 0; u < kTT; ++u) acc[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < kPB / 32; ++s) {
+          Frag f[O::kSplit];
+          O::split(xs[b][s], f);
+#pragma unroll
+          for (int u = 0; u < kTT; ++u) {
+            const Frag d = O::row(tile + (16 * (u * kTG + tg) + l16) * L::kLdP + 32 * s + 8 * g4);
+#pragma unroll
+            for (int z = O::kSplit - 1; z >= 0; --z) acc[u] = O::mma(f[z], d, acc[u]);
+            if (u % 4 == 3) __builtin_amdgcn_sched_barrier(0);
           }
         }
-      }
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const int t = 16 * it + l16;
-        const float first = G.first[t], last = G.last[t], bt = G.b[t];
-        const f32x4_t qv = O::load4(lq + t * L::kLdN + n0 + 4 * g4), kv = O::load4(lk + t * L::kLdN + n0 + 4 * g4);
+        for (int u = 0; u < kTT; ++u) {
+          const int t = 16 * (u * kTG + tg) + l16;
+          const float sv = scale[t], gt = gate == nullptr ? 1.0f : gate[t];
+          const f32x4_t ov = O::load4(other + t * L::kLdN + 16 * (nw0 + b) + 4 * g4);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float a = aq[it][r] * first, d = ak[it][r] * last;
-          qs[it] = fmaf(a, qv[r], qs[it]);
-          ks[it] = fmaf(d, kv[r], ks[it]);
-          dq[b][it][r] += a;
-          dk[b][it][r] = fmaf(d, bt, dk[b][it][r]);
+          for (int r = 0; r < 4; ++r) {
+            const float a = acc[u][r] * sv;
+            sums[u] = fmaf(a, ov[r], sums[u]);
+            out[b][u][r] = gate == nullptr ? out[b][u][r] + a : fmaf(a, gt, out[b][u][r]);
+          }
+          if (u % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
       }
-    }
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      qs[it] += __shfl_xor(qs[it], 16, kWave);
-      qs[it] += __shfl_xor(qs[it], 32, kWave);
-      ks[it] += __shfl_xor(ks[it], 16, kWave);
-      ks[it] += __shfl_xor(ks[it], 32, kWave);
-      if (g4 == 0) {
-        lqs[w * kQ + 16 * it + l16] = qs[it];
-        lks[w * kQ + 16 * it + l16] = ks[it];
+      for (int u = 0; u < kTT; ++u) {
+        sums[u] += __shfl_xor(sums[u], 16, kWave);
+        sums[u] += __shfl_xor(sums[u], 32, kWave);
+        if (g4 == 0) slot[nw0 / kNW * Q + 16 * (u * kTG + tg) + l16] = sums[u];
       }
-    }
-    through = wave_sum(through);
-    if (lane == 0) lthrough[w] = through;
+    };
+    products(x, ldy, lq, G.first, nullptr, dq, lqs);
+    __builtin_amdgcn_sched_barrier(0);
+    // dS_out as the operand of dv: row p = 16 (w % 4) + l16, 8 columns n = 32 s + 8 g4 + 0..7
+    f32x4_t zs[NT / 32][2];
+    const int zl = fresh(threadIdx.x) & 63;
+#pragma unroll
+    for (int s = 0; s < NT / 32; ++s)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        zs[s][u] = *reinterpret_cast<const f32x4_t*>(dsp + (16 * (w & 3) + (zl & 15)) * NT + 32 * s + 8 * (zl >> 4) + 4 * u);
+    products(y, lv, lk, G.last, G.b, dk, lks);
+    __builtin_amdgcn_sched_barrier(0);
 
-    // z^T: rows p = 16 w + 4 g4 + 0..3, column j = 16 jt + l16; the states' part first
-    f32x4_t z[4];
+    {
+      const int lane = fresh(threadIdx.x) & 63, l16 = lane & 15, g4 = lane >> 4;
+      // z^T: rows p = 16 (w % 4) + 4 g4 + 0..3, column j = 16 (kZG u + w / 4) + l16; the states' part first
+      f32x4_t z[4];
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) z[jt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int u = 0; u < 4; ++u) z[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int s = 0; s < NT / 32; ++s) {
-      const float* dp = dsp + (16 * w + l16) * NT + 32 * s + 8 * g4;
-      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(dp), b = *reinterpret_cast<const f32x4_t*>(dp + 4);
-      const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      const Frag f = O::narrow(x);
+      for (int s = 0; s < NT / 32; ++s) {
+        const Frag f = frag_from_acc<T>(zs[s][0], zs[s][1]);
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) z[jt] = O::mma(f, O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4), z[jt]);
-    }
+        for (int u = 0; u < 4; ++u)
+          z[u] = O::mma(f, O::row(lk + (16 * (kZG * u + (w >> 2)) + l16) * L::kLdN + 32 * s + 8 * g4), z[u]);
+      }
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) z[jt] *= G.last[16 * jt + l16];
-    __syncthreads();   // (L A)^T and the sums are written
+      for (int u = 0; u < 4; ++u) z[u] *= G.last[16 * (kZG * u + (w >> 2)) + l16];
+      __syncthreads();   // (L A)^T and the sums are written
 #pragma unroll
-    for (int s = 0; s < kQ / 32; ++s) {
-      const Frag f = O::col(ldy, L::kLdP, 32 * s, 16 * w, lane);
+      for (int s = 0; s < Q / 32; ++s) {
+        const Frag f = O::col(ldy, L::kLdP, 32 * s, 16 * (w & 3), lane);
 #pragma unroll
-      for (int jt = 0; jt < 2 * s + 2; ++jt) z[jt] = O::mma(f, O::row(lm + (16 * jt + l16) * L::kLdM + 32 * s + 8 * g4), z[jt]);
-    }
-    const int rp = rows_p_of(pb), p0 = 16 * w + 4 * g4;
+        for (int u = 0; u < 4; ++u) {
+          const int jt = kZG * u + (w >> 2);
+          if (s >= kZG * u / 2)   // jt / 2: tiles above the diagonal are zero
+            z[u] = O::mma(f, O::row(lm + (16 * jt + l16) * L::kLdM + 32 * s + 8 * g4), z[u]);
+        }
+      }
+      const int rp = rows_p_of(pb), p0 = 16 * (w & 3) + 4 * g4;
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      const int j = 16 * jt + l16;
-      if (j < rows && p0 < rp) {
-        const f32x4_t o = z[jt] * G.b[j];
-        T* op = static_cast<T*>(A.dv) + ((bi * A.tokens + t0 + j) * A.heads + h) * A.P + pb * kPB + p0;
-        if (A.dvvec) {
-          O::store4(op, o);
-        } else {
+      for (int u = 0; u < 4; ++u) {
+        const int j = 16 * (kZG * u + (w >> 2)) + l16;
+        if (j < rows && p0 < rp) {
+          const f32x4_t o = z[u] * G.b[j];
+          T* op = static_cast<T*>(A.dv) + ((bi * A.tokens + t0 + j) * A.heads + h) * A.P + pb * kPB + p0;
+          if (A.dvvec) {
+            O::store4(op, o);
+          } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (p0 + r < rp) op[r] = O::from_f32(o[r]);
+            for (int r = 0; r < 4; ++r)
+              if (p0 + r < rp) op[r] = O::from_f32(o[r]);
+          }
         }
       }
     }
 
     if (w == 0) {
-      const float b = G.b[lane];
-      const float rs = (lrow[lane] + lrow[kQ + lane]) + (lrow[2 * kQ + lane] + lrow[3 * kQ + lane]);
-      const float cs = (lcol[lane] + lcol[kQ + lane]) + (lcol[2 * kQ + lane] + lcol[3 * kQ + lane]);
-      const float us = (lqs[lane] + lqs[kQ + lane]) + (lqs[2 * kQ + lane] + lqs[3 * kQ + lane]);
-      const float ws = (lks[lane] + lks[kQ + lane]) + (lks[2 * kQ + lane] + lks[3 * kQ + lane]);
-      acc_in += rs - b * cs + us;
-      acc_leave = fmaf(b, ws, acc_leave);
-      acc_db += cs + ws;
-      acc_z += (lthrough[0] + lthrough[1]) + (lthrough[2] + lthrough[3]);
-      if (pb + 1 == A.pblocks) {
-        const double pin = wave_prefix_d(static_cast<double>(acc_in));
-        const double pl = wave_prefix_d(static_cast<double>(acc_leave));
-        const double suffix = read_lane_d(pin, 63) - pin + static_cast<double>(acc_in);
-        const double before = pl - static_cast<double>(acc_leave);
-        if (lane < rows) {
-          const long long o = (bi * A.tokens + t0 + lane) * A.heads + h;
-          const double d = suffix + before + static_cast<double>(G.end[0]) * static_cast<double>(acc_z);
-          // nothing crosses a token whose decay is 0: what the sums leave there is rounding
-          A.dg[o] = G.own[lane] == 0.0f ? 0.0f : static_cast<float>(d);
-          if (A.db != nullptr) A.db[o] = acc_db;
+      const int lane = fresh(threadIdx.x) & 63;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int t = 64 * u + lane;
+        float rs = 0.0f, cs = 0.0f, us = 0.0f, ws = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kTiles; ++e) {
+          rs += lrow[e * Q + t];
+          cs += lcol[e * Q + t];
         }
-        acc_in = acc_leave = acc_db = acc_z = 0.0f;
+#pragma unroll
+        for (int e = 0; e < kBlocks / kNW; ++e) {
+          us += lqs[e * Q + t];
+          ws += lks[e * Q + t];
+        }
+        const float b = G.b[t];
+        acc_in[u] += rs - b * cs + us;
+        acc_leave[u] = fmaf(b, ws, acc_leave[u]);
+        acc_db[u] += cs + ws;
+      }
+#pragma unroll
+      for (int e = 0; e < kTiles; ++e) acc_z += lthrough[e];
+      if (pb + 1 == A.pblocks) {
+        double pin[kU], pl[kU], tin = 0.0, tl = 0.0;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          pin[u] = tin + wave_prefix_d(static_cast<double>(acc_in[u]));
+          pl[u] = tl + wave_prefix_d(static_cast<double>(acc_leave[u]));
+          tin = read_lane_d(pin[u], 63);
+          tl = read_lane_d(pl[u], 63);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int t = 64 * u + lane;
+          if (t < rows) {
+            const long long o = (bi * A.tokens + t0 + t) * A.heads + h;
+            const double d = tin - pin[u] + static_cast<double>(acc_in[u]) + pl[u] - static_cast<double>(acc_leave[u]) +
+                             static_cast<double>(G.end[0]) * static_cast<double>(acc_z);
+            // nothing crosses a token whose decay is 0: what the sums leave there is rounding
+            A.dg[o] = G.own[t] == 0.0f ? 0.0f : static_cast<float>(d);
+            if (A.db != nullptr) A.db[o] = acc_db[u];
+          }
+          acc_in[u] = acc_leave[u] = acc_db[u] = 0.0f;
+        }
+        acc_z = 0.0f;
       }
     }
     __syncthreads();   // the tiles, gates and sums are done with
   }
 
-  // D = sum over heads of L b E, once as D [i][j] and once as D^T [j][i]
+  // D = sum over heads of L b E, once as D [i][j] (where v and dy were) and
+  // once as D^T [j][i] (where (L A)^T was, whose other tiles are zero)
   T* ld = lv;
-  T* ldt = ldy;
-  for (int i = tid; i < kQ * L::kLdP; i += kThreads) ld[i] = ldt[i] = O::from_f32(0.0f);
+  for (int i = tid; i < Q * L::kLdM; i += kThreads) ld[i] = O::from_f32(0.0f);
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < kMaxTiles; ++t) {
     if (t < ntile) {
-      const int j = 16 * tile_col(w, t) + l16, i0 = 16 * tile_row(w, t) + 4 * g4;
-      O::store4(ldt + j * L::kLdP + i0, dsum[t]);
+      const int j = 16 * tcol[t] + l16, i0 = 16 * trow[t] + 4 * g4;
+      O::store4(lm + j * L::kLdM + i0, dsum[t]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) ld[(i0 + r) * L::kLdP + j] = O::from_f32(dsum[t][r]);
+      for (int r = 0; r < 4; ++r) ld[(i0 + r) * L::kLdM + j] = O::from_f32(dsum[t][r]);
     }
   }
   __syncthreads();
 #pragma unroll
   for (int b = 0; b < kNW; ++b) {
-    const int n0 = 16 * (w * kNW + b);
+    const int n0 = 16 * (nw0 + b);
 #pragma unroll
-    for (int s = 0; s < kQ / 32; ++s) {
+    for (int s = 0; s < Q / 32; ++s) {
       const Frag fk = O::col(lk, L::kLdN, 32 * s, n0, lane), fq = O::col(lq, L::kLdN, 32 * s, n0, lane);
 #pragma unroll
-      for (int it = 2 * s; it < 4; ++it) dq[b][it] = O::mma(fk, O::row(ld + (16 * it + l16) * L::kLdP + 32 * s + 8 * g4), dq[b][it]);
-#pragma unroll
-      for (int it = 0; it < 2 * s + 2; ++it) dk[b][it] = O::mma(fq, O::row(ldt + (16 * it + l16) * L::kLdP + 32 * s + 8 * g4), dk[b][it]);
+      for (int u = 0; u < kTT; ++u) {
+        const int it = u * kTG + tg;
+        // tiles of D with j > i (of D^T with i < j) are zero
+        if (s <= (u * kTG + kTG - 1) / 2) dq[b][u] = O::mma(fk, O::row(ld + (16 * it + l16) * L::kLdM + 32 * s + 8 * g4), dq[b][u]);
+        if (s >= u * kTG / 2) dk[b][u] = O::mma(fq, O::row(lm + (16 * it + l16) * L::kLdM + 32 * s + 8 * g4), dk[b][u]);
+      }
     }
     const int n = n0 + 4 * g4;
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int t = 16 * it + l16;
+    for (int u = 0; u < kTT; ++u) {
+      const int t = 16 * (u * kTG + tg) + l16;
       if (t >= rows || n >= A.N) continue;
       const long long o = ((bi * A.tokens + t0 + t) * A.groups + grp) * A.N + n;
       if (A.nsplit > 1) {
@@ -356,35 +440,37 @@ __global__ void __launch_bounds__(kThreads, 2) scan_grad_kernel(ScanGrad A) {
         float* pq = A.parts + (2LL * split) * half + o;
         float* pk = pq + half;
         if (A.N % 4 == 0) {
-          *reinterpret_cast<f32x4_t*>(pq) = dq[b][it];
-          *reinterpret_cast<f32x4_t*>(pk) = dk[b][it];
+          *reinterpret_cast<f32x4_t*>(pq) = dq[b][u];
+          *reinterpret_cast<f32x4_t*>(pk) = dk[b][u];
         } else {
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             if (n + r < A.N) {
-              pq[r] = dq[b][it][r];
-              pk[r] = dk[b][it][r];
+              pq[r] = dq[b][u][r];
+              pk[r] = dk[b][u][r];
             }
         }
       } else if (A.dkvec) {
-        O::store4(static_cast<T*>(A.dq) + o, dq[b][it]);
-        O::store4(static_cast<T*>(A.dk) + o, dk[b][it]);
+        O::store4(static_cast<T*>(A.dq) + o, dq[b][u]);
+        O::store4(static_cast<T*>(A.dk) + o, dk[b][u]);
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (n + r < A.N) {
-            static_cast<T*>(A.dq)[o + r] = O::from_f32(dq[b][it][r]);
-            static_cast<T*>(A.dk)[o + r] = O::from_f32(dk[b][it][r]);
+            static_cast<T*>(A.dq)[o + r] = O::from_f32(dq[b][u][r]);
+            static_cast<T*>(A.dk)[o + r] = O::from_f32(dk[b][u][r]);
           }
       }
     }
   }
 }
 
+constexpr int kPartThreads = 256;
+
 // dq and dk out of the head splits' parts, added in order.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) scan_parts_kernel(const float* parts, int nsplit, long long half, T* dq, T* dk) {
-  const long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+__global__ void __launch_bounds__(kPartThreads) scan_parts_kernel(const float* parts, int nsplit, long long half, T* dq, T* dk) {
+  const long long i = static_cast<long long>(blockIdx.x) * kPartThreads + threadIdx.x;
   if (i >= 2 * half) return;
   float s = 0.0f;
   for (int u = 0; u < nsplit; ++u) s += parts[2LL * u * half + i];
@@ -394,16 +480,17 @@ __global__ void __launch_bounds__(kThreads) scan_parts_kernel(const float* parts
 
 template <typename T, int NT>
 hipError_t grad(const ScanGrad& A, hipStream_t st) {
-  constexpr int bytes = GradLds<T, NT>::bytes;
-  const void* fn = reinterpret_cast<const void*>(scan_grad_kernel<T, NT>);
+  constexpr int Q = sizeof(T) == 2 ? kScanGradBf16 : kScanGradF32;
+  constexpr int bytes = GradLds<T, NT, Q>::bytes;
+  const void* fn = reinterpret_cast<const void*>(scan_grad_kernel<T, NT, Q>);
   hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
-  const long long items = static_cast<long long>(A.batch) * A.nchunks * A.groups * A.nsplit;
-  hipLaunchKernelGGL((scan_grad_kernel<T, NT>), dim3(static_cast<unsigned>(items)), dim3(kThreads), bytes, st, A);
+  const long long items = static_cast<long long>(A.batch) * A.nblocks * A.groups * A.nsplit;
+  hipLaunchKernelGGL((scan_grad_kernel<T, NT, Q>), dim3(static_cast<unsigned>(items)), dim3(4 * Q), bytes, st, A);
   e = hipGetLastError();
   if (e != hipSuccess || A.nsplit == 1) return e;
   const long long half = static_cast<long long>(A.batch) * A.tokens * A.groups * A.N;
-  hipLaunchKernelGGL((scan_parts_kernel<T>), dim3(static_cast<unsigned>((2 * half + kThreads - 1) / kThreads)), dim3(kThreads), 0,
+  hipLaunchKernelGGL((scan_parts_kernel<T>), dim3(static_cast<unsigned>((2 * half + kPartThreads - 1) / kPartThreads)), dim3(kPartThreads), 0,
                      st, A.parts, A.nsplit, half, static_cast<T*>(A.dq), static_cast<T*>(A.dk));
   return hipGetLastError();
 }

@@ -304,6 +304,7 @@ hipError_t launch_adamw(const AdamwLaunch& A, bool grad_bf16, int blocks, hipStr
 
 // Gated scan (gated_scan.hip, gated_scan_backward.hip).
 constexpr int kScanChunk = 64;     // tokens per chunk
+constexpr int kScanGradBf16 = 128, kScanGradF32 = 64;   // tokens per workgroup of the backward pass
 constexpr int kScanRows = 64;      // state rows (value components) per workgroup
 constexpr int kScanMaxN = 128;     // largest key length
 inline int scan_padded_n(int n) { return n <= 64 ? 64 : 128; }
@@ -324,8 +325,9 @@ struct ScanWalk {
   void* y;                    // [batch][tokens][heads][P]
   const float* init;          // null, or [batch][heads][P][N]: the state before the first chunk visited
   float* fin;                 // null, or the state after the last
-  float* states;              // null, or [batch][heads * pblocks][nchunks][kScanRows][padded N]: the
-                              // state that each chunk is visited with
+  int keep, nblocks;          // blocks of `keep` chunks
+  float* states;              // null, or [batch][heads * pblocks][nblocks][kScanRows][padded N]: the
+                              // state that each block is visited with
   float* seg_state;           // nseg > 1: [batch][heads * pblocks][nseg][kScanRows][padded N]
   float* seg_decay;           //           [batch][heads * pblocks][nseg]
 };
@@ -333,11 +335,12 @@ struct ScanWalk {
 hipError_t launch_scan_walk(const ScanWalk* W, int dirs, bool read, bool bf16, hipStream_t st);
 struct ScanGrad {
   SeqOperand v, k, q, dy, g, b;
-  int batch, tokens, heads, groups, P, N, pblocks, nchunks;
-  int nsplit;                 // workgroups that share a chunk's heads
+  int batch, tokens, heads, groups, P, N, pblocks;
+  int nblocks;                // blocks of kScanGradBf16 (float32: kScanGradF32) tokens
+  int nsplit;                 // workgroups that share a block's heads
   int dvvec, dkvec;           // rows of dv; of dq and dk: 4-element stores
-  const float* states;        // as ScanWalk.states: before each chunk
-  const float* dstates;       // gradients of the states after each chunk
+  const float* states;        // as ScanWalk.states: before each block
+  const float* dstates;       // gradients of the states after each block
   void *dv, *dk, *dq;
   float *dg, *db;             // [batch][tokens][heads]; db may be null
   float* parts;               // nsplit > 1: [nsplit][2][batch * tokens * groups * N]

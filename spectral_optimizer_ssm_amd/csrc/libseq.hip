@@ -64,11 +64,12 @@ int check_operands(const muon_scan_args* a) {
   return MUON_OK;
 }
 
-// Workgroups that fill the chip: two on each of 256 compute units.
-constexpr long long kFill = 512;
+// Workgroups that fill the chip: two on each of 256 compute units for the walk,
+// one for the backward pass (its tiles fill the LDS).
+constexpr long long kFill = 512, kGradFill = 256;
 
 struct ScanPlan {
-  int pblocks, nchunks, nseg, seg_chunks, nsplit;
+  int pblocks, nchunks, nblocks, nseg, seg_chunks, nsplit;   // nblocks: of the backward pass
   size_t states, dstates, seg, seg2, decay, decay2, parts, end;   // workspace offsets
 };
 // The walk of one sequence is serial, so with few sequences and heads the time
@@ -77,9 +78,13 @@ struct ScanPlan {
 // kSegChunks chunks fill idle compute units.
 constexpr int kSegChunks = 4;
 
+int grad_tokens(int dtype) { return dtype == MUON_BF16 ? kScanGradBf16 : kScanGradF32; }
+
 int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
   p->pblocks = (a->P + kScanRows - 1) / kScanRows;
   p->nchunks = static_cast<int>((static_cast<long long>(a->tokens) + kScanChunk - 1) / kScanChunk);
+  const int block = grad_tokens(a->dtype);
+  p->nblocks = static_cast<int>((static_cast<long long>(a->tokens) + block - 1) / block);
   const long long vrows = static_cast<long long>(a->batch) * a->heads * p->pblocks;
   const long long walks = backward ? 2 * vrows : vrows;
   if (a->batch == 0 || a->tokens == 0) {
@@ -92,8 +97,8 @@ int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
   if (nseg < 1) nseg = 1;
   p->seg_chunks = static_cast<int>((p->nchunks + nseg - 1) / nseg);
   p->nseg = (p->nchunks + p->seg_chunks - 1) / p->seg_chunks;
-  const long long groups = static_cast<long long>(a->batch) * p->nchunks * a->groups;
-  p->nsplit = static_cast<int>(std::min<long long>(a->heads / a->groups, std::max<long long>(1, (kFill + groups - 1) / groups)));
+  const long long groups = static_cast<long long>(a->batch) * p->nblocks * a->groups;
+  p->nsplit = static_cast<int>(std::min<long long>(a->heads / a->groups, std::max<long long>(1, kGradFill / groups)));
   const int per_split = (a->heads / a->groups + p->nsplit - 1) / p->nsplit;
   p->nsplit = (a->heads / a->groups + per_split - 1) / per_split;   // none without heads
   if (vrows * p->nseg > INT_MAX || groups * p->nsplit > INT_MAX) return MUON_EUNSUPPORTED;
@@ -110,8 +115,8 @@ int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
   if (backward) {
     p->seg2 = take(seg_bytes);
     p->decay2 = take(decay_bytes);
-    p->states = take(vrows * p->nchunks * tile);
-    p->dstates = take(vrows * p->nchunks * tile);
+    p->states = take(vrows * p->nblocks * tile);
+    p->dstates = take(vrows * p->nblocks * tile);
     const size_t half = static_cast<size_t>(a->batch) * a->tokens * a->groups * a->N;
     if (p->nsplit > 1 && 2 * half / 256 + 1 > static_cast<size_t>(INT_MAX)) return MUON_EUNSUPPORTED;
     p->parts = take(p->nsplit > 1 ? static_cast<size_t>(p->nsplit) * 2 * half * 4 : 0);
@@ -136,6 +141,7 @@ ScanWalk walk_of(const muon_scan_args* a, const ScanPlan& p) {
   w.batch = a->batch; w.tokens = a->tokens; w.heads = a->heads; w.groups = a->groups;
   w.P = a->P; w.N = a->N;
   w.pblocks = p.pblocks; w.nchunks = p.nchunks; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
+  w.keep = grad_tokens(a->dtype) / kScanChunk; w.nblocks = p.nblocks;
   w.init = a->S0;
   return w;
 }
@@ -233,7 +239,7 @@ int muon_gated_scan_backward(const muon_scan_args* a, const muon_seq* dY, const 
   const bool bf16 = a->dtype == MUON_BF16;
   char* ws = static_cast<char*>(workspace);
   const auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
-  // 1. the states before every chunk and the gradients of the states after it
+  // 1. the states before every block and the gradients of the states after it
   ScanWalk w[2] = {walk_of(a, p), walk_of(a, p)};
   w[0].states = at(p.states);
   w[1].x = operand(*dY, a->P, es);
@@ -249,11 +255,11 @@ int muon_gated_scan_backward(const muon_scan_args* a, const muon_seq* dY, const 
     w[1].seg_decay = at(p.decay2);
   }
   if (launch_scan_walk(w, 2, false, bf16, st) != hipSuccess) return MUON_EHIP;
-  // 2. the gradients, chunk by chunk
+  // 2. the gradients, block by block
   ScanGrad r{};
   r.v = w[0].x; r.k = w[0].k; r.q = w[0].q; r.dy = w[1].x; r.g = w[0].g; r.b = w[0].b;
   r.batch = a->batch; r.tokens = a->tokens; r.heads = a->heads; r.groups = a->groups; r.P = a->P; r.N = a->N;
-  r.pblocks = p.pblocks; r.nchunks = p.nchunks; r.nsplit = p.nsplit;
+  r.pblocks = p.pblocks; r.nblocks = p.nblocks; r.nsplit = p.nsplit;
   r.dvvec = a->P % 4 == 0 && aligned_to(dV, 4 * es);
   r.dkvec = a->N % 4 == 0 && aligned_to(dK, 4 * es) && aligned_to(dQ, 4 * es);
   r.states = at(p.states);

@@ -18,7 +18,6 @@ namespace scan {
 
 constexpr int kQ = kScanChunk;   // tokens per chunk
 constexpr int kPB = kScanRows;   // state rows (value components) per workgroup
-constexpr int kThreads = 256;
 constexpr float kLog2e = 1.44269504088896340736f;
 // log decays below this are taken as this: e^-10000 is 0 in float32 and in
 // float64 alike, and sums of 64 of them stay finite
@@ -142,22 +141,33 @@ __device__ __forceinline__ typename Ops<T>::Frag frag_from_acc(f32x4_t a, f32x4_
   return Ops<T>::narrow(v);
 }
 
-// A [kQ][WIDTH] tile of a sequence operand on its way into LDS: 16-byte pieces
-// held in registers.  Rows past `rows` and columns past `width` are zero.
-template <typename T, int WIDTH>
+// A value that the compiler takes for new: what depends on it is computed where
+// it is used, and not once before a long loop, in registers that the loop's
+// accumulators need.
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// A [ROWS][WIDTH] tile of a sequence operand on its way into LDS: 16-byte
+// pieces held in the registers of THREADS threads.  Rows past `rows` and
+// columns past `width` are zero.
+template <typename T, int WIDTH, int ROWS, int THREADS>
 struct TileLoad {
+  static constexpr int kThreads = THREADS;
   static constexpr int kVec = Ops<T>::kVec;
   static constexpr int kRowPieces = WIDTH / kVec;
-  static constexpr int kPieces = kQ * kRowPieces / kThreads;
+  static constexpr int kPieces = ROWS * kRowPieces / kThreads;
+  static_assert(ROWS * kRowPieces % kThreads == 0, "whole pieces");
   static constexpr int kLd = WIDTH + Ops<T>::kPad;
   u32x4_t r[kPieces];
 
   // p: element (token 0, column 0); vec: 16-byte loads are aligned and width
   // is a multiple of a piece
-  __device__ __forceinline__ void load(const T* p, long long st, int rows, int width, bool vec) {
+  __device__ __forceinline__ void load(const T* p, long long st, int rows, int width, bool vec, int tid) {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int idx = i * kThreads + static_cast<int>(threadIdx.x);
+      const int idx = i * kThreads + tid;
       const int row = idx / kRowPieces, col = (idx % kRowPieces) * kVec;
       r[i] = u32x4_t{0u, 0u, 0u, 0u};
       if (row < rows && col < width) {
@@ -176,10 +186,10 @@ struct TileLoad {
       }
     }
   }
-  __device__ __forceinline__ void store(T* lds) const {
+  __device__ __forceinline__ void store(T* lds, int tid) const {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int idx = i * kThreads + static_cast<int>(threadIdx.x);
+      const int idx = i * kThreads + tid;
       const int row = idx / kRowPieces, col = (idx % kRowPieces) * kVec;
       *reinterpret_cast<u32x4_t*>(lds + row * kLd + col) = r[i];
     }
@@ -210,30 +220,43 @@ __device__ __forceinline__ double read_lane_d(double v, int lane) {
   return __longlong_as_double((static_cast<long long>(hi) << 32) | static_cast<unsigned>(lo));
 }
 
-// One chunk's gates.  c is the inclusive prefix sum of the log2 decays, summed
-// in float64 and kept as two floats, so that e^{c_i - c_j} keeps float32
-// accuracy after a reset (log decay -inf) has made both sums large.
+// The gates of a chunk of Q tokens.  c is the inclusive prefix sum of the log2
+// decays, summed in float64 and kept as two floats, so that e^{c_i - c_j}
+// keeps float32 accuracy after a reset (log decay -inf) has made both sums
+// large.
+template <int Q>
 struct Gates {
-  float hi[kQ], lo[kQ];   // c
-  float b[kQ];            // input gates
-  float first[kQ];        // e^{c_i}
-  float last[kQ];         // e^{c_end - c_j}
-  float own[kQ];          // e^{g_t}
-  float end[4];           // e^{c_end}
+  float hi[Q], lo[Q];   // c
+  float b[Q];           // input gates
+  float first[Q];       // e^{c_i}
+  float last[Q];        // e^{c_end - c_j}
+  float own[Q];         // e^{g_t}
+  float end[4];         // e^{c_end}
 };
 
-// lane = token; by one wave.  Returns c_end.
-__device__ __forceinline__ double write_gates(Gates& G, float log_decay, float gate, int lane) {
-  const float ld = log_decay < kMinLogDecay ? kMinLogDecay : log_decay;   // keeps NaN
-  const double c = wave_prefix_d(static_cast<double>(ld) * static_cast<double>(1.44269504088896340736));
-  const double e = read_lane_d(c, 63);
-  const float hi = static_cast<float>(c);
-  G.hi[lane] = hi;
-  G.lo[lane] = static_cast<float>(c - static_cast<double>(hi));
-  G.b[lane] = gate;
-  G.own[lane] = __builtin_amdgcn_exp2f(ld * kLog2e);
-  G.first[lane] = __builtin_amdgcn_exp2f(static_cast<float>(c));
-  G.last[lane] = __builtin_amdgcn_exp2f(static_cast<float>(e - c));
+// By one wave: lane l brings the gates of tokens l, 64 + l, ...  Returns c_end.
+template <int Q>
+__device__ __forceinline__ double write_gates(Gates<Q>& G, const float (&log_decay)[Q / 64], const float (&gate)[Q / 64],
+                                              int lane) {
+  float ld[Q / 64];
+  double c[Q / 64], e = 0.0;
+#pragma unroll
+  for (int u = 0; u < Q / 64; ++u) {
+    ld[u] = log_decay[u] < kMinLogDecay ? kMinLogDecay : log_decay[u];   // keeps NaN
+    c[u] = e + wave_prefix_d(static_cast<double>(ld[u]) * static_cast<double>(1.44269504088896340736));
+    e = read_lane_d(c[u], 63);
+  }
+#pragma unroll
+  for (int u = 0; u < Q / 64; ++u) {
+    const int t = 64 * u + lane;
+    const float hi = static_cast<float>(c[u]);
+    G.hi[t] = hi;
+    G.lo[t] = static_cast<float>(c[u] - static_cast<double>(hi));
+    G.b[t] = gate[u];
+    G.own[t] = __builtin_amdgcn_exp2f(ld[u] * kLog2e);
+    G.first[t] = __builtin_amdgcn_exp2f(static_cast<float>(c[u]));
+    G.last[t] = __builtin_amdgcn_exp2f(static_cast<float>(e - c[u]));
+  }
   if (lane == 0) G.end[0] = __builtin_amdgcn_exp2f(static_cast<float>(e));
   return e;
 }
@@ -242,16 +265,22 @@ __device__ __forceinline__ float between(float hi_i, float lo_i, float hi_j, flo
   return __builtin_amdgcn_exp2f((hi_i - hi_j) + (lo_i - lo_j));
 }
 
-// The ten 16 x 16 tiles on and below the diagonal of a kQ x kQ matrix, dealt
-// to four waves (three at most each): tile t of wave w is (row, column) block
-// (tile_row(w, t), tile_col(w, t)).
-constexpr int kMaxTiles = 3;
-__device__ __forceinline__ int tile_count(int w) { return w == 3 ? 1 : 3; }
-__device__ __forceinline__ int tile_row(int w, int t) {
-  return t < 2 ? (w < 2 ? 3 : 2) : (w == 0 ? 0 : 1);
+// Tile e of the 16 x 16 tiles on and below the diagonal, row by row.
+__device__ __forceinline__ int tile_row(int e) {
+  int r = 0;
+  while ((r + 1) * (r + 2) / 2 <= e) ++r;
+  return r;
 }
-__device__ __forceinline__ int tile_col(int w, int t) {
-  return t == 2 ? (w == 2 ? 1 : 0) : (w == 1 || w == 3 ? 2 + t : t);
+__device__ __forceinline__ int tile_col(int e, int row) { return e - row * (row + 1) / 2; }
+
+// 8 consecutive floats of LDS.
+__device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
+  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] = a[i];
+    o[4 + i] = b[i];
+  }
 }
 
 }  // namespace scan
