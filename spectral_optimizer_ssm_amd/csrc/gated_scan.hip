@@ -52,14 +52,14 @@ struct WalkPair {
 // the tokens' products with the halves are partial sums of y, which the two
 // waves of the same rows exchange through LDS, each finishing half of the
 // tokens.  Eight waves a workgroup rather than four (160 -> ... us).
-template <typename T, int NT, bool READ>
+template <typename T, int NT, bool READ, bool VEC>
 __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_walk_kernel(WalkPair W) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
   typedef WalkLds<T, NT> L;
   constexpr int kT = NT / 32;       // state tiles of a wave
   extern __shared__ __attribute__((aligned(16))) char lds[];
-  const ScanWalk& A = W.w[blockIdx.y];
+  const ScanWalk A = W.w[blockIdx.y];
   T* lk = reinterpret_cast<T*>(lds + L::k);
   T* lx = reinterpret_cast<T*>(lds + L::x);
   T* lq = reinterpret_cast<T*>(lds + L::q);
@@ -67,66 +67,73 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_wal
   f32x4_t* ly = reinterpret_cast<f32x4_t*>(lds + L::y);
   Gates<kQ>* gates = reinterpret_cast<Gates<kQ>*>(lds + L::gates);
 
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l16 = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g4 = lane >> 4;
   const int pw = w & 3, nh = w >> 2, nbase = nh * (NT / 2);
   const int vheads = A.heads * A.pblocks;
-  const long long item = blockIdx.x;
-  const int seg = static_cast<int>(item % A.nseg);
-  const int vh = static_cast<int>(item / A.nseg % vheads);
-  const long long bi = item / A.nseg / vheads;
+  const int seg = static_cast<int>(blockIdx.x) % A.nseg;
+  const int vh = static_cast<int>(blockIdx.x) / A.nseg % vheads;
+  const long long bi = static_cast<int>(blockIdx.x) / A.nseg / vheads;
   const int h = vh / A.pblocks, pb = vh - h * A.pblocks, grp = h / (A.heads / A.groups);
   const int rows_p = A.P - pb * kPB < kPB ? A.P - pb * kPB : kPB;
   if (A.totals && seg + 1 == A.nseg) return;   // nothing starts after the last segment
   const long long vrow = bi * vheads + vh;
+  const bool reverse = A.reverse != 0;
   const int cc0 = seg * A.seg_chunks;
   const int cc1 = cc0 + A.seg_chunks < A.nchunks ? cc0 + A.seg_chunks : A.nchunks;
 
+  const int N = A.N, last_chunk = A.nchunks - 1;
+  const long long tokens = A.tokens, xst = A.x.st, kst = A.k.st, qst = A.q.st, gst = A.g.st, bst = A.b.st;
   const T* xp = static_cast<const T*>(A.x.p) + bi * A.x.sb + h * A.x.sh + pb * kPB;
   const T* kp = static_cast<const T*>(A.k.p) + bi * A.k.sb + grp * A.k.sh;
   const T* qp = READ ? static_cast<const T*>(A.q.p) + bi * A.q.sb + grp * A.q.sh : nullptr;
   const float* gp = static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh;
   const float* bp = A.b.p == nullptr ? nullptr : static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh;
+  T* yp = READ ? static_cast<T*>(A.y) + (bi * tokens * A.heads + h) * A.P + pb * kPB : nullptr;
+  const long long yst = static_cast<long long>(A.heads) * A.P;
 
-  // token of a lane in the cc-th chunk visited; its gates (past the end: no decay, no input)
-  const auto chunk_of = [&](int cc) { return A.reverse ? A.nchunks - 1 - cc : cc; };
+  const auto chunk_of = [&](int cc) { return reverse ? last_chunk - cc : cc; };
+  const auto rows_of = [&](int chunk) {
+    const long long left = tokens - static_cast<long long>(chunk) * kQ;
+    return left < kQ ? static_cast<int>(left) : kQ;
+  };
+  // gates of the cc-th chunk visited, a token a lane (past the end: no decay, no input)
   float gv[1] = {0.0f}, bv[1] = {0.0f};
   const auto load_gates = [&](int cc) {
-    const long long t = static_cast<long long>(chunk_of(cc)) * kQ + lane;
-    gv[0] = 0.0f;
-    bv[0] = 0.0f;
-    if (t < A.tokens) {
-      gv[0] = gp[t * A.g.st];
-      bv[0] = bp == nullptr ? 1.0f : bp[t * A.b.st];
+    const int chunk = chunk_of(cc), rows = rows_of(chunk);
+    const long long t = static_cast<long long>(chunk) * kQ + lane;
+    gv[0] = bv[0] = 0.0f;
+    if (lane < rows) {
+      gv[0] = gp[t * gst];
+      bv[0] = bp == nullptr ? 1.0f : bp[t * bst];
     }
   };
 
-  TileLoad<T, NT, kQ, kWalkThreads> tk, tq;
-  TileLoad<T, kPB, kQ, kWalkThreads> tx;
-  const auto load_tiles = [&](int cc, int tid) {
-    const long long t0 = static_cast<long long>(chunk_of(cc)) * kQ;
-    const int rows = A.tokens - t0 < kQ ? static_cast<int>(A.tokens - t0) : kQ;
-    tk.load(kp + t0 * A.k.st, A.k.st, rows, A.N, A.k.vec, tid);
-    tx.load(xp + t0 * A.x.st, A.x.st, rows, rows_p, A.x.vec && rows_p % O::kVec == 0, tid);
-    if constexpr (READ) tq.load(qp + t0 * A.q.st, A.q.st, rows, A.N, A.q.vec, tid);
+  TileLoad<T, NT, kQ, kWalkThreads, VEC> tk, tq;
+  TileLoad<T, kPB, kQ, kWalkThreads, VEC> tx;
+  const auto load_tiles = [&](int cc) {
+    const int chunk = chunk_of(cc), rows = rows_of(chunk);
+    const long long t0 = static_cast<long long>(chunk) * kQ;
+    tk.load(kp + t0 * kst, kst, rows, N, tid);
+    tx.load(xp + t0 * xst, xst, rows, rows_p, tid);
+    if constexpr (READ) tq.load(qp + t0 * qst, qst, rows, N, tid);
   };
 
   // the state: tile t holds S^T rows n = nbase + 16 t + 4 g4 + 0..3, column p = 16 pw + l16
   f32x4_t st[kT];
-  const int prow = pb * kPB + 16 * pw + l16;
-  const long long tile_off = static_cast<long long>(16 * pw + l16) * NT + nbase + 4 * g4;
+  const int prow = pb * kPB + 16 * pw + l16, tile_off = (16 * pw + l16) * NT + nbase + 4 * g4;
   if (A.seg_state != nullptr && !A.totals) {
     const float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off;
 #pragma unroll
     for (int t = 0; t < kT; ++t) st[t] = *reinterpret_cast<const f32x4_t*>(sp + 16 * t);
   } else {
     const bool init = A.init != nullptr && !A.totals;
-    const float* sp = A.init + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
+    const float* sp = A.init + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(N);
 #pragma unroll
     for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int n = nbase + 16 * t + 4 * g4 + r;
-        st[t][r] = init && prow < A.P && n < A.N ? sp[n] : 0.0f;
+        st[t][r] = init && prow < A.P && n < N ? sp[n] : 0.0f;
       }
   }
 
@@ -139,41 +146,46 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_wal
       for (int e = 0; e < 4; ++e) lm[(r0 + l16) * L::kLdM + c0 + 4 * g4 + e] = O::from_f32(0.0f);
     }
   }
+  float* states = A.states == nullptr ? nullptr : A.states + vrow * A.nblocks * (kPB * NT);
+  const int keep = A.keep;
   double seg_log = 0.0;
-  load_tiles(cc0, threadIdx.x);
+  load_tiles(cc0);
   if (w == 7) {
     load_gates(cc0);
-    seg_log += write_gates(gates[cc0 & 1], gv, bv, lane);
+    seg_log += write_gates(gates[cc0 & 1], gv, bv, lane, reverse);
     if (cc0 + 1 < cc1) load_gates(cc0 + 1);
   }
   for (int cc = cc0; cc < cc1; ++cc) {
     __syncthreads();   // the last chunk's tiles are done with
-    tk.store(lk, threadIdx.x);
-    tx.store(lx, threadIdx.x);
-    if constexpr (READ) tq.store(lq, threadIdx.x);
+    tk.store(lk, tid);
+    tx.store(lx, tid);
+    if constexpr (READ) tq.store(lq, tid);
     __syncthreads();
     const Gates<kQ>& G = gates[cc & 1];
-    if (cc + 1 < cc1) load_tiles(cc + 1, threadIdx.x);
+    if (cc + 1 < cc1) load_tiles(cc + 1);
     const int chunk = chunk_of(cc);
-    const long long t0 = static_cast<long long>(chunk) * kQ;
 
     f32x4_t y[4];   // y^T: rows p = 16 pw + 4 g4 + 0..3, column i = 16 it + l16
     if constexpr (READ) {
       // M^T tiles: rows j, columns i, so a lane's four values are neighbours in M
-      for (int e = w; e < 10; e += 8) {
-        const int it = tile_row(e), jt = tile_col(e, it);
-        f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int s = 0; s < NT / 32; ++s)
-          a = O::mma(O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4),
-                     O::row(lq + (16 * it + l16) * L::kLdN + 32 * s + 8 * g4), a);
-        const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
-        const float hi = G.hi[i], lo = G.lo[i];
-        const f32x4_t jh = *reinterpret_cast<const f32x4_t*>(G.hi + j0), jl = *reinterpret_cast<const f32x4_t*>(G.lo + j0);
-        const f32x4_t jb = *reinterpret_cast<const f32x4_t*>(G.b + j0);
+      for (int u = 0; u < 2; ++u) {
+        const int e = w + 8 * u;
+        if (e < 10) {
+          const int it = tile_row(e), jt = tile_col(e, it);
+          f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) a[r] = j0 + r <= i ? a[r] * between(hi, lo, jh[r], jl[r]) * jb[r] : 0.0f;
-        O::store4(lm + i * L::kLdM + j0, a);
+          for (int s = 0; s < NT / 32; ++s)
+            a = O::mma(O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4),
+                       O::row(lq + (16 * it + l16) * L::kLdN + 32 * s + 8 * g4), a);
+          const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
+          const float hi = G.hi[i], lo = G.lo[i];
+          const f32x4_t jh = *reinterpret_cast<const f32x4_t*>(G.hi + j0), jl = *reinterpret_cast<const f32x4_t*>(G.lo + j0);
+          const f32x4_t jb = *reinterpret_cast<const f32x4_t*>(G.b + j0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) a[r] = j0 + r <= i ? a[r] * between(hi, lo, jh[r], jl[r]) * jb[r] : 0.0f;
+          O::store4(lm + i * L::kLdM + j0, a);
+        }
       }
       // what this half of S_in gives: S_in q_i
 #pragma unroll
@@ -193,16 +205,18 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_wal
         ly[(w * 2 + u) * 64 + lane] = nh == 0 ? y[2 + u] : y[u];
         y[u] = nh == 0 ? y[u] : y[2 + u];
       }
-    }
-    // the state that a block of `keep` chunks starts from (in reversed time: ends with)
-    if (A.states != nullptr &&
-        (A.reverse ? chunk % A.keep == A.keep - 1 || chunk == A.nchunks - 1 : chunk % A.keep == 0)) {
-      float* sp = A.states + (vrow * A.nblocks + chunk / A.keep) * (kPB * NT) + tile_off;
+    } else {
+      // the state that a block of `keep` chunks starts from (in reversed time: ends with)
+      if (states != nullptr && (reverse ? chunk % keep == keep - 1 || chunk == last_chunk : chunk % keep == 0)) {
+        float* sp = states + static_cast<long long>(chunk / keep) * (kPB * NT) + state_offset(nbase + 4 * g4, 16 * pw + l16);
 #pragma unroll
-      for (int t = 0; t < kT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sp[t * (kPB / 32) * 512 + r * 8] = st[t][r];
+      }
     }
     if (w == 7 && cc + 1 < cc1) {
-      seg_log += write_gates(gates[(cc + 1) & 1], gv, bv, lane);
+      seg_log += write_gates(gates[(cc + 1) & 1], gv, bv, lane, reverse);
       if (cc + 2 < cc1) load_gates(cc + 2);
     }
 
@@ -214,16 +228,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_wal
     for (int s = 0; s < kQ / 32; ++s) {
       float xv[8], wv[8];
       O::widen(O::col(lx, L::kLdP, 32 * s, 16 * pw, lane), xv);
-      const int j0 = 32 * s + 8 * g4;
-      if (A.reverse) {
-        load8(G.first + j0, wv);
-      } else {
-        float bw[8];
-        load8(G.last + j0, wv);
-        load8(G.b + j0, bw);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) wv[e] *= bw[e];
-      }
+      load8(G.in + 32 * s + 8 * g4, wv);
 #pragma unroll
       for (int e = 0; e < 8; ++e) xv[e] *= wv[e];
       Frag f[O::kSplit], kf[kT];
@@ -238,7 +243,6 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_wal
 
     if constexpr (READ) {
       __syncthreads();   // M and the halves of y are written
-      const int p0 = 16 * pw + 4 * g4;
 #pragma unroll
       for (int u = 0; u < 2; ++u) y[u] = (y[u] + ly[((w ^ 4) * 2 + u) * 64 + lane]) * G.first[32 * nh + 16 * u + l16];
 #pragma unroll
@@ -249,20 +253,9 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_wal
           for (int u = 0; u < 2; ++u)
             y[u] = O::mma(vf, O::row(lm + (32 * nh + 16 * u + l16) * L::kLdM + 32 * s + 8 * g4), y[u]);
         }
+      const TileStore<T, VEC> out(yp + static_cast<long long>(chunk) * kQ * yst, yst, rows_of(chunk), rows_p);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const long long t = t0 + 32 * nh + 16 * u + l16;
-        if (t < A.tokens && p0 < rows_p) {
-          T* yp = static_cast<T*>(A.y) + ((bi * A.tokens + t) * A.heads + h) * A.P + pb * kPB + p0;
-          if (A.yvec) {
-            O::store4(yp, y[u]);
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (p0 + r < rows_p) yp[r] = O::from_f32(y[u][r]);
-          }
-        }
-      }
+      for (int u = 0; u < 2; ++u) out.put(32 * nh + 16 * u + l16, 16 * pw + 4 * g4, y[u]);
     }
   }
 
@@ -272,13 +265,13 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_wal
     for (int t = 0; t < kT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
     if (w == 7 && lane == 0) A.seg_decay[vrow * A.nseg + seg] = __builtin_amdgcn_exp2f(static_cast<float>(seg_log));
   } else if (A.fin != nullptr && cc1 == A.nchunks) {
-    float* sp = A.fin + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
+    float* sp = A.fin + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(N);
 #pragma unroll
     for (int t = 0; t < kT; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int n = nbase + 16 * t + 4 * g4 + r;
-        if (prow < A.P && n < A.N) sp[n] = st[t][r];
+        if (prow < A.P && n < N) sp[n] = st[t][r];
       }
   }
 }
@@ -305,28 +298,32 @@ __global__ void __launch_bounds__(kStepThreads) scan_segments_kernel(WalkPair W,
   sp[static_cast<long long>(A.nseg - 1) * kPB * nt] = cur;
 }
 
-template <typename T, int NT, bool READ>
+template <typename T, int NT, bool READ, bool VEC>
 hipError_t walk(const WalkPair& W, int dirs, hipStream_t st) {
   const ScanWalk& a = W.w[0];
-  const int bytes = READ ? WalkLds<T, NT>::read_bytes : WalkLds<T, NT>::states_bytes;
-  const void* fn = reinterpret_cast<const void*>(scan_walk_kernel<T, NT, READ>);
+  constexpr int bytes = READ ? WalkLds<T, NT>::read_bytes : WalkLds<T, NT>::states_bytes;
+  const void* fn = reinterpret_cast<const void*>(scan_walk_kernel<T, NT, READ, VEC>);
   const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
   const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg;
-  hipLaunchKernelGGL((scan_walk_kernel<T, NT, READ>), dim3(static_cast<unsigned>(items), dirs), dim3(kWalkThreads), bytes, st,
+  hipLaunchKernelGGL((scan_walk_kernel<T, NT, READ, VEC>), dim3(static_cast<unsigned>(items), dirs), dim3(kWalkThreads), bytes, st,
                      W);
   return hipGetLastError();
 }
 
-template <typename T>
-hipError_t walk_any(const WalkPair& W, int dirs, bool read, hipStream_t st) {
-  if (W.w[0].N <= 64) return read ? walk<T, 64, true>(W, dirs, st) : walk<T, 64, false>(W, dirs, st);
-  return read ? walk<T, 128, true>(W, dirs, st) : walk<T, 128, false>(W, dirs, st);
+template <typename T, int NT>
+hipError_t walk_any(const WalkPair& W, int dirs, bool read, bool vec, hipStream_t st) {
+  if (read) return vec ? walk<T, NT, true, true>(W, dirs, st) : walk<T, NT, true, false>(W, dirs, st);
+  return vec ? walk<T, NT, false, true>(W, dirs, st) : walk<T, NT, false, false>(W, dirs, st);
+}
+hipError_t walk_any(const WalkPair& W, int dirs, bool read, bool vec, bool bf16, hipStream_t st) {
+  if (W.w[0].N <= 64) return bf16 ? walk_any<bf16_t, 64>(W, dirs, read, vec, st) : walk_any<float, 64>(W, dirs, read, vec, st);
+  return bf16 ? walk_any<bf16_t, 128>(W, dirs, read, vec, st) : walk_any<float, 128>(W, dirs, read, vec, st);
 }
 
 }  // namespace
 
-hipError_t launch_scan_walk(const ScanWalk* walks, int dirs, bool read, bool bf16, hipStream_t st) {
+hipError_t launch_scan_walk(const ScanWalk* walks, int dirs, bool read, bool vec, bool bf16, hipStream_t st) {
   WalkPair W{{walks[0], walks[dirs - 1]}};
   const ScanWalk& a = walks[0];
   if (a.nseg > 1) {
@@ -335,7 +332,7 @@ hipError_t launch_scan_walk(const ScanWalk* walks, int dirs, bool read, bool bf1
       x.totals = 1;
       x.states = nullptr;
     }
-    hipError_t e = bf16 ? walk_any<bf16_t>(S, dirs, false, st) : walk_any<float>(S, dirs, false, st);
+    hipError_t e = walk_any(S, dirs, false, vec, bf16, st);
     if (e != hipSuccess) return e;
     const int nt = scan_padded_n(a.N);
     const long long vrows = static_cast<long long>(a.batch) * a.heads * a.pblocks;
@@ -344,7 +341,7 @@ hipError_t launch_scan_walk(const ScanWalk* walks, int dirs, bool read, bool bf1
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  return bf16 ? walk_any<bf16_t>(W, dirs, read, st) : walk_any<float>(W, dirs, read, st);
+  return walk_any(W, dirs, read, vec, bf16, st);
 }
 
 // ---------------------------------------------------------------------------

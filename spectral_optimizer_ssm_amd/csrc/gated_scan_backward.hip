@@ -22,6 +22,8 @@
 // that dv reads are rounded to bfloat16 once; dq and dk take the states as
 // three bfloat16 pieces (float32 accuracy), since db and dg, which are
 // float32, are dot products of them.
+#include <type_traits>
+
 #include "scan_tiles.cuh"
 
 namespace muon {
@@ -43,12 +45,17 @@ struct GradLds {
   static constexpr int dy = v + Q * kLdP * (int)sizeof(T);        // [Q][kPB]; v and dy at the end: D [i][j]
   static constexpr int m = dy + Q * kLdP * (int)sizeof(T);        // (L A)^T [j][i]; at the end D^T
   static constexpr int gates = m + Q * kLdM * (int)sizeof(T);     // Gates
-  static constexpr int rows = gates + (int)sizeof(Gates<Q>);      // row sums of W by the first column tile of a run
+  static constexpr int rows = gates + (int)sizeof(Gates<Q>);      // row sums of W by column tile
   static constexpr int cols = rows + kTiles * Q * 4;              // column sums of L A E by row tile
   static constexpr int qs = cols + kTiles * Q * 4;                // e^{c_i} q_i . S_in^T dy_i by block of n
   static constexpr int ks = qs + kTiles * Q * 4;                  // e^{c_end - c_j} k_j . dS_out^T v_j by block of n
   static constexpr int through = ks + kTiles * Q * 4;             // <S_in, dS_out> by wave
-  static constexpr int bytes = through + kTiles * 4;
+  static constexpr int inside = through + 8 * 4;                  // by token, over a head's blocks of value rows:
+  static constexpr int leave = inside + Q * 4;                    //   what dg sums from t on, what it sums up to t,
+  static constexpr int dgate = leave + Q * 4;                     //   and db
+  static constexpr int bytes = dgate + Q * 4;
+  // dS_out [n][p] as the operand of dv goes where v was, if it fits
+  static constexpr bool kStateInV = NT * kLdP <= Q * kLdP;
   static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
   static_assert(kLdM <= 2 * kLdP, "D fits where v and dy were");
 };
@@ -62,7 +69,7 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-template <typename T, int NT, int Q>
+template <typename T, int NT, int Q, bool VEC>
 __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
@@ -87,6 +94,9 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
   float* lqs = reinterpret_cast<float*>(lds + L::qs);
   float* lks = reinterpret_cast<float*>(lds + L::ks);
   float* lthrough = reinterpret_cast<float*>(lds + L::through);
+  float* lin = reinterpret_cast<float*>(lds + L::inside);
+  float* lleave = reinterpret_cast<float*>(lds + L::leave);
+  float* ldb = reinterpret_cast<float*>(lds + L::dgate);
 
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g4 = lane >> 4;
   const int split = static_cast<int>(blockIdx.x % A.nsplit);
@@ -108,56 +118,58 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     return ((bi * vheads + h * A.pblocks + pb) * A.nblocks + c) * static_cast<long long>(kPB * NT);
   };
 
-  TileLoad<T, kPB, Q, kThreads> tv, tdy;
+  TileLoad<T, kPB, Q, kThreads, VEC> tv, tdy;
   float gv[kU], bv[kU];
-  const auto load_head = [&](int i, int tid) {
+  // (rows_ and bytes 0: nothing is read and zeros come back, so the last pass needs no branch around its prefetch)
+  const auto load_head = [&](int i, int rows_, int tid) {
     const int lane = tid & 63;
     const int h = h0 + i / A.pblocks, pb = i % A.pblocks, rp = rows_p_of(pb);
     const T* vp = static_cast<const T*>(A.v.p) + bi * A.v.sb + h * A.v.sh + t0 * A.v.st + pb * kPB;
     const T* dp = static_cast<const T*>(A.dy.p) + bi * A.dy.sb + h * A.dy.sh + t0 * A.dy.st + pb * kPB;
-    tv.load(vp, A.v.st, rows, rp, A.v.vec && rp % O::kVec == 0, tid);
-    tdy.load(dp, A.dy.st, rows, rp, A.dy.vec && rp % O::kVec == 0, tid);
-    if (w == kTiles - 1) {
+    tv.load(vp, A.v.st, rows_, rp, tid);
+    tdy.load(dp, A.dy.st, rows_, rp, tid);
+    const float* gp = static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh + t0 * A.g.st;
+    const float* bp = A.b.p == nullptr ? gp : static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh + t0 * A.b.st;
+    const long long bst = A.b.p == nullptr ? 0 : A.b.st;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int t = 64 * u + lane;
-        gv[u] = 0.0f;
-        bv[u] = 0.0f;
-        if (t < rows) {
-          gv[u] = (static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh)[(t0 + t) * A.g.st];
-          bv[u] = A.b.p == nullptr ? 1.0f : (static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh)[(t0 + t) * A.b.st];
-        }
-      }
+    for (int u = 0; u < kU; ++u) {   // by every wave, one uses them: a branch here costs more than the loads
+      const int t = 64 * u + lane, in = t < rows ? t : rows - 1;
+      gv[u] = gp[in * A.g.st];
+      bv[u] = bp[in * bst];
     }
   };
-  // the states as operands [n][p]: row n = n0 + l16, 8 components p = 32 s + 8 g4 + 0..7
+  // the states as operands: row n = n0 + l16, 8 components p = 32 s + 8 g4 + 0..7 (the walk's order, state_offset)
   const int nw0 = (w % (kBlocks / kNW)) * kNW, tg = w / (kBlocks / kNW);
-  const auto load_columns = [&](const float* base, int l16, int g4, float (&x)[kNW][kPB / 32][8]) {
+  const auto load_columns = [&](const float* base, int bytes, int lane, f32x4_t (&x)[kNW][kPB / 32][2]) {
+    const __amdgpu_buffer_rsrc_t r = rsrc(base, bytes);
 #pragma unroll
     for (int b = 0; b < kNW; ++b)
 #pragma unroll
       for (int s = 0; s < kPB / 32; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[b][s][e] = base[(32 * s + 8 * g4 + e) * NT + 16 * (nw0 + b) + l16];
+        for (int u = 0; u < 2; ++u) x[b][s][u] = load_f32x4(r, (nw0 * (kPB / 32) * 64 + lane) * 32, (b * (kPB / 32) + s) * 2048 + 16 * u);
   };
 
   {
-    TileLoad<T, NT, Q, kThreads> tq, tk;
-    tq.load(static_cast<const T*>(A.q.p) + bi * A.q.sb + grp * A.q.sh + t0 * A.q.st, A.q.st, rows, A.N, A.q.vec, tid);
-    tk.load(static_cast<const T*>(A.k.p) + bi * A.k.sb + grp * A.k.sh + t0 * A.k.st, A.k.st, rows, A.N, A.k.vec, tid);
+    TileLoad<T, NT, Q, kThreads, VEC> tq, tk;
+    tq.load(static_cast<const T*>(A.q.p) + bi * A.q.sb + grp * A.q.sh + t0 * A.q.st, A.q.st, rows, A.N, tid);
+    tk.load(static_cast<const T*>(A.k.p) + bi * A.k.sb + grp * A.k.sh + t0 * A.k.st, A.k.st, rows, A.N, tid);
     tq.store(lq, tid);
     tk.store(lk, tid);
   }
-  if (nvirt > 0) load_head(0, tid);
+  f32x4_t x[kNW][kPB / 32][2], y[kNW][kPB / 32][2];
+  if (nvirt > 0) {
+    load_head(0, rows, tid);
+    load_columns(A.states + state_at(0), kPB * NT * 4, lane, x);
+    load_columns(A.dstates + state_at(0), kPB * NT * 4, lane, y);
+  }
   // tiles of (L A)^T and slots of the sums that no wave writes
   for (int i = tid; i < Q * L::kLdM; i += kThreads) lm[i] = O::from_f32(0.0f);
-  for (int i = tid; i < kTiles * Q; i += kThreads) {
-    lrow[i] = 0.0f;
-    lcol[i] = 0.0f;
-  }
+  for (int i = tid; i < 4 * kTiles * Q; i += kThreads) lrow[i] = 0.0f;
   __syncthreads();
 
   // A and the sum of L b E, by tile: rows i, columns j
+  // (a wave with one tile less repeats its neighbour's first, to the same result, and leaves it out of D)
   const int tile0 = w * kAll / kTiles, ntile = (w + 1) * kAll / kTiles - tile0;
   int trow[kMaxTiles], tcol[kMaxTiles];
   f32x4_t sc[kMaxTiles], dsum[kMaxTiles];
@@ -166,9 +178,8 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     trow[t] = tile_row(tile0 + t);
     tcol[t] = tile_col(tile0 + t, trow[t]);
     sc[t] = dsum[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (t < ntile)
 #pragma unroll
-      for (int s = 0; s < NT / 32; ++s)
+    for (int s = 0; s < NT / 32; ++s)
         sc[t] = O::mma(O::row(lq + (16 * trow[t] + l16) * L::kLdN + 32 * s + 8 * g4),
                        O::row(lk + (16 * tcol[t] + l16) * L::kLdN + 32 * s + 8 * g4), sc[t]);
   }
@@ -179,26 +190,27 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
 #pragma unroll
     for (int u = 0; u < kTT; ++u) dq[b][u] = dk[b][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  float acc_in[kU] = {}, acc_leave[kU] = {}, acc_db[kU] = {}, acc_z = 0.0f;   // wave 0, over a head's blocks
+  float acc_z = 0.0f;   // <S_in, dS_out> over a head's blocks
   for (int i = 0; i < nvirt; ++i) {
     const int tid = fresh(threadIdx.x), lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
     const int h = h0 + i / A.pblocks, pb = i % A.pblocks;
-    const float* dsp = A.dstates + state_at(i);
-    float x[kNW][kPB / 32][8], y[kNW][kPB / 32][8];
-    load_columns(A.states + state_at(i), l16, g4, x);
-    load_columns(dsp, l16, g4, y);
     tv.store(lv, tid);
     tdy.store(ldy, tid);
-    if (w == kTiles - 1) write_gates(G, gv, bv, lane);
+    if (w == kTiles - 1) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {   // past the end: no decay, no input
+        const bool live = 64 * u + lane < rows;
+        gv[u] = live ? gv[u] : 0.0f;
+        bv[u] = !live ? 0.0f : A.b.p == nullptr ? 1.0f : bv[u];
+      }
+      write_gates(G, gv, bv, lane, false);
+    }
     __syncthreads();
-    if (i + 1 < nvirt) load_head(i + 1, tid);
     __builtin_amdgcn_sched_barrier(0);
 
-    float racc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int run = 0;
 #pragma unroll
     for (int t = 0; t < kMaxTiles; ++t) {
-      if (t < ntile) {
+      {
         const int it = trow[t], jt = tcol[t];
         f32x4_t e = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -208,7 +220,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
         const int j = 16 * jt + l16, i0 = 16 * it + 4 * g4;
         const float hi = G.hi[j], lo = G.lo[j], b = G.b[j];
         const f32x4_t ih = *reinterpret_cast<const f32x4_t*>(G.hi + i0), il = *reinterpret_cast<const f32x4_t*>(G.lo + i0);
-        f32x4_t mm;
+        f32x4_t mm, rs;
         float col = 0.0f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -217,26 +229,16 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
           dsum[t][r] = fmaf(d * e[r], b, dsum[t][r]);
           const float we = mm[r] * e[r];
           col += we;
-          racc[r] = fmaf(we, b, racc[r]);
+          rs[r] = row_sum(we * b);
         }
         O::store4(lm + j * L::kLdM + i0, mm);
         col += __shfl_xor(col, 16, kWave);
         col += __shfl_xor(col, 32, kWave);
         if (g4 == 0) lcol[it * Q + j] = col;
-        if (t + 1 == ntile || trow[t + 1 < kMaxTiles ? t + 1 : t] != it) {   // the run in this row of tiles ends
-          f32x4_t rs;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            rs[r] = row_sum(racc[r]);
-            racc[r] = 0.0f;
-          }
-          if (l16 == 0) *reinterpret_cast<f32x4_t*>(lrow + tcol[run] * Q + i0) = rs;
-          run = t + 1;
-        }
+        if (l16 == 0) *reinterpret_cast<f32x4_t*>(lrow + jt * Q + i0) = rs;
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    __builtin_amdgcn_sched_barrier(0);
 
     // the states' part of dq, then of dk, and the states' product
     float through = 0.0f;
@@ -245,82 +247,113 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
 #pragma unroll
       for (int s = 0; s < kPB / 32; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) through = fmaf(x[b][s][e], y[b][s][e], through);
+        for (int e = 0; e < 8; ++e) through = fmaf(x[b][s][e / 4][e % 4], y[b][s][e / 4][e % 4], through);
     through = wave_total(through);
     if (lane == 0) lthrough[w] = tg == 0 ? through : 0.0f;
-    float sums[kTT];
-    const auto products = [&](const float (&xs)[kNW][kPB / 32][8], const T* tile, const T* other, const float* scale,
-                              const float* gate, f32x4_t (&out)[kNW][kTT], float* slot) {
-      const int lane = fresh(threadIdx.x) & 63, l16 = lane & 15, g4 = lane >> 4;
+    Frag f[kNW][kPB / 32][O::kSplit];
+    const auto split = [&](const f32x4_t (&xs)[kNW][kPB / 32][2]) {
 #pragma unroll
-      for (int u = 0; u < kTT; ++u) sums[u] = 0.0f;
-#pragma unroll
-      for (int b = 0; b < kNW; ++b) {
-        f32x4_t acc[kTT];
-#pragma unroll
-        for (int u = 0; u < kTT; ++u) acc[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int b = 0; b < kNW; ++b)
 #pragma unroll
         for (int s = 0; s < kPB / 32; ++s) {
-          Frag f[O::kSplit];
-          O::split(xs[b][s], f);
+          const f32x4_t a = xs[b][s][0], c = xs[b][s][1];
+          const float v[8] = {a[0], a[1], a[2], a[3], c[0], c[1], c[2], c[3]};
+          O::split(v, f[b][s]);
+        }
+    };
+    // four token tiles at a time, so that their sums and operands leave room for what stays
+    const auto products = [&](auto gated, const T* tile, const T* other, const float* scale, f32x4_t (&out)[kNW][kTT],
+                              float* slot) {
+      const int lane = fresh(threadIdx.x) & 63, l16 = lane & 15, g4 = lane >> 4;
 #pragma unroll
-          for (int u = 0; u < kTT; ++u) {
-            const Frag d = O::row(tile + (16 * (u * kTG + tg) + l16) * L::kLdP + 32 * s + 8 * g4);
+      for (int u0 = 0; u0 < kTT; u0 += 4) {
+        float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int z = O::kSplit - 1; z >= 0; --z) acc[u] = O::mma(f[z], d, acc[u]);
-            if (u % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        for (int b = 0; b < kNW; ++b) {
+          f32x4_t acc[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) acc[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int s = 0; s < kPB / 32; ++s) {
+            Frag d[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) d[u] = O::row(tile + (16 * ((u0 + u) * kTG + tg) + l16) * L::kLdP + 32 * s + 8 * g4);
+#pragma unroll
+            for (int z = O::kSplit - 1; z >= 0; --z)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) acc[u] = O::mma(f[b][s][z], d[u], acc[u]);
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int t = 16 * ((u0 + u) * kTG + tg) + l16;
+            const float sv = scale[t], gt = gated ? G.b[t] : 1.0f;
+            const f32x4_t ov = O::load4(other + t * L::kLdN + 16 * (nw0 + b) + 4 * g4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float a = acc[u][r] * sv;
+              sums[u] = fmaf(a, ov[r], sums[u]);
+              out[b][u0 + u][r] = gated ? fmaf(a, gt, out[b][u0 + u][r]) : out[b][u0 + u][r] + a;
+            }
           }
         }
 #pragma unroll
-        for (int u = 0; u < kTT; ++u) {
-          const int t = 16 * (u * kTG + tg) + l16;
-          const float sv = scale[t], gt = gate == nullptr ? 1.0f : gate[t];
-          const f32x4_t ov = O::load4(other + t * L::kLdN + 16 * (nw0 + b) + 4 * g4);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float a = acc[u][r] * sv;
-            sums[u] = fmaf(a, ov[r], sums[u]);
-            out[b][u][r] = gate == nullptr ? out[b][u][r] + a : fmaf(a, gt, out[b][u][r]);
-          }
-          if (u % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        for (int u = 0; u < 4; ++u) {
+          sums[u] += __shfl_xor(sums[u], 16, kWave);
+          sums[u] += __shfl_xor(sums[u], 32, kWave);
         }
-      }
+        if (g4 == 0)
 #pragma unroll
-      for (int u = 0; u < kTT; ++u) {
-        sums[u] += __shfl_xor(sums[u], 16, kWave);
-        sums[u] += __shfl_xor(sums[u], 32, kWave);
-        if (g4 == 0) slot[nw0 / kNW * Q + 16 * (u * kTG + tg) + l16] = sums[u];
+          for (int u = 0; u < 4; ++u) slot[nw0 / kNW * Q + 16 * ((u0 + u) * kTG + tg) + l16] = sums[u];
+        __builtin_amdgcn_sched_barrier(0);
       }
     };
-    products(x, ldy, lq, G.first, nullptr, dq, lqs);
-    __builtin_amdgcn_sched_barrier(0);
-    // dS_out as the operand of dv: row p = 16 (w % 4) + l16, 8 columns n = 32 s + 8 g4 + 0..7
-    f32x4_t zs[NT / 32][2];
-    const int zl = fresh(threadIdx.x) & 63;
-#pragma unroll
-    for (int s = 0; s < NT / 32; ++s)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        zs[s][u] = *reinterpret_cast<const f32x4_t*>(dsp + (16 * (w & 3) + (zl & 15)) * NT + 32 * s + 8 * (zl >> 4) + 4 * u);
-    products(y, lv, lk, G.last, G.b, dk, lks);
-    __builtin_amdgcn_sched_barrier(0);
-
+    split(x);
+    products(std::false_type(), ldy, lq, G.first, dq, lqs);
+    split(y);
+    products(std::true_type(), lv, lk, G.last, dk, lks);
+    __syncthreads();   // (L A)^T and the sums are written, v is done with
     {
       const int lane = fresh(threadIdx.x) & 63, l16 = lane & 15, g4 = lane >> 4;
-      // z^T: rows p = 16 (w % 4) + 4 g4 + 0..3, column j = 16 (kZG u + w / 4) + l16; the states' part first
-      f32x4_t z[4];
+      if constexpr (L::kStateInV) {
+        // dS_out [n][p], rounded, as the operand of dv
+        if (tg == 0)
 #pragma unroll
-      for (int u = 0; u < 4; ++u) z[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int b = 0; b < kNW; ++b)
 #pragma unroll
-      for (int s = 0; s < NT / 32; ++s) {
-        const Frag f = frag_from_acc<T>(zs[s][0], zs[s][1]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          z[u] = O::mma(f, O::row(lk + (16 * (kZG * u + (w >> 2)) + l16) * L::kLdN + 32 * s + 8 * g4), z[u]);
+            for (int s = 0; s < kPB / 32; ++s) {
+              T* p = lv + (16 * (nw0 + b) + l16) * L::kLdP + 32 * s + 8 * g4;   // the first of its pieces
+              *reinterpret_cast<Frag*>(p) = f[b][s][0];
+            }
       }
+      // the next head's tiles and states
+      const float* dsp = A.dstates + state_at(i);
+      const bool more = i + 1 < nvirt;
+      const int next = more ? i + 1 : i;
+      load_head(next, more ? rows : 0, fresh(threadIdx.x));
+      load_columns(A.states + state_at(next), more ? kPB * NT * 4 : 0, lane, x);
+      load_columns(A.dstates + state_at(next), more ? kPB * NT * 4 : 0, lane, y);
+      __builtin_amdgcn_sched_barrier(0);
+      // sums of a token: 16 tokens a wave, one of the four kinds each quarter of it
+      {
+        const int t = 16 * w + l16;
+        const float* src = reinterpret_cast<const float*>(lds + L::rows) + g4 * kTiles * Q + t;
+        float a = 0.0f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) z[u] *= G.last[16 * (kZG * u + (w >> 2)) + l16];
-      __syncthreads();   // (L A)^T and the sums are written
+        for (int e = 0; e < kTiles; ++e) a += src[e * Q];
+        const float b = G.b[t];
+        const float cs = __shfl_xor(a, 16, kWave), us = __shfl_xor(a, 32, kWave), ws = __shfl_xor(a, 48, kWave);
+        if (g4 == 0) {   // a: the row's sum
+          const float in = a - b * cs + us, lv_ = b * ws, d = cs + ws;
+          lin[t] = pb == 0 ? in : lin[t] + in;
+          lleave[t] = pb == 0 ? lv_ : lleave[t] + lv_;
+          ldb[t] = pb == 0 ? d : ldb[t] + d;
+        }
+      }
+
+      // z^T: rows p = 16 (w % 4) + 4 g4 + 0..3, column j = 16 (kZG u + w / 4) + l16
+      f32x4_t z[4], zs[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) z[u] = zs[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int s = 0; s < Q / 32; ++s) {
         const Frag f = O::col(ldy, L::kLdP, 32 * s, 16 * (w & 3), lane);
@@ -331,68 +364,58 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
             z[u] = O::mma(f, O::row(lm + (16 * jt + l16) * L::kLdM + 32 * s + 8 * g4), z[u]);
         }
       }
-      const int rp = rows_p_of(pb), p0 = 16 * (w & 3) + 4 * g4;
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (L::kStateInV) __syncthreads();   // dS_out is written
+#pragma unroll
+      for (int s = 0; s < NT / 32; ++s) {
+        Frag f;
+        if constexpr (L::kStateInV) {
+          f = O::col(lv, L::kLdP, 32 * s, 16 * (w & 3), lane);
+        } else {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = dsp[state_offset(32 * s + 8 * g4 + e, 16 * (w & 3) + l16)];
+          f = O::narrow(v);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          zs[u] = O::mma(f, O::row(lk + (16 * (kZG * u + (w >> 2)) + l16) * L::kLdN + 32 * s + 8 * g4), zs[u]);
+      }
+      const TileStore<T, VEC> out(static_cast<T*>(A.dv) + ((bi * A.tokens + t0) * A.heads + h) * A.P + pb * kPB,
+                                  static_cast<long long>(A.heads) * A.P, rows, rows_p_of(pb));
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int j = 16 * (kZG * u + (w >> 2)) + l16;
-        if (j < rows && p0 < rp) {
-          const f32x4_t o = z[u] * G.b[j];
-          T* op = static_cast<T*>(A.dv) + ((bi * A.tokens + t0 + j) * A.heads + h) * A.P + pb * kPB + p0;
-          if (A.dvvec) {
-            O::store4(op, o);
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (p0 + r < rp) op[r] = O::from_f32(o[r]);
-          }
-        }
+        out.put(j, 16 * (w & 3) + 4 * g4, (z[u] + zs[u] * G.last[j]) * G.b[j]);
       }
     }
+    if constexpr (!L::kStateInV) __syncthreads();   // the tokens' sums are written
 
     if (w == 0) {
       const int lane = fresh(threadIdx.x) & 63;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int t = 64 * u + lane;
-        float rs = 0.0f, cs = 0.0f, us = 0.0f, ws = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kTiles; ++e) {
-          rs += lrow[e * Q + t];
-          cs += lcol[e * Q + t];
-        }
-#pragma unroll
-        for (int e = 0; e < kBlocks / kNW; ++e) {
-          us += lqs[e * Q + t];
-          ws += lks[e * Q + t];
-        }
-        const float b = G.b[t];
-        acc_in[u] += rs - b * cs + us;
-        acc_leave[u] = fmaf(b, ws, acc_leave[u]);
-        acc_db[u] += cs + ws;
-      }
-#pragma unroll
       for (int e = 0; e < kTiles; ++e) acc_z += lthrough[e];
       if (pb + 1 == A.pblocks) {
-        double pin[kU], pl[kU], tin = 0.0, tl = 0.0;
+        // with a_t what dg sums from t on and l_t what it sums up to t: the sum of all a, plus those of l - a before t
+        double before[kU], total = 0.0, all = 0.0;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          pin[u] = tin + wave_prefix_d(static_cast<double>(acc_in[u]));
-          pl[u] = tl + wave_prefix_d(static_cast<double>(acc_leave[u]));
-          tin = read_lane_d(pin[u], 63);
-          tl = read_lane_d(pl[u], 63);
+          const double a = static_cast<double>(lin[64 * u + lane]), d = static_cast<double>(lleave[64 * u + lane]) - a;
+          const double p = wave_prefix_d(d);
+          before[u] = total + p - d;
+          total += read_lane_d(p, 63);
+          all += read_lane_d(wave_prefix_d(a), 63);
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int t = 64 * u + lane;
           if (t < rows) {
             const long long o = (bi * A.tokens + t0 + t) * A.heads + h;
-            const double d = tin - pin[u] + static_cast<double>(acc_in[u]) + pl[u] - static_cast<double>(acc_leave[u]) +
-                             static_cast<double>(G.end[0]) * static_cast<double>(acc_z);
+            const double d = all + before[u] + static_cast<double>(G.end[0]) * static_cast<double>(acc_z);
             // nothing crosses a token whose decay is 0: what the sums leave there is rounding
             A.dg[o] = G.own[t] == 0.0f ? 0.0f : static_cast<float>(d);
-            if (A.db != nullptr) A.db[o] = acc_db[u];
+            if (A.db != nullptr) A.db[o] = ldb[t];
           }
-          acc_in[u] = acc_leave[u] = acc_db[u] = 0.0f;
         }
         acc_z = 0.0f;
       }
@@ -407,7 +430,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < kMaxTiles; ++t) {
-    if (t < ntile) {
+    if (t + 1 < kMaxTiles || t < ntile) {
       const int j = 16 * tcol[t] + l16, i0 = 16 * trow[t] + 4 * g4;
       O::store4(lm + j * L::kLdM + i0, dsum[t]);
 #pragma unroll
@@ -478,15 +501,15 @@ __global__ void __launch_bounds__(kPartThreads) scan_parts_kernel(const float* p
   else dk[i - half] = Ops<T>::from_f32(s);
 }
 
-template <typename T, int NT>
+template <typename T, int NT, bool VEC>
 hipError_t grad(const ScanGrad& A, hipStream_t st) {
   constexpr int Q = sizeof(T) == 2 ? kScanGradBf16 : kScanGradF32;
   constexpr int bytes = GradLds<T, NT, Q>::bytes;
-  const void* fn = reinterpret_cast<const void*>(scan_grad_kernel<T, NT, Q>);
+  const void* fn = reinterpret_cast<const void*>(scan_grad_kernel<T, NT, Q, VEC>);
   hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
   const long long items = static_cast<long long>(A.batch) * A.nblocks * A.groups * A.nsplit;
-  hipLaunchKernelGGL((scan_grad_kernel<T, NT, Q>), dim3(static_cast<unsigned>(items)), dim3(4 * Q), bytes, st, A);
+  hipLaunchKernelGGL((scan_grad_kernel<T, NT, Q, VEC>), dim3(static_cast<unsigned>(items)), dim3(4 * Q), bytes, st, A);
   e = hipGetLastError();
   if (e != hipSuccess || A.nsplit == 1) return e;
   const long long half = static_cast<long long>(A.batch) * A.tokens * A.groups * A.N;
@@ -497,9 +520,13 @@ hipError_t grad(const ScanGrad& A, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_scan_grad(const ScanGrad& A, bool bf16, hipStream_t st) {
-  if (A.N <= 64) return bf16 ? grad<bf16_t, 64>(A, st) : grad<float, 64>(A, st);
-  return bf16 ? grad<bf16_t, 128>(A, st) : grad<float, 128>(A, st);
+hipError_t launch_scan_grad(const ScanGrad& A, bool vec, bool bf16, hipStream_t st) {
+  if (bf16) {
+    if (A.N <= 64) return vec ? grad<bf16_t, 64, true>(A, st) : grad<bf16_t, 64, false>(A, st);
+    return vec ? grad<bf16_t, 128, true>(A, st) : grad<bf16_t, 128, false>(A, st);
+  }
+  if (A.N <= 64) return vec ? grad<float, 64, true>(A, st) : grad<float, 64, false>(A, st);
+  return vec ? grad<float, 128, true>(A, st) : grad<float, 128, false>(A, st);
 }
 
 }  // namespace muon

@@ -311,7 +311,6 @@ inline int scan_padded_n(int n) { return n <= 64 ? 64 : 128; }
 struct SeqOperand {    // [batch][tokens][heads or groups][width], innermost stride 1
   const void* p;
   long long sb, st, sh;   // strides in elements
-  int vec;             // every row is 16-byte aligned and a multiple of 16 bytes wide
 };
 struct ScanWalk {
   SeqOperand x, k, q;  // values, keys, queries; in reversed time dy and queries (q unused)
@@ -321,31 +320,38 @@ struct ScanWalk {
   int nseg, seg_chunks;       // segments of the time axis and their chunks
   int reverse;                // chunks from the last to the first, weights e^{c_i}
   int totals;                 // set by the launcher: segments from a zero state, into seg_state
-  int yvec;                   // rows of y take 4-element stores
   void* y;                    // [batch][tokens][heads][P]
   const float* init;          // null, or [batch][heads][P][N]: the state before the first chunk visited
   float* fin;                 // null, or the state after the last
   int keep, nblocks;          // blocks of `keep` chunks
-  float* states;              // null, or [batch][heads * pblocks][nblocks][kScanRows][padded N]: the
-                              // state that each block is visited with
+  float* states;              // null, or [batch][heads * pblocks][nblocks][kScanRows x padded N]: the
+                              // state that each block is visited with, in the order of state_offset
   float* seg_state;           // nseg > 1: [batch][heads * pblocks][nseg][kScanRows][padded N]
   float* seg_decay;           //           [batch][heads * pblocks][nseg]
 };
-// One walk, or two (dirs = 2, of equal sizes) in one launch.
-hipError_t launch_scan_walk(const ScanWalk* W, int dirs, bool read, bool bf16, hipStream_t st);
+// One walk, or two (dirs = 2, of equal sizes) in one launch; vec: see scan_vec.
+hipError_t launch_scan_walk(const ScanWalk* W, int dirs, bool read, bool vec, bool bf16, hipStream_t st);
+// Whether 16-byte buffer loads of rows of `width` elements fit an operand (es
+// bytes an element): every row starts aligned and holds whole pieces, rows do
+// not overlap, and a tile's rows lie within 32-bit offsets.
+inline bool scan_vec(const SeqOperand& s, int width, int es) {
+  const long long q = 16 / es;
+  return (reinterpret_cast<uintptr_t>(s.p) & 15u) == 0 && s.sb % q == 0 && s.st % q == 0 && s.sh % q == 0 && width % q == 0 &&
+         s.st >= width && s.st * es * kScanGradBf16 < (1LL << 31) - 256;
+}
 struct ScanGrad {
   SeqOperand v, k, q, dy, g, b;
   int batch, tokens, heads, groups, P, N, pblocks;
   int nblocks;                // blocks of kScanGradBf16 (float32: kScanGradF32) tokens
   int nsplit;                 // workgroups that share a block's heads
-  int dvvec, dkvec;           // rows of dv; of dq and dk: 4-element stores
+  int dkvec;                  // rows of dq and dk: 4-element stores
   const float* states;        // as ScanWalk.states: before each block
   const float* dstates;       // gradients of the states after each block
   void *dv, *dk, *dq;
   float *dg, *db;             // [batch][tokens][heads]; db may be null
   float* parts;               // nsplit > 1: [nsplit][2][batch * tokens * groups * N]
 };
-hipError_t launch_scan_grad(const ScanGrad& A, bool bf16, hipStream_t st);
+hipError_t launch_scan_grad(const ScanGrad& A, bool vec, bool bf16, hipStream_t st);
 struct ScanStep {
   SeqOperand v, k, q, g, b;
   int batch, heads, groups, P, N;

@@ -41,12 +41,7 @@ bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
 bool seq_ok(const muon_seq& s, size_t es) {
   return s.p != nullptr && aligned_to(s.p, es) && s.sb >= 0 && s.st >= 0 && s.sh >= 0;
 }
-// 16-byte loads of whole rows: every row starts aligned and holds a multiple of 16 bytes.
-SeqOperand operand(const muon_seq& s, int width, size_t es) {
-  const long long q = 16 / static_cast<long long>(es);
-  const bool vec = aligned16(s.p) && s.sb % q == 0 && s.st % q == 0 && s.sh % q == 0 && width % q == 0;
-  return {s.p, s.sb, s.st, s.sh, vec ? 1 : 0};
-}
+SeqOperand operand(const muon_seq& s) { return {s.p, s.sb, s.st, s.sh}; }
 
 int check_dims(const muon_scan_args* a) {
   if (a == nullptr) return MUON_EINVAL;
@@ -132,18 +127,23 @@ size_t scan_bytes(const muon_scan_args* a, bool backward) {
 
 ScanWalk walk_of(const muon_scan_args* a, const ScanPlan& p) {
   ScanWalk w{};
-  const size_t es = dtype_size(a->dtype);
-  w.x = operand(a->v, a->P, es);
-  w.k = operand(a->k, a->N, es);
-  w.q = operand(a->q, a->N, es);
-  w.g = operand(a->log_decay, 1, 4);
-  if (a->gate.p != nullptr) w.b = operand(a->gate, 1, 4);
+  w.x = operand(a->v);
+  w.k = operand(a->k);
+  w.q = operand(a->q);
+  w.g = operand(a->log_decay);
+  if (a->gate.p != nullptr) w.b = operand(a->gate);
   w.batch = a->batch; w.tokens = a->tokens; w.heads = a->heads; w.groups = a->groups;
   w.P = a->P; w.N = a->N;
   w.pblocks = p.pblocks; w.nchunks = p.nchunks; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
   w.keep = grad_tokens(a->dtype) / kScanChunk; w.nblocks = p.nblocks;
   w.init = a->S0;
   return w;
+}
+
+bool walk_vec(const ScanWalk& w, int es) { return scan_vec(w.x, w.P, es) && scan_vec(w.k, w.N, es); }
+// Rows of an output, `st` elements apart, take 4-element buffer stores.
+bool rows_out(const void* p, long long st, int width, int es) {
+  return width % 4 == 0 && aligned_to(p, 4 * es) && st * es * kScanGradBf16 < (1LL << 31) - 256;
 }
 
 size_t state_bytes(const muon_scan_args* a) { return static_cast<size_t>(a->batch) * a->heads * a->P * a->N * 4; }
@@ -173,7 +173,7 @@ int muon_gated_scan(const muon_scan_args* a, void* Y, float* S_out, void* worksp
   ScanPlan p;
   rc = plan_scan(a, false, &p);
   if (rc != MUON_OK) return rc;
-  const size_t es = dtype_size(a->dtype);
+  const int es = static_cast<int>(dtype_size(a->dtype));
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if (S_out != nullptr && !aligned_to(S_out, 4)) return MUON_EINVAL;
   if (a->batch == 0) return MUON_OK;
@@ -193,11 +193,11 @@ int muon_gated_scan(const muon_scan_args* a, void* Y, float* S_out, void* worksp
   ScanWalk w = walk_of(a, p);
   char* ws = static_cast<char*>(workspace);
   w.y = Y;
-  w.yvec = a->P % 4 == 0 && aligned_to(Y, 4 * es);
   w.fin = S_out;
   w.seg_state = p.nseg > 1 ? reinterpret_cast<float*>(ws + p.seg) : nullptr;
   w.seg_decay = p.nseg > 1 ? reinterpret_cast<float*>(ws + p.decay) : nullptr;
-  return launch_scan_walk(&w, 1, true, a->dtype == MUON_BF16, st) == hipSuccess ? MUON_OK : MUON_EHIP;
+  const bool vec = walk_vec(w, es) && scan_vec(w.q, a->N, es) && rows_out(Y, static_cast<long long>(a->heads) * a->P, a->P, es);
+  return launch_scan_walk(&w, 1, true, vec, a->dtype == MUON_BF16, st) == hipSuccess ? MUON_OK : MUON_EHIP;
 }
 
 size_t muon_gated_scan_backward_workspace_size(const muon_scan_args* args) { return scan_bytes(args, true); }
@@ -210,7 +210,7 @@ int muon_gated_scan_backward(const muon_scan_args* a, const muon_seq* dY, const 
   ScanPlan p;
   rc = plan_scan(a, true, &p);
   if (rc != MUON_OK) return rc;
-  const size_t es = dtype_size(a->dtype);
+  const int es = static_cast<int>(dtype_size(a->dtype));
   const hipStream_t st = static_cast<hipStream_t>(stream);
   if ((dS != nullptr && !aligned_to(dS, 4)) || (dS0 != nullptr && !aligned_to(dS0, 4))) return MUON_EINVAL;
   if (a->batch == 0) return MUON_OK;
@@ -242,7 +242,7 @@ int muon_gated_scan_backward(const muon_scan_args* a, const muon_seq* dY, const 
   // 1. the states before every block and the gradients of the states after it
   ScanWalk w[2] = {walk_of(a, p), walk_of(a, p)};
   w[0].states = at(p.states);
-  w[1].x = operand(*dY, a->P, es);
+  w[1].x = operand(*dY);
   w[1].k = w[1].q;
   w[1].reverse = 1;
   w[1].init = dS;
@@ -254,19 +254,19 @@ int muon_gated_scan_backward(const muon_scan_args* a, const muon_seq* dY, const 
     w[1].seg_state = at(p.seg2);
     w[1].seg_decay = at(p.decay2);
   }
-  if (launch_scan_walk(w, 2, false, bf16, st) != hipSuccess) return MUON_EHIP;
+  const bool vec = walk_vec(w[0], es) && walk_vec(w[1], es) && rows_out(dV, static_cast<long long>(a->heads) * a->P, a->P, es);
+  if (launch_scan_walk(w, 2, false, vec, bf16, st) != hipSuccess) return MUON_EHIP;
   // 2. the gradients, block by block
   ScanGrad r{};
   r.v = w[0].x; r.k = w[0].k; r.q = w[0].q; r.dy = w[1].x; r.g = w[0].g; r.b = w[0].b;
   r.batch = a->batch; r.tokens = a->tokens; r.heads = a->heads; r.groups = a->groups; r.P = a->P; r.N = a->N;
   r.pblocks = p.pblocks; r.nblocks = p.nblocks; r.nsplit = p.nsplit;
-  r.dvvec = a->P % 4 == 0 && aligned_to(dV, 4 * es);
   r.dkvec = a->N % 4 == 0 && aligned_to(dK, 4 * es) && aligned_to(dQ, 4 * es);
   r.states = at(p.states);
   r.dstates = at(p.dstates);
   r.dv = dV; r.dk = dK; r.dq = dQ; r.dg = dlog_decay; r.db = dgate;
   r.parts = at(p.parts);
-  return launch_scan_grad(r, bf16, st) == hipSuccess ? MUON_OK : MUON_EHIP;
+  return launch_scan_grad(r, vec, bf16, st) == hipSuccess ? MUON_OK : MUON_EHIP;
 }
 
 int muon_gated_scan_step(const muon_scan_args* a, void* Y, float* S_out, void* stream) {
@@ -288,11 +288,11 @@ int muon_gated_scan_step(const muon_scan_args* a, void* Y, float* S_out, void* s
   if (clash({span(Y, value_bytes(a)), so}, {v, k, q, g, gate_span(a), in_place ? Span{nullptr, 0} : s0})) return MUON_EINVAL;
   if (static_cast<long long>(a->batch) * a->heads * ((a->P + 15) / 16) > INT_MAX) return MUON_EUNSUPPORTED;
   ScanStep s{};
-  s.v = operand(a->v, a->P, es);
-  s.k = operand(a->k, a->N, es);
-  s.q = operand(a->q, a->N, es);
-  s.g = operand(a->log_decay, 1, 4);
-  if (a->gate.p != nullptr) s.b = operand(a->gate, 1, 4);
+  s.v = operand(a->v);
+  s.k = operand(a->k);
+  s.q = operand(a->q);
+  s.g = operand(a->log_decay);
+  if (a->gate.p != nullptr) s.b = operand(a->gate);
   s.batch = a->batch; s.heads = a->heads; s.groups = a->groups; s.P = a->P; s.N = a->N;
   s.y = Y;
   s.S = a->S0;

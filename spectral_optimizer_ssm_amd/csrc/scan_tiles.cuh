@@ -149,49 +149,89 @@ __device__ __forceinline__ int fresh(int v) {
   return v;
 }
 
+// Buffer resources: an access at or past `bytes` reads 0 and stores nothing,
+// so ragged tiles need no branches.  kNowhere is such an offset.
+constexpr int kNowhere = 0x7ffffff0;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), bytes, 0x00020000);
+}
+__device__ __forceinline__ float load_f32(__amdgpu_buffer_rsrc_t r, int offset) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0));
+}
+__device__ __forceinline__ f32x4_t load_f32x4(__amdgpu_buffer_rsrc_t r, int offset, int base) {
+  return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, offset, base, 0));
+}
+
 // A [ROWS][WIDTH] tile of a sequence operand on its way into LDS: 16-byte
-// pieces held in the registers of THREADS threads.  Rows past `rows` and
-// columns past `width` are zero.
-template <typename T, int WIDTH, int ROWS, int THREADS>
+// pieces held in the registers of THREADS threads.  Rows past the last token
+// and columns past `width` are zero.  VEC (chosen by the host, scan_vec): rows
+// start 16-byte aligned, hold whole pieces, do not overlap and lie within
+// 2 GiB of each other; otherwise element by element.
+template <typename T, int WIDTH, int ROWS, int THREADS, bool VEC>
 struct TileLoad {
-  static constexpr int kThreads = THREADS;
   static constexpr int kVec = Ops<T>::kVec;
   static constexpr int kRowPieces = WIDTH / kVec;
-  static constexpr int kPieces = ROWS * kRowPieces / kThreads;
-  static_assert(ROWS * kRowPieces % kThreads == 0, "whole pieces");
+  static constexpr int kPieces = ROWS * kRowPieces / THREADS;
   static constexpr int kLd = WIDTH + Ops<T>::kPad;
+  static_assert(ROWS * kRowPieces % THREADS == 0, "whole pieces");
   u32x4_t r[kPieces];
 
-  // p: element (token 0, column 0); vec: 16-byte loads are aligned and width
-  // is a multiple of a piece
-  __device__ __forceinline__ void load(const T* p, long long st, int rows, int width, bool vec, int tid) {
+  // p: element (first token, column 0); rows: tokens left, at most ROWS
+  __device__ __forceinline__ void load(const T* p, long long st, int rows, int width, int tid) {
+    if constexpr (VEC) {
+      const __amdgpu_buffer_rsrc_t b = rsrc(p, static_cast<int>(rows * st) * static_cast<int>(sizeof(T)));
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int idx = i * kThreads + tid;
-      const int row = idx / kRowPieces, col = (idx % kRowPieces) * kVec;
-      r[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (row < rows && col < width) {
+      for (int i = 0; i < kPieces; ++i) {
+        const int idx = i * THREADS + tid, row = idx / kRowPieces, col = (idx % kRowPieces) * kVec;
+        const int off = (row * static_cast<int>(st) + col) * static_cast<int>(sizeof(T));
+        r[i] = __builtin_amdgcn_raw_buffer_load_b128(b, col < width ? off : kNowhere, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int idx = i * THREADS + tid, row = idx / kRowPieces, col = (idx % kRowPieces) * kVec;
         const T* e = p + row * st + col;
-        if (vec) {
-          r[i] = *reinterpret_cast<const u32x4_t*>(e);
-        } else if constexpr (sizeof(T) == 2) {
+        r[i] = u32x4_t{0u, 0u, 0u, 0u};
+        if (row >= rows) continue;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (col + j < width) r[i][j / 2] |= static_cast<uint32_t>(e[j]) << (16 * (j & 1));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (col + j < width) r[i][j] = __float_as_uint(e[j]);
-        }
+        for (int j = 0; j < kVec; ++j)
+          if (col + j < width) {
+            if constexpr (sizeof(T) == 2) r[i][j / 2] |= static_cast<uint32_t>(e[j]) << (16 * (j & 1));
+            else r[i][j] = __float_as_uint(e[j]);
+          }
       }
     }
   }
   __device__ __forceinline__ void store(T* lds, int tid) const {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int idx = i * kThreads + tid;
-      const int row = idx / kRowPieces, col = (idx % kRowPieces) * kVec;
+      const int idx = i * THREADS + tid, row = idx / kRowPieces, col = (idx % kRowPieces) * kVec;
       *reinterpret_cast<u32x4_t*>(lds + row * kLd + col) = r[i];
+    }
+  }
+};
+
+// Four neighbours of an output row (columns col..col + 3 of `width`) at element
+// offset `off` of a tile of rows at p; rows < `rows` are written.
+template <typename T, bool VEC>
+struct TileStore {
+  T* p;
+  __amdgpu_buffer_rsrc_t b;
+  long long st;
+  int rows, width;
+  __device__ __forceinline__ TileStore(T* p, long long st, int rows, int width)
+      : p(p), b(rsrc(p, VEC ? static_cast<int>(rows * st) * static_cast<int>(sizeof(T)) : 0)), st(st), rows(rows), width(width) {}
+  __device__ __forceinline__ void put(int row, int col, f32x4_t v) const {
+    if constexpr (VEC) {
+      const int off = col < width ? (row * static_cast<int>(st) + col) * static_cast<int>(sizeof(T)) : kNowhere;
+      if constexpr (sizeof(T) == 2)
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, b, off, 0, 0);
+      else
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), b, off, 0, 0);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (row < rows && col + r < width) p[row * st + col + r] = Ops<T>::from_f32(v[r]);
     }
   }
 };
@@ -231,13 +271,14 @@ struct Gates {
   float first[Q];       // e^{c_i}
   float last[Q];        // e^{c_end - c_j}
   float own[Q];         // e^{g_t}
+  float in[Q];          // weights of what enters a state: e^{c_end - c_j} b_j, in reversed time e^{c_i}
   float end[4];         // e^{c_end}
 };
 
 // By one wave: lane l brings the gates of tokens l, 64 + l, ...  Returns c_end.
 template <int Q>
 __device__ __forceinline__ double write_gates(Gates<Q>& G, const float (&log_decay)[Q / 64], const float (&gate)[Q / 64],
-                                              int lane) {
+                                              int lane, bool reverse) {
   float ld[Q / 64];
   double c[Q / 64], e = 0.0;
 #pragma unroll
@@ -254,8 +295,10 @@ __device__ __forceinline__ double write_gates(Gates<Q>& G, const float (&log_dec
     G.lo[t] = static_cast<float>(c[u] - static_cast<double>(hi));
     G.b[t] = gate[u];
     G.own[t] = __builtin_amdgcn_exp2f(ld[u] * kLog2e);
-    G.first[t] = __builtin_amdgcn_exp2f(static_cast<float>(c[u]));
-    G.last[t] = __builtin_amdgcn_exp2f(static_cast<float>(e - c[u]));
+    const float first = __builtin_amdgcn_exp2f(static_cast<float>(c[u])), last = __builtin_amdgcn_exp2f(static_cast<float>(e - c[u]));
+    G.first[t] = first;
+    G.last[t] = last;
+    G.in[t] = reverse ? first : last * gate[u];
   }
   if (lane == 0) G.end[0] = __builtin_amdgcn_exp2f(static_cast<float>(e));
   return e;
@@ -265,11 +308,10 @@ __device__ __forceinline__ float between(float hi_i, float lo_i, float hi_j, flo
   return __builtin_amdgcn_exp2f((hi_i - hi_j) + (lo_i - lo_j));
 }
 
-// Tile e of the 16 x 16 tiles on and below the diagonal, row by row.
+// Tile e of the 16 x 16 tiles on and below the diagonal, row by row (at most
+// eight rows).
 __device__ __forceinline__ int tile_row(int e) {
-  int r = 0;
-  while ((r + 1) * (r + 2) / 2 <= e) ++r;
-  return r;
+  return (e >= 1) + (e >= 3) + (e >= 6) + (e >= 10) + (e >= 15) + (e >= 21) + (e >= 28);
 }
 __device__ __forceinline__ int tile_col(int e, int row) { return e - row * (row + 1) / 2; }
 
@@ -281,6 +323,13 @@ __device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
     o[i] = a[i];
     o[4 + i] = b[i];
   }
+}
+
+// Element (n, p) of a state in the workspace: in the order in which the
+// backward pass holds it, blocks of 16 n by 32 p, lane (n % 16) + 16 (p % 32 / 8)
+// with 8 neighbours p.
+__device__ __forceinline__ int state_offset(int n, int p) {
+  return (((n >> 4) * (kPB / 32) + (p >> 5)) * 64 + (n & 15) + 16 * ((p & 31) >> 3)) * 8 + (p & 7);
 }
 
 }  // namespace scan
