@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
         col += __shfl_xor(col, 32, kWave);
         if (g4 == 0) lcol[it * Q + j] = col;
         if (l16 == 0) *reinterpret_cast<f32x4_t*>(lrow + jt * Q + i0) = rs;
+        settle(dsum[t]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
               sums[u] = fmaf(a, ov[r], sums[u]);
               out[b][u0 + u][r] = gated ? fmaf(a, gt, out[b][u0 + u][r]) : out[b][u0 + u][r] + a;
             }
+            settle(out[b][u0 + u]);
           }
         }
 #pragma unroll

@@ -149,6 +149,11 @@ __device__ __forceinline__ int fresh(int v) {
   return v;
 }
 
+// Keeps the computation of an accumulator where it is written: sums that are read
+// only after a long loop are otherwise moved behind the phases that follow, and
+// everything they add is kept until there.
+__device__ __forceinline__ void settle(f32x4_t& v) { asm volatile("" : "+v"(v)); }
+
 // Buffer resources: an access at or past `bytes` reads 0 and stores nothing,
 // so ragged tiles need no branches.  kNowhere is such an offset.
 constexpr int kNowhere = 0x7ffffff0;
