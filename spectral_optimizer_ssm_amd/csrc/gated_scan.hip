@@ -100,18 +100,17 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_wal
   float gv[1] = {0.0f}, bv[1] = {0.0f};
   const auto load_gates = [&](int cc) {
     const int chunk = chunk_of(cc), rows = rows_of(chunk);
-    const long long t = static_cast<long long>(chunk) * kQ + lane;
-    gv[0] = bv[0] = 0.0f;
-    if (lane < rows) {
-      gv[0] = gp[t * gst];
-      bv[0] = bp == nullptr ? 1.0f : bp[t * bst];
-    }
+    const long long t = static_cast<long long>(chunk) * kQ + (lane < rows ? lane : rows - 1);
+    gv[0] = gp[t * gst];
+    bv[0] = bp == nullptr ? 1.0f : bp[t * bst];
+    if (lane >= rows) gv[0] = bv[0] = 0.0f;
   };
 
   TileLoad<T, NT, kQ, kWalkThreads, VEC> tk, tq;
   TileLoad<T, kPB, kQ, kWalkThreads, VEC> tx;
+  // (past the last chunk nothing is read: a branch around the prefetch would keep two copies of its registers)
   const auto load_tiles = [&](int cc) {
-    const int chunk = chunk_of(cc), rows = rows_of(chunk);
+    const int chunk = chunk_of(cc < cc1 ? cc : cc0), rows = cc < cc1 ? rows_of(chunk) : 0;
     const long long t0 = static_cast<long long>(chunk) * kQ;
     tk.load(kp + t0 * kst, kst, rows, N, tid);
     tx.load(xp + t0 * xst, xst, rows, rows_p, tid);
@@ -162,7 +161,7 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_wal
     if constexpr (READ) tq.store(lq, tid);
     __syncthreads();
     const Gates<kQ>& G = gates[cc & 1];
-    if (cc + 1 < cc1) load_tiles(cc + 1);
+    load_tiles(cc + 1);
     const int chunk = chunk_of(cc);
 
     f32x4_t y[4];   // y^T: rows p = 16 pw + 4 g4 + 0..3, column i = 16 it + l16

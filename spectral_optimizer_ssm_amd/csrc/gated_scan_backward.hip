@@ -131,12 +131,13 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     const float* gp = static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh + t0 * A.g.st;
     const float* bp = A.b.p == nullptr ? gp : static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh + t0 * A.b.st;
     const long long bst = A.b.p == nullptr ? 0 : A.b.st;
+    if (w == kTiles - 1)
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {   // by every wave, one uses them: a branch here costs more than the loads
-      const int t = 64 * u + lane, in = t < rows ? t : rows - 1;
-      gv[u] = gp[in * A.g.st];
-      bv[u] = bp[in * bst];
-    }
+      for (int u = 0; u < kU; ++u) {
+        const int t = 64 * u + lane, in = t < rows ? t : rows - 1;
+        gv[u] = gp[in * A.g.st];
+        bv[u] = bp[in * bst];
+      }
   };
   // the states as operands: row n = n0 + l16, 8 components p = 32 s + 8 g4 + 0..7 (the walk's order, state_offset)
   const int nw0 = (w % (kBlocks / kNW)) * kNW, tg = w / (kBlocks / kNW);
