@@ -27,252 +27,331 @@ using namespace scan;
 constexpr int kWalkThreads = 512;
 constexpr int kStepThreads = 256;
 
+struct WalkPair {
+  ScanWalk w[2];
+};
+
+// LDS of the walk.
 template <typename T, int NT>
 struct WalkLds {
   static constexpr int kLdN = NT + Ops<T>::kPad;
-  static constexpr int kLdP = kPB + Ops<T>::kPad;
   static constexpr int kLdM = kQ + Ops<T>::kPad;
-  static constexpr int k = 0;                                   // k [kQ][NT]
-  static constexpr int x = k + kQ * kLdN * (int)sizeof(T);      // x [kQ][kPB]
-  static constexpr int gates = x + kQ * kLdP * (int)sizeof(T);  // Gates[2]
+  static constexpr int kt = 0;                                  // k^T [NT][kQ]
+  static constexpr int xt = kt + NT * kLdM * (int)sizeof(T);    // x^T [kPB][kQ]
+  static constexpr int gates = xt + kPB * kLdM * (int)sizeof(T);   // Gates[2]
   static constexpr int states_bytes = gates + 2 * (int)sizeof(Gates<kQ>);
-  static constexpr int q = states_bytes;                        // q [kQ][NT]
+  static constexpr int k = states_bytes;                        // k [kQ][NT]
+  static constexpr int q = k + kQ * kLdN * (int)sizeof(T);      // q [kQ][NT]
   static constexpr int m = q + kQ * kLdN * (int)sizeof(T);      // weights M [i][j]
   static constexpr int y = m + kQ * kLdM * (int)sizeof(T);      // halves of y that waves hand over [8][2][64] float4
   static constexpr int read_bytes = y + 8 * 2 * 64 * 16;
 };
 
-struct WalkPair {
-  ScanWalk w[2];
-};
-
-// READ: y is computed (q is read); else only states move.
-//
-// Wave w holds rows p = 16 (w % 4) + 0..15 of S and columns n of half w / 4:
-// the tokens' products with the halves are partial sums of y, which the two
-// waves of the same rows exchange through LDS, each finishing half of the
-// tokens.  Eight waves a workgroup rather than four (160 -> ... us).
-template <typename T, int NT, bool READ, bool VEC>
-__global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_walk_kernel(WalkPair W) {
+// One sequence (segment), head and block of kPB state rows.  Wave w of eight
+// holds rows p = 16 (w % 4) + 0..15 of S and columns n of half w / 4.
+template <typename T, int NT, bool VEC>
+struct Walk {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
   typedef WalkLds<T, NT> L;
-  constexpr int kT = NT / 32;       // state tiles of a wave
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  const ScanWalk A = W.w[blockIdx.y];
-  T* lk = reinterpret_cast<T*>(lds + L::k);
-  T* lx = reinterpret_cast<T*>(lds + L::x);
-  T* lq = reinterpret_cast<T*>(lds + L::q);
-  T* lm = reinterpret_cast<T*>(lds + L::m);
-  f32x4_t* ly = reinterpret_cast<f32x4_t*>(lds + L::y);
-  Gates<kQ>* gates = reinterpret_cast<Gates<kQ>*>(lds + L::gates);
+  static constexpr int kT = NT / 32;       // state tiles of a wave
 
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g4 = lane >> 4;
-  const int pw = w & 3, nh = w >> 2, nbase = nh * (NT / 2);
-  const int vheads = A.heads * A.pblocks;
-  const int seg = static_cast<int>(blockIdx.x) % A.nseg;
-  const int vh = static_cast<int>(blockIdx.x) / A.nseg % vheads;
-  const long long bi = static_cast<int>(blockIdx.x) / A.nseg / vheads;
-  const int h = vh / A.pblocks, pb = vh - h * A.pblocks, grp = h / (A.heads / A.groups);
-  const int rows_p = A.P - pb * kPB < kPB ? A.P - pb * kPB : kPB;
-  if (A.totals && seg + 1 == A.nseg) return;   // nothing starts after the last segment
-  const long long vrow = bi * vheads + vh;
-  const bool reverse = A.reverse != 0;
-  const int cc0 = seg * A.seg_chunks;
-  const int cc1 = cc0 + A.seg_chunks < A.nchunks ? cc0 + A.seg_chunks : A.nchunks;
-
-  const int N = A.N, last_chunk = A.nchunks - 1;
-  const long long tokens = A.tokens, xst = A.x.st, kst = A.k.st, qst = A.q.st, gst = A.g.st, bst = A.b.st;
-  const T* xp = static_cast<const T*>(A.x.p) + bi * A.x.sb + h * A.x.sh + pb * kPB;
-  const T* kp = static_cast<const T*>(A.k.p) + bi * A.k.sb + grp * A.k.sh;
-  const T* qp = READ ? static_cast<const T*>(A.q.p) + bi * A.q.sb + grp * A.q.sh : nullptr;
-  const float* gp = static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh;
-  const float* bp = A.b.p == nullptr ? nullptr : static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh;
-  T* yp = READ ? static_cast<T*>(A.y) + (bi * tokens * A.heads + h) * A.P + pb * kPB : nullptr;
-  const long long yst = static_cast<long long>(A.heads) * A.P;
-
-  const auto chunk_of = [&](int cc) { return reverse ? last_chunk - cc : cc; };
-  const auto rows_of = [&](int chunk) {
-    const long long left = tokens - static_cast<long long>(chunk) * kQ;
-    return left < kQ ? static_cast<int>(left) : kQ;
-  };
-  // gates of the cc-th chunk visited, a token a lane (past the end: no decay, no input)
-  float gv[1] = {0.0f}, bv[1] = {0.0f};
-  const auto load_gates = [&](int cc) {
-    const int chunk = chunk_of(cc), rows = rows_of(chunk);
-    const long long t = static_cast<long long>(chunk) * kQ + (lane < rows ? lane : rows - 1);
-    gv[0] = gp[t * gst];
-    bv[0] = bp == nullptr ? 1.0f : bp[t * bst];
-    if (lane >= rows) gv[0] = bv[0] = 0.0f;
-  };
-
-  TileLoad<T, NT, kQ, kWalkThreads, VEC> tk, tq;
-  TileLoad<T, kPB, kQ, kWalkThreads, VEC> tx;
-  // (past the last chunk nothing is read: a branch around the prefetch would keep two copies of its registers)
-  const auto load_tiles = [&](int cc) {
-    const int chunk = chunk_of(cc < cc1 ? cc : cc0), rows = cc < cc1 ? rows_of(chunk) : 0;
-    const long long t0 = static_cast<long long>(chunk) * kQ;
-    tk.load(kp + t0 * kst, kst, rows, N, tid);
-    tx.load(xp + t0 * xst, xst, rows, rows_p, tid);
-    if constexpr (READ) tq.load(qp + t0 * qst, qst, rows, N, tid);
-  };
-
+  const ScanWalk& A;
+  int tid, lane, w, l16, g4, pw, nh, nbase;
+  int seg, h, pb, grp, rows_p, cc0, cc1, last_chunk;
+  long long bi, vrow;
+  bool reverse;
+  const float *gp, *bp;
   // the state: tile t holds S^T rows n = nbase + 16 t + 4 g4 + 0..3, column p = 16 pw + l16
   f32x4_t st[kT];
-  const int prow = pb * kPB + 16 * pw + l16, tile_off = (16 * pw + l16) * NT + nbase + 4 * g4;
-  if (A.seg_state != nullptr && !A.totals) {
-    const float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off;
-#pragma unroll
-    for (int t = 0; t < kT; ++t) st[t] = *reinterpret_cast<const f32x4_t*>(sp + 16 * t);
-  } else {
-    const bool init = A.init != nullptr && !A.totals;
-    const float* sp = A.init + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(N);
-#pragma unroll
-    for (int t = 0; t < kT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int n = nbase + 16 * t + 4 * g4 + r;
-        st[t][r] = init && prow < A.P && n < N ? sp[n] : 0.0f;
-      }
-  }
+  float gv[1], bv[1];
 
-  if constexpr (READ) {
-    // tiles (0, 1) and (2, 3) of M lie above the diagonal inside the 32-wide
-    // steps that are multiplied: zero for good
-    if (w < 2) {
-      const int r0 = 32 * w, c0 = 32 * w + 16;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) lm[(r0 + l16) * L::kLdM + c0 + 4 * g4 + e] = O::from_f32(0.0f);
-    }
+  __device__ __forceinline__ explicit Walk(const ScanWalk& A) : A(A) {
+    tid = threadIdx.x;
+    lane = tid & 63;
+    w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    l16 = lane & 15;
+    g4 = lane >> 4;
+    pw = w & 3;
+    nh = w >> 2;
+    nbase = nh * (NT / 2);
+    const int vheads = A.heads * A.pblocks;
+    // the heads that share keys are neighbours, for every segment
+    const int item = xcd_item(blockIdx.x, gridDim.x);
+    const int vh = item % vheads;
+    seg = item / vheads % A.nseg;
+    bi = item / vheads / A.nseg;
+    h = vh / A.pblocks;
+    pb = vh - h * A.pblocks;
+    grp = h / (A.heads / A.groups);
+    rows_p = A.P - pb * kPB < kPB ? A.P - pb * kPB : kPB;
+    vrow = bi * vheads + vh;
+    reverse = A.reverse != 0;
+    last_chunk = A.nchunks - 1;
+    cc0 = seg * A.seg_chunks;
+    cc1 = cc0 + A.seg_chunks < A.nchunks ? cc0 + A.seg_chunks : A.nchunks;
+    gp = static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh;
+    bp = A.b.p == nullptr ? nullptr : static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh;
+    gv[0] = bv[0] = 0.0f;
   }
-  float* states = A.states == nullptr ? nullptr : A.states + vrow * A.nblocks * (kPB * NT);
-  const int keep = A.keep;
-  double seg_log = 0.0;
-  load_tiles(cc0);
-  if (w == 7) {
-    load_gates(cc0);
-    seg_log += write_gates(gates[cc0 & 1], gv, bv, lane, reverse);
-    if (cc0 + 1 < cc1) load_gates(cc0 + 1);
+  // the cc-th chunk visited, and its tokens (none past the segment: a branch
+  // around a prefetch would keep two copies of its registers)
+  __device__ __forceinline__ int chunk_of(int cc) const { return reverse ? last_chunk - cc : cc; }
+  __device__ __forceinline__ int rows_of(int cc) const {
+    const long long left = A.tokens - static_cast<long long>(chunk_of(cc)) * kQ;
+    return cc >= cc1 ? 0 : left < kQ ? static_cast<int>(left) : kQ;
   }
-  for (int cc = cc0; cc < cc1; ++cc) {
-    __syncthreads();   // the last chunk's tiles are done with
-    tk.store(lk, tid);
-    tx.store(lx, tid);
-    if constexpr (READ) tq.store(lq, tid);
-    __syncthreads();
-    const Gates<kQ>& G = gates[cc & 1];
-    load_tiles(cc + 1);
-    const int chunk = chunk_of(cc);
+  __device__ __forceinline__ long long token_of(int cc) const { return static_cast<long long>(chunk_of(cc < cc1 ? cc : cc0)) * kQ; }
 
-    f32x4_t y[4];   // y^T: rows p = 16 pw + 4 g4 + 0..3, column i = 16 it + l16
-    if constexpr (READ) {
-      // M^T tiles: rows j, columns i, so a lane's four values are neighbours in M
+  // gates of the cc-th chunk visited, a token a lane (past the end: no decay, no input)
+  __device__ __forceinline__ void load_gates(int cc) {
+    const int rows = rows_of(cc);
+    const long long t = token_of(cc) + (lane < rows ? lane : 0);
+    gv[0] = gp[t * A.g.st];
+    bv[0] = bp == nullptr ? 1.0f : bp[t * A.b.st];
+    if (lane >= rows) gv[0] = bv[0] = 0.0f;
+  }
+  __device__ __forceinline__ int tile_off() const { return (16 * pw + l16) * NT + nbase + 4 * g4; }
+
+  __device__ __forceinline__ void load_state() {
+    const int prow = pb * kPB + 16 * pw + l16;
+    if (A.seg_state != nullptr && !A.totals) {
+      const float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int e = w + 8 * u;
-        if (e < 10) {
-          const int it = tile_row(e), jt = tile_col(e, it);
-          f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int s = 0; s < NT / 32; ++s)
-            a = O::mma(O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4),
-                       O::row(lq + (16 * it + l16) * L::kLdN + 32 * s + 8 * g4), a);
-          const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
-          const float hi = G.hi[i], lo = G.lo[i];
-          const f32x4_t jh = *reinterpret_cast<const f32x4_t*>(G.hi + j0), jl = *reinterpret_cast<const f32x4_t*>(G.lo + j0);
-          const f32x4_t jb = *reinterpret_cast<const f32x4_t*>(G.b + j0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) a[r] = j0 + r <= i ? a[r] * between(hi, lo, jh[r], jl[r]) * jb[r] : 0.0f;
-          O::store4(lm + i * L::kLdM + j0, a);
-        }
-      }
-      // what this half of S_in gives: S_in q_i
-#pragma unroll
-      for (int it = 0; it < 4; ++it) y[it] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int s = 0; s < kT / 2; ++s) {
-        const Frag f = frag_from_acc<T>(st[2 * s], st[2 * s + 1]);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const T* qr = lq + (16 * it + l16) * L::kLdN + nbase + 32 * s + 4 * g4;
-          y[it] = O::mma(f, O::row2(qr, qr + 16), y[it]);
-        }
-      }
-      // token tiles 2 nh and 2 nh + 1 stay, the others go to the other half's wave
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        ly[(w * 2 + u) * 64 + lane] = nh == 0 ? y[2 + u] : y[u];
-        y[u] = nh == 0 ? y[u] : y[2 + u];
-      }
+      for (int t = 0; t < kT; ++t) st[t] = *reinterpret_cast<const f32x4_t*>(sp + 16 * t);
     } else {
-      // the state that a block of `keep` chunks starts from (in reversed time: ends with)
-      if (states != nullptr && (reverse ? chunk % keep == keep - 1 || chunk == last_chunk : chunk % keep == 0)) {
-        float* sp = states + static_cast<long long>(chunk / keep) * (kPB * NT) + state_offset(nbase + 4 * g4, 16 * pw + l16);
+      const bool init = A.init != nullptr && !A.totals;
+      const float* sp = A.init + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
 #pragma unroll
-        for (int t = 0; t < kT; ++t)
+      for (int t = 0; t < kT; ++t)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) sp[t * (kPB / 32) * 512 + r * 8] = st[t][r];
-      }
+        for (int r = 0; r < 4; ++r) {
+          const int n = nbase + 16 * t + 4 * g4 + r;
+          st[t][r] = init && prow < A.P && n < A.N ? sp[n] : 0.0f;
+        }
     }
-    if (w == 7 && cc + 1 < cc1) {
-      seg_log += write_gates(gates[(cc + 1) & 1], gv, bv, lane, reverse);
-      if (cc + 2 < cc1) load_gates(cc + 2);
+  }
+  __device__ __forceinline__ void store_state(double seg_log) const {
+    if (A.totals) {
+      float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off();
+#pragma unroll
+      for (int t = 0; t < kT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
+      if (w == 7 && lane == 0) A.seg_decay[vrow * A.nseg + seg] = __builtin_amdgcn_exp2f(static_cast<float>(seg_log));
+    } else if (A.fin != nullptr && cc1 == A.nchunks) {
+      const int prow = pb * kPB + 16 * pw + l16;
+      float* sp = A.fin + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int n = nbase + 16 * t + 4 * g4 + r;
+          if (prow < A.P && n < A.N) sp[n] = st[t][r];
+        }
     }
-
-    // the chunk's own part of the state
+  }
+  // S = e^{c_end} S + sum_j in_j x_j k_j^T
+  __device__ __forceinline__ void update(const Gates<kQ>& G, const T* lkt, const T* lxt) {
     const float end = G.end[0];
 #pragma unroll
     for (int t = 0; t < kT; ++t) st[t] *= end;
 #pragma unroll
     for (int s = 0; s < kQ / 32; ++s) {
       float xv[8], wv[8];
-      O::widen(O::col(lx, L::kLdP, 32 * s, 16 * pw, lane), xv);
+      O::widen(transposed_row(lxt, 16 * pw + l16, 32 * s + 8 * g4), xv);
       load8(G.in + 32 * s + 8 * g4, wv);
 #pragma unroll
       for (int e = 0; e < 8; ++e) xv[e] *= wv[e];
       Frag f[O::kSplit], kf[kT];
       O::split(xv, f);
 #pragma unroll
-      for (int t = 0; t < kT; ++t) kf[t] = O::col(lk, L::kLdN, 32 * s, nbase + 16 * t, lane);
+      for (int t = 0; t < kT; ++t) kf[t] = transposed_row(lkt, nbase + 16 * t + l16, 32 * s + 8 * g4);
 #pragma unroll
       for (int u = O::kSplit - 1; u >= 0; --u)
 #pragma unroll
         for (int t = 0; t < kT; ++t) st[t] = O::mma(kf[t], f[u], st[t]);
     }
+  }
+};
 
-    if constexpr (READ) {
-      __syncthreads();   // M and the halves of y are written
+// States only: the state before every block of `keep` chunks (in reversed time:
+// after it), a segment's total, or both.
+template <typename T, int NT, bool VEC>
+__global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_states_kernel(WalkPair P) {
+  typedef WalkLds<T, NT> L;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const ScanWalk A = P.w[blockIdx.y];
+  Walk<T, NT, VEC> W(A);
+  if (A.totals && W.seg + 1 == A.nseg) return;   // nothing starts after the last segment
+  T* lkt = reinterpret_cast<T*>(lds + L::kt);
+  T* lxt = reinterpret_cast<T*>(lds + L::xt);
+  Gates<kQ>* gates = reinterpret_cast<Gates<kQ>*>(lds + L::gates);
+  const T* xp = static_cast<const T*>(A.x.p) + W.bi * A.x.sb + W.h * A.x.sh + W.pb * kPB;
+  const T* kp = static_cast<const T*>(A.k.p) + W.bi * A.k.sb + W.grp * A.k.sh;
+  PairLoad<T, NT, kWalkThreads, VEC> tk;
+  PairLoad<T, kPB, kWalkThreads, VEC> tx;
+  const auto load_tiles = [&](int cc) {
+    const int rows = W.rows_of(cc);
+    const long long t0 = W.token_of(cc);
+    tk.load(kp + t0 * A.k.st, A.k.st, rows, A.N, W.tid);
+    tx.load(xp + t0 * A.x.st, A.x.st, rows, W.rows_p, W.tid);
+  };
+  W.load_state();
+  float* states = A.states == nullptr ? nullptr : A.states + W.vrow * A.nblocks * (kPB * NT);
+  double seg_log = 0.0;
+  load_tiles(W.cc0);
+  if (W.w == 7) {
+    W.load_gates(W.cc0);
+    seg_log += write_gates(gates[0], W.gv, W.bv, W.lane, W.reverse);
+    W.load_gates(W.cc0 + 1);
+  }
+  for (int cc = W.cc0; cc < W.cc1; ++cc) {
+    const int slot = (cc - W.cc0) & 1;
+    __syncthreads();   // the last chunk's tiles are done with
+    tk.store_transposed(lkt, W.tid);
+    tx.store_transposed(lxt, W.tid);
+    __syncthreads();
+    load_tiles(cc + 1);
+    const int chunk = W.chunk_of(cc);
+    if (states != nullptr &&
+        (W.reverse ? chunk % A.keep == A.keep - 1 || chunk == W.last_chunk : chunk % A.keep == 0)) {
+      float* sp = states + static_cast<long long>(chunk / A.keep) * (kPB * NT) + state_offset(W.nbase + 4 * W.g4, 16 * W.pw + W.l16);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) y[u] = (y[u] + ly[((w ^ 4) * 2 + u) * 64 + lane]) * G.first[32 * nh + 16 * u + l16];
+      for (int t = 0; t < W.kT; ++t)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (s <= nh) {
-          const Frag vf = O::col(lx, L::kLdP, 32 * s, 16 * pw, lane);
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-            y[u] = O::mma(vf, O::row(lm + (32 * nh + 16 * u + l16) * L::kLdM + 32 * s + 8 * g4), y[u]);
-        }
-      const TileStore<T, VEC> out(yp + static_cast<long long>(chunk) * kQ * yst, yst, rows_of(chunk), rows_p);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) out.put(32 * nh + 16 * u + l16, 16 * pw + 4 * g4, y[u]);
+        for (int r = 0; r < 4; ++r) sp[t * (kPB / 32) * 512 + r * 8] = W.st[t][r];
     }
+    if (W.w == 7) {
+      const double e = write_gates(gates[slot ^ 1], W.gv, W.bv, W.lane, W.reverse);   // past the end: 0
+      seg_log += e;
+      W.load_gates(cc + 2);
+    }
+    W.update(gates[slot], lkt, lxt);
   }
+  W.store_state(seg_log);
+}
 
-  if (A.totals) {
-    float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off;
+// Outputs and states.  The tokens' products with the two halves of n are
+// partial sums of y, which the two waves of the same rows exchange through LDS,
+// each finishing half of the tokens.
+template <typename T, int NT, bool VEC>
+__global__ void __launch_bounds__(kWalkThreads, 2) scan_read_kernel(WalkPair P) {
+  typedef Ops<T> O;
+  typedef typename O::Frag Frag;
+  typedef WalkLds<T, NT> L;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const ScanWalk A = P.w[0];
+  Walk<T, NT, VEC> W(A);
+  const int tid = W.tid, lane = W.lane, w = W.w, l16 = W.l16, g4 = W.g4, pw = W.pw, nh = W.nh, nbase = W.nbase;
+  T* lkt = reinterpret_cast<T*>(lds + L::kt);
+  T* lxt = reinterpret_cast<T*>(lds + L::xt);
+  T* lk = reinterpret_cast<T*>(lds + L::k);
+  T* lq = reinterpret_cast<T*>(lds + L::q);
+  T* lm = reinterpret_cast<T*>(lds + L::m);
+  f32x4_t* ly = reinterpret_cast<f32x4_t*>(lds + L::y);
+  Gates<kQ>* gates = reinterpret_cast<Gates<kQ>*>(lds + L::gates);
+  const T* xp = static_cast<const T*>(A.x.p) + W.bi * A.x.sb + W.h * A.x.sh + W.pb * kPB;
+  const T* kp = static_cast<const T*>(A.k.p) + W.bi * A.k.sb + W.grp * A.k.sh;
+  const T* qp = static_cast<const T*>(A.q.p) + W.bi * A.q.sb + W.grp * A.q.sh;
+  T* yp = static_cast<T*>(A.y) + (W.bi * A.tokens * A.heads + W.h) * A.P + W.pb * kPB;
+  const long long yst = static_cast<long long>(A.heads) * A.P;
+
+  PairLoad<T, NT, kWalkThreads, VEC> tk;
+  PairLoad<T, kPB, kWalkThreads, VEC> tx;
+  TileLoad<T, NT, kQ, kWalkThreads, VEC> tq;
+  const auto load_tiles = [&](int cc) {
+    const int rows = W.rows_of(cc);
+    const long long t0 = W.token_of(cc);
+    tk.load(kp + t0 * A.k.st, A.k.st, rows, A.N, tid);
+    tq.load(qp + t0 * A.q.st, A.q.st, rows, A.N, tid);
+    tx.load(xp + t0 * A.x.st, A.x.st, rows, W.rows_p, tid);
+  };
+
+  W.load_state();
+  // tiles (0, 1) and (2, 3) of M lie above the diagonal inside the 32-wide
+  // steps that are multiplied: zero for good
+  if (w < 2) {
+    const int r0 = 32 * w, c0 = r0 + 16;
 #pragma unroll
-    for (int t = 0; t < kT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
-    if (w == 7 && lane == 0) A.seg_decay[vrow * A.nseg + seg] = __builtin_amdgcn_exp2f(static_cast<float>(seg_log));
-  } else if (A.fin != nullptr && cc1 == A.nchunks) {
-    float* sp = A.fin + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(N);
-#pragma unroll
-    for (int t = 0; t < kT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int n = nbase + 16 * t + 4 * g4 + r;
-        if (prow < A.P && n < N) sp[n] = st[t][r];
-      }
+    for (int e = 0; e < 4; ++e) lm[(r0 + l16) * L::kLdM + c0 + 4 * g4 + e] = O::from_f32(0.0f);
   }
+  load_tiles(W.cc0);
+  if (w == 7) {
+    W.load_gates(W.cc0);
+    write_gates(gates[0], W.gv, W.bv, lane, false);
+    W.load_gates(W.cc0 + 1);
+  }
+  for (int cc = W.cc0; cc < W.cc1; ++cc) {
+    const int slot = (cc - W.cc0) & 1;
+    const Gates<kQ>& G = gates[slot];
+    __syncthreads();   // the last chunk's tiles are done with
+    tk.store(lk, tid);
+    tk.store_transposed(lkt, tid);
+    tq.store(lq, tid);
+    tx.store_transposed(lxt, tid);
+    __syncthreads();
+    load_tiles(cc + 1);
+    // M^T tiles: rows j, columns i, so a lane's four values are neighbours in M.  Ten tiles for seven waves: the
+    // last one has the next chunk's gates to prepare.
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int e = w + 7 * u;
+      if (w < 7 && e < 10) {
+        const int it = tile_row(e), jt = tile_col(e, it);
+        f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < NT / 32; ++s)
+          a = O::mma(O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4), O::row(lq + (16 * it + l16) * L::kLdN + 32 * s + 8 * g4), a);
+        const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
+        const float hi = G.hi[i], lo = G.lo[i];
+        const f32x4_t jh = *reinterpret_cast<const f32x4_t*>(G.hi + j0), jl = *reinterpret_cast<const f32x4_t*>(G.lo + j0);
+        const f32x4_t jb = *reinterpret_cast<const f32x4_t*>(G.b + j0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) a[r] = j0 + r <= i ? a[r] * between(hi, lo, jh[r], jl[r]) * jb[r] : 0.0f;
+        O::store4(lm + i * L::kLdM + j0, a);
+      }
+    }
+    if (w == 7) {
+      write_gates(gates[slot ^ 1], W.gv, W.bv, lane, false);
+      W.load_gates(cc + 2);
+    }
+    // what this half of S_in gives, e^{c_i} S_in q_i: y^T rows p = 16 pw + 4 g4 + 0..3, column i = 16 it + l16
+    f32x4_t y[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) y[it] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < W.kT / 2; ++s) {
+      const Frag f = frag_from_acc<T>(W.st[2 * s], W.st[2 * s + 1]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const T* qr = lq + (16 * it + l16) * L::kLdN + nbase + 32 * s + 4 * g4;
+        y[it] = O::mma(f, O::row2(qr, qr + 16), y[it]);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) y[it] *= G.first[16 * it + l16];
+    // token tiles 2 nh and 2 nh + 1 stay, the others go to the other half's wave
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      ly[(w * 2 + u) * 64 + lane] = nh == 0 ? y[2 + u] : y[u];
+      y[u] = nh == 0 ? y[u] : y[2 + u];
+    }
+    W.update(G, lkt, lxt);
+    __syncthreads();   // M and the halves of y are written
+    // what the chunk's own tokens give
+#pragma unroll
+    for (int u = 0; u < 2; ++u) y[u] += ly[((w ^ 4) * 2 + u) * 64 + lane];
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (s <= nh) {
+        const Frag vf = transposed_row(lxt, 16 * pw + l16, 32 * s + 8 * g4);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) y[u] = O::mma(vf, O::row(lm + (32 * nh + 16 * u + l16) * L::kLdM + 32 * s + 8 * g4), y[u]);
+      }
+    const TileStore<T, VEC> out(yp + W.token_of(cc) * yst, yst, W.rows_of(cc), W.rows_p);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) out.put(32 * nh + 16 * u + l16, 16 * pw + 4 * g4, y[u]);
+  }
+  W.store_state(0.0);
 }
 
 // The state that each segment starts from, out of the segments' own totals
@@ -301,12 +380,12 @@ template <typename T, int NT, bool READ, bool VEC>
 hipError_t walk(const WalkPair& W, int dirs, hipStream_t st) {
   const ScanWalk& a = W.w[0];
   constexpr int bytes = READ ? WalkLds<T, NT>::read_bytes : WalkLds<T, NT>::states_bytes;
-  const void* fn = reinterpret_cast<const void*>(scan_walk_kernel<T, NT, READ, VEC>);
-  const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
+  const auto kernel = READ ? scan_read_kernel<T, NT, VEC> : scan_states_kernel<T, NT, VEC>;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
   const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg;
-  hipLaunchKernelGGL((scan_walk_kernel<T, NT, READ, VEC>), dim3(static_cast<unsigned>(items), dirs), dim3(kWalkThreads), bytes, st,
-                     W);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items), dirs), dim3(kWalkThreads), bytes, st, W);
   return hipGetLastError();
 }
 

@@ -59,18 +59,21 @@ int check_operands(const muon_scan_args* a) {
   return MUON_OK;
 }
 
-// Workgroups that fill the chip: two on each of 256 compute units for the walk,
-// one for the backward pass (its tiles fill the LDS).
-constexpr long long kFill = 512, kGradFill = 256;
+// Workgroups that fill 256 compute units: one of the forward walk or of the
+// backward pass on each (their tiles fill the LDS), two of the states' walk.
+constexpr long long kReadFill = 256, kStatesFill = 512, kGradFill = 256;
 
 struct ScanPlan {
   int pblocks, nchunks, nblocks, nseg, seg_chunks, nsplit;   // nblocks: of the backward pass
   size_t states, dstates, seg, seg2, decay, decay2, parts, end;   // workspace offsets
 };
 // The walk of one sequence is serial, so with few sequences and heads the time
-// axis is cut into segments (their totals first, then all of them at once):
-// worth its second reading of the inputs only where segments of at least
-// kSegChunks chunks fill idle compute units.
+// axis is cut into segments: their totals first, then all of them at once.
+// Each token is walked over twice, so segments have to fill otherwise idle
+// compute units.  Forward, the second walk is the longer one, and two segments
+// already win (24 heads of 16,384 tokens: 490 us in one, 137 in twenty); for
+// the backward pass both are the same walk, and it takes three.  A segment has
+// at least kSegChunks chunks.
 constexpr int kSegChunks = 4;
 
 int grad_tokens(int dtype) { return dtype == MUON_BF16 ? kScanGradBf16 : kScanGradF32; }
@@ -88,8 +91,8 @@ int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
     p->end = kAlign;
     return MUON_OK;
   }
-  long long nseg = std::min<long long>(kFill / walks, p->nchunks / kSegChunks);
-  if (nseg < 1) nseg = 1;
+  long long nseg = std::min<long long>((backward ? kStatesFill : kReadFill) / walks, p->nchunks / kSegChunks);
+  if (nseg < (backward ? 3 : 2)) nseg = 1;
   p->seg_chunks = static_cast<int>((p->nchunks + nseg - 1) / nseg);
   p->nseg = (p->nchunks + p->seg_chunks - 1) / p->seg_chunks;
   const long long groups = static_cast<long long>(a->batch) * p->nblocks * a->groups;

@@ -154,6 +154,13 @@ __device__ __forceinline__ int fresh(int v) {
 // everything they add is kept until there.
 __device__ __forceinline__ void settle(f32x4_t& v) { asm volatile("" : "+v"(v)); }
 
+// Workgroups go to the eight XCDs in turn; this gives each XCD a run of
+// neighbouring items instead, whose shared operands its L2 then holds once.
+__device__ __forceinline__ int xcd_item(int block, int items) {
+  const int x = block & 7, i = block >> 3, each = items >> 3, more = items & 7;
+  return x * each + (x < more ? x : more) + i;
+}
+
 // Buffer resources: an access at or past `bytes` reads 0 and stores nothing,
 // so ragged tiles need no branches.  kNowhere is such an offset.
 constexpr int kNowhere = 0x7ffffff0;
@@ -215,6 +222,85 @@ struct TileLoad {
     }
   }
 };
+
+// A [kQ][WIDTH] tile that is (also) needed transposed: a thread holds the same
+// 16-byte columns of two neighbouring tokens, so that it writes both tokens of
+// a transposed row at once.  The transposed tile [WIDTH][kQ] keeps row n's
+// 16-byte pieces in the order piece ^ (n / kVec % 8): the threads of a wave
+// write 16 rows that lie 8 apart, which would otherwise be one bank.
+template <typename T, int WIDTH, int THREADS, bool VEC>
+struct PairLoad {
+  static constexpr int kVec = Ops<T>::kVec;
+  static constexpr int kRowPieces = WIDTH / kVec;
+  static constexpr int kAll = kQ / 2 * kRowPieces;
+  static constexpr int kPairs = (kAll + THREADS - 1) / THREADS;
+  static constexpr int kLd = WIDTH + Ops<T>::kPad;
+  static constexpr int kLdT = kQ + Ops<T>::kPad;
+  u32x4_t r[kPairs][2];
+
+  __device__ __forceinline__ void load(const T* p, long long st, int rows, int width, int tid) {
+    const __amdgpu_buffer_rsrc_t b = rsrc(p, VEC ? static_cast<int>(rows * st) * static_cast<int>(sizeof(T)) : 0);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int idx = i * THREADS + tid, col = (idx % kRowPieces) * kVec;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int row = 2 * (idx / kRowPieces) + u;   // past the tile's rows: past `rows` too
+        if constexpr (VEC) {
+          const int off = (row * static_cast<int>(st) + col) * static_cast<int>(sizeof(T));
+          r[i][u] = __builtin_amdgcn_raw_buffer_load_b128(b, col < width && idx < kAll ? off : kNowhere, 0, 0);
+        } else {
+          const T* e = p + row * st + col;
+          r[i][u] = u32x4_t{0u, 0u, 0u, 0u};
+          if (row >= rows) continue;
+#pragma unroll
+          for (int j = 0; j < kVec; ++j)
+            if (col + j < width) {
+              if constexpr (sizeof(T) == 2) r[i][u][j / 2] |= static_cast<uint32_t>(e[j]) << (16 * (j & 1));
+              else r[i][u][j] = __float_as_uint(e[j]);
+            }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int idx = i * THREADS + tid, col = (idx % kRowPieces) * kVec;
+      if (kAll % THREADS != 0 && idx >= kAll) return;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) *reinterpret_cast<u32x4_t*>(lds + (2 * (idx / kRowPieces) + u) * kLd + col) = r[i][u];
+    }
+  }
+  __device__ __forceinline__ void store_transposed(T* lds, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int idx = i * THREADS + tid, piece = idx % kRowPieces, j = 2 * (idx / kRowPieces);
+      if (kAll % THREADS != 0 && idx >= kAll) return;
+      T* p = lds + piece * kVec * kLdT + ((j / kVec) ^ (piece & 7)) * kVec + j % kVec;
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t a = r[i][0][e], b = r[i][1][e];
+          *reinterpret_cast<uint32_t*>(p + (2 * e) * kLdT) = (a & 0xffffu) | (b << 16);
+          *reinterpret_cast<uint32_t*>(p + (2 * e + 1) * kLdT) = (a >> 16) | (b & 0xffff0000u);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<u32x2_t*>(p + e * kLdT) = u32x2_t{r[i][0][e], r[i][1][e]};
+      }
+    }
+  }
+};
+// Row n, tokens j0..j0 + 7 (j0 a multiple of 8) of a transposed tile.
+template <typename T>
+__device__ __forceinline__ typename Ops<T>::Frag transposed_row(const T* tile, int n, int j0) {
+  constexpr int kVec = Ops<T>::kVec, kLdT = kQ + Ops<T>::kPad;
+  const T* row = tile + n * kLdT;
+  const int x = (n / kVec) & 7, c = j0 / kVec;
+  if constexpr (sizeof(T) == 2) return Ops<T>::row(row + (c ^ x) * kVec);
+  else return Ops<T>::row2(row + (c ^ x) * kVec, row + ((c + 1) ^ x) * kVec);
+}
 
 // Four neighbours of an output row (columns col..col + 3 of `width`) at element
 // offset `off` of a tile of rows at p; rows < `rows` are written.
