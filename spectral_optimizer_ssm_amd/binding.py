@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -46,16 +47,6 @@ class GroupC(ctypes.Structure):
                 ("nesterov", ctypes.c_int),
                 ("cap_u", ctypes.POINTER(ctypes.c_void_p)), ("cap_v", ctypes.POINTER(ctypes.c_void_p)),
                 ("cap_sigma", ctypes.c_void_p), ("cap", ctypes.c_float)]
-
-
-class SeqC(ctypes.Structure):
-    _fields_ = [("p", ctypes.c_void_p), ("sb", ctypes.c_longlong), ("st", ctypes.c_longlong), ("sh", ctypes.c_longlong)]
-
-
-class ScanArgs(ctypes.Structure):
-    _fields_ = [("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("heads", ctypes.c_int), ("groups", ctypes.c_int),
-                ("P", ctypes.c_int), ("N", ctypes.c_int), ("dtype", ctypes.c_int), ("v", SeqC), ("k", SeqC), ("q", SeqC),
-                ("log_decay", SeqC), ("gate", SeqC), ("S0", ctypes.c_void_p)]
 
 
 EXPORTS = ("muon_step_workspace_size", "muon_step", "muon_step_phases", "muon_step_timed", "muon_ns_workspace_size",
@@ -123,14 +114,14 @@ def lib():
     L.muon_spectral_diag_timed.argtypes = [vp, i, i, i, ctypes.c_longlong, i, vp, vp, vp, vp, sz, vp,
                                            ctypes.POINTER(ctypes.c_void_p), i]
     L.muon_spectral_diag_timed.restype = i
-    ll, sa = ctypes.c_longlong, ctypes.POINTER(ScanArgs)
+    ll, sa = ctypes.c_longlong, ctypes.c_char_p   # packed muon_scan_args, muon_seq
     L.muon_gated_scan_workspace_size.argtypes = [sa]
     L.muon_gated_scan_workspace_size.restype = sz
     L.muon_gated_scan.argtypes = [sa, vp, vp, vp, sz, vp]
     L.muon_gated_scan.restype = i
     L.muon_gated_scan_backward_workspace_size.argtypes = [sa]
     L.muon_gated_scan_backward_workspace_size.restype = sz
-    L.muon_gated_scan_backward.argtypes = [sa, ctypes.POINTER(SeqC), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.muon_gated_scan_backward.argtypes = [sa, sa, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.muon_gated_scan_backward.restype = i
     L.muon_gated_scan_step.argtypes = [sa, vp, vp, vp]
     L.muon_gated_scan_step.restype = i
@@ -647,53 +638,119 @@ def muon_spectral_diag(A, iters=32, orth_err=True, sigma_max=True, sigma_min=Tru
 
 
 # ----------------------------------------------------------------------------
-# sequence operators
+# sequence operators.  Their smallest calls take a few microseconds on the GPU,
+# so the marshalling here counts: argument records are packed in one step, the
+# checks read each property of a tensor once.
 # ----------------------------------------------------------------------------
-def _seq(t) -> SeqC:
-    """A [batch, tokens, heads, width] (or, for gates, [batch, tokens, heads])
-    tensor as a muon_seq (the stride of a dimension of one is never used)."""
-    sb, st, sh = (int(t.stride(d)) if t.shape[d] > 1 else 0 for d in range(3))
-    return SeqC(t.data_ptr(), sb, st, sh)
+_SCAN_ARGS = struct.Struct("@7i4x" + 5 * "Pqqq" + "P")     # muon_scan_args
+_SEQ = struct.Struct("@Pqqq")                              # muon_seq
+_NO_SEQ = (0, 0, 0, 0)
 
 
-def _scan_args(V, K, Q, log_decay, gate, S0, device):
-    """The muon_scan_args of a call, checked."""
+def _device_index() -> int:
     import torch
-    if V.dim() != 4 or K.dim() != 4 or K.shape != Q.shape or V.shape[:2] != K.shape[:2]:
-        raise ValueError("V must be [batch, tokens, heads, P]; K and Q [batch, tokens, groups, N]")
-    b, t, h, p = (int(x) for x in V.shape)
-    g, n = int(K.shape[2]), int(K.shape[3])
-    if h == 0 or g == 0 or h % g != 0:
-        raise ValueError(f"the groups ({g}) must divide the heads ({h})")
-    for name, x in (("V", V), ("K", K), ("Q", Q)):
-        if x.numel() > 0 and x.shape[3] > 1 and x.stride(3) != 1:
-            raise ValueError(f"{name} must have adjacent elements in its last dimension")
-    for name, x in (("log_decay", log_decay), ("gate", gate)):
-        if x is not None and tuple(x.shape) != (b, t, h):
-            raise ValueError(f"{name} must be a [{b}, {t}, {h}] float32 tensor")
-    _check_tensors([V, K, Q], "V, K and Q", (torch.bfloat16, torch.float32), device)
-    _check_tensors([x for x in (log_decay, gate) if x is not None], "log_decay and gate", (torch.float32,), device)
-    if S0 is not None:
-        _check_state(S0, "S0", (b, h, p, n), device)
-    return ScanArgs(b, t, h, g, p, n, _dtype_code(V), _seq(V), _seq(K), _seq(Q), _seq(log_decay),
-                    SeqC() if gate is None else _seq(gate), None if S0 is None else S0.data_ptr())
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
 
 
-def _check_state(S, name, shape, device):
+def _raw_stream(stream, index) -> Optional[int]:
+    """The caller's stream (or torch's current one) as a hipStream_t."""
     import torch
-    if not S.is_contiguous() or tuple(S.shape) != shape:
+    if stream is not None:
+        return int(stream.cuda_stream) or None
+    return torch._C._cuda_getCurrentRawStream(index) or None
+
+
+def _where(t, name, index):
+    """t lives on the current GPU."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
+
+
+def _type_code(t, name) -> int:
+    import torch
+    if t.dtype is torch.bfloat16:
+        return MUON_BF16
+    if t.dtype is torch.float32:
+        return MUON_F32
+    raise TypeError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+
+
+def _same_type(t, ref, name):
+    if t.dtype is not ref.dtype:
+        raise TypeError(f"{name} must be {ref.dtype} (got {t.dtype})")
+
+
+def _f32_on(t, name, index):
+    import torch
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be float32 (got {t.dtype})")
+    _where(t, name, index)
+
+
+def _seq(t, shape, name, token=True):
+    """(pointer, strides of batch, tokens and heads) of a tensor [batch,
+    tokens, heads, ...] (token False: [batch, heads, ...]) whose last dimension,
+    if it has one beyond the heads, is adjacent.  The stride of a dimension of
+    one is never used."""
+    st = t.stride()
+    k = 3 if token else 2
+    if len(st) > k and st[k] != 1 and shape[k] > 1 and t.numel() > 0:
+        raise ValueError(f"{name} must have adjacent elements in its last dimension")
+    if token:
+        return t.data_ptr(), st[0] if shape[0] > 1 else 0, st[1] if shape[1] > 1 else 0, st[2] if shape[2] > 1 else 0
+    return t.data_ptr(), st[0] if shape[0] > 1 else 0, 0, st[1] if shape[1] > 1 else 0
+
+
+def _check_state(S, name, shape, index):
+    if tuple(S.shape) != shape or not S.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{', '.join(map(str, shape))}] float32 tensor")
-    _check_tensors([S], name, (torch.float32,), device)
+    _f32_on(S, name, index)
 
 
-def _out(t, name, shape, dtype, device):
+def _scan_call(V, K, Q, log_decay, gate, S0, index, token=True):
+    """(packed muon_scan_args, (batch, tokens, heads, groups, P, N)) of a call, checked."""
+    vs, ks = V.shape, K.shape
+    want = 4 if token else 3
+    if len(vs) != want or len(ks) != want or Q.shape != ks or vs[:want - 2] != ks[:want - 2]:
+        raise ValueError("V must be [batch, tokens, heads, P]; K and Q [batch, tokens, groups, N]" if token else
+                         "V must be [batch, heads, P]; K and Q [batch, groups, N]")
+    b, t = vs[0], vs[1] if token else 1
+    h, p, g, n = vs[-2], vs[-1], ks[-2], ks[-1]
+    if g == 0 or h == 0 or h % g != 0:
+        raise ValueError(f"the groups ({g}) must divide the heads ({h})")
+    code = _type_code(V, "V")
+    _same_type(K, V, "K")
+    _same_type(Q, V, "Q")
+    _where(V, "V", index)
+    _where(K, "K", index)
+    _where(Q, "Q", index)
+    gs = vs[:-1]
+    if log_decay.shape != gs:
+        raise ValueError(f"log_decay must be a [{', '.join(map(str, gs))}] float32 tensor")
+    _f32_on(log_decay, "log_decay", index)
+    if gate is not None:
+        if gate.shape != gs:
+            raise ValueError(f"gate must be a [{', '.join(map(str, gs))}] float32 tensor")
+        _f32_on(gate, "gate", index)
+    if S0 is not None:
+        _check_state(S0, "S0", (b, h, p, n), index)
+    packed = _SCAN_ARGS.pack(b, t, h, g, p, n, code, *_seq(V, vs, "V", token), *_seq(K, ks, "K", token),
+                             *_seq(Q, ks, "Q", token), *_seq(log_decay, gs, "log_decay", token),
+                             *(_NO_SEQ if gate is None else _seq(gate, gs, "gate", token)),
+                             0 if S0 is None else S0.data_ptr())
+    return packed, (b, t, h, g, p, n)
+
+
+def _out(t, name, shape, dtype, index):
     """The caller's output tensor when given (checked), else a new one."""
     import torch
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        return torch.empty(shape, dtype=dtype, device=index)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{', '.join(map(str, shape))}] tensor")
-    _check_tensors([t], name, (dtype,), device)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    _where(t, name, index)
     return t
 
 
@@ -704,10 +761,26 @@ def _ptr(t):
 def _used_on(stream, *tensors):
     """Tensors made on torch's current stream for a call on another one: their
     memory is not given out again before that stream is past the call."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+def _new_workspace(workspace, need, index):
+    import torch
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=index)
+    return _workspace(workspace, need, torch.device("cuda", index))
+
+
+def muon_gated_scan_workspace_size(V, K, backward=False) -> int:
+    """Workspace bytes of muon_gated_scan (backward: of
+    muon_gated_scan_backward) for V and K of these shapes and dtype."""
+    b, t, h, p = V.shape
+    args = _SCAN_ARGS.pack(b, t, h, K.shape[2], p, K.shape[3], _type_code(V, "V"), *(5 * _NO_SEQ), 0)
+    L = lib()
+    fn = L.muon_gated_scan_backward_workspace_size if backward else L.muon_gated_scan_workspace_size
+    return int(fn(args))
 
 
 def muon_gated_scan(V, K, Q, log_decay, gate=None, S0=None, Y=None, S_out=None, workspace=None, stream=None):
@@ -722,28 +795,19 @@ def muon_gated_scan(V, K, Q, log_decay, gate=None, S0=None, Y=None, S_out=None, 
     muon_gated_scan_workspace_size bytes to use instead of a new one."""
     import torch
     L = lib()
-    dev = _current_device()
-    a = _scan_args(V, K, Q, log_decay, gate, S0, dev)
-    need = int(L.muon_gated_scan_workspace_size(ctypes.byref(a)))
+    dev = _device_index()
+    args, (b, t, h, g, p, n) = _scan_call(V, K, Q, log_decay, gate, S0, dev)
+    need = L.muon_gated_scan_workspace_size(args)
     if need == 0:
         raise MuonError(MUON_EUNSUPPORTED, "muon_gated_scan_workspace_size")
-    Y = _out(Y, "Y", (a.batch, a.tokens, a.heads, a.P), V.dtype, dev)
-    S_out = _out(S_out, "S_out", (a.batch, a.heads, a.P, a.N), torch.float32, dev)
-    ws = _workspace(workspace, need, dev)
-    _check(L.muon_gated_scan(ctypes.byref(a), _ptr(Y), _ptr(S_out), ws.data_ptr(), ws.numel(), _stream_handle(stream)),
-           "muon_gated_scan")
-    _used_on(stream, Y, S_out, ws)
+    Y = _out(Y, "Y", (b, t, h, p), V.dtype, dev)
+    S_out = _out(S_out, "S_out", (b, h, p, n), torch.float32, dev)
+    ws = _new_workspace(workspace, need, dev)
+    rc = L.muon_gated_scan(args, _ptr(Y), _ptr(S_out), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    _check(rc, "muon_gated_scan")
+    if stream is not None:
+        _used_on(stream, Y, S_out, ws)
     return Y, S_out
-
-
-def muon_gated_scan_workspace_size(V, K, backward=False) -> int:
-    """Workspace bytes of muon_gated_scan (backward: of
-    muon_gated_scan_backward) for V and K of these shapes and dtype."""
-    b, t, h, p = (int(x) for x in V.shape)
-    a = ScanArgs(b, t, h, int(K.shape[2]), p, int(K.shape[3]), _dtype_code(V))
-    L = lib()
-    fn = L.muon_gated_scan_backward_workspace_size if backward else L.muon_gated_scan_workspace_size
-    return int(fn(ctypes.byref(a)))
 
 
 def muon_gated_scan_backward(V, K, Q, log_decay, dY, gate=None, S0=None, dS=None, dV=None, dK=None, dQ=None,
@@ -755,31 +819,33 @@ def muon_gated_scan_backward(V, K, Q, log_decay, dY, gate=None, S0=None, dS=None
     gate, dS0 without S0."""
     import torch
     L = lib()
-    dev = _current_device()
-    a = _scan_args(V, K, Q, log_decay, gate, S0, dev)
-    state = (a.batch, a.heads, a.P, a.N)
-    if tuple(dY.shape) != tuple(V.shape) or (dY.numel() > 0 and dY.shape[3] > 1 and dY.stride(3) != 1):
-        raise ValueError("dY must have V's shape and adjacent elements in its last dimension")
-    _check_tensors([dY], "dY", (V.dtype,), dev)
+    dev = _device_index()
+    args, (b, t, h, g, p, n) = _scan_call(V, K, Q, log_decay, gate, S0, dev)
+    state, keys, gates = (b, h, p, n), (b, t, g, n), (b, t, h)
+    if dY.shape != V.shape:
+        raise ValueError("dY must have V's shape")
+    _same_type(dY, V, "dY")
+    _where(dY, "dY", dev)
     if dS is not None:
         _check_state(dS, "dS", state, dev)
-    need = int(L.muon_gated_scan_backward_workspace_size(ctypes.byref(a)))
+    need = L.muon_gated_scan_backward_workspace_size(args)
     if need == 0:
         raise MuonError(MUON_EUNSUPPORTED, "muon_gated_scan_backward_workspace_size")
-    dV = _out(dV, "dV", tuple(V.shape), V.dtype, dev)
-    dK = _out(dK, "dK", tuple(K.shape), V.dtype, dev)
-    dQ = _out(dQ, "dQ", tuple(K.shape), V.dtype, dev)
-    dlog_decay = _out(dlog_decay, "dlog_decay", tuple(V.shape[:3]), torch.float32, dev)
+    dV = _out(dV, "dV", (b, t, h, p), V.dtype, dev)
+    dK = _out(dK, "dK", keys, V.dtype, dev)
+    dQ = _out(dQ, "dQ", keys, V.dtype, dev)
+    dlog_decay = _out(dlog_decay, "dlog_decay", gates, torch.float32, dev)
     if dgate is not None or gate is not None:
-        dgate = _out(dgate, "dgate", tuple(V.shape[:3]), torch.float32, dev)
+        dgate = _out(dgate, "dgate", gates, torch.float32, dev)
     if dS0 is not None or S0 is not None:
         dS0 = _out(dS0, "dS0", state, torch.float32, dev)
-    ws = _workspace(workspace, need, dev)
-    dy = _seq(dY)
-    _check(L.muon_gated_scan_backward(ctypes.byref(a), ctypes.byref(dy), _ptr(dS), _ptr(dV), _ptr(dK), _ptr(dQ),
-                                      _ptr(dlog_decay), _ptr(dgate), _ptr(dS0), ws.data_ptr(), ws.numel(),
-                                      _stream_handle(stream)), "muon_gated_scan_backward")
-    _used_on(stream, dV, dK, dQ, dlog_decay, dgate, dS0, ws)
+    ws = _new_workspace(workspace, need, dev)
+    rc = L.muon_gated_scan_backward(args, _SEQ.pack(*_seq(dY, dY.shape, "dY")), _ptr(dS), _ptr(dV), _ptr(dK), _ptr(dQ),
+                                    _ptr(dlog_decay), _ptr(dgate), _ptr(dS0), ws.data_ptr(), ws.numel(),
+                                    _raw_stream(stream, dev))
+    _check(rc, "muon_gated_scan_backward")
+    if stream is not None:
+        _used_on(stream, dV, dK, dQ, dlog_decay, dgate, dS0, ws)
     return dV, dK, dQ, dlog_decay, dgate, dS0
 
 
@@ -788,49 +854,51 @@ def muon_gated_scan_step(V, K, Q, log_decay, S, gate=None, Y=None, S_out=None, s
     [batch, groups, N], log_decay and gate [batch, heads], S [batch, heads, P,
     N] float32, updated in place unless S_out is given.  Returns (Y, S_out or
     S)."""
-    L = lib()
-    dev = _current_device()
-    if V.dim() != 3 or K.dim() != 3 or Q.dim() != 3:
-        raise ValueError("V must be [batch, heads, P]; K and Q [batch, groups, N]")
-    one = lambda x: None if x is None else x.unsqueeze(1)  # noqa: E731
-    a = _scan_args(one(V), one(K), one(Q), one(log_decay), one(gate), S, dev)
-    Y = _out(Y, "Y", tuple(V.shape), V.dtype, dev)
+    dev = _device_index()
+    args, (b, t, h, g, p, n) = _scan_call(V, K, Q, log_decay, gate, S, dev, token=False)
+    Y = _out(Y, "Y", (b, h, p), V.dtype, dev)
     if S_out is None:
         S_out = S
     else:
-        _check_state(S_out, "S_out", tuple(S.shape), dev)
-    _check(L.muon_gated_scan_step(ctypes.byref(a), _ptr(Y), _ptr(S_out), _stream_handle(stream)), "muon_gated_scan_step")
-    _used_on(stream, Y)
+        _check_state(S_out, "S_out", (b, h, p, n), dev)
+    rc = lib().muon_gated_scan_step(args, _ptr(Y), _ptr(S_out), _raw_stream(stream, dev))
+    _check(rc, "muon_gated_scan_step")
+    if stream is not None:
+        _used_on(stream, Y)
     return Y, S_out
 
 
 def _rows(t, name):
     """(rows, n, row stride) of a tensor whose last dimension is adjacent and
     whose other dimensions fold into one row stride."""
-    n = int(t.shape[-1])
+    shape = t.shape
+    n = shape[-1]
     rows = t.numel() // n if n else 0
-    if n > 1 and t.numel() > 0 and t.stride(-1) != 1:
+    if t.is_contiguous():
+        return rows, n, n
+    st = t.stride()
+    if n > 1 and rows > 0 and st[-1] != 1:
         raise ValueError(f"{name} must have adjacent elements in its last dimension")
     ld, expect = n, None
-    for d in range(t.dim() - 2, -1, -1):
-        if t.shape[d] == 1:
+    for d in range(len(shape) - 2, -1, -1):
+        if shape[d] == 1:
             continue
         if expect is None:
-            ld = int(t.stride(d))
-        elif int(t.stride(d)) != expect:
+            ld = st[d]
+        elif st[d] != expect:
             raise ValueError(f"the rows of {name} must be one stride apart")
-        expect = int(t.stride(d)) * int(t.shape[d])
+        expect = st[d] * shape[d]
     return rows, n, ld
 
 
-def _check_row_params(n, device, **params):
-    import torch
-    for name, t in params.items():
-        if t is None:
-            continue
-        if not t.is_contiguous() or tuple(t.shape) != (n,):
-            raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
-        _check_tensors([t], name, (torch.float32,), device)
+def _param(t, name, n, index):
+    """Pointer of a float32 parameter of n elements (None: none)."""
+    if t is None:
+        return None
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
+    _f32_on(t, name, index)
+    return t.data_ptr()
 
 
 def muon_layer_norm(X, weight=None, bias=None, eps=1e-5, center=True, Y=None, stream=None):
@@ -840,23 +908,28 @@ def muon_layer_norm(X, weight=None, bias=None, eps=1e-5, center=True, Y=None, st
     mean, rstd): Y of X's dtype, the float32 statistics of the rows for the
     backward pass (mean None without centering)."""
     import torch
-    L = lib()
-    dev = _current_device()
-    _check_tensors([X], "X", (torch.bfloat16, torch.float32), dev)
+    dev = _device_index()
+    code = _type_code(X, "X")
+    _where(X, "X", dev)
     rows, n, ldx = _rows(X, "X")
-    _check_row_params(n, dev, weight=weight, bias=bias)
+    w, b = _param(weight, "weight", n, dev), _param(bias, "bias", n, dev)
     if Y is None:
         Y = torch.empty(X.shape, dtype=X.dtype, device=dev)
-    if Y.shape != X.shape:
-        raise ValueError("Y must have X's shape")
-    _check_tensors([Y], "Y", (X.dtype,), dev)
-    ldy = _rows(Y, "Y")[2]
-    lead = tuple(X.shape[:-1])
+        ldy = n
+    else:
+        if Y.shape != X.shape:
+            raise ValueError("Y must have X's shape")
+        _same_type(Y, X, "Y")
+        _where(Y, "Y", dev)
+        ldy = _rows(Y, "Y")[2]
+    lead = X.shape[:-1]
     mean = torch.empty(lead, dtype=torch.float32, device=dev) if center else None
     rstd = torch.empty(lead, dtype=torch.float32, device=dev)
-    _check(L.muon_layer_norm(_ptr(X), ldx, _dtype_code(X), rows, n, _ptr(weight), _ptr(bias), float(eps), int(bool(center)),
-                             _ptr(Y), ldy, _ptr(mean), _ptr(rstd), _stream_handle(stream)), "muon_layer_norm")
-    _used_on(stream, Y, mean, rstd)
+    rc = lib().muon_layer_norm(_ptr(X), ldx, code, rows, n, w, b, eps, 1 if center else 0, _ptr(Y), ldy, _ptr(mean),
+                               _ptr(rstd), _raw_stream(stream, dev))
+    _check(rc, "muon_layer_norm")
+    if stream is not None:
+        _used_on(stream, Y, mean, rstd)
     return Y, mean, rstd
 
 
@@ -866,32 +939,35 @@ def muon_layer_norm_backward(dY, X, weight, mean, rstd, center=True, bias_grad=T
     weight, dbias None unless bias_grad."""
     import torch
     L = lib()
-    dev = _current_device()
-    _check_tensors([X], "X", (torch.bfloat16, torch.float32), dev)
-    _check_tensors([dY], "dY", (X.dtype,), dev)
+    dev = _device_index()
+    code = _type_code(X, "X")
+    _same_type(dY, X, "dY")
+    _where(X, "X", dev)
+    _where(dY, "dY", dev)
     if dY.shape != X.shape:
         raise ValueError("dY must have X's shape")
     rows, n, ldx = _rows(X, "X")
     lddy = _rows(dY, "dY")[2]
-    _check_row_params(n, dev, weight=weight)
+    w = _param(weight, "weight", n, dev)
     if center and mean is None:
         raise ValueError("mean is needed with centering")
     for name, t in (("mean", mean if center else None), ("rstd", rstd)):
         if t is None:
             continue
-        if not t.is_contiguous() or t.numel() != rows:
+        if t.numel() != rows or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous float32 tensor with one entry per row")
-        _check_tensors([t], name, (torch.float32,), dev)
-    dt = _dtype_code(X)
-    need = int(L.muon_layer_norm_backward_workspace_size(rows, n, dt))
+        _f32_on(t, name, dev)
+    need = L.muon_layer_norm_backward_workspace_size(rows, n, code)
     if need == 0:
         raise MuonError(MUON_EUNSUPPORTED, "muon_layer_norm_backward_workspace_size")
     dX = torch.empty(X.shape, dtype=X.dtype, device=dev)
     dweight = torch.empty(n, dtype=torch.float32, device=dev) if weight is not None else None
     dbias = torch.empty(n, dtype=torch.float32, device=dev) if bias_grad else None
-    ws = _workspace(workspace, need, dev)
-    _check(L.muon_layer_norm_backward(_ptr(dY), lddy, _ptr(X), ldx, dt, rows, n, _ptr(weight), _ptr(mean) if center else None,
-                                      _ptr(rstd), _ptr(dX), n, _ptr(dweight), _ptr(dbias), ws.data_ptr(), ws.numel(),
-                                      _stream_handle(stream)), "muon_layer_norm_backward")
-    _used_on(stream, dX, dweight, dbias, ws)
+    ws = _new_workspace(workspace, need, dev)
+    rc = L.muon_layer_norm_backward(_ptr(dY), lddy, _ptr(X), ldx, code, rows, n, w, _ptr(mean) if center else None, _ptr(rstd),
+                                    _ptr(dX), n, _ptr(dweight), _ptr(dbias), ws.data_ptr(), ws.numel(),
+                                    _raw_stream(stream, dev))
+    _check(rc, "muon_layer_norm_backward")
+    if stream is not None:
+        _used_on(stream, dX, dweight, dbias, ws)
     return dX, dweight, dbias
