@@ -4,80 +4,89 @@
 //   dx = r (t - mean(t) - xh mean(t xh)),  dw = sum_rows dy xh,  dbias = sum_rows dy.
 // Without centering mu = 0 and mean(t) leaves dx (a root-mean-square norm).
 //
-// Bound by HBM: a row is read once into registers (a wave a row, a workgroup a
-// row beyond kWaveMax 16-byte pieces a lane), the variance is taken from the
-// registers around the mean (two passes, so a large mean costs no digits), and
-// every statistic and sum is float32.  Rows longer than a workgroup's
-// registers are read again from cache.  The backward pass keeps one column sum
-// per element of its registers over all the rows that it walks; workgroups'
-// sums go to the workspace and a second kernel adds them in fixed order.
+// Bound by HBM: a row is read once into registers (by a wave, or by a workgroup
+// of 256 or 512 threads beyond kPieces pieces a lane), the variance is taken
+// from the registers around the mean (two passes, so a large mean costs no
+// digits), and every statistic and sum is float32.  Rows longer than a
+// workgroup's registers are read again from cache.  The backward pass keeps one
+// column sum per element of its registers over all the rows that it walks, with
+// the next row's loads in flight; the workgroups' sums go to the workspace and a
+// second kernel adds them in fixed order.
 #include "launch.h"
 
 namespace muon {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPieces = 4;       // most 16-byte pieces a thread holds of a row
+constexpr int kPieces = 4;       // most pieces a thread holds of a row
 
 template <typename T>
-struct Vec;
-template <>
-struct Vec<bf16_t> {
-  static constexpr int n = 8;
-};
-template <>
-struct Vec<float> {
-  static constexpr int n = 4;
+struct Vec {
+  static constexpr int n = 16 / static_cast<int>(sizeof(T));   // elements of a piece
 };
 
-// Elements [col, col + n) of a row as floats (0 past `width`).
-template <typename T>
-__device__ __forceinline__ void load_piece(const T* row, int col, int width, bool vec, float (&o)[Vec<T>::n]) {
+// Element e of piece i of thread t, of the TPR that share a row.  Aligned rows
+// (VEC): 16 adjacent bytes a piece.  Others: neighbouring threads take
+// neighbouring elements.
+template <typename T, int TPR, bool VEC>
+__device__ __forceinline__ int col_of(int i, int e, int t) {
+  return VEC ? (i * TPR + t) * Vec<T>::n + e : (i * Vec<T>::n + e) * TPR + t;
+}
+
+// Piece i of a row as floats (0 past the end); U: of the row's type, or the
+// float parameters at the same columns.
+template <typename T, typename U, int TPR, bool VEC>
+__device__ __forceinline__ void load_piece(const U* row, int i, int t, int n, float (&o)[Vec<T>::n]) {
+  if constexpr (VEC) {
+    const int col = col_of<T, TPR, VEC>(i, 0, t);
 #pragma unroll
-  for (int i = 0; i < Vec<T>::n; ++i) o[i] = 0.0f;
-  if (col >= width) return;
-  if (vec) {
-    const u32x4_t w = *reinterpret_cast<const u32x4_t*>(row + col);
-    if constexpr (sizeof(T) == 2) {
+    for (int k = 0; k < Vec<T>::n * static_cast<int>(sizeof(U)) / 16; ++k) {
+      u32x4_t w = {0u, 0u, 0u, 0u};
+      if (col < n) w = reinterpret_cast<const u32x4_t*>(row + col)[k];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[2 * i] = lo_bf16(w[i]);
-        o[2 * i + 1] = hi_bf16(w[i]);
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (sizeof(U) == 2) {
+          o[2 * e] = lo_bf16(w[e]);
+          o[2 * e + 1] = hi_bf16(w[e]);
+        } else {
+          o[4 * k + e] = __uint_as_float(w[e]);
+        }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = __uint_as_float(w[i]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < Vec<T>::n; ++i)
-      if (col + i < width) {
-        if constexpr (sizeof(T) == 2) o[i] = bf16_to_f32(row[col + i]);
-        else o[i] = row[col + i];
+    for (int e = 0; e < Vec<T>::n; ++e) {
+      const int col = col_of<T, TPR, VEC>(i, e, t);
+      o[e] = 0.0f;
+      if (col < n) {
+        if constexpr (sizeof(U) == 2) o[e] = bf16_to_f32(row[col]);
+        else o[e] = row[col];
       }
+    }
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void store_piece(T* row, int col, int width, bool vec, const float (&v)[Vec<T>::n]) {
-  if (col >= width) return;
-  if (vec) {
+template <typename T, int TPR, bool VEC>
+__device__ __forceinline__ void store_piece(T* row, int i, int t, int n, const float (&v)[Vec<T>::n]) {
+  if constexpr (VEC) {
+    const int col = col_of<T, TPR, VEC>(i, 0, t);
+    if (col >= n) return;
     u32x4_t w;
-    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(v[i]);
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (sizeof(T) == 2) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+      else w[e] = __float_as_uint(v[e]);
     }
     *reinterpret_cast<u32x4_t*>(row + col) = w;
   } else {
 #pragma unroll
-    for (int i = 0; i < Vec<T>::n; ++i)
-      if (col + i < width) {
-        if constexpr (sizeof(T) == 2) row[col + i] = f32_to_bf16(v[i]);
-        else row[col + i] = v[i];
+    for (int e = 0; e < Vec<T>::n; ++e) {
+      const int col = col_of<T, TPR, VEC>(i, e, t);
+      if (col < n) {
+        if constexpr (sizeof(T) == 2) row[col] = f32_to_bf16(v[e]);
+        else row[col] = v[e];
       }
+    }
   }
 }
 
@@ -88,23 +97,27 @@ __device__ __forceinline__ float row_total(float v, float* red) {
   else return block_sum(v, red);
 }
 
-// PIECES 16-byte pieces of a row a thread, TPR threads a row.
-template <typename T, int TPR, int PIECES>
-__global__ void __launch_bounds__(kThreads) norm_kernel(NormLaunch A) {
-  constexpr int V = Vec<T>::n;
-  __shared__ float red[kThreads / kWave];
+// Threads of a workgroup whose rows take TPR threads each.
+template <int TPR>
+constexpr int threads_of() { return TPR < kThreads ? kThreads : TPR; }
+
+// PIECES pieces of a row a thread, TPR threads a row.
+template <typename T, int TPR, int PIECES, bool VEC>
+__global__ void __launch_bounds__(threads_of<TPR>()) norm_kernel(NormLaunch A) {
+  constexpr int V = Vec<T>::n, kRows = threads_of<TPR>() / TPR;
+  __shared__ float red[threads_of<TPR>() / kWave];
   const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
-  const long long row = static_cast<long long>(blockIdx.x) * (kThreads / TPR) + sub;
+  const long long row = static_cast<long long>(blockIdx.x) * kRows + sub;
   if (row >= A.rows) return;   // whole waves or whole workgroups
   const T* x = static_cast<const T*>(A.x) + row * A.ldx;
   float v[PIECES][V];
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i) {
-    load_piece<T>(x, (i * TPR + t) * V, A.n, A.vec, v[i]);
+  for (int i = 0; i < PIECES; ++i) load_piece<T, T, TPR, VEC>(x, i, t, A.n, v[i]);
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) s += v[i][e];
-  }
   const float inv_n = 1.0f / static_cast<float>(A.n);
   const float mu = A.center ? row_total<TPR>(s, red) * inv_n : 0.0f;
   float q = 0.0f;
@@ -112,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormLaunch A) {
   for (int i = 0; i < PIECES; ++i)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float d = (i * TPR + t) * V + e < A.n ? v[i][e] - mu : 0.0f;
+      const float d = col_of<T, TPR, VEC>(i, e, t) < A.n ? v[i][e] - mu : 0.0f;
       v[i][e] = d;
       q = fmaf(d, d, q);
     }
@@ -120,24 +133,20 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormLaunch A) {
   T* y = static_cast<T*>(A.y) + row * A.ldy;
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
-    const int col = (i * TPR + t) * V;
-    float wv[V], bv[V];
-    if (A.w != nullptr) {
+    float p[V];
 #pragma unroll
-      for (int u = 0; u < V / 4; ++u) load_piece<float>(A.w, col + 4 * u, A.n, A.pvec, *reinterpret_cast<float(*)[4]>(wv + 4 * u));
+    for (int e = 0; e < V; ++e) v[i][e] *= r;
+    if (A.w != nullptr) {
+      load_piece<T, float, TPR, VEC>(A.w, i, t, A.n, p);
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[i][e] *= p[e];
     }
     if (A.bias != nullptr) {
+      load_piece<T, float, TPR, VEC>(A.bias, i, t, A.n, p);
 #pragma unroll
-      for (int u = 0; u < V / 4; ++u) load_piece<float>(A.bias, col + 4 * u, A.n, A.pvec, *reinterpret_cast<float(*)[4]>(bv + 4 * u));
+      for (int e = 0; e < V; ++e) v[i][e] += p[e];
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float o = v[i][e] * r;
-      if (A.w != nullptr) o *= wv[e];
-      if (A.bias != nullptr) o += bv[e];
-      v[i][e] = o;
-    }
-    store_piece<T>(y, col, A.n, A.vec, v[i]);
+    store_piece<T, TPR, VEC>(y, i, t, A.n, v[i]);
   }
   if (t == 0) {
     if (A.mean != nullptr) A.mean[row] = mu;
@@ -148,44 +157,33 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(NormLaunch A) {
 // Rows of any length: a workgroup a row, three readings.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_long_kernel(NormLaunch A) {
-  constexpr int V = Vec<T>::n;
   __shared__ float red[kThreads / kWave];
   const long long row = blockIdx.x;
   const T* x = static_cast<const T*>(A.x) + row * A.ldx;
   const float inv_n = 1.0f / static_cast<float>(A.n);
-  float mu = 0.0f, v[V];
+  const auto at = [&](int c) {
+    if constexpr (sizeof(T) == 2) return bf16_to_f32(x[c]);
+    else return x[c];
+  };
+  float mu = 0.0f;
   if (A.center) {
     float s = 0.0f;
-    for (int col = threadIdx.x * V; col < A.n; col += kThreads * V) {
-      load_piece<T>(x, col, A.n, A.vec, v);
-#pragma unroll
-      for (int e = 0; e < V; ++e) s += v[e];
-    }
+    for (int c = threadIdx.x; c < A.n; c += kThreads) s += at(c);
     mu = block_sum(s, red) * inv_n;
   }
   float q = 0.0f;
-  for (int col = threadIdx.x * V; col < A.n; col += kThreads * V) {
-    load_piece<T>(x, col, A.n, A.vec, v);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float d = col + e < A.n ? v[e] - mu : 0.0f;
-      q = fmaf(d, d, q);
-    }
+  for (int c = threadIdx.x; c < A.n; c += kThreads) {
+    const float d = at(c) - mu;
+    q = fmaf(d, d, q);
   }
   const float r = 1.0f / sqrtf(block_sum(q, red) * inv_n + A.eps);
   T* y = static_cast<T*>(A.y) + row * A.ldy;
-  for (int col = threadIdx.x * V; col < A.n; col += kThreads * V) {
-    load_piece<T>(x, col, A.n, A.vec, v);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float o = (v[e] - mu) * r;
-      if (col + e < A.n) {
-        if (A.w != nullptr) o *= A.w[col + e];
-        if (A.bias != nullptr) o += A.bias[col + e];
-      }
-      v[e] = o;
-    }
-    store_piece<T>(y, col, A.n, A.vec, v);
+  for (int c = threadIdx.x; c < A.n; c += kThreads) {
+    float o = (at(c) - mu) * r;
+    if (A.w != nullptr) o *= A.w[c];
+    if (A.bias != nullptr) o += A.bias[c];
+    if constexpr (sizeof(T) == 2) y[c] = f32_to_bf16(o);
+    else y[c] = o;
   }
   if (threadIdx.x == 0) {
     if (A.mean != nullptr) A.mean[row] = mu;
@@ -193,36 +191,52 @@ __global__ void __launch_bounds__(kThreads) norm_long_kernel(NormLaunch A) {
   }
 }
 
-// Workgroup b walks rows b kThreads / TPR + 0.., a grid apart, and leaves its
-// column sums in part[b][2][n] (or, alone in the grid, in dw and dbias).
-template <typename T, int TPR, int PIECES>
-__global__ void __launch_bounds__(kThreads) norm_grad_kernel(NormGradLaunch A) {
-  constexpr int V = Vec<T>::n;
-  constexpr int kRows = kThreads / TPR;
-  __shared__ float red[kThreads / kWave];
+// Workgroup b walks rows b kRows + 0.., a grid apart, and leaves its column
+// sums in part[b][2][n] (or, alone in the grid, in dw and dbias).
+template <typename T, int TPR, int PIECES, bool VEC>
+__global__ void __launch_bounds__(threads_of<TPR>()) norm_grad_kernel(NormGradLaunch A) {
+  constexpr int V = Vec<T>::n, kAll = threads_of<TPR>(), kRows = kAll / TPR;
+  __shared__ float red[kAll / kWave];
   __shared__ float cols[TPR == kWave ? kWave * V * PIECES : 1];
   const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const float inv_n = 1.0f / static_cast<float>(A.n);
   float wv[PIECES][V], dw[PIECES][V], db[PIECES][V];
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i)
+  for (int i = 0; i < PIECES; ++i) {
+    if (A.w != nullptr) load_piece<T, float, TPR, VEC>(A.w, i, t, A.n, wv[i]);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const int col = (i * TPR + t) * V + e;
-      wv[i][e] = col < A.n ? (A.w != nullptr ? A.w[col] : 1.0f) : 0.0f;
+      if (A.w == nullptr) wv[i][e] = 1.0f;
       dw[i][e] = db[i][e] = 0.0f;
     }
-  for (long long row = static_cast<long long>(blockIdx.x) * kRows + sub; row < A.rows;
-       row += static_cast<long long>(gridDim.x) * kRows) {
+  }
+  const long long step = static_cast<long long>(gridDim.x) * kRows;
+  const bool center = A.mean != nullptr;
+  float xn[PIECES][V], gn[PIECES][V], mun = 0.0f, rn = 0.0f;
+  const auto load_row = [&](long long row) {
     const T* x = static_cast<const T*>(A.x) + row * A.ldx;
     const T* dy = static_cast<const T*>(A.dy) + row * A.lddy;
-    const float mu = A.mean != nullptr ? A.mean[row] : 0.0f, r = A.rstd[row];
-    float xh[PIECES][V], g[PIECES][V];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      load_piece<T>(x, (i * TPR + t) * V, A.n, A.vec, xh[i]);
-      load_piece<T>(dy, (i * TPR + t) * V, A.n, A.vec, g[i]);
+      load_piece<T, T, TPR, VEC>(x, i, t, A.n, xn[i]);
+      load_piece<T, T, TPR, VEC>(dy, i, t, A.n, gn[i]);
     }
+    mun = center ? A.mean[row] : 0.0f;
+    rn = A.rstd[row];
+  };
+  long long row = static_cast<long long>(blockIdx.x) * kRows + sub;
+  if (row < A.rows) load_row(row);
+  for (; row < A.rows; row += step) {
+    float xh[PIECES][V], g[PIECES][V];
+    const float mu = mun, r = rn;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        xh[i][e] = xn[i][e];
+        g[i][e] = gn[i][e];
+      }
+    load_row(row + step < A.rows ? row + step : row);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i)
@@ -235,27 +249,22 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(NormGradLaunch A) {
         s1 += g[i][e];
         s2 = fmaf(g[i][e], xh[i][e], s2);
       }
-    s1 = A.mean != nullptr ? row_total<TPR>(s1, red) * inv_n : 0.0f;
+    s1 = center ? row_total<TPR>(s1, red) * inv_n : 0.0f;
     s2 = row_total<TPR>(s2, red) * inv_n;
     T* dx = static_cast<T*>(A.dx) + row * A.lddx;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
 #pragma unroll
       for (int e = 0; e < V; ++e) g[i][e] = r * (g[i][e] - s1 - xh[i][e] * s2);
-      store_piece<T>(dx, (i * TPR + t) * V, A.n, A.vec, g[i]);
+      store_piece<T, TPR, VEC>(dx, i, t, A.n, g[i]);
     }
   }
-  float* out[2];
-  out[0] = gridDim.x == 1 ? A.dw : A.part + 2LL * blockIdx.x * A.n;
-  out[1] = gridDim.x == 1 ? A.dbias : A.part + (2LL * blockIdx.x + 1) * A.n;
-  if (gridDim.x > 1) {   // sums that nobody asked for are not written
-    if (A.dw == nullptr) out[0] = nullptr;
-    if (A.dbias == nullptr) out[1] = nullptr;
-  }
+  float* out[2] = {A.dw, A.dbias};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     float (&acc)[PIECES][V] = k == 0 ? dw : db;
-    if (out[k] == nullptr) continue;
+    if (out[k] == nullptr) continue;   // a sum that nobody asked for
+    float* to = gridDim.x == 1 ? out[k] : A.part + (2LL * blockIdx.x + k) * A.n;
     if constexpr (TPR == kWave) {
       // the waves' sums, in order
       for (int u = 0; u < kRows; ++u) {
@@ -271,17 +280,17 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(NormGradLaunch A) {
         }
       }
       __syncthreads();
-      for (int col = threadIdx.x; col < A.n; col += kThreads) {
-        const int piece = col / V, e = col % V;
-        out[k][col] = cols[((piece / kWave) * V + e) * kWave + piece % kWave];
+      for (int j = threadIdx.x; j < kWave * V * PIECES; j += kAll) {
+        const int slot = j / kWave, col = col_of<T, TPR, VEC>(slot / V, slot % V, j % kWave);
+        if (col < A.n) to[col] = cols[j];
       }
     } else {
 #pragma unroll
       for (int i = 0; i < PIECES; ++i)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const int col = (i * TPR + t) * V + e;
-          if (col < A.n) out[k][col] = acc[i][e];
+          const int col = col_of<T, TPR, VEC>(i, e, t);
+          if (col < A.n) to[col] = acc[i][e];
         }
     }
   }
@@ -291,7 +300,6 @@ __global__ void __launch_bounds__(kThreads) norm_grad_kernel(NormGradLaunch A) {
 // workspace (each element always by the same thread).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_grad_long_kernel(NormGradLaunch A) {
-  constexpr int V = Vec<T>::n;
   __shared__ float red[kThreads / kWave];
   const float inv_n = 1.0f / static_cast<float>(A.n);
   float* pw = A.part + 2LL * blockIdx.x * A.n;
@@ -301,111 +309,125 @@ __global__ void __launch_bounds__(kThreads) norm_grad_long_kernel(NormGradLaunch
     const T* x = static_cast<const T*>(A.x) + row * A.ldx;
     const T* dy = static_cast<const T*>(A.dy) + row * A.lddy;
     const float mu = A.mean != nullptr ? A.mean[row] : 0.0f, r = A.rstd[row];
-    float xv[V], g[V], s1 = 0.0f, s2 = 0.0f;
-    for (int col = threadIdx.x * V; col < A.n; col += kThreads * V) {
-      load_piece<T>(x, col, A.n, A.vec, xv);
-      load_piece<T>(dy, col, A.n, A.vec, g);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (col + e >= A.n) continue;
-        const float xh = (xv[e] - mu) * r, t = A.w != nullptr ? g[e] * A.w[col + e] : g[e];
-        s1 += t;
-        s2 = fmaf(t, xh, s2);
-        pw[col + e] = first ? g[e] * xh : fmaf(g[e], xh, pw[col + e]);
-        pb[col + e] = first ? g[e] : pb[col + e] + g[e];
-      }
+    const auto val = [](T v) {
+      if constexpr (sizeof(T) == 2) return bf16_to_f32(v);
+      else return v;
+    };
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int c = threadIdx.x; c < A.n; c += kThreads) {
+      const float xh = (val(x[c]) - mu) * r, g = val(dy[c]), t = A.w != nullptr ? g * A.w[c] : g;
+      s1 += t;
+      s2 = fmaf(t, xh, s2);
+      pw[c] = first ? g * xh : fmaf(g, xh, pw[c]);
+      pb[c] = first ? g : pb[c] + g;
     }
     first = false;
     s1 = A.mean != nullptr ? block_sum(s1, red) * inv_n : 0.0f;
     s2 = block_sum(s2, red) * inv_n;
     T* dx = static_cast<T*>(A.dx) + row * A.lddx;
-    for (int col = threadIdx.x * V; col < A.n; col += kThreads * V) {
-      load_piece<T>(x, col, A.n, A.vec, xv);
-      load_piece<T>(dy, col, A.n, A.vec, g);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float t = A.w != nullptr && col + e < A.n ? g[e] * A.w[col + e] : g[e];
-        g[e] = r * (t - s1 - (xv[e] - mu) * r * s2);
-      }
-      store_piece<T>(dx, col, A.n, A.vec, g);
+    for (int c = threadIdx.x; c < A.n; c += kThreads) {
+      const float xh = (val(x[c]) - mu) * r, g = val(dy[c]), t = A.w != nullptr ? g * A.w[c] : g;
+      const float o = r * (t - s1 - xh * s2);
+      if constexpr (sizeof(T) == 2) dx[c] = f32_to_bf16(o);
+      else dx[c] = o;
     }
   }
   if (first)   // no rows: empty sums
-    for (int col = threadIdx.x; col < 2 * A.n; col += kThreads) pw[col] = 0.0f;
+    for (int c = threadIdx.x; c < 2 * A.n; c += kThreads) pw[c] = 0.0f;
 }
 
-// dw and dbias from the workgroups' sums: 64 columns a workgroup, its four
-// waves each a quarter of the parts, added in order.
-__global__ void __launch_bounds__(kThreads) norm_parts_kernel(const float* part, int parts, int n, float* dw, float* dbias) {
-  __shared__ float s[kThreads];
+// dw and dbias from the workgroups' sums: 64 columns a workgroup, its sixteen
+// waves each every sixteenth part, their sums added in order.
+constexpr int kPartWaves = 16;
+__global__ void __launch_bounds__(kPartWaves * kWave) norm_parts_kernel(const float* part, int parts, int n, float* dw, float* dbias) {
+  __shared__ float s[kPartWaves * kWave];
   float* out = blockIdx.y == 0 ? dw : dbias;
   if (out == nullptr) return;
-  const int col = static_cast<int>(blockIdx.x) * kWave + (threadIdx.x & 63), w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & (kWave - 1), col = static_cast<int>(blockIdx.x) * kWave + lane, w = threadIdx.x / kWave;
   float acc = 0.0f;
-  if (col < n)
-    for (int p = w; p < parts; p += 4) acc += part[(2LL * p + blockIdx.y) * n + col];
+  if (col < n) {
+    const float* p = part + static_cast<long long>(blockIdx.y) * n + col;
+#pragma unroll 8
+    for (int i = w; i < parts; i += kPartWaves) acc += p[2LL * i * n];
+  }
   s[threadIdx.x] = acc;
   __syncthreads();
-  if (w == 0 && col < n) out[col] = (s[threadIdx.x] + s[64 + threadIdx.x]) + (s[128 + threadIdx.x] + s[192 + threadIdx.x]);
+  if (w == 0 && col < n) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPartWaves; ++i) t += s[i * kWave + lane];
+    out[col] = t;
+  }
 }
 
-// Pieces a lane needs when a wave (or a workgroup) takes the row.
-int pieces(int n, int elems, int threads) { return (n + elems * threads - 1) / (elems * threads); }
+// Threads that share a row of n elements (0: more than a workgroup holds) and
+// the pieces of it that each takes.
+struct RowPlan {
+  int threads, pieces;
+};
+RowPlan row_plan(int n, int elems) {
+  for (int t : {kWave, kThreads, 2 * kThreads}) {
+    const int p = (n + elems * t - 1) / (elems * t);
+    if (p <= kPieces) return {t, p <= 1 ? 1 : p <= 2 ? 2 : 4};
+  }
+  return {0, 0};
+}
 
-template <typename T, int TPR>
-hipError_t norm_pieces(const NormLaunch& A, int p, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>((A.rows + kThreads / TPR - 1) / (kThreads / TPR))), block(kThreads);
-  if (p == 1) hipLaunchKernelGGL((norm_kernel<T, TPR, 1>), grid, block, 0, st, A);
-  else if (p == 2) hipLaunchKernelGGL((norm_kernel<T, TPR, 2>), grid, block, 0, st, A);
-  else hipLaunchKernelGGL((norm_kernel<T, TPR, 4>), grid, block, 0, st, A);
+template <typename T, int TPR, int PIECES>
+hipError_t norm(const NormLaunch& A, hipStream_t st) {
+  constexpr int kRows = threads_of<TPR>() / TPR;
+  const dim3 grid(static_cast<unsigned>((A.rows + kRows - 1) / kRows)), block(threads_of<TPR>());
+  if (A.vec) hipLaunchKernelGGL((norm_kernel<T, TPR, PIECES, true>), grid, block, 0, st, A);
+  else hipLaunchKernelGGL((norm_kernel<T, TPR, PIECES, false>), grid, block, 0, st, A);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t norm_any(const NormLaunch& A, hipStream_t st) {
-  const int p = pieces(A.n, Vec<T>::n, kWave), pw = pieces(A.n, Vec<T>::n, kThreads);
-  if (p <= kPieces) return norm_pieces<T, kWave>(A, p, st);
-  if (pw <= kPieces) return norm_pieces<T, kThreads>(A, pw, st);
+  const RowPlan p = row_plan(A.n, Vec<T>::n);
+  if (p.threads == kWave) return p.pieces == 1 ? norm<T, kWave, 1>(A, st) : p.pieces == 2 ? norm<T, kWave, 2>(A, st) : norm<T, kWave, 4>(A, st);
+  if (p.threads == kThreads) return p.pieces == 2 ? norm<T, kThreads, 2>(A, st) : norm<T, kThreads, 4>(A, st);
+  if (p.threads != 0) return norm<T, 2 * kThreads, 4>(A, st);
   hipLaunchKernelGGL((norm_long_kernel<T>), dim3(static_cast<unsigned>(A.rows)), dim3(kThreads), 0, st, A);
   return hipGetLastError();
 }
 
-template <typename T, int TPR>
-hipError_t grad_pieces(const NormGradLaunch& A, int p, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(A.parts)), block(kThreads);
-  if (p == 1) hipLaunchKernelGGL((norm_grad_kernel<T, TPR, 1>), grid, block, 0, st, A);
-  else if (p == 2) hipLaunchKernelGGL((norm_grad_kernel<T, TPR, 2>), grid, block, 0, st, A);
-  else hipLaunchKernelGGL((norm_grad_kernel<T, TPR, 4>), grid, block, 0, st, A);
+template <typename T, int TPR, int PIECES>
+hipError_t grad(const NormGradLaunch& A, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(A.parts)), block(threads_of<TPR>());
+  if (A.vec) hipLaunchKernelGGL((norm_grad_kernel<T, TPR, PIECES, true>), grid, block, 0, st, A);
+  else hipLaunchKernelGGL((norm_grad_kernel<T, TPR, PIECES, false>), grid, block, 0, st, A);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t grad_any(const NormGradLaunch& A, hipStream_t st) {
-  const int p = pieces(A.n, Vec<T>::n, kWave), pw = pieces(A.n, Vec<T>::n, kThreads);
+  const RowPlan p = row_plan(A.n, Vec<T>::n);
   hipError_t e;
-  bool direct = A.parts == 1;
-  if (p <= kPieces) {
-    e = grad_pieces<T, kWave>(A, p, st);
-  } else if (pw <= kPieces) {
-    e = grad_pieces<T, kThreads>(A, pw, st);
+  if (p.threads == kWave) {
+    e = p.pieces == 1 ? grad<T, kWave, 1>(A, st) : p.pieces == 2 ? grad<T, kWave, 2>(A, st) : grad<T, kWave, 4>(A, st);
+  } else if (p.threads == kThreads) {
+    e = p.pieces == 2 ? grad<T, kThreads, 2>(A, st) : grad<T, kThreads, 4>(A, st);
+  } else if (p.threads != 0) {
+    e = grad<T, 2 * kThreads, 4>(A, st);
   } else {
-    direct = false;
     hipLaunchKernelGGL((norm_grad_long_kernel<T>), dim3(static_cast<unsigned>(A.parts)), dim3(kThreads), 0, st, A);
     e = hipGetLastError();
   }
-  if (e != hipSuccess || direct || (A.dw == nullptr && A.dbias == nullptr)) return e;
-  hipLaunchKernelGGL(norm_parts_kernel, dim3((A.n + kWave - 1) / kWave, 2), dim3(kThreads), 0, st, A.part, A.parts, A.n, A.dw,
-                     A.dbias);
+  if (e != hipSuccess || (A.parts == 1 && p.threads != 0) || (A.dw == nullptr && A.dbias == nullptr)) return e;
+  hipLaunchKernelGGL(norm_parts_kernel, dim3((A.n + kWave - 1) / kWave, 2), dim3(kPartWaves * kWave), 0, st, A.part, A.parts,
+                     A.n, A.dw, A.dbias);
   return hipGetLastError();
 }
 
 }  // namespace
 
 // Workgroups of the backward pass: enough to fill the chip, at least eight
-// rows a wave where there are that many.
+// rows a wave (or workgroup, where it takes a row together) where there are
+// that many.
 int norm_grad_parts(long long rows, int n, bool bf16) {
-  const bool wave_rows = pieces(n, bf16 ? Vec<bf16_t>::n : Vec<float>::n, kWave) <= kPieces;
-  const long long per = wave_rows ? 4 * 8 : 8;
+  const RowPlan p = row_plan(n, bf16 ? Vec<bf16_t>::n : Vec<float>::n);
+  const long long per = p.threads == kWave ? 8LL * kThreads / kWave : 2;
   const long long want = (rows + per - 1) / per;
   return static_cast<int>(want < 1 ? 1 : want > 512 ? 512 : want);
 }

@@ -339,8 +339,7 @@ int muon_layer_norm(const void* X, long long ldx, int dtype, long long rows, int
     return MUON_EINVAL;
   NormLaunch A{};
   A.x = X; A.y = Y; A.ldx = ldx; A.ldy = ldy; A.rows = rows; A.n = n; A.center = center;
-  A.vec = rows_vec(X, ldx, n, es) && rows_vec(Y, ldy, n, es);
-  A.pvec = aligned16(weight) && aligned16(bias) && n % 4 == 0;
+  A.vec = rows_vec(X, ldx, n, es) && rows_vec(Y, ldy, n, es) && aligned16(weight) && aligned16(bias);
   A.w = weight; A.bias = bias; A.eps = eps; A.mean = mean; A.rstd = rstd;
   return launch_norm(A, dtype == MUON_BF16, static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_EHIP;
 }
@@ -370,7 +369,7 @@ int muon_layer_norm_backward(const void* dY, long long lddy, const void* X, long
     return MUON_EINVAL;
   NormGradLaunch A{};
   A.dy = dY; A.x = X; A.dx = dX; A.lddy = lddy; A.ldx = ldx; A.lddx = lddx; A.rows = rows; A.n = n;
-  A.vec = rows_vec(dY, lddy, n, es) && rows_vec(X, ldx, n, es) && rows_vec(dX, lddx, n, es);
+  A.vec = rows_vec(dY, lddy, n, es) && rows_vec(X, ldx, n, es) && rows_vec(dX, lddx, n, es) && aligned16(weight);
   A.w = weight; A.mean = mean; A.rstd = rstd; A.dw = dweight; A.dbias = dbias;
   A.part = static_cast<float*>(workspace);
   A.parts = norm_grad_parts(rows, n, dtype == MUON_BF16);
