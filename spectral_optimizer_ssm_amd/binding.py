@@ -647,17 +647,26 @@ _SEQ = struct.Struct("@Pqqq")                              # muon_seq
 _NO_SEQ = (0, 0, 0, 0)
 
 
-def _device_index() -> int:
+torch = None   # imported by the first call
+
+
+def _load_torch():
+    global torch
     import torch
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _device_index() -> int:
+    """Index of torch's current GPU."""
+    if torch is None:
+        _load_torch()
+    return torch.cuda.current_device()
 
 
 def _raw_stream(stream, index) -> Optional[int]:
     """The caller's stream (or torch's current one) as a hipStream_t."""
-    import torch
-    if stream is not None:
-        return int(stream.cuda_stream) or None
-    return torch._C._cuda_getCurrentRawStream(index) or None
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index) or None
+    return int(stream.cuda_stream) or None
 
 
 def _where(t, name, index):
@@ -667,7 +676,6 @@ def _where(t, name, index):
 
 
 def _type_code(t, name) -> int:
-    import torch
     if t.dtype is torch.bfloat16:
         return MUON_BF16
     if t.dtype is torch.float32:
@@ -681,7 +689,6 @@ def _same_type(t, ref, name):
 
 
 def _f32_on(t, name, index):
-    import torch
     if t.dtype is not torch.float32:
         raise TypeError(f"{name} must be float32 (got {t.dtype})")
     _where(t, name, index)
@@ -743,7 +750,6 @@ def _scan_call(V, K, Q, log_decay, gate, S0, index, token=True):
 
 def _out(t, name, shape, dtype, index):
     """The caller's output tensor when given (checked), else a new one."""
-    import torch
     if t is None:
         return torch.empty(shape, dtype=dtype, device=index)
     if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
@@ -767,7 +773,6 @@ def _used_on(stream, *tensors):
 
 
 def _new_workspace(workspace, need, index):
-    import torch
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=index)
     return _workspace(workspace, need, torch.device("cuda", index))
@@ -776,6 +781,8 @@ def _new_workspace(workspace, need, index):
 def muon_gated_scan_workspace_size(V, K, backward=False) -> int:
     """Workspace bytes of muon_gated_scan (backward: of
     muon_gated_scan_backward) for V and K of these shapes and dtype."""
+    if torch is None:
+        _load_torch()
     b, t, h, p = V.shape
     args = _SCAN_ARGS.pack(b, t, h, K.shape[2], p, K.shape[3], _type_code(V, "V"), *(5 * _NO_SEQ), 0)
     L = lib()
@@ -793,7 +800,6 @@ def muon_gated_scan(V, K, Q, log_decay, gate=None, S0=None, Y=None, S_out=None, 
     of V's dtype and float32, and the last state, in the tensors given or in
     new ones.  workspace: a uint8 tensor of at least
     muon_gated_scan_workspace_size bytes to use instead of a new one."""
-    import torch
     L = lib()
     dev = _device_index()
     args, (b, t, h, g, p, n) = _scan_call(V, K, Q, log_decay, gate, S0, dev)
@@ -817,7 +823,6 @@ def muon_gated_scan_backward(V, K, Q, log_decay, dY, gate=None, S0=None, dS=None
     dlog_decay, dgate, dS0), of the shapes and dtypes of what they are the
     gradients of, in the tensors given or in new ones; dgate is None without a
     gate, dS0 without S0."""
-    import torch
     L = lib()
     dev = _device_index()
     args, (b, t, h, g, p, n) = _scan_call(V, K, Q, log_decay, gate, S0, dev)
@@ -907,14 +912,13 @@ def muon_layer_norm(X, weight=None, bias=None, eps=1e-5, center=True, Y=None, st
     root-mean-square norm (mean 0).  weight and bias are float32.  Returns (Y,
     mean, rstd): Y of X's dtype, the float32 statistics of the rows for the
     backward pass (mean None without centering)."""
-    import torch
     dev = _device_index()
     code = _type_code(X, "X")
     _where(X, "X", dev)
     rows, n, ldx = _rows(X, "X")
     w, b = _param(weight, "weight", n, dev), _param(bias, "bias", n, dev)
     if Y is None:
-        Y = torch.empty(X.shape, dtype=X.dtype, device=dev)
+        Y = torch.empty_like(X, memory_format=torch.contiguous_format)
         ldy = n
     else:
         if Y.shape != X.shape:
@@ -923,8 +927,8 @@ def muon_layer_norm(X, weight=None, bias=None, eps=1e-5, center=True, Y=None, st
         _where(Y, "Y", dev)
         ldy = _rows(Y, "Y")[2]
     lead = X.shape[:-1]
-    mean = torch.empty(lead, dtype=torch.float32, device=dev) if center else None
     rstd = torch.empty(lead, dtype=torch.float32, device=dev)
+    mean = torch.empty_like(rstd) if center else None
     rc = lib().muon_layer_norm(_ptr(X), ldx, code, rows, n, w, b, eps, 1 if center else 0, _ptr(Y), ldy, _ptr(mean),
                                _ptr(rstd), _raw_stream(stream, dev))
     _check(rc, "muon_layer_norm")
@@ -937,7 +941,6 @@ def muon_layer_norm_backward(dY, X, weight, mean, rstd, center=True, bias_grad=T
     """Gradients through muon_layer_norm from its input, weight and the
     statistics that it returned: (dX, dweight, dbias), dweight None without a
     weight, dbias None unless bias_grad."""
-    import torch
     L = lib()
     dev = _device_index()
     code = _type_code(X, "X")
@@ -960,7 +963,7 @@ def muon_layer_norm_backward(dY, X, weight, mean, rstd, center=True, bias_grad=T
     need = L.muon_layer_norm_backward_workspace_size(rows, n, code)
     if need == 0:
         raise MuonError(MUON_EUNSUPPORTED, "muon_layer_norm_backward_workspace_size")
-    dX = torch.empty(X.shape, dtype=X.dtype, device=dev)
+    dX = torch.empty_like(X, memory_format=torch.contiguous_format)
     dweight = torch.empty(n, dtype=torch.float32, device=dev) if weight is not None else None
     dbias = torch.empty(n, dtype=torch.float32, device=dev) if bias_grad else None
     ws = _new_workspace(workspace, need, dev)
