@@ -290,8 +290,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) scan_read_kernel(WalkPair P) 
     tx.store_transposed(lxt, tid);
     __syncthreads();
     load_tiles(cc + 1);
-    // M^T tiles: rows j, columns i, so a lane's four values are neighbours in M.  Ten tiles for seven waves: the
-    // last one has the next chunk's gates to prepare.
+    // tiles of M.  Ten for seven waves: the last one has the next chunk's gates to prepare.
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int e = w + 7 * u;
@@ -300,14 +299,11 @@ __global__ void __launch_bounds__(kWalkThreads, 2) scan_read_kernel(WalkPair P) 
         f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < NT / 32; ++s)
-          a = O::mma(O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4), O::row(lq + (16 * it + l16) * L::kLdN + 32 * s + 8 * g4), a);
-        const int i = 16 * it + l16, j0 = 16 * jt + 4 * g4;
-        const float hi = G.hi[i], lo = G.lo[i];
-        const f32x4_t jh = *reinterpret_cast<const f32x4_t*>(G.hi + j0), jl = *reinterpret_cast<const f32x4_t*>(G.lo + j0);
-        const f32x4_t jb = *reinterpret_cast<const f32x4_t*>(G.b + j0);
+          a = O::mma(O::row(lq + (16 * it + l16) * L::kLdN + 32 * s + 8 * g4), O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4), a);
+        const int i0 = 16 * it + 4 * g4, j = 16 * jt + l16;
+        a *= between4(G, it, jt, i0, j) * G.b[j];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) a[r] = j0 + r <= i ? a[r] * between(hi, lo, jh[r], jl[r]) * jb[r] : 0.0f;
-        O::store4(lm + i * L::kLdM + j0, a);
+        for (int r = 0; r < 4; ++r) lm[(i0 + r) * L::kLdM + j] = O::from_f32(a[r]);
       }
     }
     if (w == 7) {

@@ -60,15 +60,6 @@ struct GradLds {
   static_assert(kLdM <= 2 * kLdP, "D fits where v and dy were");
 };
 
-// Sum over the 16 lanes of a row.
-__device__ __forceinline__ float row_sum(float v) {
-  v += dpp_f<kDppXor1>(v);
-  v += dpp_f<kDppXor2>(v);
-  v += dpp_f<0x141>(v);   // row_half_mirror
-  v += dpp_f<0x140>(v);   // row_mirror
-  return v;
-}
-
 template <typename T, int NT, int Q, bool VEC>
 __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
   typedef Ops<T> O;
@@ -209,6 +200,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
 
+    float cols[kMaxTiles];
 #pragma unroll
     for (int t = 0; t < kMaxTiles; ++t) {
       {
@@ -219,27 +211,34 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
           e = O::mma(O::row(ldy + (16 * it + l16) * L::kLdP + 32 * s + 8 * g4),
                      O::row(lv + (16 * jt + l16) * L::kLdP + 32 * s + 8 * g4), e);
         const int j = 16 * jt + l16, i0 = 16 * it + 4 * g4;
-        const float hi = G.hi[j], lo = G.lo[j], b = G.b[j];
-        const f32x4_t ih = *reinterpret_cast<const f32x4_t*>(G.hi + i0), il = *reinterpret_cast<const f32x4_t*>(G.lo + i0);
+        const float b = G.b[j];
+        const f32x4_t d = between4(G, it, jt, i0, j);
         f32x4_t mm, rs;
-        float col = 0.0f;
+        cols[t] = 0.0f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float d = i0 + r >= j ? between(ih[r], il[r], hi, lo) : 0.0f;
-          mm[r] = d * sc[t][r];
-          dsum[t][r] = fmaf(d * e[r], b, dsum[t][r]);
+          mm[r] = d[r] * sc[t][r];
+          dsum[t][r] = fmaf(d[r] * e[r], b, dsum[t][r]);
           const float we = mm[r] * e[r];
-          col += we;
-          rs[r] = row_sum(we * b);
+          cols[t] += we;
+          rs[r] = we * b;
         }
         O::store4(lm + j * L::kLdM + i0, mm);
-        col += __shfl_xor(col, 16, kWave);
-        col += __shfl_xor(col, 32, kWave);
-        if (g4 == 0) lcol[it * Q + j] = col;
-        if (l16 == 0) *reinterpret_cast<f32x4_t*>(lrow + jt * Q + i0) = rs;
+        const float row = sum_lanes4(rs[0], rs[1], rs[2], rs[3], l16);
+        if (l16 < 4) lrow[jt * Q + i0 + l16] = row;
         settle(dsum[t]);
       }
       __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // column sums, four tiles at a time (a wave's last group may name its last tile twice)
+#pragma unroll
+    for (int t = 0; t < kMaxTiles; t += 4) {
+      const int a = t, b = t + 1 < kMaxTiles ? t + 1 : a, c = t + 2 < kMaxTiles ? t + 2 : a, d = t + 3 < kMaxTiles ? t + 3 : a;
+      const float sum = sum_rows4(cols[a], cols[b], cols[c], cols[d]);
+      const int it = g4 == 0 ? trow[a] : g4 == 1 ? trow[b] : g4 == 2 ? trow[c] : trow[d];
+      const int jt = g4 == 0 ? tcol[a] : g4 == 1 ? tcol[b] : g4 == 2 ? tcol[c] : tcol[d];
+      lcol[it * Q + 16 * jt + l16] = sum;
     }
 
     // the states' part of dq, then of dk, and the states' product
@@ -299,14 +298,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
             settle(out[b][u0 + u]);
           }
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          sums[u] += __shfl_xor(sums[u], 16, kWave);
-          sums[u] += __shfl_xor(sums[u], 32, kWave);
-        }
-        if (g4 == 0)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) slot[nw0 / kNW * Q + 16 * ((u0 + u) * kTG + tg) + l16] = sums[u];
+        slot[nw0 / kNW * Q + 16 * ((u0 + g4) * kTG + tg) + l16] = sum_rows4(sums[0], sums[1], sums[2], sums[3]);
         __builtin_amdgcn_sched_barrier(0);
       }
     };

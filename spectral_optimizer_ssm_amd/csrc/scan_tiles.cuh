@@ -362,6 +362,7 @@ struct Gates {
   float first[Q];       // e^{c_i}
   float last[Q];        // e^{c_end - c_j}
   float own[Q];         // e^{g_t}
+  float row[Q];         // e^{c_t - c_r}, r the first token of t's 16
   float in[Q];          // weights of what enters a state: e^{c_end - c_j} b_j, in reversed time e^{c_i}
   float end[4];         // e^{c_end}
 };
@@ -390,13 +391,56 @@ __device__ __forceinline__ double write_gates(Gates<Q>& G, const float (&log_dec
     G.first[t] = first;
     G.last[t] = last;
     G.in[t] = reverse ? first : last * gate[u];
+    G.row[t] = __builtin_amdgcn_exp2f(static_cast<float>(c[u] - __shfl(c[u], lane & 48, kWave)));
   }
   if (lane == 0) G.end[0] = __builtin_amdgcn_exp2f(static_cast<float>(e));
   return e;
 }
 
-__device__ __forceinline__ float between(float hi_i, float lo_i, float hi_j, float lo_j) {
-  return __builtin_amdgcn_exp2f((hi_i - hi_j) + (lo_i - lo_j));
+// e^{c_i - c_j} for the four rows i = i0..i0 + 3 and the column j of a tile in
+// rows i of 16-token block it.  Below the diagonal block it is taken by way of
+// the block's first token, one exponential for the four (its two factors are at
+// most 1 where the log decays are); on it, one by one, 0 for j > i.
+template <int Q>
+__device__ __forceinline__ f32x4_t between4(const Gates<Q>& G, int it, int jt, int i0, int j) {
+  const float hi = G.hi[j], lo = G.lo[j];
+  f32x4_t d;
+  if (it != jt) {
+    const float to = __builtin_amdgcn_exp2f((G.hi[16 * it] - hi) + (G.lo[16 * it] - lo));
+    d = *reinterpret_cast<const f32x4_t*>(G.row + i0) * to;
+  } else {
+    const f32x4_t ih = *reinterpret_cast<const f32x4_t*>(G.hi + i0), il = *reinterpret_cast<const f32x4_t*>(G.lo + i0);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float e = __builtin_amdgcn_exp2f((ih[r] - hi) + (il[r] - lo));
+      d[r] = i0 + r >= j ? e : 0.0f;
+    }
+  }
+  return d;
+}
+
+// Sums over the four 16-lane rows of a wave, for four values at once: row g of
+// the result holds the sum of s_g (v_permlane16_swap, v_permlane32_swap: no
+// LDS).
+__device__ __forceinline__ float sum_rows4(float s0, float s1, float s2, float s3) {
+  const auto swap_add16 = [](float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  };
+  const float a = swap_add16(s0, s1), b = swap_add16(s2, s3);
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// Sums over the 16 lanes of a row, for four values at once: lane l of the row
+// holds the sum of s_{l % 4}.
+__device__ __forceinline__ float sum_lanes4(float s0, float s1, float s2, float s3, int l16) {
+  const bool odd = l16 & 1, two = l16 & 2;
+  const float a = (odd ? s1 : s0) + dpp_f<kDppXor1>(odd ? s0 : s1);
+  const float b = (odd ? s3 : s2) + dpp_f<kDppXor1>(odd ? s2 : s3);
+  float v = (two ? b : a) + dpp_f<kDppXor2>(two ? a : b);
+  v += dpp_f<kDppRor8>(v);
+  v += dpp_f<0x124>(v);   // row_ror:4
+  return v;
 }
 
 // Tile e of the 16 x 16 tiles on and below the diagonal, row by row (at most
