@@ -24,7 +24,11 @@ namespace {
 
 using namespace scan;
 
-constexpr int kWalkThreads = 512;
+// Waves that multiply, and one more that prepares the gates of the next chunk
+// while they do: its prefix sum in float64 is a long dependent chain.
+constexpr int kReadWaves = 8, kStatesWaves = 4;
+constexpr int kReadThreads = kReadWaves * kWave, kStatesThreads = kStatesWaves * kWave;
+constexpr int kStateCols = 64;   // columns n of S per workgroup of the states' walk
 constexpr int kStepThreads = 256;
 
 struct WalkPair {
@@ -33,51 +37,53 @@ struct WalkPair {
 
 // LDS of the walk.
 template <typename T, int NT>
-struct WalkLds {
+struct ReadLds {
   static constexpr int kLdN = NT + Ops<T>::kPad;
   static constexpr int kLdM = kQ + Ops<T>::kPad;
   static constexpr int kt = 0;                                  // k^T [NT][kQ]
   static constexpr int xt = kt + NT * kLdM * (int)sizeof(T);    // x^T [kPB][kQ]
   static constexpr int gates = xt + kPB * kLdM * (int)sizeof(T);   // Gates[2]
-  static constexpr int states_bytes = gates + 2 * (int)sizeof(Gates<kQ>);
-  static constexpr int k = states_bytes;                        // k [kQ][NT]
+  static constexpr int k = gates + 2 * (int)sizeof(Gates<kQ>);  // k [kQ][NT]
   static constexpr int q = k + kQ * kLdN * (int)sizeof(T);      // q [kQ][NT]
   static constexpr int m = q + kQ * kLdN * (int)sizeof(T);      // weights M [i][j]
   static constexpr int y = m + kQ * kLdM * (int)sizeof(T);      // halves of y that waves hand over [8][2][64] float4
-  static constexpr int read_bytes = y + 8 * 2 * 64 * 16;
+  static constexpr int bytes = y + 8 * 2 * 64 * 16;
+  static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
+};
+template <typename T>
+struct StatesLds {
+  static constexpr int kLdM = kQ + Ops<T>::kPad;
+  static constexpr int kt = 0;                                         // k^T [kStateCols][kQ]
+  static constexpr int xt = kt + kStateCols * kLdM * (int)sizeof(T);   // x^T [kPB][kQ]
+  static constexpr int gates = xt + kPB * kLdM * (int)sizeof(T);       // Gates[2]
+  static constexpr int bytes = gates + 2 * (int)sizeof(Gates<kQ>);
 };
 
-// One sequence (segment), head and block of kPB state rows.  Wave w of eight
-// holds rows p = 16 (w % 4) + 0..15 of S and columns n of half w / 4.
-template <typename T, int NT, bool VEC>
+// One sequence (segment), head and block of kPB state rows.  A wave holds rows
+// p = 16 pw + 0..15 of S and KT 16-column tiles from column nbase.
+template <typename T, int NT, int KT>
 struct Walk {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
-  typedef WalkLds<T, NT> L;
-  static constexpr int kT = NT / 32;       // state tiles of a wave
 
   const ScanWalk& A;
-  int tid, lane, w, l16, g4, pw, nh, nbase;
+  int tid, lane, w, l16, g4, pw, nbase;
   int seg, h, pb, grp, rows_p, cc0, cc1, last_chunk;
   long long bi, vrow;
   bool reverse;
-  const float *gp, *bp;
-  // the state: tile t holds S^T rows n = nbase + 16 t + 4 g4 + 0..3, column p = 16 pw + l16
-  f32x4_t st[kT];
-  float gv[1], bv[1];
+  // tile t holds S^T rows n = nbase + 16 t + 4 g4 + 0..3, column p = 16 pw + l16
+  f32x4_t st[KT];
 
-  __device__ __forceinline__ explicit Walk(const ScanWalk& A) : A(A) {
+  __device__ __forceinline__ Walk(const ScanWalk& A, int item) : A(A) {
     tid = threadIdx.x;
     lane = tid & 63;
     w = __builtin_amdgcn_readfirstlane(tid >> 6);
     l16 = lane & 15;
     g4 = lane >> 4;
     pw = w & 3;
-    nh = w >> 2;
-    nbase = nh * (NT / 2);
+    nbase = 0;
     const int vheads = A.heads * A.pblocks;
     // the heads that share keys are neighbours, for every segment
-    const int item = xcd_item(blockIdx.x, gridDim.x);
     const int vh = item % vheads;
     seg = item / vheads % A.nseg;
     bi = item / vheads / A.nseg;
@@ -90,9 +96,6 @@ struct Walk {
     last_chunk = A.nchunks - 1;
     cc0 = seg * A.seg_chunks;
     cc1 = cc0 + A.seg_chunks < A.nchunks ? cc0 + A.seg_chunks : A.nchunks;
-    gp = static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh;
-    bp = A.b.p == nullptr ? nullptr : static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh;
-    gv[0] = bv[0] = 0.0f;
   }
   // the cc-th chunk visited, and its tokens (none past the segment: a branch
   // around a prefetch would keep two copies of its registers)
@@ -102,28 +105,47 @@ struct Walk {
     return cc >= cc1 ? 0 : left < kQ ? static_cast<int>(left) : kQ;
   }
   __device__ __forceinline__ long long token_of(int cc) const { return static_cast<long long>(chunk_of(cc < cc1 ? cc : cc0)) * kQ; }
-
-  // gates of the cc-th chunk visited, a token a lane (past the end: no decay, no input)
-  __device__ __forceinline__ void load_gates(int cc) {
-    const int rows = rows_of(cc);
-    const long long t = token_of(cc) + (lane < rows ? lane : 0);
-    gv[0] = gp[t * A.g.st];
-    bv[0] = bp == nullptr ? 1.0f : bp[t * A.b.st];
-    if (lane >= rows) gv[0] = bv[0] = 0.0f;
-  }
   __device__ __forceinline__ int tile_off() const { return (16 * pw + l16) * NT + nbase + 4 * g4; }
+
+  // The gate wave's part: gates of every chunk, one ahead of the others, who
+  // meet it at `barriers` barriers a chunk (the gates are needed after the
+  // second).
+  template <int BARRIERS>
+  __device__ __forceinline__ void gate_wave(Gates<kQ>* gates) const {
+    const float* gp = static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh;
+    const float* bp = A.b.p == nullptr ? nullptr : static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh;
+    float gv[1], bv[1];
+    const auto load = [&](int cc) {   // a token a lane (past the end: no decay, no input)
+      const int rows = rows_of(cc);
+      const long long t = token_of(cc) + (lane < rows ? lane : 0);
+      gv[0] = gp[t * A.g.st];
+      bv[0] = bp == nullptr ? 1.0f : bp[t * A.b.st];
+      if (lane >= rows) gv[0] = bv[0] = 0.0f;
+    };
+    load(cc0);
+    double log = write_gates(gates[0], gv, bv, lane, reverse);
+    load(cc0 + 1);
+    for (int cc = cc0; cc < cc1; ++cc) {
+      __syncthreads();
+      __syncthreads();
+      log += write_gates(gates[(cc - cc0 + 1) & 1], gv, bv, lane, reverse);   // past the segment: 0
+      load(cc + 2);
+      if constexpr (BARRIERS > 2) __syncthreads();
+    }
+    if (A.totals && lane == 0) A.seg_decay[vrow * A.nseg + seg] = __builtin_amdgcn_exp2f(static_cast<float>(log));
+  }
 
   __device__ __forceinline__ void load_state() {
     const int prow = pb * kPB + 16 * pw + l16;
     if (A.seg_state != nullptr && !A.totals) {
       const float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off();
 #pragma unroll
-      for (int t = 0; t < kT; ++t) st[t] = *reinterpret_cast<const f32x4_t*>(sp + 16 * t);
+      for (int t = 0; t < KT; ++t) st[t] = *reinterpret_cast<const f32x4_t*>(sp + 16 * t);
     } else {
       const bool init = A.init != nullptr && !A.totals;
       const float* sp = A.init + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
 #pragma unroll
-      for (int t = 0; t < kT; ++t)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int n = nbase + 16 * t + 4 * g4 + r;
@@ -131,17 +153,16 @@ struct Walk {
         }
     }
   }
-  __device__ __forceinline__ void store_state(double seg_log) const {
+  __device__ __forceinline__ void store_state() const {
     if (A.totals) {
       float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off();
 #pragma unroll
-      for (int t = 0; t < kT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
-      if (w == 7 && lane == 0) A.seg_decay[vrow * A.nseg + seg] = __builtin_amdgcn_exp2f(static_cast<float>(seg_log));
+      for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
     } else if (A.fin != nullptr && cc1 == A.nchunks) {
       const int prow = pb * kPB + 16 * pw + l16;
       float* sp = A.fin + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
 #pragma unroll
-      for (int t = 0; t < kT; ++t)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int n = nbase + 16 * t + 4 * g4 + r;
@@ -149,11 +170,11 @@ struct Walk {
         }
     }
   }
-  // S = e^{c_end} S + sum_j in_j x_j k_j^T
-  __device__ __forceinline__ void update(const Gates<kQ>& G, const T* lkt, const T* lxt) {
+  // S = e^{c_end} S + sum_j in_j x_j k_j^T; this wave's columns: from row n0 of lkt
+  __device__ __forceinline__ void update(const Gates<kQ>& G, const T* lkt, int n0, const T* lxt) {
     const float end = G.end[0];
 #pragma unroll
-    for (int t = 0; t < kT; ++t) st[t] *= end;
+    for (int t = 0; t < KT; ++t) st[t] *= end;
 #pragma unroll
     for (int s = 0; s < kQ / 32; ++s) {
       float xv[8], wv[8];
@@ -161,51 +182,53 @@ struct Walk {
       load8(G.in + 32 * s + 8 * g4, wv);
 #pragma unroll
       for (int e = 0; e < 8; ++e) xv[e] *= wv[e];
-      Frag f[O::kSplit], kf[kT];
+      Frag f[O::kSplit], kf[KT];
       O::split(xv, f);
 #pragma unroll
-      for (int t = 0; t < kT; ++t) kf[t] = transposed_row(lkt, nbase + 16 * t + l16, 32 * s + 8 * g4);
+      for (int t = 0; t < KT; ++t) kf[t] = transposed_row(lkt, n0 + 16 * t + l16, 32 * s + 8 * g4);
 #pragma unroll
       for (int u = O::kSplit - 1; u >= 0; --u)
 #pragma unroll
-        for (int t = 0; t < kT; ++t) st[t] = O::mma(kf[t], f[u], st[t]);
+        for (int t = 0; t < KT; ++t) st[t] = O::mma(kf[t], f[u], st[t]);
     }
   }
 };
 
 // States only: the state before every block of `keep` chunks (in reversed time:
-// after it), a segment's total, or both.
+// after it), a segment's total, or both.  The columns of S are independent, so
+// a workgroup takes kStateCols of them: three workgroups fit a compute unit and
+// fill the chip more evenly than one of twice the size.
 template <typename T, int NT, bool VEC>
-__global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_states_kernel(WalkPair P) {
-  typedef WalkLds<T, NT> L;
+__global__ void __launch_bounds__(kStatesThreads + kWave) scan_states_kernel(WalkPair P) {
+  typedef StatesLds<T> L;
+  constexpr int kParts = NT / kStateCols, KT = kStateCols / 16;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const ScanWalk A = P.w[blockIdx.y];
-  Walk<T, NT, VEC> W(A);
+  const int block = xcd_item(blockIdx.x, gridDim.x), part = block % kParts;
+  Walk<T, NT, KT> W(A, block / kParts);
+  W.nbase = kStateCols * part;
   if (A.totals && W.seg + 1 == A.nseg) return;   // nothing starts after the last segment
   T* lkt = reinterpret_cast<T*>(lds + L::kt);
   T* lxt = reinterpret_cast<T*>(lds + L::xt);
   Gates<kQ>* gates = reinterpret_cast<Gates<kQ>*>(lds + L::gates);
+  if (W.w == kStatesWaves) {
+    W.template gate_wave<2>(gates);
+    return;
+  }
   const T* xp = static_cast<const T*>(A.x.p) + W.bi * A.x.sb + W.h * A.x.sh + W.pb * kPB;
-  const T* kp = static_cast<const T*>(A.k.p) + W.bi * A.k.sb + W.grp * A.k.sh;
-  PairLoad<T, NT, kWalkThreads, VEC> tk;
-  PairLoad<T, kPB, kWalkThreads, VEC> tx;
+  const T* kp = static_cast<const T*>(A.k.p) + W.bi * A.k.sb + W.grp * A.k.sh + W.nbase;
+  PairLoad<T, kStateCols, kStatesThreads, VEC> tk;
+  PairLoad<T, kPB, kStatesThreads, VEC> tx;
   const auto load_tiles = [&](int cc) {
     const int rows = W.rows_of(cc);
     const long long t0 = W.token_of(cc);
-    tk.load(kp + t0 * A.k.st, A.k.st, rows, A.N, W.tid);
+    tk.load(kp + t0 * A.k.st, A.k.st, rows, A.N - W.nbase, W.tid);
     tx.load(xp + t0 * A.x.st, A.x.st, rows, W.rows_p, W.tid);
   };
   W.load_state();
   float* states = A.states == nullptr ? nullptr : A.states + W.vrow * A.nblocks * (kPB * NT);
-  double seg_log = 0.0;
   load_tiles(W.cc0);
-  if (W.w == 7) {
-    W.load_gates(W.cc0);
-    seg_log += write_gates(gates[0], W.gv, W.bv, W.lane, W.reverse);
-    W.load_gates(W.cc0 + 1);
-  }
   for (int cc = W.cc0; cc < W.cc1; ++cc) {
-    const int slot = (cc - W.cc0) & 1;
     __syncthreads();   // the last chunk's tiles are done with
     tk.store_transposed(lkt, W.tid);
     tx.store_transposed(lxt, W.tid);
@@ -216,32 +239,30 @@ __global__ void __launch_bounds__(kWalkThreads, sizeof(T) == 2 ? 4 : 2) scan_sta
         (W.reverse ? chunk % A.keep == A.keep - 1 || chunk == W.last_chunk : chunk % A.keep == 0)) {
       float* sp = states + static_cast<long long>(chunk / A.keep) * (kPB * NT) + state_offset(W.nbase + 4 * W.g4, 16 * W.pw + W.l16);
 #pragma unroll
-      for (int t = 0; t < W.kT; ++t)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) sp[t * (kPB / 32) * 512 + r * 8] = W.st[t][r];
     }
-    if (W.w == 7) {
-      const double e = write_gates(gates[slot ^ 1], W.gv, W.bv, W.lane, W.reverse);   // past the end: 0
-      seg_log += e;
-      W.load_gates(cc + 2);
-    }
-    W.update(gates[slot], lkt, lxt);
+    W.update(gates[(cc - W.cc0) & 1], lkt, 0, lxt);
   }
-  W.store_state(seg_log);
+  W.store_state();
 }
 
 // Outputs and states.  The tokens' products with the two halves of n are
 // partial sums of y, which the two waves of the same rows exchange through LDS,
 // each finishing half of the tokens.
 template <typename T, int NT, bool VEC>
-__global__ void __launch_bounds__(kWalkThreads, 2) scan_read_kernel(WalkPair P) {
+__global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(WalkPair P) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
-  typedef WalkLds<T, NT> L;
+  typedef ReadLds<T, NT> L;
+  constexpr int KT = NT / 32;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const ScanWalk A = P.w[0];
-  Walk<T, NT, VEC> W(A);
-  const int tid = W.tid, lane = W.lane, w = W.w, l16 = W.l16, g4 = W.g4, pw = W.pw, nh = W.nh, nbase = W.nbase;
+  Walk<T, NT, KT> W(A, xcd_item(blockIdx.x, gridDim.x));
+  // wave w of eight: rows 16 (w % 4) + 0..15, the columns of half w / 4
+  const int tid = W.tid, lane = W.lane, w = W.w, l16 = W.l16, g4 = W.g4, pw = W.pw, nh = w >> 2, nbase = nh * (NT / 2);
+  W.nbase = nbase;
   T* lkt = reinterpret_cast<T*>(lds + L::kt);
   T* lxt = reinterpret_cast<T*>(lds + L::xt);
   T* lk = reinterpret_cast<T*>(lds + L::k);
@@ -249,15 +270,19 @@ __global__ void __launch_bounds__(kWalkThreads, 2) scan_read_kernel(WalkPair P) 
   T* lm = reinterpret_cast<T*>(lds + L::m);
   f32x4_t* ly = reinterpret_cast<f32x4_t*>(lds + L::y);
   Gates<kQ>* gates = reinterpret_cast<Gates<kQ>*>(lds + L::gates);
+  if (w == kReadWaves) {
+    W.template gate_wave<3>(gates);
+    return;
+  }
   const T* xp = static_cast<const T*>(A.x.p) + W.bi * A.x.sb + W.h * A.x.sh + W.pb * kPB;
   const T* kp = static_cast<const T*>(A.k.p) + W.bi * A.k.sb + W.grp * A.k.sh;
   const T* qp = static_cast<const T*>(A.q.p) + W.bi * A.q.sb + W.grp * A.q.sh;
   T* yp = static_cast<T*>(A.y) + (W.bi * A.tokens * A.heads + W.h) * A.P + W.pb * kPB;
   const long long yst = static_cast<long long>(A.heads) * A.P;
 
-  PairLoad<T, NT, kWalkThreads, VEC> tk;
-  PairLoad<T, kPB, kWalkThreads, VEC> tx;
-  TileLoad<T, NT, kQ, kWalkThreads, VEC> tq;
+  PairLoad<T, NT, kReadThreads, VEC> tk;
+  PairLoad<T, kPB, kReadThreads, VEC> tx;
+  TileLoad<T, NT, kQ, kReadThreads, VEC> tq;
   const auto load_tiles = [&](int cc) {
     const int rows = W.rows_of(cc);
     const long long t0 = W.token_of(cc);
@@ -275,14 +300,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) scan_read_kernel(WalkPair P) 
     for (int e = 0; e < 4; ++e) lm[(r0 + l16) * L::kLdM + c0 + 4 * g4 + e] = O::from_f32(0.0f);
   }
   load_tiles(W.cc0);
-  if (w == 7) {
-    W.load_gates(W.cc0);
-    write_gates(gates[0], W.gv, W.bv, lane, false);
-    W.load_gates(W.cc0 + 1);
-  }
   for (int cc = W.cc0; cc < W.cc1; ++cc) {
-    const int slot = (cc - W.cc0) & 1;
-    const Gates<kQ>& G = gates[slot];
+    const Gates<kQ>& G = gates[(cc - W.cc0) & 1];
     __syncthreads();   // the last chunk's tiles are done with
     tk.store(lk, tid);
     tk.store_transposed(lkt, tid);
@@ -290,11 +309,11 @@ __global__ void __launch_bounds__(kWalkThreads, 2) scan_read_kernel(WalkPair P) 
     tx.store_transposed(lxt, tid);
     __syncthreads();
     load_tiles(cc + 1);
-    // tiles of M.  Ten for seven waves: the last one has the next chunk's gates to prepare.
+    // the ten tiles of M
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int e = w + 7 * u;
-      if (w < 7 && e < 10) {
+      const int e = w + 8 * u;
+      if (e < 10) {
         const int it = tile_row(e), jt = tile_col(e, it);
         f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -306,16 +325,12 @@ __global__ void __launch_bounds__(kWalkThreads, 2) scan_read_kernel(WalkPair P) 
         for (int r = 0; r < 4; ++r) lm[(i0 + r) * L::kLdM + j] = O::from_f32(a[r]);
       }
     }
-    if (w == 7) {
-      write_gates(gates[slot ^ 1], W.gv, W.bv, lane, false);
-      W.load_gates(cc + 2);
-    }
     // what this half of S_in gives, e^{c_i} S_in q_i: y^T rows p = 16 pw + 4 g4 + 0..3, column i = 16 it + l16
     f32x4_t y[4];
 #pragma unroll
     for (int it = 0; it < 4; ++it) y[it] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int s = 0; s < W.kT / 2; ++s) {
+    for (int s = 0; s < KT / 2; ++s) {
       const Frag f = frag_from_acc<T>(W.st[2 * s], W.st[2 * s + 1]);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
@@ -331,7 +346,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) scan_read_kernel(WalkPair P) 
       ly[(w * 2 + u) * 64 + lane] = nh == 0 ? y[2 + u] : y[u];
       y[u] = nh == 0 ? y[u] : y[2 + u];
     }
-    W.update(G, lkt, lxt);
+    W.update(G, lkt, nbase, lxt);
     __syncthreads();   // M and the halves of y are written
     // what the chunk's own tokens give
 #pragma unroll
@@ -347,7 +362,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) scan_read_kernel(WalkPair P) 
 #pragma unroll
     for (int u = 0; u < 2; ++u) out.put(32 * nh + 16 * u + l16, 16 * pw + 4 * g4, y[u]);
   }
-  W.store_state(0.0);
+  W.store_state();
 }
 
 // The state that each segment starts from, out of the segments' own totals
@@ -375,13 +390,13 @@ __global__ void __launch_bounds__(kStepThreads) scan_segments_kernel(WalkPair W,
 template <typename T, int NT, bool READ, bool VEC>
 hipError_t walk(const WalkPair& W, int dirs, hipStream_t st) {
   const ScanWalk& a = W.w[0];
-  constexpr int bytes = READ ? WalkLds<T, NT>::read_bytes : WalkLds<T, NT>::states_bytes;
-  static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
+  constexpr int bytes = READ ? ReadLds<T, NT>::bytes : StatesLds<T>::bytes, parts = READ ? 1 : NT / kStateCols;
   const auto kernel = READ ? scan_read_kernel<T, NT, VEC> : scan_states_kernel<T, NT, VEC>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
-  const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg;
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items), dirs), dim3(kWalkThreads), bytes, st, W);
+  const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg * parts;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items), dirs), dim3((READ ? kReadThreads : kStatesThreads) + kWave), bytes,
+                     st, W);
   return hipGetLastError();
 }
 

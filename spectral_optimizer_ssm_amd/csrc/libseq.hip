@@ -99,7 +99,7 @@ int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
   p->nsplit = static_cast<int>(std::min<long long>(a->heads / a->groups, std::max<long long>(1, kGradFill / groups)));
   const int per_split = (a->heads / a->groups + p->nsplit - 1) / p->nsplit;
   p->nsplit = (a->heads / a->groups + per_split - 1) / per_split;   // none without heads
-  if (vrows * p->nseg > INT_MAX || groups * p->nsplit > INT_MAX) return MUON_EUNSUPPORTED;
+  if (2 * vrows * p->nseg > INT_MAX || groups * p->nsplit > INT_MAX) return MUON_EUNSUPPORTED;
   const size_t tile = static_cast<size_t>(kScanRows) * scan_padded_n(a->N) * sizeof(float);
   size_t off = 0;
   const auto take = [&](size_t bytes) {
