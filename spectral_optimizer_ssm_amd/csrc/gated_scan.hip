@@ -41,8 +41,8 @@ struct ReadLds {
   static constexpr int kLdN = NT + Ops<T>::kPad;
   static constexpr int kLdM = kQ + Ops<T>::kPad;
   static constexpr int kt = 0;                                  // k^T [NT][kQ]
-  static constexpr int xt = kt + NT * kLdM * (int)sizeof(T);    // x^T [kPB][kQ]
-  static constexpr int gates = xt + kPB * kLdM * (int)sizeof(T);   // Gates[2]
+  static constexpr int xt = kt + NT * kQ * (int)sizeof(T);    // x^T [kPB][kQ]
+  static constexpr int gates = xt + kPB * kQ * (int)sizeof(T);   // Gates[2]
   static constexpr int k = gates + 2 * (int)sizeof(Gates<kQ>);  // k [kQ][NT]
   static constexpr int q = k + kQ * kLdN * (int)sizeof(T);      // q [kQ][NT]
   static constexpr int m = q + kQ * kLdN * (int)sizeof(T);      // weights M [i][j]
@@ -52,10 +52,9 @@ struct ReadLds {
 };
 template <typename T>
 struct StatesLds {
-  static constexpr int kLdM = kQ + Ops<T>::kPad;
-  static constexpr int kt = 0;                                         // k^T [kStateCols][kQ]
-  static constexpr int xt = kt + kStateCols * kLdM * (int)sizeof(T);   // x^T [kPB][kQ]
-  static constexpr int gates = xt + kPB * kLdM * (int)sizeof(T);       // Gates[2]
+  static constexpr int kt = 0;                                  // k^T [kStateCols][kQ]
+  static constexpr int xt = kt + kStateCols * kQ * (int)sizeof(T);   // x^T [kPB][kQ]
+  static constexpr int gates = xt + kPB * kQ * (int)sizeof(T);       // Gates[2]
   static constexpr int bytes = gates + 2 * (int)sizeof(Gates<kQ>);
 };
 
@@ -199,7 +198,7 @@ struct Walk {
 // a workgroup takes kStateCols of them: three workgroups fit a compute unit and
 // fill the chip more evenly than one of twice the size.
 template <typename T, int NT, bool VEC>
-__global__ void __launch_bounds__(kStatesThreads + kWave) scan_states_kernel(WalkPair P) {
+__global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 ? 5 : 3) scan_states_kernel(WalkPair P) {
   typedef StatesLds<T> L;
   constexpr int kParts = NT / kStateCols, KT = kStateCols / 16;
   extern __shared__ __attribute__((aligned(16))) char lds[];

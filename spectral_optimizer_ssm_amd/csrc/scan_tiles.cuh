@@ -223,11 +223,17 @@ struct TileLoad {
   }
 };
 
+// The 16-byte pieces of row n of a transposed tile [WIDTH][kQ] are permuted by
+// XOR with this.  16 rows, that a fragment reads at once, cover all LDS banks,
+// and so do the rows 8 (float32: 4) apart that half a wave writes at once.
+template <typename T>
+__device__ __forceinline__ constexpr int pieces_order(int n) {
+  return sizeof(T) == 2 ? ((n >> 1) ^ (n >> 4)) & 7 : (n ^ ((n >> 4) & 3)) & 15;
+}
+
 // A [kQ][WIDTH] tile that is (also) needed transposed: a thread holds the same
 // 16-byte columns of two neighbouring tokens, so that it writes both tokens of
-// a transposed row at once.  The transposed tile [WIDTH][kQ] keeps row n's
-// 16-byte pieces in the order piece ^ (n / kVec % 8): the threads of a wave
-// write 16 rows that lie 8 apart, which would otherwise be one bank.
+// a transposed row at once.
 template <typename T, int WIDTH, int THREADS, bool VEC>
 struct PairLoad {
   static constexpr int kVec = Ops<T>::kVec;
@@ -235,17 +241,24 @@ struct PairLoad {
   static constexpr int kAll = kQ / 2 * kRowPieces;
   static constexpr int kPairs = (kAll + THREADS - 1) / THREADS;
   static constexpr int kLd = WIDTH + Ops<T>::kPad;
-  static constexpr int kLdT = kQ + Ops<T>::kPad;
+  // half a wave: kNear pieces of 32 / kNear pairs of tokens
+  static constexpr int kNear = sizeof(T) == 2 ? 8 : 16;
+  static_assert(kRowPieces % kNear == 0, "whole half waves");
   u32x4_t r[kPairs][2];
+
+  static __device__ __forceinline__ int piece_of(int idx) { return idx % kNear + kNear * (idx / 32 % (kRowPieces / kNear)); }
+  static __device__ __forceinline__ int pair_of(int idx) {
+    return idx % 32 / kNear + 32 / kNear * (idx / 32 / (kRowPieces / kNear));
+  }
 
   __device__ __forceinline__ void load(const T* p, long long st, int rows, int width, int tid) {
     const __amdgpu_buffer_rsrc_t b = rsrc(p, VEC ? static_cast<int>(rows * st) * static_cast<int>(sizeof(T)) : 0);
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const int idx = i * THREADS + tid, col = (idx % kRowPieces) * kVec;
+      const int idx = i * THREADS + tid, col = piece_of(idx) * kVec;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int row = 2 * (idx / kRowPieces) + u;   // past the tile's rows: past `rows` too
+        const int row = 2 * pair_of(idx) + u;   // past the tile's rows: past `rows` too
         if constexpr (VEC) {
           const int off = (row * static_cast<int>(st) + col) * static_cast<int>(sizeof(T));
           r[i][u] = __builtin_amdgcn_raw_buffer_load_b128(b, col < width && idx < kAll ? off : kNowhere, 0, 0);
@@ -266,28 +279,30 @@ struct PairLoad {
   __device__ __forceinline__ void store(T* lds, int tid) const {
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const int idx = i * THREADS + tid, col = (idx % kRowPieces) * kVec;
+      const int idx = i * THREADS + tid, col = piece_of(idx) * kVec;
       if (kAll % THREADS != 0 && idx >= kAll) return;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) *reinterpret_cast<u32x4_t*>(lds + (2 * (idx / kRowPieces) + u) * kLd + col) = r[i][u];
+      for (int u = 0; u < 2; ++u) *reinterpret_cast<u32x4_t*>(lds + (2 * pair_of(idx) + u) * kLd + col) = r[i][u];
     }
   }
   __device__ __forceinline__ void store_transposed(T* lds, int tid) const {
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const int idx = i * THREADS + tid, piece = idx % kRowPieces, j = 2 * (idx / kRowPieces);
+      const int idx = i * THREADS + tid, piece = piece_of(idx), j = 2 * pair_of(idx);
       if (kAll % THREADS != 0 && idx >= kAll) return;
-      T* p = lds + piece * kVec * kLdT + ((j / kVec) ^ (piece & 7)) * kVec + j % kVec;
+      T* p = lds + piece * kVec * kQ + j % kVec;
+      const int c = (j / kVec) ^ pieces_order<T>(piece * kVec);
       if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t a = r[i][0][e], b = r[i][1][e];
-          *reinterpret_cast<uint32_t*>(p + (2 * e) * kLdT) = (a & 0xffffu) | (b << 16);
-          *reinterpret_cast<uint32_t*>(p + (2 * e + 1) * kLdT) = (a >> 16) | (b & 0xffff0000u);
+          T* o = p + 2 * e * kQ + (c ^ e) * kVec;   // rows 2 e and 2 e + 1: pieces_order has e alike
+          *reinterpret_cast<uint32_t*>(o) = (a & 0xffffu) | (b << 16);
+          *reinterpret_cast<uint32_t*>(o + kQ) = (a >> 16) | (b & 0xffff0000u);
         }
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<u32x2_t*>(p + e * kLdT) = u32x2_t{r[i][0][e], r[i][1][e]};
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<u32x2_t*>(p + e * kQ + (c ^ e) * kVec) = u32x2_t{r[i][0][e], r[i][1][e]};
       }
     }
   }
@@ -295,9 +310,9 @@ struct PairLoad {
 // Row n, tokens j0..j0 + 7 (j0 a multiple of 8) of a transposed tile.
 template <typename T>
 __device__ __forceinline__ typename Ops<T>::Frag transposed_row(const T* tile, int n, int j0) {
-  constexpr int kVec = Ops<T>::kVec, kLdT = kQ + Ops<T>::kPad;
-  const T* row = tile + n * kLdT;
-  const int x = (n / kVec) & 7, c = j0 / kVec;
+  constexpr int kVec = Ops<T>::kVec;
+  const T* row = tile + n * kQ;
+  const int x = pieces_order<T>(n), c = j0 / kVec;
   if constexpr (sizeof(T) == 2) return Ops<T>::row(row + (c ^ x) * kVec);
   else return Ops<T>::row2(row + (c ^ x) * kVec, row + ((c + 1) ^ x) * kVec);
 }
