@@ -35,29 +35,6 @@ struct WalkPair {
   ScanWalk w[2];
 };
 
-// LDS of the walk.
-template <typename T, int NT>
-struct ReadLds {
-  static constexpr int kLdN = NT + Ops<T>::kPad;
-  static constexpr int kLdM = kQ + Ops<T>::kPad;
-  static constexpr int kt = 0;                                  // k^T [NT][kQ]
-  static constexpr int xt = kt + NT * kQ * (int)sizeof(T);    // x^T [kPB][kQ]
-  static constexpr int gates = xt + kPB * kQ * (int)sizeof(T);   // Gates[2]
-  static constexpr int k = gates + 2 * (int)sizeof(Gates<kQ>);  // k [kQ][NT]
-  static constexpr int q = k + kQ * kLdN * (int)sizeof(T);      // q [kQ][NT]
-  static constexpr int m = q + kQ * kLdN * (int)sizeof(T);      // weights M [i][j]
-  static constexpr int y = m + kQ * kLdM * (int)sizeof(T);      // halves of y that waves hand over [8][2][64] float4
-  static constexpr int bytes = y + 8 * 2 * 64 * 16;
-  static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
-};
-template <typename T>
-struct StatesLds {
-  static constexpr int kt = 0;                                  // k^T [kStateCols][kQ]
-  static constexpr int xt = kt + kStateCols * kQ * (int)sizeof(T);   // x^T [kPB][kQ]
-  static constexpr int gates = xt + kPB * kQ * (int)sizeof(T);       // Gates[2]
-  static constexpr int bytes = gates + 2 * (int)sizeof(Gates<kQ>);
-};
-
 // One sequence (segment), head and block of kPB state rows.  A wave holds rows
 // p = 16 pw + 0..15 of S and KT 16-column tiles from column nbase.
 template <typename T, int NT, int KT>
@@ -199,17 +176,14 @@ struct Walk {
 // fill the chip more evenly than one of twice the size.
 template <typename T, int NT, bool VEC>
 __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 ? 5 : 3) scan_states_kernel(WalkPair P) {
-  typedef StatesLds<T> L;
   constexpr int kParts = NT / kStateCols, KT = kStateCols / 16;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
+  __shared__ __attribute__((aligned(16))) T lkt[kStateCols * kQ], lxt[kPB * kQ];   // k^T, x^T
+  __shared__ Gates<kQ> gates[2];
   const ScanWalk A = P.w[blockIdx.y];
   const int block = xcd_item(blockIdx.x, gridDim.x), part = block % kParts;
   Walk<T, NT, KT> W(A, block / kParts);
   W.nbase = kStateCols * part;
   if (A.totals && W.seg + 1 == A.nseg) return;   // nothing starts after the last segment
-  T* lkt = reinterpret_cast<T*>(lds + L::kt);
-  T* lxt = reinterpret_cast<T*>(lds + L::xt);
-  Gates<kQ>* gates = reinterpret_cast<Gates<kQ>*>(lds + L::gates);
   if (W.w == kStatesWaves) {
     W.template gate_wave<2>(gates);
     return;
@@ -254,21 +228,19 @@ template <typename T, int NT, bool VEC>
 __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(WalkPair P) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
-  typedef ReadLds<T, NT> L;
+  typedef Tile<T, NT> TN;
+  typedef Tile<T, kQ> TM;
   constexpr int KT = NT / 32;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
+  // arrays of their own: the compiler may move reads of one across writes to another
+  __shared__ __attribute__((aligned(16))) T lkt[NT * kQ], lxt[kPB * kQ], lk[kQ * NT], lq[kQ * NT];
+  __shared__ __attribute__((aligned(16))) T lm[kQ * kQ];                     // the weights M [i][j]
+  __shared__ f32x4_t ly[kReadWaves * 2 * kWave];   // halves of y that waves hand over
+  __shared__ Gates<kQ> gates[2];
   const ScanWalk A = P.w[0];
   Walk<T, NT, KT> W(A, xcd_item(blockIdx.x, gridDim.x));
   // wave w of eight: rows 16 (w % 4) + 0..15, the columns of half w / 4
   const int tid = W.tid, lane = W.lane, w = W.w, l16 = W.l16, g4 = W.g4, pw = W.pw, nh = w >> 2, nbase = nh * (NT / 2);
   W.nbase = nbase;
-  T* lkt = reinterpret_cast<T*>(lds + L::kt);
-  T* lxt = reinterpret_cast<T*>(lds + L::xt);
-  T* lk = reinterpret_cast<T*>(lds + L::k);
-  T* lq = reinterpret_cast<T*>(lds + L::q);
-  T* lm = reinterpret_cast<T*>(lds + L::m);
-  f32x4_t* ly = reinterpret_cast<f32x4_t*>(lds + L::y);
-  Gates<kQ>* gates = reinterpret_cast<Gates<kQ>*>(lds + L::gates);
   if (w == kReadWaves) {
     W.template gate_wave<3>(gates);
     return;
@@ -296,7 +268,7 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
   if (w < 2) {
     const int r0 = 32 * w, c0 = r0 + 16;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) lm[(r0 + l16) * L::kLdM + c0 + 4 * g4 + e] = O::from_f32(0.0f);
+    for (int e = 0; e < 4; ++e) lm[TM::at(r0 + l16, c0 + 4 * g4 + e)] = O::from_f32(0.0f);
   }
   load_tiles(W.cc0);
   for (int cc = W.cc0; cc < W.cc1; ++cc) {
@@ -317,11 +289,11 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
         f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < NT / 32; ++s)
-          a = O::mma(O::row(lq + (16 * it + l16) * L::kLdN + 32 * s + 8 * g4), O::row(lk + (16 * jt + l16) * L::kLdN + 32 * s + 8 * g4), a);
+          a = O::mma(TN::row(lq, 16 * it + l16, 32 * s + 8 * g4), TN::row(lk, 16 * jt + l16, 32 * s + 8 * g4), a);
         const int i0 = 16 * it + 4 * g4, j = 16 * jt + l16;
         a *= between4(G, it, jt, i0, j) * G.b[j];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) lm[(i0 + r) * L::kLdM + j] = O::from_f32(a[r]);
+        for (int r = 0; r < 4; ++r) lm[TM::at(i0 + r, j)] = O::from_f32(a[r]);
       }
     }
     // what this half of S_in gives, e^{c_i} S_in q_i: y^T rows p = 16 pw + 4 g4 + 0..3, column i = 16 it + l16
@@ -333,8 +305,7 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
       const Frag f = frag_from_acc<T>(W.st[2 * s], W.st[2 * s + 1]);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const T* qr = lq + (16 * it + l16) * L::kLdN + nbase + 32 * s + 4 * g4;
-        y[it] = O::mma(f, O::row2(qr, qr + 16), y[it]);
+        y[it] = O::mma(f, TN::template row2<16>(lq, 16 * it + l16, nbase + 32 * s + 4 * g4), y[it]);
       }
     }
 #pragma unroll
@@ -355,7 +326,7 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
       if (s <= nh) {
         const Frag vf = transposed_row(lxt, 16 * pw + l16, 32 * s + 8 * g4);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) y[u] = O::mma(vf, O::row(lm + (32 * nh + 16 * u + l16) * L::kLdM + 32 * s + 8 * g4), y[u]);
+        for (int u = 0; u < 2; ++u) y[u] = O::mma(vf, TM::row(lm, 32 * nh + 16 * u + l16, 32 * s + 8 * g4), y[u]);
       }
     const TileStore<T, VEC> out(yp + W.token_of(cc) * yst, yst, W.rows_of(cc), W.rows_p);
 #pragma unroll
@@ -389,13 +360,10 @@ __global__ void __launch_bounds__(kStepThreads) scan_segments_kernel(WalkPair W,
 template <typename T, int NT, bool READ, bool VEC>
 hipError_t walk(const WalkPair& W, int dirs, hipStream_t st) {
   const ScanWalk& a = W.w[0];
-  constexpr int bytes = READ ? ReadLds<T, NT>::bytes : StatesLds<T>::bytes, parts = READ ? 1 : NT / kStateCols;
+  constexpr int parts = READ ? 1 : NT / kStateCols, threads = (READ ? kReadThreads : kStatesThreads) + kWave;
   const auto kernel = READ ? scan_read_kernel<T, NT, VEC> : scan_states_kernel<T, NT, VEC>;
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != hipSuccess) return e;
   const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg * parts;
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items), dirs), dim3((READ ? kReadThreads : kStatesThreads) + kWave), bytes,
-                     st, W);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items), dirs), dim3(threads), 0, st, W);
   return hipGetLastError();
 }
 

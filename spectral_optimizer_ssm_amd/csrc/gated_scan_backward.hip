@@ -35,16 +35,13 @@ using namespace scan;
 // with float32 ones, whose tiles fill the LDS of a compute unit.
 template <typename T, int NT, int Q>
 struct GradLds {
-  static constexpr int kLdN = NT + Ops<T>::kPad;
-  static constexpr int kLdP = kPB + Ops<T>::kPad;
-  static constexpr int kLdM = Q + Ops<T>::kPad;
   static constexpr int kTiles = Q / 16;                           // token tiles, and waves
   static constexpr int q = 0;                                     // [Q][NT]
-  static constexpr int k = q + Q * kLdN * (int)sizeof(T);         // [Q][NT]
-  static constexpr int v = k + Q * kLdN * (int)sizeof(T);         // [Q][kPB]
-  static constexpr int dy = v + Q * kLdP * (int)sizeof(T);        // [Q][kPB]; v and dy at the end: D [i][j]
-  static constexpr int m = dy + Q * kLdP * (int)sizeof(T);        // (L A)^T [j][i]; at the end D^T
-  static constexpr int gates = m + Q * kLdM * (int)sizeof(T);     // Gates
+  static constexpr int k = q + Q * NT * (int)sizeof(T);         // [Q][NT]
+  static constexpr int v = k + Q * NT * (int)sizeof(T);         // [Q][kPB]
+  static constexpr int dy = v + Q * kPB * (int)sizeof(T);        // [Q][kPB]; v and dy at the end: D [i][j]
+  static constexpr int m = dy + Q * kPB * (int)sizeof(T);        // (L A)^T [j][i]; at the end D^T
+  static constexpr int gates = m + Q * Q * (int)sizeof(T);     // Gates
   static constexpr int rows = gates + (int)sizeof(Gates<Q>);      // row sums of W by column tile
   static constexpr int cols = rows + kTiles * Q * 4;              // column sums of L A E by row tile
   static constexpr int qs = cols + kTiles * Q * 4;                // e^{c_i} q_i . S_in^T dy_i by block of n
@@ -55,9 +52,9 @@ struct GradLds {
   static constexpr int dgate = leave + Q * 4;                     //   and db
   static constexpr int bytes = dgate + Q * 4;
   // dS_out [n][p] as the operand of dv goes where v was, if it fits
-  static constexpr bool kStateInV = NT * kLdP <= Q * kLdP;
+  static constexpr bool kStateInV = NT <= Q;
   static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
-  static_assert(kLdM <= 2 * kLdP, "D fits where v and dy were");
+  static_assert(Q <= 2 * kPB, "D fits where v and dy were");
 };
 
 template <typename T, int NT, int Q, bool VEC>
@@ -65,6 +62,9 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
   typedef GradLds<T, NT, Q> L;
+  typedef Tile<T, NT> TN;
+  typedef Tile<T, kPB> TP;
+  typedef Tile<T, Q> TM;
   constexpr int kThreads = 4 * Q, kTiles = L::kTiles, kU = Q / 64;
   // the tiles on and below the diagonal, dealt to the waves in runs
   constexpr int kAll = kTiles * (kTiles + 1) / 2, kMaxTiles = (kAll + kTiles - 1) / kTiles;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     load_columns(A.dstates + state_at(0), kPB * NT * 4, lane, y);
   }
   // tiles of (L A)^T and slots of the sums that no wave writes
-  for (int i = tid; i < Q * L::kLdM; i += kThreads) lm[i] = O::from_f32(0.0f);
+  for (int i = tid; i < Q * Q; i += kThreads) lm[i] = O::from_f32(0.0f);
   for (int i = tid; i < 4 * kTiles * Q; i += kThreads) lrow[i] = 0.0f;
   __syncthreads();
 
@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     sc[t] = dsum[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < NT / 32; ++s)
-        sc[t] = O::mma(O::row(lq + (16 * trow[t] + l16) * L::kLdN + 32 * s + 8 * g4),
-                       O::row(lk + (16 * tcol[t] + l16) * L::kLdN + 32 * s + 8 * g4), sc[t]);
+        sc[t] = O::mma(TN::row(lq, 16 * trow[t] + l16, 32 * s + 8 * g4),
+                       TN::row(lk, 16 * tcol[t] + l16, 32 * s + 8 * g4), sc[t]);
   }
   // dq^T and dk^T: rows n = 16 (nw0 + b) + 4 g4 + 0..3, column i (j) = 16 (u kTG + tg) + l16
   f32x4_t dq[kNW][kTT], dk[kNW][kTT];
@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
         f32x4_t e = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < kPB / 32; ++s)
-          e = O::mma(O::row(ldy + (16 * it + l16) * L::kLdP + 32 * s + 8 * g4),
-                     O::row(lv + (16 * jt + l16) * L::kLdP + 32 * s + 8 * g4), e);
+          e = O::mma(TP::row(ldy, 16 * it + l16, 32 * s + 8 * g4),
+                     TP::row(lv, 16 * jt + l16, 32 * s + 8 * g4), e);
         const int j = 16 * jt + l16, i0 = 16 * it + 4 * g4;
         const float b = G.b[j];
         const f32x4_t d = between4(G, it, jt, i0, j);
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
           cols[t] += we;
           rs[r] = we * b;
         }
-        O::store4(lm + j * L::kLdM + i0, mm);
+        TM::store4(lm, j, i0, mm);
         const float row = sum_lanes4(rs[0], rs[1], rs[2], rs[3], l16);
         if (l16 < 4) lrow[jt * Q + i0 + l16] = row;
         settle(dsum[t]);
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
           for (int s = 0; s < kPB / 32; ++s) {
             Frag d[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) d[u] = O::row(tile + (16 * ((u0 + u) * kTG + tg) + l16) * L::kLdP + 32 * s + 8 * g4);
+            for (int u = 0; u < 4; ++u) d[u] = TP::row(tile, 16 * ((u0 + u) * kTG + tg) + l16, 32 * s + 8 * g4);
 #pragma unroll
             for (int z = O::kSplit - 1; z >= 0; --z)
 #pragma unroll
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
           for (int u = 0; u < 4; ++u) {
             const int t = 16 * ((u0 + u) * kTG + tg) + l16;
             const float sv = scale[t], gt = gated ? G.b[t] : 1.0f;
-            const f32x4_t ov = O::load4(other + t * L::kLdN + 16 * (nw0 + b) + 4 * g4);
+            const f32x4_t ov = TN::load4(other, t, 16 * (nw0 + b) + 4 * g4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float a = acc[u][r] * sv;
@@ -316,8 +316,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
           for (int b = 0; b < kNW; ++b)
 #pragma unroll
             for (int s = 0; s < kPB / 32; ++s) {
-              T* p = lv + (16 * (nw0 + b) + l16) * L::kLdP + 32 * s + 8 * g4;   // the first of its pieces
-              *reinterpret_cast<Frag*>(p) = f[b][s][0];
+              TP::store8(lv, 16 * (nw0 + b) + l16, 32 * s + 8 * g4, f[b][s][0]);   // the first of its pieces
             }
       }
       // the next head's tiles and states
@@ -351,12 +350,12 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
       for (int u = 0; u < 4; ++u) z[u] = zs[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int s = 0; s < Q / 32; ++s) {
-        const Frag f = O::col(ldy, L::kLdP, 32 * s, 16 * (w & 3), lane);
+        const Frag f = TP::col(ldy, 32 * s, 16 * (w & 3), lane);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int jt = kZG * u + (w >> 2);
           if (s >= kZG * u / 2)   // jt / 2: tiles above the diagonal are zero
-            z[u] = O::mma(f, O::row(lm + (16 * jt + l16) * L::kLdM + 32 * s + 8 * g4), z[u]);
+            z[u] = O::mma(f, TM::row(lm, 16 * jt + l16, 32 * s + 8 * g4), z[u]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -365,7 +364,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
       for (int s = 0; s < NT / 32; ++s) {
         Frag f;
         if constexpr (L::kStateInV) {
-          f = O::col(lv, L::kLdP, 32 * s, 16 * (w & 3), lane);
+          f = TP::col(lv, 32 * s, 16 * (w & 3), lane);
         } else {
           float v[8];
 #pragma unroll
@@ -374,7 +373,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          zs[u] = O::mma(f, O::row(lk + (16 * (kZG * u + (w >> 2)) + l16) * L::kLdN + 32 * s + 8 * g4), zs[u]);
+          zs[u] = O::mma(f, TN::row(lk, 16 * (kZG * u + (w >> 2)) + l16, 32 * s + 8 * g4), zs[u]);
       }
       const TileStore<T, VEC> out(static_cast<T*>(A.dv) + ((bi * A.tokens + t0) * A.heads + h) * A.P + pb * kPB,
                                   static_cast<long long>(A.heads) * A.P, rows, rows_p_of(pb));
@@ -421,15 +420,15 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
   // D = sum over heads of L b E, once as D [i][j] (where v and dy were) and
   // once as D^T [j][i] (where (L A)^T was, whose other tiles are zero)
   T* ld = lv;
-  for (int i = tid; i < Q * L::kLdM; i += kThreads) ld[i] = O::from_f32(0.0f);
+  for (int i = tid; i < Q * Q; i += kThreads) ld[i] = O::from_f32(0.0f);
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < kMaxTiles; ++t) {
     if (t + 1 < kMaxTiles || t < ntile) {
       const int j = 16 * tcol[t] + l16, i0 = 16 * trow[t] + 4 * g4;
-      O::store4(lm + j * L::kLdM + i0, dsum[t]);
+      TM::store4(lm, j, i0, dsum[t]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) ld[(i0 + r) * L::kLdM + j] = O::from_f32(dsum[t][r]);
+      for (int r = 0; r < 4; ++r) ld[TM::at(i0 + r, j)] = O::from_f32(dsum[t][r]);
     }
   }
   __syncthreads();
@@ -438,13 +437,13 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     const int n0 = 16 * (nw0 + b);
 #pragma unroll
     for (int s = 0; s < Q / 32; ++s) {
-      const Frag fk = O::col(lk, L::kLdN, 32 * s, n0, lane), fq = O::col(lq, L::kLdN, 32 * s, n0, lane);
+      const Frag fk = TN::col(lk, 32 * s, n0, lane), fq = TN::col(lq, 32 * s, n0, lane);
 #pragma unroll
       for (int u = 0; u < kTT; ++u) {
         const int it = u * kTG + tg;
         // tiles of D with j > i (of D^T with i < j) are zero
-        if (s <= (u * kTG + kTG - 1) / 2) dq[b][u] = O::mma(fk, O::row(ld + (16 * it + l16) * L::kLdM + 32 * s + 8 * g4), dq[b][u]);
-        if (s >= u * kTG / 2) dk[b][u] = O::mma(fq, O::row(lm + (16 * it + l16) * L::kLdM + 32 * s + 8 * g4), dk[b][u]);
+        if (s <= (u * kTG + kTG - 1) / 2) dq[b][u] = O::mma(fk, TM::row(ld, 16 * it + l16, 32 * s + 8 * g4), dq[b][u]);
+        if (s >= u * kTG / 2) dk[b][u] = O::mma(fq, TM::row(lm, 16 * it + l16, 32 * s + 8 * g4), dk[b][u]);
       }
     }
     const int n = n0 + 4 * g4;

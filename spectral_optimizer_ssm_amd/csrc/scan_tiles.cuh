@@ -34,7 +34,6 @@ template <>
 struct Ops<bf16_t> {
   typedef bf16x8_t Frag;
   static constexpr int kVec = 8;      // elements per 16 bytes
-  static constexpr int kPad = 8;      // elements appended to an LDS row
   static constexpr int kSplit = 3;    // bf16 pieces that carry a float32's 24 bits
   __device__ static __forceinline__ f32x4_t mma(Frag a, Frag b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -47,16 +46,6 @@ struct Ops<bf16_t> {
   __device__ static __forceinline__ Frag row2(const bf16_t* p, const bf16_t* q) {
     const u32x2_t a = *reinterpret_cast<const u32x2_t*>(p), b = *reinterpret_cast<const u32x2_t*>(q);
     return __builtin_bit_cast(Frag, u32x4_t{a[0], a[1], b[0], b[1]});
-  }
-  // column col0 + l % 16 of rows row0 + 8 g + 0..7 (ds_read_b64_tr_b16: in
-  // each 16-lane group the lanes address a 4 x 16 block, 4 elements each, and
-  // receive one column)
-  __device__ static __forceinline__ Frag col(const bf16_t* tile, int ld, int row0, int col0, int lane) {
-    const bf16_t* p = tile + (row0 + 8 * (lane >> 4) + ((lane & 15) >> 2)) * ld + col0 + 4 * (lane & 3);
-    const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p);
-    const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(p + 4 * ld));
-    const u32x2_t ua = __builtin_bit_cast(u32x2_t, a), ub = __builtin_bit_cast(u32x2_t, b);
-    return __builtin_bit_cast(Frag, u32x4_t{ua[0], ua[1], ub[0], ub[1]});
   }
   __device__ static __forceinline__ void widen(Frag f, float (&o)[8]) {
     const u32x4_t w = __builtin_bit_cast(u32x4_t, f);
@@ -98,7 +87,6 @@ template <>
 struct Ops<float> {
   typedef FragF32 Frag;
   static constexpr int kVec = 4;
-  static constexpr int kPad = 4;
   static constexpr int kSplit = 1;
   __device__ static __forceinline__ f32x4_t mma(const Frag& a, const Frag& b, f32x4_t c) {
 #pragma unroll
@@ -108,14 +96,6 @@ struct Ops<float> {
   __device__ static __forceinline__ Frag row2(const float* p, const float* q) {
     const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(q);
     return Frag{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
-  }
-  __device__ static __forceinline__ Frag row(const float* p) { return row2(p, p + 4); }
-  __device__ static __forceinline__ Frag col(const float* tile, int ld, int row0, int col0, int lane) {
-    const float* p = tile + (row0 + 8 * (lane >> 4)) * ld + col0 + (lane & 15);
-    Frag f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f.v[e] = p[e * ld];
-    return f;
   }
   __device__ static __forceinline__ void widen(const Frag& f, float (&o)[8]) {
 #pragma unroll
@@ -131,6 +111,60 @@ struct Ops<float> {
   __device__ static __forceinline__ void store4(float* p, f32x4_t v) { *reinterpret_cast<f32x4_t*>(p) = v; }
   __device__ static __forceinline__ f32x4_t load4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
   __device__ static __forceinline__ float from_f32(float v) { return v; }
+};
+
+// A row-major tile of rows of WIDTH elements in LDS.  The 16-byte pieces of a
+// row are permuted by XOR with its number, so that the 16 rows that a fragment
+// reads at once cover all banks; 128-byte rows, two to a sweep of the banks,
+// take half of it.
+template <typename T, int WIDTH>
+struct Tile {
+  typedef Ops<T> O;
+  typedef typename O::Frag Frag;
+  static constexpr int kVec = O::kVec, kBytes = WIDTH * static_cast<int>(sizeof(T));
+  static_assert(kBytes == 128 || kBytes % 256 == 0, "rows of whole sweeps of the banks, or half a sweep");
+  // of column col; what lies in its 16 bytes is contiguous
+  __device__ static __forceinline__ int at(int row, int col) {
+    const int x = kBytes == 128 ? (row >> 1) & 7 : row & 15;
+    return row * WIDTH + ((col / kVec) ^ x) * kVec + col % kVec;
+  }
+  // 8 elements from column col, a multiple of 8
+  __device__ static __forceinline__ Frag row(const T* tile, int row, int col) {
+    if constexpr (sizeof(T) == 2) return O::row(tile + at(row, col));
+    else return row2(tile, row, col);
+  }
+  // elements col..col + 3 and col + D..col + D + 3
+  template <int D = 4>
+  __device__ static __forceinline__ Frag row2(const T* tile, int row, int col) {
+    return O::row2(tile + at(row, col), tile + at(row, col + D));
+  }
+  __device__ static __forceinline__ void store8(T* tile, int row, int col, Frag f) {
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<Frag*>(tile + at(row, col)) = f;
+    } else {
+      O::store4(tile + at(row, col), f32x4_t{f.v[0], f.v[1], f.v[2], f.v[3]});
+      O::store4(tile + at(row, col + 4), f32x4_t{f.v[4], f.v[5], f.v[6], f.v[7]});
+    }
+  }
+  // column col0 + l % 16 of rows row0 + 8 g + 0..7 (bfloat16: ds_read_b64_tr_b16,
+  // where in each 16-lane group the lanes address a 4 x 16 block, 4 elements
+  // each, and receive one column)
+  __device__ static __forceinline__ Frag col(const T* tile, int row0, int col0, int lane) {
+    if constexpr (sizeof(T) == 2) {
+      const int r = row0 + 8 * (lane >> 4) + ((lane & 15) >> 2), c = col0 + 4 * (lane & 3);
+      const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(tile + at(r, c)));
+      const s16x4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(tile + at(r + 4, c)));
+      const u32x2_t ua = __builtin_bit_cast(u32x2_t, a), ub = __builtin_bit_cast(u32x2_t, b);
+      return __builtin_bit_cast(Frag, u32x4_t{ua[0], ua[1], ub[0], ub[1]});
+    } else {
+      Frag f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f.v[e] = tile[at(row0 + 8 * (lane >> 4) + e, col0 + (lane & 15))];
+      return f;
+    }
+  }
+  __device__ static __forceinline__ f32x4_t load4(const T* tile, int row, int col) { return O::load4(tile + at(row, col)); }
+  __device__ static __forceinline__ void store4(T* tile, int row, int col, f32x4_t v) { O::store4(tile + at(row, col), v); }
 };
 
 // Fragment of a float32 result held in two accumulator tiles (rows 0..15 and
@@ -184,7 +218,6 @@ struct TileLoad {
   static constexpr int kVec = Ops<T>::kVec;
   static constexpr int kRowPieces = WIDTH / kVec;
   static constexpr int kPieces = ROWS * kRowPieces / THREADS;
-  static constexpr int kLd = WIDTH + Ops<T>::kPad;
   static_assert(ROWS * kRowPieces % THREADS == 0, "whole pieces");
   u32x4_t r[kPieces];
 
@@ -218,7 +251,7 @@ struct TileLoad {
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
       const int idx = i * THREADS + tid, row = idx / kRowPieces, col = (idx % kRowPieces) * kVec;
-      *reinterpret_cast<u32x4_t*>(lds + row * kLd + col) = r[i];
+      *reinterpret_cast<u32x4_t*>(lds + Tile<T, WIDTH>::at(row, col)) = r[i];
     }
   }
 };
@@ -240,7 +273,6 @@ struct PairLoad {
   static constexpr int kRowPieces = WIDTH / kVec;
   static constexpr int kAll = kQ / 2 * kRowPieces;
   static constexpr int kPairs = (kAll + THREADS - 1) / THREADS;
-  static constexpr int kLd = WIDTH + Ops<T>::kPad;
   // half a wave: kNear pieces of 32 / kNear pairs of tokens
   static constexpr int kNear = sizeof(T) == 2 ? 8 : 16;
   static_assert(kRowPieces % kNear == 0, "whole half waves");
@@ -282,7 +314,7 @@ struct PairLoad {
       const int idx = i * THREADS + tid, col = piece_of(idx) * kVec;
       if (kAll % THREADS != 0 && idx >= kAll) return;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) *reinterpret_cast<u32x4_t*>(lds + (2 * pair_of(idx) + u) * kLd + col) = r[i][u];
+      for (int u = 0; u < 2; ++u) *reinterpret_cast<u32x4_t*>(lds + Tile<T, WIDTH>::at(2 * pair_of(idx) + u, col)) = r[i][u];
     }
   }
   __device__ __forceinline__ void store_transposed(T* lds, int tid) const {
