@@ -35,6 +35,23 @@ struct WalkPair {
   ScanWalk w[2];
 };
 
+// The gates of a chunk on their way into LDS: a token a lane, past the end no
+// decay and no input.
+struct GateLoad {
+  float g[1], b[1];
+  template <typename W>
+  __device__ __forceinline__ void load(const W& w, int cc) {
+    const ScanWalk& A = w.A;
+    const float* gp = static_cast<const float*>(A.g.p) + w.bi * A.g.sb + w.h * A.g.sh;
+    const float* bp = A.b.p == nullptr ? nullptr : static_cast<const float*>(A.b.p) + w.bi * A.b.sb + w.h * A.b.sh;
+    const int rows = w.rows_of(cc);
+    const long long t = w.token_of(cc) + (w.lane < rows ? w.lane : 0);
+    g[0] = gp[t * A.g.st];
+    b[0] = bp == nullptr ? 1.0f : bp[t * A.b.st];
+    if (w.lane >= rows) g[0] = b[0] = 0.0f;
+  }
+};
+
 // One sequence (segment), head and block of kPB state rows.  A wave holds rows
 // p = 16 pw + 0..15 of S and KT 16-column tiles from column nbase.
 template <typename T, int NT, int KT>
@@ -84,29 +101,17 @@ struct Walk {
   __device__ __forceinline__ int tile_off() const { return (16 * pw + l16) * NT + nbase + 4 * g4; }
 
   // The gate wave's part: gates of every chunk, one ahead of the others, who
-  // meet it at `barriers` barriers a chunk (the gates are needed after the
-  // second).
-  template <int BARRIERS>
+  // meet it at two barriers a chunk (the gates are needed after the second).
   __device__ __forceinline__ void gate_wave(Gates<kQ>* gates) const {
-    const float* gp = static_cast<const float*>(A.g.p) + bi * A.g.sb + h * A.g.sh;
-    const float* bp = A.b.p == nullptr ? nullptr : static_cast<const float*>(A.b.p) + bi * A.b.sb + h * A.b.sh;
-    float gv[1], bv[1];
-    const auto load = [&](int cc) {   // a token a lane (past the end: no decay, no input)
-      const int rows = rows_of(cc);
-      const long long t = token_of(cc) + (lane < rows ? lane : 0);
-      gv[0] = gp[t * A.g.st];
-      bv[0] = bp == nullptr ? 1.0f : bp[t * A.b.st];
-      if (lane >= rows) gv[0] = bv[0] = 0.0f;
-    };
-    load(cc0);
-    double log = write_gates(gates[0], gv, bv, lane, reverse);
-    load(cc0 + 1);
+    GateLoad gl;
+    gl.load(*this, cc0);
+    double log = write_gates(gates[0], gl.g, gl.b, lane, reverse);
+    gl.load(*this, cc0 + 1);
     for (int cc = cc0; cc < cc1; ++cc) {
       __syncthreads();
       __syncthreads();
-      log += write_gates(gates[(cc - cc0 + 1) & 1], gv, bv, lane, reverse);   // past the segment: 0
-      load(cc + 2);
-      if constexpr (BARRIERS > 2) __syncthreads();
+      log += write_gates(gates[(cc - cc0 + 1) & 1], gl.g, gl.b, lane, reverse);   // past the segment: 0
+      gl.load(*this, cc + 2);
     }
     if (A.totals && lane == 0) A.seg_decay[vrow * A.nseg + seg] = __builtin_amdgcn_exp2f(static_cast<float>(log));
   }
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
   W.nbase = kStateCols * part;
   if (A.totals && W.seg + 1 == A.nseg) return;   // nothing starts after the last segment
   if (W.w == kStatesWaves) {
-    W.template gate_wave<2>(gates);
+    W.gate_wave(gates);
     return;
   }
   const T* xp = static_cast<const T*>(A.x.p) + W.bi * A.x.sb + W.h * A.x.sh + W.pb * kPB;
@@ -241,8 +246,34 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
   // wave w of eight: rows 16 (w % 4) + 0..15, the columns of half w / 4
   const int tid = W.tid, lane = W.lane, w = W.w, l16 = W.l16, g4 = W.g4, pw = W.pw, nh = w >> 2, nbase = nh * (NT / 2);
   W.nbase = nbase;
+  // tile e of M, rows i and columns j
+  const auto weights = [&](int e, const Gates<kQ>& G) {
+    const int it = tile_row(e), jt = tile_col(e, it);
+    f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < NT / 32; ++s)
+      a = O::mma(TN::row(lq, 16 * it + l16, 32 * s + 8 * g4), TN::row(lk, 16 * jt + l16, 32 * s + 8 * g4), a);
+    const int i0 = 16 * it + 4 * g4, j = 16 * jt + l16;
+    a *= between4(G, it, jt, i0, j) * G.b[j];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) lm[TM::at(i0 + r, j)] = O::from_f32(a[r]);
+  };
   if (w == kReadWaves) {
-    W.template gate_wave<3>(gates);
+    // the ninth wave: two of the ten tiles of M, then the next chunk's gates
+    GateLoad gl;
+    gl.load(W, W.cc0);
+    write_gates(gates[0], gl.g, gl.b, lane, false);
+    gl.load(W, W.cc0 + 1);
+    for (int cc = W.cc0; cc < W.cc1; ++cc) {
+      const int slot = (cc - W.cc0) & 1;
+      __syncthreads();
+      __syncthreads();
+      weights(kReadWaves, gates[slot]);
+      weights(kReadWaves + 1, gates[slot]);
+      write_gates(gates[slot ^ 1], gl.g, gl.b, lane, false);
+      gl.load(W, cc + 2);
+      __syncthreads();
+    }
     return;
   }
   const T* xp = static_cast<const T*>(A.x.p) + W.bi * A.x.sb + W.h * A.x.sh + W.pb * kPB;
@@ -280,22 +311,7 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
     tx.store_transposed(lxt, tid);
     __syncthreads();
     load_tiles(cc + 1);
-    // the ten tiles of M
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int e = w + 8 * u;
-      if (e < 10) {
-        const int it = tile_row(e), jt = tile_col(e, it);
-        f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < NT / 32; ++s)
-          a = O::mma(TN::row(lq, 16 * it + l16, 32 * s + 8 * g4), TN::row(lk, 16 * jt + l16, 32 * s + 8 * g4), a);
-        const int i0 = 16 * it + 4 * g4, j = 16 * jt + l16;
-        a *= between4(G, it, jt, i0, j) * G.b[j];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) lm[TM::at(i0 + r, j)] = O::from_f32(a[r]);
-      }
-    }
+    weights(w, G);
     // what this half of S_in gives, e^{c_i} S_in q_i: y^T rows p = 16 pw + 4 g4 + 0..3, column i = 16 it + l16
     f32x4_t y[4];
 #pragma unroll
