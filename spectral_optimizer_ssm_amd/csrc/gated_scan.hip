@@ -64,7 +64,7 @@ struct Walk {
   int seg, h, pb, grp, rows_p, cc0, cc1, last_chunk;
   long long bi, vrow;
   bool reverse;
-  // tile t holds S^T rows n = nbase + 16 t + 4 g4 + 0..3, column p = 16 pw + l16
+  // tile t holds S^T rows n = nbase + state_row(t, 4 g4 + 0..3), column p = 16 pw + l16
   f32x4_t st[KT];
 
   __device__ __forceinline__ Walk(const ScanWalk& A, int item) : A(A) {
@@ -98,7 +98,7 @@ struct Walk {
     return cc >= cc1 ? 0 : left < kQ ? static_cast<int>(left) : kQ;
   }
   __device__ __forceinline__ long long token_of(int cc) const { return static_cast<long long>(chunk_of(cc < cc1 ? cc : cc0)) * kQ; }
-  __device__ __forceinline__ int tile_off() const { return (16 * pw + l16) * NT + nbase + 4 * g4; }
+  __device__ __forceinline__ int tile_off(int t) const { return (16 * pw + l16) * NT + nbase + state_row(t, 4 * g4); }
 
   // The gate wave's part: gates of every chunk, one ahead of the others, who
   // meet it at two barriers a chunk (the gates are needed after the second).
@@ -119,9 +119,9 @@ struct Walk {
   __device__ __forceinline__ void load_state() {
     const int prow = pb * kPB + 16 * pw + l16;
     if (A.seg_state != nullptr && !A.totals) {
-      const float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off();
+      const float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT);
 #pragma unroll
-      for (int t = 0; t < KT; ++t) st[t] = *reinterpret_cast<const f32x4_t*>(sp + 16 * t);
+      for (int t = 0; t < KT; ++t) st[t] = *reinterpret_cast<const f32x4_t*>(sp + tile_off(t));
     } else {
       const bool init = A.init != nullptr && !A.totals;
       const float* sp = A.init + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
@@ -129,16 +129,16 @@ struct Walk {
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int n = nbase + 16 * t + 4 * g4 + r;
+          const int n = nbase + state_row(t, 4 * g4) + r;
           st[t][r] = init && prow < A.P && n < A.N ? sp[n] : 0.0f;
         }
     }
   }
   __device__ __forceinline__ void store_state() const {
     if (A.totals) {
-      float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT) + tile_off();
+      float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT);
 #pragma unroll
-      for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4_t*>(sp + 16 * t) = st[t];
+      for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4_t*>(sp + tile_off(t)) = st[t];
     } else if (A.fin != nullptr && cc1 == A.nchunks) {
       const int prow = pb * kPB + 16 * pw + l16;
       float* sp = A.fin + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
@@ -146,32 +146,40 @@ struct Walk {
       for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int n = nbase + 16 * t + 4 * g4 + r;
+          const int n = nbase + state_row(t, 4 * g4) + r;
           if (prow < A.P && n < A.N) sp[n] = st[t][r];
         }
     }
   }
-  // S = e^{c_end} S + sum_j in_j x_j k_j^T; this wave's columns: from row n0 of lkt
-  __device__ __forceinline__ void update(const Gates<kQ>& G, const T* lkt, int n0, const T* lxt) {
+  // S = e^{c_end} S + sum_j in_j x_j k_j^T; this wave's columns: from row n0 of
+  // lkt.  The weighted values, in pieces: `values(s, f)` for tokens 32 s + 0..31.
+  template <typename F>
+  __device__ __forceinline__ void update(const Gates<kQ>& G, const T* lkt, int n0, F values) {
     const float end = G.end[0];
 #pragma unroll
     for (int t = 0; t < KT; ++t) st[t] *= end;
 #pragma unroll
     for (int s = 0; s < kQ / 32; ++s) {
-      float xv[8], wv[8];
-      O::widen(transposed_row(lxt, 16 * pw + l16, 32 * s + 8 * g4), xv);
-      load8(G.in + 32 * s + 8 * g4, wv);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) xv[e] *= wv[e];
       Frag f[O::kSplit], kf[KT];
-      O::split(xv, f);
+      values(s, f);
 #pragma unroll
-      for (int t = 0; t < KT; ++t) kf[t] = transposed_row(lkt, n0 + 16 * t + l16, 32 * s + 8 * g4);
+      for (int t = 0; t < KT; ++t) kf[t] = transposed_row(lkt, n0 + state_row(t, l16), 32 * s + 8 * g4);
 #pragma unroll
       for (int u = O::kSplit - 1; u >= 0; --u)
 #pragma unroll
         for (int t = 0; t < KT; ++t) st[t] = O::mma(kf[t], f[u], st[t]);
     }
+  }
+  // ... weighted and split here
+  __device__ __forceinline__ void update_from(const Gates<kQ>& G, const T* lkt, int n0, const T* lxt) {
+    update(G, lkt, n0, [&](int s, Frag (&f)[O::kSplit]) {
+      float xv[8], wv[8];
+      O::widen(transposed_row(lxt, 16 * pw + l16, 32 * s + 8 * g4), xv);
+      load8(G.in + 32 * s + 8 * g4, wv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) xv[e] *= wv[e];
+      O::split(xv, f);
+    });
   }
 };
 
@@ -215,13 +223,15 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
     const int chunk = W.chunk_of(cc);
     if (states != nullptr &&
         (W.reverse ? chunk % A.keep == A.keep - 1 || chunk == W.last_chunk : chunk % A.keep == 0)) {
-      float* sp = states + static_cast<long long>(chunk / A.keep) * (kPB * NT) + state_offset(W.nbase + 4 * W.g4, 16 * W.pw + W.l16);
+      float* sp = states + static_cast<long long>(chunk / A.keep) * (kPB * NT);
 #pragma unroll
-      for (int t = 0; t < KT; ++t)
+      for (int t = 0; t < KT; ++t) {
+        float* row = sp + state_offset(W.nbase + state_row(t, 4 * W.g4), 16 * W.pw + W.l16);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sp[t * (kPB / 32) * 512 + r * 8] = W.st[t][r];
+        for (int r = 0; r < 4; ++r) row[r * 8] = W.st[t][r];
+      }
     }
-    W.update(gates[(cc - W.cc0) & 1], lkt, 0, lxt);
+    W.update_from(gates[(cc - W.cc0) & 1], lkt, 0, lxt);
   }
   W.store_state();
 }
@@ -237,8 +247,12 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
   typedef Tile<T, kQ> TM;
   constexpr int KT = NT / 32;
   // arrays of their own: the compiler may move reads of one across writes to another
-  __shared__ __attribute__((aligned(16))) T lkt[NT * kQ], lxt[kPB * kQ], lk[kQ * NT], lq[kQ * NT];
-  __shared__ __attribute__((aligned(16))) T lm[kQ * kQ];                     // the weights M [i][j]
+  // bfloat16: the weighted values of a chunk are split once for all waves.
+  // x^T is read last in a chunk, when the next chunk's tiles are stored already.
+  constexpr bool kPlanes = sizeof(T) == 2;
+  __shared__ __attribute__((aligned(16))) T lkt[NT * kQ], lk[kQ * NT], lq[kQ * NT], lxts[kPlanes ? 2 : 1][kPB * kQ];
+  __shared__ __attribute__((aligned(16))) T lxw[kPlanes ? 3 * kPB * kQ : 8];   // weighted x^T in three pieces
+  __shared__ __attribute__((aligned(16))) T lm[kQ * kQ];                       // the weights M [i][j]
   __shared__ f32x4_t ly[kReadWaves * 2 * kWave];   // halves of y that waves hand over
   __shared__ Gates<kQ> gates[2];
   const ScanWalk A = P.w[0];
@@ -264,15 +278,16 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
     gl.load(W, W.cc0);
     write_gates(gates[0], gl.g, gl.b, lane, false);
     gl.load(W, W.cc0 + 1);
+    __syncthreads();
     for (int cc = W.cc0; cc < W.cc1; ++cc) {
       const int slot = (cc - W.cc0) & 1;
-      __syncthreads();
       __syncthreads();
       weights(kReadWaves, gates[slot]);
       weights(kReadWaves + 1, gates[slot]);
       write_gates(gates[slot ^ 1], gl.g, gl.b, lane, false);
       gl.load(W, cc + 2);
       __syncthreads();
+      if constexpr (!kPlanes) __syncthreads();
     }
     return;
   }
@@ -282,8 +297,8 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
   T* yp = static_cast<T*>(A.y) + (W.bi * A.tokens * A.heads + W.h) * A.P + W.pb * kPB;
   const long long yst = static_cast<long long>(A.heads) * A.P;
 
-  PairLoad<T, NT, kReadThreads, VEC> tk;
-  PairLoad<T, kPB, kReadThreads, VEC> tx;
+  PairLoad<T, NT, kReadThreads, VEC, NT == 64 ? 4 : O::kVec> tk;
+  PairLoad<T, kPB, kReadThreads, VEC, 4> tx;
   TileLoad<T, NT, kQ, kReadThreads, VEC> tq;
   const auto load_tiles = [&](int cc) {
     const int rows = W.rows_of(cc);
@@ -301,16 +316,22 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
 #pragma unroll
     for (int e = 0; e < 4; ++e) lm[TM::at(r0 + l16, c0 + 4 * g4 + e)] = O::from_f32(0.0f);
   }
-  load_tiles(W.cc0);
-  for (int cc = W.cc0; cc < W.cc1; ++cc) {
-    const Gates<kQ>& G = gates[(cc - W.cc0) & 1];
-    __syncthreads();   // the last chunk's tiles are done with
+  const auto store_tiles = [&](int slot) {
     tk.store(lk, tid);
     tk.store_transposed(lkt, tid);
     tq.store(lq, tid);
-    tx.store_transposed(lxt, tid);
-    __syncthreads();
-    load_tiles(cc + 1);
+    tx.store_transposed(lxts[kPlanes ? slot : 0], tid);
+    if constexpr (kPlanes) tx.store_split(lxw, gates[slot].in, tid);
+  };
+  load_tiles(W.cc0);
+  __syncthreads();   // the first gates are written
+  store_tiles(0);
+  load_tiles(W.cc0 + 1);
+  for (int cc = W.cc0; cc < W.cc1; ++cc) {
+    const int slot = (cc - W.cc0) & 1;
+    const Gates<kQ>& G = gates[slot];
+    const T* lxt = lxts[kPlanes ? slot : 0];
+    __syncthreads();   // the tiles are written
     weights(w, G);
     // what this half of S_in gives, e^{c_i} S_in q_i: y^T rows p = 16 pw + 4 g4 + 0..3, column i = 16 it + l16
     f32x4_t y[4];
@@ -321,7 +342,7 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
       const Frag f = frag_from_acc<T>(W.st[2 * s], W.st[2 * s + 1]);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        y[it] = O::mma(f, TN::template row2<16>(lq, 16 * it + l16, nbase + 32 * s + 4 * g4), y[it]);
+        y[it] = O::mma(f, TN::row(lq, 16 * it + l16, nbase + 32 * s + 8 * g4), y[it]);
       }
     }
 #pragma unroll
@@ -332,8 +353,14 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
       ly[(w * 2 + u) * 64 + lane] = nh == 0 ? y[2 + u] : y[u];
       y[u] = nh == 0 ? y[u] : y[2 + u];
     }
-    W.update(G, lkt, nbase, lxt);
-    __syncthreads();   // M and the halves of y are written
+    if constexpr (kPlanes)
+      W.update(G, lkt, nbase, [&](int s, Frag (&f)[O::kSplit]) {
+#pragma unroll
+        for (int u = 0; u < O::kSplit; ++u) f[u] = transposed_row(lxw + u * kPB * kQ, 16 * pw + l16, 32 * s + 8 * g4);
+      });
+    else
+      W.update_from(G, lkt, nbase, lxt);
+    __syncthreads();   // M, the halves of y and the next gates are written; the tiles but x^T are done with
     // what the chunk's own tokens give
 #pragma unroll
     for (int u = 0; u < 2; ++u) y[u] += ly[((w ^ 4) * 2 + u) * 64 + lane];
@@ -347,6 +374,9 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
     const TileStore<T, VEC> out(yp + W.token_of(cc) * yst, yst, W.rows_of(cc), W.rows_p);
 #pragma unroll
     for (int u = 0; u < 2; ++u) out.put(32 * nh + 16 * u + l16, 16 * pw + 4 * g4, y[u]);
+    if constexpr (!kPlanes) __syncthreads();
+    store_tiles(slot ^ 1);
+    load_tiles(cc + 2);
   }
   W.store_state();
 }

@@ -257,28 +257,42 @@ struct TileLoad {
 };
 
 // The 16-byte pieces of row n of a transposed tile [WIDTH][kQ] are permuted by
-// XOR with this.  16 rows, that a fragment reads at once, cover all LDS banks,
-// and so do the rows 8 (float32: 4) apart that half a wave writes at once.
+// XOR with this.  The 16 rows that a fragment reads at once (neighbours, or those
+// of state_row) cover all LDS banks, and so do the rows 8 (float32: 4) apart
+// that half a wave writes at once.
 template <typename T>
 __device__ __forceinline__ constexpr int pieces_order(int n) {
-  return sizeof(T) == 2 ? ((n >> 1) ^ (n >> 4)) & 7 : (n ^ ((n >> 4) & 3)) & 15;
+  const auto bit = [n](int i) { return n >> i & 1; };
+  return sizeof(T) == 2 ? (bit(1) ^ bit(5)) | bit(3) << 1 | (bit(2) ^ bit(4)) << 2
+                        : (bit(0) ^ bit(4)) | (bit(1) ^ bit(5)) << 1 | bit(3) << 2 | (bit(2) ^ bit(4)) << 3;
 }
+// The column of the state that row r of a wave's 16-row tile t of S^T holds: the
+// two tiles of 32 columns give a lane, which has rows 4 g + 0..3 of each, 8
+// neighbours, as the operand of S q wants them.
+__device__ __forceinline__ constexpr int state_row(int t, int r) { return 32 * (t >> 1) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3); }
 
 // A [kQ][WIDTH] tile that is (also) needed transposed: a thread holds the same
-// 16-byte columns of two neighbouring tokens, so that it writes both tokens of
-// a transposed row at once.
-template <typename T, int WIDTH, int THREADS, bool VEC>
+// PIECE columns of two neighbouring tokens, so that it writes both tokens of a
+// transposed row at once.
+template <typename T, int WIDTH, int THREADS, bool VEC, int PIECE = Ops<T>::kVec>
 struct PairLoad {
   static constexpr int kVec = Ops<T>::kVec;
-  static constexpr int kRowPieces = WIDTH / kVec;
+  static constexpr int kWords = PIECE * static_cast<int>(sizeof(T)) / 4;
+  static constexpr int kRowPieces = WIDTH / PIECE;
   static constexpr int kAll = kQ / 2 * kRowPieces;
-  static constexpr int kPairs = (kAll + THREADS - 1) / THREADS;
+  static constexpr int kPairs = kAll / THREADS;
   // half a wave: kNear pieces of 32 / kNear pairs of tokens
   static constexpr int kNear = sizeof(T) == 2 ? 8 : 16;
+  static_assert(kAll % THREADS == 0, "whole pairs");
   static_assert(kRowPieces % kNear == 0, "whole half waves");
-  u32x4_t r[kPairs][2];
+  typedef uint32_t Piece __attribute__((ext_vector_type(kWords)));
+  Piece r[kPairs][2];
 
-  static __device__ __forceinline__ int piece_of(int idx) { return idx % kNear + kNear * (idx / 32 % (kRowPieces / kNear)); }
+  // (pieces of 4 bfloat16: of 0..3 and 8..11, whose order differs)
+  static __device__ __forceinline__ int piece_of(int idx) {
+    const int i = idx % kNear + kNear * (idx / 32 % (kRowPieces / kNear));
+    return sizeof(T) == 2 && PIECE == 4 ? (i & ~12) | (i & 4) << 1 | (i & 8) >> 1 : i;
+  }
   static __device__ __forceinline__ int pair_of(int idx) {
     return idx % 32 / kNear + 32 / kNear * (idx / 32 / (kRowPieces / kNear));
   }
@@ -287,19 +301,20 @@ struct PairLoad {
     const __amdgpu_buffer_rsrc_t b = rsrc(p, VEC ? static_cast<int>(rows * st) * static_cast<int>(sizeof(T)) : 0);
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const int idx = i * THREADS + tid, col = piece_of(idx) * kVec;
+      const int idx = i * THREADS + tid, col = piece_of(idx) * PIECE;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int row = 2 * pair_of(idx) + u;   // past the tile's rows: past `rows` too
+        const int row = 2 * pair_of(idx) + u;
         if constexpr (VEC) {
-          const int off = (row * static_cast<int>(st) + col) * static_cast<int>(sizeof(T));
-          r[i][u] = __builtin_amdgcn_raw_buffer_load_b128(b, col < width && idx < kAll ? off : kNowhere, 0, 0);
+          const int off = col < width ? (row * static_cast<int>(st) + col) * static_cast<int>(sizeof(T)) : kNowhere;
+          if constexpr (kWords == 4) r[i][u] = __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0);
+          else r[i][u] = __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0);
         } else {
           const T* e = p + row * st + col;
-          r[i][u] = u32x4_t{0u, 0u, 0u, 0u};
+          r[i][u] = Piece(0u);
           if (row >= rows) continue;
 #pragma unroll
-          for (int j = 0; j < kVec; ++j)
+          for (int j = 0; j < PIECE; ++j)
             if (col + j < width) {
               if constexpr (sizeof(T) == 2) r[i][u][j / 2] |= static_cast<uint32_t>(e[j]) << (16 * (j & 1));
               else r[i][u][j] = __float_as_uint(e[j]);
@@ -311,32 +326,48 @@ struct PairLoad {
   __device__ __forceinline__ void store(T* lds, int tid) const {
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-      const int idx = i * THREADS + tid, col = piece_of(idx) * kVec;
-      if (kAll % THREADS != 0 && idx >= kAll) return;
+      const int idx = i * THREADS + tid;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) *reinterpret_cast<u32x4_t*>(lds + Tile<T, WIDTH>::at(2 * pair_of(idx) + u, col)) = r[i][u];
+      for (int u = 0; u < 2; ++u)
+        *reinterpret_cast<Piece*>(lds + Tile<T, WIDTH>::at(2 * pair_of(idx) + u, piece_of(idx) * PIECE)) = r[i][u];
+    }
+  }
+  // f(row n of the transposed tile, offset in it, the two tokens' element n, index of the first token)
+  template <typename F>
+  __device__ __forceinline__ void each_transposed(int tid, F f) const {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int idx = i * THREADS + tid, n0 = piece_of(idx) * PIECE, j = 2 * pair_of(idx);
+      const int c = (j / kVec) ^ pieces_order<T>(n0), at = n0 * kQ + j % kVec;
+#pragma unroll
+      for (int e = 0; e < PIECE; ++e)   // n0 is a multiple of PIECE: the order of n0 + e is theirs together
+        f(at + e * kQ + (c ^ pieces_order<T>(e)) * kVec, r[i][0], r[i][1], e, j);
     }
   }
   __device__ __forceinline__ void store_transposed(T* lds, int tid) const {
+    each_transposed(tid, [&](int at, Piece a, Piece b, int e, int) {
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint32_t*>(lds + at) =
+            e % 2 == 0 ? (a[e / 2] & 0xffffu) | (b[e / 2] << 16) : (a[e / 2] >> 16) | (b[e / 2] & 0xffff0000u);
+      else
+        *reinterpret_cast<u32x2_t*>(lds + at) = u32x2_t{a[e], b[e]};
+    });
+  }
+  // (bfloat16) The elements by their tokens' weights, transposed, as three
+  // tiles of pieces that carry the products' 24 bits.
+  __device__ __forceinline__ void store_split(T* lds, const float* weights, int tid) const {
+    static_assert(sizeof(T) == 2, "bfloat16 operands");
+    each_transposed(tid, [&](int at, Piece a, Piece b, int e, int j) {
+      const uint32_t p = a[e / 2], q = b[e / 2];
+      float u = (e % 2 == 0 ? lo_bf16(p) : hi_bf16(p)) * weights[j], v = (e % 2 == 0 ? lo_bf16(q) : hi_bf16(q)) * weights[j + 1];
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const int idx = i * THREADS + tid, piece = piece_of(idx), j = 2 * pair_of(idx);
-      if (kAll % THREADS != 0 && idx >= kAll) return;
-      T* p = lds + piece * kVec * kQ + j % kVec;
-      const int c = (j / kVec) ^ pieces_order<T>(piece * kVec);
-      if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t a = r[i][0][e], b = r[i][1][e];
-          T* o = p + 2 * e * kQ + (c ^ e) * kVec;   // rows 2 e and 2 e + 1: pieces_order has e alike
-          *reinterpret_cast<uint32_t*>(o) = (a & 0xffffu) | (b << 16);
-          *reinterpret_cast<uint32_t*>(o + kQ) = (a >> 16) | (b & 0xffff0000u);
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) *reinterpret_cast<u32x2_t*>(p + e * kQ + (c ^ e) * kVec) = u32x2_t{r[i][0][e], r[i][1][e]};
+      for (int z = 0; z < 3; ++z) {
+        const uint32_t w = pack_bf16x2(u, v);
+        *reinterpret_cast<uint32_t*>(lds + z * WIDTH * kQ + at) = w;
+        u -= lo_bf16(w);
+        v -= hi_bf16(w);
       }
-    }
+    });
   }
 };
 // Row n, tokens j0..j0 + 7 (j0 a multiple of 8) of a transposed tile.
