@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
 // partial sums of y, which the two waves of the same rows exchange through LDS,
 // each finishing half of the tokens.
 template <typename T, int NT, bool VEC>
-__global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(WalkPair P) {
+__global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadThreads, sizeof(T) == 2 ? 3 : 2) scan_read_kernel(WalkPair P) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
   typedef Tile<T, NT> TN;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
 #pragma unroll
     for (int r = 0; r < 4; ++r) lm[TM::at(i0 + r, j)] = O::from_f32(a[r]);
   };
-  if (w == kReadWaves) {
+  if (kPlanes && w == kReadWaves) {
     // the ninth wave: two of the ten tiles of M, then the next chunk's gates
     GateLoad gl;
     gl.load(W, W.cc0);
@@ -287,7 +287,6 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
       write_gates(gates[slot ^ 1], gl.g, gl.b, lane, false);
       gl.load(W, cc + 2);
       __syncthreads();
-      if constexpr (!kPlanes) __syncthreads();
     }
     return;
   }
@@ -324,6 +323,14 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
     if constexpr (kPlanes) tx.store_split(lxw, gates[slot].in, tid);
   };
   load_tiles(W.cc0);
+  // float32: no ninth wave, whose registers the others need, and no step that waits for its gates
+  GateLoad gl;
+  const bool gate_wave = !kPlanes && w == kReadWaves - 1;
+  if (gate_wave) {
+    gl.load(W, W.cc0);
+    write_gates(gates[0], gl.g, gl.b, lane, false);
+    gl.load(W, W.cc0 + 1);
+  }
   __syncthreads();   // the first gates are written
   store_tiles(0);
   load_tiles(W.cc0 + 1);
@@ -333,6 +340,11 @@ __global__ void __launch_bounds__(kReadThreads + kWave, 3) scan_read_kernel(Walk
     const T* lxt = lxts[kPlanes ? slot : 0];
     __syncthreads();   // the tiles are written
     weights(w, G);
+    if (!kPlanes && w < 2) weights(kReadWaves + w, G);
+    if (gate_wave) {
+      write_gates(gates[slot ^ 1], gl.g, gl.b, lane, false);
+      gl.load(W, cc + 2);
+    }
     // what this half of S_in gives, e^{c_i} S_in q_i: y^T rows p = 16 pw + 4 g4 + 0..3, column i = 16 it + l16
     f32x4_t y[4];
 #pragma unroll
@@ -406,7 +418,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_segments_kernel(WalkPair W,
 template <typename T, int NT, bool READ, bool VEC>
 hipError_t walk(const WalkPair& W, int dirs, hipStream_t st) {
   const ScanWalk& a = W.w[0];
-  constexpr int parts = READ ? 1 : NT / kStateCols, threads = (READ ? kReadThreads : kStatesThreads) + kWave;
+  constexpr int parts = READ ? 1 : NT / kStateCols, threads = READ ? kReadThreads + (sizeof(T) == 2 ? kWave : 0) : kStatesThreads + kWave;
   const auto kernel = READ ? scan_read_kernel<T, NT, VEC> : scan_states_kernel<T, NT, VEC>;
   const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg * parts;
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items), dirs), dim3(threads), 0, st, W);
