@@ -53,8 +53,10 @@ struct GateLoad {
 };
 
 // One sequence (segment), head and block of kPB state rows.  A wave holds rows
-// p = 16 pw + 0..15 of S and KT 16-column tiles from column nbase.
-template <typename T, int NT, int KT>
+// p = 16 pw + 0..15 of S and KT 16-column tiles from column nbase: of S^T where
+// it reads (READ), where the tiles are operands; of S where it stores states,
+// whose neighbours p then lie in one lane.
+template <typename T, int NT, int KT, bool READ>
 struct Walk {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
@@ -64,7 +66,6 @@ struct Walk {
   int seg, h, pb, grp, rows_p, cc0, cc1, last_chunk;
   long long bi, vrow;
   bool reverse;
-  // tile t holds S^T rows n = nbase + state_row(t, 4 g4 + 0..3), column p = 16 pw + l16
   f32x4_t st[KT];
 
   __device__ __forceinline__ Walk(const ScanWalk& A, int item) : A(A) {
@@ -98,7 +99,9 @@ struct Walk {
     return cc >= cc1 ? 0 : left < kQ ? static_cast<int>(left) : kQ;
   }
   __device__ __forceinline__ long long token_of(int cc) const { return static_cast<long long>(chunk_of(cc < cc1 ? cc : cc0)) * kQ; }
-  __device__ __forceinline__ int tile_off(int t) const { return (16 * pw + l16) * NT + nbase + state_row(t, 4 * g4); }
+  // element r of tile t
+  __device__ __forceinline__ int n_of(int t, int r) const { return nbase + (READ ? state_row(t, 4 * g4) + r : 16 * t + l16); }
+  __device__ __forceinline__ int p_of(int r) const { return 16 * pw + (READ ? l16 : 4 * g4 + r); }
 
   // The gate wave's part: gates of every chunk, one ahead of the others, who
   // meet it at two barriers a chunk (the gates are needed after the second).
@@ -117,38 +120,36 @@ struct Walk {
   }
 
   __device__ __forceinline__ void load_state() {
-    const int prow = pb * kPB + 16 * pw + l16;
     if (A.seg_state != nullptr && !A.totals) {
       const float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT);
 #pragma unroll
-      for (int t = 0; t < KT; ++t) st[t] = *reinterpret_cast<const f32x4_t*>(sp + tile_off(t));
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st[t][r] = sp[p_of(r) * NT + n_of(t, r)];
     } else {
       const bool init = A.init != nullptr && !A.totals;
-      const float* sp = A.init + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
+      const float* sp = A.init + ((bi * A.heads + h) * A.P + pb * kPB) * static_cast<long long>(A.N);
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int n = nbase + state_row(t, 4 * g4) + r;
-          st[t][r] = init && prow < A.P && n < A.N ? sp[n] : 0.0f;
-        }
+        for (int r = 0; r < 4; ++r)
+          st[t][r] = init && p_of(r) < rows_p && n_of(t, r) < A.N ? sp[p_of(r) * A.N + n_of(t, r)] : 0.0f;
     }
   }
   __device__ __forceinline__ void store_state() const {
     if (A.totals) {
       float* sp = A.seg_state + (vrow * A.nseg + seg) * (kPB * NT);
 #pragma unroll
-      for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4_t*>(sp + tile_off(t)) = st[t];
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sp[p_of(r) * NT + n_of(t, r)] = st[t][r];
     } else if (A.fin != nullptr && cc1 == A.nchunks) {
-      const int prow = pb * kPB + 16 * pw + l16;
-      float* sp = A.fin + ((bi * A.heads + h) * A.P + prow) * static_cast<long long>(A.N);
+      float* sp = A.fin + ((bi * A.heads + h) * A.P + pb * kPB) * static_cast<long long>(A.N);
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int n = nbase + state_row(t, 4 * g4) + r;
-          if (prow < A.P && n < A.N) sp[n] = st[t][r];
-        }
+        for (int r = 0; r < 4; ++r)
+          if (p_of(r) < rows_p && n_of(t, r) < A.N) sp[p_of(r) * A.N + n_of(t, r)] = st[t][r];
     }
   }
   // S = e^{c_end} S + sum_j in_j x_j k_j^T; this wave's columns: from row n0 of
@@ -163,11 +164,11 @@ struct Walk {
       Frag f[O::kSplit], kf[KT];
       values(s, f);
 #pragma unroll
-      for (int t = 0; t < KT; ++t) kf[t] = transposed_row(lkt, n0 + state_row(t, l16), 32 * s + 8 * g4);
+      for (int t = 0; t < KT; ++t) kf[t] = transposed_row(lkt, n0 + (READ ? state_row(t, l16) : 16 * t + l16), 32 * s + 8 * g4);
 #pragma unroll
       for (int u = O::kSplit - 1; u >= 0; --u)
 #pragma unroll
-        for (int t = 0; t < KT; ++t) st[t] = O::mma(kf[t], f[u], st[t]);
+        for (int t = 0; t < KT; ++t) st[t] = READ ? O::mma(kf[t], f[u], st[t]) : O::mma(f[u], kf[t], st[t]);
     }
   }
   // ... weighted and split here
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
   __shared__ Gates<kQ> gates[2];
   const ScanWalk A = P.w[blockIdx.y];
   const int block = xcd_item(blockIdx.x, gridDim.x), part = block % kParts;
-  Walk<T, NT, KT> W(A, block / kParts);
+  Walk<T, NT, KT, false> W(A, block / kParts);
   W.nbase = kStateCols * part;
   if (A.totals && W.seg + 1 == A.nseg) return;   // nothing starts after the last segment
   if (W.w == kStatesWaves) {
@@ -225,11 +226,7 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
         (W.reverse ? chunk % A.keep == A.keep - 1 || chunk == W.last_chunk : chunk % A.keep == 0)) {
       float* sp = states + static_cast<long long>(chunk / A.keep) * (kPB * NT);
 #pragma unroll
-      for (int t = 0; t < KT; ++t) {
-        float* row = sp + state_offset(W.nbase + state_row(t, 4 * W.g4), 16 * W.pw + W.l16);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) row[r * 8] = W.st[t][r];
-      }
+      for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4_t*>(sp + state_offset(W.n_of(t, 0), W.p_of(0))) = W.st[t];
     }
     W.update_from(gates[(cc - W.cc0) & 1], lkt, 0, lxt);
   }
@@ -256,7 +253,7 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
   __shared__ f32x4_t ly[kReadWaves * 2 * kWave];   // halves of y that waves hand over
   __shared__ Gates<kQ> gates[2];
   const ScanWalk A = P.w[0];
-  Walk<T, NT, KT> W(A, xcd_item(blockIdx.x, gridDim.x));
+  Walk<T, NT, KT, true> W(A, xcd_item(blockIdx.x, gridDim.x));
   // wave w of eight: rows 16 (w % 4) + 0..15, the columns of half w / 4
   const int tid = W.tid, lane = W.lane, w = W.w, l16 = W.l16, g4 = W.g4, pw = W.pw, nh = w >> 2, nbase = nh * (NT / 2);
   W.nbase = nbase;

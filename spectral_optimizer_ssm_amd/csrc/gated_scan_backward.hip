@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
 #pragma unroll
       for (int s = 0; s < kPB / 32; ++s)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) x[b][s][u] = load_f32x4(r, (nw0 * (kPB / 32) * 64 + lane) * 32, (b * (kPB / 32) + s) * 2048 + 16 * u);
+        for (int u = 0; u < 2; ++u) x[b][s][u] = load_f32x4(r, (nw0 * (kPB / 32) * 128 + lane) * 16, ((b * (kPB / 32) + s) * 2 + u) * 1024);
   };
 
   {

@@ -538,11 +538,11 @@ __device__ __forceinline__ void load8(const float* p, float (&o)[8]) {
   }
 }
 
-// Element (n, p) of a state in the workspace: in the order in which the
-// backward pass holds it, blocks of 16 n by 32 p, lane (n % 16) + 16 (p % 32 / 8)
-// with 8 neighbours p.
+// Element (n, p) of a state in the workspace, in the order in which the
+// backward pass loads it: blocks of 16 n by 32 p, of which lane
+// (n % 16) + 16 (p % 32 / 8) holds 8 neighbours p, four by one load.
 __device__ __forceinline__ int state_offset(int n, int p) {
-  return (((n >> 4) * (kPB / 32) + (p >> 5)) * 64 + (n & 15) + 16 * ((p & 31) >> 3)) * 8 + (p & 7);
+  return (((n >> 4) * (kPB / 32) + (p >> 5)) * 2 + ((p >> 2) & 1)) * 256 + ((n & 15) + 16 * ((p & 31) >> 3)) * 4 + (p & 3);
 }
 
 }  // namespace scan
