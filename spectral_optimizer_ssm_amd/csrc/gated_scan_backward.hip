@@ -41,8 +41,8 @@ struct GradLds {
   static constexpr int v = k + Q * NT * (int)sizeof(T);         // [Q][kPB]
   static constexpr int dy = v + Q * kPB * (int)sizeof(T);        // [Q][kPB]; v and dy at the end: D [i][j]
   static constexpr int m = dy + Q * kPB * (int)sizeof(T);        // (L A)^T [j][i]; at the end D^T
-  static constexpr int gates = m + Q * Q * (int)sizeof(T);     // Gates
-  static constexpr int rows = gates + (int)sizeof(Gates<Q>);      // row sums of W by column tile
+  static constexpr int gates = m + Q * Q * (int)sizeof(T);     // Gates[2]
+  static constexpr int rows = gates + 2 * (int)sizeof(Gates<Q>);      // row sums of W by column tile
   static constexpr int cols = rows + kTiles * Q * 4;              // column sums of L A E by row tile
   static constexpr int qs = cols + kTiles * Q * 4;                // e^{c_i} q_i . S_in^T dy_i by block of n
   static constexpr int ks = qs + kTiles * Q * 4;                  // e^{c_end - c_j} k_j . dS_out^T v_j by block of n
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
   T* lv = reinterpret_cast<T*>(lds + L::v);
   T* ldy = reinterpret_cast<T*>(lds + L::dy);
   T* lm = reinterpret_cast<T*>(lds + L::m);
-  Gates<Q>& G = *reinterpret_cast<Gates<Q>*>(lds + L::gates);
+  Gates<Q>* gates = reinterpret_cast<Gates<Q>*>(lds + L::gates);
   float* lrow = reinterpret_cast<float*>(lds + L::rows);
   float* lcol = reinterpret_cast<float*>(lds + L::cols);
   float* lqs = reinterpret_cast<float*>(lds + L::qs);
@@ -125,10 +125,21 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     if (w == kTiles - 1)
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const int t = 64 * u + lane, in = t < rows ? t : rows - 1;
+        const int t = kU * lane + u, in = t < rows ? t : rows - 1;
         gv[u] = gp[in * A.g.st];
         bv[u] = bp[in * bst];
       }
+  };
+  // by the last wave, of what load_head has brought
+  const auto next_gates = [&](Gates<Q>& G) {
+    const int lane = fresh(threadIdx.x) & 63;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {   // past the end: no decay, no input
+      const bool live = kU * lane + u < rows;
+      gv[u] = live ? gv[u] : 0.0f;
+      bv[u] = !live ? 0.0f : A.b.p == nullptr ? 1.0f : bv[u];
+    }
+    write_gates(G, gv, bv, lane, false);
   };
   // the states as operands: row n = n0 + l16, 8 components p = 32 s + 8 g4 + 0..7 (the walk's order, state_offset)
   const int nw0 = (w % (kBlocks / kNW)) * kNW, tg = w / (kBlocks / kNW);
@@ -154,6 +165,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     load_head(0, rows, tid);
     load_columns(A.states + state_at(0), kPB * NT * 4, lane, x);
     load_columns(A.dstates + state_at(0), kPB * NT * 4, lane, y);
+    if (w == kTiles - 1) next_gates(gates[0]);
   }
   // tiles of (L A)^T and slots of the sums that no wave writes
   for (int i = tid; i < Q * Q; i += kThreads) lm[i] = O::from_f32(0.0f);
@@ -186,19 +198,21 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
   for (int i = 0; i < nvirt; ++i) {
     const int tid = fresh(threadIdx.x), lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
     const int h = h0 + i / A.pblocks, pb = i % A.pblocks;
+    const Gates<Q>& G = gates[i & 1];
     tv.store(lv, tid);
     tdy.store(ldy, tid);
-    if (w == kTiles - 1) {
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {   // past the end: no decay, no input
-        const bool live = 64 * u + lane < rows;
-        gv[u] = live ? gv[u] : 0.0f;
-        bv[u] = !live ? 0.0f : A.b.p == nullptr ? 1.0f : bv[u];
-      }
-      write_gates(G, gv, bv, lane, false);
-    }
     __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
+    // The next head's tiles, and below its states, each as soon as their registers
+    // are free: issued together they would stall the waves, which can have only so
+    // many loads under way.  (float32: all late, the registers are needed.)
+    constexpr bool kEarly = sizeof(T) == 2;
+    const bool more = i + 1 < nvirt;
+    const int next = more ? i + 1 : i;
+    if constexpr (kEarly) {
+      load_head(next, more ? rows : 0, fresh(threadIdx.x));
+      __builtin_amdgcn_sched_barrier(0);
+    }
 
     float cols[kMaxTiles];
 #pragma unroll
@@ -303,8 +317,16 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
       }
     };
     split(x);
+    if constexpr (kEarly) {
+      load_columns(A.states + state_at(next), more ? kPB * NT * 4 : 0, lane, x);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     products(std::false_type(), ldy, lq, G.first, dq, lqs);
     split(y);
+    if constexpr (kEarly) {
+      load_columns(A.dstates + state_at(next), more ? kPB * NT * 4 : 0, lane, y);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     products(std::true_type(), lv, lk, G.last, dk, lks);
     __syncthreads();   // (L A)^T and the sums are written, v is done with
     {
@@ -319,13 +341,12 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
               TP::store8(lv, 16 * (nw0 + b) + l16, 32 * s + 8 * g4, f[b][s][0]);   // the first of its pieces
             }
       }
-      // the next head's tiles and states
       const float* dsp = A.dstates + state_at(i);
-      const bool more = i + 1 < nvirt;
-      const int next = more ? i + 1 : i;
-      load_head(next, more ? rows : 0, fresh(threadIdx.x));
-      load_columns(A.states + state_at(next), more ? kPB * NT * 4 : 0, lane, x);
-      load_columns(A.dstates + state_at(next), more ? kPB * NT * 4 : 0, lane, y);
+      if constexpr (!kEarly) {
+        load_head(next, more ? rows : 0, fresh(threadIdx.x));
+        load_columns(A.states + state_at(next), more ? kPB * NT * 4 : 0, lane, x);
+        load_columns(A.dstates + state_at(next), more ? kPB * NT * 4 : 0, lane, y);
+      }
       __builtin_amdgcn_sched_barrier(0);
       // sums of a token: 16 tokens a wave, one of the four kinds each quarter of it
       {
@@ -385,31 +406,34 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     }
     if constexpr (!L::kStateInV) __syncthreads();   // the tokens' sums are written
 
+    // the last wave has the next head's gates to prepare, the first one this head's dg
+    if (w == kTiles - 1 && more) next_gates(gates[(i + 1) & 1]);
     if (w == 0) {
       const int lane = fresh(threadIdx.x) & 63;
 #pragma unroll
       for (int e = 0; e < kTiles; ++e) acc_z += lthrough[e];
       if (pb + 1 == A.pblocks) {
         // with a_t what dg sums from t on and l_t what it sums up to t: the sum of all a, plus those of l - a before t
-        double before[kU], total = 0.0, all = 0.0;
+        double d[kU], a = 0.0, ds = 0.0;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const double a = static_cast<double>(lin[64 * u + lane]), d = static_cast<double>(lleave[64 * u + lane]) - a;
-          const double p = wave_prefix_d(d);
-          before[u] = total + p - d;
-          total += read_lane_d(p, 63);
-          all += read_lane_d(wave_prefix_d(a), 63);
+          const double at = static_cast<double>(lin[kU * lane + u]);
+          d[u] = static_cast<double>(lleave[kU * lane + u]) - at;
+          a += at;
+          ds += d[u];
         }
+        double before = wave_prefix_d(ds) - ds;
+        before += read_lane_d(wave_prefix_d(a), 63) + static_cast<double>(G.end[0]) * static_cast<double>(acc_z);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-          const int t = 64 * u + lane;
+          const int t = kU * lane + u;
           if (t < rows) {
             const long long o = (bi * A.tokens + t0 + t) * A.heads + h;
-            const double d = all + before[u] + static_cast<double>(G.end[0]) * static_cast<double>(acc_z);
             // nothing crosses a token whose decay is 0: what the sums leave there is rounding
-            A.dg[o] = G.own[t] == 0.0f ? 0.0f : static_cast<float>(d);
+            A.dg[o] = G.own[t] == 0.0f ? 0.0f : static_cast<float>(before);
             if (A.db != nullptr) A.db[o] = ldb[t];
           }
+          before += d[u];
         }
         acc_z = 0.0f;
       }

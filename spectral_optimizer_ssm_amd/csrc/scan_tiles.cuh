@@ -445,31 +445,36 @@ struct Gates {
   float end[4];         // e^{c_end}
 };
 
-// By one wave: lane l brings the gates of tokens l, 64 + l, ...  Returns c_end.
+// By one wave: lane l brings the gates of tokens U l..U l + U - 1.  Returns c_end.
 template <int Q>
 __device__ __forceinline__ double write_gates(Gates<Q>& G, const float (&log_decay)[Q / 64], const float (&gate)[Q / 64],
                                               int lane, bool reverse) {
-  float ld[Q / 64];
-  double c[Q / 64], e = 0.0;
+  constexpr int U = Q / 64;
+  float ld[U];
+  double own[U], sum = 0.0;
 #pragma unroll
-  for (int u = 0; u < Q / 64; ++u) {
+  for (int u = 0; u < U; ++u) {
     ld[u] = log_decay[u] < kMinLogDecay ? kMinLogDecay : log_decay[u];   // keeps NaN
-    c[u] = e + wave_prefix_d(static_cast<double>(ld[u]) * static_cast<double>(1.44269504088896340736));
-    e = read_lane_d(c[u], 63);
+    own[u] = static_cast<double>(ld[u]) * static_cast<double>(1.44269504088896340736);
+    sum += own[u];
   }
+  const double upto = wave_prefix_d(sum), e = read_lane_d(upto, 63);
+  double c = upto - sum, first16 = 0.0;
 #pragma unroll
-  for (int u = 0; u < Q / 64; ++u) {
-    const int t = 64 * u + lane;
-    const float hi = static_cast<float>(c[u]);
+  for (int u = 0; u < U; ++u) {
+    const int t = U * lane + u;
+    c = u + 1 == U ? upto : c + own[u];
+    if (u == 0) first16 = __shfl(c, lane & ~(16 / U - 1), kWave);
+    const float hi = static_cast<float>(c);
     G.hi[t] = hi;
-    G.lo[t] = static_cast<float>(c[u] - static_cast<double>(hi));
+    G.lo[t] = static_cast<float>(c - static_cast<double>(hi));
     G.b[t] = gate[u];
     G.own[t] = __builtin_amdgcn_exp2f(ld[u] * kLog2e);
-    const float first = __builtin_amdgcn_exp2f(static_cast<float>(c[u])), last = __builtin_amdgcn_exp2f(static_cast<float>(e - c[u]));
+    const float first = __builtin_amdgcn_exp2f(static_cast<float>(c)), last = __builtin_amdgcn_exp2f(static_cast<float>(e - c));
     G.first[t] = first;
     G.last[t] = last;
     G.in[t] = reverse ? first : last * gate[u];
-    G.row[t] = __builtin_amdgcn_exp2f(static_cast<float>(c[u] - __shfl(c[u], lane & 48, kWave)));
+    G.row[t] = __builtin_amdgcn_exp2f(static_cast<float>(c - first16));
   }
   if (lane == 0) G.end[0] = __builtin_amdgcn_exp2f(static_cast<float>(e));
   return e;
