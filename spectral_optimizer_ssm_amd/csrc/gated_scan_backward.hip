@@ -33,61 +33,35 @@ using namespace scan;
 
 // A block of Q tokens by 4 Q threads: 128 tokens with bfloat16 operands, 64
 // with float32 ones, whose tiles fill the LDS of a compute unit.
-template <typename T, int NT, int Q>
-struct GradLds {
-  static constexpr int kTiles = Q / 16;                           // token tiles, and waves
-  static constexpr int q = 0;                                     // [Q][NT]
-  static constexpr int k = q + Q * NT * (int)sizeof(T);         // [Q][NT]
-  static constexpr int v = k + Q * NT * (int)sizeof(T);         // [Q][kPB]
-  static constexpr int dy = v + Q * kPB * (int)sizeof(T);        // [Q][kPB]; v and dy at the end: D [i][j]
-  static constexpr int m = dy + Q * kPB * (int)sizeof(T);        // (L A)^T [j][i]; at the end D^T
-  static constexpr int gates = m + Q * Q * (int)sizeof(T);     // Gates[2]
-  static constexpr int rows = gates + 2 * (int)sizeof(Gates<Q>);      // row sums of W by column tile
-  static constexpr int cols = rows + kTiles * Q * 4;              // column sums of L A E by row tile
-  static constexpr int qs = cols + kTiles * Q * 4;                // e^{c_i} q_i . S_in^T dy_i by block of n
-  static constexpr int ks = qs + kTiles * Q * 4;                  // e^{c_end - c_j} k_j . dS_out^T v_j by block of n
-  static constexpr int through = ks + kTiles * Q * 4;             // <S_in, dS_out> by wave
-  static constexpr int inside = through + 8 * 4;                  // by token, over a head's blocks of value rows:
-  static constexpr int leave = inside + Q * 4;                    //   what dg sums from t on, what it sums up to t,
-  static constexpr int dgate = leave + Q * 4;                     //   and db
-  static constexpr int bytes = dgate + Q * 4;
-  // dS_out [n][p] as the operand of dv goes where v was, if it fits
-  static constexpr bool kStateInV = NT <= Q;
-  static_assert(bytes <= 160 * 1024, "LDS of a compute unit");
-  static_assert(Q <= 2 * kPB, "D fits where v and dy were");
-};
-
 template <typename T, int NT, int Q, bool VEC>
-__global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
+__global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
-  typedef GradLds<T, NT, Q> L;
   typedef Tile<T, NT> TN;
   typedef Tile<T, kPB> TP;
   typedef Tile<T, Q> TM;
-  constexpr int kThreads = 4 * Q, kTiles = L::kTiles, kU = Q / 64;
-  // the tiles on and below the diagonal, dealt to the waves in runs
-  constexpr int kAll = kTiles * (kTiles + 1) / 2, kMaxTiles = (kAll + kTiles - 1) / kTiles;
+  constexpr int kThreads = 4 * Q, kTiles = Q / 16, kU = Q / 64;
+  // a wave has one of the diagonal's tiles, first, and a run of those below it
+  constexpr int kBelow = kTiles * (kTiles - 1) / 2, kMaxTiles = 1 + (kBelow + kTiles - 1) / kTiles;
   // dq and dk: 16-wide blocks of n per wave, groups of waves that share a block's tokens
   constexpr int kBlocks = NT / 16, kNW = kBlocks > kTiles ? kBlocks / kTiles : 1;
   constexpr int kTG = kTiles > kBlocks ? kTiles / kBlocks : 1, kTT = kTiles / kTG;
   // dv: four blocks of value rows, the tokens dealt to kTiles / 4 groups of waves
   constexpr int kZG = kTiles / 4;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  T* lq = reinterpret_cast<T*>(lds + L::q);
-  T* lk = reinterpret_cast<T*>(lds + L::k);
-  T* lv = reinterpret_cast<T*>(lds + L::v);
-  T* ldy = reinterpret_cast<T*>(lds + L::dy);
-  T* lm = reinterpret_cast<T*>(lds + L::m);
-  Gates<Q>* gates = reinterpret_cast<Gates<Q>*>(lds + L::gates);
-  float* lrow = reinterpret_cast<float*>(lds + L::rows);
-  float* lcol = reinterpret_cast<float*>(lds + L::cols);
-  float* lqs = reinterpret_cast<float*>(lds + L::qs);
-  float* lks = reinterpret_cast<float*>(lds + L::ks);
-  float* lthrough = reinterpret_cast<float*>(lds + L::through);
-  float* lin = reinterpret_cast<float*>(lds + L::inside);
-  float* lleave = reinterpret_cast<float*>(lds + L::leave);
-  float* ldb = reinterpret_cast<float*>(lds + L::dgate);
+  // dS_out [n][p] as the operand of dv goes where v was, if it fits
+  constexpr bool kStateInV = NT <= Q;
+  // arrays of their own: the compiler may move reads of one across writes to another
+  __shared__ __attribute__((aligned(16))) T lq[Q * NT], lk[Q * NT], lv[2 * Q * kPB];   // q; k; v and dy, at the end D [i][j]
+  __shared__ __attribute__((aligned(16))) T lm[Q * Q];                                  // (L A)^T [j][i], at the end D^T
+  static_assert(Q <= 2 * kPB, "D fits where v and dy were");
+  __shared__ Gates<Q> gates[2];
+  // by token: row sums of W by column tile, column sums of L A E by row tile,
+  // e^{c_i} q_i . S_in^T dy_i and e^{c_end - c_j} k_j . dS_out^T v_j by block of n
+  __shared__ float lsums[4][kTiles * Q];
+  // <S_in, dS_out> by wave; by token, over a head's blocks of value rows: what dg sums from t on, up to t, and db
+  __shared__ float lthrough[kTiles], lin[Q], lleave[Q], ldb[Q];
+  T* ldy = lv + Q * kPB;
+  float *lrow = lsums[0], *lcol = lsums[1], *lqs = lsums[2], *lks = lsums[3];
 
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), l16 = lane & 15, g4 = lane >> 4;
   const int split = static_cast<int>(blockIdx.x % A.nsplit);
@@ -169,18 +143,19 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
   }
   // tiles of (L A)^T and slots of the sums that no wave writes
   for (int i = tid; i < Q * Q; i += kThreads) lm[i] = O::from_f32(0.0f);
-  for (int i = tid; i < 4 * kTiles * Q; i += kThreads) lrow[i] = 0.0f;
+  for (int i = tid; i < 4 * kTiles * Q; i += kThreads) lsums[0][i] = 0.0f;
   __syncthreads();
 
   // A and the sum of L b E, by tile: rows i, columns j
   // (a wave with one tile less repeats its neighbour's first, to the same result, and leaves it out of D)
-  const int tile0 = w * kAll / kTiles, ntile = (w + 1) * kAll / kTiles - tile0;
+  const int tile0 = w * kBelow / kTiles, ntile = 1 + (w + 1) * kBelow / kTiles - tile0;
   int trow[kMaxTiles], tcol[kMaxTiles];
   f32x4_t sc[kMaxTiles], dsum[kMaxTiles];
 #pragma unroll
   for (int t = 0; t < kMaxTiles; ++t) {
-    trow[t] = tile_row(tile0 + t);
-    tcol[t] = tile_col(tile0 + t, trow[t]);
+    const int r = t == 0 ? 0 : tile_row(tile0 + t - 1);
+    trow[t] = t == 0 ? w : r + 1;
+    tcol[t] = t == 0 ? w : tile_col(tile0 + t - 1, r);
     sc[t] = dsum[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < NT / 32; ++s)
@@ -226,7 +201,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
                      TP::row(lv, 16 * jt + l16, 32 * s + 8 * g4), e);
         const int j = 16 * jt + l16, i0 = 16 * it + 4 * g4;
         const float b = G.b[j];
-        const f32x4_t d = between4(G, it, jt, i0, j);
+        const f32x4_t d = t == 0 ? between4_diagonal(G, i0, j) : between4_below(G, it, i0, j);
         f32x4_t mm, rs;
         cols[t] = 0.0f;
 #pragma unroll
@@ -331,7 +306,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
     __syncthreads();   // (L A)^T and the sums are written, v is done with
     {
       const int lane = fresh(threadIdx.x) & 63, l16 = lane & 15, g4 = lane >> 4;
-      if constexpr (L::kStateInV) {
+      if constexpr (kStateInV) {
         // dS_out [n][p], rounded, as the operand of dv
         if (tg == 0)
 #pragma unroll
@@ -351,7 +326,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
       // sums of a token: 16 tokens a wave, one of the four kinds each quarter of it
       {
         const int t = 16 * w + l16;
-        const float* src = reinterpret_cast<const float*>(lds + L::rows) + g4 * kTiles * Q + t;
+        const float* src = lsums[g4] + t;
         float a = 0.0f;
 #pragma unroll
         for (int e = 0; e < kTiles; ++e) a += src[e * Q];
@@ -380,11 +355,11 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (L::kStateInV) __syncthreads();   // dS_out is written
+      if constexpr (kStateInV) __syncthreads();   // dS_out is written
 #pragma unroll
       for (int s = 0; s < NT / 32; ++s) {
         Frag f;
-        if constexpr (L::kStateInV) {
+        if constexpr (kStateInV) {
           f = TP::col(lv, 32 * s, 16 * (w & 3), lane);
         } else {
           float v[8];
@@ -404,7 +379,7 @@ __global__ void __launch_bounds__(4 * Q, 2) scan_grad_kernel(ScanGrad A) {
         out.put(j, 16 * (w & 3) + 4 * g4, (z[u] + zs[u] * G.last[j]) * G.b[j]);
       }
     }
-    if constexpr (!L::kStateInV) __syncthreads();   // the tokens' sums are written
+    if constexpr (!kStateInV) __syncthreads();   // the tokens' sums are written
 
     // the last wave has the next head's gates to prepare, the first one this head's dg
     if (w == kTiles - 1 && more) next_gates(gates[(i + 1) & 1]);
@@ -522,13 +497,9 @@ __global__ void __launch_bounds__(kPartThreads) scan_parts_kernel(const float* p
 template <typename T, int NT, bool VEC>
 hipError_t grad(const ScanGrad& A, hipStream_t st) {
   constexpr int Q = sizeof(T) == 2 ? kScanGradBf16 : kScanGradF32;
-  constexpr int bytes = GradLds<T, NT, Q>::bytes;
-  const void* fn = reinterpret_cast<const void*>(scan_grad_kernel<T, NT, Q, VEC>);
-  hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != hipSuccess) return e;
   const long long items = static_cast<long long>(A.batch) * A.nblocks * A.groups * A.nsplit;
-  hipLaunchKernelGGL((scan_grad_kernel<T, NT, Q, VEC>), dim3(static_cast<unsigned>(items)), dim3(4 * Q), bytes, st, A);
-  e = hipGetLastError();
+  hipLaunchKernelGGL((scan_grad_kernel<T, NT, Q, VEC>), dim3(static_cast<unsigned>(items)), dim3(4 * Q), 0, st, A);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || A.nsplit == 1) return e;
   const long long half = static_cast<long long>(A.batch) * A.tokens * A.groups * A.N;
   hipLaunchKernelGGL((scan_parts_kernel<T>), dim3(static_cast<unsigned>((2 * half + kPartThreads - 1) / kPartThreads)), dim3(kPartThreads), 0,

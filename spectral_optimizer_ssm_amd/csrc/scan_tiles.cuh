@@ -485,21 +485,25 @@ __device__ __forceinline__ double write_gates(Gates<Q>& G, const float (&log_dec
 // the block's first token, one exponential for the four (its two factors are at
 // most 1 where the log decays are); on it, one by one, 0 for j > i.
 template <int Q>
-__device__ __forceinline__ f32x4_t between4(const Gates<Q>& G, int it, int jt, int i0, int j) {
+__device__ __forceinline__ f32x4_t between4_below(const Gates<Q>& G, int it, int i0, int j) {
+  const float to = __builtin_amdgcn_exp2f((G.hi[16 * it] - G.hi[j]) + (G.lo[16 * it] - G.lo[j]));
+  return *reinterpret_cast<const f32x4_t*>(G.row + i0) * to;
+}
+template <int Q>
+__device__ __forceinline__ f32x4_t between4_diagonal(const Gates<Q>& G, int i0, int j) {
   const float hi = G.hi[j], lo = G.lo[j];
+  const f32x4_t ih = *reinterpret_cast<const f32x4_t*>(G.hi + i0), il = *reinterpret_cast<const f32x4_t*>(G.lo + i0);
   f32x4_t d;
-  if (it != jt) {
-    const float to = __builtin_amdgcn_exp2f((G.hi[16 * it] - hi) + (G.lo[16 * it] - lo));
-    d = *reinterpret_cast<const f32x4_t*>(G.row + i0) * to;
-  } else {
-    const f32x4_t ih = *reinterpret_cast<const f32x4_t*>(G.hi + i0), il = *reinterpret_cast<const f32x4_t*>(G.lo + i0);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float e = __builtin_amdgcn_exp2f((ih[r] - hi) + (il[r] - lo));
-      d[r] = i0 + r >= j ? e : 0.0f;
-    }
+  for (int r = 0; r < 4; ++r) {
+    const float e = __builtin_amdgcn_exp2f((ih[r] - hi) + (il[r] - lo));
+    d[r] = i0 + r >= j ? e : 0.0f;
   }
   return d;
+}
+template <int Q>
+__device__ __forceinline__ f32x4_t between4(const Gates<Q>& G, int it, int jt, int i0, int j) {
+  return it != jt ? between4_below(G, it, i0, j) : between4_diagonal(G, i0, j);
 }
 
 // Sums over the four 16-lane rows of a wave, for four values at once: row g of
