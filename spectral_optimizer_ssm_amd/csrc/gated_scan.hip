@@ -63,7 +63,7 @@ struct Walk {
 
   const ScanWalk& A;
   int tid, lane, w, l16, g4, pw, nbase;
-  int seg, h, pb, grp, rows_p, cc0, cc1, last_chunk;
+  int seg, h, pb, grp, rows_p, cc0, cc1, last_chunk, tail;   // tail: tokens of the last chunk
   long long bi, vrow;
   bool reverse;
   f32x4_t st[KT];
@@ -88,17 +88,17 @@ struct Walk {
     vrow = bi * vheads + vh;
     reverse = A.reverse != 0;
     last_chunk = A.nchunks - 1;
+    tail = static_cast<int>(A.tokens - static_cast<long long>(last_chunk) * kQ);
     cc0 = seg * A.seg_chunks;
     cc1 = cc0 + A.seg_chunks < A.nchunks ? cc0 + A.seg_chunks : A.nchunks;
   }
   // the cc-th chunk visited, and its tokens (none past the segment: a branch
   // around a prefetch would keep two copies of its registers)
   __device__ __forceinline__ int chunk_of(int cc) const { return reverse ? last_chunk - cc : cc; }
-  __device__ __forceinline__ int rows_of(int cc) const {
-    const long long left = A.tokens - static_cast<long long>(chunk_of(cc)) * kQ;
-    return cc >= cc1 ? 0 : left < kQ ? static_cast<int>(left) : kQ;
-  }
+  __device__ __forceinline__ int rows_of(int cc) const { return cc >= cc1 ? 0 : chunk_of(cc) == last_chunk ? tail : kQ; }
   __device__ __forceinline__ long long token_of(int cc) const { return static_cast<long long>(chunk_of(cc < cc1 ? cc : cc0)) * kQ; }
+  // elements from a chunk to the next one visited, of rows `st` apart
+  __device__ __forceinline__ long long step(long long st) const { return (reverse ? -kQ : kQ) * st; }
   // element r of tile t
   __device__ __forceinline__ int n_of(int t, int r) const { return nbase + (READ ? state_row(t, 4 * g4) + r : 16 * t + l16); }
   __device__ __forceinline__ int p_of(int r) const { return 16 * pw + (READ ? l16 : 4 * g4 + r); }
@@ -184,7 +184,7 @@ struct Walk {
   }
 };
 
-// States only: the state before every block of `keep` chunks (in reversed time:
+// States only: the state before every block of 2^keep_log2 chunks (in reversed time:
 // after it), a segment's total, or both.  The columns of S are independent, so
 // a workgroup takes kStateCols of them: three workgroups fit a compute unit and
 // fill the chip more evenly than one of twice the size.
@@ -206,11 +206,14 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
   const T* kp = static_cast<const T*>(A.k.p) + W.bi * A.k.sb + W.grp * A.k.sh + W.nbase;
   PairLoad<T, kStateCols, kStatesThreads, VEC> tk;
   PairLoad<T, kPB, kStatesThreads, VEC> tx;
-  const auto load_tiles = [&](int cc) {
+  kp += W.token_of(W.cc0) * A.k.st;
+  xp += W.token_of(W.cc0) * A.x.st;
+  const auto load_tiles = [&](int cc) {   // chunk after chunk
     const int rows = W.rows_of(cc);
-    const long long t0 = W.token_of(cc);
-    tk.load(kp + t0 * A.k.st, A.k.st, rows, A.N - W.nbase, W.tid);
-    tx.load(xp + t0 * A.x.st, A.x.st, rows, W.rows_p, W.tid);
+    tk.load(kp, A.k.st, rows, A.N - W.nbase, W.tid);
+    tx.load(xp, A.x.st, rows, W.rows_p, W.tid);
+    kp += W.step(A.k.st);
+    xp += W.step(A.x.st);
   };
   W.load_state();
   float* states = A.states == nullptr ? nullptr : A.states + W.vrow * A.nblocks * (kPB * NT);
@@ -221,10 +224,9 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
     tx.store_transposed(lxt, W.tid);
     __syncthreads();
     load_tiles(cc + 1);
-    const int chunk = W.chunk_of(cc);
-    if (states != nullptr &&
-        (W.reverse ? chunk % A.keep == A.keep - 1 || chunk == W.last_chunk : chunk % A.keep == 0)) {
-      float* sp = states + static_cast<long long>(chunk / A.keep) * (kPB * NT);
+    const int chunk = W.chunk_of(cc), within = chunk & ((1 << A.keep_log2) - 1);
+    if (states != nullptr && (W.reverse ? within + 1 == 1 << A.keep_log2 || chunk == W.last_chunk : within == 0)) {
+      float* sp = states + static_cast<long long>(chunk >> A.keep_log2) * (kPB * NT);
 #pragma unroll
       for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4_t*>(sp + state_offset(W.n_of(t, 0), W.p_of(0))) = W.st[t];
     }
@@ -296,12 +298,18 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
   PairLoad<T, NT, kReadThreads, VEC, NT == 64 ? 4 : O::kVec> tk;
   PairLoad<T, kPB, kReadThreads, VEC, 4> tx;
   TileLoad<T, NT, kQ, kReadThreads, VEC> tq;
-  const auto load_tiles = [&](int cc) {
+  kp += W.token_of(W.cc0) * A.k.st;
+  qp += W.token_of(W.cc0) * A.q.st;
+  xp += W.token_of(W.cc0) * A.x.st;
+  yp += W.token_of(W.cc0) * yst;
+  const auto load_tiles = [&](int cc) {   // chunk after chunk
     const int rows = W.rows_of(cc);
-    const long long t0 = W.token_of(cc);
-    tk.load(kp + t0 * A.k.st, A.k.st, rows, A.N, tid);
-    tq.load(qp + t0 * A.q.st, A.q.st, rows, A.N, tid);
-    tx.load(xp + t0 * A.x.st, A.x.st, rows, W.rows_p, tid);
+    tk.load(kp, A.k.st, rows, A.N, tid);
+    tq.load(qp, A.q.st, rows, A.N, tid);
+    tx.load(xp, A.x.st, rows, W.rows_p, tid);
+    kp += W.step(A.k.st);
+    qp += W.step(A.q.st);
+    xp += W.step(A.x.st);
   };
 
   W.load_state();
@@ -380,7 +388,8 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
 #pragma unroll
         for (int u = 0; u < 2; ++u) y[u] = O::mma(vf, TM::row(lm, 32 * nh + 16 * u + l16, 32 * s + 8 * g4), y[u]);
       }
-    const TileStore<T, VEC> out(yp + W.token_of(cc) * yst, yst, W.rows_of(cc), W.rows_p);
+    const TileStore<T, VEC> out(yp, yst, W.rows_of(cc), W.rows_p);
+    yp += W.step(yst);
 #pragma unroll
     for (int u = 0; u < 2; ++u) out.put(32 * nh + 16 * u + l16, 16 * pw + 4 * g4, y[u]);
     if constexpr (!kPlanes) __syncthreads();

@@ -78,17 +78,16 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
   const int nvirt = (h1 - h0) * A.pblocks;   // (head, block of kPB value components), heads outermost
   const int vheads = A.heads * A.pblocks;
   const auto rows_p_of = [&](int pb) { return A.P - pb * kPB < kPB ? A.P - pb * kPB : kPB; };
+  // offset of the states of the i-th of them
   const auto state_at = [&](int i) {
-    const int h = h0 + i / A.pblocks, pb = i % A.pblocks;
-    return ((bi * vheads + h * A.pblocks + pb) * A.nblocks + c) * static_cast<long long>(kPB * NT);
+    return ((bi * vheads + h0 * A.pblocks + i) * A.nblocks + c) * static_cast<long long>(kPB * NT);
   };
 
   TileLoad<T, kPB, Q, kThreads, VEC> tv, tdy;
   float gv[kU], bv[kU];
   // (rows_ and bytes 0: nothing is read and zeros come back, so the last pass needs no branch around its prefetch)
-  const auto load_head = [&](int i, int rows_, int tid) {
-    const int lane = tid & 63;
-    const int h = h0 + i / A.pblocks, pb = i % A.pblocks, rp = rows_p_of(pb);
+  const auto load_head = [&](int h, int pb, int rows_, int tid) {
+    const int lane = tid & 63, rp = rows_p_of(pb);
     const T* vp = static_cast<const T*>(A.v.p) + bi * A.v.sb + h * A.v.sh + t0 * A.v.st + pb * kPB;
     const T* dp = static_cast<const T*>(A.dy.p) + bi * A.dy.sb + h * A.dy.sh + t0 * A.dy.st + pb * kPB;
     tv.load(vp, A.v.st, rows_, rp, tid);
@@ -136,7 +135,7 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
   }
   f32x4_t x[kNW][kPB / 32][2], y[kNW][kPB / 32][2];
   if (nvirt > 0) {
-    load_head(0, rows, tid);
+    load_head(h0, 0, rows, tid);
     load_columns(A.states + state_at(0), kPB * NT * 4, lane, x);
     load_columns(A.dstates + state_at(0), kPB * NT * 4, lane, y);
     if (w == kTiles - 1) next_gates(gates[0]);
@@ -170,9 +169,8 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
     for (int u = 0; u < kTT; ++u) dq[b][u] = dk[b][u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
   float acc_z = 0.0f;   // <S_in, dS_out> over a head's blocks
-  for (int i = 0; i < nvirt; ++i) {
+  for (int i = 0, h = h0, pb = 0; i < nvirt; ++i) {
     const int tid = fresh(threadIdx.x), lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
-    const int h = h0 + i / A.pblocks, pb = i % A.pblocks;
     const Gates<Q>& G = gates[i & 1];
     tv.store(lv, tid);
     tdy.store(ldy, tid);
@@ -184,8 +182,9 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
     constexpr bool kEarly = sizeof(T) == 2;
     const bool more = i + 1 < nvirt;
     const int next = more ? i + 1 : i;
+    const int next_pb = !more ? pb : pb + 1 < A.pblocks ? pb + 1 : 0, next_h = h + (more && next_pb == 0);
     if constexpr (kEarly) {
-      load_head(next, more ? rows : 0, fresh(threadIdx.x));
+      load_head(next_h, next_pb, more ? rows : 0, fresh(threadIdx.x));
       __builtin_amdgcn_sched_barrier(0);
     }
 
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
       }
       const float* dsp = A.dstates + state_at(i);
       if constexpr (!kEarly) {
-        load_head(next, more ? rows : 0, fresh(threadIdx.x));
+        load_head(next_h, next_pb, more ? rows : 0, fresh(threadIdx.x));
         load_columns(A.states + state_at(next), more ? kPB * NT * 4 : 0, lane, x);
         load_columns(A.dstates + state_at(next), more ? kPB * NT * 4 : 0, lane, y);
       }
@@ -413,6 +412,8 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
         acc_z = 0.0f;
       }
     }
+    h = next_h;
+    pb = next_pb;
     __syncthreads();   // the tiles, gates and sums are done with
   }
 

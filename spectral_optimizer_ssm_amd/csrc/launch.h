@@ -323,7 +323,7 @@ struct ScanWalk {
   void* y;                    // [batch][tokens][heads][P]
   const float* init;          // null, or [batch][heads][P][N]: the state before the first chunk visited
   float* fin;                 // null, or the state after the last
-  int keep, nblocks;          // blocks of `keep` chunks
+  int keep_log2, nblocks;     // blocks of 2^keep_log2 chunks
   float* states;              // null, or [batch][heads * pblocks][nblocks][kScanRows x padded N]: the
                               // state that each block is visited with, in the order of state_offset
   float* seg_state;           // nseg > 1: [batch][heads * pblocks][nseg][kScanRows][padded N]

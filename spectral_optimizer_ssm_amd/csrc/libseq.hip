@@ -61,7 +61,7 @@ int check_operands(const muon_scan_args* a) {
 
 // Workgroups that fill 256 compute units: one of the forward walk or of the
 // backward pass on each (their tiles fill the LDS), two of the states' walk.
-constexpr long long kReadFill = 256, kStatesFill = 512, kGradFill = 256;
+constexpr long long kReadFill = 256, kStatesFill = 384, kGradFill = 256;
 
 struct ScanPlan {
   int pblocks, nchunks, nblocks, nseg, seg_chunks, nsplit;   // nblocks: of the backward pass
@@ -138,7 +138,7 @@ ScanWalk walk_of(const muon_scan_args* a, const ScanPlan& p) {
   w.batch = a->batch; w.tokens = a->tokens; w.heads = a->heads; w.groups = a->groups;
   w.P = a->P; w.N = a->N;
   w.pblocks = p.pblocks; w.nchunks = p.nchunks; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
-  w.keep = grad_tokens(a->dtype) / kScanChunk; w.nblocks = p.nblocks;
+  w.keep_log2 = grad_tokens(a->dtype) / kScanChunk / 2; w.nblocks = p.nblocks;
   w.init = a->S0;
   return w;
 }
