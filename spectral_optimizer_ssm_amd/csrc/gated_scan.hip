@@ -6,14 +6,15 @@
 //   S_out = e^{c_end} S_in + sum_j e^{c_end - c_j} b_j v_j k_j^T,
 // matrix products all.  One workgroup walks the chunks of a sequence, head and
 // block of kPB state rows with the state in its registers (float32, so it
-// crosses HBM only at the ends): each of its four waves holds 16 rows of S.
-// Held as S^T with n along the accumulator rows, the state is the operand of
-// S_in q without leaving the registers.
+// crosses HBM only at the ends): eight waves, each with 16 rows of S and half
+// of its columns.  Held as S^T with n along the accumulator rows, the state is
+// the operand of S_in q without leaving the registers.
 //
 // Rounding, bfloat16 operands: the weights e^{c_i - c_j} b_j (q_i . k_j) and
 // the copy of S_in that is read are rounded to bfloat16 once, which leaves y
 // within its own rounding; the weighted values that enter the state are split
-// into three bfloat16 pieces, so the state keeps float32 accuracy.
+// into three bfloat16 pieces, so the state keeps float32 accuracy.  Gates are
+// float64 sums, kept as two floats.
 //
 // In reversed time the same walk with (dy, q) for (v, k), weights e^{c_i} and
 // no reads gives the gradients of the states (muon_gated_scan_backward).
@@ -25,7 +26,7 @@ namespace {
 using namespace scan;
 
 // Waves that multiply, and one more that prepares the gates of the next chunk
-// while they do: its prefix sum in float64 is a long dependent chain.
+// while they do (not in the float32 forward walk).
 constexpr int kReadWaves = 8, kStatesWaves = 4;
 constexpr int kReadThreads = kReadWaves * kWave, kStatesThreads = kStatesWaves * kWave;
 constexpr int kStateCols = 64;   // columns n of S per workgroup of the states' walk
@@ -184,10 +185,15 @@ struct Walk {
   }
 };
 
-// States only: the state before every block of 2^keep_log2 chunks (in reversed time:
-// after it), a segment's total, or both.  The columns of S are independent, so
-// a workgroup takes kStateCols of them: three workgroups fit a compute unit and
-// fill the chip more evenly than one of twice the size.
+// States only: the state before every block of 2^keep_log2 chunks (in reversed
+// time: after it), or a segment's total.  The columns of S are independent, so
+// a workgroup takes kStateCols of them: several fit a compute unit and fill the
+// chip more evenly than ones of twice the size (125 -> 117 us where both
+// directions of eight sequences of 2,048 tokens, 24 heads, bfloat16, are walked).
+// S is held by rows, so that a lane stores 16 adjacent bytes of a state (117 ->
+// 97 us).  Of those 97 us about 40 are the 201 MB of float32 states that go to
+// HBM; the rest is issue: a wave's step is 180 vector, 24 matrix and 130 scalar
+// instructions, and splitting the values is half of the first.
 template <typename T, int NT, bool VEC>
 __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 ? 5 : 3) scan_states_kernel(WalkPair P) {
   constexpr int kParts = NT / kStateCols, KT = kStateCols / 16;
@@ -235,9 +241,21 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
   W.store_state();
 }
 
-// Outputs and states.  The tokens' products with the two halves of n are
-// partial sums of y, which the two waves of the same rows exchange through LDS,
-// each finishing half of the tokens.
+// Outputs and states.  Between two barriers: the tiles of M, what S_in gives
+// (partial sums over the two halves of n, which the two waves of the same rows
+// exchange through LDS, each finishing half of the tokens), and the next S; then
+// what the chunk's own tokens give, and the next chunk's tiles go to LDS.
+//
+// Eight sequences of 2,048 tokens, 24 heads of 64 x 128, bfloat16: 92 us (192
+// workgroups, 32 steps of about 6,500 clocks); HBM needs 112 MB, 22 us.  Bound
+// by issue and LDS together: a step is 2,200 clocks of vector and 1,400 of
+// matrix instructions a SIMD and 2,300 of LDS, and two waves a SIMD that meet
+// at barriers overlap little of it.  What made the step short: 16-byte LDS reads
+// without bank conflicts everywhere (107 -> 94 us, with two barriers instead of
+// three and the weighted values split once for all waves), the gates, whose
+// float64 prefix sum is a long chain, and two of the ten tiles of M on a wave of
+// their own.  Four waves that hold all columns take 123 us (two such workgroups
+// to a compute unit: 16,384 tokens, 24 heads, 118 us against 118).
 template <typename T, int NT, bool VEC>
 __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadThreads, sizeof(T) == 2 ? 3 : 2) scan_read_kernel(WalkPair P) {
   typedef Ops<T> O;
@@ -245,9 +263,10 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
   typedef Tile<T, NT> TN;
   typedef Tile<T, kQ> TM;
   constexpr int KT = NT / 32;
-  // arrays of their own: the compiler may move reads of one across writes to another
-  // bfloat16: the weighted values of a chunk are split once for all waves.
-  // x^T is read last in a chunk, when the next chunk's tiles are stored already.
+  // bfloat16: the weighted values of a chunk are split once for all waves, and
+  // x^T, which a chunk reads last, is double, so that the next chunk's tiles need
+  // no third barrier.  float32 values are not split, and its tiles fill the LDS.
+  // (Arrays of their own: the compiler may move reads of one across writes to another.)
   constexpr bool kPlanes = sizeof(T) == 2;
   __shared__ __attribute__((aligned(16))) T lkt[NT * kQ], lk[kQ * NT], lq[kQ * NT], lxts[kPlanes ? 2 : 1][kPB * kQ];
   __shared__ __attribute__((aligned(16))) T lxw[kPlanes ? 3 * kPB * kQ : 8];   // weighted x^T in three pieces
@@ -328,7 +347,7 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
     if constexpr (kPlanes) tx.store_split(lxw, gates[slot].in, tid);
   };
   load_tiles(W.cc0);
-  // float32: no ninth wave, whose registers the others need, and no step that waits for its gates
+  // float32: no ninth wave, whose registers the others need (77 tokens, 12 heads, N = 72: 23 us, 28 with it)
   GateLoad gl;
   const bool gate_wave = !kPlanes && w == kReadWaves - 1;
   if (gate_wave) {
@@ -358,9 +377,7 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
     for (int s = 0; s < KT / 2; ++s) {
       const Frag f = frag_from_acc<T>(W.st[2 * s], W.st[2 * s + 1]);
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        y[it] = O::mma(f, TN::row(lq, 16 * it + l16, nbase + 32 * s + 8 * g4), y[it]);
-      }
+      for (int it = 0; it < 4; ++it) y[it] = O::mma(f, TN::row(lq, 16 * it + l16, nbase + 32 * s + 8 * g4), y[it]);
     }
 #pragma unroll
     for (int it = 0; it < 4; ++it) y[it] *= G.first[16 * it + l16];
@@ -400,7 +417,9 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
 }
 
 // The state that each segment starts from, out of the segments' own totals
-// (in place: a total is read before its slot is overwritten).
+// (in place: a total is read before its slot is overwritten).  A thread an
+// element, segment after segment: 6 us for 24 heads of 64 x 128 and ten segments,
+// bound by the chain of loads.
 __global__ void __launch_bounds__(kStepThreads) scan_segments_kernel(WalkPair W, int nt) {
   const ScanWalk& A = W.w[blockIdx.z];
   const int e = static_cast<int>(blockIdx.y) * kStepThreads + static_cast<int>(threadIdx.x);   // of kPB * nt
@@ -465,8 +484,10 @@ hipError_t launch_scan_walk(const ScanWalk* walks, int dirs, bool read, bool vec
 }
 
 // ---------------------------------------------------------------------------
-// one token: S' = e^g S + b v k^T, y = S' q.  Reads and writes the state once;
-// a half-wave holds a row's N <= 128 elements, 4 consecutive ones a lane.
+// one token: S' = e^g S + b v k^T, y = S' q.  Reads and writes the state once,
+// which is what bounds it: 160 sequences of 24 heads, 64 x 128, take 55 us for
+// 252 MB (4.6 TB/s); one sequence is 5 us of launch and latency.  A half-wave
+// holds a row's N <= 128 elements, 4 consecutive ones a lane.
 // ---------------------------------------------------------------------------
 namespace {
 

@@ -307,6 +307,9 @@ constexpr int kScanChunk = 64;     // tokens per chunk
 constexpr int kScanGradBf16 = 128, kScanGradF32 = 64;   // tokens per workgroup of the backward pass
 constexpr int kScanRows = 64;      // state rows (value components) per workgroup
 constexpr int kScanMaxN = 128;     // largest key length
+// Kernels for up to 64 and up to 128 columns of the state: eight sequences of
+// 2,048 tokens with 24 heads and N = 64 take 80 us forward and 160 backward with
+// 64 columns, 84 and 222 padded to 128 (float32: 155 and 358, 252 and 582).
 inline int scan_padded_n(int n) { return n <= 64 ? 64 : 128; }
 struct SeqOperand {    // [batch][tokens][heads or groups][width], innermost stride 1
   const void* p;
@@ -333,7 +336,9 @@ struct ScanWalk {
 hipError_t launch_scan_walk(const ScanWalk* W, int dirs, bool read, bool vec, bool bf16, hipStream_t st);
 // Whether 16-byte buffer loads of rows of `width` elements fit an operand (es
 // bytes an element): every row starts aligned and holds whole pieces, rows do
-// not overlap, and a tile's rows lie within 32-bit offsets.
+// not overlap, and a tile's rows lie within 32-bit offsets.  Element by element,
+// eight sequences of 2,048 tokens, 24 heads, take 313 us forward and 620
+// backward, against 91 and 255.
 inline bool scan_vec(const SeqOperand& s, int width, int es) {
   const long long q = 16 / es;
   return (reinterpret_cast<uintptr_t>(s.p) & 15u) == 0 && s.sb % q == 0 && s.st % q == 0 && s.sh % q == 0 && width % q == 0 &&

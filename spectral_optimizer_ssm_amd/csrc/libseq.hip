@@ -59,8 +59,13 @@ int check_operands(const muon_scan_args* a) {
   return MUON_OK;
 }
 
-// Workgroups that fill 256 compute units: one of the forward walk or of the
-// backward pass on each (their tiles fill the LDS), two of the states' walk.
+// Where to stop cutting work: one workgroup of the forward walk or of the
+// backward pass for each of 256 compute units (their tiles fill its LDS), and
+// 384 walks of the states, which are lighter.  Measured with 24 heads of 64 x
+// 128 sharing keys, bfloat16: 16,384 tokens forward take 120 us with up to 256
+// walks, 127 with 512 and 154 with 170; 8,191 tokens backward 188 us with up to
+// 384, 190 with 256, 193 with 512 and 204 with 768; eight sequences of 2,048
+// tokens backward 238 us with 256 workgroups, 299 with 128 and 267 with 512.
 constexpr long long kReadFill = 256, kStatesFill = 384, kGradFill = 256;
 
 struct ScanPlan {
@@ -71,9 +76,12 @@ struct ScanPlan {
 // axis is cut into segments: their totals first, then all of them at once.
 // Each token is walked over twice, so segments have to fill otherwise idle
 // compute units.  Forward, the second walk is the longer one, and two segments
-// already win (24 heads of 16,384 tokens: 490 us in one, 137 in twenty); for
-// the backward pass both are the same walk, and it takes three.  A segment has
-// at least kSegChunks chunks.
+// already win (96 heads of 4,096 tokens: 130 us in two, 155 in one; 24 heads of
+// 16,384: 130 in ten, 594 in one).  For the backward pass both are the same
+// walk: 24 heads of 16,384 tokens take 327 us in eight and 442 in one, but 48
+// of 8,192 take 315 in four and 309 in one, so fewer than five are not cut.  A
+// segment has at least kSegChunks chunks (24 heads of 2,048 tokens forward:
+// 39 us with four, 44 with eight, and no less with two).
 constexpr int kSegChunks = 4;
 
 int grad_tokens(int dtype) { return dtype == MUON_BF16 ? kScanGradBf16 : kScanGradF32; }
@@ -92,7 +100,7 @@ int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
     return MUON_OK;
   }
   long long nseg = std::min<long long>((backward ? kStatesFill : kReadFill) / walks, p->nchunks / kSegChunks);
-  if (nseg < (backward ? 3 : 2)) nseg = 1;
+  if (nseg < (backward ? 5 : 2)) nseg = 1;
   p->seg_chunks = static_cast<int>((p->nchunks + nseg - 1) / nseg);
   p->nseg = (p->nchunks + p->seg_chunks - 1) / p->seg_chunks;
   const long long groups = static_cast<long long>(a->batch) * p->nblocks * a->groups;

@@ -7,7 +7,7 @@
 // second operand's row), rows 4 g + 0..3 (the first operand's).  Any
 // permutation of the contraction indices that both operands share gives the
 // same product, so a result kept in registers can be the next product's
-// operand without a trip through LDS (Frag::from_acc).  bfloat16 operands
+// operand without a trip through LDS (frag_from_acc).  bfloat16 operands
 // take one v_mfma_f32_16x16x32_bf16 per step, float32 ones eight
 // v_mfma_f32_16x16x4f32.
 #pragma once
@@ -41,11 +41,6 @@ struct Ops<bf16_t> {
   // 8 consecutive elements
   __device__ static __forceinline__ Frag row(const bf16_t* p) {
     return __builtin_bit_cast(Frag, *reinterpret_cast<const u32x4_t*>(p));
-  }
-  // two runs of 4 consecutive elements
-  __device__ static __forceinline__ Frag row2(const bf16_t* p, const bf16_t* q) {
-    const u32x2_t a = *reinterpret_cast<const u32x2_t*>(p), b = *reinterpret_cast<const u32x2_t*>(q);
-    return __builtin_bit_cast(Frag, u32x4_t{a[0], a[1], b[0], b[1]});
   }
   __device__ static __forceinline__ void widen(Frag f, float (&o)[8]) {
     const u32x4_t w = __builtin_bit_cast(u32x4_t, f);
@@ -93,6 +88,7 @@ struct Ops<float> {
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
     return c;
   }
+  // two runs of 4 consecutive elements
   __device__ static __forceinline__ Frag row2(const float* p, const float* q) {
     const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(q);
     return Frag{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
@@ -131,12 +127,7 @@ struct Tile {
   // 8 elements from column col, a multiple of 8
   __device__ static __forceinline__ Frag row(const T* tile, int row, int col) {
     if constexpr (sizeof(T) == 2) return O::row(tile + at(row, col));
-    else return row2(tile, row, col);
-  }
-  // elements col..col + 3 and col + D..col + D + 3
-  template <int D = 4>
-  __device__ static __forceinline__ Frag row2(const T* tile, int row, int col) {
-    return O::row2(tile + at(row, col), tile + at(row, col + D));
+    else return O::row2(tile + at(row, col), tile + at(row, col + 4));
   }
   __device__ static __forceinline__ void store8(T* tile, int row, int col, Frag f) {
     if constexpr (sizeof(T) == 2) {
@@ -200,9 +191,6 @@ __device__ __forceinline__ int xcd_item(int block, int items) {
 constexpr int kNowhere = 0x7ffffff0;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), bytes, 0x00020000);
-}
-__device__ __forceinline__ float load_f32(__amdgpu_buffer_rsrc_t r, int offset) {
-  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0));
 }
 __device__ __forceinline__ f32x4_t load_f32x4(__amdgpu_buffer_rsrc_t r, int offset, int base) {
   return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, offset, base, 0));
