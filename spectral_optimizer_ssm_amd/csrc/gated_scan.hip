@@ -11,8 +11,9 @@
 // the operand of S_in q without leaving the registers.
 //
 // Rounding, bfloat16 operands: the weights e^{c_i - c_j} b_j (q_i . k_j) and
-// the copy of S_in that is read are rounded to bfloat16 once, which leaves y
-// within its own rounding; the weighted values that enter the state are split
+// the copy of S_in that is read are rounded to bfloat16 once, which leaves the
+// error of y at 1.4 times that of its own rounding (at just that in sequences of
+// one chunk, where they are two pieces); the weighted values that enter the state are split
 // into three bfloat16 pieces, so the state keeps float32 accuracy.  Gates are
 // float64 sums, kept as two floats.
 //
@@ -254,9 +255,10 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
 // without bank conflicts everywhere (107 -> 94 us, with two barriers instead of
 // three and the weighted values split once for all waves), the gates, whose
 // float64 prefix sum is a long chain, and two of the ten tiles of M on a wave of
-// their own.  Four waves that hold all columns take 123 us (two such workgroups
+// their own.  PIECES: of M and of the copy of S_in that is read; a sequence of
+// one chunk takes two (see launch_scan_walk).  Four waves that hold all columns take 123 us (two such workgroups
 // to a compute unit: 16,384 tokens, 24 heads, 118 us against 118).
-template <typename T, int NT, bool VEC>
+template <typename T, int NT, bool VEC, int PIECES>
 __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadThreads, sizeof(T) == 2 ? 3 : 2) scan_read_kernel(WalkPair P) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
@@ -268,9 +270,10 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
   // no third barrier.  float32 values are not split, and its tiles fill the LDS.
   // (Arrays of their own: the compiler may move reads of one across writes to another.)
   constexpr bool kPlanes = sizeof(T) == 2;
+  static_assert(kPlanes || PIECES == 1, "pieces are bfloat16");
   __shared__ __attribute__((aligned(16))) T lkt[NT * kQ], lk[kQ * NT], lq[kQ * NT], lxts[kPlanes ? 2 : 1][kPB * kQ];
   __shared__ __attribute__((aligned(16))) T lxw[kPlanes ? 3 * kPB * kQ : 8];   // weighted x^T in three pieces
-  __shared__ __attribute__((aligned(16))) T lm[kQ * kQ];                       // the weights M [i][j]
+  __shared__ __attribute__((aligned(16))) T lm[PIECES * kQ * kQ];             // the weights M [i][j], in pieces
   __shared__ f32x4_t ly[kReadWaves * 2 * kWave];   // halves of y that waves hand over
   __shared__ Gates<kQ> gates[2];
   const ScanWalk A = P.w[0];
@@ -288,7 +291,11 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
     const int i0 = 16 * it + 4 * g4, j = 16 * jt + l16;
     a *= between4(G, it, jt, i0, j) * G.b[j];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) lm[TM::at(i0 + r, j)] = O::from_f32(a[r]);
+    for (int r = 0; r < 4; ++r) {
+      const T hi = O::from_f32(a[r]);
+      lm[TM::at(i0 + r, j)] = hi;
+      if constexpr (PIECES == 2) lm[kQ * kQ + TM::at(i0 + r, j)] = O::from_f32(a[r] - bf16_to_f32(hi));
+    }
   };
   if (kPlanes && w == kReadWaves) {
     // the ninth wave: two of the ten tiles of M, then the next chunk's gates
@@ -337,7 +344,7 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
   if (w < 2) {
     const int r0 = 32 * w, c0 = r0 + 16;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) lm[TM::at(r0 + l16, c0 + 4 * g4 + e)] = O::from_f32(0.0f);
+    for (int e = 0; e < 4 * PIECES; ++e) lm[e / 4 * kQ * kQ + TM::at(r0 + l16, c0 + 4 * g4 + e % 4)] = O::from_f32(0.0f);
   }
   const auto store_tiles = [&](int slot) {
     tk.store(lk, tid);
@@ -375,9 +382,16 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
     for (int it = 0; it < 4; ++it) y[it] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < KT / 2; ++s) {
-      const Frag f = frag_from_acc<T>(W.st[2 * s], W.st[2 * s + 1]);
+      const f32x4_t a = W.st[2 * s], b = W.st[2 * s + 1];
+      const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+      Frag f[PIECES];
+      O::split(v, f);
 #pragma unroll
-      for (int it = 0; it < 4; ++it) y[it] = O::mma(f, TN::row(lq, 16 * it + l16, nbase + 32 * s + 8 * g4), y[it]);
+      for (int it = 0; it < 4; ++it) {
+        const Frag qf = TN::row(lq, 16 * it + l16, nbase + 32 * s + 8 * g4);
+#pragma unroll
+        for (int u = PIECES - 1; u >= 0; --u) y[it] = O::mma(f[u], qf, y[it]);
+      }
     }
 #pragma unroll
     for (int it = 0; it < 4; ++it) y[it] *= G.first[16 * it + l16];
@@ -403,7 +417,10 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
       if (s <= nh) {
         const Frag vf = transposed_row(lxt, 16 * pw + l16, 32 * s + 8 * g4);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) y[u] = O::mma(vf, TM::row(lm, 32 * nh + 16 * u + l16, 32 * s + 8 * g4), y[u]);
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int z = PIECES - 1; z >= 0; --z)
+            y[u] = O::mma(vf, TM::row(lm + z * kQ * kQ, 32 * nh + 16 * u + l16, 32 * s + 8 * g4), y[u]);
       }
     const TileStore<T, VEC> out(yp, yst, W.rows_of(cc), W.rows_p);
     yp += W.step(yst);
@@ -440,24 +457,39 @@ __global__ void __launch_bounds__(kStepThreads) scan_segments_kernel(WalkPair W,
   sp[static_cast<long long>(A.nseg - 1) * kPB * nt] = cur;
 }
 
-template <typename T, int NT, bool READ, bool VEC>
-hipError_t walk(const WalkPair& W, int dirs, hipStream_t st) {
-  const ScanWalk& a = W.w[0];
-  constexpr int parts = READ ? 1 : NT / kStateCols, threads = READ ? kReadThreads + (sizeof(T) == 2 ? kWave : 0) : kStatesThreads + kWave;
-  const auto kernel = READ ? scan_read_kernel<T, NT, VEC> : scan_states_kernel<T, NT, VEC>;
-  const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg * parts;
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(items), dirs), dim3(threads), 0, st, W);
+template <typename T, int NT, bool VEC>
+hipError_t states(const WalkPair& W, int dirs, long long items, hipStream_t st) {
+  hipLaunchKernelGGL((scan_states_kernel<T, NT, VEC>), dim3(static_cast<unsigned>(items * (NT / kStateCols)), dirs),
+                     dim3(kStatesThreads + kWave), 0, st, W);
   return hipGetLastError();
 }
-
-template <typename T, int NT>
-hipError_t walk_any(const WalkPair& W, int dirs, bool read, bool vec, hipStream_t st) {
-  if (read) return vec ? walk<T, NT, true, true>(W, dirs, st) : walk<T, NT, true, false>(W, dirs, st);
-  return vec ? walk<T, NT, false, true>(W, dirs, st) : walk<T, NT, false, false>(W, dirs, st);
+template <typename T, int NT, bool VEC, int PIECES>
+hipError_t read(const WalkPair& W, long long items, hipStream_t st) {
+  hipLaunchKernelGGL((scan_read_kernel<T, NT, VEC, PIECES>), dim3(static_cast<unsigned>(items)),
+                     dim3(kReadThreads + (sizeof(T) == 2 ? kWave : 0)), 0, st, W);
+  return hipGetLastError();
 }
-hipError_t walk_any(const WalkPair& W, int dirs, bool read, bool vec, bool bf16, hipStream_t st) {
-  if (W.w[0].N <= 64) return bf16 ? walk_any<bf16_t, 64>(W, dirs, read, vec, st) : walk_any<float, 64>(W, dirs, read, vec, st);
-  return bf16 ? walk_any<bf16_t, 128>(W, dirs, read, vec, st) : walk_any<float, 128>(W, dirs, read, vec, st);
+template <typename T, int NT, bool VEC>
+hipError_t walk(const WalkPair& W, int dirs, bool reads, hipStream_t st) {
+  const ScanWalk& a = W.w[0];
+  const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg;
+  if (!reads) return states<T, NT, VEC>(W, dirs, items, st);
+  if constexpr (sizeof(T) == 2) {
+    // Rounding one of a few weights moves a whole row of y: with two tokens y is
+    // off by up to 1.5 times its own rounding.  Two pieces of weights and states
+    // leave only that, and 64 sequences of 64 tokens, 24 heads, take 69 us instead
+    // of 67; eight of 2,048, where the errors average out, would take 102 instead of 90.
+    if (a.nchunks == 1) return read<T, NT, VEC, 2>(W, items, st);
+  }
+  return read<T, NT, VEC, 1>(W, items, st);
+}
+template <typename T, int NT>
+hipError_t walk_any(const WalkPair& W, int dirs, bool reads, bool vec, hipStream_t st) {
+  return vec ? walk<T, NT, true>(W, dirs, reads, st) : walk<T, NT, false>(W, dirs, reads, st);
+}
+hipError_t walk_any(const WalkPair& W, int dirs, bool reads, bool vec, bool bf16, hipStream_t st) {
+  if (W.w[0].N <= 64) return bf16 ? walk_any<bf16_t, 64>(W, dirs, reads, vec, st) : walk_any<float, 64>(W, dirs, reads, vec, st);
+  return bf16 ? walk_any<bf16_t, 128>(W, dirs, reads, vec, st) : walk_any<float, 128>(W, dirs, reads, vec, st);
 }
 
 }  // namespace

@@ -26,7 +26,9 @@
 // 64 tokens would read and write twice the states.
 //
 // Rounding, bfloat16 operands: L A, the sum of L b E and the copy of dS_out
-// that dv reads are rounded to bfloat16 once; dq and dk take the states as
+// that dv reads are rounded to bfloat16 once, which leaves dv, dq and dk at 1.2 to
+// 1.4 times the error of their own rounding (at just that in sequences of one
+// chunk, where they are two pieces); dq and dk take the states as
 // three bfloat16 pieces (float32 accuracy), since db and dg, which are
 // float32, are dot products of them.
 #include <type_traits>
@@ -38,9 +40,9 @@ namespace {
 
 using namespace scan;
 
-// A block of Q tokens by 4 Q threads: 128 tokens with bfloat16 operands, 64
-// with float32 ones, whose tiles fill the LDS of a compute unit.
-template <typename T, int NT, int Q, bool VEC>
+// A block of Q tokens by 4 Q threads.  PIECES: bfloat16 pieces of the products'
+// rounded operands, L A, D and the copy of dS_out (see scan_grad_tokens).
+template <typename T, int NT, int Q, bool VEC, int PIECES>
 __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
@@ -56,11 +58,11 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
   // dv: four blocks of value rows, the tokens dealt to kTiles / 4 groups of waves
   constexpr int kZG = kTiles / 4;
   // dS_out [n][p] as the operand of dv goes where v was, if it fits
-  constexpr bool kStateInV = NT <= Q;
+  constexpr bool kStateInV = NT <= Q && PIECES == 1;
   // arrays of their own: the compiler may move reads of one across writes to another
   __shared__ __attribute__((aligned(16))) T lq[Q * NT], lk[Q * NT], lv[2 * Q * kPB];   // q; k; v and dy, at the end D [i][j]
-  __shared__ __attribute__((aligned(16))) T lm[Q * Q];                                  // (L A)^T [j][i], at the end D^T
-  static_assert(Q <= 2 * kPB, "D fits where v and dy were");
+  __shared__ __attribute__((aligned(16))) T lm[PIECES * Q * Q];                                  // (L A)^T [j][i], at the end D^T
+  static_assert(PIECES * Q <= 2 * kPB, "D fits where v and dy were");
   __shared__ Gates<Q> gates[2];
   // by token: row sums of W by column tile, column sums of L A E by row tile,
   // e^{c_i} q_i . S_in^T dy_i and e^{c_end - c_j} k_j . dS_out^T v_j by block of n
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
     if (w == kTiles - 1) next_gates(gates[0]);
   }
   // tiles of (L A)^T and slots of the sums that no wave writes
-  for (int i = tid; i < Q * Q; i += kThreads) lm[i] = O::from_f32(0.0f);
+  for (int i = tid; i < PIECES * Q * Q; i += kThreads) lm[i] = O::from_f32(0.0f);
   for (int i = tid; i < 4 * kTiles * Q; i += kThreads) lsums[0][i] = 0.0f;
   __syncthreads();
 
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
           cols[t] += we;
           rs[r] = we * b;
         }
-        TM::store4(lm, j, i0, mm);
+        TM::template store4_pieces<PIECES>(lm, Q * Q, j, i0, mm);
         const float row = sum_lanes4(rs[0], rs[1], rs[2], rs[3], l16);
         if (l16 < 4) lrow[jt * Q + i0 + l16] = row;
         settle(dsum[t]);
@@ -359,25 +361,30 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
         for (int u = 0; u < 4; ++u) {
           const int jt = kZG * u + (w >> 2);
           if (s >= kZG * u / 2)   // jt / 2: tiles above the diagonal are zero
-            z[u] = O::mma(f, TM::row(lm, 16 * jt + l16, 32 * s + 8 * g4), z[u]);
+#pragma unroll
+            for (int e = PIECES - 1; e >= 0; --e) z[u] = O::mma(f, TM::row(lm + e * Q * Q, 16 * jt + l16, 32 * s + 8 * g4), z[u]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (kStateInV) __syncthreads();   // dS_out is written
 #pragma unroll
       for (int s = 0; s < NT / 32; ++s) {
-        Frag f;
+        Frag f[PIECES];
         if constexpr (kStateInV) {
-          f = TP::col(lv, 32 * s, 16 * (w & 3), lane);
+          f[0] = TP::col(lv, 32 * s, 16 * (w & 3), lane);
         } else {
           float v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = dsp[state_offset(32 * s + 8 * g4 + e, 16 * (w & 3) + l16)];
-          f = O::narrow(v);
+          O::split(v, f);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          zs[u] = O::mma(f, TN::row(lk, 16 * (kZG * u + (w >> 2)) + l16, 32 * s + 8 * g4), zs[u]);
+        {
+          const Frag kf = TN::row(lk, 16 * (kZG * u + (w >> 2)) + l16, 32 * s + 8 * g4);
+#pragma unroll
+          for (int e = PIECES - 1; e >= 0; --e) zs[u] = O::mma(f[e], kf, zs[u]);
+        }
       }
       const TileStore<T, VEC> out(static_cast<T*>(A.dv) + ((bi * A.tokens + t0) * A.heads + h) * A.P + pb * kPB,
                                   static_cast<long long>(A.heads) * A.P, rows, rows_p_of(pb));
@@ -429,15 +436,19 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
   // D = sum over heads of L b E, once as D [i][j] (where v and dy were) and
   // once as D^T [j][i] (where (L A)^T was, whose other tiles are zero)
   T* ld = lv;
-  for (int i = tid; i < Q * Q; i += kThreads) ld[i] = O::from_f32(0.0f);
+  for (int i = tid; i < PIECES * Q * Q; i += kThreads) ld[i] = O::from_f32(0.0f);
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < kMaxTiles; ++t) {
     if (t + 1 < kMaxTiles || t < ntile) {
       const int j = 16 * tcol[t] + l16, i0 = 16 * trow[t] + 4 * g4;
-      TM::store4(lm, j, i0, dsum[t]);
+      TM::template store4_pieces<PIECES>(lm, Q * Q, j, i0, dsum[t]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) ld[TM::at(i0 + r, j)] = O::from_f32(dsum[t][r]);
+      for (int e = 0; e < PIECES; ++e) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ld[e * Q * Q + TM::at(i0 + r, j)] = O::from_f32(dsum[t][r]);
+        dsum[t] -= O::rounded4(dsum[t]);
+      }
     }
   }
   __syncthreads();
@@ -451,8 +462,11 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
       for (int u = 0; u < kTT; ++u) {
         const int it = u * kTG + tg;
         // tiles of D with j > i (of D^T with i < j) are zero
-        if (s <= (u * kTG + kTG - 1) / 2) dq[b][u] = O::mma(fk, TM::row(ld, 16 * it + l16, 32 * s + 8 * g4), dq[b][u]);
-        if (s >= u * kTG / 2) dk[b][u] = O::mma(fq, TM::row(lm, 16 * it + l16, 32 * s + 8 * g4), dk[b][u]);
+#pragma unroll
+        for (int e = PIECES - 1; e >= 0; --e) {
+          if (s <= (u * kTG + kTG - 1) / 2) dq[b][u] = O::mma(fk, TM::row(ld + e * Q * Q, 16 * it + l16, 32 * s + 8 * g4), dq[b][u]);
+          if (s >= u * kTG / 2) dk[b][u] = O::mma(fq, TM::row(lm + e * Q * Q, 16 * it + l16, 32 * s + 8 * g4), dk[b][u]);
+        }
       }
     }
     const int n = n0 + 4 * g4;
@@ -505,11 +519,10 @@ __global__ void __launch_bounds__(kPartThreads) scan_parts_kernel(const float* p
   else dk[i - half] = Ops<T>::from_f32(s);
 }
 
-template <typename T, int NT, bool VEC>
+template <typename T, int NT, int Q, bool VEC, int PIECES>
 hipError_t grad(const ScanGrad& A, hipStream_t st) {
-  constexpr int Q = sizeof(T) == 2 ? kScanGradBf16 : kScanGradF32;
   const long long items = static_cast<long long>(A.batch) * A.nblocks * A.groups * A.nsplit;
-  hipLaunchKernelGGL((scan_grad_kernel<T, NT, Q, VEC>), dim3(static_cast<unsigned>(items)), dim3(4 * Q), 0, st, A);
+  hipLaunchKernelGGL((scan_grad_kernel<T, NT, Q, VEC, PIECES>), dim3(static_cast<unsigned>(items)), dim3(4 * Q), 0, st, A);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || A.nsplit == 1) return e;
   const long long half = static_cast<long long>(A.batch) * A.tokens * A.groups * A.N;
@@ -518,15 +531,18 @@ hipError_t grad(const ScanGrad& A, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <int NT>
+hipError_t grad_bf16(const ScanGrad& A, bool vec, hipStream_t st) {
+  if (scan_grad_tokens(true, A.tokens) == 64) return vec ? grad<bf16_t, NT, 64, true, 2>(A, st) : grad<bf16_t, NT, 64, false, 2>(A, st);
+  return vec ? grad<bf16_t, NT, 128, true, 1>(A, st) : grad<bf16_t, NT, 128, false, 1>(A, st);
+}
+
 }  // namespace
 
 hipError_t launch_scan_grad(const ScanGrad& A, bool vec, bool bf16, hipStream_t st) {
-  if (bf16) {
-    if (A.N <= 64) return vec ? grad<bf16_t, 64, true>(A, st) : grad<bf16_t, 64, false>(A, st);
-    return vec ? grad<bf16_t, 128, true>(A, st) : grad<bf16_t, 128, false>(A, st);
-  }
-  if (A.N <= 64) return vec ? grad<float, 64, true>(A, st) : grad<float, 64, false>(A, st);
-  return vec ? grad<float, 128, true>(A, st) : grad<float, 128, false>(A, st);
+  if (bf16) return A.N <= 64 ? grad_bf16<64>(A, vec, st) : grad_bf16<128>(A, vec, st);
+  if (A.N <= 64) return vec ? grad<float, 64, 64, true, 1>(A, st) : grad<float, 64, 64, false, 1>(A, st);
+  return vec ? grad<float, 128, 64, true, 1>(A, st) : grad<float, 128, 64, false, 1>(A, st);
 }
 
 }  // namespace muon

@@ -304,7 +304,12 @@ hipError_t launch_adamw(const AdamwLaunch& A, bool grad_bf16, int blocks, hipStr
 
 // Gated scan (gated_scan.hip, gated_scan_backward.hip).
 constexpr int kScanChunk = 64;     // tokens per chunk
-constexpr int kScanGradBf16 = 128, kScanGradF32 = 64;   // tokens per workgroup of the backward pass
+// Tokens per workgroup of the backward pass: as many as the tiles in LDS allow,
+// 128 bfloat16 or 64 float32 ones; sequences of up to 64 tokens are one block of
+// 64, which leaves room for second pieces of the rounded operands: with a few
+// tokens a rounded weight moves a whole row, and dv would be off by up to twice
+// its own rounding.
+inline int scan_grad_tokens(bool bf16, int tokens) { return bf16 && tokens > kScanChunk ? 2 * kScanChunk : kScanChunk; }
 constexpr int kScanRows = 64;      // state rows (value components) per workgroup
 constexpr int kScanMaxN = 128;     // largest key length
 // Kernels for up to 64 and up to 128 columns of the state: eight sequences of
@@ -342,12 +347,12 @@ hipError_t launch_scan_walk(const ScanWalk* W, int dirs, bool read, bool vec, bo
 inline bool scan_vec(const SeqOperand& s, int width, int es) {
   const long long q = 16 / es;
   return (reinterpret_cast<uintptr_t>(s.p) & 15u) == 0 && s.sb % q == 0 && s.st % q == 0 && s.sh % q == 0 && width % q == 0 &&
-         s.st >= width && s.st * es * kScanGradBf16 < (1LL << 31) - 256;
+         s.st >= width && s.st * es * 2 * kScanChunk < (1LL << 31) - 256;
 }
 struct ScanGrad {
   SeqOperand v, k, q, dy, g, b;
   int batch, tokens, heads, groups, P, N, pblocks;
-  int nblocks;                // blocks of kScanGradBf16 (float32: kScanGradF32) tokens
+  int nblocks;                // blocks of scan_grad_tokens
   int nsplit;                 // workgroups that share a block's heads
   int dkvec;                  // rows of dq and dk: 4-element stores
   const float* states;        // as ScanWalk.states: before each block

@@ -84,12 +84,12 @@ struct ScanPlan {
 // 39 us with four, 44 with eight, and no less with two).
 constexpr int kSegChunks = 4;
 
-int grad_tokens(int dtype) { return dtype == MUON_BF16 ? kScanGradBf16 : kScanGradF32; }
+int grad_tokens(const muon_scan_args* a) { return scan_grad_tokens(a->dtype == MUON_BF16, a->tokens); }
 
 int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
   p->pblocks = (a->P + kScanRows - 1) / kScanRows;
   p->nchunks = static_cast<int>((static_cast<long long>(a->tokens) + kScanChunk - 1) / kScanChunk);
-  const int block = grad_tokens(a->dtype);
+  const int block = grad_tokens(a);
   p->nblocks = static_cast<int>((static_cast<long long>(a->tokens) + block - 1) / block);
   const long long vrows = static_cast<long long>(a->batch) * a->heads * p->pblocks;
   const long long walks = backward ? 2 * vrows : vrows;
@@ -146,7 +146,7 @@ ScanWalk walk_of(const muon_scan_args* a, const ScanPlan& p) {
   w.batch = a->batch; w.tokens = a->tokens; w.heads = a->heads; w.groups = a->groups;
   w.P = a->P; w.N = a->N;
   w.pblocks = p.pblocks; w.nchunks = p.nchunks; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
-  w.keep_log2 = grad_tokens(a->dtype) / kScanChunk / 2; w.nblocks = p.nblocks;
+  w.keep_log2 = grad_tokens(a) / kScanChunk / 2; w.nblocks = p.nblocks;
   w.init = a->S0;
   return w;
 }
@@ -154,7 +154,7 @@ ScanWalk walk_of(const muon_scan_args* a, const ScanPlan& p) {
 bool walk_vec(const ScanWalk& w, int es) { return scan_vec(w.x, w.P, es) && scan_vec(w.k, w.N, es); }
 // Rows of an output, `st` elements apart, take 4-element buffer stores.
 bool rows_out(const void* p, long long st, int width, int es) {
-  return width % 4 == 0 && aligned_to(p, 4 * es) && st * es * kScanGradBf16 < (1LL << 31) - 256;
+  return width % 4 == 0 && aligned_to(p, 4 * es) && st * es * 2 * kScanChunk < (1LL << 31) - 256;
 }
 
 size_t state_bytes(const muon_scan_args* a) { return static_cast<size_t>(a->batch) * a->heads * a->P * a->N * 4; }

@@ -54,19 +54,20 @@ struct Ops<bf16_t> {
     return __builtin_bit_cast(Frag, u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                             pack_bf16x2(v[6], v[7])});
   }
-  // acc += (float32 operand) b: the operand as three bfloat16 pieces (rounded,
-  // then the remainder, then its remainder), so its 24 bits all count
-  __device__ static __forceinline__ void split(const float (&v)[8], Frag (&f)[kSplit]) {
+  // a float32 operand as PIECES bfloat16 ones (rounded, then the remainder, then
+  // its remainder): kSplit for all of its 24 bits
+  template <int PIECES>
+  __device__ static __forceinline__ void split(const float (&v)[8], Frag (&f)[PIECES]) {
     float r[8], w[8];
-    f[0] = narrow(v);
-    widen(f[0], w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = v[i] - w[i];
-    f[1] = narrow(r);
-    widen(f[1], w);
+    for (int i = 0; i < 8; ++i) r[i] = v[i];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = r[i] - w[i];
-    f[2] = narrow(r);
+    for (int u = 0; u < PIECES; ++u) {
+      f[u] = narrow(r);
+      widen(f[u], w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r[i] = r[i] - w[i];
+    }
   }
   __device__ static __forceinline__ void store4(bf16_t* p, f32x4_t v) {
     *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
@@ -74,6 +75,10 @@ struct Ops<bf16_t> {
   __device__ static __forceinline__ f32x4_t load4(const bf16_t* p) {
     const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
     return f32x4_t{lo_bf16(w[0]), hi_bf16(w[0]), lo_bf16(w[1]), hi_bf16(w[1])};
+  }
+  __device__ static __forceinline__ f32x4_t rounded4(f32x4_t v) {
+    const uint32_t a = pack_bf16x2(v[0], v[1]), b = pack_bf16x2(v[2], v[3]);
+    return f32x4_t{lo_bf16(a), hi_bf16(a), lo_bf16(b), hi_bf16(b)};
   }
   __device__ static __forceinline__ bf16_t from_f32(float v) { return f32_to_bf16(v); }
 };
@@ -103,7 +108,9 @@ struct Ops<float> {
     for (int i = 0; i < 8; ++i) f.v[i] = v[i];
     return f;
   }
-  __device__ static __forceinline__ void split(const float (&v)[8], Frag (&f)[kSplit]) { f[0] = narrow(v); }
+  template <int PIECES>
+  __device__ static __forceinline__ void split(const float (&v)[8], Frag (&f)[PIECES]) { f[0] = narrow(v); }
+  __device__ static __forceinline__ f32x4_t rounded4(f32x4_t v) { return v; }
   __device__ static __forceinline__ void store4(float* p, f32x4_t v) { *reinterpret_cast<f32x4_t*>(p) = v; }
   __device__ static __forceinline__ f32x4_t load4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
   __device__ static __forceinline__ float from_f32(float v) { return v; }
@@ -156,6 +163,15 @@ struct Tile {
   }
   __device__ static __forceinline__ f32x4_t load4(const T* tile, int row, int col) { return O::load4(tile + at(row, col)); }
   __device__ static __forceinline__ void store4(T* tile, int row, int col, f32x4_t v) { O::store4(tile + at(row, col), v); }
+  // as PIECES tiles, `size` elements apart
+  template <int PIECES>
+  __device__ static __forceinline__ void store4_pieces(T* tile, int size, int row, int col, f32x4_t v) {
+#pragma unroll
+    for (int u = 0; u < PIECES; ++u) {
+      store4(tile + u * size, row, col, v);
+      if (u + 1 < PIECES) v -= O::rounded4(v);
+    }
+  }
 };
 
 // Fragment of a float32 result held in two accumulator tiles (rows 0..15 and
