@@ -517,9 +517,12 @@ hipError_t launch_scan_walk(const ScanWalk* walks, int dirs, bool read, bool vec
 
 // ---------------------------------------------------------------------------
 // one token: S' = e^g S + b v k^T, y = S' q.  Reads and writes the state once,
-// which is what bounds it: 160 sequences of 24 heads, 64 x 128, take 55 us for
-// 252 MB (4.6 TB/s); one sequence is 5 us of launch and latency.  A half-wave
-// holds a row's N <= 128 elements, 4 consecutive ones a lane.
+// which is what bounds it: 160 sequences of 24 heads, 64 x 128, take 56 us for
+// 252 MB (4.5 TB/s); one sequence is 4.5 us of launch and latency.  The state is
+// next read a token later, by when other layers' states have passed, so it is
+// stored past the caches (two such batches in turn: 66 -> 56 us; one alone the
+// same with either).  A half-wave holds a row's N <= 128 elements, 4 consecutive
+// ones a lane.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -587,7 +590,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanStep A) {
     float* op = A.S_out + (bh * A.P + p) * A.N + n0;
     if (n0 < A.N) {
       if (vec) {
-        *reinterpret_cast<f32x4_t*>(op) = s[u];
+        __builtin_nontemporal_store(s[u], reinterpret_cast<f32x4_t*>(op));
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
