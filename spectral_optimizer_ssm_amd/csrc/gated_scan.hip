@@ -517,16 +517,16 @@ hipError_t launch_scan_walk(const ScanWalk* walks, int dirs, bool read, bool vec
 
 // ---------------------------------------------------------------------------
 // one token: S' = e^g S + b v k^T, y = S' q.  Reads and writes the state once,
-// which is what bounds it: 160 sequences of 24 heads, 64 x 128, take 56 us for
-// 252 MB (4.5 TB/s); one sequence is 4.5 us of launch and latency.  The state is
-// next read a token later, by when other layers' states have passed, so it is
-// stored past the caches (two such batches in turn: 66 -> 56 us; one alone the
-// same with either).  A half-wave holds a row's N <= 128 elements, 4 consecutive
-// ones a lane.
+// which is what bounds it: 160 sequences of 24 heads, 64 x 128, take 49 us for
+// 252 MB (5.1 TB/s, the rate of a large copy); one sequence is 4.5 us of launch
+// and latency.  The state is next read a token later, by when other layers'
+// states have passed, so it goes past the caches (such batches in turn: 62 us
+// with stores past them, 71 without; 49 and 52 with loads past them or not).  A
+// half-wave holds a row's N <= 128 elements, 4 consecutive ones a lane.
 // ---------------------------------------------------------------------------
 namespace {
 
-constexpr int kStepRows = 16;   // state rows per workgroup: 8 half-waves, 2 rows each
+constexpr int kStepHalves = kStepThreads / 32;   // half-waves of a workgroup, a row of the state at a time
 
 template <typename T>
 __device__ __forceinline__ float load1(const T* p);
@@ -535,10 +535,12 @@ __device__ __forceinline__ float load1<bf16_t>(const bf16_t* p) { return bf16_to
 template <>
 __device__ __forceinline__ float load1<float>(const float* p) { return *p; }
 
-template <typename T>
+// EACH: rows of a half-wave, whose loads are under way together.
+template <typename T, int EACH>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanStep A) {
+  constexpr int kRows = EACH * kStepHalves;
   const int half = threadIdx.x >> 5, l = threadIdx.x & 31, n0 = 4 * l;
-  const int pblocks = (A.P + kStepRows - 1) / kStepRows;
+  const int pblocks = (A.P + kRows - 1) / kRows;
   const int pb = static_cast<int>(blockIdx.x) % pblocks;
   const long long bh = blockIdx.x / pblocks;
   const int h = static_cast<int>(bh % A.heads), grp = h / (A.heads / A.groups);
@@ -547,18 +549,18 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanStep A) {
   const T* kp = static_cast<const T*>(A.k.p) + bi * A.k.sb + grp * A.k.sh;
   const T* qp = static_cast<const T*>(A.q.p) + bi * A.q.sb + grp * A.q.sh;
   const bool vec = A.N % 4 == 0;   // rows of the state stay 16-byte aligned
-  f32x4_t s[2];
-  bool live[2];
-  const float* sp[2];
+  f32x4_t s[EACH];
+  bool live[EACH];
+  const float* sp[EACH];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int p = pb * kStepRows + 8 * u + half;
+  for (int u = 0; u < EACH; ++u) {
+    const int p = pb * kRows + kStepHalves * u + half;
     live[u] = p < A.P;
     sp[u] = A.S + (bh * A.P + p) * A.N + n0;
     s[u] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     if (live[u] && n0 < A.N) {
       if (vec) {
-        s[u] = *reinterpret_cast<const f32x4_t*>(sp[u]);
+        s[u] = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(sp[u]));
       } else {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -575,8 +577,8 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanStep A) {
   const float decay = expf(static_cast<const float*>(A.g.p)[bi * A.g.sb + h * A.g.sh]);
   const float gate = A.b.p == nullptr ? 1.0f : static_cast<const float*>(A.b.p)[bi * A.b.sb + h * A.b.sh];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int p = pb * kStepRows + 8 * u + half;
+  for (int u = 0; u < EACH; ++u) {
+    const int p = pb * kRows + kStepHalves * u + half;
     const float v = live[u] ? gate * load1<T>(vp + p) : 0.0f;
     float y = 0.0f;
 #pragma unroll
@@ -601,13 +603,23 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanStep A) {
   }
 }
 
+template <int EACH>
+hipError_t step(const ScanStep& A, bool bf16, hipStream_t st) {
+  constexpr int kRows = EACH * kStepHalves;
+  const dim3 grid(static_cast<unsigned>(static_cast<long long>(A.batch) * A.heads * ((A.P + kRows - 1) / kRows)));
+  if (bf16) hipLaunchKernelGGL((scan_step_kernel<bf16_t, EACH>), grid, dim3(kStepThreads), 0, st, A);
+  else hipLaunchKernelGGL((scan_step_kernel<float, EACH>), grid, dim3(kStepThreads), 0, st, A);
+  return hipGetLastError();
+}
+
 }  // namespace
 
+// Four rows a half-wave where that leaves two workgroups to each of 256 compute
+// units, two where it does not: 192 heads of 64 x 128 take 6.6 us by four and
+// 5.9 by two (24 heads 5.4 and 4.4), 384 heads 8.0 and 8.6, 1,536 heads 20 and 26.
 hipError_t launch_scan_step(const ScanStep& A, bool bf16, hipStream_t st) {
-  const long long blocks = static_cast<long long>(A.batch) * A.heads * ((A.P + kStepRows - 1) / kStepRows);
-  if (bf16) hipLaunchKernelGGL(scan_step_kernel<bf16_t>, dim3(static_cast<unsigned>(blocks)), dim3(kStepThreads), 0, st, A);
-  else hipLaunchKernelGGL(scan_step_kernel<float>, dim3(static_cast<unsigned>(blocks)), dim3(kStepThreads), 0, st, A);
-  return hipGetLastError();
+  const long long rows = static_cast<long long>(A.batch) * A.heads * A.P;
+  return rows >= 2LL * 256 * 4 * kStepHalves ? step<4>(A, bf16, st) : step<2>(A, bf16, st);
 }
 
 namespace {

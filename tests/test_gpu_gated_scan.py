@@ -324,6 +324,19 @@ def test_step(mu, shape, dtype, in_place):
     assert ref.rel(y, yr[:, 0]) <= (BF16_TOL if dtype == BF16 else F32_TOL)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(13, 24, 1, 60, 128), (12, 24, 2, 64, 99), (300, 4, 1, 17, 72), (64, 2, 2, 130, 36)], ids=str)
+def test_step_of_batches(mu, shape, dtype):
+    """More than 16,384 rows of states, which take four rows a half-wave."""
+    B, H, G, P, N = shape
+    x = inputs(B, 1, H, G, P, N, dtype, seed=14)
+    yr, Sr, _ = ref.scan(x["v"], x["k"], x["q"], x["g"], x["b"], x["S0"])
+    S = x["S0"].cuda()
+    y, _ = mu.muon_gated_scan_step(*(x[n][:, 0].cuda() for n in ("v", "k", "q", "g")), S, gate=x["b"][:, 0].cuda())
+    assert ref.rel(S, Sr) <= F32_TOL
+    assert ref.rel(y, yr[:, 0]) <= (BF16_TOL if dtype == BF16 else F32_TOL)
+
+
 def test_steps_are_the_scan(mu):
     """Token by token from the state that a prompt's scan left, a reset among
     the tokens, without a gate."""
