@@ -380,7 +380,6 @@ struct NormLaunch {
   void* y;
   long long ldx, ldy, rows;
   int n, center;
-  int vec;             // rows of x and y, w and bias 16-byte aligned, n a multiple of 16 bytes of them
   const float *w, *bias;   // may be null
   float eps;
   float *mean, *rstd;      // [rows], may be null
@@ -390,7 +389,7 @@ struct NormGradLaunch {
   const void *dy, *x;
   void* dx;
   long long lddy, ldx, lddx, rows;
-  int n, vec;              // vec: rows and w 16-byte aligned, n a multiple of 16 bytes of a row
+  int n;
   const float* w;          // may be null
   const float *mean, *rstd;   // mean null: no centering
   float *dw, *dbias;       // may be null

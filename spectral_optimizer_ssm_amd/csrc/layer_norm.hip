@@ -12,8 +12,8 @@
 // column sum per element of its registers over all the rows that it walks, with
 // the next row's loads in flight; the workgroups' sums go to the workspace and a
 // second kernel adds them in fixed order.  16,384 bfloat16 rows of 768 take
-// 12 us forward (50 MB, 4.2 TB/s) and 22 us backward (75 MB, 19 us of it the
-// walk at 4.0 TB/s).
+// 12 us forward (50 MB, 4.2 TB/s) and 21 us backward (75 MB, 18 us of it the
+// walk at 4.2 TB/s).
 #include "launch.h"
 
 namespace muon {
@@ -27,70 +27,66 @@ struct Vec {
   static constexpr int n = 16 / static_cast<int>(sizeof(T));   // elements of a piece
 };
 
-// Element e of piece i of thread t, of the TPR that share a row.  Aligned rows
-// (VEC): 16 adjacent bytes a piece.  Others, which have no such pieces:
-// neighbouring threads take neighbouring elements (16,384 bfloat16 rows of 768,
-// 769 apart: 25 us forward and 76 backward, 12 and 22 aligned).
-template <typename T, int TPR, bool VEC>
-__device__ __forceinline__ int col_of(int i, int e, int t) {
-  return VEC ? (i * TPR + t) * Vec<T>::n + e : (i * Vec<T>::n + e) * TPR + t;
-}
+// Piece i of a row of n elements that thread t takes, of the TPR that share it:
+// 16 adjacent bytes from element `base`, of which those from `first` on count.
+// The memory takes 16 bytes at any address, so rows need no alignment, and a
+// piece that would pass the row's end is moved back to end with it: what it then
+// shares with its neighbour both compute and store alike, and only one counts in
+// sums (16,384 bfloat16 rows of 767: 13 us forward and 22 backward, as of 768).
+template <typename T, int TPR>
+struct Piece {
+  static constexpr int V = Vec<T>::n;
+  int base, first;
+  __device__ __forceinline__ Piece(int i, int t, int n) {
+    const int col = (i * TPR + t) * V;
+    base = col < n - V ? col : n - V;
+    first = col - base;
+  }
+  __device__ __forceinline__ bool any() const { return first < V; }
+  __device__ __forceinline__ bool counts(int e) const { return e >= first; }
+};
 
-// Piece i of a row as floats (0 past the end); U: of the row's type, or the
-// float parameters at the same columns.
-template <typename T, typename U, int TPR, bool VEC>
-__device__ __forceinline__ void load_piece(const U* row, int i, int t, int n, float (&o)[Vec<T>::n]) {
-  if constexpr (VEC) {
-    const int col = col_of<T, TPR, VEC>(i, 0, t);
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+template <typename T, int TPR>
+__device__ __forceinline__ u32x4_t load_raw(const T* row, int i, int t, int n) {
+  return *reinterpret_cast<const u32x4_any*>(row + Piece<T, TPR>(i, t, n).base);
+}
+template <typename T>
+__device__ __forceinline__ void unpack(u32x4_t w, float (&o)[Vec<T>::n]) {
 #pragma unroll
-    for (int k = 0; k < Vec<T>::n * static_cast<int>(sizeof(U)) / 16; ++k) {
-      u32x4_t w = {0u, 0u, 0u, 0u};
-      if (col < n) w = reinterpret_cast<const u32x4_t*>(row + col)[k];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(U) == 2) {
-          o[2 * e] = lo_bf16(w[e]);
-          o[2 * e + 1] = hi_bf16(w[e]);
-        } else {
-          o[4 * k + e] = __uint_as_float(w[e]);
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < Vec<T>::n; ++e) {
-      const int col = col_of<T, TPR, VEC>(i, e, t);
-      o[e] = 0.0f;
-      if (col < n) {
-        if constexpr (sizeof(U) == 2) o[e] = bf16_to_f32(row[col]);
-        else o[e] = row[col];
-      }
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (sizeof(T) == 2) {
+      o[2 * e] = lo_bf16(w[e]);
+      o[2 * e + 1] = hi_bf16(w[e]);
+    } else {
+      o[e] = __uint_as_float(w[e]);
     }
   }
 }
+// The float parameters at a piece's columns.
+template <typename T, int TPR>
+__device__ __forceinline__ void load_param(const float* row, int i, int t, int n, float (&o)[Vec<T>::n]) {
+  const float* p = row + Piece<T, TPR>(i, t, n).base;
+#pragma unroll
+  for (int e = 0; e < Vec<T>::n; e += 4) {
+    const u32x4_t w = *reinterpret_cast<const u32x4_any*>(p + e);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[e + k] = __uint_as_float(w[k]);
+  }
+}
 
-template <typename T, int TPR, bool VEC>
+template <typename T, int TPR>
 __device__ __forceinline__ void store_piece(T* row, int i, int t, int n, const float (&v)[Vec<T>::n]) {
-  if constexpr (VEC) {
-    const int col = col_of<T, TPR, VEC>(i, 0, t);
-    if (col >= n) return;
-    u32x4_t w;
+  const Piece<T, TPR> p(i, t, n);
+  if (!p.any()) return;
+  u32x4_t w;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (sizeof(T) == 2) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-      else w[e] = __float_as_uint(v[e]);
-    }
-    *reinterpret_cast<u32x4_t*>(row + col) = w;
-  } else {
-#pragma unroll
-    for (int e = 0; e < Vec<T>::n; ++e) {
-      const int col = col_of<T, TPR, VEC>(i, e, t);
-      if (col < n) {
-        if constexpr (sizeof(T) == 2) row[col] = f32_to_bf16(v[e]);
-        else row[col] = v[e];
-      }
-    }
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (sizeof(T) == 2) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+    else w[e] = __float_as_uint(v[e]);
   }
+  *reinterpret_cast<u32x4_any*>(row + p.base) = w;
 }
 
 // Sum over the TPR threads that share a row; every thread gets it.
@@ -105,33 +101,37 @@ template <int TPR>
 constexpr int threads_of() { return TPR < kThreads ? kThreads : TPR; }
 
 // PIECES pieces of a row a thread, TPR threads a row.
-template <typename T, int TPR, int PIECES, bool VEC>
+template <typename T, int TPR, int PIECES>
 __global__ void __launch_bounds__(threads_of<TPR>()) norm_kernel(NormLaunch A) {
   constexpr int V = Vec<T>::n, kRows = threads_of<TPR>() / TPR;
   __shared__ float red[threads_of<TPR>() / kWave];
-  const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  const int sub = kRows == 1 ? 0 : threadIdx.x / TPR, t = threadIdx.x % TPR;
   const long long row = static_cast<long long>(blockIdx.x) * kRows + sub;
   if (row >= A.rows) return;   // whole waves or whole workgroups
   const T* x = static_cast<const T*>(A.x) + row * A.ldx;
   float v[PIECES][V];
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i) load_piece<T, T, TPR, VEC>(x, i, t, A.n, v[i]);
+  for (int i = 0; i < PIECES; ++i) unpack<T>(load_raw<T, TPR>(x, i, t, A.n), v[i]);
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i)
+  for (int i = 0; i < PIECES; ++i) {
+    const Piece<T, TPR> p(i, t, A.n);
 #pragma unroll
-    for (int e = 0; e < V; ++e) s += v[i][e];
+    for (int e = 0; e < V; ++e) s += p.counts(e) ? v[i][e] : 0.0f;
+  }
   const float inv_n = 1.0f / static_cast<float>(A.n);
   const float mu = A.center ? row_total<TPR>(s, red) * inv_n : 0.0f;
   float q = 0.0f;
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i)
+  for (int i = 0; i < PIECES; ++i) {
+    const Piece<T, TPR> p(i, t, A.n);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const float d = col_of<T, TPR, VEC>(i, e, t) < A.n ? v[i][e] - mu : 0.0f;
-      v[i][e] = d;
+      v[i][e] -= mu;
+      const float d = p.counts(e) ? v[i][e] : 0.0f;
       q = fmaf(d, d, q);
     }
+  }
   const float r = 1.0f / sqrtf(row_total<TPR>(q, red) * inv_n + A.eps);
   T* y = static_cast<T*>(A.y) + row * A.ldy;
 #pragma unroll
@@ -140,16 +140,16 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_kernel(NormLaunch A) {
 #pragma unroll
     for (int e = 0; e < V; ++e) v[i][e] *= r;
     if (A.w != nullptr) {
-      load_piece<T, float, TPR, VEC>(A.w, i, t, A.n, p);
+      load_param<T, TPR>(A.w, i, t, A.n, p);
 #pragma unroll
       for (int e = 0; e < V; ++e) v[i][e] *= p[e];
     }
     if (A.bias != nullptr) {
-      load_piece<T, float, TPR, VEC>(A.bias, i, t, A.n, p);
+      load_param<T, TPR>(A.bias, i, t, A.n, p);
 #pragma unroll
       for (int e = 0; e < V; ++e) v[i][e] += p[e];
     }
-    store_piece<T, TPR, VEC>(y, i, t, A.n, v[i]);
+    store_piece<T, TPR>(y, i, t, A.n, v[i]);
   }
   if (t == 0) {
     if (A.mean != nullptr) A.mean[row] = mu;
@@ -196,17 +196,17 @@ __global__ void __launch_bounds__(kThreads) norm_long_kernel(NormLaunch A) {
 
 // Workgroup b walks rows b kRows + 0.., a grid apart, and leaves its column
 // sums in part[b][2][n] (or, alone in the grid, in dw and dbias).
-template <typename T, int TPR, int PIECES, bool VEC>
+template <typename T, int TPR, int PIECES>
 __global__ void __launch_bounds__(threads_of<TPR>()) norm_grad_kernel(NormGradLaunch A) {
   constexpr int V = Vec<T>::n, kAll = threads_of<TPR>(), kRows = kAll / TPR;
   __shared__ float red[kAll / kWave];
   __shared__ float cols[TPR == kWave ? kWave * V * PIECES : 1];
-  const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  const int sub = kRows == 1 ? 0 : threadIdx.x / TPR, t = threadIdx.x % TPR;
   const float inv_n = 1.0f / static_cast<float>(A.n);
   float wv[PIECES][V], dw[PIECES][V], db[PIECES][V];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
-    if (A.w != nullptr) load_piece<T, float, TPR, VEC>(A.w, i, t, A.n, wv[i]);
+    if (A.w != nullptr) load_param<T, TPR>(A.w, i, t, A.n, wv[i]);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if (A.w == nullptr) wv[i][e] = 1.0f;
@@ -215,14 +215,15 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_grad_kernel(NormGradLa
   }
   const long long step = static_cast<long long>(gridDim.x) * kRows;
   const bool center = A.mean != nullptr;
-  float xn[PIECES][V], gn[PIECES][V], mun = 0.0f, rn = 0.0f;
+  u32x4_t xn[PIECES], gn[PIECES];   // the next row's, as they are loaded
+  float mun = 0.0f, rn = 0.0f;
   const auto load_row = [&](long long row) {
     const T* x = static_cast<const T*>(A.x) + row * A.ldx;
     const T* dy = static_cast<const T*>(A.dy) + row * A.lddy;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      load_piece<T, T, TPR, VEC>(x, i, t, A.n, xn[i]);
-      load_piece<T, T, TPR, VEC>(dy, i, t, A.n, gn[i]);
+      xn[i] = load_raw<T, TPR>(x, i, t, A.n);
+      gn[i] = load_raw<T, TPR>(dy, i, t, A.n);
     }
     mun = center ? A.mean[row] : 0.0f;
     rn = A.rstd[row];
@@ -233,25 +234,28 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_grad_kernel(NormGradLa
     float xh[PIECES][V], g[PIECES][V];
     const float mu = mun, r = rn;
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        xh[i][e] = xn[i][e];
-        g[i][e] = gn[i][e];
-      }
+    for (int i = 0; i < PIECES; ++i) {
+      asm volatile("" : "+v"(xn[i]), "+v"(gn[i]));   // unpacked here, not where they were loaded, in twice the registers
+      unpack<T>(xn[i], xh[i]);
+      unpack<T>(gn[i], g[i]);
+    }
     load_row(row + step < A.rows ? row + step : row);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i)
+    for (int i = 0; i < PIECES; ++i) {
+      const Piece<T, TPR> p(i, t, A.n);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        xh[i][e] = (xh[i][e] - mu) * r;   // past the row: times g = 0
+        xh[i][e] = (xh[i][e] - mu) * r;
         dw[i][e] = fmaf(g[i][e], xh[i][e], dw[i][e]);
         db[i][e] += g[i][e];
         g[i][e] *= wv[i][e];
-        s1 += g[i][e];
-        s2 = fmaf(g[i][e], xh[i][e], s2);
+        const float c = p.counts(e) ? g[i][e] : 0.0f;
+        s1 += c;
+        s2 = fmaf(c, xh[i][e], s2);
       }
+    }
+    asm volatile("" : "+v"(s1), "+v"(s2));   // both summed up before the branch: their terms take no registers across it
     s1 = center ? row_total<TPR>(s1, red) * inv_n : 0.0f;
     s2 = row_total<TPR>(s2, red) * inv_n;
     T* dx = static_cast<T*>(A.dx) + row * A.lddx;
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_grad_kernel(NormGradLa
     for (int i = 0; i < PIECES; ++i) {
 #pragma unroll
       for (int e = 0; e < V; ++e) g[i][e] = r * (g[i][e] - s1 - xh[i][e] * s2);
-      store_piece<T, TPR, VEC>(dx, i, t, A.n, g[i]);
+      store_piece<T, TPR>(dx, i, t, A.n, g[i]);
     }
   }
   float* out[2] = {A.dw, A.dbias};
@@ -284,17 +288,18 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_grad_kernel(NormGradLa
       }
       __syncthreads();
       for (int j = threadIdx.x; j < kWave * V * PIECES; j += kAll) {
-        const int slot = j / kWave, col = col_of<T, TPR, VEC>(slot / V, slot % V, j % kWave);
-        if (col < A.n) to[col] = cols[j];
+        const int slot = j / kWave;
+        const Piece<T, TPR> p(slot / V, j % kWave, A.n);
+        if (p.counts(slot % V)) to[p.base + slot % V] = cols[j];
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i)
+      for (int i = 0; i < PIECES; ++i) {
+        const Piece<T, TPR> p(i, t, A.n);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int col = col_of<T, TPR, VEC>(i, e, t);
-          if (col < A.n) to[col] = acc[i][e];
-        }
+        for (int e = 0; e < V; ++e)
+          if (p.counts(e)) to[p.base + e] = acc[i][e];
+      }
     }
   }
 }
@@ -363,16 +368,18 @@ __global__ void __launch_bounds__(kPartWaves * kWave) norm_parts_kernel(const fl
   }
 }
 
-// Threads that share a row of n elements (0: more than a workgroup holds) and
+// Threads that share a row of n elements (0: more than a workgroup holds, or less
+// than a piece) and
 // the pieces of it that each takes: as few threads as hold it.  A wave needs no
-// barrier: 8,192 bfloat16 rows of 2,048 take 14 us forward and 29 backward by
-// waves, 27 and 83 by workgroups.  Reading a row again costs more than a larger
-// workgroup: 1,024 rows of 16,384 take 17 us by 512 threads that hold it, 65
-// read in three passes.
+// barrier: 8,192 bfloat16 rows of 2,048 take 15 us forward and 25 backward by
+// waves, 29 and 80 by workgroups.  Reading a row again costs more than a larger
+// workgroup: 1,024 rows of 16,384 take 15 and 52 us by 512 threads that hold it,
+// 65 and 323 read in passes.
 struct RowPlan {
   int threads, pieces;
 };
 RowPlan row_plan(int n, int elems) {
+  if (n < elems) return {0, 0};
   for (int t : {kWave, kThreads, 2 * kThreads}) {
     const int p = (n + elems * t - 1) / (elems * t);
     if (p <= kPieces) return {t, p <= 1 ? 1 : p <= 2 ? 2 : 4};
@@ -384,8 +391,7 @@ template <typename T, int TPR, int PIECES>
 hipError_t norm(const NormLaunch& A, hipStream_t st) {
   constexpr int kRows = threads_of<TPR>() / TPR;
   const dim3 grid(static_cast<unsigned>((A.rows + kRows - 1) / kRows)), block(threads_of<TPR>());
-  if (A.vec) hipLaunchKernelGGL((norm_kernel<T, TPR, PIECES, true>), grid, block, 0, st, A);
-  else hipLaunchKernelGGL((norm_kernel<T, TPR, PIECES, false>), grid, block, 0, st, A);
+  hipLaunchKernelGGL((norm_kernel<T, TPR, PIECES>), grid, block, 0, st, A);
   return hipGetLastError();
 }
 
@@ -402,8 +408,7 @@ hipError_t norm_any(const NormLaunch& A, hipStream_t st) {
 template <typename T, int TPR, int PIECES>
 hipError_t grad(const NormGradLaunch& A, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(A.parts)), block(threads_of<TPR>());
-  if (A.vec) hipLaunchKernelGGL((norm_grad_kernel<T, TPR, PIECES, true>), grid, block, 0, st, A);
-  else hipLaunchKernelGGL((norm_grad_kernel<T, TPR, PIECES, false>), grid, block, 0, st, A);
+  hipLaunchKernelGGL((norm_grad_kernel<T, TPR, PIECES>), grid, block, 0, st, A);
   return hipGetLastError();
 }
 
@@ -432,13 +437,14 @@ hipError_t grad_any(const NormGradLaunch& A, hipStream_t st) {
 // Workgroups of the backward pass: enough to fill the chip, where there are that
 // many rows eight to a wave, or four to a workgroup that takes a row together,
 // since each leaves 2 n sums to be added: 1,024 bfloat16 rows of 16,384 take
-// 47 us four to a workgroup, 74 two and 64 sixteen.  At most 512: 65,536 rows of
-// 768 take 72 us with 512, 114 with 256, 82 with 1,024.
+// 52 us four to a workgroup, 80 two and 77 sixteen.  At most 512 (65,536 rows of
+// 768: 70 us, 100 with 256, 76 with 1,024), or 256 of 512 threads, of which a
+// compute unit holds one (1,031 float32 rows of 4,099: 21 us, 28 with 258).
 int norm_grad_parts(long long rows, int n, bool bf16) {
   const RowPlan p = row_plan(n, bf16 ? Vec<bf16_t>::n : Vec<float>::n);
-  const long long per = p.threads == kWave ? 8LL * kThreads / kWave : 4;
+  const long long per = p.threads == kWave ? 8LL * kThreads / kWave : 4, most = p.threads == 2 * kThreads ? 256 : 512;
   const long long want = (rows + per - 1) / per;
-  return static_cast<int>(want < 1 ? 1 : want > 512 ? 512 : want);
+  return static_cast<int>(want < 1 ? 1 : want > most ? most : want);
 }
 
 hipError_t launch_norm(const NormLaunch& A, bool bf16, hipStream_t st) {

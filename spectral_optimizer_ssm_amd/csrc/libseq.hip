@@ -324,10 +324,6 @@ int check_norm(int dtype, long long rows, int n) {
 Span rows_span(const void* p, long long rows, int n, long long ld, size_t es) {
   return span(p, rows == 0 ? 0 : static_cast<size_t>((rows - 1) * ld + n) * es);
 }
-bool rows_vec(const void* p, long long ld, int n, size_t es) {
-  const long long q = 16 / static_cast<long long>(es);
-  return aligned16(p) && ld % q == 0 && n % q == 0;
-}
 
 }  // namespace
 
@@ -347,7 +343,6 @@ int muon_layer_norm(const void* X, long long ldx, int dtype, long long rows, int
     return MUON_EINVAL;
   NormLaunch A{};
   A.x = X; A.y = Y; A.ldx = ldx; A.ldy = ldy; A.rows = rows; A.n = n; A.center = center;
-  A.vec = rows_vec(X, ldx, n, es) && rows_vec(Y, ldy, n, es) && aligned16(weight) && aligned16(bias);
   A.w = weight; A.bias = bias; A.eps = eps; A.mean = mean; A.rstd = rstd;
   return launch_norm(A, dtype == MUON_BF16, static_cast<hipStream_t>(stream)) == hipSuccess ? MUON_OK : MUON_EHIP;
 }
@@ -377,7 +372,6 @@ int muon_layer_norm_backward(const void* dY, long long lddy, const void* X, long
     return MUON_EINVAL;
   NormGradLaunch A{};
   A.dy = dY; A.x = X; A.dx = dX; A.lddy = lddy; A.ldx = ldx; A.lddx = lddx; A.rows = rows; A.n = n;
-  A.vec = rows_vec(dY, lddy, n, es) && rows_vec(X, ldx, n, es) && rows_vec(dX, lddx, n, es) && aligned16(weight);
   A.w = weight; A.mean = mean; A.rstd = rstd; A.dw = dweight; A.dbias = dbias;
   A.part = static_cast<float*>(workspace);
   A.parts = norm_grad_parts(rows, n, dtype == MUON_BF16);

@@ -102,6 +102,21 @@ def test_norm_one_or_two_elements(mu, rows, n, dtype, center):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n", [255, 257, 511, 513, 1023, 1025, 2047, 2049, 4095, 4097, 8191, 8193, 16383, 16385])
+def test_norm_lengths(mu, n, dtype):
+    """Around the lengths where rows take another share of threads; rows that
+    end inside a piece of 16 bytes."""
+    check(mu, *inputs(9, n, dtype, seed=n), True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n", [3, 4, 5, 7, 8, 9])
+def test_norm_short_rows(mu, n, dtype):
+    """Rows of about one piece of 16 bytes: few elements, so by element."""
+    test_norm_one_or_two_elements(mu, 9, n, dtype, True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_norm_without_parameters(mu, dtype):
     check(mu, *inputs(50, 300, dtype, affine=False), True)
 
