@@ -101,6 +101,11 @@ struct Walk {
   __device__ __forceinline__ long long token_of(int cc) const { return static_cast<long long>(chunk_of(cc < cc1 ? cc : cc0)) * kQ; }
   // elements from a chunk to the next one visited, of rows `st` apart
   __device__ __forceinline__ long long step(long long st) const { return (reverse ? -kQ : kQ) * st; }
+  // Columns from n on, or tokens from t of a chunk with `rows`, are padding:
+  // float32 products, which their matrix instructions bound, leave it out (77
+  // tokens, 12 heads, N = 72: 24 -> 19 us).
+  __device__ __forceinline__ bool padding(int n) const { return sizeof(T) == 4 && n >= A.N; }
+  static __device__ __forceinline__ bool ended(int t, int rows) { return sizeof(T) == 4 && t >= rows; }
   // element r of tile t
   __device__ __forceinline__ int n_of(int t, int r) const { return nbase + (READ ? state_row(t, 4 * g4) + r : 16 * t + l16); }
   __device__ __forceinline__ int p_of(int r) const { return 16 * pw + (READ ? l16 : 4 * g4 + r); }
@@ -157,12 +162,13 @@ struct Walk {
   // S = e^{c_end} S + sum_j in_j x_j k_j^T; this wave's columns: from row n0 of
   // lkt.  The weighted values, in pieces: `values(s, f)` for tokens 32 s + 0..31.
   template <typename F>
-  __device__ __forceinline__ void update(const Gates<kQ>& G, const T* lkt, int n0, F values) {
+  __device__ __forceinline__ void update(const Gates<kQ>& G, const T* lkt, int n0, int rows, F values) {
     const float end = G.end[0];
 #pragma unroll
     for (int t = 0; t < KT; ++t) st[t] *= end;
 #pragma unroll
     for (int s = 0; s < kQ / 32; ++s) {
+      if (ended(32 * s, rows)) continue;
       Frag f[O::kSplit], kf[KT];
       values(s, f);
 #pragma unroll
@@ -170,12 +176,13 @@ struct Walk {
 #pragma unroll
       for (int u = O::kSplit - 1; u >= 0; --u)
 #pragma unroll
-        for (int t = 0; t < KT; ++t) st[t] = READ ? O::mma(kf[t], f[u], st[t]) : O::mma(f[u], kf[t], st[t]);
+        for (int t = 0; t < KT; ++t)
+          if (!padding(nbase + (READ ? 32 * (t / 2) : 16 * t))) st[t] = READ ? O::mma(kf[t], f[u], st[t]) : O::mma(f[u], kf[t], st[t]);
     }
   }
   // ... weighted and split here
-  __device__ __forceinline__ void update_from(const Gates<kQ>& G, const T* lkt, int n0, const T* lxt) {
-    update(G, lkt, n0, [&](int s, Frag (&f)[O::kSplit]) {
+  __device__ __forceinline__ void update_from(const Gates<kQ>& G, const T* lkt, int n0, int rows, const T* lxt) {
+    update(G, lkt, n0, rows, [&](int s, Frag (&f)[O::kSplit]) {
       float xv[8], wv[8];
       O::widen(transposed_row(lxt, 16 * pw + l16, 32 * s + 8 * g4), xv);
       load8(G.in + 32 * s + 8 * g4, wv);
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
 #pragma unroll
       for (int t = 0; t < KT; ++t) *reinterpret_cast<f32x4_t*>(sp + state_offset(W.n_of(t, 0), W.p_of(0))) = W.st[t];
     }
-    W.update_from(gates[(cc - W.cc0) & 1], lkt, 0, lxt);
+    W.update_from(gates[(cc - W.cc0) & 1], lkt, 0, W.rows_of(cc), lxt);
   }
   W.store_state();
 }
@@ -282,12 +289,13 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
   const int tid = W.tid, lane = W.lane, w = W.w, l16 = W.l16, g4 = W.g4, pw = W.pw, nh = w >> 2, nbase = nh * (NT / 2);
   W.nbase = nbase;
   // tile e of M, rows i and columns j
-  const auto weights = [&](int e, const Gates<kQ>& G) {
+  const auto weights = [&](int e, int rows, const Gates<kQ>& G) {
     const int it = tile_row(e), jt = tile_col(e, it);
+    if (W.ended(16 * it, rows)) return;
     f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < NT / 32; ++s)
-      a = O::mma(TN::row(lq, 16 * it + l16, 32 * s + 8 * g4), TN::row(lk, 16 * jt + l16, 32 * s + 8 * g4), a);
+      if (!W.padding(32 * s)) a = O::mma(TN::row(lq, 16 * it + l16, 32 * s + 8 * g4), TN::row(lk, 16 * jt + l16, 32 * s + 8 * g4), a);
     const int i0 = 16 * it + 4 * g4, j = 16 * jt + l16;
     a *= between4(G, it, jt, i0, j) * G.b[j];
 #pragma unroll
@@ -307,8 +315,8 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
     for (int cc = W.cc0; cc < W.cc1; ++cc) {
       const int slot = (cc - W.cc0) & 1;
       __syncthreads();
-      weights(kReadWaves, gates[slot]);
-      weights(kReadWaves + 1, gates[slot]);
+      weights(kReadWaves, kQ, gates[slot]);
+      weights(kReadWaves + 1, kQ, gates[slot]);
       write_gates(gates[slot ^ 1], gl.g, gl.b, lane, false);
       gl.load(W, cc + 2);
       __syncthreads();
@@ -369,9 +377,10 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
     const int slot = (cc - W.cc0) & 1;
     const Gates<kQ>& G = gates[slot];
     const T* lxt = lxts[kPlanes ? slot : 0];
+    const int rows = W.rows_of(cc);
     __syncthreads();   // the tiles are written
-    weights(w, G);
-    if (!kPlanes && w < 2) weights(kReadWaves + w, G);
+    weights(w, rows, G);
+    if (!kPlanes && w < 2) weights(kReadWaves + w, rows, G);
     if (gate_wave) {
       write_gates(gates[slot ^ 1], gl.g, gl.b, lane, false);
       gl.load(W, cc + 2);
@@ -382,12 +391,14 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
     for (int it = 0; it < 4; ++it) y[it] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < KT / 2; ++s) {
+      if (W.padding(nbase + 32 * s)) continue;
       const f32x4_t a = W.st[2 * s], b = W.st[2 * s + 1];
       const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
       Frag f[PIECES];
       O::split(v, f);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
+        if (W.ended(16 * it, rows)) continue;
         const Frag qf = TN::row(lq, 16 * it + l16, nbase + 32 * s + 8 * g4);
 #pragma unroll
         for (int u = PIECES - 1; u >= 0; --u) y[it] = O::mma(f[u], qf, y[it]);
@@ -402,19 +413,19 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
       y[u] = nh == 0 ? y[u] : y[2 + u];
     }
     if constexpr (kPlanes)
-      W.update(G, lkt, nbase, [&](int s, Frag (&f)[O::kSplit]) {
+      W.update(G, lkt, nbase, rows, [&](int s, Frag (&f)[O::kSplit]) {
 #pragma unroll
         for (int u = 0; u < O::kSplit; ++u) f[u] = transposed_row(lxw + u * kPB * kQ, 16 * pw + l16, 32 * s + 8 * g4);
       });
     else
-      W.update_from(G, lkt, nbase, lxt);
+      W.update_from(G, lkt, nbase, rows, lxt);
     __syncthreads();   // M, the halves of y and the next gates are written; the tiles but x^T are done with
     // what the chunk's own tokens give
 #pragma unroll
     for (int u = 0; u < 2; ++u) y[u] += ly[((w ^ 4) * 2 + u) * 64 + lane];
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      if (s <= nh) {
+      if (s <= nh && !W.ended(32 * nh, rows)) {
         const Frag vf = transposed_row(lxt, 16 * pw + l16, 32 * s + 8 * g4);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -422,7 +433,7 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
           for (int z = PIECES - 1; z >= 0; --z)
             y[u] = O::mma(vf, TM::row(lm + z * kQ * kQ, 32 * nh + 16 * u + l16, 32 * s + 8 * g4), y[u]);
       }
-    const TileStore<T, VEC> out(yp, yst, W.rows_of(cc), W.rows_p);
+    const TileStore<T, VEC> out(yp, yst, rows, W.rows_p);
     yp += W.step(yst);
 #pragma unroll
     for (int u = 0; u < 2; ++u) out.put(32 * nh + 16 * u + l16, 16 * pw + 4 * g4, y[u]);
