@@ -362,7 +362,8 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
     if constexpr (kPlanes) tx.store_split(lxw, gates[slot].in, tid);
   };
   load_tiles(W.cc0);
-  // float32: no ninth wave, whose registers the others need (77 tokens, 12 heads, N = 72: 23 us, 28 with it)
+  // float32: no ninth wave, whose registers the others need (77 tokens, 12 heads, N = 72, padding multiplied: 28 us
+  // with it, 23 without)
   GateLoad gl;
   const bool gate_wave = !kPlanes && w == kReadWaves - 1;
   if (gate_wave) {
