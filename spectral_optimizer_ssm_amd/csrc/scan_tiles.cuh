@@ -215,8 +215,8 @@ __device__ __forceinline__ f32x4_t load_f32x4(__amdgpu_buffer_rsrc_t r, int offs
 // A [ROWS][WIDTH] tile of a sequence operand on its way into LDS: 16-byte
 // pieces held in the registers of THREADS threads.  Rows past the last token
 // and columns past `width` are zero.  VEC (chosen by the host, scan_vec): rows
-// start 16-byte aligned, hold whole pieces, do not overlap and lie within
-// 2 GiB of each other; otherwise element by element.
+// hold whole pieces, do not overlap and lie within 2 GiB of each other; otherwise
+// element by element.
 template <typename T, int WIDTH, int ROWS, int THREADS, bool VEC>
 struct TileLoad {
   static constexpr int kVec = Ops<T>::kVec;

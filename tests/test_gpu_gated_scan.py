@@ -207,6 +207,27 @@ def test_scan_sliced_operands(mu, shape, dtype):
     assert all(torch.equal(i, j) for i, j in zip(a, b))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("off", [1, 2, 3, 5])
+def test_scan_at_any_element(mu, off, dtype):
+    """Rows of whole 16-byte pieces that start at any element, at an odd stride:
+    bit for bit what the same rows give in tensors of their own."""
+    B, T, H, G, P, N = 2, 130, 4, 2, 64, 128
+    x = {n: t.cuda() for n, t in inputs(B, T, H, G, P, N, dtype, seed=17).items()}
+    wide = torch.full((B, T, off + H * P + 2 * G * N + 3), float("nan"), dtype=dtype, device="cuda")
+    wide2 = torch.full((B, T, off + H * P), float("nan"), dtype=dtype, device="cuda")
+    v, k, q = wide[..., off:off + H * P + 2 * G * N].split([H * P, G * N, G * N], dim=2)
+    v, k, q, dy = v.unflatten(2, (H, P)), k.unflatten(2, (G, N)), q.unflatten(2, (G, N)), wide2[..., off:].unflatten(2, (H, P))
+    for to, name in ((v, "v"), (k, "k"), (q, "q"), (dy, "dy")):
+        to.copy_(x[name])
+    rest = dict(gate=x["b"], S0=x["S0"])
+    for a, b in zip(mu.muon_gated_scan(v, k, q, x["g"], **rest), mu.muon_gated_scan(x["v"], x["k"], x["q"], x["g"], **rest)):
+        assert torch.equal(a, b)
+    a = mu.muon_gated_scan_backward(v, k, q, x["g"], dy, dS=x["dS"], **rest)
+    b = mu.muon_gated_scan_backward(x["v"], x["k"], x["q"], x["g"], x["dy"], dS=x["dS"], **rest)
+    assert all(torch.equal(i, j) for i, j in zip(a, b))
+
+
 def test_scan_permuted_and_broadcast_operands(mu):
     """Head-major storage, and gates and keys broadcast over tokens (stride 0)."""
     x = inputs(2, 100, 4, 2, 64, 128, BF16, seed=8)
