@@ -447,10 +447,10 @@ typedef struct {
  * chunk of 64 tokens that holds it, earlier tokens included).  Rows that are
  * 16-byte aligned and a multiple of 16 bytes wide take vectorised loads.
  * States, sums and gates are float32 (decays summed in float64); with
- * MUON_BF16 the products that give y and the gradients of v, k, q have
- * bfloat16 operands and float32 sums, those that give states and gate
- * gradients carry float32 accuracy.  Results are deterministic and do not
- * depend on the device. */
+ * MUON_BF16 the operands of the products that give y and the gradients of v,
+ * k, q carry 16 bits or more, with float32 sums, so that these are off by little
+ * more than their own rounding; states and gate gradients have float32
+ * accuracy.  Results are deterministic and do not depend on the device. */
 typedef struct {
   int batch, tokens, heads, groups, P, N;
   int dtype;

@@ -11,11 +11,12 @@
 // the operand of S_in q without leaving the registers.
 //
 // Rounding, bfloat16 operands: the weights e^{c_i - c_j} b_j (q_i . k_j) and
-// the copy of S_in that is read are rounded to bfloat16 once, which leaves the
-// error of y at 1.4 times that of its own rounding (at just that in sequences of
-// one chunk, where they are two pieces); the weighted values that enter the state are split
-// into three bfloat16 pieces, so the state keeps float32 accuracy.  Gates are
-// float64 sums, kept as two floats.
+// the copy of S_in that is read are two bfloat16 pieces (16 bits), so that y is
+// off by its own rounding alone, at any length and from a sequence's first token
+// on; in one piece y would be off by 1.4 times that, and by 2.2 times where a row
+// sums few tokens, and eight sequences of 2,048 tokens would take 92 us instead of
+// 103.  The weighted values that enter the state are three pieces, so the state
+// keeps float32 accuracy.  Gates are float64 sums, kept as two floats.
 //
 // In reversed time the same walk with (dy, q) for (v, k), weights e^{c_i} and
 // no reads gives the gradients of the states (muon_gated_scan_backward).
@@ -254,33 +255,30 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
 // exchange through LDS, each finishing half of the tokens), and the next S; then
 // what the chunk's own tokens give, and the next chunk's tiles go to LDS.
 //
-// Eight sequences of 2,048 tokens, 24 heads of 64 x 128, bfloat16: 92 us (192
-// workgroups, 32 steps of about 6,500 clocks); HBM needs 112 MB, 22 us.  Bound
-// by issue and LDS together: a step is 2,200 clocks of vector and 1,400 of
-// matrix instructions a SIMD and 2,300 of LDS, and two waves a SIMD that meet
+// Eight sequences of 2,048 tokens, 24 heads of 64 x 128, bfloat16: 103 us (192
+// workgroups, 32 steps of about 7,300 clocks); HBM needs 112 MB, 22 us.  Bound
+// by issue and LDS together (with one piece of M and S_in a step of 6,500 was 2,200
+// clocks of vector and 1,400 of matrix instructions a SIMD and 2,300 of LDS): two waves a SIMD that meet
 // at barriers overlap little of it.  What made the step short: 16-byte LDS reads
 // without bank conflicts everywhere (107 -> 94 us, with two barriers instead of
 // three and the weighted values split once for all waves), the gates, whose
 // float64 prefix sum is a long chain, and two of the ten tiles of M on a wave of
-// their own.  PIECES: of M and of the copy of S_in that is read; a sequence of
-// one chunk takes two (see launch_scan_walk).  Four waves that hold all columns take 123 us (two such workgroups
-// to a compute unit: 16,384 tokens, 24 heads, 118 us against 118).
-template <typename T, int NT, bool VEC, int PIECES>
+// their own.  Four waves that hold all columns, in one piece, took 123 us against 107.
+template <typename T, int NT, bool VEC>
 __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadThreads, sizeof(T) == 2 ? 3 : 2) scan_read_kernel(WalkPair P) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
   typedef Tile<T, NT> TN;
   typedef Tile<T, kQ> TM;
-  constexpr int KT = NT / 32;
+  constexpr int KT = NT / 32, kPieces = O::kRounded;   // of M and of the copy of S_in that is read
   // bfloat16: the weighted values of a chunk are split once for all waves, and
   // x^T, which a chunk reads last, is double, so that the next chunk's tiles need
   // no third barrier.  float32 values are not split, and its tiles fill the LDS.
   // (Arrays of their own: the compiler may move reads of one across writes to another.)
   constexpr bool kPlanes = sizeof(T) == 2;
-  static_assert(kPlanes || PIECES == 1, "pieces are bfloat16");
   __shared__ __attribute__((aligned(16))) T lkt[NT * kQ], lk[kQ * NT], lq[kQ * NT], lxts[kPlanes ? 2 : 1][kPB * kQ];
   __shared__ __attribute__((aligned(16))) T lxw[kPlanes ? 3 * kPB * kQ : 8];   // weighted x^T in three pieces
-  __shared__ __attribute__((aligned(16))) T lm[PIECES * kQ * kQ];             // the weights M [i][j], in pieces
+  __shared__ __attribute__((aligned(16))) T lm[kPieces * kQ * kQ];            // the weights M [i][j], in pieces
   __shared__ f32x4_t ly[kReadWaves * 2 * kWave];   // halves of y that waves hand over
   __shared__ Gates<kQ> gates[2];
   const ScanWalk A = P.w[0];
@@ -302,7 +300,7 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
     for (int r = 0; r < 4; ++r) {
       const T hi = O::from_f32(a[r]);
       lm[TM::at(i0 + r, j)] = hi;
-      if constexpr (PIECES == 2) lm[kQ * kQ + TM::at(i0 + r, j)] = O::from_f32(a[r] - bf16_to_f32(hi));
+      if constexpr (kPieces == 2) lm[kQ * kQ + TM::at(i0 + r, j)] = O::from_f32(a[r] - bf16_to_f32(hi));
     }
   };
   if (kPlanes && w == kReadWaves) {
@@ -352,7 +350,7 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
   if (w < 2) {
     const int r0 = 32 * w, c0 = r0 + 16;
 #pragma unroll
-    for (int e = 0; e < 4 * PIECES; ++e) lm[e / 4 * kQ * kQ + TM::at(r0 + l16, c0 + 4 * g4 + e % 4)] = O::from_f32(0.0f);
+    for (int e = 0; e < 4 * kPieces; ++e) lm[e / 4 * kQ * kQ + TM::at(r0 + l16, c0 + 4 * g4 + e % 4)] = O::from_f32(0.0f);
   }
   const auto store_tiles = [&](int slot) {
     tk.store(lk, tid);
@@ -395,14 +393,14 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
       if (W.padding(nbase + 32 * s)) continue;
       const f32x4_t a = W.st[2 * s], b = W.st[2 * s + 1];
       const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      Frag f[PIECES];
+      Frag f[kPieces];
       O::split(v, f);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         if (W.ended(16 * it, rows)) continue;
         const Frag qf = TN::row(lq, 16 * it + l16, nbase + 32 * s + 8 * g4);
 #pragma unroll
-        for (int u = PIECES - 1; u >= 0; --u) y[it] = O::mma(f[u], qf, y[it]);
+        for (int u = kPieces - 1; u >= 0; --u) y[it] = O::mma(f[u], qf, y[it]);
       }
     }
 #pragma unroll
@@ -431,7 +429,7 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int z = PIECES - 1; z >= 0; --z)
+          for (int z = kPieces - 1; z >= 0; --z)
             y[u] = O::mma(vf, TM::row(lm + z * kQ * kQ, 32 * nh + 16 * u + l16, 32 * s + 8 * g4), y[u]);
       }
     const TileStore<T, VEC> out(yp, yst, rows, W.rows_p);
@@ -475,9 +473,9 @@ hipError_t states(const WalkPair& W, int dirs, long long items, hipStream_t st) 
                      dim3(kStatesThreads + kWave), 0, st, W);
   return hipGetLastError();
 }
-template <typename T, int NT, bool VEC, int PIECES>
+template <typename T, int NT, bool VEC>
 hipError_t read(const WalkPair& W, long long items, hipStream_t st) {
-  hipLaunchKernelGGL((scan_read_kernel<T, NT, VEC, PIECES>), dim3(static_cast<unsigned>(items)),
+  hipLaunchKernelGGL((scan_read_kernel<T, NT, VEC>), dim3(static_cast<unsigned>(items)),
                      dim3(kReadThreads + (sizeof(T) == 2 ? kWave : 0)), 0, st, W);
   return hipGetLastError();
 }
@@ -486,14 +484,7 @@ hipError_t walk(const WalkPair& W, int dirs, bool reads, hipStream_t st) {
   const ScanWalk& a = W.w[0];
   const long long items = static_cast<long long>(a.batch) * a.heads * a.pblocks * a.nseg;
   if (!reads) return states<T, NT, VEC>(W, dirs, items, st);
-  if constexpr (sizeof(T) == 2) {
-    // Rounding one of a few weights moves a whole row of y: with two tokens y is
-    // off by up to 1.5 times its own rounding.  Two pieces of weights and states
-    // leave only that, and 64 sequences of 64 tokens, 24 heads, take 69 us instead
-    // of 67; eight of 2,048, where the errors average out, would take 102 instead of 90.
-    if (a.nchunks == 1) return read<T, NT, VEC, 2>(W, items, st);
-  }
-  return read<T, NT, VEC, 1>(W, items, st);
+  return read<T, NT, VEC>(W, items, st);
 }
 template <typename T, int NT>
 hipError_t walk_any(const WalkPair& W, int dirs, bool reads, bool vec, hipStream_t st) {

@@ -19,18 +19,19 @@
 // fixed order.
 //
 // Eight sequences of 2,048 tokens, 24 heads of 64 x 128 sharing keys, bfloat16:
-// 137 us, of which the two states' 201 MB alone need 40 at the rate of a large
+// 152 us, of which the two states' 201 MB alone need 40 at the rate of a large
 // copy.  A head's step is about 23,000 clocks: per SIMD 12,000 of vector
 // instructions (the weights and sums of E's tiles, the states' splits) and 4,500
 // of matrix ones, 6,000 of LDS, with two waves a SIMD to overlap them.  Blocks of
 // 64 tokens would read and write twice the states.
 //
 // Rounding, bfloat16 operands: L A, the sum of L b E and the copy of dS_out
-// that dv reads are rounded to bfloat16 once, which leaves dv, dq and dk at 1.2 to
-// 1.4 times the error of their own rounding (at just that in sequences of one
-// chunk, where they are two pieces); dq and dk take the states as
-// three bfloat16 pieces (float32 accuracy), since db and dg, which are
-// float32, are dot products of them.
+// that dv reads are two bfloat16 pieces (16 bits), so that dv, dq and dk are off by
+// their own rounding alone (by 1.2 to 1.4 times that in one piece, which would take
+// 137 us for 152); dq and dk take the states as three pieces (float32 accuracy), since
+// db and dg, which are float32, are dot products of them.  The pieces of L A and
+// of the sums are kept as the tiles on one side of the diagonal, or they would not
+// fit the LDS beside the block's operands.
 #include <type_traits>
 
 #include "scan_tiles.cuh"
@@ -40,16 +41,15 @@ namespace {
 
 using namespace scan;
 
-// A block of Q tokens by 4 Q threads.  PIECES: bfloat16 pieces of the products'
-// rounded operands, L A, D and the copy of dS_out (see scan_grad_tokens).
-template <typename T, int NT, int Q, bool VEC, int PIECES>
+// A block of Q tokens by 4 Q threads.
+template <typename T, int NT, int Q, bool VEC>
 __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
   typedef Ops<T> O;
   typedef typename O::Frag Frag;
   typedef Tile<T, NT> TN;
   typedef Tile<T, kPB> TP;
-  typedef Tile<T, Q> TM;
-  constexpr int kThreads = 4 * Q, kTiles = Q / 16, kU = Q / 64;
+  typedef Triangle<T, Q / 16> TM;
+  constexpr int kThreads = 4 * Q, kTiles = Q / 16, kU = Q / 64, kPieces = O::kRounded;
   // a wave has one of the diagonal's tiles, first, and a run of those below it
   constexpr int kBelow = kTiles * (kTiles - 1) / 2, kMaxTiles = 1 + (kBelow + kTiles - 1) / kTiles;
   // dq and dk: 16-wide blocks of n per wave, groups of waves that share a block's tokens
@@ -57,12 +57,11 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
   constexpr int kTG = kTiles > kBlocks ? kTiles / kBlocks : 1, kTT = kTiles / kTG;
   // dv: four blocks of value rows, the tokens dealt to kTiles / 4 groups of waves
   constexpr int kZG = kTiles / 4;
-  // dS_out [n][p] as the operand of dv goes where v was, if it fits
-  constexpr bool kStateInV = NT <= Q && PIECES == 1;
+  // dS_out [n][p] as the operand of dv goes where v was, if it fits, its second piece where dy was
+  constexpr bool kStateInV = NT <= Q;
   // arrays of their own: the compiler may move reads of one across writes to another
-  __shared__ __attribute__((aligned(16))) T lq[Q * NT], lk[Q * NT], lv[2 * Q * kPB];   // q; k; v and dy, at the end D [i][j]
-  __shared__ __attribute__((aligned(16))) T lm[PIECES * Q * Q];                                  // (L A)^T [j][i], at the end D^T
-  static_assert(PIECES * Q <= 2 * kPB, "D fits where v and dy were");
+  __shared__ __attribute__((aligned(16))) T lq[Q * NT], lk[Q * NT], lv[2 * Q * kPB];   // q; k; v and dy
+  __shared__ __attribute__((aligned(16))) T lm[TM::kSize];                                       // (L A)^T [j][i], at the end D^T, then D
   __shared__ Gates<Q> gates[2];
   // by token: row sums of W by column tile, column sums of L A E by row tile,
   // e^{c_i} q_i . S_in^T dy_i and e^{c_end - c_j} k_j . dS_out^T v_j by block of n
@@ -149,8 +148,8 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
     load_columns(A.dstates + state_at(0), kPB * NT * 4, lane, y);
     if (w == kTiles - 1) next_gates(gates[0]);
   }
-  // tiles of (L A)^T and slots of the sums that no wave writes
-  for (int i = tid; i < PIECES * Q * Q; i += kThreads) lm[i] = O::from_f32(0.0f);
+  // slots of the sums that no wave writes
+  TM::clear_zeros(lm, tid);
   for (int i = tid; i < 4 * kTiles * Q; i += kThreads) lsums[0][i] = 0.0f;
   __syncthreads();
 
@@ -222,7 +221,7 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
           cols[t] += we;
           rs[r] = we * b;
         }
-        TM::template store4_pieces<PIECES>(lm, Q * Q, j, i0, mm);
+        TM::store4(lm, TM::tile(it, jt), l16, 4 * g4, mm);
         const float row = sum_lanes4(rs[0], rs[1], rs[2], rs[3], l16);
         if (l16 < 4) lrow[jt * Q + i0 + l16] = row;
         settle(dsum[t]);
@@ -316,16 +315,15 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
     __syncthreads();   // (L A)^T and the sums are written, v is done with
     {
       const int lane = fresh(threadIdx.x) & 63, l16 = lane & 15, g4 = lane >> 4;
-      if constexpr (kStateInV) {
-        // dS_out [n][p], rounded, as the operand of dv
-        if (tg == 0)
+      // a piece of dS_out [n][p], as the operand of dv
+      const auto store_state = [&](T* tile, int piece) {
 #pragma unroll
-          for (int b = 0; b < kNW; ++b)
+        for (int b = 0; b < kNW; ++b)
 #pragma unroll
-            for (int s = 0; s < kPB / 32; ++s) {
-              TP::store8(lv, 16 * (nw0 + b) + l16, 32 * s + 8 * g4, f[b][s][0]);   // the first of its pieces
-            }
-      }
+          for (int s = 0; s < kPB / 32; ++s) TP::store8(tile, 16 * (nw0 + b) + l16, 32 * s + 8 * g4, f[b][s][piece]);
+      };
+      if constexpr (kStateInV)
+        if (tg == 0) store_state(lv, 0);
       const float* dsp = A.dstates + state_at(i);
       if constexpr (!kEarly) {
         load_head(next_h, next_pb, more ? rows : 0, fresh(threadIdx.x));
@@ -360,30 +358,45 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int jt = kZG * u + (w >> 2);
-          if (s >= kZG * u / 2)   // jt / 2: tiles above the diagonal are zero
+          if (s >= kZG * u / 2)   // jt / 2: tiles of tokens before j are zero
 #pragma unroll
-            for (int e = PIECES - 1; e >= 0; --e) z[u] = O::mma(f, TM::row(lm + e * Q * Q, 16 * jt + l16, 32 * s + 8 * g4), z[u]);
+            for (int e = kPieces - 1; e >= 0; --e) z[u] = O::mma(f, TM::row(lm, e, TM::tile(2 * s + (g4 >> 1), jt), l16, 8 * (g4 & 1)), z[u]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (kStateInV) __syncthreads();   // dS_out is written
+      if constexpr (kStateInV) {
+        __syncthreads();   // dS_out is written, dy is done with
+        if constexpr (kPieces == 2)
+          if (tg == 0) store_state(ldy, 1);
+      }
+      const auto state_product = [&](int s, const auto& f, int pieces) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const Frag kf = TN::row(lk, 16 * (kZG * u + (w >> 2)) + l16, 32 * s + 8 * g4);
+#pragma unroll
+          for (int e = pieces - 1; e >= 0; --e) zs[u] = O::mma(f[e], kf, zs[u]);
+        }
+      };
 #pragma unroll
       for (int s = 0; s < NT / 32; ++s) {
-        Frag f[PIECES];
         if constexpr (kStateInV) {
-          f[0] = TP::col(lv, 32 * s, 16 * (w & 3), lane);
+          const Frag f[1] = {TP::col(lv, 32 * s, 16 * (w & 3), lane)};
+          state_product(s, f, 1);
         } else {
           float v[8];
+          Frag f[kPieces];
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = dsp[state_offset(32 * s + 8 * g4 + e, 16 * (w & 3) + l16)];
           O::split(v, f);
+          state_product(s, f, kPieces);
         }
+      }
+      if constexpr (kStateInV && kPieces == 2) {
+        __syncthreads();   // its second piece is written
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-        {
-          const Frag kf = TN::row(lk, 16 * (kZG * u + (w >> 2)) + l16, 32 * s + 8 * g4);
-#pragma unroll
-          for (int e = PIECES - 1; e >= 0; --e) zs[u] = O::mma(f[e], kf, zs[u]);
+        for (int s = 0; s < NT / 32; ++s) {
+          const Frag f[1] = {TP::col(ldy, 32 * s, 16 * (w & 3), lane)};
+          state_product(s, f, 1);
         }
       }
       const TileStore<T, VEC> out(static_cast<T*>(A.dv) + ((bi * A.tokens + t0) * A.heads + h) * A.P + pb * kPB,
@@ -433,42 +446,46 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
     __syncthreads();   // the tiles, gates and sums are done with
   }
 
-  // D = sum over heads of L b E, once as D [i][j] (where v and dy were) and
-  // once as D^T [j][i] (where (L A)^T was, whose other tiles are zero)
-  T* ld = lv;
-  for (int i = tid; i < PIECES * Q * Q; i += kThreads) ld[i] = O::from_f32(0.0f);
+  // D = sum over heads of L b E, as D^T [j][i] for dk, then as D [i][j] for dq
+  const auto each_tile = [&](auto store) {
+#pragma unroll
+    for (int t = 0; t < kMaxTiles; ++t)
+      if (t + 1 < kMaxTiles || t < ntile) store(TM::tile(trow[t], tcol[t]), dsum[t]);
+  };
+  each_tile([&](int tile, const f32x4_t& d) { TM::store4(lm, tile, l16, 4 * g4, d); });
   __syncthreads();
+  const int hi = g4 >> 1, lo = 8 * (g4 & 1);
 #pragma unroll
-  for (int t = 0; t < kMaxTiles; ++t) {
-    if (t + 1 < kMaxTiles || t < ntile) {
-      const int j = 16 * tcol[t] + l16, i0 = 16 * trow[t] + 4 * g4;
-      TM::template store4_pieces<PIECES>(lm, Q * Q, j, i0, dsum[t]);
+  for (int s = 0; s < Q / 32; ++s)
 #pragma unroll
-      for (int e = 0; e < PIECES; ++e) {
+    for (int b = 0; b < kNW; ++b) {
+      const Frag fq = TN::col(lq, 32 * s, 16 * (nw0 + b), lane);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) ld[e * Q * Q + TM::at(i0 + r, j)] = O::from_f32(dsum[t][r]);
-        dsum[t] -= O::rounded4(dsum[t]);
-      }
+      for (int u = 0; u < kTT; ++u)
+        if (s >= u * kTG / 2)   // tokens i before j are zero
+#pragma unroll
+          for (int e = kPieces - 1; e >= 0; --e) dk[b][u] = O::mma(fq, TM::row(lm, e, TM::tile(2 * s + hi, u * kTG + tg), l16, lo), dk[b][u]);
     }
-  }
+  __syncthreads();   // D^T is done with
+  each_tile([&](int tile, const f32x4_t& d) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) TM::store1(lm, tile, 4 * g4 + r, l16, d[r]);
+  });
   __syncthreads();
+#pragma unroll
+  for (int s = 0; s < Q / 32; ++s)
+#pragma unroll
+    for (int b = 0; b < kNW; ++b) {
+      const Frag fk = TN::col(lk, 32 * s, 16 * (nw0 + b), lane);
+#pragma unroll
+      for (int u = 0; u < kTT; ++u)
+        if (s <= (u * kTG + kTG - 1) / 2)
+#pragma unroll
+          for (int e = kPieces - 1; e >= 0; --e) dq[b][u] = O::mma(fk, TM::row(lm, e, TM::tile(u * kTG + tg, 2 * s + hi), l16, lo), dq[b][u]);
+    }
 #pragma unroll
   for (int b = 0; b < kNW; ++b) {
     const int n0 = 16 * (nw0 + b);
-#pragma unroll
-    for (int s = 0; s < Q / 32; ++s) {
-      const Frag fk = TN::col(lk, 32 * s, n0, lane), fq = TN::col(lq, 32 * s, n0, lane);
-#pragma unroll
-      for (int u = 0; u < kTT; ++u) {
-        const int it = u * kTG + tg;
-        // tiles of D with j > i (of D^T with i < j) are zero
-#pragma unroll
-        for (int e = PIECES - 1; e >= 0; --e) {
-          if (s <= (u * kTG + kTG - 1) / 2) dq[b][u] = O::mma(fk, TM::row(ld + e * Q * Q, 16 * it + l16, 32 * s + 8 * g4), dq[b][u]);
-          if (s >= u * kTG / 2) dk[b][u] = O::mma(fq, TM::row(lm + e * Q * Q, 16 * it + l16, 32 * s + 8 * g4), dk[b][u]);
-        }
-      }
-    }
     const int n = n0 + 4 * g4;
 #pragma unroll
     for (int u = 0; u < kTT; ++u) {
@@ -526,10 +543,10 @@ __global__ void __launch_bounds__(kPartThreads) scan_parts_kernel(const float* p
   }
 }
 
-template <typename T, int NT, int Q, bool VEC, int PIECES>
+template <typename T, int NT, int Q, bool VEC>
 hipError_t grad(const ScanGrad& A, hipStream_t st) {
   const long long items = static_cast<long long>(A.batch) * A.nblocks * A.groups * A.nsplit;
-  hipLaunchKernelGGL((scan_grad_kernel<T, NT, Q, VEC, PIECES>), dim3(static_cast<unsigned>(items)), dim3(4 * Q), 0, st, A);
+  hipLaunchKernelGGL((scan_grad_kernel<T, NT, Q, VEC>), dim3(static_cast<unsigned>(items)), dim3(4 * Q), 0, st, A);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || A.nsplit == 1) return e;
   const long long half = static_cast<long long>(A.batch) * A.tokens * A.groups * A.N;
@@ -543,16 +560,16 @@ hipError_t grad(const ScanGrad& A, hipStream_t st) {
 
 template <int NT>
 hipError_t grad_bf16(const ScanGrad& A, bool vec, hipStream_t st) {
-  if (scan_grad_tokens(true, A.tokens) == 64) return vec ? grad<bf16_t, NT, 64, true, 2>(A, st) : grad<bf16_t, NT, 64, false, 2>(A, st);
-  return vec ? grad<bf16_t, NT, 128, true, 1>(A, st) : grad<bf16_t, NT, 128, false, 1>(A, st);
+  if (scan_grad_tokens(true, A.tokens) == 64) return vec ? grad<bf16_t, NT, 64, true>(A, st) : grad<bf16_t, NT, 64, false>(A, st);
+  return vec ? grad<bf16_t, NT, 128, true>(A, st) : grad<bf16_t, NT, 128, false>(A, st);
 }
 
 }  // namespace
 
 hipError_t launch_scan_grad(const ScanGrad& A, bool vec, bool bf16, hipStream_t st) {
   if (bf16) return A.N <= 64 ? grad_bf16<64>(A, vec, st) : grad_bf16<128>(A, vec, st);
-  if (A.N <= 64) return vec ? grad<float, 64, 64, true, 1>(A, st) : grad<float, 64, 64, false, 1>(A, st);
-  return vec ? grad<float, 128, 64, true, 1>(A, st) : grad<float, 128, 64, false, 1>(A, st);
+  if (A.N <= 64) return vec ? grad<float, 64, 64, true>(A, st) : grad<float, 64, 64, false>(A, st);
+  return vec ? grad<float, 128, 64, true>(A, st) : grad<float, 128, 64, false>(A, st);
 }
 
 }  // namespace muon

@@ -306,9 +306,8 @@ hipError_t launch_adamw(const AdamwLaunch& A, bool grad_bf16, int blocks, hipStr
 constexpr int kScanChunk = 64;     // tokens per chunk
 // Tokens per workgroup of the backward pass: as many as the tiles in LDS allow,
 // 128 bfloat16 or 64 float32 ones; sequences of up to 64 tokens are one block of
-// 64, which leaves room for second pieces of the rounded operands: with a few
-// tokens a rounded weight moves a whole row, and dv would be off by up to twice
-// its own rounding.
+// 64, half of whose tiles would be padding otherwise (64 of them, 24 heads: 112 us, 124
+// in blocks of 128).
 inline int scan_grad_tokens(bool bf16, int tokens) { return bf16 && tokens > kScanChunk ? 2 * kScanChunk : kScanChunk; }
 constexpr int kScanRows = 64;      // state rows (value components) per workgroup
 constexpr int kScanMaxN = 128;     // largest key length

@@ -35,6 +35,7 @@ struct Ops<bf16_t> {
   typedef bf16x8_t Frag;
   static constexpr int kVec = 8;      // elements per 16 bytes
   static constexpr int kSplit = 3;    // bf16 pieces that carry a float32's 24 bits
+  static constexpr int kRounded = 2;  // and 16 bits, for operands of results that are rounded to bf16 themselves
   __device__ static __forceinline__ f32x4_t mma(Frag a, Frag b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -87,7 +88,7 @@ template <>
 struct Ops<float> {
   typedef FragF32 Frag;
   static constexpr int kVec = 4;
-  static constexpr int kSplit = 1;
+  static constexpr int kSplit = 1, kRounded = 1;
   __device__ static __forceinline__ f32x4_t mma(const Frag& a, const Frag& b, f32x4_t c) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
@@ -162,15 +163,42 @@ struct Tile {
     }
   }
   __device__ static __forceinline__ f32x4_t load4(const T* tile, int row, int col) { return O::load4(tile + at(row, col)); }
-  __device__ static __forceinline__ void store4(T* tile, int row, int col, f32x4_t v) { O::store4(tile + at(row, col), v); }
-  // as PIECES tiles, `size` elements apart
-  template <int PIECES>
-  __device__ static __forceinline__ void store4_pieces(T* tile, int size, int row, int col, f32x4_t v) {
+};
+
+// The 16 x 16 tiles on one side of the diagonal of a matrix of TILES x TILES of
+// them, and one of zeros for those on the other side: the weights of a block, in
+// kRounded pieces.  A tile's 16-byte pieces lie column by column, so that what
+// 16 lanes read or 32 lanes write at once is contiguous.
+template <typename T, int TILES>
+struct Triangle {
+  typedef Ops<T> O;
+  typedef typename O::Frag Frag;
+  static constexpr int kVec = O::kVec, kTiles = TILES * (TILES + 1) / 2, kPiece = (kTiles + 1) * 256, kSize = O::kRounded * kPiece;
+  // of the tile at `far` tiles from the matrix' corner along one side and `near` along the other
+  static __device__ __forceinline__ int tile(int far, int near) { return far >= near ? far * (far + 1) / 2 + near : kTiles; }
+  static __device__ __forceinline__ int at(int tile, int row, int col) { return tile * 256 + ((col / kVec) * 16 + row) * kVec + col % kVec; }
+  // 8 elements from column col, a multiple of 8
+  static __device__ __forceinline__ Frag row(const T* m, int piece, int tile, int row, int col) {
+    m += piece * kPiece;
+    if constexpr (sizeof(T) == 2) return O::row(m + at(tile, row, col));
+    else return O::row2(m + at(tile, row, col), m + at(tile, row, col + 4));
+  }
+  static __device__ __forceinline__ void store4(T* m, int tile, int row, int col, f32x4_t v) {
 #pragma unroll
-    for (int u = 0; u < PIECES; ++u) {
-      store4(tile + u * size, row, col, v);
-      if (u + 1 < PIECES) v -= O::rounded4(v);
+    for (int e = 0; e < O::kRounded; ++e) {
+      O::store4(m + e * kPiece + at(tile, row, col), v);
+      if (e + 1 < O::kRounded) v -= O::rounded4(v);
     }
+  }
+  static __device__ __forceinline__ void store1(T* m, int tile, int row, int col, float v) {
+    const T hi = O::from_f32(v);
+    m[at(tile, row, col)] = hi;
+    if constexpr (O::kRounded == 2) m[kPiece + at(tile, row, col)] = O::from_f32(v - bf16_to_f32(hi));
+  }
+  static __device__ __forceinline__ void clear_zeros(T* m, int tid) {
+#pragma unroll
+    for (int e = 0; e < O::kRounded; ++e)
+      if (tid < 256) m[e * kPiece + kTiles * 256 + tid] = O::from_f32(0.0f);
   }
 };
 
