@@ -476,7 +476,8 @@ int muon_gated_scan(const muon_scan_args* args, void* Y, float* S_out, void* wor
  *   (dK and dQ summed over a group's heads), dlog_decay and dgate
  *   [batch][tokens][heads] float32 (dgate may be NULL), dS0 NULL or
  *   [batch][heads][P][N] float32.
- * The gradient of a log decay whose e^g is 0 in float32 is 0. */
+ * dlog_decay adds only what crosses its token, so a strong decay costs it no
+ * accuracy; where a sequence starts (-inf) it is 0. */
 size_t muon_gated_scan_backward_workspace_size(const muon_scan_args* args);
 int muon_gated_scan_backward(const muon_scan_args* args, const muon_seq* dY, const float* dS, void* dV, void* dK,
                              void* dQ, float* dlog_decay, float* dgate, float* dS0, void* workspace,

@@ -7,9 +7,13 @@
 //   dk_j = sum_h b_j [ sum_i L_ij E_ij q_i + e^{c_end - c_j} dS_out^T v_j ]
 // over the heads h that share the keys and queries.  The log decay of t scales
 // whatever crosses t: with W_ij = L_ij b_j A_ij E_ij,
-//   dg_t = sum_{i >= t} (sum_j W_ij - sum_j W_ji + dy_i . e^{c_i} S_in q_i)
-//        + sum_{j < t} b_j e^{c_end - c_j} v_j . dS_out k_j + e^{c_end} <S_in, dS_out>,
-// where no sum leaves the block, so nothing large cancels.
+//   dg_t = sum_{j < t <= i} W_ij + sum_{i >= t} dy_i . e^{c_i} S_in q_i
+//        + sum_{j < t} b_j e^{c_end - c_j} v_j . dS_out k_j + e^{c_end} <S_in, dS_out>.
+// Only what crosses t is added, so its float32 accuracy holds where a strong
+// decay leaves little of it.  With t in token tile T, the pairs are those of T's
+// own tile, whose rows are summed up to each column; the rest of T's columns
+// before t (tiles below) and of its rows from t on (tiles to the left); and the
+// whole tiles below T and to its left.
 //
 // One workgroup takes a block of tokens and walks the heads that share its keys
 // and queries: A, and the sum over heads of L b E, stay in registers, so the
@@ -63,11 +67,13 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
   __shared__ __attribute__((aligned(16))) T lq[Q * NT], lk[Q * NT], lv[2 * Q * kPB];   // q; k; v and dy
   __shared__ __attribute__((aligned(16))) T lm[TM::kSize];                                       // (L A)^T [j][i], at the end D^T, then D
   __shared__ Gates<Q> gates[2];
-  // by token: row sums of W by column tile, column sums of L A E by row tile,
-  // e^{c_i} q_i . S_in^T dy_i and e^{c_end - c_j} k_j . dS_out^T v_j by block of n
+  // by token: row sums of W by column tile (in its own tile, what crosses it there),
+  // column sums of L A E by row tile, e^{c_i} q_i . S_in^T dy_i and
+  // e^{c_end - c_j} k_j . dS_out^T v_j by block of n
   __shared__ float lsums[4][kTiles * Q];
-  // <S_in, dS_out> by wave; by token, over a head's blocks of value rows: what dg sums from t on, up to t, and db
-  __shared__ float lthrough[kTiles], lin[Q], lleave[Q], ldb[Q];
+  // <S_in, dS_out> by wave; over a head's blocks of value rows, by token: its own tile's part of dg, and db; by
+  // tile: the sums of the last two of lsums (b_j times the second), and of W by column tile
+  __shared__ float lthrough[kTiles], lown[Q], ldb[Q], lfrom[kTiles], lupto[kTiles], lpairs[kTiles * kTiles];
   T* ldy = lv + Q * kPB;
   float *lrow = lsums[0], *lcol = lsums[1], *lqs = lsums[2], *lks = lsums[3];
 
@@ -222,8 +228,20 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
           rs[r] = we * b;
         }
         TM::store4(lm, TM::tile(it, jt), l16, 4 * g4, mm);
-        const float row = sum_lanes4(rs[0], rs[1], rs[2], rs[3], l16);
-        if (l16 < 4) lrow[jt * Q + i0 + l16] = row;
+        if (t == 0) {
+          // rows from token l16 of the tile on, columns before it
+          float c = 0.0f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float before = lanes_before(rs[r]);
+            c += 4 * g4 + r >= l16 ? before : 0.0f;
+          }
+          c = sum_rows4(c, c, c, c);
+          if (g4 == 0) lrow[jt * Q + j] = c;
+        } else {
+          const float row = sum_lanes4(rs[0], rs[1], rs[2], rs[3], l16);
+          if (l16 < 4) lrow[jt * Q + i0 + l16] = row;
+        }
         settle(dsum[t]);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -335,16 +353,29 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
       {
         const int t = 16 * w + l16;
         const float* src = lsums[g4] + t;
-        float a = 0.0f;
+        float part[kTiles], a = 0.0f, own = 0.0f;   // own: of its own tile, of rows and columns
 #pragma unroll
-        for (int e = 0; e < kTiles; ++e) a += src[e * Q];
+        for (int e = 0; e < kTiles; ++e) {
+          part[e] = src[e * Q];
+          if (e == w && g4 < 2) own = part[e];
+          else a += part[e];
+        }
         const float b = G.b[t];
         const float cs = __shfl_xor(a, 16, kWave), us = __shfl_xor(a, 32, kWave), ws = __shfl_xor(a, 48, kWave);
-        if (g4 == 0) {   // a: the row's sum
-          const float in = a - b * cs + us, lv_ = b * ws, d = cs + ws;
-          lin[t] = pb == 0 ? in : lin[t] + in;
-          lleave[t] = pb == 0 ? lv_ : lleave[t] + lv_;
-          ldb[t] = pb == 0 ? d : ldb[t] + d;
+        const float cs_own = __shfl_xor(own, 16, kWave);
+        // (of use in the first quarter, whose a and own are the rows')
+        const float within = own + lanes_from(a + us) + lanes_before(b * (cs + ws)), d = cs_own + cs + ws;
+        const float ends = sum_lanes4(us, b * ws, us, b * ws, l16);
+        const auto keep = [&](float* p, float v) { *p = pb == 0 ? v : *p + v; };
+        if (g4 == 0) {
+          keep(lown + t, within);
+          keep(ldb + t, d);
+          if (l16 < 2) keep((l16 == 0 ? lfrom : lupto) + w, ends);
+        }
+#pragma unroll
+        for (int e = 0; e < kTiles; e += 4) {
+          const float pairs = sum_lanes4(part[e], part[e + 1], part[e + 2], part[e + 3], l16);
+          if (g4 == 0 && l16 < 4) keep(lpairs + w * kTiles + e + l16, pairs);
         }
       }
 
@@ -416,27 +447,23 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
 #pragma unroll
       for (int e = 0; e < kTiles; ++e) acc_z += lthrough[e];
       if (pb + 1 == A.pblocks) {
-        // with a_t what dg sums from t on and l_t what it sums up to t: the sum of all a, plus those of l - a before t
-        double d[kU], a = 0.0, ds = 0.0;
+        // what crosses the whole tile of this lane's tokens: tile m's share, then all of them
+        const int mine = lane / (kWave / kTiles), m = lane % kTiles;
+        float a = m > mine ? lfrom[m] : m < mine ? lupto[m] : 0.0f;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const double at = static_cast<double>(lin[kU * lane + u]);
-          d[u] = static_cast<double>(lleave[kU * lane + u]) - at;
-          a += at;
-          ds += d[u];
-        }
-        double before = wave_prefix_d(ds) - ds;
-        before += read_lane_d(wave_prefix_d(a), 63) + static_cast<double>(G.end[0]) * static_cast<double>(acc_z);
+        for (int e = 0; e + 2 < kTiles; ++e) a += m > mine && e < mine ? lpairs[m * kTiles + e] : 0.0f;
+        a += dpp_f<kDppXor1>(a);
+        a += dpp_f<kDppXor2>(a);
+        if constexpr (kTiles == 8) a += dpp_f<kDppHalfMirror>(a);
+        a += G.end[0] * acc_z;
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int t = kU * lane + u;
           if (t < rows) {
             const long long o = (bi * A.tokens + t0 + t) * A.heads + h;
-            // nothing crosses a token whose decay is 0: what the sums leave there is rounding
-            A.dg[o] = G.own[t] == 0.0f ? 0.0f : static_cast<float>(before);
+            A.dg[o] = a + lown[t];
             if (A.db != nullptr) A.db[o] = ldb[t];
           }
-          before += d[u];
         }
         acc_z = 0.0f;
       }

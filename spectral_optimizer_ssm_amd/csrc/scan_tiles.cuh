@@ -18,7 +18,6 @@ namespace scan {
 
 constexpr int kQ = kScanChunk;   // tokens per chunk
 constexpr int kPB = kScanRows;   // state rows (value components) per workgroup
-constexpr float kLog2e = 1.44269504088896340736f;
 // log decays below this are taken as this: e^-10000 is 0 in float32 and in
 // float64 alike, and sums of 64 of them stay finite
 constexpr float kMinLogDecay = -1.0e4f;
@@ -471,7 +470,6 @@ struct Gates {
   float b[Q];           // input gates
   float first[Q];       // e^{c_i}
   float last[Q];        // e^{c_end - c_j}
-  float own[Q];         // e^{g_t}
   float row[Q];         // e^{c_t - c_r}, r the first token of t's 16
   float in[Q];          // weights of what enters a state: e^{c_end - c_j} b_j, in reversed time e^{c_i}
   float end[4];         // e^{c_end}
@@ -482,12 +480,11 @@ template <int Q>
 __device__ __forceinline__ double write_gates(Gates<Q>& G, const float (&log_decay)[Q / 64], const float (&gate)[Q / 64],
                                               int lane, bool reverse) {
   constexpr int U = Q / 64;
-  float ld[U];
   double own[U], sum = 0.0;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    ld[u] = log_decay[u] < kMinLogDecay ? kMinLogDecay : log_decay[u];   // keeps NaN
-    own[u] = static_cast<double>(ld[u]) * static_cast<double>(1.44269504088896340736);
+    const float ld = log_decay[u] < kMinLogDecay ? kMinLogDecay : log_decay[u];   // keeps NaN
+    own[u] = static_cast<double>(ld) * static_cast<double>(1.44269504088896340736);
     sum += own[u];
   }
   const double upto = wave_prefix_d(sum), e = read_lane_d(upto, 63);
@@ -501,7 +498,6 @@ __device__ __forceinline__ double write_gates(Gates<Q>& G, const float (&log_dec
     G.hi[t] = hi;
     G.lo[t] = static_cast<float>(c - static_cast<double>(hi));
     G.b[t] = gate[u];
-    G.own[t] = __builtin_amdgcn_exp2f(ld[u] * kLog2e);
     const float first = __builtin_amdgcn_exp2f(static_cast<float>(c)), last = __builtin_amdgcn_exp2f(static_cast<float>(e - c));
     G.first[t] = first;
     G.last[t] = last;
@@ -560,6 +556,21 @@ __device__ __forceinline__ float sum_lanes4(float s0, float s1, float s2, float 
   v += dpp_f<kDppRor8>(v);
   v += dpp_f<0x124>(v);   // row_ror:4
   return v;
+}
+
+// Sums over the lanes of a 16-lane row: up to a lane, before it, and from it on.
+__device__ __forceinline__ float lanes_upto(float v) {
+  v += dpp_f<kDppShr1>(v);
+  v += dpp_f<kDppShr2>(v);
+  v += dpp_f<kDppShr4>(v);
+  return v + dpp_f<kDppShr8>(v);
+}
+__device__ __forceinline__ float lanes_before(float v) { return dpp_f<kDppShr1>(lanes_upto(v)); }
+__device__ __forceinline__ float lanes_from(float v) {
+  v += dpp_f<kDppShl1>(v);
+  v += dpp_f<kDppShl2>(v);
+  v += dpp_f<kDppShl4>(v);
+  return v + dpp_f<kDppShl8>(v);
 }
 
 // Tile e of the 16 x 16 tiles on and below the diagonal, row by row (at most
