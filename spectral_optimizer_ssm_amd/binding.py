@@ -308,9 +308,23 @@ def _marshal_groups(groups: Sequence[MuonGroup], precision: int = MUON_BF16, dev
     return arr, keep
 
 
-def _workspace(workspace, need, device):
+def _new(shape, dtype, device, stream):
+    """A new tensor that a call on `stream` (None: torch's current one) writes.
+    It comes from that stream's memory: a block that was freed on another stream
+    may still be in use there when the call starts.  The caller's own stream is
+    recorded, so the memory is not given out again before its work with it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _workspace(workspace, need, device, stream=None):
     """The caller's workspace when it is a large enough uint8 tensor on the
-    device, else a new one."""
+    device, else a new one for a call on `stream`."""
     import torch
     if workspace is not None:
         if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
@@ -319,7 +333,7 @@ def _workspace(workspace, need, device):
             raise ValueError(f"workspace must be on {device} (got {workspace.device})")
         if workspace.numel() >= need:
             return workspace
-    return torch.empty(need, dtype=torch.uint8, device=device)
+    return _new(need, torch.uint8, device, stream)
 
 
 # ----------------------------------------------------------------------------
@@ -363,7 +377,7 @@ def muon_step(groups: Sequence[MuonGroup], steps=5, coeffs=(1.5, -0.5), eps=1e-7
     if need == 0:  # the size query has no status: ask the step itself, which validates first
         rc = L.muon_step(cg, len(groups), ctypes.byref(cfg), None, 0, None, None)
         _check(MUON_EINVAL if rc in (MUON_OK, MUON_EWORKSPACE) else rc, "muon_step")
-    workspace = _workspace(workspace, need, dev)
+    workspace = _workspace(workspace, need, dev, stream)
     if norms_out is not None:
         total = sum(int(c.count) for c in cg)
         if not norms_out.is_contiguous() or norms_out.numel() < total:
@@ -420,7 +434,7 @@ def muon_ns_orthogonalize(G, O, steps=5, coeffs=(1.5, -0.5), eps=1e-7, per_step=
     need = int(L.muon_ns_workspace_size(m, n, b, dt, ctypes.byref(cfg)))
     if need == 0:
         _check(MUON_EINVAL, "muon_ns_workspace_size")
-    workspace = _workspace(workspace, need, dev)
+    workspace = _workspace(workspace, need, dev, stream)
     rc = L.muon_ns_orthogonalize(ctypes.c_void_p(G3.data_ptr()), ctypes.c_void_p(O3.data_ptr()), dt, m, n, ld, b,
                                  stride, ctypes.byref(cfg), ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
                                  _stream_handle(stream))
@@ -490,7 +504,7 @@ def muon_ns_factored(V, K, C=None, O=None, steps=1, coeffs=(1.5, -0.5), eps=1e-7
     _check_tensors([V, K], "V and K", (torch.bfloat16, torch.float32), dev)
     dt = _dtype_code(V)
     if C is None:
-        C = torch.empty(b, r, r, dtype=torch.float32, device=dev)
+        C = _new((b, r, r), torch.float32, dev, stream)
     if not C.is_contiguous() or tuple(C.shape) != (b, r, r):
         raise ValueError(f"C must be a contiguous [{b}, {r}, {r}] float32 tensor")
     _check_tensors([C], "C", (torch.float32,), dev)
@@ -540,7 +554,7 @@ def muon_ssm_momentum(V, K, M, S=None, decay=None, beta=0.9, steps=1, coeffs=(1.
     need = int(L.muon_ssm_momentum_workspace_size(m, n, r, nseq, T))
     if need == 0:
         raise MuonError(MUON_EUNSUPPORTED, "muon_ssm_momentum_workspace_size")
-    ws = _workspace(workspace, need, dev)
+    ws = _workspace(workspace, need, dev, stream)
     cfg, arr = make_cfg(steps, coeffs, eps, MUON_BF16, per_step)
     args = (ctypes.c_void_p(V.data_ptr()), ctypes.c_void_p(K.data_ptr()), MUON_BF16, m, n, r, nseq, T, float(beta),
             _fptr(decay if S is not None else None), _fptr(M), _fptr(S), ctypes.byref(cfg),
@@ -619,12 +633,12 @@ def muon_spectral_diag(A, iters=32, orth_err=True, sigma_max=True, sigma_min=Tru
     outs = {}
     for name, want in (("orth_err", orth_err), ("sigma_max", sigma_max), ("sigma_min", sigma_min)):
         if want:
-            outs[name] = torch.empty(b, dtype=torch.float32, device=dev)
+            outs[name] = _new(b, torch.float32, dev, stream)
     need = L.muon_spectral_diag_workspace_size(m, n, b, dt, int(iters))
     if need == 0:
         rc = L.muon_spectral_diag(None, dt, m, n, b, int(iters), None, None, None, None, 0, None)
         _check(rc if rc != MUON_OK else -1, "muon_spectral_diag")
-    workspace = _workspace(workspace, max(int(need), 1), dev)
+    workspace = _workspace(workspace, max(int(need), 1), dev, stream)
     ptr = lambda k: ctypes.c_void_p(outs[k].data_ptr()) if k in outs else None  # noqa: E731
     args = (ctypes.c_void_p(A.data_ptr()), dt, m, n, b, int(iters), ptr("orth_err"), ptr("sigma_max"),
             ptr("sigma_min"), ctypes.c_void_p(workspace.data_ptr()), need, _stream_handle(stream))
@@ -662,11 +676,27 @@ def _device_index() -> int:
     return torch.cuda.current_device()
 
 
-def _raw_stream(stream, index) -> Optional[int]:
-    """The caller's stream (or torch's current one) as a hipStream_t."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index) or None
-    return int(stream.cuda_stream) or None
+def _raw_stream(index) -> Optional[int]:
+    """torch's current stream as a hipStream_t."""
+    return torch._C._cuda_getCurrentRawStream(index) or None
+
+
+def _on(stream, call, *args, **kwargs):
+    """call(...) on another stream than torch's current one: made torch's current
+    stream for it, so that new outputs and workspaces come from its memory (a
+    block that was freed on the caller's may still be in use there when the call
+    starts).  Of what the call gave or was given to write, neither stream gives
+    the memory out again before the other is done with it."""
+    if torch is None:
+        _load_torch()
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = call(*args, **kwargs)
+    for t in (*out, kwargs.get("workspace")):
+        if t is not None:
+            t.record_stream(here)
+            t.record_stream(stream)
+    return out
 
 
 def _where(t, name, index):
@@ -764,14 +794,6 @@ def _ptr(t):
     return None if t is None or t.numel() == 0 else t.data_ptr()
 
 
-def _used_on(stream, *tensors):
-    """Tensors made on torch's current stream for a call on another one: their
-    memory is not given out again before that stream is past the call."""
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
-
-
 def _new_workspace(workspace, need, index):
     if workspace is None:
         return torch.empty(need, dtype=torch.uint8, device=index)
@@ -800,6 +822,8 @@ def muon_gated_scan(V, K, Q, log_decay, gate=None, S0=None, Y=None, S_out=None, 
     of V's dtype and float32, and the last state, in the tensors given or in
     new ones.  workspace: a uint8 tensor of at least
     muon_gated_scan_workspace_size bytes to use instead of a new one."""
+    if stream is not None:
+        return _on(stream, muon_gated_scan, V, K, Q, log_decay, gate=gate, S0=S0, Y=Y, S_out=S_out, workspace=workspace)
     L = lib()
     dev = _device_index()
     args, (b, t, h, g, p, n) = _scan_call(V, K, Q, log_decay, gate, S0, dev)
@@ -809,10 +833,8 @@ def muon_gated_scan(V, K, Q, log_decay, gate=None, S0=None, Y=None, S_out=None, 
     Y = _out(Y, "Y", (b, t, h, p), V.dtype, dev)
     S_out = _out(S_out, "S_out", (b, h, p, n), torch.float32, dev)
     ws = _new_workspace(workspace, need, dev)
-    rc = L.muon_gated_scan(args, _ptr(Y), _ptr(S_out), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
+    rc = L.muon_gated_scan(args, _ptr(Y), _ptr(S_out), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     _check(rc, "muon_gated_scan")
-    if stream is not None:
-        _used_on(stream, Y, S_out, ws)
     return Y, S_out
 
 
@@ -823,6 +845,9 @@ def muon_gated_scan_backward(V, K, Q, log_decay, dY, gate=None, S0=None, dS=None
     dlog_decay, dgate, dS0), of the shapes and dtypes of what they are the
     gradients of, in the tensors given or in new ones; dgate is None without a
     gate, dS0 without S0."""
+    if stream is not None:
+        return _on(stream, muon_gated_scan_backward, V, K, Q, log_decay, dY, gate=gate, S0=S0, dS=dS, dV=dV, dK=dK, dQ=dQ,
+                   dlog_decay=dlog_decay, dgate=dgate, dS0=dS0, workspace=workspace)
     L = lib()
     dev = _device_index()
     args, (b, t, h, g, p, n) = _scan_call(V, K, Q, log_decay, gate, S0, dev)
@@ -847,10 +872,8 @@ def muon_gated_scan_backward(V, K, Q, log_decay, dY, gate=None, S0=None, dS=None
     ws = _new_workspace(workspace, need, dev)
     rc = L.muon_gated_scan_backward(args, _SEQ.pack(*_seq(dY, dY.shape, "dY")), _ptr(dS), _ptr(dV), _ptr(dK), _ptr(dQ),
                                     _ptr(dlog_decay), _ptr(dgate), _ptr(dS0), ws.data_ptr(), ws.numel(),
-                                    _raw_stream(stream, dev))
+                                    _raw_stream(dev))
     _check(rc, "muon_gated_scan_backward")
-    if stream is not None:
-        _used_on(stream, dV, dK, dQ, dlog_decay, dgate, dS0, ws)
     return dV, dK, dQ, dlog_decay, dgate, dS0
 
 
@@ -859,6 +882,8 @@ def muon_gated_scan_step(V, K, Q, log_decay, S, gate=None, Y=None, S_out=None, s
     [batch, groups, N], log_decay and gate [batch, heads], S [batch, heads, P,
     N] float32, updated in place unless S_out is given.  Returns (Y, S_out or
     S)."""
+    if stream is not None:
+        return _on(stream, muon_gated_scan_step, V, K, Q, log_decay, S, gate=gate, Y=Y, S_out=S_out)
     dev = _device_index()
     args, (b, t, h, g, p, n) = _scan_call(V, K, Q, log_decay, gate, S, dev, token=False)
     Y = _out(Y, "Y", (b, h, p), V.dtype, dev)
@@ -866,10 +891,8 @@ def muon_gated_scan_step(V, K, Q, log_decay, S, gate=None, Y=None, S_out=None, s
         S_out = S
     else:
         _check_state(S_out, "S_out", (b, h, p, n), dev)
-    rc = lib().muon_gated_scan_step(args, _ptr(Y), _ptr(S_out), _raw_stream(stream, dev))
+    rc = lib().muon_gated_scan_step(args, _ptr(Y), _ptr(S_out), _raw_stream(dev))
     _check(rc, "muon_gated_scan_step")
-    if stream is not None:
-        _used_on(stream, Y)
     return Y, S_out
 
 
@@ -912,6 +935,8 @@ def muon_layer_norm(X, weight=None, bias=None, eps=1e-5, center=True, Y=None, st
     root-mean-square norm (mean 0).  weight and bias are float32.  Returns (Y,
     mean, rstd): Y of X's dtype, the float32 statistics of the rows for the
     backward pass (mean None without centering)."""
+    if stream is not None:
+        return _on(stream, muon_layer_norm, X, weight=weight, bias=bias, eps=eps, center=center, Y=Y)
     dev = _device_index()
     code = _type_code(X, "X")
     _where(X, "X", dev)
@@ -930,10 +955,8 @@ def muon_layer_norm(X, weight=None, bias=None, eps=1e-5, center=True, Y=None, st
     rstd = torch.empty(lead, dtype=torch.float32, device=dev)
     mean = torch.empty_like(rstd) if center else None
     rc = lib().muon_layer_norm(_ptr(X), ldx, code, rows, n, w, b, eps, 1 if center else 0, _ptr(Y), ldy, _ptr(mean),
-                               _ptr(rstd), _raw_stream(stream, dev))
+                               _ptr(rstd), _raw_stream(dev))
     _check(rc, "muon_layer_norm")
-    if stream is not None:
-        _used_on(stream, Y, mean, rstd)
     return Y, mean, rstd
 
 
@@ -941,6 +964,9 @@ def muon_layer_norm_backward(dY, X, weight, mean, rstd, center=True, bias_grad=T
     """Gradients through muon_layer_norm from its input, weight and the
     statistics that it returned: (dX, dweight, dbias), dweight None without a
     weight, dbias None unless bias_grad."""
+    if stream is not None:
+        return _on(stream, muon_layer_norm_backward, dY, X, weight, mean, rstd, center=center, bias_grad=bias_grad,
+                   workspace=workspace)
     L = lib()
     dev = _device_index()
     code = _type_code(X, "X")
@@ -969,8 +995,6 @@ def muon_layer_norm_backward(dY, X, weight, mean, rstd, center=True, bias_grad=T
     ws = _new_workspace(workspace, need, dev)
     rc = L.muon_layer_norm_backward(_ptr(dY), lddy, _ptr(X), ldx, code, rows, n, w, _ptr(mean) if center else None, _ptr(rstd),
                                     _ptr(dX), n, _ptr(dweight), _ptr(dbias), ws.data_ptr(), ws.numel(),
-                                    _raw_stream(stream, dev))
+                                    _raw_stream(dev))
     _check(rc, "muon_layer_norm_backward")
-    if stream is not None:
-        _used_on(stream, dX, dweight, dbias, ws)
     return dX, dweight, dbias
