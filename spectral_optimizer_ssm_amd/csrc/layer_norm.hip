@@ -96,6 +96,14 @@ __device__ __forceinline__ float row_total(float v, float* red) {
   else return block_sum(v, red);
 }
 
+// A dimension of a launch has fewer than 2^32 work items, which 2^24 rows of a
+// workgroup each exceed: past 2^20 workgroups the grid has a second dimension.
+dim3 grid_of(long long blocks) {
+  const long long x = blocks < (1 << 20) ? blocks : 1 << 20;
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>((blocks + x - 1) / x));
+}
+__device__ __forceinline__ long long block_of_grid() { return static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x; }
+
 // Threads of a workgroup whose rows take TPR threads each.
 template <int TPR>
 constexpr int threads_of() { return TPR < kThreads ? kThreads : TPR; }
@@ -106,7 +114,7 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_kernel(NormLaunch A) {
   constexpr int V = Vec<T>::n, kRows = threads_of<TPR>() / TPR;
   __shared__ float red[threads_of<TPR>() / kWave];
   const int sub = kRows == 1 ? 0 : threadIdx.x / TPR, t = threadIdx.x % TPR;
-  const long long row = static_cast<long long>(blockIdx.x) * kRows + sub;
+  const long long row = block_of_grid() * kRows + sub;
   if (row >= A.rows) return;   // whole waves or whole workgroups
   const T* x = static_cast<const T*>(A.x) + row * A.ldx;
   float v[PIECES][V];
@@ -161,7 +169,8 @@ __global__ void __launch_bounds__(threads_of<TPR>()) norm_kernel(NormLaunch A) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_long_kernel(NormLaunch A) {
   __shared__ float red[kThreads / kWave];
-  const long long row = blockIdx.x;
+  const long long row = block_of_grid();
+  if (row >= A.rows) return;
   const T* x = static_cast<const T*>(A.x) + row * A.ldx;
   const float inv_n = 1.0f / static_cast<float>(A.n);
   const auto at = [&](int c) {
@@ -390,7 +399,7 @@ RowPlan row_plan(int n, int elems) {
 template <typename T, int TPR, int PIECES>
 hipError_t norm(const NormLaunch& A, hipStream_t st) {
   constexpr int kRows = threads_of<TPR>() / TPR;
-  const dim3 grid(static_cast<unsigned>((A.rows + kRows - 1) / kRows)), block(threads_of<TPR>());
+  const dim3 grid = grid_of((A.rows + kRows - 1) / kRows), block(threads_of<TPR>());
   hipLaunchKernelGGL((norm_kernel<T, TPR, PIECES>), grid, block, 0, st, A);
   return hipGetLastError();
 }
@@ -401,7 +410,7 @@ hipError_t norm_any(const NormLaunch& A, hipStream_t st) {
   if (p.threads == kWave) return p.pieces == 1 ? norm<T, kWave, 1>(A, st) : p.pieces == 2 ? norm<T, kWave, 2>(A, st) : norm<T, kWave, 4>(A, st);
   if (p.threads == kThreads) return p.pieces == 2 ? norm<T, kThreads, 2>(A, st) : norm<T, kThreads, 4>(A, st);
   if (p.threads != 0) return norm<T, 2 * kThreads, 4>(A, st);
-  hipLaunchKernelGGL((norm_long_kernel<T>), dim3(static_cast<unsigned>(A.rows)), dim3(kThreads), 0, st, A);
+  hipLaunchKernelGGL((norm_long_kernel<T>), grid_of(A.rows), dim3(kThreads), 0, st, A);
   return hipGetLastError();
 }
 
