@@ -442,8 +442,10 @@ typedef struct {
  *              after it (values below -10000 are taken as that)
  *   gate       b, as log_decay; gate.p NULL: 1
  *   S0         NULL (zero), or [batch][heads][P][N] float32, contiguous
- * Supported: N <= 128 (else MUON_EUNSUPPORTED), any P; batch or tokens may be
- * 0.  v, k, q and the states must be finite (a NaN or Inf reaches the whole
+ * Supported: N <= 128, any P, and as many sequences and heads as one launch
+ * takes: batch x heads x ceil(P / 64) up to 6.7e6, for the backward pass also
+ * batch x groups x ceil(tokens / 64), for one token batch x heads x ceil(P / 32)
+ * up to 1.6e7 (else MUON_EUNSUPPORTED).  batch or tokens may be 0.  v, k, q and the states must be finite (a NaN or Inf reaches the whole
  * chunk of 64 tokens that holds it, earlier tokens included).  Rows that are
  * 16-byte aligned and a multiple of 16 bytes wide take vectorised loads.
  * States, sums and gates are float32 (decays summed in float64); with

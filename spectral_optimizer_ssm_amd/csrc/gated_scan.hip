@@ -20,6 +20,8 @@
 //
 // In reversed time the same walk with (dy, q) for (v, k), weights e^{c_i} and
 // no reads gives the gradients of the states (muon_gated_scan_backward).
+#include <climits>
+
 #include "scan_tiles.cuh"
 
 namespace muon {
@@ -32,7 +34,7 @@ using namespace scan;
 constexpr int kReadWaves = 8, kStatesWaves = 4;
 constexpr int kReadThreads = kReadWaves * kWave, kStatesThreads = kStatesWaves * kWave;
 constexpr int kStateCols = 64;   // columns n of S per workgroup of the states' walk
-constexpr int kStepThreads = 256;
+constexpr int kStepThreads = kScanStepThreads;
 
 struct WalkPair {
   ScanWalk w[2];
@@ -543,7 +545,7 @@ template <typename T, int EACH>
 __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanStep A) {
   constexpr int kRows = EACH * kStepHalves;
   const int half = threadIdx.x >> 5, l = threadIdx.x & 31, n0 = 4 * l;
-  const int pblocks = (A.P + kRows - 1) / kRows;
+  const int pblocks = (A.P - 1) / kRows + 1;
   const int pb = static_cast<int>(blockIdx.x) % pblocks;
   const long long bh = blockIdx.x / pblocks;
   const int h = static_cast<int>(bh % A.heads), grp = h / (A.heads / A.groups);
@@ -608,21 +610,28 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanStep A) {
 
 template <int EACH>
 hipError_t step(const ScanStep& A, bool bf16, hipStream_t st) {
-  constexpr int kRows = EACH * kStepHalves;
-  const dim3 grid(static_cast<unsigned>(static_cast<long long>(A.batch) * A.heads * ((A.P + kRows - 1) / kRows)));
+  const dim3 grid(static_cast<unsigned>(scan_step_blocks(A.batch, A.heads, A.P)));
   if (bf16) hipLaunchKernelGGL((scan_step_kernel<bf16_t, EACH>), grid, dim3(kStepThreads), 0, st, A);
   else hipLaunchKernelGGL((scan_step_kernel<float, EACH>), grid, dim3(kStepThreads), 0, st, A);
   return hipGetLastError();
 }
 
-}  // namespace
-
 // Four rows a half-wave where that leaves two workgroups to each of 256 compute
 // units, two where it does not: 192 heads of 64 x 128 take 6.6 us by four and
 // 5.9 by two (24 heads 5.4 and 4.4), 384 heads 8.0 and 8.6, 1,536 heads 20 and 26.
+int step_rows(int batch, int heads, int P) {
+  return static_cast<double>(batch) * heads * P >= 2.0 * 256 * 4 * kStepHalves ? 4 : 2;
+}
+
+}  // namespace
+
+long long scan_step_blocks(int batch, int heads, int P) {
+  const int rows = step_rows(batch, heads, P) * kStepHalves, pblocks = (P - 1) / rows + 1;
+  const long long bh = static_cast<long long>(batch) * heads;
+  return bh > LLONG_MAX / pblocks ? LLONG_MAX : bh * pblocks;
+}
 hipError_t launch_scan_step(const ScanStep& A, bool bf16, hipStream_t st) {
-  const long long rows = static_cast<long long>(A.batch) * A.heads * A.P;
-  return rows >= 2LL * 256 * 4 * kStepHalves ? step<4>(A, bf16, st) : step<2>(A, bf16, st);
+  return step_rows(A.batch, A.heads, A.P) == 4 ? step<4>(A, bf16, st) : step<2>(A, bf16, st);
 }
 
 namespace {

@@ -309,6 +309,10 @@ constexpr int kScanChunk = 64;     // tokens per chunk
 // 64, half of whose tiles would be padding otherwise (64 of them, 24 heads: 112 us, 124
 // in blocks of 128).
 inline int scan_grad_tokens(bool bf16, int tokens) { return bf16 && tokens > kScanChunk ? 2 * kScanChunk : kScanChunk; }
+// Work items that a launch has at most for a walk (sequence, head, kScanRows state
+// rows: two workgroups of the states' walk) or a block of the backward pass; cut
+// walks and split blocks are few.
+constexpr int kScanItemThreads = 640;
 constexpr int kScanRows = 64;      // state rows (value components) per workgroup
 constexpr int kScanMaxN = 128;     // largest key length
 // Kernels for up to 64 and up to 128 columns of the state: eight sequences of
@@ -366,6 +370,8 @@ struct ScanStep {
   const float* S;             // [batch][heads][P][N]
   float* S_out;               // may be S
 };
+constexpr int kScanStepThreads = 256;
+long long scan_step_blocks(int batch, int heads, int P);
 hipError_t launch_scan_step(const ScanStep& A, bool bf16, hipStream_t st);
 
 // dst = src, or 0 where src is null (the final state of a scan without tokens).

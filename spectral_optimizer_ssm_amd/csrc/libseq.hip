@@ -59,6 +59,15 @@ int check_operands(const muon_scan_args* a) {
   return MUON_OK;
 }
 
+// A dimension of a launch has fewer than 2^32 work items; past that a grid is
+// taken modulo 2^32, without an error.
+bool launchable(long long blocks, int threads) { return blocks <= 0xffffffffLL / threads; }
+// The product, or LLONG_MAX where it does not fit.
+long long times(long long a, long long b, long long c) {
+  long long p;
+  return __builtin_mul_overflow(a, b, &p) || __builtin_mul_overflow(p, c, &p) ? LLONG_MAX : p;
+}
+
 // Where to stop cutting work: one workgroup of the forward walk or of the
 // backward pass for each of 256 compute units (their tiles fill its LDS), and
 // 384 walks of the states, which are lighter.  Measured with 24 heads of 64 x
@@ -87,11 +96,12 @@ constexpr int kSegChunks = 4;
 int grad_tokens(const muon_scan_args* a) { return scan_grad_tokens(a->dtype == MUON_BF16, a->tokens); }
 
 int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
-  p->pblocks = (a->P + kScanRows - 1) / kScanRows;
+  p->pblocks = (a->P - 1) / kScanRows + 1;
   p->nchunks = static_cast<int>((static_cast<long long>(a->tokens) + kScanChunk - 1) / kScanChunk);
   const int block = grad_tokens(a);
   p->nblocks = static_cast<int>((static_cast<long long>(a->tokens) + block - 1) / block);
-  const long long vrows = static_cast<long long>(a->batch) * a->heads * p->pblocks;
+  const long long vrows = times(a->batch, a->heads, p->pblocks), groups = times(a->batch, p->nblocks, a->groups);
+  if (!launchable(vrows, kScanItemThreads) || (backward && !launchable(groups, kScanItemThreads))) return MUON_EUNSUPPORTED;
   const long long walks = backward ? 2 * vrows : vrows;
   if (a->batch == 0 || a->tokens == 0) {
     p->nseg = p->nsplit = 1;
@@ -103,11 +113,9 @@ int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
   if (nseg < (backward ? 5 : 2)) nseg = 1;
   p->seg_chunks = static_cast<int>((p->nchunks + nseg - 1) / nseg);
   p->nseg = (p->nchunks + p->seg_chunks - 1) / p->seg_chunks;
-  const long long groups = static_cast<long long>(a->batch) * p->nblocks * a->groups;
   p->nsplit = static_cast<int>(std::min<long long>(a->heads / a->groups, std::max<long long>(1, kGradFill / groups)));
   const int per_split = (a->heads / a->groups + p->nsplit - 1) / p->nsplit;
   p->nsplit = (a->heads / a->groups + per_split - 1) / per_split;   // none without heads
-  if (2 * vrows * p->nseg > INT_MAX || groups * p->nsplit > INT_MAX) return MUON_EUNSUPPORTED;
   const size_t tile = static_cast<size_t>(kScanRows) * scan_padded_n(a->N) * sizeof(float);
   size_t off = 0;
   const auto take = [&](size_t bytes) {
@@ -124,7 +132,6 @@ int plan_scan(const muon_scan_args* a, bool backward, ScanPlan* p) {
     p->states = take(vrows * p->nblocks * tile);
     p->dstates = take(vrows * p->nblocks * tile);
     const size_t half = static_cast<size_t>(a->batch) * a->tokens * a->groups * a->N;
-    if (p->nsplit > 1 && 2 * half / 256 + 1 > static_cast<size_t>(INT_MAX)) return MUON_EUNSUPPORTED;
     p->parts = take(p->nsplit > 1 ? static_cast<size_t>(p->nsplit) * 2 * half * 4 : 0);
   }
   p->end = std::max(off, kAlign);
@@ -284,6 +291,7 @@ int muon_gated_scan_step(const muon_scan_args* a, void* Y, float* S_out, void* s
   int rc = check_dims(a);
   if (rc != MUON_OK) return rc;
   if (a->tokens != 1) return MUON_EINVAL;
+  if (!launchable(scan_step_blocks(a->batch, a->heads, a->P), kScanStepThreads)) return MUON_EUNSUPPORTED;
   if (a->batch == 0) return MUON_OK;
   rc = check_operands(a);
   if (rc != MUON_OK) return rc;
@@ -297,7 +305,6 @@ int muon_gated_scan_step(const muon_scan_args* a, void* Y, float* S_out, void* s
   const Span s0 = span(a->S0, state_bytes(a)), so = span(S_out, state_bytes(a));
   const bool in_place = a->S0 == S_out;
   if (clash({span(Y, value_bytes(a)), so}, {v, k, q, g, gate_span(a), in_place ? Span{nullptr, 0} : s0})) return MUON_EINVAL;
-  if (static_cast<long long>(a->batch) * a->heads * ((a->P + 15) / 16) > INT_MAX) return MUON_EUNSUPPORTED;
   ScanStep s{};
   s.v = operand(a->v);
   s.k = operand(a->k);

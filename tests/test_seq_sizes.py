@@ -1,0 +1,47 @@
+"""Sizes past what the sequence operators' launches and counts hold are
+refused (no GPU needed: nothing is enqueued, pointers are made up)."""
+import pytest
+
+from test_seq_abi import ADDR, EUNSUPPORTED, args, bwd, fwd, mu  # noqa: F401
+
+torch = pytest.importorskip("torch")
+
+INT_MAX = 2**31 - 1
+AT_ONE = {n: (ADDR[n], 0, 0, 0) for n in ("v", "k", "q", "g")}    # strides that fit any size
+
+
+@pytest.mark.parametrize("sizes", [
+    dict(batch=7_000_000, heads=1, groups=1, P=1, N=1),           # 7e6 walks of 640 work items: past 2^32
+    dict(batch=7_000_000, heads=1, groups=1, P=64, N=128),
+    dict(batch=1, heads=3_500_000, groups=1, P=65, N=1),          # two blocks of value rows each
+    dict(batch=1, heads=1, groups=1, P=INT_MAX, N=1),             # ceil(P / 64) without overflow
+    dict(batch=INT_MAX, heads=INT_MAX, groups=1, P=INT_MAX, N=1),
+    dict(batch=1 << 30, heads=1 << 30, groups=1 << 30, P=1 << 30, N=1),
+], ids=str)
+@pytest.mark.parametrize("tokens", [1, 100])
+def test_scan_past_a_launch(mu, sizes, tokens):
+    a = args(tokens=tokens, **sizes, **AT_ONE)
+    L = mu.lib()
+    assert L.muon_gated_scan_workspace_size(a) == 0 and L.muon_gated_scan_backward_workspace_size(a) == 0
+    assert fwd(mu, a) == EUNSUPPORTED and bwd(mu, a) == EUNSUPPORTED
+
+
+def test_backward_past_a_launch(mu):
+    """Blocks of tokens, which the forward pass walks one after the other."""
+    a = args(batch=1000, tokens=1_000_000, heads=1, groups=1, P=1, N=1)
+    assert mu.lib().muon_gated_scan_workspace_size(a) > 0
+    assert mu.lib().muon_gated_scan_backward_workspace_size(a) == 0 and bwd(mu, a) == EUNSUPPORTED
+
+
+@pytest.mark.parametrize("sizes", [
+    dict(batch=17_000_000, heads=1, groups=1, P=1, N=4), dict(batch=1, heads=9_000_000, groups=1, P=33, N=1),
+    dict(batch=1, heads=1, groups=1, P=INT_MAX, N=1), dict(batch=INT_MAX, heads=INT_MAX, groups=1, P=INT_MAX, N=1),
+], ids=str)
+def test_step_past_a_launch(mu, sizes):
+    assert mu.lib().muon_gated_scan_step(args(tokens=1, **sizes, **AT_ONE), ADDR["Y"], ADDR["S"], None) == EUNSUPPORTED
+
+
+def test_sizes_below_that_are_accepted(mu):
+    L = mu.lib()
+    assert L.muon_gated_scan_workspace_size(args(batch=6_000_000, tokens=1, heads=1, groups=1, P=64, N=128)) > 0
+    assert L.muon_gated_scan_backward_workspace_size(args(batch=1000, tokens=200_000, heads=1, groups=1, P=1, N=1)) > 0
