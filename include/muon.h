@@ -422,7 +422,7 @@ int muon_spectral_diag_timed(const void* A, int dtype, int m, int n, long long b
 
 /* An operand of a sequence operator, [batch][tokens][heads or groups][width]:
  * token t of sequence b, head h starts at element b sb + t st + h sh of p
- * (strides in elements, >= 0; the width elements themselves are adjacent), so
+ * (strides in elements, >= 0 the width elements themselves are adjacent), so
  * a column range of a wider tensor needs no copy. */
 typedef struct {
   const void* p;
@@ -500,7 +500,8 @@ int muon_gated_scan_step(const muon_scan_args* args, void* Y, float* S_out, void
  *               apart (>= n); Y must not overlap X
  *   weight, bias  NULL (1 and 0), or float32[n]
  *   mean, rstd  NULL, or float32[rows] receiving mu and r
- * Statistics are float32, the variance taken around the mean.  rows < 2^31. */
+ * Statistics are float32, the variance taken around the mean.  rows < 2^31 and
+ * n <= 2^27 (else MUON_EUNSUPPORTED). */
 int muon_layer_norm(const void* X, long long ldx, int dtype, long long rows, int n, const float* weight,
                     const float* bias, float eps, int center, void* Y, long long ldy, float* mean, float* rstd,
                     void* stream);

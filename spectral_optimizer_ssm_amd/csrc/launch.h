@@ -377,7 +377,9 @@ hipError_t launch_scan_step(const ScanStep& A, bool bf16, hipStream_t st);
 // dst = src, or 0 where src is null (the final state of a scan without tokens).
 hipError_t launch_copy_f32(const float* src, float* dst, long long n, hipStream_t st);
 
-// Layer norm (layer_norm.hip).
+// Layer norm (layer_norm.hip).  Longest row: its columns count in int, and 1,024
+// threads for 64 of them below 2^32.
+constexpr int kNormMaxN = 1 << 27;
 struct NormLaunch {
   const void* x;
   void* y;

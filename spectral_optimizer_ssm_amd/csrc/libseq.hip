@@ -326,7 +326,7 @@ namespace {
 int check_norm(int dtype, long long rows, int n) {
   if (dtype != MUON_F32 && dtype != MUON_BF16) return MUON_EINVAL;
   if (rows < 0 || n <= 0) return MUON_EINVAL;
-  return rows > INT_MAX ? MUON_EUNSUPPORTED : MUON_OK;
+  return rows > INT_MAX || n > kNormMaxN ? MUON_EUNSUPPORTED : MUON_OK;
 }
 Span rows_span(const void* p, long long rows, int n, long long ld, size_t es) {
   return span(p, rows == 0 ? 0 : static_cast<size_t>((rows - 1) * ld + n) * es);

@@ -2,7 +2,7 @@
 refused (no GPU needed: nothing is enqueued, pointers are made up)."""
 import pytest
 
-from test_seq_abi import ADDR, EUNSUPPORTED, args, bwd, fwd, mu  # noqa: F401
+from test_seq_abi import ADDR, EUNSUPPORTED, args, bwd, fwd, mu, norm, norm_bwd  # noqa: F401
 
 torch = pytest.importorskip("torch")
 
@@ -45,3 +45,13 @@ def test_sizes_below_that_are_accepted(mu):
     L = mu.lib()
     assert L.muon_gated_scan_workspace_size(args(batch=6_000_000, tokens=1, heads=1, groups=1, P=64, N=128)) > 0
     assert L.muon_gated_scan_backward_workspace_size(args(batch=1000, tokens=200_000, heads=1, groups=1, P=1, N=1)) > 0
+
+
+@pytest.mark.parametrize("n", [2**27 + 1, 2**28, 2**30, INT_MAX])
+def test_norm_rows_too_long(mu, n):
+    """Columns are counted in int, by steps of a workgroup."""
+    far = 1 << 50
+    assert norm(mu, n=n, ldx=n, ldy=n, rows=1, X=far, Y=2 * far, w=None, b=None) == EUNSUPPORTED
+    assert norm_bwd(mu, n=n, ldx=n, lddy=n, lddx=n, rows=1, X=far, dY=2 * far, dX=3 * far, w=None, dw=None, db=None) == EUNSUPPORTED
+    assert mu.lib().muon_layer_norm_backward_workspace_size(1, n, 1) == 0
+    assert mu.lib().muon_layer_norm_backward_workspace_size(1, 2**27, 1) > 0
