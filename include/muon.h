@@ -422,7 +422,7 @@ int muon_spectral_diag_timed(const void* A, int dtype, int m, int n, long long b
 
 /* An operand of a sequence operator, [batch][tokens][heads or groups][width]:
  * token t of sequence b, head h starts at element b sb + t st + h sh of p
- * (strides in elements, >= 0 the width elements themselves are adjacent), so
+ * (strides in elements, >= 0 and within 2^58 elements together; the width elements themselves are adjacent), so
  * a column range of a wider tensor needs no copy. */
 typedef struct {
   const void* p;

@@ -38,8 +38,17 @@ bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
   return false;
 }
 
-bool seq_ok(const muon_seq& s, size_t es) {
-  return s.p != nullptr && aligned_to(s.p, es) && s.sb >= 0 && s.st >= 0 && s.sh >= 0;
+// Whether a strided operand's bytes can be counted: no memory holds 2^60.
+bool extent_ok(std::initializer_list<long long> steps, std::initializer_list<long long> strides) {
+  long long sum = 0, p;
+  const long long* st = strides.begin();
+  for (long long n : steps)
+    if (__builtin_mul_overflow(n, *st++, &p) || __builtin_add_overflow(sum, p, &sum) || sum > 1LL << 58) return false;
+  return true;
+}
+bool seq_ok(const muon_seq& s, int batch, int tokens, int heads, size_t es) {
+  return s.p != nullptr && aligned_to(s.p, es) && s.sb >= 0 && s.st >= 0 && s.sh >= 0 &&
+         extent_ok({batch - 1, tokens - 1, heads - 1}, {s.sb, s.st, s.sh});
 }
 SeqOperand operand(const muon_seq& s) { return {s.p, s.sb, s.st, s.sh}; }
 
@@ -53,8 +62,9 @@ int check_dims(const muon_scan_args* a) {
 }
 int check_operands(const muon_scan_args* a) {
   const size_t es = dtype_size(a->dtype);
-  if (!seq_ok(a->v, es) || !seq_ok(a->k, es) || !seq_ok(a->q, es) || !seq_ok(a->log_decay, 4)) return MUON_EINVAL;
-  if (a->gate.p != nullptr && !seq_ok(a->gate, 4)) return MUON_EINVAL;
+  const auto ok = [a](const muon_seq& s, int heads, size_t es) { return seq_ok(s, a->batch, a->tokens, heads, es); };
+  if (!ok(a->v, a->heads, es) || !ok(a->k, a->groups, es) || !ok(a->q, a->groups, es) || !ok(a->log_decay, a->heads, 4)) return MUON_EINVAL;
+  if (a->gate.p != nullptr && !ok(a->gate, a->heads, 4)) return MUON_EINVAL;
   if (a->S0 != nullptr && !aligned_to(a->S0, 4)) return MUON_EINVAL;
   return MUON_OK;
 }
@@ -239,7 +249,7 @@ int muon_gated_scan_backward(const muon_scan_args* a, const muon_seq* dY, const 
   }
   rc = check_operands(a);
   if (rc != MUON_OK) return rc;
-  if (dY == nullptr || !seq_ok(*dY, es) || dV == nullptr || dK == nullptr || dQ == nullptr || dlog_decay == nullptr ||
+  if (dY == nullptr || !seq_ok(*dY, a->batch, a->tokens, a->heads, es) || dV == nullptr || dK == nullptr || dQ == nullptr || dlog_decay == nullptr ||
       !aligned_to(dV, es) || !aligned_to(dK, es) || !aligned_to(dQ, es) || !aligned_to(dlog_decay, 4) ||
       (dgate != nullptr && !aligned_to(dgate, 4)))
     return MUON_EINVAL;
@@ -328,6 +338,7 @@ int check_norm(int dtype, long long rows, int n) {
   if (rows < 0 || n <= 0) return MUON_EINVAL;
   return rows > INT_MAX || n > kNormMaxN ? MUON_EUNSUPPORTED : MUON_OK;
 }
+bool rows_ok(long long rows, int n, long long ld) { return ld >= n && (rows == 0 || extent_ok({rows - 1}, {ld})); }
 Span rows_span(const void* p, long long rows, int n, long long ld, size_t es) {
   return span(p, rows == 0 ? 0 : static_cast<size_t>((rows - 1) * ld + n) * es);
 }
@@ -338,7 +349,7 @@ int muon_layer_norm(const void* X, long long ldx, int dtype, long long rows, int
                     float eps, int center, void* Y, long long ldy, float* mean, float* rstd, void* stream) {
   const int rc = check_norm(dtype, rows, n);
   if (rc != MUON_OK) return rc;
-  if (!(eps >= 0.0f) || !std::isfinite(eps) || (center != 0 && center != 1) || ldx < n || ldy < n) return MUON_EINVAL;
+  if (!(eps >= 0.0f) || !std::isfinite(eps) || (center != 0 && center != 1) || !rows_ok(rows, n, ldx) || !rows_ok(rows, n, ldy)) return MUON_EINVAL;
   if (rows == 0) return MUON_OK;
   const size_t es = dtype_size(dtype);
   if (X == nullptr || Y == nullptr || !aligned_to(X, es) || !aligned_to(Y, es) || !aligned_to(weight, 4) ||
@@ -364,7 +375,7 @@ int muon_layer_norm_backward(const void* dY, long long lddy, const void* X, long
                              float* dweight, float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
   const int rc = check_norm(dtype, rows, n);
   if (rc != MUON_OK) return rc;
-  if (lddy < n || ldx < n || lddx < n) return MUON_EINVAL;
+  if (!rows_ok(rows, n, lddy) || !rows_ok(rows, n, ldx) || !rows_ok(rows, n, lddx)) return MUON_EINVAL;
   const size_t es = dtype_size(dtype), need = muon_layer_norm_backward_workspace_size(rows, n, dtype);
   if (!aligned_to(dweight, 4) || !aligned_to(dbias, 4) || !aligned_to(weight, 4)) return MUON_EINVAL;
   if (rows == 0 && dweight == nullptr && dbias == nullptr) return MUON_OK;

@@ -2,7 +2,7 @@
 refused (no GPU needed: nothing is enqueued, pointers are made up)."""
 import pytest
 
-from test_seq_abi import ADDR, EUNSUPPORTED, args, bwd, fwd, mu, norm, norm_bwd  # noqa: F401
+from test_seq_abi import ADDR, EINVAL, EUNSUPPORTED, args, bwd, fwd, mu, norm, norm_bwd  # noqa: F401
 
 torch = pytest.importorskip("torch")
 
@@ -47,6 +47,20 @@ def test_sizes_below_that_are_accepted(mu):
     assert L.muon_gated_scan_backward_workspace_size(args(batch=1000, tokens=200_000, heads=1, groups=1, P=1, N=1)) > 0
 
 
+@pytest.mark.parametrize("name", ["v", "k", "q", "g", "b"])
+@pytest.mark.parametrize("strides", [(2**62, 1, 1), (1, 2**61, 1), (1, 1, 2**62), (2**63 - 1, 2**63 - 1, 2**63 - 1)], ids=str)
+def test_strides_past_any_memory(mu, name, strides):
+    """Extents that overflow 64 bits, by which an overlap would go unseen."""
+    a = args(**{name: (ADDR["b" if name == "b" else name], *strides)})
+    assert fwd(mu, a) == EINVAL and bwd(mu, a) == EINVAL
+    one = args(tokens=1, **{name: (ADDR["b" if name == "b" else name], 2**62, 0, 2**62)})
+    assert mu.lib().muon_gated_scan_step(one, ADDR["Y"], ADDR["S"], None) == EINVAL
+
+
+def test_gradient_strides_past_any_memory(mu):
+    assert bwd(mu, args(), dY=(ADDR["dY"], 2**62, 256, 64)) == EINVAL
+
+
 @pytest.mark.parametrize("n", [2**27 + 1, 2**28, 2**30, INT_MAX])
 def test_norm_rows_too_long(mu, n):
     """Columns are counted in int, by steps of a workgroup."""
@@ -55,3 +69,9 @@ def test_norm_rows_too_long(mu, n):
     assert norm_bwd(mu, n=n, ldx=n, lddy=n, lddx=n, rows=1, X=far, dY=2 * far, dX=3 * far, w=None, dw=None, db=None) == EUNSUPPORTED
     assert mu.lib().muon_layer_norm_backward_workspace_size(1, n, 1) == 0
     assert mu.lib().muon_layer_norm_backward_workspace_size(1, 2**27, 1) > 0
+
+
+@pytest.mark.parametrize("ld", ["ldx", "ldy"])
+def test_norm_row_strides_past_any_memory(mu, ld):
+    assert norm(mu, **{ld: 2**62}) == EINVAL
+    assert norm_bwd(mu, **{"lddx" if ld == "ldy" else ld: 2**62}) == EINVAL and norm_bwd(mu, lddy=2**61) == EINVAL
