@@ -445,9 +445,15 @@ typedef struct {
  * Supported: N <= 128, any P, and as many sequences and heads as one launch
  * takes: batch x heads x ceil(P / 64) up to 6.7e6, for the backward pass also
  * batch x groups x ceil(tokens / 64), for one token batch x heads x ceil(P / 32)
- * up to 1.6e7 (else MUON_EUNSUPPORTED).  batch or tokens may be 0.  v, k, q and the states must be finite (a NaN or Inf reaches the whole
- * chunk of 64 tokens that holds it, earlier tokens included).  Rows that are
- * 16-byte aligned and a multiple of 16 bytes wide take vectorised loads.
+ * up to 1.6e7 (else MUON_EUNSUPPORTED).  batch or tokens may be 0.
+ * v, k, q and dY must be finite: a NaN or Inf reaches the whole chunk of 64
+ * tokens that holds it (128 in the backward pass with MUON_BF16) and the
+ * sequences that run on from there, but none that starts in a later chunk (back
+ * in time: that ends in an earlier one).  A state that is not finite is lost with
+ * its sequence, so one that starts at the first token may be given any.
+ * Rows of whole 16-byte pieces, at any address, take 16-byte loads if tokens are
+ * at least a row apart and outputs lie on multiples of four elements; others
+ * are read element by element.
  * States, sums and gates are float32 (decays summed in float64); with
  * MUON_BF16 the operands of the products that give y and the gradients of v,
  * k, q carry 16 bits or more, with float32 sums, so that these are off by little

@@ -168,7 +168,7 @@ struct Walk {
   __device__ __forceinline__ void update(const Gates<kQ>& G, const T* lkt, int n0, int rows, F values) {
     const float end = G.end[0];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) st[t] *= end;
+    for (int t = 0; t < KT; ++t) st[t] = decayed(st[t], end);
 #pragma unroll
     for (int s = 0; s < kQ / 32; ++s) {
       if (ended(32 * s, rows)) continue;
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(sizeof(T) == 2 ? kReadThreads + kWave : kReadT
       }
     }
 #pragma unroll
-    for (int it = 0; it < 4; ++it) y[it] *= G.first[16 * it + l16];
+    for (int it = 0; it < 4; ++it) y[it] = decayed(y[it], G.first[16 * it + l16]);
     // token tiles 2 nh and 2 nh + 1 stay, the others go to the other half's wave
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_segments_kernel(WalkPair W,
   for (int s = 0; s + 1 < A.nseg; ++s) {
     const float own = sp[static_cast<long long>(s) * kPB * nt];
     sp[static_cast<long long>(s) * kPB * nt] = cur;
-    cur = fmaf(dp[s], cur, own);
+    cur = own + decayed(cur, dp[s]);
   }
   sp[static_cast<long long>(A.nseg - 1) * kPB * nt] = cur;
 }
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kStepThreads) scan_step_kernel(ScanStep A) {
     float y = 0.0f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      s[u][r] = fmaf(decay, s[u][r], v * k[r]);
+      s[u][r] = fmaf(decay, decay == 0.0f ? 0.0f : s[u][r], v * k[r]);
       y = fmaf(s[u][r], q[r], y);
     }
 #pragma unroll

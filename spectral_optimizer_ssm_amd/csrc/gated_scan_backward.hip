@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
             const f32x4_t ov = TN::load4(other, t, 16 * (nw0 + b) + 4 * g4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float a = acc[u][r] * sv;
+              const float a = decayed(acc[u][r], sv);
               sums[u] = fmaf(a, ov[r], sums[u]);
               out[b][u0 + u][r] = gated ? fmaf(a, gt, out[b][u0 + u][r]) : out[b][u0 + u][r] + a;
             }
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int j = 16 * (kZG * u + (w >> 2)) + l16;
-        out.put(j, 16 * (w & 3) + 4 * g4, (z[u] + zs[u] * G.last[j]) * G.b[j]);
+        out.put(j, 16 * (w & 3) + 4 * g4, (z[u] + decayed(zs[u], G.last[j])) * G.b[j]);
       }
     }
     if constexpr (!kStateInV) __syncthreads();   // the tokens' sums are written
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(4 * Q, Q / 64) scan_grad_kernel(ScanGrad A) {
         a += dpp_f<kDppXor1>(a);
         a += dpp_f<kDppXor2>(a);
         if constexpr (kTiles == 8) a += dpp_f<kDppHalfMirror>(a);
-        a += G.end[0] * acc_z;
+        a += decayed(acc_z, G.end[0]);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const int t = kU * lane + u;

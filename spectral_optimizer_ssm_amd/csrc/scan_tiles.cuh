@@ -534,6 +534,14 @@ __device__ __forceinline__ f32x4_t between4(const Gates<Q>& G, int it, int jt, i
   return it != jt ? between4_below(G, it, i0, j) : between4_diagonal(G, i0, j);
 }
 
+// By a decay: nothing is left of what has decayed to 0, whatever it was, so a
+// sequence that starts is not reached by a NaN or an infinity of the last one's
+// state.
+__device__ __forceinline__ float decayed(float v, float by) { return by == 0.0f ? 0.0f : v * by; }
+__device__ __forceinline__ f32x4_t decayed(f32x4_t v, float by) {
+  return f32x4_t{decayed(v[0], by), decayed(v[1], by), decayed(v[2], by), decayed(v[3], by)};
+}
+
 // Sums over the four 16-lane rows of a wave, for four values at once: row g of
 // the result holds the sum of s_g (v_permlane16_swap, v_permlane32_swap: no
 // LDS).
