@@ -50,7 +50,8 @@ bool seq_ok(const muon_seq& s, int batch, int tokens, int heads, size_t es) {
   return s.p != nullptr && aligned_to(s.p, es) && s.sb >= 0 && s.st >= 0 && s.sh >= 0 &&
          extent_ok({batch - 1, tokens - 1, heads - 1}, {s.sb, s.st, s.sh});
 }
-SeqOperand operand(const muon_seq& s) { return {s.p, s.sb, s.st, s.sh}; }
+// (the token stride of a single token is free: a row's, so that its loads are whole pieces)
+SeqOperand operand(const muon_seq& s, int tokens, int width) { return {s.p, s.sb, tokens == 1 ? width : s.st, s.sh}; }
 
 int check_dims(const muon_scan_args* a) {
   if (a == nullptr) return MUON_EINVAL;
@@ -155,11 +156,11 @@ size_t scan_bytes(const muon_scan_args* a, bool backward) {
 
 ScanWalk walk_of(const muon_scan_args* a, const ScanPlan& p) {
   ScanWalk w{};
-  w.x = operand(a->v);
-  w.k = operand(a->k);
-  w.q = operand(a->q);
-  w.g = operand(a->log_decay);
-  if (a->gate.p != nullptr) w.b = operand(a->gate);
+  w.x = operand(a->v, a->tokens, a->P);
+  w.k = operand(a->k, a->tokens, a->N);
+  w.q = operand(a->q, a->tokens, a->N);
+  w.g = operand(a->log_decay, a->tokens, 1);
+  if (a->gate.p != nullptr) w.b = operand(a->gate, a->tokens, 1);
   w.batch = a->batch; w.tokens = a->tokens; w.heads = a->heads; w.groups = a->groups;
   w.P = a->P; w.N = a->N;
   w.pblocks = p.pblocks; w.nchunks = p.nchunks; w.nseg = p.nseg; w.seg_chunks = p.seg_chunks;
@@ -270,7 +271,7 @@ int muon_gated_scan_backward(const muon_scan_args* a, const muon_seq* dY, const 
   // 1. the states before every block and the gradients of the states after it
   ScanWalk w[2] = {walk_of(a, p), walk_of(a, p)};
   w[0].states = at(p.states);
-  w[1].x = operand(*dY);
+  w[1].x = operand(*dY, a->tokens, a->P);
   w[1].k = w[1].q;
   w[1].reverse = 1;
   w[1].init = dS;
@@ -316,11 +317,11 @@ int muon_gated_scan_step(const muon_scan_args* a, void* Y, float* S_out, void* s
   const bool in_place = a->S0 == S_out;
   if (clash({span(Y, value_bytes(a)), so}, {v, k, q, g, gate_span(a), in_place ? Span{nullptr, 0} : s0})) return MUON_EINVAL;
   ScanStep s{};
-  s.v = operand(a->v);
-  s.k = operand(a->k);
-  s.q = operand(a->q);
-  s.g = operand(a->log_decay);
-  if (a->gate.p != nullptr) s.b = operand(a->gate);
+  s.v = operand(a->v, a->tokens, a->P);
+  s.k = operand(a->k, a->tokens, a->N);
+  s.q = operand(a->q, a->tokens, a->N);
+  s.g = operand(a->log_decay, a->tokens, 1);
+  if (a->gate.p != nullptr) s.b = operand(a->gate, a->tokens, 1);
   s.batch = a->batch; s.heads = a->heads; s.groups = a->groups; s.P = a->P; s.N = a->N;
   s.y = Y;
   s.S = a->S0;
