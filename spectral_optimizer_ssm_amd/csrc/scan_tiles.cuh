@@ -7,7 +7,7 @@
 // second operand's row), rows 4 g + 0..3 (the first operand's).  Any
 // permutation of the contraction indices that both operands share gives the
 // same product, so a result kept in registers can be the next product's
-// operand without a trip through LDS (frag_from_acc).  bfloat16 operands
+// operand without a trip through LDS (state_row).  bfloat16 operands
 // take one v_mfma_f32_16x16x32_bf16 per step, float32 ones eight
 // v_mfma_f32_16x16x4f32.
 #pragma once
@@ -200,14 +200,6 @@ struct Triangle {
       if (tid < 256) m[e * kPiece + kTiles * 256 + tid] = O::from_f32(0.0f);
   }
 };
-
-// Fragment of a float32 result held in two accumulator tiles (rows 0..15 and
-// 16..31 of a 32-row block): contraction indices 4 g + 0..3 of each.
-template <typename T>
-__device__ __forceinline__ typename Ops<T>::Frag frag_from_acc(f32x4_t a, f32x4_t b) {
-  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  return Ops<T>::narrow(v);
-}
 
 // A value that the compiler takes for new: what depends on it is computed where
 // it is used, and not once before a long loop, in registers that the loop's
