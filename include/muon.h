@@ -440,6 +440,8 @@ typedef struct {
  *   log_decay  g: [batch][tokens][heads] float32 (sh: stride of the heads).
  *              -inf starts a new sequence at t: nothing before it is read
  *              after it (values below -10000 are taken as that)
+ *              (g > 0 grows the state: no sum of it inside a chunk may pass 88,
+ *              where e^g leaves float32)
  *   gate       b, as log_decay; gate.p NULL: 1
  *   S0         NULL (zero), or [batch][heads][P][N] float32, contiguous
  * Supported: N <= 128, any P, and as many sequences and heads as one launch

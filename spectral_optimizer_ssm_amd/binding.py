@@ -841,7 +841,9 @@ def muon_gated_scan(V, K, Q, log_decay, gate=None, S0=None, Y=None, S_out=None, 
 def muon_gated_scan_backward(V, K, Q, log_decay, dY, gate=None, S0=None, dS=None, dV=None, dK=None, dQ=None,
                              dlog_decay=None, dgate=None, dS0=None, workspace=None, stream=None):
     """Gradients through muon_gated_scan: the forward call's inputs, dY the
-    gradient of Y and dS that of S_out (None: zero).  Returns (dV, dK, dQ,
+    gradient of Y and dS that of S_out (None: zero); dY may have any strides but
+    adjacent elements in its last dimension (an expanded one, such as the gradient
+    of Y.sum(), needs .contiguous()).  Returns (dV, dK, dQ,
     dlog_decay, dgate, dS0), of the shapes and dtypes of what they are the
     gradients of, in the tensors given or in new ones; dgate is None without a
     gate, dS0 without S0."""
@@ -963,7 +965,9 @@ def muon_layer_norm(X, weight=None, bias=None, eps=1e-5, center=True, Y=None, st
 def muon_layer_norm_backward(dY, X, weight, mean, rstd, center=True, bias_grad=True, workspace=None, stream=None):
     """Gradients through muon_layer_norm from its input, weight and the
     statistics that it returned: (dX, dweight, dbias), dweight None without a
-    weight, dbias None unless bias_grad."""
+    weight, dbias None unless bias_grad.  dY's rows are one stride apart and do
+    not overlap (an expanded dY, such as the gradient of Y.sum(), needs
+    .contiguous())."""
     if stream is not None:
         return _on(stream, muon_layer_norm_backward, dY, X, weight, mean, rstd, center=center, bias_grad=bias_grad,
                    workspace=workspace)

@@ -14,8 +14,7 @@
 // the copy of S_in that is read are two bfloat16 pieces (16 bits), so that y is
 // off by its own rounding alone, at any length and from a sequence's first token
 // on; in one piece y would be off by 1.4 times that, and by 2.2 times where a row
-// sums few tokens, and eight sequences of 2,048 tokens would take 92 us instead of
-// 103.  The weighted values that enter the state are three pieces, so the state
+// sums few tokens, and eight sequences of 2,048 tokens would take 92 us for 103.  The weighted values that enter the state are three pieces, so the state
 // keeps float32 accuracy.  Gates are float64 sums, kept as two floats.
 //
 // In reversed time the same walk with (dy, q) for (v, k), weights e^{c_i} and
@@ -202,9 +201,9 @@ struct Walk {
 // chip more evenly than ones of twice the size (125 -> 117 us where both
 // directions of eight sequences of 2,048 tokens, 24 heads, bfloat16, are walked).
 // S is held by rows, so that a lane stores 16 adjacent bytes of a state (117 ->
-// 97 us).  Of those 97 us about 40 are the 201 MB of float32 states that go to
-// HBM; the rest is issue: a wave's step is 180 vector, 24 matrix and 130 scalar
-// instructions, and splitting the values is half of the first.
+// 97 us).  Without the stores of 201 MB of float32 states it took 67; the rest
+// is issue: a wave's step is 190 vector, 24 matrix and 130 scalar instructions,
+// and splitting the values is half of the first.
 template <typename T, int NT, bool VEC>
 __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 ? 5 : 3) scan_states_kernel(WalkPair P) {
   constexpr int kParts = NT / kStateCols, KT = kStateCols / 16;
@@ -257,10 +256,10 @@ __global__ void __launch_bounds__(kStatesThreads + kWave, VEC && sizeof(T) == 2 
 // exchange through LDS, each finishing half of the tokens), and the next S; then
 // what the chunk's own tokens give, and the next chunk's tiles go to LDS.
 //
-// Eight sequences of 2,048 tokens, 24 heads of 64 x 128, bfloat16: 103 us (192
-// workgroups, 32 steps of about 7,300 clocks); HBM needs 112 MB, 22 us.  Bound
-// by issue and LDS together (with one piece of M and S_in a step of 6,500 was 2,200
-// clocks of vector and 1,400 of matrix instructions a SIMD and 2,300 of LDS): two waves a SIMD that meet
+// Eight sequences of 2,048 tokens, 24 heads of 64 x 128, bfloat16: 98 to 104 us
+// (192 workgroups, 32 steps of about 7,500 clocks); HBM needs 112 MB, 22 us.
+// Bound by issue and LDS together: a step is 2,900 clocks of vector and 1,600 of
+// matrix instructions a SIMD and 2,500 of LDS, and two waves a SIMD that meet
 // at barriers overlap little of it.  What made the step short: 16-byte LDS reads
 // without bank conflicts everywhere (107 -> 94 us, with two barriers instead of
 // three and the weighted values split once for all waves), the gates, whose

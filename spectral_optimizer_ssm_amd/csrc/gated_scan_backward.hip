@@ -23,16 +23,16 @@
 // fixed order.
 //
 // Eight sequences of 2,048 tokens, 24 heads of 64 x 128 sharing keys, bfloat16:
-// 152 us, of which the two states' 201 MB alone need 40 at the rate of a large
-// copy.  A head's step is about 23,000 clocks: per SIMD 12,000 of vector
-// instructions (the weights and sums of E's tiles, the states' splits) and 4,500
-// of matrix ones, 6,000 of LDS, with two waves a SIMD to overlap them.  Blocks of
+// 174 us, of which the two states' 201 MB alone need 40 at the rate of a large
+// copy.  Bound by issue: of about 400,000 clocks a SIMD has 180,000 of vector
+// instructions (the weights and sums of E's tiles, the states' splits) and 64,000
+// of matrix ones, with two waves to overlap them and the LDS.  Blocks of
 // 64 tokens would read and write twice the states.
 //
 // Rounding, bfloat16 operands: L A, the sum of L b E and the copy of dS_out
 // that dv reads are two bfloat16 pieces (16 bits), so that dv, dq and dk are off by
-// their own rounding alone (by 1.2 to 1.4 times that in one piece, which would take
-// 137 us for 152); dq and dk take the states as three pieces (float32 accuracy), since
+// their own rounding alone (by 1.2 to 1.4 times that in one piece, which would save
+// 15 us); dq and dk take the states as three pieces (float32 accuracy), since
 // db and dg, which are float32, are dot products of them.  The pieces of L A and
 // of the sums are kept as the tiles on one side of the diagonal, or they would not
 // fit the LDS beside the block's operands.

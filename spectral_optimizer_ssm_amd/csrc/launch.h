@@ -316,8 +316,8 @@ constexpr int kScanItemThreads = 640;
 constexpr int kScanRows = 64;      // state rows (value components) per workgroup
 constexpr int kScanMaxN = 128;     // largest key length
 // Kernels for up to 64 and up to 128 columns of the state: eight sequences of
-// 2,048 tokens with 24 heads and N = 64 take 80 us forward and 160 backward with
-// 64 columns, 84 and 222 padded to 128 (float32: 155 and 358, 252 and 582).
+// 2,048 tokens with 24 heads and N = 64 take 89 us forward and 176 backward with
+// 64 columns, 95 and 239 padded to 128 (float32: 167 and 417, 190 and 634).
 inline int scan_padded_n(int n) { return n <= 64 ? 64 : 128; }
 struct SeqOperand {    // [batch][tokens][heads or groups][width], innermost stride 1
   const void* p;
@@ -345,8 +345,8 @@ hipError_t launch_scan_walk(const ScanWalk* W, int dirs, bool read, bool vec, bo
 // Whether 16-byte buffer loads of rows of `width` elements fit an operand (es
 // bytes an element): rows hold whole pieces, do not overlap, and a tile's lie
 // within 32-bit offsets.  They may start anywhere: the memory takes 16 bytes at
-// any address (eight sequences of 2,048 tokens, 24 heads, at an odd element: 93 us
-// forward and 244 backward, as much as aligned, 315 and 614 element by element).
+// any address (eight sequences of 2,048 tokens, 24 heads, at an odd element: 99 us
+// forward and 263 backward, 98 and 257 aligned, 329 and 638 element by element).
 inline bool scan_vec(const SeqOperand& s, int width, int es) {
   return width % (16 / es) == 0 && s.st >= width && s.st * es * 2 * kScanChunk < (1LL << 31) - 256;
 }

@@ -4,7 +4,7 @@
 //   dx = r (t - mean(t) - xh mean(t xh)),  dw = sum_rows dy xh,  dbias = sum_rows dy.
 // Without centering mu = 0 and mean(t) leaves dx (a root-mean-square norm).
 //
-// Bound by HBM: a row is read once into registers (by a wave, or by a workgroup
+// Bound by memory: a row is read once into registers (by a wave, or by a workgroup
 // of 256 or 512 threads beyond kPieces pieces a lane), the variance is taken
 // from the registers around the mean (two passes, so a large mean costs no
 // digits), and every statistic and sum is float32.  Rows longer than a
@@ -378,9 +378,8 @@ __global__ void __launch_bounds__(kPartWaves * kWave) norm_parts_kernel(const fl
 }
 
 // Threads that share a row of n elements (0: more than a workgroup holds, or less
-// than a piece) and
-// the pieces of it that each takes: as few threads as hold it.  A wave needs no
-// barrier: 8,192 bfloat16 rows of 2,048 take 15 us forward and 25 backward by
+// than a piece) and the pieces of it that each takes: as few threads as hold it.
+// A wave needs no barrier: 8,192 bfloat16 rows of 2,048 take 15 us forward and 25 backward by
 // waves, 29 and 80 by workgroups.  Reading a row again costs more than a larger
 // workgroup: 1,024 rows of 16,384 take 15 and 52 us by 512 threads that hold it,
 // 65 and 323 read in passes.

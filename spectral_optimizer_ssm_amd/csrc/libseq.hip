@@ -82,10 +82,10 @@ long long times(long long a, long long b, long long c) {
 // Where to stop cutting work: one workgroup of the forward walk or of the
 // backward pass for each of 256 compute units (their tiles fill its LDS), and
 // 384 walks of the states, which are lighter.  Measured with 24 heads of 64 x
-// 128 sharing keys, bfloat16: 16,384 tokens forward take 120 us with up to 256
-// walks, 127 with 512 and 154 with 170; 8,191 tokens backward 188 us with up to
-// 384, 190 with 256, 193 with 512 and 204 with 768; eight sequences of 2,048
-// tokens backward 238 us with 256 workgroups, 299 with 128 and 267 with 512.
+// 128 sharing keys, bfloat16: 16,384 tokens forward take 136 us with up to 256
+// walks, 146 with 512 and 171 with 170; 8,191 tokens backward 170 us with up to
+// 384, 180 with 256, 178 with 512 and 187 with 768; eight sequences of 2,048
+// tokens backward 257 us with 256 workgroups, 351 with 128 and 280 with 512.
 constexpr long long kReadFill = 256, kStatesFill = 384, kGradFill = 256;
 
 struct ScanPlan {
@@ -96,12 +96,13 @@ struct ScanPlan {
 // axis is cut into segments: their totals first, then all of them at once.
 // Each token is walked over twice, so segments have to fill otherwise idle
 // compute units.  Forward, the second walk is the longer one, and two segments
-// already win (96 heads of 4,096 tokens: 130 us in two, 155 in one; 24 heads of
-// 16,384: 130 in ten, 594 in one).  For the backward pass both are the same
-// walk: 24 heads of 16,384 tokens take 327 us in eight and 442 in one, but 48
-// of 8,192 take 315 in four and 309 in one, so fewer than five are not cut.  A
-// segment has at least kSegChunks chunks (24 heads of 2,048 tokens forward:
-// 39 us with four, 44 with eight, and no less with two).
+// already win (96 heads of 4,096 tokens: 152 us in two, 180 in one; 24 heads of
+// 16,384: 136 in ten, 692 in one).  For the backward pass both are the same
+// walk: 24 heads of 16,384 tokens take 352 us in eight and 445 in one, but 48
+// of 8,192 take 327 in four and 316 in one, and 96 of 4,096 take 325 in two and
+// 281 in one, so fewer than five are not cut.  A segment has at least kSegChunks
+// chunks (24 heads of 2,048 tokens forward: 39 us with four, 47 with eight, and
+// no less with two).
 constexpr int kSegChunks = 4;
 
 int grad_tokens(const muon_scan_args* a) { return scan_grad_tokens(a->dtype == MUON_BF16, a->tokens); }
