@@ -525,6 +525,115 @@ int muon_layer_norm_backward(const void* dY, long long lddy, const void* X, long
                              long long lddx, float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
                              void* stream);
 
+/* Token numbers: token t is element (t / run) stride + (t % run) step of p
+ * (strides in elements, >= 0, run >= 1), so a slice of a batch of texts needs no copy. */
+typedef struct {
+  const void* p;
+  int bits;              /* 32 or 64: int32 or int64 */
+  long long run, stride, step;
+} muon_ids;
+
+/* Token embedding (the tied embedding that "Muon Meets Mamba" leaves to AdamW;
+ * Mamba-2 130M: 50,280 rows of 768): Y_t = scale table[id_t], rounded once.  An id
+ * outside [0, vocab) (padding) gives a row of zeros.
+ *   table  vocab rows of n elements of table_dtype, ldt elements apart (>= n)
+ *   Y      rows of dtype, ldy apart
+ * table_dtype and dtype: MUON_F32 or MUON_BF16, in any combination.  tokens and
+ * vocab <= 2^30, n <= 2^21, tokens * n and vocab * n <= 2^40 (else
+ * MUON_EUNSUPPORTED); tokens may be 0.  Y must not overlap its inputs. */
+int muon_embedding(const void* table, int table_dtype, long long ldt, int vocab, int n, const muon_ids* ids,
+                   long long tokens, float scale, void* Y, int dtype, long long ldy, void* stream);
+
+/* Gradient of muon_embedding by its table: dtable[v] = scale times the sum of dY_t
+ * over the tokens with id v (rows of dtype, lddy apart), 0 where there is none; ids
+ * outside the table are left out, and the rows of dY at them are not read.
+ *   dtable  [vocab][n] of table_dtype, contiguous; accumulate 1: added to what is
+ *           there (MUON_F32 only), rows of tokens that do not occur untouched
+ * Sums are float32 over the tokens in their order, in an order that depends on the
+ * sizes alone; no atomics touch them, so results repeat bit for bit.  The workspace
+ * (16-byte aligned) holds the sorted tokens and part sums.  Outputs and workspace
+ * must not overlap inputs or each other. */
+size_t muon_embedding_backward_workspace_size(long long tokens, int vocab, int n);
+int muon_embedding_backward(const void* dY, int dtype, long long lddy, const muon_ids* ids, long long tokens,
+                            float scale, int vocab, int n, void* dtable, int table_dtype, int accumulate,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* What muon_group_norm does beside the norm; silu(z) = z / (1 + e^-z). */
+typedef enum {
+  MUON_GATE_BEFORE = 0,  /* Y = norm(X silu(Z)) weight + bias (the norm behind the scan of a Mamba-2 block) */
+  MUON_GATE_AFTER = 1,   /* Y = (norm(X) weight + bias) silu(Z) */
+  MUON_ACT_SILU = 2,     /* Y = silu(norm(X) weight + bias); no Z */
+  MUON_ACT_NONE = 3      /* Y = norm(X) weight + bias; no Z */
+} muon_gate;
+
+/* Group norm, channels last: each of `rows` rows holds `groups` groups of `width`
+ * adjacent channels, and each group of a row is normalised by itself,
+ *   norm(u) = (u - mu) r,  mu = mean(u),  r = 1 / sqrt(mean((u - mu)^2) + eps)
+ * over its channels, or with center 0 the same with mu = 0.
+ *   X, Z, Y       rows of dtype (MUON_F32 or MUON_BF16), ldx, ldz and ldy elements
+ *                 apart (>= groups width); Z NULL for MUON_ACT_*; Y must not overlap
+ *                 X or Z
+ *   weight, bias  NULL (1 and 0), or float32[groups width]
+ *   mean, rstd    NULL, or float32[rows][groups] receiving mu and r
+ * Everything up to the rounding of Y is float32, the variance taken around the mean.
+ * rows * groups < 2^31, groups < 65536 and groups * width <= 2^27 (else
+ * MUON_EUNSUPPORTED). */
+int muon_group_norm(const void* X, long long ldx, const void* Z, long long ldz, int dtype, long long rows, int groups,
+                    int width, const float* weight, const float* bias, float eps, int center, int gate, void* Y,
+                    long long ldy, float* mean, float* rstd, void* stream);
+
+/* Gradients of muon_group_norm, from its inputs and the mu (mean NULL: center was 0)
+ * and r that it gave: dX and dZ (rows lddx and lddz apart; dZ NULL for MUON_ACT_*) of
+ * dtype, dweight and dbias float32[groups width] or NULL (not wanted; written as 0
+ * when rows is 0).  The sums over the rows are float32 in a fixed order; the
+ * workspace (16-byte aligned) holds their parts.  Outputs must not overlap inputs or
+ * each other. */
+size_t muon_group_norm_backward_workspace_size(long long rows, int groups, int width, int dtype);
+int muon_group_norm_backward(const void* dY, long long lddy, const void* X, long long ldx, const void* Z, long long ldz,
+                             int dtype, long long rows, int groups, int width, const float* weight, const float* bias,
+                             const float* mean, const float* rstd, int gate, void* dX, long long lddx, void* dZ,
+                             long long lddz, float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Log probabilities of given tokens, the entropy and the likeliest tokens, from rows
+ * of logits.  For each row x, with m = max(x):
+ *   L = log sum_j e^{scale (x_j - m)},  log p_j = scale (x_j - m) - L,
+ *   H = -sum_j p_j log p_j
+ *   X           rows of vocab logits of dtype, ldx elements apart (>= vocab)
+ *   scale       > 0, finite (one over the temperature)
+ *   tokens      NULL, or a token a row; one outside [0, vocab) (padding) has log p 0
+ *   logprobs    NULL, or float32[rows]: log p of the row's token (tokens needed)
+ *   entropy     NULL, or float32[rows]: H
+ *   stats       NULL, or float32[rows][2]: m and L, for the gradients
+ *   top         0..64: how many of the largest logits to give, ties by the lowest
+ *               index: top_ids int32[rows][top], top_logprobs float32[rows][top],
+ *               both NULL when top is 0
+ * A logit of -inf (a forbidden token) has p 0 and is never among the top, whose
+ * places past the last possible token hold -1 and -inf.  A row of nothing but -inf
+ * has log p -inf for every token, H 0 and m and L -inf.  A NaN or +inf makes its
+ * row's results NaN (top_ids -1).  Statistics are float32.  rows < 2^31, vocab <=
+ * 2^27, rows * vocab <= 2^40 (else MUON_EUNSUPPORTED); rows may be 0.  Outputs and
+ * workspace (16-byte aligned) must not overlap inputs or each other. */
+size_t muon_token_logprobs_workspace_size(long long rows, int vocab, int dtype, int top);
+int muon_token_logprobs(const void* X, long long ldx, int dtype, long long rows, int vocab, float scale,
+                        const muon_ids* tokens, float* logprobs, float* entropy, float* stats, int top, int* top_ids,
+                        float* top_logprobs, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of a loss by the logits, through logprobs and entropy: with dlp and dH its
+ * gradients by them,
+ *   dX_j = scale (dlp ([j = token] - p_j) - dH p_j (log p_j + H)).
+ *   stats       as muon_token_logprobs gave them
+ *   dlogprobs   NULL (0; so may be tokens then), or float32, the rows' sdlp elements
+ *               apart (>= 0; 0: one value for all); rows whose token is outside
+ *               [0, vocab) take none
+ *   dentropy    NULL (0), or as dlogprobs with sdh; entropy: H, needed with it
+ *   dX          rows of dtype, lddx apart; may be X with the same stride (in place)
+ * A row that takes no gradient, or has only -inf logits, gets 0 whatever it holds. */
+int muon_token_logprobs_backward(const void* X, long long ldx, int dtype, long long rows, int vocab, float scale,
+                                 const muon_ids* tokens, const float* stats, const float* dlogprobs, long long sdlp,
+                                 const float* entropy, const float* dentropy, long long sdh, void* dX, long long lddx,
+                                 void* stream);
+
 /* Human-readable name of a muon_status. */
 const char* muon_status_string(int status);
 

@@ -9,5 +9,8 @@ from .binding import (MUON_BF16, MUON_F32, MUON_NS_ACCUMULATE, MUON_NS_AUTO, MUO
                       muon_ns_factored, muon_ssm_momentum, muon_ns_orthogonalize, muon_ns_orthogonalize_noalloc, muon_query_flags,
                       muon_gated_scan, muon_gated_scan_backward, muon_gated_scan_step, muon_gated_scan_workspace_size,
                       muon_layer_norm, muon_layer_norm_backward, muon_spectral_diag,
+                      muon_embedding, muon_embedding_backward, muon_embedding_backward_workspace_size, muon_group_norm,
+                      muon_group_norm_backward, muon_token_logprobs, muon_token_logprobs_backward,
+                      muon_token_logprobs_workspace_size,
                       muon_ns_workspace_size, muon_step, muon_step_phases, muon_step_workspace_size,
                       muon_version, status_string)

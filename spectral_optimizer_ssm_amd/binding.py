@@ -57,6 +57,9 @@ EXPORTS = ("muon_step_workspace_size", "muon_step", "muon_step_phases", "muon_st
            "muon_gated_scan_workspace_size", "muon_gated_scan", "muon_gated_scan_backward_workspace_size",
            "muon_gated_scan_backward", "muon_gated_scan_step", "muon_layer_norm",
            "muon_layer_norm_backward_workspace_size", "muon_layer_norm_backward",
+           "muon_embedding", "muon_embedding_backward_workspace_size", "muon_embedding_backward", "muon_group_norm",
+           "muon_group_norm_backward_workspace_size", "muon_group_norm_backward", "muon_token_logprobs_workspace_size",
+           "muon_token_logprobs", "muon_token_logprobs_backward",
            "muon_status_string", "muon_version")
 
 
@@ -114,7 +117,7 @@ def lib():
     L.muon_spectral_diag_timed.argtypes = [vp, i, i, i, ctypes.c_longlong, i, vp, vp, vp, vp, sz, vp,
                                            ctypes.POINTER(ctypes.c_void_p), i]
     L.muon_spectral_diag_timed.restype = i
-    ll, sa = ctypes.c_longlong, ctypes.c_char_p   # packed muon_scan_args, muon_seq
+    ll, sa = ctypes.c_longlong, ctypes.c_char_p   # packed muon_scan_args, muon_seq, muon_ids
     L.muon_gated_scan_workspace_size.argtypes = [sa]
     L.muon_gated_scan_workspace_size.restype = sz
     L.muon_gated_scan.argtypes = [sa, vp, vp, vp, sz, vp]
@@ -131,6 +134,25 @@ def lib():
     L.muon_layer_norm_backward_workspace_size.restype = sz
     L.muon_layer_norm_backward.argtypes = [vp, ll, vp, ll, i, ll, i, vp, vp, vp, vp, ll, vp, vp, vp, sz, vp]
     L.muon_layer_norm_backward.restype = i
+    L.muon_embedding.argtypes = [vp, i, ll, i, i, sa, ll, f, vp, i, ll, vp]
+    L.muon_embedding.restype = i
+    L.muon_embedding_backward_workspace_size.argtypes = [ll, i, i]
+    L.muon_embedding_backward_workspace_size.restype = sz
+    L.muon_embedding_backward.argtypes = [vp, i, ll, sa, ll, f, i, i, vp, i, i, vp, sz, vp]
+    L.muon_embedding_backward.restype = i
+    L.muon_group_norm.argtypes = [vp, ll, vp, ll, i, ll, i, i, vp, vp, f, i, i, vp, ll, vp, vp, vp]
+    L.muon_group_norm.restype = i
+    L.muon_group_norm_backward_workspace_size.argtypes = [ll, i, i, i]
+    L.muon_group_norm_backward_workspace_size.restype = sz
+    L.muon_group_norm_backward.argtypes = [vp, ll, vp, ll, vp, ll, i, ll, i, i, vp, vp, vp, vp, i, vp, ll, vp, ll, vp, vp, vp,
+                                           sz, vp]
+    L.muon_group_norm_backward.restype = i
+    L.muon_token_logprobs_workspace_size.argtypes = [ll, i, i, i]
+    L.muon_token_logprobs_workspace_size.restype = sz
+    L.muon_token_logprobs.argtypes = [vp, ll, i, ll, i, f, sa, vp, vp, vp, i, vp, vp, vp, sz, vp]
+    L.muon_token_logprobs.restype = i
+    L.muon_token_logprobs_backward.argtypes = [vp, ll, i, ll, i, f, sa, vp, vp, ll, vp, vp, ll, vp, ll, vp]
+    L.muon_token_logprobs_backward.restype = i
     L.muon_status_string.argtypes = [i]
     L.muon_status_string.restype = ctypes.c_char_p
     L.muon_version.argtypes = []
@@ -1002,3 +1024,339 @@ def muon_layer_norm_backward(dY, X, weight, mean, rstd, center=True, bias_grad=T
                                     _raw_stream(dev))
     _check(rc, "muon_layer_norm_backward")
     return dX, dweight, dbias
+
+
+# ----------------------------------------------------------------------------
+# what a language model has around its blocks: the embedding of its tokens, the
+# gated norm and the log probabilities of its answers
+# ----------------------------------------------------------------------------
+_IDS = struct.Struct("@Pi4xqqq")                            # muon_ids
+MUON_GATE_BEFORE, MUON_GATE_AFTER, MUON_ACT_SILU, MUON_ACT_NONE = 0, 1, 2, 3
+
+
+def _ids(t, name, index):
+    """Packed muon_ids of a tensor of token numbers whose dimensions fold into runs of one stride."""
+    if t.dtype is torch.int64:
+        bits = 64
+    elif t.dtype is torch.int32:
+        bits = 32
+    else:
+        raise TypeError(f"{name} must be int64 or int32 (got {t.dtype})")
+    _where(t, name, index)
+    count = t.numel()
+    if t.is_contiguous() or count == 0:
+        return _IDS.pack(t.data_ptr(), bits, max(count, 1), 0, 1)
+    dims = [(n, s) for n, s in zip(t.shape, t.stride()) if n > 1]
+    run, step = dims.pop()
+    while dims and dims[-1][1] == run * step:
+        run *= dims.pop()[0]
+    stride, expect = 0, None
+    while dims:
+        n, s = dims.pop()
+        if expect is None:
+            stride = s
+        elif s != expect:
+            raise ValueError(f"{name} must lie in runs of one stride, one stride apart")
+        expect = n * s
+    return _IDS.pack(t.data_ptr(), bits, run, stride, step)
+
+
+def _per_row(t, name, lead, index):
+    """(pointer, stride) of a float32 value per row: any one stride, 0 where all are one value."""
+    if t.shape != lead:
+        raise ValueError(f"{name} must be a [{', '.join(map(str, lead))}] float32 tensor")
+    _f32_on(t, name, index)
+    if t.numel() == 0 or t.is_contiguous():
+        return _ptr(t), 1
+    stride = expect = None
+    for n, s in zip(reversed(t.shape), reversed(t.stride())):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = s
+        elif s != expect:
+            raise ValueError(f"the values of {name} must be one stride apart")
+        expect = n * s
+    return t.data_ptr(), stride
+
+
+def muon_embedding(table, ids, scale=1.0, dtype=None, Y=None, stream=None):
+    """Y[t] = scale * table[ids[t]]: table [vocab, n] bf16 or float32 (rows one stride
+    apart), ids int64 or int32 of any shape, Y of ids' shape and n, of `dtype` (default:
+    the table's).  An id outside the table (padding) gives zeros.  Returns Y."""
+    return (_on(stream, _embedding, table, ids, scale, dtype, Y) if stream is not None else
+            _embedding(table, ids, scale, dtype, Y))[0]
+
+
+def _embedding(table, ids, scale, dtype, Y):
+    dev = _device_index()
+    if table.dim() != 2:
+        raise ValueError("table must be [vocab, n]")
+    vocab, n = table.shape
+    code = _type_code(table, "table")
+    _where(table, "table", dev)
+    packed = _ids(ids, "ids", dev)
+    ldt = _rows(table, "table")[2]
+    shape = ids.shape + (n,)
+    if Y is None:
+        Y = torch.empty(shape, dtype=table.dtype if dtype is None else dtype, device=dev)
+        ldy = n
+    else:
+        if Y.shape != shape:
+            raise ValueError(f"Y must be a [{', '.join(map(str, shape))}] tensor")
+        if dtype is not None and Y.dtype is not dtype:
+            raise TypeError(f"Y must be {dtype} (got {Y.dtype})")
+        _where(Y, "Y", dev)
+        ldy = _rows(Y, "Y")[2]
+    rc = lib().muon_embedding(_ptr(table), code, ldt, vocab, n, packed, ids.numel(), scale, _ptr(Y), _type_code(Y, "Y"), ldy,
+                              _raw_stream(dev))
+    _check(rc, "muon_embedding")
+    return (Y,)
+
+
+def muon_embedding_backward(dY, ids, vocab, scale=1.0, dtype=None, dtable=None, accumulate=False, workspace=None, stream=None):
+    """Gradient of muon_embedding by its table: dtable[v] = scale * the sum of dY[t] over
+    the tokens with id v, [vocab, n] of `dtype` (default float32).  dY: of ids' shape and
+    n, rows one stride apart.  dtable: a contiguous tensor to use; with accumulate (then
+    needed, float32) the sums are added to what it holds.  workspace: a uint8 tensor of
+    at least muon_embedding_backward_workspace_size bytes to use instead of a new one.
+    Returns dtable."""
+    if stream is not None:
+        return _on(stream, _embedding_backward, dY, ids, vocab, scale, dtype, dtable, accumulate, workspace=workspace)[0]
+    return _embedding_backward(dY, ids, vocab, scale, dtype, dtable, accumulate, workspace=workspace)[0]
+
+
+def _embedding_backward(dY, ids, vocab, scale, dtype, dtable, accumulate, workspace=None):
+    L = lib()
+    dev = _device_index()
+    code = _type_code(dY, "dY")
+    if dY.dim() == 0 or dY.shape[:-1] != ids.shape:
+        raise ValueError("dY must have ids' shape and the width of a row")
+    _where(dY, "dY", dev)
+    packed = _ids(ids, "ids", dev)
+    n, tokens = dY.shape[-1], ids.numel()
+    lddy = _rows(dY, "dY")[2]
+    if accumulate and dtable is None:
+        raise ValueError("accumulate needs the dtable to add to")
+    if dtype is None:
+        dtype = torch.float32 if dtable is None else dtable.dtype
+    need = L.muon_embedding_backward_workspace_size(tokens, vocab, n)
+    if need == 0:
+        rc = L.muon_embedding_backward(None, code, n, None, tokens, scale, vocab, n, None, MUON_F32, 0, None, 0, None)
+        _check(rc if rc != MUON_OK else MUON_EINVAL, "muon_embedding_backward")
+    dtable = _out(dtable, "dtable", (vocab, n), dtype, dev)
+    ws = _new_workspace(workspace, need, dev)
+    rc = L.muon_embedding_backward(_ptr(dY), code, lddy, packed, tokens, scale, vocab, n, _ptr(dtable), _type_code(dtable, "dtable"),
+                                   1 if accumulate else 0, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    _check(rc, "muon_embedding_backward")
+    return (dtable,)
+
+
+def muon_embedding_backward_workspace_size(ids, vocab, n) -> int:
+    """Workspace bytes of muon_embedding_backward for these ids."""
+    return int(lib().muon_embedding_backward_workspace_size(ids.numel(), vocab, n))
+
+
+def _gate_code(gate, gate_first, activation):
+    if gate is not None:
+        if activation != "silu":
+            raise ValueError("a gate goes through silu")
+        return MUON_GATE_BEFORE if gate_first else MUON_GATE_AFTER
+    if activation not in ("silu", "none"):
+        raise ValueError(f"activation must be 'silu' or 'none' (got {activation!r})")
+    return MUON_ACT_SILU if activation == "silu" else MUON_ACT_NONE
+
+
+def _grouped(X, groups, gate, index):
+    """(type code, rows, width, row stride, gate pointer, gate stride) of a group norm's operands."""
+    code = _type_code(X, "X")
+    _where(X, "X", index)
+    rows, n, ldx = _rows(X, "X")
+    if groups <= 0 or n % groups != 0:
+        raise ValueError(f"the groups ({groups}) must divide the channels ({n})")
+    if gate is None:
+        return code, rows, n // groups, ldx, None, 0
+    if gate.shape != X.shape:
+        raise ValueError("gate must have X's shape")
+    _same_type(gate, X, "gate")
+    _where(gate, "gate", index)
+    return code, rows, n // groups, ldx, _ptr(gate), _rows(gate, "gate")[2]
+
+
+def muon_group_norm(X, groups, weight=None, bias=None, gate=None, gate_first=True, activation="silu", eps=1e-5, center=False,
+                    Y=None, stream=None):
+    """Group norm over the channels in X's last dimension (bf16 or float32, rows one
+    stride apart), cut into `groups` groups of adjacent channels, each normalised by
+    itself: norm(u) = u / sqrt(mean(u^2) + eps), with center (u - mean) / sqrt(var + eps).
+    gate Z (X's shape): Y = norm(X silu(Z)) * weight + bias, with gate_first=False
+    (norm(X) * weight + bias) silu(Z); without it Y = silu(norm(X) * weight + bias), or
+    with activation="none" the norm alone.  weight and bias are float32.  Returns (Y, mean,
+    rstd): Y of X's dtype, the float32 statistics [..., groups] for the backward pass
+    (mean None without centering)."""
+    if stream is not None:
+        return _on(stream, muon_group_norm, X, groups, weight=weight, bias=bias, gate=gate, gate_first=gate_first,
+                   activation=activation, eps=eps, center=center, Y=Y)
+    dev = _device_index()
+    mode = _gate_code(gate, gate_first, activation)
+    code, rows, width, ldx, z, ldz = _grouped(X, groups, gate, dev)
+    n = groups * width
+    w, b = _param(weight, "weight", n, dev), _param(bias, "bias", n, dev)
+    if Y is None:
+        Y = torch.empty_like(X, memory_format=torch.contiguous_format)
+        ldy = n
+    else:
+        if Y.shape != X.shape:
+            raise ValueError("Y must have X's shape")
+        _same_type(Y, X, "Y")
+        _where(Y, "Y", dev)
+        ldy = _rows(Y, "Y")[2]
+    rstd = torch.empty(X.shape[:-1] + (groups,), dtype=torch.float32, device=dev)
+    mean = torch.empty_like(rstd) if center else None
+    rc = lib().muon_group_norm(_ptr(X), ldx, z, ldz, code, rows, groups, width, w, b, eps, 1 if center else 0, mode, _ptr(Y), ldy,
+                               _ptr(mean), _ptr(rstd), _raw_stream(dev))
+    _check(rc, "muon_group_norm")
+    return Y, mean, rstd
+
+
+def muon_group_norm_backward(dY, X, groups, weight, bias, mean, rstd, gate=None, gate_first=True, activation="silu", center=False,
+                             workspace=None, stream=None):
+    """Gradients through muon_group_norm from its inputs and the statistics that it
+    returned: (dX, dgate, dweight, dbias), None for what the call did not have.  dY's
+    rows are one stride apart and do not overlap (an expanded dY, such as the gradient of
+    Y.sum(), needs .contiguous())."""
+    if stream is not None:
+        return _on(stream, muon_group_norm_backward, dY, X, groups, weight, bias, mean, rstd, gate=gate, gate_first=gate_first,
+                   activation=activation, center=center, workspace=workspace)
+    L = lib()
+    dev = _device_index()
+    mode = _gate_code(gate, gate_first, activation)
+    code, rows, width, ldx, z, ldz = _grouped(X, groups, gate, dev)
+    n = groups * width
+    _same_type(dY, X, "dY")
+    _where(dY, "dY", dev)
+    if dY.shape != X.shape:
+        raise ValueError("dY must have X's shape")
+    lddy = _rows(dY, "dY")[2]
+    w, b = _param(weight, "weight", n, dev), _param(bias, "bias", n, dev)
+    if center and mean is None:
+        raise ValueError("mean is needed with centering")
+    for name, t in (("mean", mean if center else None), ("rstd", rstd)):
+        if t is None:
+            continue
+        if t.numel() != rows * groups or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor with one entry per row and group")
+        _f32_on(t, name, dev)
+    need = L.muon_group_norm_backward_workspace_size(rows, groups, width, code)
+    if need == 0:
+        raise MuonError(MUON_EUNSUPPORTED, "muon_group_norm_backward_workspace_size")
+    dX = torch.empty_like(X, memory_format=torch.contiguous_format)
+    dgate = None if gate is None else torch.empty_like(X, memory_format=torch.contiguous_format)
+    dweight = torch.empty(n, dtype=torch.float32, device=dev) if weight is not None else None
+    dbias = torch.empty(n, dtype=torch.float32, device=dev) if bias is not None else None
+    ws = _new_workspace(workspace, need, dev)
+    rc = L.muon_group_norm_backward(_ptr(dY), lddy, _ptr(X), ldx, z, ldz, code, rows, groups, width, w, b,
+                                    _ptr(mean) if center else None, _ptr(rstd), mode, _ptr(dX), n, _ptr(dgate), n, _ptr(dweight),
+                                    _ptr(dbias), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    _check(rc, "muon_group_norm_backward")
+    return dX, dgate, dweight, dbias
+
+
+def muon_token_logprobs(logits, tokens=None, scale=1.0, entropy=True, top=0, workspace=None, stream=None):
+    """Log probabilities of given tokens under the softmax of scale * logits: logits [...,
+    vocab] bf16 or float32 (rows one stride apart), tokens [...] int64 or int32 (None: no
+    token is asked for); one outside the vocabulary (padding) has 0.  Returns (logprobs,
+    entropy, stats, top_ids, top_logprobs): float32 [...], None without tokens; the
+    entropy, float32 [...], None unless asked for; [..., 2] for the backward pass; the
+    `top` (up to 64) likeliest tokens, int32 [..., top], ties by the lowest index, and
+    their log probabilities, None when top is 0.  Forbidden tokens have logits of -inf
+    and are never among the top, which is filled up with -1 and -inf."""
+    if stream is not None:
+        return _on(stream, muon_token_logprobs, logits, tokens, scale=scale, entropy=entropy, top=top, workspace=workspace)
+    L = lib()
+    dev = _device_index()
+    code = _type_code(logits, "logits")
+    if logits.dim() == 0:
+        raise ValueError("logits must be [..., vocab]")
+    _where(logits, "logits", dev)
+    lead = logits.shape[:-1]
+    packed = None
+    if tokens is not None:
+        if tokens.shape != lead:
+            raise ValueError(f"tokens must be a [{', '.join(map(str, lead))}] tensor")
+        packed = _ids(tokens, "tokens", dev)
+    rows, vocab, ldx = _rows(logits, "logits")
+    need = L.muon_token_logprobs_workspace_size(rows, vocab, code, top)
+    if need == 0:
+        rc = L.muon_token_logprobs(None, vocab, code, rows, vocab, 1.0, None, None, None, None, top, None, None, None, 0, None)
+        _check(rc if rc != MUON_OK else MUON_EINVAL, "muon_token_logprobs")
+    new = lambda *tail, dtype=torch.float32: torch.empty(lead + tail, dtype=dtype, device=dev)  # noqa: E731
+    logprobs = None if tokens is None else new()
+    ent = new() if entropy else None
+    stats = new(2)
+    top_ids, top_logprobs = (new(top, dtype=torch.int32), new(top)) if top else (None, None)
+    ws = _new_workspace(workspace, need, dev)
+    rc = L.muon_token_logprobs(_ptr(logits), ldx, code, rows, vocab, scale, packed, _ptr(logprobs), _ptr(ent), _ptr(stats), top,
+                               _ptr(top_ids), _ptr(top_logprobs), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    _check(rc, "muon_token_logprobs")
+    return logprobs, ent, stats, top_ids, top_logprobs
+
+
+def muon_token_logprobs_workspace_size(logits, top=0) -> int:
+    """Workspace bytes of muon_token_logprobs for logits of this shape and dtype."""
+    if torch is None:
+        _load_torch()
+    vocab = logits.shape[-1]
+    return int(lib().muon_token_logprobs_workspace_size(logits.numel() // max(vocab, 1), vocab, _type_code(logits, "logits"), top))
+
+
+def muon_token_logprobs_backward(logits, tokens, stats, dlogprobs, scale=1.0, entropy=None, dentropy=None, dlogits=None,
+                                 stream=None):
+    """Gradient by the logits through muon_token_logprobs, from its inputs and the stats
+    that it returned: dlogprobs [...] float32 (None: 0), and with dentropy (the gradient
+    by the entropy) the entropy that it returned.  Both may be expanded from one value.
+    dlogits: a tensor to use, which may be the logits themselves (in place).  Returns
+    dlogits."""
+    if stream is not None:
+        return _on(stream, _token_logprobs_backward, logits, tokens, stats, dlogprobs, scale, entropy, dentropy, dlogits)[0]
+    return _token_logprobs_backward(logits, tokens, stats, dlogprobs, scale, entropy, dentropy, dlogits)[0]
+
+
+def _token_logprobs_backward(logits, tokens, stats, dlogprobs, scale, entropy, dentropy, dlogits):
+    dev = _device_index()
+    code = _type_code(logits, "logits")
+    if logits.dim() == 0:
+        raise ValueError("logits must be [..., vocab]")
+    _where(logits, "logits", dev)
+    lead = logits.shape[:-1]
+    packed = None
+    if tokens is not None:
+        if tokens.shape != lead:
+            raise ValueError(f"tokens must be a [{', '.join(map(str, lead))}] tensor")
+        packed = _ids(tokens, "tokens", dev)
+    elif dlogprobs is not None:
+        raise ValueError("dlogprobs needs the tokens")
+    if stats.shape != lead + (2,) or not stats.is_contiguous():
+        raise ValueError("stats must be what muon_token_logprobs returned for these logits")
+    _f32_on(stats, "stats", dev)
+    dl, sdl = (None, 0) if dlogprobs is None else _per_row(dlogprobs, "dlogprobs", lead, dev)
+    dh, sdh, h = None, 0, None
+    if dentropy is not None:
+        if entropy is None or entropy.shape != lead or not entropy.is_contiguous():
+            raise ValueError("dentropy needs the entropy that muon_token_logprobs returned")
+        _f32_on(entropy, "entropy", dev)
+        h = _ptr(entropy)
+        dh, sdh = _per_row(dentropy, "dentropy", lead, dev)
+    rows, vocab, ldx = _rows(logits, "logits")
+    if dlogits is None:
+        dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
+        lddx = vocab
+    else:
+        if dlogits.shape != logits.shape:
+            raise ValueError("dlogits must have the logits' shape")
+        _same_type(dlogits, logits, "dlogits")
+        _where(dlogits, "dlogits", dev)
+        lddx = _rows(dlogits, "dlogits")[2]
+    rc = lib().muon_token_logprobs_backward(_ptr(logits), ldx, code, rows, vocab, scale, packed, _ptr(stats), dl, sdl, h, dh, sdh,
+                                            _ptr(dlogits), lddx, _raw_stream(dev))
+    _check(rc, "muon_token_logprobs_backward")
+    return (dlogits,)

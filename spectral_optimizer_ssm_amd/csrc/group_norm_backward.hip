@@ -1,0 +1,280 @@
+// Gradients of the group norm (group_norm.hip).  With a = silu(z), xh = (u - mu) r,
+// o = xh w + b and, behind the norm, do = dy (gate before), dy a (after) or
+// dy act'(o) (none):
+//   t = do w,  du = r (t - mean(t) - xh mean(t xh)),  dw = sum_rows do xh,  db = sum_rows do
+//   before: dx = du a, dz = du x a'(z);  after: dx = du, dz = dy o a'(z);  none: dx = du.
+// Without centering mean(t) leaves du.
+//
+// A workgroup walks rows of one group of channels, keeps the sums of dw and db for
+// its columns in registers and leaves them in the workspace, where a second kernel
+// adds them in fixed order.
+#include "group_norm.cuh"
+
+namespace muon {
+namespace {
+
+// FULL: centered, or the bias's gradient is wanted.  Workgroup (b, g) walks group g
+// of rows b kUnits + 0.., a grid apart, and leaves part[b][2][groups w].
+template <typename T, NormGate G, bool FULL, int TPR, int PIECES>
+__global__ void __launch_bounds__(group_threads<TPR>()) group_norm_grad_kernel(GroupNormGradLaunch A) {
+  constexpr int V = Vec<T>::n, kAll = group_threads<TPR>(), kUnits = kAll / TPR;
+  __shared__ float red[kAll / kWave];
+  __shared__ float cols[kUnits > 1 ? kUnits * TPR * V : 1];
+  const int sub = kUnits == 1 ? 0 : threadIdx.x / TPR, t = threadIdx.x % TPR;
+  const int g = blockIdx.y, c0 = g * A.w;
+  const float inv_w = 1.0f / static_cast<float>(A.w);
+  float wv[PIECES][V], dw[PIECES][V], db[FULL ? PIECES : 1][V];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    if (A.weight != nullptr) load_param<T, TPR>(A.weight + c0, i, t, A.w, wv[i]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (A.weight == nullptr) wv[i][e] = 1.0f;
+      dw[i][e] = 0.0f;
+      if constexpr (FULL) db[i][e] = 0.0f;
+    }
+  }
+  const bool center = FULL && A.mean != nullptr;
+  u32x4_t xn[PIECES], gn[PIECES], zn[G == kGateNone ? 1 : PIECES];   // the next row's, as they are loaded
+  float mun = 0.0f, rn = 0.0f;
+  const auto load_row = [&](long long row) {
+    const T* x = static_cast<const T*>(A.x) + row * A.ldx + c0;
+    const T* dy = static_cast<const T*>(A.dy) + row * A.lddy + c0;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      xn[i] = load_raw<T, TPR>(x, i, t, A.w);
+      gn[i] = load_raw<T, TPR>(dy, i, t, A.w);
+      if constexpr (G != kGateNone) zn[i] = load_raw<T, TPR>(static_cast<const T*>(A.z) + row * A.ldz + c0, i, t, A.w);
+    }
+    mun = center ? A.mean[row * A.groups + g] : 0.0f;
+    rn = A.rstd[row * A.groups + g];
+  };
+  const long long step = static_cast<long long>(gridDim.x) * kUnits;
+  long long row = static_cast<long long>(blockIdx.x) * kUnits + sub;
+  if (row < A.rows) load_row(row);
+  for (; row < A.rows; row += step) {
+    // h: xh;  d: do, then t;  k: what dx and dz take du times (before), the gate's slope times dy (after)
+    float h[PIECES][V], d[PIECES][V];
+    u32x4_t xr[G == kGateBefore ? PIECES : 1], zr[G == kGateNone ? 1 : PIECES];
+    const float mu = mun, r = rn;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      asm volatile("" : "+v"(xn[i]), "+v"(gn[i]));   // unpacked here, not where they were loaded, in twice the registers
+      unpack<T>(xn[i], h[i]);
+      unpack<T>(gn[i], d[i]);
+      if constexpr (G == kGateBefore) xr[i] = xn[i];
+      if constexpr (G != kGateNone) {
+        asm volatile("" : "+v"(zn[i]));
+        zr[i] = zn[i];
+      }
+    }
+    load_row(row + step < A.rows ? row + step : row);
+    T* dz = G == kGateNone ? nullptr : static_cast<T*>(A.dz) + row * A.lddz + c0;
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const Piece<T, TPR> p(i, t, A.w);
+      float z[V], b[V];
+      if constexpr (G != kGateNone) unpack<T>(zr[i], z);
+      if (G != kGateBefore) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) b[e] = 0.0f;
+        if (A.bias != nullptr) load_param<T, TPR>(A.bias + c0, i, t, A.w, b);
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if constexpr (G == kGateBefore) h[i][e] *= z[e] * sigmoid<T>(z[e]);
+        h[i][e] = (h[i][e] - mu) * r;
+        if constexpr (G == kGateAfter) {
+          const float s = sigmoid<T>(z[e]), dy = d[i][e];
+          d[i][e] = dy * (z[e] * s);
+          z[e] = dy * fmaf(h[i][e], wv[i][e], b[e]) * silu_slope(z[e], s);
+        }
+        if (G == kGateNone && A.act == kActSilu) {
+          const float o = fmaf(h[i][e], wv[i][e], b[e]);
+          d[i][e] *= silu_slope(o, sigmoid<T>(o));
+        }
+        dw[i][e] = fmaf(d[i][e], h[i][e], dw[i][e]);
+        if constexpr (FULL) db[i][e] += d[i][e];
+        d[i][e] *= wv[i][e];
+        const float c = p.counts(e) ? d[i][e] : 0.0f;
+        if constexpr (FULL) s1 += c;
+        s2 = fmaf(c, h[i][e], s2);
+      }
+      if constexpr (G == kGateAfter) store_piece<T, TPR>(dz, i, t, A.w, z);
+    }
+    asm volatile("" : "+v"(s1), "+v"(s2));   // both summed up before the branch: their terms take no registers across it
+    s1 = center ? group_total<TPR>(s1, red) * inv_w : 0.0f;
+    s2 = group_total<TPR>(s2, red) * inv_w;
+    T* dx = static_cast<T*>(A.dx) + row * A.lddx + c0;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) d[i][e] = r * (d[i][e] - s1 - h[i][e] * s2);
+      if constexpr (G == kGateBefore) {
+        float x[V], z[V];
+        unpack<T>(xr[i], x);
+        unpack<T>(zr[i], z);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float s = sigmoid<T>(z[e]);
+          x[e] *= d[i][e] * silu_slope(z[e], s);
+          d[i][e] *= z[e] * s;
+        }
+        store_piece<T, TPR>(dz, i, t, A.w, x);
+      }
+      store_piece<T, TPR>(dx, i, t, A.w, d[i]);
+    }
+  }
+  const long long n = static_cast<long long>(A.groups) * A.w;
+  const auto leave = [&](auto& acc, int k, float* out) {
+    if (out == nullptr) return;   // a sum that nobody asked for
+    float* to = (gridDim.x == 1 ? out : A.part + (2LL * blockIdx.x + k) * n) + c0;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const Piece<T, TPR> p(i, t, A.w);
+      if constexpr (kUnits == 1) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (p.counts(e)) to[p.base + e] = acc[i][e];
+      } else {
+        // the units' sums, in order
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < V; ++e) cols[(e * kUnits + sub) * TPR + t] = acc[i][e];
+        __syncthreads();
+        for (int j = threadIdx.x; j < TPR * V; j += kAll) {
+          const int e = j / TPR;
+          const Piece<T, TPR> q(i, j % TPR, A.w);
+          float s = 0.0f;
+#pragma unroll 8
+          for (int u = 0; u < kUnits; ++u) s += cols[(e * kUnits + u) * TPR + j % TPR];
+          if (q.counts(e)) to[q.base + e] = s;
+        }
+      }
+    }
+  };
+  leave(dw, 0, A.dw);
+  if constexpr (FULL) leave(db, 1, A.db);
+}
+
+// Groups of any width, a workgroup a row at a time; column sums in the workspace
+// (each element always by the same thread).
+template <typename T, NormGate G>
+__global__ void __launch_bounds__(kGroupThreads) group_norm_grad_any_kernel(GroupNormGradLaunch A) {
+  __shared__ float red[kGroupThreads / kWave];
+  const int g = blockIdx.y, c0 = g * A.w;
+  const long long n = static_cast<long long>(A.groups) * A.w;
+  const float inv_w = 1.0f / static_cast<float>(A.w);
+  float* pw = A.part + 2LL * blockIdx.x * n + c0;
+  float* pb = pw + n;
+  for (int c = threadIdx.x; c < A.w; c += kGroupThreads) pw[c] = pb[c] = 0.0f;
+  for (long long row = blockIdx.x; row < A.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(A.x) + row * A.ldx + c0;
+    const T* dy = static_cast<const T*>(A.dy) + row * A.lddy + c0;
+    const T* z = G == kGateNone ? nullptr : static_cast<const T*>(A.z) + row * A.ldz + c0;
+    T* dx = static_cast<T*>(A.dx) + row * A.lddx + c0;
+    T* dz = G == kGateNone ? nullptr : static_cast<T*>(A.dz) + row * A.lddz + c0;
+    const float mu = A.mean != nullptr ? A.mean[row * A.groups + g] : 0.0f, r = A.rstd[row * A.groups + g];
+    struct At {
+      float h, d, o, z, s;   // xh, do, o, the gate and its sigmoid
+    };
+    const auto at = [&](int c) {
+      At v;
+      float u = element(x[c]);
+      v.d = element(dy[c]);
+      v.z = v.s = 0.0f;
+      if constexpr (G != kGateNone) {
+        v.z = element(z[c]);
+        v.s = sigmoid<T>(v.z);
+      }
+      if constexpr (G == kGateBefore) u *= v.z * v.s;
+      v.h = (u - mu) * r;
+      v.o = v.h * (A.weight != nullptr ? A.weight[c0 + c] : 1.0f) + (A.bias != nullptr ? A.bias[c0 + c] : 0.0f);
+      if constexpr (G == kGateAfter) v.d *= v.z * v.s;
+      if (G == kGateNone && A.act == kActSilu) v.d *= silu_slope(v.o, sigmoid<T>(v.o));
+      return v;
+    };
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int c = threadIdx.x; c < A.w; c += kGroupThreads) {
+      const At v = at(c);
+      const float t = A.weight != nullptr ? v.d * A.weight[c0 + c] : v.d;
+      s1 += t;
+      s2 = fmaf(t, v.h, s2);
+      pw[c] = fmaf(v.d, v.h, pw[c]);
+      pb[c] += v.d;
+    }
+    s1 = A.mean != nullptr ? block_sum(s1, red) * inv_w : 0.0f;
+    s2 = block_sum(s2, red) * inv_w;
+    for (int c = threadIdx.x; c < A.w; c += kGroupThreads) {
+      const At v = at(c);
+      const float t = A.weight != nullptr ? v.d * A.weight[c0 + c] : v.d;
+      float o = r * (t - s1 - v.h * s2), k = 0.0f;
+      if constexpr (G == kGateBefore) {
+        k = o * element(x[c]) * silu_slope(v.z, v.s);
+        o *= v.z * v.s;
+      }
+      if constexpr (G == kGateAfter) k = element(dy[c]) * v.o * silu_slope(v.z, v.s);
+      if constexpr (sizeof(T) == 2) {
+        dx[c] = f32_to_bf16(o);
+        if constexpr (G != kGateNone) dz[c] = f32_to_bf16(k);
+      } else {
+        dx[c] = o;
+        if constexpr (G != kGateNone) dz[c] = k;
+      }
+    }
+  }
+}
+
+template <typename T, NormGate G, int TPR, int PIECES>
+hipError_t run(const GroupNormGradLaunch& A, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(A.parts), static_cast<unsigned>(A.groups)), block(group_threads<TPR>());
+  if (A.mean == nullptr && A.db == nullptr)
+    hipLaunchKernelGGL((group_norm_grad_kernel<T, G, false, TPR, PIECES>), grid, block, 0, st, A);
+  else
+    hipLaunchKernelGGL((group_norm_grad_kernel<T, G, true, TPR, PIECES>), grid, block, 0, st, A);
+  return hipGetLastError();
+}
+
+template <typename T, NormGate G>
+hipError_t run_any(const GroupNormGradLaunch& A, hipStream_t st) {
+  const GroupPlan p = group_plan(A.w, Vec<T>::n);
+  hipError_t e;
+  switch (p.threads) {
+    case 8: e = run<T, G, 8, 1>(A, st); break;
+    case 16: e = p.pieces == 1 ? run<T, G, 16, 1>(A, st) : run<T, G, 16, 2>(A, st); break;
+    case 64:
+      e = p.pieces == 1 ? run<T, G, 64, 1>(A, st) : p.pieces == 2 ? run<T, G, 64, 2>(A, st) : p.pieces == 3 ? run<T, G, 64, 3>(A, st) : run<T, G, 64, 4>(A, st);
+      break;
+    case 256: e = p.pieces == 2 ? run<T, G, 256, 2>(A, st) : run<T, G, 256, 4>(A, st); break;
+    case 512: e = run<T, G, 512, 4>(A, st); break;
+    default:
+      hipLaunchKernelGGL((group_norm_grad_any_kernel<T, G>), dim3(static_cast<unsigned>(A.parts), static_cast<unsigned>(A.groups)), dim3(kGroupThreads), 0, st, A);
+      e = hipGetLastError();
+  }
+  if (e != hipSuccess || (A.parts == 1 && p.threads != 0) || (A.dw == nullptr && A.db == nullptr)) return e;
+  return launch_norm_parts(A.part, A.parts, A.groups * A.w, A.dw, A.db, st);
+}
+
+template <typename T>
+hipError_t run_gate(const GroupNormGradLaunch& A, NormGate gate, hipStream_t st) {
+  return gate == kGateBefore ? run_any<T, kGateBefore>(A, st) : gate == kGateAfter ? run_any<T, kGateAfter>(A, st) : run_any<T, kGateNone>(A, st);
+}
+
+}  // namespace
+
+// Workgroups for each group of channels: enough to fill the chip, eight rows a
+// thread where there are that many.
+int group_norm_grad_parts(int rows, int groups, int w, bool bf16) {
+  const GroupPlan p = group_plan(w, bf16 ? Vec<bf16_t>::n : Vec<float>::n);
+  const long long units = p.threads == 0 || p.threads >= kGroupThreads ? 1 : kGroupThreads / p.threads;
+  const long long most = p.threads == 512 ? 256 : 512;
+  const long long per = units * (units > 1 ? 8 : 4), want = (rows + per - 1) / per, fill = (most + groups - 1) / groups;
+  return static_cast<int>(want < 1 ? 1 : want > fill ? fill : want);
+}
+
+hipError_t launch_group_norm_grad(const GroupNormGradLaunch& A, NormGate gate, bool bf16, hipStream_t st) {
+  return bf16 ? run_gate<bf16_t>(A, gate, st) : run_gate<float>(A, gate, st);
+}
+
+}  // namespace muon

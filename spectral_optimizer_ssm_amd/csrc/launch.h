@@ -404,4 +404,102 @@ struct NormGradLaunch {
 int norm_grad_parts(long long rows, int n, bool bf16);
 hipError_t launch_norm_grad(const NormGradLaunch& A, bool bf16, hipStream_t st);
 
+// Token numbers (embedding.hip, token_logprobs.hip): token t is element
+// (t / run) stride + (t % run) step of p; t / run = umulhi(t, magic) >> shift for
+// t < 2^31 (magic 0: one run).
+struct IdsOperand {
+  const void* p;
+  int wide;                  // int64, else int32
+  uint32_t run, magic;
+  int shift;
+  long long stride, step;
+};
+
+// Embedding (embedding.hip): y_t = scale table[id_t], zero for ids outside the table.
+struct EmbedLaunch {
+  const void* table;
+  void* y;
+  IdsOperand ids;
+  long long ldt, ldy;
+  uint32_t tokens;
+  int vocab, n;
+  float scale;
+};
+hipError_t launch_embed(const EmbedLaunch& A, bool table_bf16, bool bf16, hipStream_t st);
+struct EmbedGradLaunch {
+  const void* dy;
+  void* dtable;              // [vocab][n]
+  IdsOperand ids;
+  long long lddy;
+  uint32_t tokens;
+  int vocab, n, accumulate;
+  float scale;
+  // workspace
+  int *count, *order, *row;  // tokens inside the table; sorted by id: their places and ids
+  float* part;               // [chunks][2][n]
+};
+int embed_grad_chunk(uint32_t tokens);   // sorted tokens that a thread adds up
+hipError_t launch_embed_grad(const EmbedGradLaunch& A, bool bf16, bool table_bf16, hipStream_t st);
+
+// Group norm (group_norm.hip, group_norm_backward.hip): each group of w channels of a
+// row is normalised by itself.
+enum NormGate { kGateBefore, kGateAfter, kGateNone };   // norm(x silu(z)) w + b; (norm(x) w + b) silu(z); silu(norm(x) w + b)
+enum NormAct { kActNone, kActSilu };                    // of kGateNone
+struct GroupNormLaunch {
+  const void *x, *z;       // z null: kGateNone
+  void* y;
+  long long ldx, ldz, ldy;
+  int rows, groups, w, center, act;
+  const float *weight, *bias;   // may be null
+  float eps;
+  float *mean, *rstd;      // [rows][groups], may be null
+};
+hipError_t launch_group_norm(const GroupNormLaunch& A, NormGate gate, bool bf16, hipStream_t st);
+struct GroupNormGradLaunch {
+  const void *dy, *x, *z;
+  void *dx, *dz;
+  long long lddy, ldx, ldz, lddx, lddz;
+  int rows, groups, w, act;
+  const float *weight, *bias;   // may be null
+  const float *mean, *rstd;     // [rows][groups]; mean null: no centering
+  float *dw, *db;          // may be null
+  float* part;             // [parts][2][groups w]
+  int parts;
+};
+int group_norm_grad_parts(int rows, int groups, int w, bool bf16);
+hipError_t launch_group_norm_grad(const GroupNormGradLaunch& A, NormGate gate, bool bf16, hipStream_t st);
+// dw and db (null: not wanted) from part[parts][2][n] (layer_norm.hip).
+hipError_t launch_norm_parts(const float* part, int parts, int n, float* dw, float* db, hipStream_t st);
+
+// Log probabilities of tokens from rows of logits (token_logprobs.hip).
+constexpr int kLogpMaxTop = 64;
+struct LogpLaunch {
+  const void* x;
+  IdsOperand ids;            // p null: no tokens
+  long long ldx, rows;
+  int vocab, top, splits;    // workgroups that share a row
+  float scale;
+  float *logp, *entropy;     // [rows], may be null
+  float* stats;              // [rows][2]: the largest logit, the log of the sum around it; may be null
+  int* top_ids;              // [rows][top]
+  float* top_logp;
+  // workspace of splits > 1
+  float* part;               // [rows][splits][3]
+  int *keys, *idx;           // [rows][splits][top]
+};
+int logp_splits(long long rows, int vocab, bool bf16);
+hipError_t launch_logp(const LogpLaunch& A, bool bf16, hipStream_t st);
+struct LogpGradLaunch {
+  const void* x;
+  void* dx;                  // may be x
+  IdsOperand ids;            // p null: no tokens
+  long long ldx, lddx, rows;
+  int vocab;
+  float scale;
+  const float* stats;
+  const float *dlogp, *dentropy, *entropy;   // dlogp or dentropy may be null
+  long long sdlogp, sdentropy;               // their strides
+};
+hipError_t launch_logp_grad(const LogpGradLaunch& A, bool bf16, hipStream_t st);
+
 }  // namespace muon

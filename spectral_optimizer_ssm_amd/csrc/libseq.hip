@@ -16,35 +16,9 @@ using namespace muon;
 
 namespace {
 
-// Bytes an operand spans.
-struct Span {
-  const char* p;
-  size_t n;
-};
-Span span(const void* p, size_t bytes) { return {static_cast<const char*>(p), bytes}; }
 Span span(const muon_seq& s, int batch, int tokens, int heads, int width, size_t es) {
   const long long last = (batch - 1) * s.sb + (tokens - 1) * s.st + (heads - 1) * s.sh + width;
   return {static_cast<const char*>(s.p), static_cast<size_t>(last) * es};
-}
-// No output may overlap an input or another output (null operands overlap nothing).
-bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-  for (const Span* a = outs.begin(); a != outs.end(); ++a) {
-    if (a->p == nullptr) continue;
-    for (const Span& b : ins)
-      if (b.p != nullptr && overlaps(a->p, a->n, b.p, b.n)) return true;
-    for (const Span* b = a + 1; b != outs.end(); ++b)
-      if (b->p != nullptr && overlaps(a->p, a->n, b->p, b->n)) return true;
-  }
-  return false;
-}
-
-// Whether a strided operand's bytes can be counted: no memory holds 2^60.
-bool extent_ok(std::initializer_list<long long> steps, std::initializer_list<long long> strides) {
-  long long sum = 0, p;
-  const long long* st = strides.begin();
-  for (long long n : steps)
-    if (__builtin_mul_overflow(n, *st++, &p) || __builtin_add_overflow(sum, p, &sum) || sum > 1LL << 58) return false;
-  return true;
 }
 bool seq_ok(const muon_seq& s, int batch, int tokens, int heads, size_t es) {
   return s.p != nullptr && aligned_to(s.p, es) && s.sb >= 0 && s.st >= 0 && s.sh >= 0 &&
@@ -70,9 +44,6 @@ int check_operands(const muon_scan_args* a) {
   return MUON_OK;
 }
 
-// A dimension of a launch has fewer than 2^32 work items; past that a grid is
-// taken modulo 2^32, without an error.
-bool launchable(long long blocks, int threads) { return blocks <= 0xffffffffLL / threads; }
 // The product, or LLONG_MAX where it does not fit.
 long long times(long long a, long long b, long long c) {
   long long p;
@@ -340,11 +311,6 @@ int check_norm(int dtype, long long rows, int n) {
   if (rows < 0 || n <= 0) return MUON_EINVAL;
   return rows > INT_MAX || n > kNormMaxN ? MUON_EUNSUPPORTED : MUON_OK;
 }
-bool rows_ok(long long rows, int n, long long ld) { return ld >= n && (rows == 0 || extent_ok({rows - 1}, {ld})); }
-Span rows_span(const void* p, long long rows, int n, long long ld, size_t es) {
-  return span(p, rows == 0 ? 0 : static_cast<size_t>((rows - 1) * ld + n) * es);
-}
-
 }  // namespace
 
 int muon_layer_norm(const void* X, long long ldx, int dtype, long long rows, int n, const float* weight, const float* bias,
