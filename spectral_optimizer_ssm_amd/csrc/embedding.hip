@@ -3,13 +3,19 @@
 // with zeros for ids outside the table, which take no gradient.
 //
 // The gradient's sums run over tokens sorted by id, in the tokens' order, so they
-// need no atomics and repeat bit for bit.  Three launches:
-//   1. a workgroup for each range of ids walks all ids twice, counts and places
-//      those in its range; others write the table's zeros meanwhile;
-//   2. a thread for 16 bytes of a row's columns and a chunk of the sorted tokens
-//      adds up each id's rows; an id that spans two borders of chunks leaves a
-//      part sum in each, all others are written at once;
+// need no atomics and repeat bit for bit (the sort's counters in LDS are the only
+// ones, and their sums are whole numbers).  Three launches:
+//   1. a workgroup for each range of ids walks all ids and places those in its range;
+//      the other workgroups write the table's zeros meanwhile, which take longer;
+//   2. a wave for a piece of the rows' columns and a chunk of the sorted tokens adds up
+//      each id's rows; an id that spans two borders of chunks leaves a part sum in
+//      each, all others are written at once;
 //   3. the parts of those ids are added, in order.
+// However often one id occurs, no wave adds more than two chunks.  Measured (bfloat16
+// gradients, a float32 table of 50,280 rows, ids by Zipf's law): 16,384 tokens of 768
+// take 21 + 13 + 7 us, bound by the zeros' 154 MB (7.2 TB/s) and the gathered rows;
+// 131,071 tokens of 515 take 42 + 44 + 13 us: the walk of the ids, 64 of which reach a
+// wave for every two that belong to it, and 240 MB of rows, parts and sums.
 #include "launch.h"
 #include "ids.cuh"
 #include "rows.cuh"
@@ -99,18 +105,76 @@ hipError_t embed_any(const EmbedLaunch& A, hipStream_t st) {
 // gradient
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
-constexpr int kRange = 256;          // most ids of a workgroup
+constexpr int kRangeBits = 9, kRange = 1 << kRangeBits;   // most ids of a workgroup
+constexpr int kKept = 1024;          // tokens that a wave keeps between its two walks
 constexpr int kFillPerThread = 8;    // 16-byte stores
 
+// Ids of a workgroup: all walk all ids, so not more than half the compute units do, and
+// the others write zeros meanwhile (16,384 tokens, table 50,280 x 768: 21 us, of which the
+// zeros alone take 21; 27 with 256 workgroups; 131,071 tokens and 515 columns: 42 and 40).
 int range_of(int vocab) {
-  const int r = (vocab + 255) / 256;   // a workgroup for each compute unit before ranges reach kRange
+  const int r = (vocab + 127) / 128;
   return r < 1 ? 1 : r > kRange ? kRange : r;
+}
+
+// Calls f(token, id) for groups of 64 tokens in order, a token a lane (past `end` with
+// id -1); `load` gives a token's id.  Sixteen groups' loads are in flight.
+template <typename L, typename F>
+__device__ __forceinline__ void walk(uint32_t from, uint32_t end, const L& load, const F& f) {
+  constexpr int U = 16;
+  const uint32_t lane = threadIdx.x & (kWave - 1);
+  uint32_t t = from;
+  for (; end - t >= U * kWave; t += U * kWave) {
+    int id[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) id[u] = load(t + u * kWave + lane);
+#pragma unroll
+    for (int u = 0; u < U; ++u) f(t + u * kWave + lane, id[u]);
+  }
+  for (; t < end; t += kWave) {
+    const uint32_t at = t + lane;
+    const int id = load(at < end ? at : end - 1);
+    f(at, at < end ? id : -1);
+  }
+}
+// An id as int, -1 past that.
+__device__ __forceinline__ int narrow(u32x2_t id) { return id[1] == 0 ? static_cast<int>(id[0]) : -1; }
+template <typename F>
+__device__ __forceinline__ void walk_ids(const IdsOperand& ids, uint32_t from, uint32_t end, const F& f) {
+  if (ids.magic != 0 || ids.step != 1) walk(from, end, [&](uint32_t t) { return narrow(__builtin_bit_cast(u32x2_t, id_at(ids, t))); }, f);
+  else if (ids.wide) walk(from, end, [&](uint32_t t) { return narrow(static_cast<const u32x2_t*>(ids.p)[t]); }, f);
+  else walk(from, end, [&](uint32_t t) { return static_cast<const int*>(ids.p)[t]; }, f);
+}
+// Lanes with a < b.
+__device__ __forceinline__ unsigned long long lanes_below(uint32_t a, uint32_t b) { return __builtin_amdgcn_uicmp(a, b, 36); }
+
+// The lanes that hold this lane's number, of those with `in` (of kRangeBits bits): two
+// numbers are most often nearly all, the others are told apart bit by bit.
+__device__ __forceinline__ unsigned long long same_lanes(bool in, int d) {
+  unsigned long long left = __ballot(in), same = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (left == 0) return same;
+    const int of = __builtin_amdgcn_readlane(d, __ffsll(left) - 1);
+    const unsigned long long those = __ballot(in && d == of);
+    if (d == of) same = those;
+    left &= ~those;
+  }
+  if (left == 0) return same;
+  unsigned long long rest = left;
+#pragma unroll
+  for (int b = 0; b < kRangeBits; ++b) {
+    const unsigned long long set = __ballot((d >> b) & 1);
+    rest &= (d >> b) & 1 ? set : ~set;
+  }
+  return (left >> (threadIdx.x & (kWave - 1))) & 1 ? rest : same;
 }
 
 // Blocks below `sorters`: ids [b range, (b + 1) range).  The others: zeros.
 template <typename TT>
-__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradLaunch A, int range, int sorters, int bits, long long bytes) {
+__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradLaunch A, int range, int sorters, long long bytes) {
   __shared__ int hist[kSortWaves][kRange];
+  __shared__ uint32_t kept[kSortWaves][kKept];   // (token from the wave's first) kRange + id from the range's first
   __shared__ int waves[kSortWaves];
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
   const long long blk = block_of_grid();
@@ -128,30 +192,45 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradLaunc
     }
     return;
   }
-  const int lo = static_cast<int>(blk) * range, hi = A.vocab - lo < range ? A.vocab : lo + range;
+  const int lo = static_cast<int>(blk) * range, here = A.vocab - lo < range ? A.vocab - lo : range;
   for (int i = threadIdx.x; i < kSortWaves * kRange; i += kSortThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  // this wave's tokens
-  const uint32_t span = ((A.tokens + kSortWaves - 1) / kSortWaves + kWave - 1) / kWave * kWave;
+  // this wave's tokens, an odd number of 64: the waves' places are on different channels of the L2
+  const uint32_t span = (((A.tokens + kSortWaves - 1) / kSortWaves + kWave - 1) / kWave | 1) * kWave;
   const uint32_t t0 = w * span < A.tokens ? w * span : A.tokens, t1 = A.tokens - t0 < span ? A.tokens : t0 + span;
-  constexpr int U = 4;
-  int below = 0;
-  for (uint32_t t = t0; t < t1; t += U * kWave) {
-    long long id[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t at = t + u * kWave + lane;
-      id[u] = at < t1 ? id_at(A.ids, at) : -1;
+  const uint32_t room = span <= 1u << (32 - kRangeBits) ? kKept : 0;
+  uint32_t below = 0, found = 0;   // uniform
+  walk_ids(A.ids, t0, t1, [&](uint32_t t, int id) {
+    const uint32_t d = static_cast<uint32_t>(id) - lo;
+    below += static_cast<uint32_t>(__popcll(lanes_below(static_cast<uint32_t>(id), static_cast<uint32_t>(lo))));
+    const unsigned long long set = lanes_below(d, static_cast<uint32_t>(here));
+    if (set == 0) return;
+    const uint32_t at = found + static_cast<uint32_t>(__popcll(set & ((1ull << lane) - 1)));
+    if (((set >> lane) & 1) && at < room) kept[w][at] = (t - t0) << kRangeBits | d;
+    found += static_cast<uint32_t>(__popcll(set));
+  });
+  // Calls f(token, in the range, id from its first) for groups of 64 of the wave's tokens.
+  const auto again = [&](const auto& f) {
+    if (found <= room) {
+      for (uint32_t i = 0; i < found; i += kWave) {
+        const bool in = i + lane < found;
+        const uint32_t v = in ? kept[w][i + lane] : 0;
+        f(t0 + (v >> kRangeBits), in, static_cast<int>(v & (kRange - 1)));
+      }
+    } else {
+      walk_ids(A.ids, t0, t1, [&](uint32_t t, int id) {
+        const uint32_t d = static_cast<uint32_t>(id) - lo;
+        const bool in = d < static_cast<uint32_t>(here);
+        f(t, in, in ? static_cast<int>(d) : 0);
+      });
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      below += id[u] >= 0 && id[u] < lo;
-      if (id[u] >= lo && id[u] < hi) atomicAdd(&hist[w][id[u] - lo], 1);
-    }
-  }
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) below += __shfl_xor(below, off, kWave);
-  if (lane == 0) waves[w] = below;
+  };
+  __syncthreads();
+  again([&](uint32_t, bool in, int d) {
+    const unsigned long long same = same_lanes(in, d);
+    if (in && (same & ((1ull << lane) - 1)) == 0) atomicAdd(&hist[w][d], static_cast<int>(__popcll(same)));
+  });
+  if (lane == 0) waves[w] = static_cast<int>(below);
   __syncthreads();
   int base = 0;   // of the range in the sorted order
   for (int i = 0; i < kSortWaves; ++i) base += waves[i];
@@ -161,7 +240,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradLaunc
   if (threadIdx.x < kRange) {
     for (int i = 0; i < kSortWaves; ++i) total += hist[i][threadIdx.x];
   }
-  int incl = total;   // prefix over the ids: the first four waves hold them
+  int incl = total;   // prefix over the ids: the first waves hold them
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
     const int v = __shfl_up(incl, off, kWave);
@@ -180,46 +259,38 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradLaunc
     }
   }
   __syncthreads();
-  for (uint32_t t = t0; t < t1; t += U * kWave) {
-    long long id[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t at = t + u * kWave + lane;
-      id[u] = at < t1 ? id_at(A.ids, at) : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool in = id[u] >= lo && id[u] < hi;
-      unsigned long long same = __ballot(in);   // lanes with this lane's id
-      if (same == 0) continue;
-      const int d = in ? static_cast<int>(id[u] - lo) : 0;
-      for (int b = 0; b < bits; ++b) {
-        const unsigned long long set = __ballot((d >> b) & 1);
-        same &= (d >> b) & 1 ? set : ~set;
-      }
-      const int lead = __ffsll(same) - 1;
-      const int before = __popcll(same & ((1ull << lane) - 1));
-      int at = 0;
-      if (in && lane == lead) at = atomicAdd(&hist[w][d], static_cast<int>(__popcll(same)));
-      at = __shfl(at, lead < 0 ? 0 : lead, kWave) + before;
-      if (in) {
-        A.order[at] = static_cast<int>(t + u * kWave + lane);
-        A.row[at] = static_cast<int>(id[u]);
-      }
-    }
-  }
+  // the tokens to their places: those of one id in the lanes' order
+  again([&](uint32_t t, bool in, int d) {
+    const unsigned long long same = same_lanes(in, d);
+    const int lead = in ? __ffsll(same) - 1 : 0;
+    int at = 0;
+    if (in && lane == lead) at = atomicAdd(&hist[w][d], static_cast<int>(__popcll(same)));
+    at = __shfl(at, lead, kWave) + static_cast<int>(__popcll(same & ((1ull << lane) - 1)));
+    if (in) A.sorted[at] = make_int2(static_cast<int>(t), lo + d);
+  });
 }
 
-// A row's piece from its sum.
+// V columns of a row from their sum, of which those from `first` on are this thread's
+// alone (those before are its neighbour's too, which stores the same).
 template <typename TT, int V>
-__device__ __forceinline__ void put(const EmbedGradLaunch& A, int id, int c, float (&acc)[V]) {
+__device__ __forceinline__ void put(const EmbedGradLaunch& A, int id, int c, int first, float (&acc)[V]) {
   TT* to = static_cast<TT*>(A.dtable) + static_cast<long long>(id) * A.n + c;
 #pragma unroll
   for (int e = 0; e < V; ++e) acc[e] *= A.scale;
   if constexpr (sizeof(TT) == 4) {
     if (A.accumulate) {
+      if (first > 0) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += to[e];
+        for (int e = 1; e < V; ++e)
+          if (e >= first) to[e] += acc[e];
+        return;
+      }
+      constexpr int W = V < 4 ? V : 4;
+      float was[V / W][W];
+#pragma unroll
+      for (int k = 0; k < V / W; ++k) load_n<float, W>(to + k * W, was[k]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += was[e / W][e % W];
     }
   }
   store_n<TT, V>(to, acc);
@@ -228,105 +299,133 @@ __device__ __forceinline__ void put(const EmbedGradLaunch& A, int id, int c, flo
 // Borders are the multiples of `chunk` below the count.  An id whose run spans two
 // borders or more is long: each chunk that it touches leaves its part.  A run that
 // spans one belongs to the chunk where it starts.
-struct Runs {
-  const int* row;
-  int count, chunk;
-  __device__ __forceinline__ bool spans(int b, int id) const {   // border b inside the run of id
-    return b > 0 && b < count && row[b - 1] == id && row[b] == id;
-  }
-  // a run that spans border b
-  __device__ __forceinline__ bool long_at(int b) const {
-    const int id = row[b];
-    return spans(b - chunk, id) || spans(b + chunk, id);
-  }
-};
-
-// The pieces of a row do not overlap here (the last one is short): part sums and
-// gradients may be added to what is there.
+//
+// A wave for 64 pieces of V columns (of a row's last ones, moved back to end with it) of
+// a chunk of the sorted tokens: places and ids are uniform.  Eight tokens' rows are in
+// flight, and the next eight's places.
 template <typename T, typename TT, int V>
-__global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedGradLaunch A, int chunk, uint32_t pieces) {
-  const long long i = block_of_grid() * kThreads + threadIdx.x;
-  const int c = static_cast<int>(i / pieces), col = static_cast<int>(i - static_cast<long long>(c) * pieces) * V;
-  const int count = *A.count;
-  const int p0 = c * chunk;
-  if (p0 >= count || static_cast<long long>(c) * chunk >= count) return;
-  const Runs R{A.row, count, chunk};
-  const T* dy = static_cast<const T*>(A.dy) + col;
+__global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedGradLaunch A, const int2* __restrict__ sorted, const int* __restrict__ counted,
+                                                             int chunk, uint32_t slices) {
+  const long long i = block_of_grid() * (kThreads / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const long long c = i / slices;
+  if (c * chunk >= A.tokens) return;
+  const int col = (static_cast<int>(i - c * slices) * kWave + static_cast<int>(threadIdx.x & (kWave - 1))) * V;
+  const int base = col < A.n - V ? col : A.n - V, first = col - base;
+  constexpr int U = 8;
+  // all that the chunk's state needs, in one go (places past the count hold anything)
+  const int p0 = static_cast<int>(c) * chunk, last = static_cast<int>(A.tokens) - 1;
+  const auto at = [&](int p) { return sorted[p < 0 ? 0 : p < last ? p : last]; };
+  int2 s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) s[u] = at(p0 + u);
+  const int before = at(p0 - 1).y, far = at(p0 - chunk - 1).y, next = at(p0 + chunk).y, next2 = at(p0 + 2 * chunk).y;
+  const int count = *counted;
+  if (p0 >= count) return;
   const int p1 = count - p0 < chunk ? count : p0 + chunk;
-  int p = p0, id = A.row[p0];
-  bool open = p0 > 0 && A.row[p0 - 1] == id;   // the run began before
-  float* part = A.part + 2LL * c * A.n + col;
-  if (open && !R.long_at(p0)) {   // the chunk before adds it up
-    while (p < p1 && A.row[p] == id) ++p;
+  const T* dy = static_cast<const T*>(A.dy) + base;
+  float* part = A.part + 2 * c * A.n;
+  int id = s[0].y;
+  // whose is the run at the start: this chunk's, the chunk's before (skip) or every chunk's that it touches (open)
+  bool open = p0 > 0 && before == id, skip = false;
+  if (open && !(p0 > chunk && far == id) && !(p0 + chunk < count && next == id)) {
     open = false;
-    if (p == p1) return;   // (a run over the whole chunk spans both its borders)
-    id = A.row[p];
+    skip = true;
   }
-  for (;;) {
-    float acc[V], v[V];
+  const bool far_on = p0 + 2 * chunk < count;
+  float acc[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.0f;
-    while (p < p1 && A.row[p] == id) {
-      load_n<T, V>(dy + static_cast<long long>(A.order[p]) * A.lddy, v);
+  for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+  const auto leave = [&](bool goes_on) {   // the run ends, or goes on behind the chunk
+    if (skip || first >= V) return;
+    if (open || goes_on) store_n<float, V>((open ? part : part + A.n) + base, acc);
+    else put<TT, V>(A, id, base, first, acc);
+  };
+  for (int q = p0;; q += U) {
+    float v[U][V];
+    int ids[U];
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += v[e];
-      ++p;
+    for (int u = 0; u < U; ++u) {
+      ids[u] = s[u].y;
+      load_n<T, V>(dy + static_cast<long long>(q + u < count ? s[u].x : 0) * A.lddy, v[u]);
     }
-    const bool on = p == p1 && p1 < count && A.row[p1] == id;   // the run goes on
-    if (open || (on && R.long_at(p1))) {
-      store_n<float, V>(open ? part : part + A.n, acc);
-    } else {
-      if (on) {
-        for (; p < count && A.row[p] == id; ++p) {
-          load_n<T, V>(dy + static_cast<long long>(A.order[p]) * A.lddy, v);
 #pragma unroll
-          for (int e = 0; e < V; ++e) acc[e] += v[e];
+    for (int u = 0; u < U; ++u) s[u] = at(q + U + u);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = q + u;
+      const bool new_run = p >= count || ids[u] != id;
+      if (new_run) leave(false);
+      if (p >= p1) {
+        if (new_run || skip) return;
+        if (p == p1 && (open || (far_on && next2 == id))) {   // (the run spans this border)
+          leave(true);
+          return;
         }
       }
-      put<TT, V>(A, id, col, acc);
+      if (new_run) {
+        id = ids[u];
+        open = skip = false;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += v[u][e];
     }
-    if (p >= p1) return;
-    id = A.row[p];
-    open = false;
   }
 }
 
-// The long runs' parts: a workgroup looks for those that start in its chunks.
+// The long runs' parts: the lanes look for those that start in the workgroup's chunks,
+// then its waves share each one's parts.
 constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave, kJoinChunks = 16;
 
-template <typename TT>
+template <typename TT, int V>
 __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(EmbedGradLaunch A, int chunk) {
-  __shared__ float sums[kJoinWaves][kWave];
-  const int count = *A.count;
+  __shared__ float sums[kJoinWaves][V][kWave];
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-  const Runs R{A.row, count, chunk};
-  const int col = static_cast<int>(blockIdx.y) * kWave + lane;
+  const int col = (static_cast<int>(blockIdx.y) * kWave + lane) * V;
+  const int base = col < A.n - V ? col : A.n - V, first = col - base;
   const long long c0 = static_cast<long long>(blockIdx.x) * kJoinChunks;
-  for (int k = 0; k < kJoinChunks; ++k) {
-    const long long b = (c0 + k + 1) * chunk;   // the border behind the chunk
-    if (b >= count) return;
-    const int p1 = static_cast<int>(b), id = A.row[p1];
-    if (A.row[p1 - 1] != id || !R.long_at(p1) || R.spans(p1 - chunk, id)) continue;
-    // the last border inside the run
-    int lo = 1, hi = (count - 1 - p1) / chunk + 1;   // p1 + lo' chunk holds id for lo' < lo
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      if (A.row[p1 + mid * chunk] == id) lo = mid + 1;
-      else hi = mid;
+  const int last = static_cast<int>(A.tokens) - 1;
+  const auto id_of = [&](long long p) { return A.sorted[p < 0 ? 0 : p < last ? p : last].y; };
+  // the border behind the lane's chunk: spanned, and the one behind it, but not the one before
+  const long long b0 = (c0 + (lane < kJoinChunks ? lane : 0) + 1) * chunk;
+  const int mine = id_of(b0), before = id_of(b0 - 1), next = id_of(b0 + chunk), far = id_of(b0 - chunk - 1);
+  const int count = *A.count;
+  const bool starts = lane < kJoinChunks && b0 + chunk < count && before == mine && next == mine && !(b0 > chunk && far == mine);
+  for (unsigned long long set = __ballot(starts); set != 0; set &= set - 1) {
+    const int k = __ffsll(set) - 1, id = __builtin_amdgcn_readlane(mine, k);
+    const long long c = c0 + k, p1 = (c + 1) * chunk;
+    // borders inside the run: `parts` are, and one of the `more` after them is the first that is not
+    int parts = 0, more = (count - 1 - static_cast<int>(p1)) / chunk + 2;
+    while (more > 1) {
+      const int step = (more + kWave - 2) / kWave;   // the lanes cover more - 1 of them
+      const long long b = p1 + static_cast<long long>(parts + step * lane + step - 1) * chunk;
+      const int n = static_cast<int>(__popcll(__ballot(b < count && id_of(b) == id)));
+      parts += n * step;
+      more = step;
     }
-    const long long c = c0 + k;
-    float acc = 0.0f;
-    if (col < A.n) {
-      if (w == 0) acc = A.part[(2 * c + 1) * A.n + col];
-      for (int j = w; j < lo; j += kJoinWaves) acc += A.part[2 * (c + 1 + j) * A.n + col];
+    float acc[V], v[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+    const float* part = A.part + 2 * (c + 1) * A.n + base;
+    if (w == 0) load_n<float, V>(part - A.n, acc);
+#pragma unroll 16
+    for (int j = w; j < parts; j += kJoinWaves) {
+      load_n<float, V>(part + 2LL * j * A.n, v);
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += v[e];
     }
     __syncthreads();
-    sums[w][lane] = acc;
+#pragma unroll
+    for (int e = 0; e < V; ++e) sums[w][e][lane] = acc[e];
     __syncthreads();
     if (w == 0 && col < A.n) {
-      float v[1] = {0.0f};
-      for (int j = 0; j < kJoinWaves; ++j) v[0] += sums[j][lane];
-      put<TT, 1>(A, id, col, v);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        acc[e] = 0.0f;
+        for (int j = 0; j < kJoinWaves; ++j) acc[e] += sums[j][e][lane];
+      }
+      put<TT, V>(A, id, base, first, acc);
     }
   }
 }
@@ -335,32 +434,36 @@ template <typename T, typename TT, int V>
 hipError_t sums(const EmbedGradLaunch& A, int chunk, hipStream_t st) {
   const long long chunks = (static_cast<long long>(A.tokens) + chunk - 1) / chunk;
   const uint32_t pieces = (static_cast<uint32_t>(A.n) + V - 1) / V;
-  hipLaunchKernelGGL((embed_sum_kernel<T, TT, V>), grid_of((chunks * pieces + kThreads - 1) / kThreads), dim3(kThreads), 0, st, A, chunk, pieces);
+  const uint32_t slices = (pieces + kWave - 1) / kWave;
+  hipLaunchKernelGGL((embed_sum_kernel<T, TT, V>), grid_of((chunks * slices + kThreads / kWave - 1) / (kThreads / kWave)), dim3(kThreads), 0, st, A,
+                     A.sorted, A.count, chunk, slices);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || chunks < 3) return e;   // no run spans two borders
+  constexpr int W = V < 4 ? V : 4;
+  const dim3 grid(static_cast<unsigned>((chunks + kJoinChunks - 1) / kJoinChunks), (A.n + kWave * W - 1) / (kWave * W));
+  hipLaunchKernelGGL((embed_join_kernel<TT, W>), grid, dim3(kJoinThreads), 0, st, A, chunk);
   return hipGetLastError();
 }
 
 template <typename T, typename TT>
 hipError_t embed_grad(const EmbedGradLaunch& A, hipStream_t st) {
   const int range = range_of(A.vocab), sorters = (A.vocab + range - 1) / range;
-  int bits = 0;
-  while ((1 << bits) < range) ++bits;
   const long long bytes = A.accumulate ? 0 : static_cast<long long>(A.vocab) * A.n * static_cast<long long>(sizeof(TT));
   const long long fill = (bytes + 16LL * kFillPerThread * kSortThreads - 1) / (16LL * kFillPerThread * kSortThreads);
-  hipLaunchKernelGGL((embed_sort_kernel<TT>), grid_of(sorters + fill), dim3(kSortThreads), 0, st, A, range, sorters, bits, bytes);
-  hipError_t e = hipGetLastError();
+  hipLaunchKernelGGL((embed_sort_kernel<TT>), grid_of(sorters + fill), dim3(kSortThreads), 0, st, A, range, sorters, bytes);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || A.tokens == 0) return e;
   const int chunk = embed_grad_chunk(A.tokens);
   constexpr int V = Vec<T>::n;
-  e = A.n % V == 0 ? sums<T, TT, V>(A, chunk, st) : sums<T, TT, 1>(A, chunk, st);
-  if (e != hipSuccess) return e;
-  const unsigned chunks = (A.tokens + chunk - 1) / chunk;
-  hipLaunchKernelGGL((embed_join_kernel<TT>), dim3((chunks + kJoinChunks - 1) / kJoinChunks, (A.n + kWave - 1) / kWave), dim3(kJoinThreads), 0, st, A, chunk);
-  return hipGetLastError();
+  return A.n >= V ? sums<T, TT, V>(A, chunk, st) : sums<T, TT, 1>(A, chunk, st);
 }
 
 }  // namespace
 
-int embed_grad_chunk(uint32_t tokens) { return tokens > 16 * 4096 ? 32 : 16; }
+// Sorted tokens of a chunk: 16,384 tokens of 768 take 15 + 7 us (sums and joins) in
+// chunks of 16, 16 + 11 of 8 and 16 + 7 of 32; 131,071 of 515 take 44 + 13 of 32,
+// 46 + 23 of 16 and 57 + 49 of 8.
+int embed_grad_chunk(uint32_t tokens) { return tokens > 1u << 16 ? 32 : 16; }
 
 hipError_t launch_embed(const EmbedLaunch& A, bool table_bf16, bool bf16, hipStream_t st) {
   if (table_bf16) return bf16 ? embed_any<bf16_t, bf16_t>(A, st) : embed_any<bf16_t, float>(A, st);

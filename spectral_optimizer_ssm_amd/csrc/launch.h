@@ -435,7 +435,8 @@ struct EmbedGradLaunch {
   int vocab, n, accumulate;
   float scale;
   // workspace
-  int *count, *order, *row;  // tokens inside the table; sorted by id: their places and ids
+  int* count;                // of the tokens inside the table
+  int2* sorted;              // those by id, in their order: token, id
   float* part;               // [chunks][2][n]
 };
 int embed_grad_chunk(uint32_t tokens);   // sorted tokens that a thread adds up

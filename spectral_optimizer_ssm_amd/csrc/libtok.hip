@@ -61,15 +61,14 @@ int check_embed(int table_dtype, int dtype, long long tokens, int vocab, int n) 
 }
 
 struct EmbedPlan {
-  size_t order, row, part, end;
+  size_t sorted, part, end;
 };
 EmbedPlan plan_embed(long long tokens, int n) {
   EmbedPlan p;
   const int chunk = embed_grad_chunk(static_cast<uint32_t>(tokens));
-  const size_t list = align_up(static_cast<size_t>(tokens) * 4, kAlign), chunks = static_cast<size_t>((tokens + chunk - 1) / chunk);
-  p.order = kAlign;   // behind the count
-  p.row = p.order + list;
-  p.part = p.row + list;
+  const size_t chunks = static_cast<size_t>((tokens + chunk - 1) / chunk);
+  p.sorted = kAlign;   // behind the count
+  p.part = p.sorted + align_up(static_cast<size_t>(tokens) * 8, kAlign);
   p.end = p.part + align_up(chunks * 2 * n * 4, kAlign);
   return p;
 }
@@ -158,8 +157,7 @@ int muon_embedding_backward(const void* dY, int dtype, long long lddy, const muo
   A.accumulate = accumulate; A.scale = scale;
   if (tokens > 0) A.ids = ids_operand(*ids, tokens);
   A.count = reinterpret_cast<int*>(ws);
-  A.order = reinterpret_cast<int*>(ws + p.order);
-  A.row = reinterpret_cast<int*>(ws + p.row);
+  A.sorted = reinterpret_cast<int2*>(ws + p.sorted);
   A.part = reinterpret_cast<float*>(ws + p.part);
   return launched(launch_embed_grad(A, dtype == MUON_BF16, table_dtype == MUON_BF16, static_cast<hipStream_t>(stream)));
 }
