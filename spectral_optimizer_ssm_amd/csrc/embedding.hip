@@ -14,8 +14,9 @@
 // However often one id occurs, no wave adds more than two chunks.  Measured (bfloat16
 // gradients, a float32 table of 50,280 rows, ids by Zipf's law): 16,384 tokens of 768
 // take 21 + 13 + 7 us, bound by the zeros' 154 MB (7.2 TB/s) and the gathered rows;
-// 131,071 tokens of 515 take 42 + 44 + 13 us: the walk of the ids, 64 of which reach a
-// wave for every two that belong to it, and 240 MB of rows, parts and sums.
+// 131,071 tokens of 515 take 52 + 59 + 15 us: the walk of the ids (37 by itself, vector
+// instructions for the 64 ids of which half of one is the workgroup's), and 240 MB of
+// rows, sums and parts.
 #include "launch.h"
 #include "ids.cuh"
 #include "rows.cuh"
@@ -111,55 +112,62 @@ constexpr int kFillPerThread = 8;    // 16-byte stores
 
 // Ids of a workgroup: all walk all ids, so not more than half the compute units do, and
 // the others write zeros meanwhile (16,384 tokens, table 50,280 x 768: 21 us, of which the
-// zeros alone take 21; 27 with 256 workgroups; 131,071 tokens and 515 columns: 42 and 40).
+// zeros alone take 21; 27 with 256 workgroups).
 int range_of(int vocab) {
   const int r = (vocab + 127) / 128;
   return r < 1 ? 1 : r > kRange ? kRange : r;
 }
 
 // Calls f(token, id) for groups of 64 tokens in order, a token a lane (past `end` with
-// id -1); `load` gives a token's id.  Sixteen groups' loads are in flight.
+// id -1); `load` gives a token's id as it lies there.  Sixteen groups' loads are in flight.
+__device__ __forceinline__ int narrow(int id) { return id; }
+__device__ __forceinline__ int narrow(u32x2_t id) { return id[1] == 0 ? static_cast<int>(id[0]) : -1; }   // -1 past 32 bits
 template <typename L, typename F>
 __device__ __forceinline__ void walk(uint32_t from, uint32_t end, const L& load, const F& f) {
-  constexpr int U = 16;
+  constexpr uint32_t U = 16;
   const uint32_t lane = threadIdx.x & (kWave - 1);
   uint32_t t = from;
   for (; end - t >= U * kWave; t += U * kWave) {
-    int id[U];
+    decltype(load(0)) id[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) id[u] = load(t + u * kWave + lane);
+    for (uint32_t u = 0; u < U; ++u) id[u] = load(t + u * kWave + lane);
 #pragma unroll
-    for (int u = 0; u < U; ++u) f(t + u * kWave + lane, id[u]);
+    for (uint32_t u = 0; u < U; ++u) f(t + u * kWave + lane, narrow(id[u]));
   }
   for (; t < end; t += kWave) {
     const uint32_t at = t + lane;
-    const int id = load(at < end ? at : end - 1);
+    const int id = narrow(load(at < end ? at : end - 1));
     f(at, at < end ? id : -1);
   }
 }
-// An id as int, -1 past that.
-__device__ __forceinline__ int narrow(u32x2_t id) { return id[1] == 0 ? static_cast<int>(id[0]) : -1; }
 template <typename F>
 __device__ __forceinline__ void walk_ids(const IdsOperand& ids, uint32_t from, uint32_t end, const F& f) {
-  if (ids.magic != 0 || ids.step != 1) walk(from, end, [&](uint32_t t) { return narrow(__builtin_bit_cast(u32x2_t, id_at(ids, t))); }, f);
-  else if (ids.wide) walk(from, end, [&](uint32_t t) { return narrow(static_cast<const u32x2_t*>(ids.p)[t]); }, f);
+  if (ids.magic != 0 || ids.step != 1) walk(from, end, [&](uint32_t t) { return __builtin_bit_cast(u32x2_t, id_at(ids, t)); }, f);
+  else if (ids.wide) walk(from, end, [&](uint32_t t) { return static_cast<const u32x2_t*>(ids.p)[t]; }, f);
   else walk(from, end, [&](uint32_t t) { return static_cast<const int*>(ids.p)[t]; }, f);
 }
 // Lanes with a < b.
 __device__ __forceinline__ unsigned long long lanes_below(uint32_t a, uint32_t b) { return __builtin_amdgcn_uicmp(a, b, 36); }
 
 // The lanes that hold this lane's number, of those with `in` (of kRangeBits bits): two
-// numbers are most often nearly all, the others are told apart bit by bit.
-__device__ __forceinline__ unsigned long long same_lanes(bool in, int d) {
-  unsigned long long left = __ballot(in), same = 0;
+// numbers are most often nearly all (each is passed to `one` with its lanes), the lanes
+// that are left are told apart by `rest`.
+template <typename F>
+__device__ __forceinline__ unsigned long long peel(bool in, int d, const F& one) {
+  unsigned long long left = __ballot(in);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    if (left == 0) return same;
-    const int of = __builtin_amdgcn_readlane(d, __ffsll(left) - 1);
+    if (left == 0) return 0;
+    const int lead = __ffsll(left) - 1, of = __builtin_amdgcn_readlane(d, lead);
     const unsigned long long those = __ballot(in && d == of);
-    if (d == of) same = those;
+    one(of, those, lead);
     left &= ~those;
   }
+  return left;
+}
+__device__ __forceinline__ unsigned long long same_lanes(bool in, int d) {
+  unsigned long long same = 0;
+  const unsigned long long left = peel(in, d, [&](int of, unsigned long long those, int) { same = d == of ? those : same; });
   if (left == 0) return same;
   unsigned long long rest = left;
 #pragma unroll
@@ -227,8 +235,10 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradLaunc
   };
   __syncthreads();
   again([&](uint32_t, bool in, int d) {
-    const unsigned long long same = same_lanes(in, d);
-    if (in && (same & ((1ull << lane) - 1)) == 0) atomicAdd(&hist[w][d], static_cast<int>(__popcll(same)));
+    const unsigned long long left = peel(in, d, [&](int of, unsigned long long those, int lead) {
+      if (lane == lead) atomicAdd(&hist[w][of], static_cast<int>(__popcll(those)));
+    });
+    if ((left >> lane) & 1) atomicAdd(&hist[w][d], 1);
   });
   if (lane == 0) waves[w] = static_cast<int>(below);
   __syncthreads();
