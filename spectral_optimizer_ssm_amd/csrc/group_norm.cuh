@@ -55,10 +55,4 @@ __device__ __forceinline__ float sigmoid(float z) {
 // d silu(z) / dz from s = sigmoid(z)
 __device__ __forceinline__ float silu_slope(float z, float s) { return s * fmaf(z, 1.0f - s, 1.0f); }
 
-template <typename T>
-__device__ __forceinline__ float element(T v) {
-  if constexpr (sizeof(T) == 2) return bf16_to_f32(v);
-  else return v;
-}
-
 }  // namespace muon

@@ -486,7 +486,7 @@ struct LogpLaunch {
   float* top_logp;
   // workspace of splits > 1
   float* part;               // [rows][splits][3]
-  int *keys, *idx;           // [rows][splits][top]
+  unsigned long long* ranks; // [rows][splits][top]
 };
 int logp_splits(long long rows, int vocab, bool bf16);
 hipError_t launch_logp(const LogpLaunch& A, bool bf16, hipStream_t st);

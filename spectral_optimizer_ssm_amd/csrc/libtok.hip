@@ -95,15 +95,14 @@ int check_logp(int dtype, long long rows, int vocab, int top) {
 }
 struct LogpPlan {
   int splits;
-  size_t keys, idx, end;
+  size_t ranks, end;
 };
 LogpPlan plan_logp(long long rows, int vocab, int dtype, int top) {
   LogpPlan p;
   p.splits = logp_splits(rows, vocab, dtype == MUON_BF16);
   const size_t parts = p.splits > 1 ? static_cast<size_t>(rows) * p.splits : 0;
-  p.keys = align_up(parts * 3 * 4, kAlign);
-  p.idx = p.keys + align_up(parts * top * 4, kAlign);
-  p.end = std::max(p.idx + align_up(parts * top * 4, kAlign), kAlign);
+  p.ranks = align_up(parts * 3 * 4, kAlign);
+  p.end = std::max(p.ranks + align_up(parts * top * 8, kAlign), kAlign);
   return p;
 }
 bool strided_ok(const float* p, long long rows, long long stride) {
@@ -255,8 +254,7 @@ int muon_token_logprobs(const void* X, long long ldx, int dtype, long long rows,
   A.logp = logprobs; A.entropy = entropy; A.stats = stats; A.top_ids = top_ids; A.top_logp = top_logprobs;
   char* ws = static_cast<char*>(workspace);
   A.part = reinterpret_cast<float*>(ws);
-  A.keys = reinterpret_cast<int*>(ws + p.keys);
-  A.idx = reinterpret_cast<int*>(ws + p.idx);
+  A.ranks = reinterpret_cast<unsigned long long*>(ws + p.ranks);
   return launched(launch_logp(A, dtype == MUON_BF16, static_cast<hipStream_t>(stream)));
 }
 

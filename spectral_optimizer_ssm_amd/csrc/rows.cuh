@@ -6,6 +6,12 @@
 namespace muon {
 
 template <typename T>
+__device__ __forceinline__ float element(T v) {
+  if constexpr (sizeof(T) == 2) return bf16_to_f32(v);
+  else return v;
+}
+
+template <typename T>
 struct Vec {
   static constexpr int n = 16 / static_cast<int>(sizeof(T));   // elements of a piece
 };

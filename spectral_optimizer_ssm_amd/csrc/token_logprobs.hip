@@ -6,12 +6,14 @@
 //
 // Bound by memory: the logits are read once.  Every thread keeps a running maximum,
 // the sum of exponentials around it and their first moment, rescaled when the
-// maximum grows; every wave keeps its k best in a sorted list, one a lane.
+// maximum grows.  The k largest of the threads' first maxima is a bar that few of a
+// row's logits pass; those are collected in LDS and the k best picked by counting.
 #include "ids.cuh"
 #include "rows.cuh"
 
 #include <float.h>
-#include <limits.h>
+
+#include <type_traits>
 
 namespace muon {
 namespace {
@@ -26,47 +28,71 @@ struct Tile {
   static constexpr int V = Vec<T>::n, U = 4, n = V * U, width = kThreads * n;
 };
 
-// Floats in order as whole numbers (no NaN; -0 and 0 are one).
-__device__ __forceinline__ int key_of(float v) {
-  const int b = __float_as_int(v + 0.0f);
-  return b ^ ((b >> 31) & INT_MAX);
+// A logit and its index as one number: larger is better, ties go to the lowest index
+// (-0 and 0 are one; not for NaN).
+typedef unsigned long long Rank;
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float value_of(int key) { return __int_as_float(key ^ ((key >> 31) & INT_MAX)); }
-constexpr int kInfKey = 0x7F800000, kMinusInfKey = -kInfKey - 1;
+__device__ __forceinline__ float value_of(uint32_t key) { return __uint_as_float(key ^ (~static_cast<uint32_t>(static_cast<int>(key) >> 31) | 0x80000000u)); }
+__device__ __forceinline__ Rank rank_of(float v, int idx) { return static_cast<Rank>(key_of(v)) << 32 | ~static_cast<uint32_t>(idx); }
+__device__ __forceinline__ float value_of(Rank r) { return value_of(static_cast<uint32_t>(r >> 32)); }
+__device__ __forceinline__ int index_of(Rank r) { return static_cast<int>(~static_cast<uint32_t>(r)); }
+constexpr uint32_t kMinusInfKey = 0x007FFFFFu;
+constexpr Rank kNobody = static_cast<Rank>(kMinusInfKey) << 32 | 0xFFFFFFFFu;   // only logits above -inf are better
 
-// A wave's k best, sorted, one a lane: key INT_MIN where there are fewer.
+// The best of a row so far: what passes the bar is put in `buf` in any order; when that
+// fills up, the k best of it stay and the last of them is the new bar.
+constexpr int kRoom = 1024;
 struct Best {
-  int key = INT_MIN, idx = -1;
-  int bar = kMinusInfKey;   // only keys above it enter (uniform): nothing that has no probability
-  float barf = -INFINITY;
+  Rank buf[kRoom + 2], best[kLogpMaxTop];
+  Rank bar;
+  int count;
 
-  __device__ __forceinline__ void raise(int to) {
-    if (to > bar) {
-      bar = to;
-      barf = value_of(to);
-    }
-  }
-  // The k-th largest of the lanes' values is no larger than the k-th of all: what lies below never enters.
-  __device__ __forceinline__ void start(float lane_max, int k) {
-    const int mine = key_of(lane_max), lane = threadIdx.x & (kWave - 1);
-    int rank = 0;
+  // best[0..min(n, k)) of buf[0..n), by counting what is better; all threads call it.
+  __device__ __forceinline__ void select(int n, int k) {
+    if (threadIdx.x < 2) buf[n + threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const Rank mine = buf[i];
+      int at = 0;
 #pragma unroll 8
-    for (int i = 0; i < kWave; ++i) {
-      const int other = __builtin_amdgcn_readlane(mine, i);
-      rank += other > mine || (other == mine && i < lane);
+      for (int j = 0; j < n; j += 2) at += (buf[j] > mine) + (buf[j + 1] > mine);
+      if (at < k) best[at] = mine;
     }
-    const int at = __ffsll(__ballot(rank == k - 1)) - 1;
-    const int kth = __builtin_amdgcn_readlane(mine, at);
-    if (kth > kMinusInfKey) raise(kth - 1 - (kth == 0));   // below 0 comes the smallest number below it, not -0
+    __syncthreads();
   }
-  // (key, idx) uniform, key above the bar; equal keys come in the order of their index
-  __device__ __forceinline__ void insert(int k, int nkey, int nidx) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int pos = __popcll(__ballot(key >= nkey));
-    const int up = __shfl_up(key, 1, kWave), upi = __shfl_up(idx, 1, kWave);
-    key = lane < pos ? key : lane == pos ? nkey : up;
-    idx = lane < pos ? idx : lane == pos ? nidx : upi;
-    raise(__builtin_amdgcn_readlane(key, k - 1));
+  __device__ __forceinline__ void keep(int n, int k) {
+    select(n, k);
+    if (threadIdx.x < k && threadIdx.x < n) buf[threadIdx.x] = best[threadIdx.x];
+    if (threadIdx.x == 0) {
+      count = n < k ? n : k;
+      if (n >= k) bar = best[k - 1];
+    }
+    __syncthreads();
+  }
+  // The k-th largest of 64 values, each the largest of four threads', is no larger than
+  // the k-th of all.
+  __device__ __forceinline__ void start(float thread_max, int k) {
+    float* all = reinterpret_cast<float*>(buf);
+    all[threadIdx.x] = thread_max;
+    if (threadIdx.x == 0) count = 0;
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+      float most = all[threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) most = fmaxf(most, all[w * kWave + threadIdx.x]);
+      const uint32_t mine = key_of(most);
+      int at = 0;
+#pragma unroll 8
+      for (int j = 0; j < kWave; ++j) {
+        const uint32_t other = __builtin_amdgcn_readlane(mine, j) + (j < static_cast<int>(threadIdx.x));   // ties: the lower lane first
+        at += other > mine;
+      }
+      if (at == k - 1) bar = most > -INFINITY ? (static_cast<Rank>(mine) << 32) - 1 : kNobody;
+    }
+    __syncthreads();
   }
 };
 
@@ -111,10 +137,7 @@ __device__ __forceinline__ RowOut finish(const LogpLaunch& A, long long row, con
     const long long id = id_at(A.ids, static_cast<uint32_t>(row));
     float v = 0.0f;
     if (id >= 0 && id < A.vocab) {
-      const T x = static_cast<const T*>(A.x)[row * A.ldx + id];
-      float f;
-      if constexpr (sizeof(T) == 2) f = bf16_to_f32(x);
-      else f = x;
+      const float f = element(static_cast<const T*>(A.x)[row * A.ldx + id]);
       v = o.none ? -INFINITY : (f - o.m) * A.scale - o.logsum;
     }
     A.logp[row] = v;
@@ -122,35 +145,21 @@ __device__ __forceinline__ RowOut finish(const LogpLaunch& A, long long row, con
   return o;
 }
 
-// Threads place the best of `lists` lists of k in LDS (sorted each) by counting what is better.
-template <typename F>
-__device__ __forceinline__ void place(const int* keys, const int* idx, int n, int k, const F& put) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int key = keys[i], at = idx[i];
-    if (key == INT_MIN) continue;
-    int rank = 0;
-    for (int j = 0; j < n; ++j) rank += keys[j] > key || (keys[j] == key && idx[j] < at);
-    if (rank < k) put(rank, key, at);
-  }
-}
-__device__ __forceinline__ void put_top(const LogpLaunch& A, long long row, const RowOut& o, int rank, int key, int at) {
+// The places of a row's list from its n best.
+__device__ __forceinline__ void put_top(const LogpLaunch& A, long long row, const RowOut& o, const Rank* best, int n) {
   const bool lost = o.logsum != o.logsum;   // a NaN or +inf in the row
-  A.top_ids[row * A.top + rank] = lost ? -1 : at;
-  A.top_logp[row * A.top + rank] = (value_of(key) - o.m) * A.scale - o.logsum;
-}
-__device__ __forceinline__ void clear_top(const LogpLaunch& A, long long row, const RowOut& o) {
   for (int i = threadIdx.x; i < A.top; i += kThreads) {
-    A.top_ids[row * A.top + i] = -1;
-    A.top_logp[row * A.top + i] = o.logsum != o.logsum ? o.logsum : -INFINITY;
+    A.top_ids[row * A.top + i] = i < n && !lost ? index_of(best[i]) : -1;
+    A.top_logp[row * A.top + i] = lost ? o.logsum : i < n ? (value_of(best[i]) - o.m) * A.scale - o.logsum : -INFINITY;
   }
 }
 
 template <typename T, bool ENTROPY, bool TOP>
-__global__ void __launch_bounds__(kThreads) logp_kernel(LogpLaunch A) {
+__global__ void __launch_bounds__(kThreads, TOP ? 6 : 8) logp_kernel(LogpLaunch A) {
   using L = Tile<T>;
   __shared__ float wsum[3][kWaves];
   __shared__ RowOut rout;
-  __shared__ int keys[TOP ? kWaves * kLogpMaxTop : 1], idx[TOP ? kWaves * kLogpMaxTop : 1];
+  __shared__ typename std::conditional<TOP, Best, int>::type best;
   const long long blk = block_of_grid();
   const long long row = A.splits == 1 ? blk : blk / A.splits;
   if (row >= A.rows) return;
@@ -164,7 +173,6 @@ __global__ void __launch_bounds__(kThreads) logp_kernel(LogpLaunch A) {
   const int c1 = static_cast<int>(c0 + len < A.vocab ? c0 + len : A.vocab);
   const float c = A.scale * kLog2e;
   Sums sum;
-  Best best;
   for (int b = c0; b < c1; b += L::width) {
     float v[L::U][L::V];
     const int first = b + static_cast<int>(threadIdx.x) * L::V;
@@ -177,10 +185,7 @@ __global__ void __launch_bounds__(kThreads) logp_kernel(LogpLaunch A) {
 #pragma unroll
         for (int e = 0; e < L::V; ++e) {
           v[u][e] = -INFINITY;
-          if (col + e < c1) {
-            if constexpr (sizeof(T) == 2) v[u][e] = bf16_to_f32(x[col + e]);
-            else v[u][e] = x[col + e];
-          }
+          if (col + e < c1) v[u][e] = element(x[col + e]);
         }
       }
     }
@@ -200,23 +205,32 @@ __global__ void __launch_bounds__(kThreads) logp_kernel(LogpLaunch A) {
       }
     if constexpr (TOP) {
       if (b == c0) best.start(top, A.top);
-      if (__ballot(top > best.barf) == 0) continue;
+      // this thread's elements that may enter, by their place in the tile; read again, for they are few
+      uint32_t pending = 0;
+      const float barf = value_of(best.bar);
+      if (top >= barf) {
 #pragma unroll
-      for (int u = 0; u < L::U; ++u) {
-        float most = -INFINITY;
+        for (int u = 0; u < L::U; ++u)
 #pragma unroll
-        for (int e = 0; e < L::V; ++e) most = fmaxf(most, v[u][e]);
-        unsigned long long in;
-        while ((in = __ballot(most > best.barf)) != 0) {
-          const int l = __ffsll(in) - 1;
-#pragma unroll
-          for (int e = 0; e < L::V; ++e) {
-            const int key = key_of(__int_as_float(__builtin_amdgcn_readlane(__float_as_int(v[u][e]), l)));
-            if (key > best.bar && key <= kInfKey)
-              best.insert(A.top, key, b + (u * kThreads + w * kWave + l) * L::V + e);
-          }
-          if (lane == l) most = -INFINITY;
+          for (int e = 0; e < L::V; ++e) pending |= v[u][e] >= barf ? 1u << (u * L::V + e) : 0u;
+      }
+      for (;;) {
+        const Rank bar = best.bar;
+        for (uint32_t left = pending; left != 0; left &= left - 1) {
+          const int i = __ffs(left) - 1, col = first + i / L::V * kThreads * L::V + i % L::V;
+          float f = -INFINITY;
+          if (col < c1) f = element(x[col]);
+          const Rank mine = rank_of(f, col);
+          int at = kRoom;
+          if (mine > bar) at = atomicAdd(&best.count, 1);
+          if (mine > bar && at < kRoom) best.buf[at] = mine;
+          if (mine <= bar || at < kRoom) pending &= ~(left & -left);
         }
+        __syncthreads();
+        const int n = best.count;
+        __syncthreads();   // all have read it before any adds to it
+        if (n > A.top + kWave) best.keep(n < kRoom ? n : kRoom, A.top);
+        if (n <= kRoom) break;   // else: what found no room comes again
       }
     }
   }
@@ -225,12 +239,6 @@ __global__ void __launch_bounds__(kThreads) logp_kernel(LogpLaunch A) {
     wsum[0][w] = sum.m;
     wsum[1][w] = sum.s;
     wsum[2][w] = sum.h;
-  }
-  if constexpr (TOP) {
-    if (lane < A.top) {
-      keys[w * A.top + lane] = best.key;
-      idx[w * A.top + lane] = best.idx;
-    }
   }
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -252,18 +260,12 @@ __global__ void __launch_bounds__(kThreads) logp_kernel(LogpLaunch A) {
     }
   }
   if constexpr (TOP) {
+    const int found = c0 < c1 ? best.count : 0, n = found < A.top ? found : A.top;
+    best.select(found, A.top);
     if (A.splits == 1) {
-      __syncthreads();
-      clear_top(A, row, rout);
-      __syncthreads();
-      place(keys, idx, kWaves * A.top, A.top, [&](int rank, int key, int at) { put_top(A, row, rout, rank, key, at); });
+      put_top(A, row, rout, best.best, n);
     } else {
-      for (int i = threadIdx.x; i < A.top; i += kThreads) A.keys[blk * A.top + i] = INT_MIN;
-      __syncthreads();
-      place(keys, idx, kWaves * A.top, A.top, [&](int rank, int key, int at) {
-        A.keys[blk * A.top + rank] = key;
-        A.idx[blk * A.top + rank] = at;
-      });
+      for (int i = threadIdx.x; i < A.top; i += kThreads) A.ranks[blk * A.top + i] = i < n ? best.best[i] : 0;
     }
   }
 }
@@ -273,15 +275,12 @@ constexpr int kMaxSplits = 32;
 // The rows whose columns several workgroups shared.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) logp_join_kernel(LogpLaunch A) {
-  __shared__ int keys[kMaxSplits * kLogpMaxTop], idx[kMaxSplits * kLogpMaxTop];
+  __shared__ Rank all[kMaxSplits * kLogpMaxTop + 2], best[kLogpMaxTop];
+  __shared__ Rank low;
+  __shared__ int count;
   __shared__ RowOut rout;
   const long long row = block_of_grid();
   if (row >= A.rows) return;
-  const int n = A.splits * A.top;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    keys[i] = A.keys[row * n + i];
-    idx[i] = keys[i] == INT_MIN ? -1 : A.idx[row * n + i];
-  }
   const float c = A.scale * kLog2e;
   if (threadIdx.x < kWave) {
     Sums s;
@@ -292,13 +291,41 @@ __global__ void __launch_bounds__(kThreads) logp_join_kernel(LogpLaunch A) {
       s.h = p[2];
     }
     s.wave_merge<true>(c);
-    if (threadIdx.x == 0) rout = finish<T>(A, row, s);
+    // the splits hold as many as `top` that are no worse than the worst of their (top / splits)-ths
+    if (A.top > 0) {
+      const int nth = (A.top + A.splits - 1) / A.splits;
+      Rank r = threadIdx.x < A.splits ? A.ranks[(row * A.splits + threadIdx.x) * A.top + nth - 1] : ~static_cast<Rank>(0);
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) {
+        const Rank o = __shfl_xor(r, off, kWave);
+        r = o < r ? o : r;
+      }
+      if (threadIdx.x == 0) low = r;
+    }
+    if (threadIdx.x == 0) {
+      count = 0;
+      rout = finish<T>(A, row, s);
+    }
   }
   __syncthreads();
   if (A.top == 0) return;
-  clear_top(A, row, rout);
+  for (int i = threadIdx.x; i < A.splits * A.top; i += kThreads) {
+    const Rank r = A.ranks[row * A.splits * A.top + i];
+    if (r != 0 && r >= low) all[atomicAdd(&count, 1)] = r;
+  }
   __syncthreads();
-  place(keys, idx, n, A.top, [&](int rank, int key, int at) { put_top(A, row, rout, rank, key, at); });
+  const int n = count;
+  if (threadIdx.x < 2) all[n + threadIdx.x] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const Rank mine = all[i];
+    int at = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; j += 2) at += (all[j] > mine) + (all[j + 1] > mine);
+    if (at < A.top) best[at] = mine;
+  }
+  __syncthreads();
+  put_top(A, row, rout, best, n < A.top ? n : A.top);
 }
 
 // A workgroup a tile of a row's columns.
@@ -341,10 +368,7 @@ __global__ void __launch_bounds__(kThreads) logp_grad_kernel(LogpGradLaunch A, u
 #pragma unroll
         for (int e = 0; e < L::V; ++e) {
           v[e] = -INFINITY;
-          if (col + e < A.vocab) {
-            if constexpr (sizeof(T) == 2) v[e] = bf16_to_f32(x[col + e]);
-            else v[e] = x[col + e];
-          }
+          if (col + e < A.vocab) v[e] = element(x[col + e]);
         }
       }
 #pragma unroll
