@@ -22,11 +22,40 @@ constexpr int kThreads = 256, kWaves = kThreads / kWave;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 constexpr float kNever = -256.0f;   // 2^-256 is 0 in float32: a finite exponent in its place
 
-// Loads of a thread in flight: 64 bytes.
-template <typename T>
+// U pieces of 16 bytes a thread.
+template <typename T, int PIECES>
 struct Tile {
-  static constexpr int V = Vec<T>::n, U = 4, n = V * U, width = kThreads * n;
+  static constexpr int V = Vec<T>::n, U = PIECES, width = kThreads * V * U;
 };
+constexpr int kPieces = 4, kGradPieces = 2;
+
+// This thread's pieces of a row's columns [from, from + width), -inf from `end` on.  A
+// tile that ends before it is loaded without a branch, so that its loads go out together.
+template <typename T, int U>
+__device__ __forceinline__ void load_tile(const T* x, int first, int from, int end, float (&v)[U][Vec<T>::n]) {
+  using L = Tile<T, U>;
+  if (end - from >= L::width) {
+    u32x4_t w[L::U];
+#pragma unroll
+    for (int u = 0; u < L::U; ++u) w[u] = *reinterpret_cast<const u32x4_any*>(x + first + u * kThreads * L::V);
+#pragma unroll
+    for (int u = 0; u < L::U; ++u) unpack<T>(w[u], v[u]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < L::U; ++u) {
+      const int col = first + u * kThreads * L::V;
+      if (col + L::V <= end) {
+        unpack<T>(*reinterpret_cast<const u32x4_any*>(x + col), v[u]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < L::V; ++e) {
+          v[u][e] = -INFINITY;
+          if (col + e < end) v[u][e] = element(x[col + e]);
+        }
+      }
+    }
+  }
+}
 
 // A logit and its index as one number: larger is better, ties go to the lowest index
 // (-0 and 0 are one; not for NaN).
@@ -155,8 +184,8 @@ __device__ __forceinline__ void put_top(const LogpLaunch& A, long long row, cons
 }
 
 template <typename T, bool ENTROPY, bool TOP>
-__global__ void __launch_bounds__(kThreads, TOP ? 6 : 8) logp_kernel(LogpLaunch A) {
-  using L = Tile<T>;
+__global__ void __launch_bounds__(kThreads, 8) logp_kernel(LogpLaunch A) {
+  using L = Tile<T, kPieces>;
   __shared__ float wsum[3][kWaves];
   __shared__ RowOut rout;
   __shared__ typename std::conditional<TOP, Best, int>::type best;
@@ -176,19 +205,7 @@ __global__ void __launch_bounds__(kThreads, TOP ? 6 : 8) logp_kernel(LogpLaunch 
   for (int b = c0; b < c1; b += L::width) {
     float v[L::U][L::V];
     const int first = b + static_cast<int>(threadIdx.x) * L::V;
-#pragma unroll
-    for (int u = 0; u < L::U; ++u) {
-      const int col = first + u * kThreads * L::V;
-      if (col + L::V <= c1) {
-        unpack<T>(*reinterpret_cast<const u32x4_any*>(x + col), v[u]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < L::V; ++e) {
-          v[u][e] = -INFINITY;
-          if (col + e < c1) v[u][e] = element(x[col + e]);
-        }
-      }
-    }
+    load_tile(x, first, b, c1, v);
     float top = -INFINITY;
 #pragma unroll
     for (int u = 0; u < L::U; ++u)
@@ -331,11 +348,11 @@ __global__ void __launch_bounds__(kThreads) logp_join_kernel(LogpLaunch A) {
 // A workgroup a tile of a row's columns.
 template <typename T, bool ENTROPY>
 __global__ void __launch_bounds__(kThreads) logp_grad_kernel(LogpGradLaunch A, unsigned tiles) {
-  using L = Tile<T>;
+  using L = Tile<T, kGradPieces>;
   const long long blk = block_of_grid();
   const long long row = blk / tiles;
   if (row >= A.rows) return;
-  const int first = static_cast<int>(blk - row * tiles) * L::width + static_cast<int>(threadIdx.x) * L::V;
+  const int from = static_cast<int>(blk - row * tiles) * L::width, first = from + static_cast<int>(threadIdx.x) * L::V;
   const T* x = static_cast<const T*>(A.x) + row * A.ldx;
   T* dx = static_cast<T*>(A.dx) + row * A.lddx;
   const float m = A.stats[2 * row], logsum = A.stats[2 * row + 1];
@@ -352,46 +369,41 @@ __global__ void __launch_bounds__(kThreads) logp_grad_kernel(LogpGradLaunch A, u
   const float a = -A.scale * (dl + dh * H), b = -A.scale * dh * kLn2;
   // nothing to pass on, or nothing that has a probability
   const bool zero = (dl == 0.0f && dh == 0.0f) || logsum == -INFINITY;
+  float v[L::U][L::V];
+  if (zero) {
+#pragma unroll
+    for (int u = 0; u < L::U; ++u)
+#pragma unroll
+      for (int e = 0; e < L::V; ++e) v[u][e] = 0.0f;
+  } else {
+    load_tile(x, first, from, A.vocab, v);
+    const int at = static_cast<int>(id) - first;   // of the token among this thread's elements
+#pragma unroll
+    for (int u = 0; u < L::U; ++u)
+#pragma unroll
+      for (int e = 0; e < L::V; ++e) {
+        const float t = fmaf(v[u][e] - m, c, -l2), p = __builtin_amdgcn_exp2f(t);
+        v[u][e] = p * (ENTROPY ? fmaf(fmaxf(t, kNever), b, a) : a);
+        if (at == u * kThreads * L::V + e) v[u][e] += A.scale * dl;
+      }
+  }
 #pragma unroll
   for (int u = 0; u < L::U; ++u) {
     const int col = first + u * kThreads * L::V;
-    if (col >= A.vocab) return;
-    const bool whole = col + L::V <= A.vocab;
-    float v[L::V];
-    if (zero) {
-#pragma unroll
-      for (int e = 0; e < L::V; ++e) v[e] = 0.0f;
-    } else {
-      if (whole) {
-        unpack<T>(*reinterpret_cast<const u32x4_any*>(x + col), v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < L::V; ++e) {
-          v[e] = -INFINITY;
-          if (col + e < A.vocab) v[e] = element(x[col + e]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < L::V; ++e) {
-        const float t = fmaf(v[e] - m, c, -l2), p = __builtin_amdgcn_exp2f(t);
-        v[e] = p * (ENTROPY ? fmaf(fmaxf(t, kNever), b, a) : a);
-        if (col + e == id) v[e] += A.scale * dl;
-      }
-    }
-    if (whole) {
+    if (col + L::V <= A.vocab) {
       u32x4_t w;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if constexpr (sizeof(T) == 2) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-        else w[e] = __float_as_uint(v[e]);
+        if constexpr (sizeof(T) == 2) w[e] = pack_bf16x2(v[u][2 * e], v[u][2 * e + 1]);
+        else w[e] = __float_as_uint(v[u][e]);
       }
       *reinterpret_cast<u32x4_any*>(dx + col) = w;
     } else {
 #pragma unroll
       for (int e = 0; e < L::V; ++e)
         if (col + e < A.vocab) {
-          if constexpr (sizeof(T) == 2) dx[col + e] = f32_to_bf16(v[e]);
-          else dx[col + e] = v[e];
+          if constexpr (sizeof(T) == 2) dx[col + e] = f32_to_bf16(v[u][e]);
+          else dx[col + e] = v[u][e];
         }
     }
   }
@@ -414,7 +426,7 @@ hipError_t logp(const LogpLaunch& A, hipStream_t st) {
 }
 template <typename T>
 hipError_t logp_grad(const LogpGradLaunch& A, hipStream_t st) {
-  const unsigned tiles = (static_cast<unsigned>(A.vocab) + Tile<T>::width - 1) / Tile<T>::width;
+  const unsigned tiles = (static_cast<unsigned>(A.vocab) + Tile<T, kGradPieces>::width - 1) / Tile<T, kGradPieces>::width;
   const dim3 grid = grid_of(A.rows * tiles), block(kThreads);
   if (A.dentropy != nullptr) hipLaunchKernelGGL((logp_grad_kernel<T, true>), grid, block, 0, st, A, tiles);
   else hipLaunchKernelGGL((logp_grad_kernel<T, false>), grid, block, 0, st, A, tiles);
@@ -425,7 +437,7 @@ hipError_t logp_grad(const LogpGradLaunch& A, hipStream_t st) {
 
 // Few rows share the chip: workgroups a row, each with half a tile or more.
 int logp_splits(long long rows, int vocab, bool bf16) {
-  const long long half = (bf16 ? Tile<bf16_t>::width : Tile<float>::width) / 2;
+  const long long half = (bf16 ? Tile<bf16_t, kPieces>::width : Tile<float, kPieces>::width) / 2;
   const long long want = rows >= 512 ? 1 : 1024 / (rows < 1 ? 1 : rows), most = vocab / half;
   const long long s = want < most ? want : most;
   return static_cast<int>(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
