@@ -6,22 +6,70 @@
 
 namespace muon {
 
-// Threads that share a group of w channels and the pieces that each takes (0: more
-// than a workgroup holds, or less than a piece): as few threads as hold it, down to
-// eight, so that narrow groups share a wave.
+// Threads that share a group of w channels and the pieces that each takes (no threads:
+// more than a workgroup holds): as few threads as hold it, down to one, so that narrow
+// groups share a wave; tiny: less than a piece, one thread and its elements one by one.
 struct GroupPlan {
   int threads, pieces;
+  bool tiny;
 };
 inline GroupPlan group_plan(int w, int elems) {
-  if (w < elems) return {0, 0};
+  if (w < elems) return {1, 1, true};
   const long long p = (static_cast<long long>(w) + elems - 1) / elems;
-  if (p <= 8) return {8, 1};
-  if (p <= 16) return {16, 1};
-  if (p <= 32) return {16, 2};
-  if (p <= 4 * 64) return {64, static_cast<int>((p + 63) / 64)};
-  if (p <= 4 * 256) return {256, p <= 2 * 256 ? 2 : 4};
-  if (p <= 4 * 512) return {512, 4};
-  return {0, 0};
+  for (int t : {1, 2, 4, 8, 16})
+    if (p <= t) return {t, 1, false};
+  if (p <= 32) return {16, 2, false};
+  if (p <= 4 * 64) return {64, static_cast<int>((p + 63) / 64), false};
+  if (p <= 4 * 256) return {256, p <= 2 * 256 ? 2 : 4, false};
+  if (p <= 4 * 512) return {512, 4, false};
+  return {0, 0, false};
+}
+
+// A Piece, or a tiny group's elements.
+template <typename T, int TPR, bool TINY>
+struct GroupPiece : Piece<T, TPR> {
+  __device__ __forceinline__ GroupPiece(int i, int t, int w) : Piece<T, TPR>(i, t, w) {}
+};
+template <typename T, int TPR>
+struct GroupPiece<T, TPR, true> {
+  static constexpr int V = Vec<T>::n, base = 0;
+  int w;
+  __device__ __forceinline__ GroupPiece(int, int, int w_) : w(w_) {}
+  __device__ __forceinline__ bool counts(int e) const { return e < w; }
+};
+template <typename T, int TPR, bool TINY>
+__device__ __forceinline__ u32x4_t group_raw(const T* row, int i, int t, int w) {
+  if constexpr (!TINY) return load_raw<T, TPR>(row, i, t, w);
+  u32x4_t o = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < Vec<T>::n; ++e)
+    if (e < w) {
+      if constexpr (sizeof(T) == 2) o[e / 2] |= static_cast<uint32_t>(row[e]) << (16 * (e % 2));
+      else o[e] = __float_as_uint(row[e]);
+    }
+  return o;
+}
+template <typename T, int TPR, bool TINY>
+__device__ __forceinline__ void group_param(const float* row, int i, int t, int w, float (&o)[Vec<T>::n]) {
+  if constexpr (!TINY) {
+    load_param<T, TPR>(row, i, t, w, o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < Vec<T>::n; ++e) o[e] = e < w ? row[e] : 0.0f;
+  }
+}
+template <typename T, int TPR, bool TINY>
+__device__ __forceinline__ void group_store(T* row, int i, int t, int w, const float (&v)[Vec<T>::n]) {
+  if constexpr (!TINY) {
+    store_piece<T, TPR>(row, i, t, w, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < Vec<T>::n; ++e)
+      if (e < w) {
+        if constexpr (sizeof(T) == 2) row[e] = f32_to_bf16(v[e]);
+        else row[e] = v[e];
+      }
+  }
 }
 
 constexpr int kGroupThreads = 256;
@@ -34,10 +82,10 @@ constexpr int kDppMirror = 0x140;
 template <int TPR>
 __device__ __forceinline__ float group_total(float v, float* red) {
   if constexpr (TPR <= 16) {
-    v += dpp_f<kDppXor1>(v);
-    v += dpp_f<kDppXor2>(v);
-    v += dpp_f<kDppHalfMirror>(v);
-    if constexpr (TPR == 16) v += dpp_f<kDppMirror>(v);
+    if constexpr (TPR >= 2) v += dpp_f<kDppXor1>(v);
+    if constexpr (TPR >= 4) v += dpp_f<kDppXor2>(v);
+    if constexpr (TPR >= 8) v += dpp_f<kDppHalfMirror>(v);
+    if constexpr (TPR >= 16) v += dpp_f<kDppMirror>(v);
     return v;
   } else if constexpr (TPR == kWave) {
     return wave_total(v);

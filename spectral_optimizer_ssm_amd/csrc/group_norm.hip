@@ -5,14 +5,14 @@
 // mu and r = 1 / sqrt(mean((u - mu)^2) + eps) of each group of w channels of a row,
 // mu = 0 without centering.
 //
-// Bound by memory.  A group is read once into the registers of 8, 16 or 64 threads,
-// or of a workgroup; the variance is taken from the registers around the mean.
+// Bound by memory.  A group is read once into the registers of 1 to 64 threads, or
+// of a workgroup; the variance is taken from the registers around the mean.
 #include "group_norm.cuh"
 
 namespace muon {
 namespace {
 
-template <typename T, NormGate G, int TPR, int PIECES>
+template <typename T, NormGate G, int TPR, int PIECES, bool TINY>
 __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_kernel(GroupNormLaunch A) {
   constexpr int V = Vec<T>::n, kUnits = group_threads<TPR>() / TPR;
   __shared__ float red[group_threads<TPR>() / kWave];
@@ -26,13 +26,13 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_kernel(GroupN
   float v[PIECES][V], a[PIECES][V];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
-    unpack<T>(load_raw<T, TPR>(x, i, t, A.w), v[i]);
-    if constexpr (G != kGateNone) unpack<T>(load_raw<T, TPR>(z, i, t, A.w), a[i]);
+    unpack<T>(group_raw<T, TPR, TINY>(x, i, t, A.w), v[i]);
+    if constexpr (G != kGateNone) unpack<T>(group_raw<T, TPR, TINY>(z, i, t, A.w), a[i]);
   }
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
-    const Piece<T, TPR> p(i, t, A.w);
+    const GroupPiece<T, TPR, TINY> p(i, t, A.w);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if constexpr (G != kGateNone) a[i][e] *= sigmoid<T>(a[i][e]);
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_kernel(GroupN
   float q = 0.0f;
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
-    const Piece<T, TPR> p(i, t, A.w);
+    const GroupPiece<T, TPR, TINY> p(i, t, A.w);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       v[i][e] -= mu;
@@ -61,12 +61,12 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_kernel(GroupN
 #pragma unroll
     for (int e = 0; e < V; ++e) v[i][e] *= r;
     if (A.weight != nullptr) {
-      load_param<T, TPR>(A.weight + c0, i, t, A.w, p);
+      group_param<T, TPR, TINY>(A.weight + c0, i, t, A.w, p);
 #pragma unroll
       for (int e = 0; e < V; ++e) v[i][e] *= p[e];
     }
     if (A.bias != nullptr) {
-      load_param<T, TPR>(A.bias + c0, i, t, A.w, p);
+      group_param<T, TPR, TINY>(A.bias + c0, i, t, A.w, p);
 #pragma unroll
       for (int e = 0; e < V; ++e) v[i][e] += p[e];
     }
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_kernel(GroupN
 #pragma unroll
       for (int e = 0; e < V; ++e) v[i][e] *= sigmoid<T>(v[i][e]);
     }
-    store_piece<T, TPR>(y, i, t, A.w, v[i]);
+    group_store<T, TPR, TINY>(y, i, t, A.w, v[i]);
   }
   if (t == 0) {
     if (A.mean != nullptr) A.mean[unit] = mu;
@@ -86,13 +86,13 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_kernel(GroupN
   }
 }
 
-// Groups of any width, three readings: a wave a group, or a workgroup.
-template <typename T, NormGate G, int TPR>
+// Groups of any width: a workgroup a group, three readings.
+template <typename T, NormGate G>
 __global__ void __launch_bounds__(kGroupThreads) group_norm_any_kernel(GroupNormLaunch A) {
-  constexpr int kUnits = kGroupThreads / TPR;
+  constexpr int TPR = kGroupThreads;
   __shared__ float red[kGroupThreads / kWave];
-  const int t = threadIdx.x % TPR;
-  const long long unit = block_of_grid() * kUnits + threadIdx.x / TPR;
+  const int t = threadIdx.x;
+  const long long unit = block_of_grid();
   if (unit >= static_cast<long long>(A.rows) * A.groups) return;
   const unsigned row = static_cast<unsigned>(unit) / A.groups;
   const int c0 = (static_cast<int>(static_cast<unsigned>(unit) - row * A.groups)) * A.w;
@@ -135,11 +135,11 @@ __global__ void __launch_bounds__(kGroupThreads) group_norm_any_kernel(GroupNorm
   }
 }
 
-template <typename T, NormGate G, int TPR, int PIECES>
+template <typename T, NormGate G, int TPR, int PIECES, bool TINY = false>
 hipError_t run(const GroupNormLaunch& A, hipStream_t st) {
   constexpr int kUnits = group_threads<TPR>() / TPR;
   const long long units = static_cast<long long>(A.rows) * A.groups;
-  hipLaunchKernelGGL((group_norm_kernel<T, G, TPR, PIECES>), grid_of((units + kUnits - 1) / kUnits), dim3(group_threads<TPR>()), 0, st, A);
+  hipLaunchKernelGGL((group_norm_kernel<T, G, TPR, PIECES, TINY>), grid_of((units + kUnits - 1) / kUnits), dim3(group_threads<TPR>()), 0, st, A);
   return hipGetLastError();
 }
 
@@ -147,6 +147,9 @@ template <typename T, NormGate G>
 hipError_t run_any(const GroupNormLaunch& A, hipStream_t st) {
   const GroupPlan p = group_plan(A.w, Vec<T>::n);
   switch (p.threads) {
+    case 1: return p.tiny ? run<T, G, 1, 1, true>(A, st) : run<T, G, 1, 1>(A, st);
+    case 2: return run<T, G, 2, 1>(A, st);
+    case 4: return run<T, G, 4, 1>(A, st);
     case 8: return run<T, G, 8, 1>(A, st);
     case 16: return p.pieces == 1 ? run<T, G, 16, 1>(A, st) : run<T, G, 16, 2>(A, st);
     case 64:
@@ -154,11 +157,7 @@ hipError_t run_any(const GroupNormLaunch& A, hipStream_t st) {
     case 256: return p.pieces == 2 ? run<T, G, 256, 2>(A, st) : run<T, G, 256, 4>(A, st);
     case 512: return run<T, G, 512, 4>(A, st);
   }
-  const long long units = static_cast<long long>(A.rows) * A.groups;
-  if (A.w < Vec<T>::n)
-    hipLaunchKernelGGL((group_norm_any_kernel<T, G, 8>), grid_of((units + kGroupThreads / 8 - 1) / (kGroupThreads / 8)), dim3(kGroupThreads), 0, st, A);
-  else
-    hipLaunchKernelGGL((group_norm_any_kernel<T, G, kGroupThreads>), grid_of(units), dim3(kGroupThreads), 0, st, A);
+  hipLaunchKernelGGL((group_norm_any_kernel<T, G>), grid_of(static_cast<long long>(A.rows) * A.groups), dim3(kGroupThreads), 0, st, A);
   return hipGetLastError();
 }
 

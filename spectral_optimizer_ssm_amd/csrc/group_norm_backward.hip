@@ -10,23 +10,40 @@
 // adds them in fixed order.
 #include "group_norm.cuh"
 
+#include <algorithm>
+
 namespace muon {
 namespace {
 
-// FULL: centered, or the bias's gradient is wanted.  Workgroup (b, g) walks group g
-// of rows b kUnits + 0.., a grid apart, and leaves part[b][2][groups w].
-template <typename T, NormGate G, bool FULL, int TPR, int PIECES>
+// As group_plan, but no thread holds four pieces, whose sums and rows fill its registers.
+GroupPlan grad_plan(int w, int elems) {
+  const long long p = (static_cast<long long>(w) + elems - 1) / elems;
+  if (p <= 3 * 64) return group_plan(w, elems);
+  if (p <= 2 * 256) return {256, p <= 256 ? 1 : 2, false};
+  if (p <= 2 * 512) return {512, 2, false};
+  if (p <= 2 * 1024) return {1024, 2, false};
+  return {0, 0, false};
+}
+
+// FULL: centered, or the bias's gradient is wanted.  Workgroup (b, s) walks `span`
+// adjacent groups, from s span on, of `per` rows at a time, a grid apart (groups that
+// share a wave lie side by side in memory), and leaves part[b][2][groups w].
+template <typename T, NormGate G, bool FULL, int TPR, int PIECES, bool TINY>
 __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_grad_kernel(GroupNormGradLaunch A) {
   constexpr int V = Vec<T>::n, kAll = group_threads<TPR>(), kUnits = kAll / TPR;
   __shared__ float red[kAll / kWave];
   __shared__ float cols[kUnits > 1 ? kUnits * TPR * V : 1];
   const int sub = kUnits == 1 ? 0 : threadIdx.x / TPR, t = threadIdx.x % TPR;
-  const int g = blockIdx.y, c0 = g * A.w;
+  constexpr bool kShared = TPR < kWave;   // groups share a wave
+  const int span = kShared ? A.span : 1, per = kShared ? A.per : kUnits, g0 = blockIdx.y * span;
+  const int up = kShared ? sub / span : sub;   // this unit's row
+  const bool live = !kShared || (up < per && g0 + sub - up * span < A.groups);
+  const int g = kShared ? (live ? g0 + sub - up * span : g0) : g0, c0 = g * A.w;
   const float inv_w = 1.0f / static_cast<float>(A.w);
   float wv[PIECES][V], dw[PIECES][V], db[FULL ? PIECES : 1][V];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
-    if (A.weight != nullptr) load_param<T, TPR>(A.weight + c0, i, t, A.w, wv[i]);
+    if (A.weight != nullptr) group_param<T, TPR, TINY>(A.weight + c0, i, t, A.w, wv[i]);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if (A.weight == nullptr) wv[i][e] = 1.0f;
@@ -42,15 +59,15 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_grad_kernel(G
     const T* dy = static_cast<const T*>(A.dy) + row * A.lddy + c0;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      xn[i] = load_raw<T, TPR>(x, i, t, A.w);
-      gn[i] = load_raw<T, TPR>(dy, i, t, A.w);
-      if constexpr (G != kGateNone) zn[i] = load_raw<T, TPR>(static_cast<const T*>(A.z) + row * A.ldz + c0, i, t, A.w);
+      xn[i] = group_raw<T, TPR, TINY>(x, i, t, A.w);
+      gn[i] = group_raw<T, TPR, TINY>(dy, i, t, A.w);
+      if constexpr (G != kGateNone) zn[i] = group_raw<T, TPR, TINY>(static_cast<const T*>(A.z) + row * A.ldz + c0, i, t, A.w);
     }
     mun = center ? A.mean[row * A.groups + g] : 0.0f;
     rn = A.rstd[row * A.groups + g];
   };
-  const long long step = static_cast<long long>(gridDim.x) * kUnits;
-  long long row = static_cast<long long>(blockIdx.x) * kUnits + sub;
+  const long long step = static_cast<long long>(gridDim.x) * per;
+  long long row = live ? static_cast<long long>(blockIdx.x) * per + up : A.rows;
   if (row < A.rows) load_row(row);
   for (; row < A.rows; row += step) {
     // h: xh;  d: do, then t;  k: what dx and dz take du times (before), the gate's slope times dy (after)
@@ -73,13 +90,13 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_grad_kernel(G
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      const Piece<T, TPR> p(i, t, A.w);
+      const GroupPiece<T, TPR, TINY> p(i, t, A.w);
       float z[V], b[V];
       if constexpr (G != kGateNone) unpack<T>(zr[i], z);
       if (G != kGateBefore) {
 #pragma unroll
         for (int e = 0; e < V; ++e) b[e] = 0.0f;
-        if (A.bias != nullptr) load_param<T, TPR>(A.bias + c0, i, t, A.w, b);
+        if (A.bias != nullptr) group_param<T, TPR, TINY>(A.bias + c0, i, t, A.w, b);
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -101,7 +118,7 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_grad_kernel(G
         if constexpr (FULL) s1 += c;
         s2 = fmaf(c, h[i][e], s2);
       }
-      if constexpr (G == kGateAfter) store_piece<T, TPR>(dz, i, t, A.w, z);
+      if constexpr (G == kGateAfter) group_store<T, TPR, TINY>(dz, i, t, A.w, z);
     }
     asm volatile("" : "+v"(s1), "+v"(s2));   // both summed up before the branch: their terms take no registers across it
     s1 = center ? group_total<TPR>(s1, red) * inv_w : 0.0f;
@@ -121,18 +138,18 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_grad_kernel(G
           x[e] *= d[i][e] * silu_slope(z[e], s);
           d[i][e] *= z[e] * s;
         }
-        store_piece<T, TPR>(dz, i, t, A.w, x);
+        group_store<T, TPR, TINY>(dz, i, t, A.w, x);
       }
-      store_piece<T, TPR>(dx, i, t, A.w, d[i]);
+      group_store<T, TPR, TINY>(dx, i, t, A.w, d[i]);
     }
   }
   const long long n = static_cast<long long>(A.groups) * A.w;
   const auto leave = [&](auto& acc, int k, float* out) {
     if (out == nullptr) return;   // a sum that nobody asked for
-    float* to = (gridDim.x == 1 ? out : A.part + (2LL * blockIdx.x + k) * n) + c0;
+    float* to = (gridDim.x == 1 ? out : A.part + (2LL * blockIdx.x + k) * n) + g0 * A.w;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      const Piece<T, TPR> p(i, t, A.w);
+      const GroupPiece<T, TPR, TINY> p(i, t, A.w);
       if constexpr (kUnits == 1) {
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -143,13 +160,13 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_grad_kernel(G
 #pragma unroll
         for (int e = 0; e < V; ++e) cols[(e * kUnits + sub) * TPR + t] = acc[i][e];
         __syncthreads();
-        for (int j = threadIdx.x; j < TPR * V; j += kAll) {
-          const int e = j / TPR;
-          const Piece<T, TPR> q(i, j % TPR, A.w);
-          float s = 0.0f;
-#pragma unroll 8
-          for (int u = 0; u < kUnits; ++u) s += cols[(e * kUnits + u) * TPR + j % TPR];
-          if (q.counts(e)) to[q.base + e] = s;
+        for (int j = threadIdx.x; j < span * TPR * V; j += kAll) {
+          const int s = kShared ? j / (TPR * V) : 0, e = j / TPR % V;
+          const GroupPiece<T, TPR, TINY> q(i, j % TPR, A.w);
+          float sum = 0.0f;
+#pragma unroll 4
+          for (int u = 0; u < per; ++u) sum += cols[(e * kUnits + u * span + s) * TPR + j % TPR];
+          if (g0 + s < A.groups && q.counts(e)) to[s * A.w + q.base + e] = sum;
         }
       }
     }
@@ -226,28 +243,30 @@ __global__ void __launch_bounds__(kGroupThreads) group_norm_grad_any_kernel(Grou
   }
 }
 
-template <typename T, NormGate G, int TPR, int PIECES>
+template <typename T, NormGate G, int TPR, int PIECES, bool TINY = false>
 hipError_t run(const GroupNormGradLaunch& A, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(A.parts), static_cast<unsigned>(A.groups)), block(group_threads<TPR>());
+  const dim3 grid(static_cast<unsigned>(A.parts), static_cast<unsigned>((A.groups + A.span - 1) / A.span)), block(group_threads<TPR>());
   if (A.mean == nullptr && A.db == nullptr)
-    hipLaunchKernelGGL((group_norm_grad_kernel<T, G, false, TPR, PIECES>), grid, block, 0, st, A);
+    hipLaunchKernelGGL((group_norm_grad_kernel<T, G, false, TPR, PIECES, TINY>), grid, block, 0, st, A);
   else
-    hipLaunchKernelGGL((group_norm_grad_kernel<T, G, true, TPR, PIECES>), grid, block, 0, st, A);
+    hipLaunchKernelGGL((group_norm_grad_kernel<T, G, true, TPR, PIECES, TINY>), grid, block, 0, st, A);
   return hipGetLastError();
 }
 
 template <typename T, NormGate G>
 hipError_t run_any(const GroupNormGradLaunch& A, hipStream_t st) {
-  const GroupPlan p = group_plan(A.w, Vec<T>::n);
+  const GroupPlan p = grad_plan(A.w, Vec<T>::n);
   hipError_t e;
   switch (p.threads) {
+    case 1: e = p.tiny ? run<T, G, 1, 1, true>(A, st) : run<T, G, 1, 1>(A, st); break;
+    case 2: e = run<T, G, 2, 1>(A, st); break;
+    case 4: e = run<T, G, 4, 1>(A, st); break;
     case 8: e = run<T, G, 8, 1>(A, st); break;
     case 16: e = p.pieces == 1 ? run<T, G, 16, 1>(A, st) : run<T, G, 16, 2>(A, st); break;
-    case 64:
-      e = p.pieces == 1 ? run<T, G, 64, 1>(A, st) : p.pieces == 2 ? run<T, G, 64, 2>(A, st) : p.pieces == 3 ? run<T, G, 64, 3>(A, st) : run<T, G, 64, 4>(A, st);
-      break;
-    case 256: e = p.pieces == 2 ? run<T, G, 256, 2>(A, st) : run<T, G, 256, 4>(A, st); break;
-    case 512: e = run<T, G, 512, 4>(A, st); break;
+    case 64: e = p.pieces == 1 ? run<T, G, 64, 1>(A, st) : p.pieces == 2 ? run<T, G, 64, 2>(A, st) : run<T, G, 64, 3>(A, st); break;
+    case 256: e = p.pieces == 1 ? run<T, G, 256, 1>(A, st) : run<T, G, 256, 2>(A, st); break;
+    case 512: e = run<T, G, 512, 2>(A, st); break;
+    case 1024: e = run<T, G, 1024, 2>(A, st); break;
     default:
       hipLaunchKernelGGL((group_norm_grad_any_kernel<T, G>), dim3(static_cast<unsigned>(A.parts), static_cast<unsigned>(A.groups)), dim3(kGroupThreads), 0, st, A);
       e = hipGetLastError();
@@ -263,14 +282,21 @@ hipError_t run_gate(const GroupNormGradLaunch& A, NormGate gate, hipStream_t st)
 
 }  // namespace
 
-// Workgroups for each group of channels: enough to fill the chip, eight rows a
-// thread where there are that many.
-int group_norm_grad_parts(int rows, int groups, int w, bool bf16) {
-  const GroupPlan p = group_plan(w, bf16 ? Vec<bf16_t>::n : Vec<float>::n);
-  const long long units = p.threads == 0 || p.threads >= kGroupThreads ? 1 : kGroupThreads / p.threads;
-  const long long most = p.threads == 512 ? 256 : 512;
-  const long long per = units * (units > 1 ? 8 : 4), want = (rows + per - 1) / per, fill = (most + groups - 1) / groups;
-  return static_cast<int>(want < 1 ? 1 : want > fill ? fill : want);
+// What a workgroup walks, and how many walk the rows of a group: enough to fill the
+// chip, eight rows a unit where there are that many.
+GroupGradPlan group_norm_grad_plan(int rows, int groups, int w, bool bf16) {
+  const GroupPlan p = grad_plan(w, bf16 ? Vec<bf16_t>::n : Vec<float>::n);
+  const int units = p.threads == 0 || p.threads >= kGroupThreads ? 1 : kGroupThreads / p.threads;
+  GroupGradPlan g{1, units, 1};
+  if (p.threads != 0 && p.threads < kWave) {
+    const int spans = (groups + units - 1) / units;
+    g.span = (groups + spans - 1) / spans;
+    g.per = units / g.span;
+  }
+  const long long most = (p.threads >= 512 ? 256 : 512) / ((groups + g.span - 1) / g.span);
+  const long long rows_of = static_cast<long long>(g.per) * (units > 1 ? 8 : 4), want = (rows + rows_of - 1) / rows_of;
+  g.parts = static_cast<int>(std::max(1LL, std::min(want, most)));
+  return g;
 }
 
 hipError_t launch_group_norm_grad(const GroupNormGradLaunch& A, NormGate gate, bool bf16, hipStream_t st) {

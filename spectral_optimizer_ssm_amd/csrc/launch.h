@@ -465,9 +465,13 @@ struct GroupNormGradLaunch {
   const float *mean, *rstd;     // [rows][groups]; mean null: no centering
   float *dw, *db;          // may be null
   float* part;             // [parts][2][groups w]
-  int parts;
+  int parts, span, per;    // see GroupGradPlan
 };
-int group_norm_grad_parts(int rows, int groups, int w, bool bf16);
+// Groups and rows that a workgroup takes at a time, and workgroups that share the rows.
+struct GroupGradPlan {
+  int span, per, parts;
+};
+GroupGradPlan group_norm_grad_plan(int rows, int groups, int w, bool bf16);
 hipError_t launch_group_norm_grad(const GroupNormGradLaunch& A, NormGate gate, bool bf16, hipStream_t st);
 // dw and db (null: not wanted) from part[parts][2][n] (layer_norm.hip).
 hipError_t launch_norm_parts(const float* part, int parts, int n, float* dw, float* db, hipStream_t st);
