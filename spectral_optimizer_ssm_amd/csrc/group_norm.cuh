@@ -94,10 +94,18 @@ __device__ __forceinline__ float group_total(float v, float* red) {
   }
 }
 
-// 1 / (1 + e^-z): with float32 rows e is the full-accuracy one.
+// 1 / (1 + e^-z).  With float32 rows what rounding -z log2(e) loses is put back, so that
+// e^-z is off by a few 2^-24 wherever s is neither 0 nor 1; past +-128 it is.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float z) {
-  const float e = sizeof(T) == 2 ? __expf(-z) : expf(-z);
+  constexpr float kLog2e = 1.44269504088896341f, kLow = 1.92596299e-8f, kLn2 = 0.69314718055994531f;   // log2(e) = kLog2e + kLow
+  float e;
+  if constexpr (sizeof(T) == 2) {
+    e = __builtin_amdgcn_exp2f(-kLog2e * z);
+  } else {
+    const float x = -__builtin_amdgcn_fmed3f(z, -128.0f, 128.0f), t = x * kLog2e;
+    e = __builtin_amdgcn_exp2f(t) * fmaf(fmaf(x, kLow, fmaf(x, kLog2e, -t)), kLn2, 1.0f);
+  }
   return __builtin_amdgcn_rcpf(1.0f + e);
 }
 // d silu(z) / dz from s = sigmoid(z)

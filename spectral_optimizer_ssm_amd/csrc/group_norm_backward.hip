@@ -40,9 +40,15 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_grad_kernel(G
   const bool live = !kShared || (up < per && g0 + sub - up * span < A.groups);
   const int g = kShared ? (live ? g0 + sub - up * span : g0) : g0, c0 = g * A.w;
   const float inv_w = 1.0f / static_cast<float>(A.w);
-  float wv[PIECES][V], dw[PIECES][V], db[FULL ? PIECES : 1][V];
+  // parameters in registers: a load in the loop would wait for the next row's as well
+  float wv[PIECES][V], bv[G == kGateBefore ? 1 : PIECES][V], dw[PIECES][V], db[FULL ? PIECES : 1][V];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
+    if constexpr (G != kGateBefore) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) bv[i][e] = 0.0f;
+      if (A.bias != nullptr) group_param<T, TPR, TINY>(A.bias + c0, i, t, A.w, bv[i]);
+    }
     if (A.weight != nullptr) group_param<T, TPR, TINY>(A.weight + c0, i, t, A.w, wv[i]);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -88,27 +94,28 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_grad_kernel(G
     load_row(row + step < A.rows ? row + step : row);
     T* dz = G == kGateNone ? nullptr : static_cast<T*>(A.dz) + row * A.lddz + c0;
     float s1 = 0.0f, s2 = 0.0f;
+    constexpr bool kKeep = G == kGateBefore && PIECES <= 2;   // there are registers for the gate's sigmoids
+    float sig[kKeep ? PIECES : 1][V];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const GroupPiece<T, TPR, TINY> p(i, t, A.w);
-      float z[V], b[V];
+      float z[V];
       if constexpr (G != kGateNone) unpack<T>(zr[i], z);
-      if (G != kGateBefore) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) b[e] = 0.0f;
-        if (A.bias != nullptr) group_param<T, TPR, TINY>(A.bias + c0, i, t, A.w, b);
-      }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        if constexpr (G == kGateBefore) h[i][e] *= z[e] * sigmoid<T>(z[e]);
+        if constexpr (G == kGateBefore) {
+          const float s = sigmoid<T>(z[e]);
+          h[i][e] *= z[e] * s;
+          if constexpr (kKeep) sig[i][e] = s;
+        }
         h[i][e] = (h[i][e] - mu) * r;
         if constexpr (G == kGateAfter) {
           const float s = sigmoid<T>(z[e]), dy = d[i][e];
           d[i][e] = dy * (z[e] * s);
-          z[e] = dy * fmaf(h[i][e], wv[i][e], b[e]) * silu_slope(z[e], s);
+          z[e] = dy * fmaf(h[i][e], wv[i][e], bv[i][e]) * silu_slope(z[e], s);
         }
         if (G == kGateNone && A.act == kActSilu) {
-          const float o = fmaf(h[i][e], wv[i][e], b[e]);
+          const float o = fmaf(h[i][e], wv[i][e], bv[i][e]);
           d[i][e] *= silu_slope(o, sigmoid<T>(o));
         }
         dw[i][e] = fmaf(d[i][e], h[i][e], dw[i][e]);
@@ -134,7 +141,9 @@ __global__ void __launch_bounds__(group_threads<TPR>()) group_norm_grad_kernel(G
         unpack<T>(zr[i], z);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float s = sigmoid<T>(z[e]);
+          float s;
+          if constexpr (kKeep) s = sig[i][e];
+          else s = sigmoid<T>(z[e]);
           x[e] *= d[i][e] * silu_slope(z[e], s);
           d[i][e] *= z[e] * s;
         }
