@@ -149,7 +149,10 @@ hipError_t run_any(const GroupNormLaunch& A, hipStream_t st) {
   switch (p.threads) {
     case 1: return p.tiny ? run<T, G, 1, 1, true>(A, st) : run<T, G, 1, 1>(A, st);
     case 2: return run<T, G, 2, 1>(A, st);
-    case 4: return run<T, G, 4, 1>(A, st);
+    case 4:
+      if constexpr (sizeof(T) == 2)
+        if (p.pieces == 3) return run<T, G, 4, 3>(A, st);
+      return run<T, G, 4, 1>(A, st);
     case 8: return run<T, G, 8, 1>(A, st);
     case 16: return p.pieces == 1 ? run<T, G, 16, 1>(A, st) : run<T, G, 16, 2>(A, st);
     case 64:

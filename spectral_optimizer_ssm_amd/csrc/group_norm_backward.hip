@@ -269,7 +269,14 @@ hipError_t run_any(const GroupNormGradLaunch& A, hipStream_t st) {
   switch (p.threads) {
     case 1: e = p.tiny ? run<T, G, 1, 1, true>(A, st) : run<T, G, 1, 1>(A, st); break;
     case 2: e = run<T, G, 2, 1>(A, st); break;
-    case 4: e = run<T, G, 4, 1>(A, st); break;
+    case 4:
+      if constexpr (sizeof(T) == 2)
+        if (p.pieces == 3) {
+          e = run<T, G, 4, 3>(A, st);
+          break;
+        }
+      e = run<T, G, 4, 1>(A, st);
+      break;
     case 8: e = run<T, G, 8, 1>(A, st); break;
     case 16: e = p.pieces == 1 ? run<T, G, 16, 1>(A, st) : run<T, G, 16, 2>(A, st); break;
     case 64: e = p.pieces == 1 ? run<T, G, 64, 1>(A, st) : p.pieces == 2 ? run<T, G, 64, 2>(A, st) : run<T, G, 64, 3>(A, st); break;
