@@ -78,7 +78,8 @@ def test_forward(mu, tokens, vocab, n, dtype, table):
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("kind", ["often", "outside", "same", "sorted"])
-@pytest.mark.parametrize("tokens,vocab,n", [(1, 1, 1), (15, 3, 5), (16, 2, 8), (17, 100, 515), (48, 2, 16), (64, 1, 768), (1000, 257, 96),
+@pytest.mark.parametrize("tokens,vocab,n", [(1, 1, 1), (15, 3, 5), (16, 2, 8), (17, 100, 515), (48, 2, 16), (64, 1, 768), (128, 9, 20), (129, 9, 20),
+                                            (144, 2, 24), (1000, 257, 96),
                                             (3000, 5, 12), (5000, 70001, 8), (4097, 600, 33)])
 def test_gradient(mu, tokens, vocab, n, kind, dtype):
     gen = torch.Generator().manual_seed(tokens + n)
@@ -164,6 +165,27 @@ def test_padding_is_never_read(mu):
     dy[[1, 3, 5]] = float("nan")
     want, size = ref.embedding_grad(torch.nan_to_num(dy), ids, 12)
     close(mu.muon_embedding_backward(dy.cuda(), ids.cuda(), 12), want, size, 8, F32)
+
+
+@pytest.mark.parametrize("table", [BF16, F32], ids=["tbf16", "tf32"])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [3, 128, 200, 1500])
+def test_nothing_outside_the_table_is_written(mu, tokens, dtype, table):
+    """Rows narrower than a piece, of a piece and a little wider, between guards."""
+    gen = torch.Generator().manual_seed(tokens)
+    for n in (1, 3, 4, 5, 6, 7, 8, 9, 15, 17, 130):
+        vocab = 37
+        ids, dy = make_ids("outside", tokens, vocab, gen), torch.randn(tokens, n, generator=gen).to(dtype)
+        buf = torch.full(((vocab + 8) * n,), 3.0, dtype=table, device="cuda")
+        out = buf[4 * n:-4 * n].view(vocab, n)
+        mu.muon_embedding_backward(dy.cuda(), ids.cuda(), vocab, dtable=out)
+        want, size = ref.embedding_grad(dy, ids, vocab)
+        close(out, want, size, grad_steps(tokens), table)
+        assert (buf[:4 * n] == 3.0).all() and (buf[-4 * n:] == 3.0).all(), n
+        if table is F32:
+            mu.muon_embedding_backward(dy.cuda(), ids.cuda(), vocab, dtable=out, accumulate=True)
+            close(out, 2 * want, 2 * size, grad_steps(tokens) + 1, table)
+            assert (buf[:4 * n] == 3.0).all() and (buf[-4 * n:] == 3.0).all(), n
 
 
 def test_no_tokens(mu):
