@@ -107,7 +107,7 @@ hipError_t embed_any(const EmbedLaunch& A, hipStream_t st) {
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
 constexpr int kRangeBits = 9, kRange = 1 << kRangeBits;   // most ids of a workgroup
-constexpr int kKept = 1024;          // tokens that a wave keeps between its two walks
+constexpr int kKept = 1792;          // tokens that a wave keeps between its two walks (112 KB of LDS)
 constexpr int kFillPerThread = 8;    // 16-byte stores
 
 // Ids of a workgroup: all walk all ids, so not more than half the compute units do, and
@@ -116,6 +116,66 @@ constexpr int kFillPerThread = 8;    // 16-byte stores
 int range_of(int vocab) {
   const int r = (vocab + 127) / 128;
   return r < 1 ? 1 : r > kRange ? kRange : r;
+}
+
+// Tokens of a wave of a workgroup that walks all: an odd number of `unit`s, so that the
+// waves' places are on different channels of the L2.
+__host__ __device__ __forceinline__ uint32_t wave_span(uint32_t tokens, uint32_t unit) {
+  return (((tokens + kSortWaves - 1) / kSortWaves + unit - 1) / unit | 1) * unit;
+}
+
+// Many tokens: their ranges are looked up first, 16 bits a token, with counts by blocks
+// of tokens, so that a workgroup looks at eight tokens a lane at once and need not count
+// those below its range (131,071 tokens of 515: 5 + 34 us instead of 52; 50,000 of 768:
+// 68 us in all instead of 77, but 33,000 of 128: 35 instead of 33).
+constexpr uint32_t kMapUnit = 512;            // tokens that a wave looks at at once
+constexpr uint32_t kMapBlock = 2048;          // tokens of a block
+constexpr int kMapRanges = 1024;              // most ranges
+constexpr uint16_t kNoRange = 0xFFFF;
+
+bool mapped(uint32_t tokens, int vocab) {
+  const int range = range_of(vocab);
+  return tokens > 40u << 10 && tokens <= 1u << 27 && (vocab + range - 1) / range <= kMapRanges;
+}
+
+__global__ void __launch_bounds__(kSortThreads) embed_map_kernel(IdsOperand ids, uint32_t tokens, int vocab, int ranges, IdsOperand by_range,
+                                                                 uint32_t padded, uint16_t* map, int* table) {
+  __shared__ int hist[kMapRanges];
+  for (int i = threadIdx.x; i < ranges; i += kSortThreads) hist[i] = 0;
+  __syncthreads();
+  const uint32_t t0 = blockIdx.x * kMapBlock;
+#pragma unroll
+  for (uint32_t k = 0; k < kMapBlock / kSortThreads; ++k) {
+    const uint32_t t = t0 + k * kSortThreads + threadIdx.x;
+    const long long id = t < tokens ? id_at(ids, t) : -1;
+    uint32_t r = kNoRange;
+    if (id >= 0 && id < vocab) {
+      r = static_cast<uint32_t>(id);   // over the ids of a range (magic 0: one)
+      if (by_range.magic != 0) r = __umulhi(r, by_range.magic) >> by_range.shift;
+      atomicAdd(&hist[r], 1);
+    }
+    if (t < padded) map[t] = static_cast<uint16_t>(r);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < ranges; i += kSortThreads) table[static_cast<long long>(blockIdx.x) * ranges + i] = hist[i];
+}
+
+// What lanes of a wave wrote to LDS before is there for its other lanes.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Inclusive sums over the lanes.
+__device__ __forceinline__ int lanes_prefix(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, kDppShr1, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, kDppShr2, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, kDppShr4, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, kDppShr8, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, kDppBcast15, 0xa, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, kDppBcast31, 0xc, 0xf, false);
+  return v;
 }
 
 // Calls f(token, id) for groups of 64 tokens in order, a token a lane (past `end` with
@@ -179,7 +239,7 @@ __device__ __forceinline__ unsigned long long same_lanes(bool in, int d) {
 }
 
 // Blocks below `sorters`: ids [b range, (b + 1) range).  The others: zeros.
-template <typename TT>
+template <typename TT, bool MAP>
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradLaunch A, int range, int sorters, long long bytes) {
   __shared__ int hist[kSortWaves][kRange];
   __shared__ uint32_t kept[kSortWaves][kKept];   // (token from the wave's first) kRange + id from the range's first
@@ -203,28 +263,74 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradLaunc
   const int lo = static_cast<int>(blk) * range, here = A.vocab - lo < range ? A.vocab - lo : range;
   for (int i = threadIdx.x; i < kSortWaves * kRange; i += kSortThreads) (&hist[0][0])[i] = 0;
   __syncthreads();
-  // this wave's tokens, an odd number of 64: the waves' places are on different channels of the L2
-  const uint32_t span = (((A.tokens + kSortWaves - 1) / kSortWaves + kWave - 1) / kWave | 1) * kWave;
+  const uint32_t span = wave_span(A.tokens, MAP ? kMapUnit : kWave);
   const uint32_t t0 = w * span < A.tokens ? w * span : A.tokens, t1 = A.tokens - t0 < span ? A.tokens : t0 + span;
-  const uint32_t room = span <= 1u << (32 - kRangeBits) ? kKept : 0;
   uint32_t below = 0, found = 0;   // uniform
-  walk_ids(A.ids, t0, t1, [&](uint32_t t, int id) {
-    const uint32_t d = static_cast<uint32_t>(id) - lo;
-    below += static_cast<uint32_t>(__popcll(lanes_below(static_cast<uint32_t>(id), static_cast<uint32_t>(lo))));
-    const unsigned long long set = lanes_below(d, static_cast<uint32_t>(here));
-    if (set == 0) return;
-    const uint32_t at = found + static_cast<uint32_t>(__popcll(set & ((1ull << lane) - 1)));
-    if (((set >> lane) & 1) && at < room) kept[w][at] = (t - t0) << kRangeBits | d;
-    found += static_cast<uint32_t>(__popcll(set));
-  });
-  // Calls f(token, in the range, id from its first) for groups of 64 of the wave's tokens.
+  // Calls f(token, in the range, id from its first) for groups of 64 of the list.
+  const auto listed = [&](const auto& f) {
+    wave_fence();
+    for (uint32_t i = 0; i < found; i += kWave) {
+      const bool in = i + lane < found;
+      const uint32_t v = in ? kept[w][i + lane] : 0;
+      f(t0 + (v >> kRangeBits), in, static_cast<int>(v & (kRange - 1)));
+    }
+  };
+  // Fills the list by the map, eight tokens a lane, and calls full() when it is.
+  const auto walk_map = [&](const auto& full) {
+    const auto look_up = [&] {   // the listed tokens' ids
+      constexpr uint32_t G = 4;
+      wave_fence();
+      for (uint32_t i = 0; i < found; i += G * kWave) {
+        uint32_t off[G];
+        int id[G];
+#pragma unroll
+        for (uint32_t g = 0; g < G; ++g) {
+          const uint32_t k = i + g * kWave + lane;
+          off[g] = kept[w][k < found ? k : i];
+          id[g] = static_cast<int>(id_at(A.ids, t0 + off[g]));
+        }
+        wave_fence();
+#pragma unroll
+        for (uint32_t g = 0; g < G; ++g)
+          if (i + g * kWave + lane < found) kept[w][i + g * kWave + lane] = off[g] << kRangeBits | static_cast<uint32_t>(id[g] - lo);
+      }
+    };
+    const uint32_t mine = static_cast<uint32_t>(blk) * 0x10001u;
+    const u32x4_t* map = reinterpret_cast<const u32x4_t*>(A.map + w * span);
+    constexpr uint32_t U = 4;
+    found = 0;
+    for (uint32_t t = 0; t < t1 - t0; t += U * kMapUnit) {
+      u32x4_t m[U];
+#pragma unroll
+      for (uint32_t u = 0; u < U; ++u) m[u] = map[((t + u * kMapUnit < span ? t + u * kMapUnit : 0) / 8) + lane];
+#pragma unroll
+      for (uint32_t u = 0; u < U; ++u) {
+        uint32_t hits = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = m[u][i] ^ mine;
+          hits |= ((x & 0xFFFFu) == 0 ? 1u << (2 * i) : 0u) | (x < 0x10000u ? 2u << (2 * i) : 0u);
+        }
+        if (t + u * kMapUnit >= span) hits = 0;   // (uniform)
+        const int n = __popc(hits), upto = lanes_prefix(n);
+        uint32_t at = found + static_cast<uint32_t>(upto - n);
+        for (; hits != 0; hits &= hits - 1, ++at) kept[w][at] = t + u * kMapUnit + 8 * lane + static_cast<uint32_t>(__ffs(hits) - 1);
+        found += static_cast<uint32_t>(__builtin_amdgcn_readlane(upto, kWave - 1));
+        if (found > kKept - kMapUnit) {
+          look_up();
+          full();
+          found = 0;
+          wave_fence();
+        }
+      }
+    }
+    look_up();
+  };
+  // The same of the ids themselves; the list ends where it is full.
+  const uint32_t room = span <= 1u << (32 - kRangeBits) ? kKept : 0;
   const auto again = [&](const auto& f) {
     if (found <= room) {
-      for (uint32_t i = 0; i < found; i += kWave) {
-        const bool in = i + lane < found;
-        const uint32_t v = in ? kept[w][i + lane] : 0;
-        f(t0 + (v >> kRangeBits), in, static_cast<int>(v & (kRange - 1)));
-      }
+      listed(f);
     } else {
       walk_ids(A.ids, t0, t1, [&](uint32_t t, int id) {
         const uint32_t d = static_cast<uint32_t>(id) - lo;
@@ -233,13 +339,36 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradLaunc
       });
     }
   };
-  __syncthreads();
-  again([&](uint32_t, bool in, int d) {
+  const auto count = [&](uint32_t, bool in, int d) {
     const unsigned long long left = peel(in, d, [&](int of, unsigned long long those, int lead) {
       if (lane == lead) atomicAdd(&hist[w][of], static_cast<int>(__popcll(those)));
     });
     if ((left >> lane) & 1) atomicAdd(&hist[w][d], 1);
-  });
+  };
+  bool whole = true;   // the list holds all of the wave's tokens
+  if constexpr (MAP) {
+    walk_map([&] {
+      listed(count);
+      whole = false;
+    });
+    listed(count);
+    const int blocks = static_cast<int>((A.tokens + kMapBlock - 1) / kMapBlock);
+    int sum = 0;
+    for (int b = w; b < blocks; b += kSortWaves)
+      for (int s = lane; s < static_cast<int>(blk); s += kWave) sum += A.table[static_cast<long long>(b) * sorters + s];
+    below = static_cast<uint32_t>(__builtin_amdgcn_readlane(lanes_prefix(sum), kWave - 1));
+  } else {
+    walk_ids(A.ids, t0, t1, [&](uint32_t t, int id) {
+      const uint32_t d = static_cast<uint32_t>(id) - lo;
+      below += static_cast<uint32_t>(__popcll(lanes_below(static_cast<uint32_t>(id), static_cast<uint32_t>(lo))));
+      const unsigned long long set = lanes_below(d, static_cast<uint32_t>(here));
+      if (set == 0) return;
+      const uint32_t at = found + static_cast<uint32_t>(__popcll(set & ((1ull << lane) - 1)));
+      if (((set >> lane) & 1) && at < room) kept[w][at] = (t - t0) << kRangeBits | d;
+      found += static_cast<uint32_t>(__popcll(set));
+    });
+    again(count);
+  }
   if (lane == 0) waves[w] = static_cast<int>(below);
   __syncthreads();
   int base = 0;   // of the range in the sorted order
@@ -270,14 +399,20 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(EmbedGradLaunc
   }
   __syncthreads();
   // the tokens to their places: those of one id in the lanes' order
-  again([&](uint32_t t, bool in, int d) {
+  const auto drop = [&](uint32_t t, bool in, int d) {
     const unsigned long long same = same_lanes(in, d);
     const int lead = in ? __ffsll(same) - 1 : 0;
     int at = 0;
     if (in && lane == lead) at = atomicAdd(&hist[w][d], static_cast<int>(__popcll(same)));
     at = __shfl(at, lead, kWave) + static_cast<int>(__popcll(same & ((1ull << lane) - 1)));
     if (in) A.sorted[at] = make_int2(static_cast<int>(t), lo + d);
-  });
+  };
+  if constexpr (MAP) {
+    if (!whole) walk_map([&] { listed(drop); });
+    listed(drop);
+  } else {
+    again(drop);
+  }
 }
 
 // V columns of a row from their sum, of which those from `first` on are this thread's
@@ -478,9 +613,7 @@ __global__ void __launch_bounds__(kThreads) embed_few_kernel(EmbedGradLaunch A, 
       for (int c = lane * W; c < A.n; c += kWave * W) store_n<TT, W>(to + (c < A.n - W ? c : A.n - W), zero);
       continue;
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");   // the list is read by the wave's other lanes
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    wave_fence();   // the list is read by the wave's other lanes
     for (int c = lane * V; c < A.n; c += kWave * V) {
       const int base = c < A.n - V ? c : A.n - V;
       const T* dy = static_cast<const T*>(A.dy) + base;
@@ -498,7 +631,7 @@ __global__ void __launch_bounds__(kThreads) embed_few_kernel(EmbedGradLaunch A, 
       }
       put<TT, V>(A, id, base, c - base, acc);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_fence();
   }
 }
 
@@ -531,14 +664,32 @@ hipError_t embed_grad(const EmbedGradLaunch& A, hipStream_t st) {
   const int range = range_of(A.vocab), sorters = (A.vocab + range - 1) / range;
   const long long bytes = A.accumulate ? 0 : static_cast<long long>(A.vocab) * A.n * static_cast<long long>(sizeof(TT));
   const long long fill = (bytes + 16LL * kFillPerThread * kSortThreads - 1) / (16LL * kFillPerThread * kSortThreads);
-  hipLaunchKernelGGL((embed_sort_kernel<TT>), grid_of(sorters + fill), dim3(kSortThreads), 0, st, A, range, sorters, bytes);
-  const hipError_t e = hipGetLastError();
+  const dim3 grid = grid_of(sorters + fill), block(kSortThreads);
+  hipError_t e;
+  if (mapped(A.tokens, A.vocab)) {
+    const uint32_t padded = kSortWaves * wave_span(A.tokens, kMapUnit);
+    hipLaunchKernelGGL(embed_map_kernel, dim3((padded + kMapBlock - 1) / kMapBlock), block, 0, st, A.ids, A.tokens, A.vocab, sorters,
+                       A.by_range, padded, A.map, A.table);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((embed_sort_kernel<TT, true>), grid, block, 0, st, A, range, sorters, bytes);
+  } else {
+    hipLaunchKernelGGL((embed_sort_kernel<TT, false>), grid, block, 0, st, A, range, sorters, bytes);
+  }
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int chunk = embed_grad_chunk(A.tokens);
   return A.n >= V ? sums<T, TT, V>(A, chunk, st) : sums<T, TT, 1>(A, chunk, st);
 }
 
 }  // namespace
+
+EmbedMapSizes embed_map_sizes(uint32_t tokens, int vocab) {
+  if (!mapped(tokens, vocab)) return {0, 0, 1};
+  const int range = range_of(vocab);
+  const size_t padded = static_cast<size_t>(kSortWaves) * wave_span(tokens, kMapUnit), ranges = (vocab + range - 1) / range;
+  return {padded * sizeof(uint16_t), (padded + kMapBlock - 1) / kMapBlock * ranges * sizeof(int), range};
+}
 
 // Sorted tokens of a chunk: 16,384 tokens of 768 take 15 + 7 us (sums and joins) in
 // chunks of 16, 16 + 11 of 8 and 16 + 7 of 32; 131,071 of 515 take 44 + 13 of 32,

@@ -438,7 +438,15 @@ struct EmbedGradLaunch {
   int* count;                // of the tokens inside the table
   int2* sorted;              // those by id, in their order: token, id
   float* part;               // [chunks][2][n]
+  uint16_t* map;             // many tokens: their ranges of ids
+  int* table;                // and how many each block of tokens has of each
+  IdsOperand by_range;       // id / ids of a range, as ids' runs
 };
+struct EmbedMapSizes {
+  size_t map, table;         // bytes
+  int range;                 // ids of a range
+};
+EmbedMapSizes embed_map_sizes(uint32_t tokens, int vocab);   // of no bytes where the map is not used
 int embed_grad_chunk(uint32_t tokens);   // sorted tokens that a thread adds up
 hipError_t launch_embed_grad(const EmbedGradLaunch& A, bool bf16, bool table_bf16, hipStream_t st);
 

@@ -33,6 +33,12 @@ Span ids_span(const muon_ids& a, long long tokens) {
 }
 // t / run as a product: exact for t < 2^31 (with l the bits of run - 1, the factor
 // 2^(31 + l) / run, rounded up, is off by at most run of 2^(31 + l)).
+void divide_by(long long run, IdsOperand* o) {
+  const int l = 64 - __builtin_clzll(static_cast<unsigned long long>(run - 1));   // run > 1
+  o->run = static_cast<uint32_t>(run);
+  o->magic = static_cast<uint32_t>((1ULL << (31 + l)) / static_cast<unsigned long long>(run) + 1);
+  o->shift = l - 1;
+}
 IdsOperand ids_operand(const muon_ids& a, long long tokens) {
   IdsOperand o{};
   o.p = a.p;
@@ -44,10 +50,7 @@ IdsOperand ids_operand(const muon_ids& a, long long tokens) {
     o.step = a.stride;
     return o;
   }
-  const int l = 64 - __builtin_clzll(static_cast<unsigned long long>(a.run - 1));
-  o.run = static_cast<uint32_t>(a.run);
-  o.magic = static_cast<uint32_t>((1ULL << (31 + l)) / static_cast<unsigned long long>(a.run) + 1);
-  o.shift = l - 1;
+  divide_by(a.run, &o);
   return o;
 }
 
@@ -61,15 +64,20 @@ int check_embed(int table_dtype, int dtype, long long tokens, int vocab, int n) 
 }
 
 struct EmbedPlan {
-  size_t sorted, part, end;
+  size_t sorted, part, map, table, end;
+  int range;
 };
-EmbedPlan plan_embed(long long tokens, int n) {
+EmbedPlan plan_embed(long long tokens, int vocab, int n) {
   EmbedPlan p;
   const int chunk = embed_grad_chunk(static_cast<uint32_t>(tokens));
   const size_t chunks = static_cast<size_t>((tokens + chunk - 1) / chunk);
   p.sorted = kAlign;   // behind the count
   p.part = p.sorted + align_up(static_cast<size_t>(tokens) * 8, kAlign);
-  p.end = p.part + align_up(chunks * 2 * n * 4, kAlign);
+  p.map = p.part + align_up(chunks * 2 * n * 4, kAlign);
+  const EmbedMapSizes m = embed_map_sizes(static_cast<uint32_t>(tokens), vocab);
+  p.table = p.map + align_up(m.map, kAlign);
+  p.end = p.table + align_up(m.table, kAlign);
+  p.range = m.range;
   return p;
 }
 
@@ -132,7 +140,7 @@ int muon_embedding(const void* table, int table_dtype, long long ldt, int vocab,
 }
 
 size_t muon_embedding_backward_workspace_size(long long tokens, int vocab, int n) {
-  return check_embed(MUON_F32, MUON_F32, tokens, vocab, n) == MUON_OK ? plan_embed(tokens, n).end : 0;
+  return check_embed(MUON_F32, MUON_F32, tokens, vocab, n) == MUON_OK ? plan_embed(tokens, vocab, n).end : 0;
 }
 
 int muon_embedding_backward(const void* dY, int dtype, long long lddy, const muon_ids* ids, long long tokens, float scale,
@@ -144,7 +152,7 @@ int muon_embedding_backward(const void* dY, int dtype, long long lddy, const muo
   const size_t es = dtype_size(dtype), et = dtype_size(table_dtype), bytes = static_cast<size_t>(vocab) * n * et;
   if (!rows_ok(tokens, n, lddy) || dtable == nullptr || !aligned_to(dtable, et)) return MUON_EINVAL;
   if (tokens > 0 && (dY == nullptr || !aligned_to(dY, es) || !ids_ok(ids, tokens))) return MUON_EINVAL;
-  const EmbedPlan p = plan_embed(tokens, n);
+  const EmbedPlan p = plan_embed(tokens, vocab, n);
   if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < p.end) return MUON_EWORKSPACE;
   if (tokens > 0 ? clash({span(dtable, bytes), span(workspace, p.end)}, {rows_span(dY, tokens, n, lddy, es), ids_span(*ids, tokens)})
                  : clash({span(dtable, bytes), span(workspace, p.end)}, {}))
@@ -158,6 +166,9 @@ int muon_embedding_backward(const void* dY, int dtype, long long lddy, const muo
   A.count = reinterpret_cast<int*>(ws);
   A.sorted = reinterpret_cast<int2*>(ws + p.sorted);
   A.part = reinterpret_cast<float*>(ws + p.part);
+  A.map = reinterpret_cast<uint16_t*>(ws + p.map);
+  A.table = reinterpret_cast<int*>(ws + p.table);
+  if (p.range > 1) divide_by(p.range, &A.by_range);
   return launched(launch_embed_grad(A, dtype == MUON_BF16, table_dtype == MUON_BF16, static_cast<hipStream_t>(stream)));
 }
 

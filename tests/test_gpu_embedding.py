@@ -118,17 +118,23 @@ def test_runs_around_the_borders_of_chunks(mu):
             close(mu.muon_embedding_backward(dy.cuda(), ids[order].cuda(), vocab), want, size, grad_steps(ids.numel()), F32)
 
 
-@pytest.mark.parametrize("kind", ["often", "same", "outside"])
-def test_many_tokens(mu, kind):
-    """Past where chunks are longer; ids of more than one range a workgroup's counters hold."""
+@pytest.mark.parametrize("kind", ["often", "same", "outside", "sorted"])
+@pytest.mark.parametrize("tokens,vocab,n", [(40_960, 3, 8), (40_961, 100, 8), (41_000, 129, 5), (70_001, 66_000, 24), (131_071, 50_280, 3),
+                                            (50_000, 600_000, 1)])
+def test_many_tokens(mu, tokens, vocab, n, kind):
+    """Around where ids are looked up before they are sorted, past where chunks are longer,
+    ranges of one id and more ranges than are counted."""
     gen = torch.Generator().manual_seed(9)
-    tokens, vocab, n = 70_001, 66_000, 24
     ids, dy = make_ids(kind, tokens, vocab, gen), torch.randn(tokens, n, generator=gen).to(BF16)
     want, size = ref.embedding_grad(dy, ids, vocab)
     a = (dy.cuda(), ids.cuda(), vocab)
-    got = mu.muon_embedding_backward(*a)
+    ws = torch.full((mu.muon_embedding_backward_workspace_size(ids, vocab, n),), 255, dtype=torch.uint8, device="cuda")
+    got = mu.muon_embedding_backward(*a, workspace=ws)
     close(got, want, size, grad_steps(tokens), F32)
     assert torch.equal(got, mu.muon_embedding_backward(*a))
+    # every other token of a wider tensor, narrow
+    wide = torch.stack([ids, ids + 1], 1).clamp(-9, 1 << 30).int().cuda()
+    assert torch.equal(got, mu.muon_embedding_backward(dy.cuda(), wide[:, 0], vocab))
 
 
 def test_strides_and_odd_addresses(mu):
