@@ -13,10 +13,11 @@
 //   3. the parts of those ids are added, in order.
 // However often one id occurs, no wave adds more than two chunks.  Measured (bfloat16
 // gradients, a float32 table of 50,280 rows, ids by Zipf's law): 16,384 tokens of 768
-// take 21 + 13 + 7 us, bound by the zeros' 154 MB (7.2 TB/s) and the gathered rows;
-// 131,071 tokens of 515 take 52 + 59 + 15 us: the walk of the ids (37 by itself, vector
-// instructions for the 64 ids of which half of one is the workgroup's), and 240 MB of
-// rows, sums and parts.
+// take 21 + 13 + 6 us, bound by the zeros' 154 MB (7.2 TB/s) and the gathered rows;
+// 131,071 tokens of 515 take 5 (a map of the ids' ranges) + 32 + 59 + 12 us: counting and
+// placing the range of the most frequent id by one workgroup, and 240 MB of rows at odd
+// addresses, sums and parts.  The forward pass of 16,384 tokens takes 10.5 us, 44 MB at
+// 4.2 TB/s.
 #include "launch.h"
 #include "ids.cuh"
 #include "rows.cuh"
@@ -99,7 +100,7 @@ hipError_t embed(const EmbedLaunch& A, hipStream_t st) {
 }
 template <typename TT, typename T>
 hipError_t embed_any(const EmbedLaunch& A, hipStream_t st) {
-  return A.n >= 4 ? embed<TT, T, 4>(A, st) : embed<TT, T, 1>(A, st);
+  return A.n >= 8 ? embed<TT, T, 8>(A, st) : A.n >= 4 ? embed<TT, T, 4>(A, st) : embed<TT, T, 1>(A, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -520,8 +521,9 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedGradLaunch A, 
 }
 
 // The long runs' parts: the lanes look for those that start in the workgroup's chunks,
-// then its waves share each one's parts.
-constexpr int kJoinThreads = 1024, kJoinWaves = kJoinThreads / kWave, kJoinChunks = 16;
+// then its waves share each one's parts (131,071 tokens of 515: 12 us, 15 with 1,024
+// threads for sixteen chunks).
+constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / kWave, kJoinChunks = 4;
 
 template <typename TT, int V>
 __global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(EmbedGradLaunch A, int chunk) {
