@@ -5,8 +5,11 @@
 // mu and r = 1 / sqrt(mean((u - mu)^2) + eps) of each group of w channels of a row,
 // mu = 0 without centering.
 //
-// Bound by memory.  A group is read once into the registers of 1 to 64 threads, or
-// of a workgroup; the variance is taken from the registers around the mean.
+// Bound by memory.  A group is read once into the registers of 1 to 64 threads, or of
+// a workgroup (16,384 bfloat16 or 8,192 float32 channels; wider ones are read three
+// times); the variance is taken from the registers around the mean.  16,384 bfloat16
+// rows of 1,536 with a gate take 28 us (151 MB, 5.3 TB/s), in groups of 8 channels 31,
+// of 75, whose rows lie at odd elements, 40.
 #include "group_norm.cuh"
 
 namespace muon {

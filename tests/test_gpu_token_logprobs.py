@@ -148,7 +148,7 @@ def test_logprobs(mu, vocab, kind, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("rows", [1, 2, 64, 300, 511, 512, 700])
+@pytest.mark.parametrize("rows", [1, 2, 64, 127, 128, 300, 511, 512, 700])
 def test_rows_share_workgroups_or_not(mu, rows, dtype):
     gen = torch.Generator().manual_seed(rows)
     x, ids = make("ties", rows, 20011, dtype, gen), torch.randint(0, 20011, (rows,), generator=gen)
