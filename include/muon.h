@@ -549,7 +549,7 @@ int muon_embedding(const void* table, int table_dtype, long long ldt, int vocab,
  * outside the table are left out, and the rows of dY at them are not read.
  *   dtable  [vocab][n] of table_dtype, contiguous; accumulate 1: added to what is
  *           there (MUON_F32 only), rows of tokens that do not occur untouched
- * Sums are float32 over the tokens in their order, in an order that depends on the
+ * Sums are float32 over the tokens in their order, in parts that depend on the ids and
  * sizes alone; no atomics touch them, so results repeat bit for bit.  The workspace
  * (16-byte aligned) holds the sorted tokens and part sums.  Outputs and workspace
  * must not overlap inputs or each other. */

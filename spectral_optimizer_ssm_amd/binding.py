@@ -1117,7 +1117,8 @@ def _embedding(table, ids, scale, dtype, Y):
 def muon_embedding_backward(dY, ids, vocab, scale=1.0, dtype=None, dtable=None, accumulate=False, workspace=None, stream=None):
     """Gradient of muon_embedding by its table: dtable[v] = scale * the sum of dY[t] over
     the tokens with id v, [vocab, n] of `dtype` (default float32).  dY: of ids' shape and
-    n, rows one stride apart.  dtable: a contiguous tensor to use; with accumulate (then
+    n, rows one stride apart (an expanded one, such as the gradient of Y.sum(), needs
+    .contiguous()).  dtable: a contiguous tensor to use; with accumulate (then
     needed, float32) the sums are added to what it holds.  workspace: a uint8 tensor of
     at least muon_embedding_backward_workspace_size bytes to use instead of a new one.
     Returns dtable."""

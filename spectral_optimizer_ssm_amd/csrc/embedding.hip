@@ -210,9 +210,8 @@ __device__ __forceinline__ void walk_ids(const IdsOperand& ids, uint32_t from, u
 // Lanes with a < b.
 __device__ __forceinline__ unsigned long long lanes_below(uint32_t a, uint32_t b) { return __builtin_amdgcn_uicmp(a, b, 36); }
 
-// The lanes that hold this lane's number, of those with `in` (of kRangeBits bits): two
-// numbers are most often nearly all (each is passed to `one` with its lanes), the lanes
-// that are left are told apart by `rest`.
+// Calls one(number, lanes, leader) for two of the lanes' numbers among those with `in`,
+// which are most often nearly all, and returns the lanes of the others.
 template <typename F>
 __device__ __forceinline__ unsigned long long peel(bool in, int d, const F& one) {
   unsigned long long left = __ballot(in);
@@ -226,6 +225,8 @@ __device__ __forceinline__ unsigned long long peel(bool in, int d, const F& one)
   }
   return left;
 }
+// The lanes that hold this lane's number (of kRangeBits bits): after two by peel, the
+// others are told apart bit by bit.
 __device__ __forceinline__ unsigned long long same_lanes(bool in, int d) {
   unsigned long long same = 0;
   const unsigned long long left = peel(in, d, [&](int of, unsigned long long those, int) { same = d == of ? those : same; });
