@@ -8,8 +8,8 @@
 // Bound by memory where the gate's exponentials leave it so.  Threads keep the sums of
 // dw and db for their columns in registers over all the rows that they walk, with the
 // next row's loads in flight, and leave them in the workspace, where a second kernel
-// adds them in fixed order: 16,384 bfloat16 rows of 1,536 with a gate take 48 + 5 us
-// (252 MB, 5.2 TB/s), 2,062 float32 rows of 24 groups of 75, centered, 20 + 4.
+// adds them in fixed order: 16,384 bfloat16 rows of 1,536 with a gate take 45 + 5 us
+// (252 MB, 5.6 TB/s), 2,062 float32 rows of 24 groups of 75, centered, 20 + 4.
 #include "group_norm.cuh"
 
 #include <algorithm>
@@ -307,8 +307,11 @@ hipError_t run_gate(const GroupNormGradLaunch& A, NormGate gate, hipStream_t st)
 // walked side by side (65,536 bfloat16 rows of 24 groups of 16: 48 us, 134 if each
 // workgroup walks one group; 24 groups of 64: 49 and 58).  At most 512 workgroups, or 256
 // of 512 threads or more: twice as many leave twice the sums (196,608 rows of 128: 47 and
-// 51 us).
-GroupGradPlan group_norm_grad_plan(int rows, int groups, int w, bool bf16) {
+// 51 us).  Waves that walk three pieces of three tensors have enough in flight alone on
+// their unit (16,384 bfloat16 rows of 1,536 with a gate: 50 us a call with 256 workgroups,
+// 54 with 512; without a gate 40 and 34; two pieces of 1,024 channels 35 either way, of
+// 768 with the gate after 36 and 32).
+GroupGradPlan group_norm_grad_plan(int rows, int groups, int w, bool bf16, bool gated) {
   const GroupPlan p = grad_plan(w, bf16 ? Vec<bf16_t>::n : Vec<float>::n);
   const int units = p.threads == 0 || p.threads >= kGroupThreads ? 1 : kGroupThreads / p.threads;
   GroupGradPlan g{1, units, 1};
@@ -317,7 +320,7 @@ GroupGradPlan group_norm_grad_plan(int rows, int groups, int w, bool bf16) {
     g.span = (groups + spans - 1) / spans;
     g.per = units / g.span;
   }
-  const long long most = (p.threads >= 512 ? 256 : 512) / ((groups + g.span - 1) / g.span);
+  const long long most = (p.threads >= 512 || (p.pieces == 3 && p.threads == kWave && gated) ? 256 : 512) / ((groups + g.span - 1) / g.span);
   const long long rows_of = static_cast<long long>(g.per) * (units > 1 ? 8 : 4), want = (rows + rows_of - 1) / rows_of;
   g.parts = static_cast<int>(std::max(1LL, std::min(want, most)));
   return g;

@@ -479,7 +479,7 @@ struct GroupNormGradLaunch {
 struct GroupGradPlan {
   int span, per, parts;
 };
-GroupGradPlan group_norm_grad_plan(int rows, int groups, int w, bool bf16);
+GroupGradPlan group_norm_grad_plan(int rows, int groups, int w, bool bf16, bool gated);
 hipError_t launch_group_norm_grad(const GroupNormGradLaunch& A, NormGate gate, bool bf16, hipStream_t st);
 // dw and db (null: not wanted) from part[parts][2][n] (layer_norm.hip).
 hipError_t launch_norm_parts(const float* part, int parts, int n, float* dw, float* db, hipStream_t st);

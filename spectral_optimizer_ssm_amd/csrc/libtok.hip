@@ -199,7 +199,7 @@ int muon_group_norm(const void* X, long long ldx, const void* Z, long long ldz, 
 
 size_t muon_group_norm_backward_workspace_size(long long rows, int groups, int width, int dtype) {
   if (check_group_norm(dtype, rows, groups, width) != MUON_OK) return 0;
-  const size_t parts = group_norm_grad_plan(static_cast<int>(rows), groups, width, dtype == MUON_BF16).parts;
+  const size_t parts = group_norm_grad_plan(static_cast<int>(rows), groups, width, dtype == MUON_BF16, false).parts;   // no gate has more
   return align_up(parts * 2 * groups * width * 4, kAlign);
 }
 
@@ -233,7 +233,7 @@ int muon_group_norm_backward(const void* dY, long long lddy, const void* X, long
   A.rows = static_cast<int>(rows); A.groups = groups; A.w = width; A.act = act_of(gate);
   A.weight = weight; A.bias = bias; A.mean = mean; A.rstd = rstd; A.dw = dweight; A.db = dbias;
   A.part = static_cast<float*>(workspace);
-  const GroupGradPlan p = group_norm_grad_plan(A.rows, groups, width, dtype == MUON_BF16);
+  const GroupGradPlan p = group_norm_grad_plan(A.rows, groups, width, dtype == MUON_BF16, gated(gate));
   A.parts = p.parts; A.span = p.span; A.per = p.per;
   return launched(launch_group_norm_grad(A, gate_of(gate), dtype == MUON_BF16, static_cast<hipStream_t>(stream)));
 }
