@@ -200,3 +200,30 @@ def test_leading_dimensions(mu):
     deep = mu.muon_group_norm(*args((2, 3, 4, 128)), gate=z.reshape(2, 3, 4, 128), center=True)
     assert deep[0].shape == (2, 3, 4, 128) and deep[1].shape == deep[2].shape == (2, 3, 4, 2)
     assert all(torch.equal(a.reshape(b.shape), b) for a, b in zip(deep, flat))
+
+
+@pytest.mark.parametrize("dtype,width", [(BF16, 1200), (F32, 700)], ids=["bf16", "f32"])
+@pytest.mark.parametrize("mode", list(MODES))
+def test_more_rows_than_workgroups_take_at_once(mu, mode, dtype, width):
+    """Three pieces a thread, whose workgroups are fewer with a gate."""
+    check(mu, inputs(17_000, width, dtype, seed=2, gated=MODES[mode][0]), 1, mode, True)
+
+
+@pytest.mark.parametrize("rows,groups,width", [(3, 5000, 1), (300, 700, 3), (2, 1500, 9), (1, 600, 70)])
+def test_many_groups(mu, rows, groups, width):
+    check(mu, inputs(rows, groups * width, F32, seed=4), groups, "before", True)
+
+
+@pytest.mark.parametrize("rows,groups,width", [(5, 3, 40), (1500, 2, 300), (700, 1, 9000)])
+def test_one_parameter(mu, rows, groups, width):
+    """A weight or a bias alone: its gradient, and the others', as with both where the other is 1 or 0."""
+    i = {k: cu(v) for k, v in inputs(rows, groups * width, BF16).items()}
+    one, zero = torch.ones_like(i["w"]), torch.zeros_like(i["w"])
+    for center in (True, False):
+        def both(w, b):
+            y, mean, rstd = mu.muon_group_norm(i["x"], groups, w, b, gate=i["z"], gate_first=False, center=center)
+            return y, *mu.muon_group_norm_backward(i["dy"], i["x"], groups, w, b, mean, rstd, gate=i["z"], gate_first=False, center=center)
+        for (w, b), (w2, b2) in (((i["w"], None), (i["w"], zero)), ((None, i["b"]), (one, i["b"])), ((None, None), (one, zero))):
+            got, want = both(w, b), both(w2, b2)
+            assert (got[3] is None) == (w is None) and (got[4] is None) == (b is None)
+            assert all(g is None or torch.equal(g, v) for g, v in zip(got, want))

@@ -227,3 +227,18 @@ def test_no_rows(mu):
     logp, H, stats, top_ids, top_logp = mu.muon_token_logprobs(e, ids, top=3)
     assert logp.shape == (0,) and top_ids.shape == (0, 3)
     assert mu.muon_token_logprobs_backward(e, ids, stats, logp).shape == (0, 50)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 3, 600])
+def test_all_but_the_end_forbidden(mu, rows, dtype):
+    """Nothing to set a bar by at first, then every logit better than all before it."""
+    vocab, first = 40_011, 17_000
+    x = torch.full((rows, vocab), -math.inf)
+    x[:, first:] = torch.linspace(-30.0, 30.0, vocab - first)
+    x = x.to(dtype)
+    ids = torch.full((rows,), vocab - 5)
+    check_forward(mu, x, ids, 1.0, 64)
+    x[:, -40:] = -math.inf
+    x[:, first:first + 30_000] = -math.inf
+    check_forward(mu, x, ids, 1.0, 64)

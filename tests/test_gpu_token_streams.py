@@ -186,3 +186,32 @@ def test_given_workspaces(mu):
         got = mu.muon_group_norm_backward(i["dy"], i["z"], 3, i["w"], None, None, rstd, gate=i["dy"], workspace=ws)
         for a, b in zip(got[:3], want["group_norm_backward"]()):
             assert torch.equal(a, b)
+
+
+def test_two_graphs_share_a_workspace(mu):
+    """Captured with one workspace between them and replayed in turn."""
+    ws = torch.full((8 << 20,), 255, dtype=torch.uint8, device="cuda")
+    sets = [inputs(7), inputs(8)]
+
+    def step(i, **kw):
+        few = mu.muon_token_logprobs(i["x"].reshape(5, -1), top=30, **kw)[1:]
+        dx = mu.muon_group_norm_backward(i["dy"], i["z"], 3, i["w"], None, None, torch.ones(700, 3, device="cuda"), gate=i["dy"], **kw)[:3]
+        return [*few, *dx, mu.muon_embedding_backward(dx[0], i["ids"], 900, **kw)]
+
+    graphs, outs = [], []
+    for i in sets:
+        step(i, workspace=ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step(i, workspace=ws))
+    for seed in range(9, 12):
+        for k, i in enumerate(sets):
+            for name, v in inputs(seed + 10 * k).items():
+                i[name].copy_(v)
+        for g in (*graphs, *graphs[::-1]):
+            g.replay()
+        torch.cuda.synchronize()
+        got = [[t.clone() for t in out] for out in outs]
+        for i, out in zip(sets, got):
+            assert all(torch.equal(a, b) for a, b in zip(out, step(i))), seed
