@@ -199,7 +199,7 @@ int muon_group_norm(const void* X, long long ldx, const void* Z, long long ldz, 
 
 size_t muon_group_norm_backward_workspace_size(long long rows, int groups, int width, int dtype) {
   if (check_group_norm(dtype, rows, groups, width) != MUON_OK) return 0;
-  const size_t parts = group_norm_grad_plan(static_cast<int>(rows), groups, width, dtype == MUON_BF16, false).parts;   // no gate has more
+  const size_t parts = group_norm_grad_plan(static_cast<int>(rows), groups, width, dtype == MUON_BF16, false).parts;   // as many as with a gate, or more
   return align_up(parts * 2 * groups * width * 4, kAlign);
 }
 
