@@ -1034,6 +1034,12 @@ _IDS = struct.Struct("@Pi4xqqq")                            # muon_ids
 MUON_GATE_BEFORE, MUON_GATE_AFTER, MUON_ACT_SILU, MUON_ACT_NONE = 0, 1, 2, 3
 
 
+def _sizes(where, a, b):
+    """Sizes that the library takes as C ints, which would cut longer ones."""
+    if not (-(1 << 31) <= a < 1 << 31 and -(1 << 31) <= b < 1 << 31):
+        raise MuonError(MUON_EUNSUPPORTED, where)
+
+
 def _ids(t, name, index):
     """Packed muon_ids of a tensor of token numbers whose dimensions fold into runs of one stride."""
     if t.dtype is torch.int64:
@@ -1093,6 +1099,7 @@ def _embedding(table, ids, scale, dtype, Y):
     if table.dim() != 2:
         raise ValueError("table must be [vocab, n]")
     vocab, n = table.shape
+    _sizes("muon_embedding", vocab, n)
     code = _type_code(table, "table")
     _where(table, "table", dev)
     packed = _ids(ids, "ids", dev)
@@ -1136,6 +1143,7 @@ def _embedding_backward(dY, ids, vocab, scale, dtype, dtable, accumulate, worksp
     _where(dY, "dY", dev)
     packed = _ids(ids, "ids", dev)
     n, tokens = dY.shape[-1], ids.numel()
+    _sizes("muon_embedding_backward", vocab, n)
     lddy = _rows(dY, "dY")[2]
     if accumulate and dtable is None:
         raise ValueError("accumulate needs the dtable to add to")
@@ -1155,6 +1163,7 @@ def _embedding_backward(dY, ids, vocab, scale, dtype, dtable, accumulate, worksp
 
 def muon_embedding_backward_workspace_size(ids, vocab, n) -> int:
     """Workspace bytes of muon_embedding_backward for these ids."""
+    _sizes("muon_embedding_backward_workspace_size", vocab, n)
     return int(lib().muon_embedding_backward_workspace_size(ids.numel(), vocab, n))
 
 
@@ -1175,6 +1184,7 @@ def _grouped(X, groups, gate, index):
     rows, n, ldx = _rows(X, "X")
     if groups <= 0 or n % groups != 0:
         raise ValueError(f"the groups ({groups}) must divide the channels ({n})")
+    _sizes("muon_group_norm", groups, n)
     if gate is None:
         return code, rows, n // groups, ldx, None, 0
     if gate.shape != X.shape:
@@ -1286,6 +1296,7 @@ def muon_token_logprobs(logits, tokens=None, scale=1.0, entropy=True, top=0, wor
             raise ValueError(f"tokens must be a [{', '.join(map(str, lead))}] tensor")
         packed = _ids(tokens, "tokens", dev)
     rows, vocab, ldx = _rows(logits, "logits")
+    _sizes("muon_token_logprobs", vocab, top)
     need = L.muon_token_logprobs_workspace_size(rows, vocab, code, top)
     if need == 0:
         rc = L.muon_token_logprobs(None, vocab, code, rows, vocab, 1.0, None, None, None, None, top, None, None, None, 0, None)
@@ -1307,6 +1318,7 @@ def muon_token_logprobs_workspace_size(logits, top=0) -> int:
     if torch is None:
         _load_torch()
     vocab = logits.shape[-1]
+    _sizes("muon_token_logprobs_workspace_size", vocab, top)
     return int(lib().muon_token_logprobs_workspace_size(logits.numel() // max(vocab, 1), vocab, _type_code(logits, "logits"), top))
 
 
@@ -1348,6 +1360,7 @@ def _token_logprobs_backward(logits, tokens, stats, dlogprobs, scale, entropy, d
         h = _ptr(entropy)
         dh, sdh = _per_row(dentropy, "dentropy", lead, dev)
     rows, vocab, ldx = _rows(logits, "logits")
+    _sizes("muon_token_logprobs_backward", vocab, 0)
     if dlogits is None:
         dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
         lddx = vocab

@@ -276,3 +276,27 @@ def test_ids_fold(on_cpu, make, want):
     base = torch.arange(t.untyped_storage().nbytes() // 8)
     at = [t.storage_offset() + i // run * stride + i % run * step for i in range(flat.numel())]
     assert torch.equal(base[torch.tensor(at, dtype=torch.long)], base.as_strided(t.shape, t.stride(), t.storage_offset()).reshape(-1))
+
+
+FAR = (1 << 32) + 8   # in 32 bits: 8
+
+
+@pytest.mark.parametrize("call", [
+    lambda m: m.muon_embedding(torch.empty(FAR, 4, device="meta"), I(3)),
+    lambda m: m.muon_embedding(torch.empty(4, FAR, device="meta"), I(1)),
+    lambda m: m.muon_embedding_backward(Z(3, 4), I(3), FAR), lambda m: m.muon_embedding_backward(Z(3, 4), I(3), 4 - (1 << 32)),
+    lambda m: m.muon_embedding_backward(Z(0, FAR), I(0), 4),
+    lambda m: m.muon_embedding_backward_workspace_size(I(3), FAR, 4),
+    lambda m: m.muon_group_norm(Z(0, FAR), 1), lambda m: m.muon_group_norm(Z(0, FAR), FAR),
+    lambda m: m.muon_group_norm_backward(Z(0, FAR), Z(0, FAR), 2, None, None, None, Z(0, 2)),
+    lambda m: m.muon_token_logprobs(Z(0, FAR), I(0)), lambda m: m.muon_token_logprobs(Z(3, 8), I(3), top=FAR),
+    lambda m: m.muon_token_logprobs_workspace_size(Z(3, 8), top=FAR),
+    lambda m: m.muon_token_logprobs_backward(Z(0, FAR), I(0), Z(0, 2), Z(0)),
+])
+def test_sizes_past_32_bits_are_not_cut(on_cpu, call, monkeypatch):
+    """Refused as themselves, never taken for what their low bits say."""
+    B = on_cpu.binding
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    with pytest.raises(on_cpu.MuonError) as e:
+        call(on_cpu)
+    assert e.value.status == B.MUON_EUNSUPPORTED
