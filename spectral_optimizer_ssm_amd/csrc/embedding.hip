@@ -128,7 +128,9 @@ __host__ __device__ __forceinline__ uint32_t wave_span(uint32_t tokens, uint32_t
 // Many tokens: their ranges are looked up first, 16 bits a token, with counts by blocks
 // of tokens, so that a workgroup looks at eight tokens a lane at once and need not count
 // those below its range (131,071 tokens of 515: 5 + 34 us instead of 52; 50,000 of 768:
-// 68 us in all instead of 77, but 33,000 of 128: 35 instead of 33).
+// 68 us in all instead of 77, but 33,000 of 128: 35 instead of 33).  A wave's list holds a
+// token as its place among the wave's, above the kRangeBits of its id: no wave walks more
+// than what those bits hold.
 constexpr uint32_t kMapUnit = 512;            // tokens that a wave looks at at once
 constexpr uint32_t kMapBlock = 2048;          // tokens of a block
 constexpr int kMapRanges = 1024;              // most ranges
@@ -136,7 +138,7 @@ constexpr uint16_t kNoRange = 0xFFFF;
 
 bool mapped(uint32_t tokens, int vocab) {
   const int range = range_of(vocab);
-  return tokens > 40u << 10 && tokens <= 1u << 27 && (vocab + range - 1) / range <= kMapRanges;
+  return tokens > 40u << 10 && wave_span(tokens, kMapUnit) <= 1u << (32 - kRangeBits) && (vocab + range - 1) / range <= kMapRanges;
 }
 
 __global__ void __launch_bounds__(kSortThreads) embed_map_kernel(IdsOperand ids, uint32_t tokens, int vocab, int ranges, IdsOperand by_range,

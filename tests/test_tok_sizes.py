@@ -1,0 +1,35 @@
+"""Where the token operators' plans change with size, seen from the host (no GPU
+needed: nothing is enqueued)."""
+import pytest
+
+from test_tok_abi import mu  # noqa: F401
+
+torch = pytest.importorskip("torch")
+
+
+def up(x):
+    return (x + 255) // 256 * 256
+
+
+def embedding_workspace(tokens, n, ranges):
+    """Bytes of the sorted tokens and the part sums, and with `ranges` of the map of the tokens'
+    ranges (16 bits each for sixteen waves, an odd number of 512 tokens to a wave) and its counts."""
+    chunk = 32 if tokens > 1 << 16 else 16
+    need = 256 + up(tokens * 8) + up((tokens + chunk - 1) // chunk * 2 * n * 4)
+    if ranges:
+        wave = (tokens + 15) // 16
+        padded = 16 * (((wave + 511) // 512) | 1) * 512
+        need += up(padded * 2) + up(padded // 2048 * ranges * 4)
+    return need
+
+
+@pytest.mark.parametrize("tokens,mapped", [(40_960, False), (40_961, True), (131_071, True), (134_209_536, True), (134_209_537, False),
+                                           (134_217_727, False), (134_217_728, False), (134_217_729, False), (1 << 30, False)])
+@pytest.mark.parametrize("vocab,ranges", [(100, 100), (50_280, 128)])
+def test_the_map_of_ranges_holds_its_offsets(mu, tokens, mapped, vocab, ranges):  # noqa: F811
+    """A token is listed as its place among its wave's, in the 23 bits beside those of its id: where a
+    wave walks more than 2^23 tokens, ranges are not looked up first."""
+    wave = (tokens + 15) // 16
+    assert not mapped or (((wave + 511) // 512) | 1) * 512 <= 1 << 23
+    got = mu.lib().muon_embedding_backward_workspace_size(tokens, vocab, 1)
+    assert got == embedding_workspace(tokens, 1, ranges if mapped else 0)
