@@ -44,3 +44,36 @@ def test_where_the_map_of_ranges_ends(mu, tokens):
     tokens no longer fits beside an id."""
     dy, ids, want = signs(tokens, 100, seed=tokens & 7)
     assert torch.equal(mu.muon_embedding_backward(dy, ids, 100), want)
+
+
+@pytest.mark.parametrize("tokens,vocab", [(1 << 30, 3), (1 << 30, 100)])
+def test_most_tokens(mu, tokens, vocab):
+    """Runs of so many chunks that four of them to a workgroup are 2^32 work items."""
+    dy, ids, want = signs(tokens, vocab, seed=vocab)
+    assert torch.equal(mu.muon_embedding_backward(dy, ids, vocab), want)
+
+
+def additions(tokens):
+    """The longest chain of additions to an element: two chunks of sorted tokens, then of the chunks'
+    parts those of one wave in eight, the eight waves' sums and what was there; and the scale."""
+    chunk = 32 if tokens > 1 << 16 else 16
+    return 2 * chunk + -(-(-(-tokens // chunk)) // 8) + 8 + 2
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("n", [257, 515, 1030])
+@pytest.mark.parametrize("tokens", [1000, 50_000, 70_000])
+def test_long_runs_of_wide_rows(mu, tokens, n, dtype):
+    """Parts of several slices of a row's columns, within additions() roundings of 2^-24 of the sum
+    of absolute values: one id, and ids with runs across a few borders."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    dy = torch.rand(tokens, n, generator=gen, device="cuda").add_(0.5).to(dtype)
+    one = torch.full((tokens,), 2, device="cuda")
+    some = torch.randint(-1, tokens // 100, (tokens,), generator=gen, device="cuda")
+    for ids, vocab in ((one, 5), (some, tokens // 100)):
+        want = torch.zeros(vocab + 1, n, dtype=torch.float64, device="cuda").index_add_(0, ids + 1, dy.double())[1:] * 0.75
+        for accumulate in (False, True):
+            got = torch.ones(vocab, n, device="cuda")
+            mu.muon_embedding_backward(dy, ids, vocab, scale=0.75, dtable=got, accumulate=accumulate)
+            sums = want + 1 if accumulate else want
+            assert ((got.double() - sums).abs() <= additions(tokens) * 2.0**-24 * sums).all()
