@@ -474,6 +474,7 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedGradLaunch A, 
   const T* dy = static_cast<const T*>(A.dy) + base;
   float* part = A.part + 2 * c * A.n;
   int id = s[0].y;
+  const int some = s[0].x;   // read in place of tokens past the count, whose rows there need not be
   // whose is the run at the start: this chunk's, the chunk's before (skip) or every chunk's that it touches (open)
   bool open = p0 > 0 && before == id, skip = false;
   if (open && !(p0 > chunk && far == id) && !(p0 + chunk < count && next == id)) {
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedGradLaunch A, 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       ids[u] = s[u].y;
-      load_n<T, V>(dy + static_cast<long long>(q + u < count ? s[u].x : 0) * A.lddy, v[u]);
+      load_n<T, V>(dy + static_cast<long long>(q + u < count ? s[u].x : some) * A.lddy, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) s[u] = at(q + U + u);

@@ -55,7 +55,7 @@ def test_most_tokens(mu, tokens, vocab):
 
 def additions(tokens):
     """The longest chain of additions to an element: two chunks of sorted tokens, then of the chunks'
-    parts those of one wave in eight, the eight waves' sums and what was there; and the scale."""
+    parts those of one wave in eight, the eight waves' sums and what was there; and the scale (more than 128 tokens)."""
     chunk = 32 if tokens > 1 << 16 else 16
     return 2 * chunk + -(-(-(-tokens // chunk)) // 8) + 8 + 2
 
@@ -77,3 +77,21 @@ def test_long_runs_of_wide_rows(mu, tokens, n, dtype):
             mu.muon_embedding_backward(dy, ids, vocab, scale=0.75, dtable=got, accumulate=accumulate)
             sums = want + 1 if accumulate else want
             assert ((got.double() - sums).abs() <= additions(tokens) * 2.0**-24 * sums).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [6, 129, 500, 41_000])
+def test_padding_holds_anything(mu, tokens, dtype):
+    """Rows at padding, the first among them, are NaN, and so are those of ids past the table; the
+    tokens that count do not fill their last chunk.  (Up to 128 tokens one chain may add them all.)"""
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    ids = torch.randint(-3, 40, (tokens,), generator=gen, device="cuda")
+    ids[0], ids[-1] = -1, 31
+    for vocab, n in ((31, 20), (40, 1), (1000, 300)):
+        dy = torch.randn(tokens, n, generator=gen, device="cuda").to(dtype)
+        there = (ids >= 0) & (ids < vocab)
+        dy[~there] = float("nan")
+        want, size = (torch.zeros(vocab, n, dtype=torch.float64, device="cuda").index_add_(0, ids[there], v) for v in
+                      (dy[there].double(), dy[there].double().abs()))
+        got = mu.muon_embedding_backward(dy, ids, vocab)
+        assert ((got.double() - want).abs() <= (additions(tokens) + 128) * 2.0**-24 * size).all()
