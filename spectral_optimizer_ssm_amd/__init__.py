@@ -10,7 +10,7 @@ from .binding import (MUON_BF16, MUON_F32, MUON_NS_ACCUMULATE, MUON_NS_AUTO, MUO
                       muon_gated_scan, muon_gated_scan_backward, muon_gated_scan_step, muon_gated_scan_workspace_size,
                       muon_layer_norm, muon_layer_norm_backward, muon_spectral_diag,
                       muon_embedding, muon_embedding_backward, muon_embedding_backward_workspace_size, muon_group_norm,
-                      muon_group_norm_backward, muon_token_logprobs, muon_token_logprobs_backward,
-                      muon_token_logprobs_workspace_size,
+                      muon_group_norm_backward, muon_group_norm_backward_workspace_size, muon_token_logprobs,
+                      muon_token_logprobs_backward, muon_token_logprobs_workspace_size,
                       muon_ns_workspace_size, muon_step, muon_step_phases, muon_step_workspace_size,
                       muon_version, status_string)

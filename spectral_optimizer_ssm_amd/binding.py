@@ -1234,7 +1234,8 @@ def muon_group_norm_backward(dY, X, groups, weight, bias, mean, rstd, gate=None,
     """Gradients through muon_group_norm from its inputs and the statistics that it
     returned: (dX, dgate, dweight, dbias), None for what the call did not have.  dY's
     rows are one stride apart and do not overlap (an expanded dY, such as the gradient of
-    Y.sum(), needs .contiguous())."""
+    Y.sum(), needs .contiguous()).  workspace: a uint8 tensor of at least
+    muon_group_norm_backward_workspace_size bytes to use instead of a new one."""
     if stream is not None:
         return _on(stream, muon_group_norm_backward, dY, X, groups, weight, bias, mean, rstd, gate=gate, gate_first=gate_first,
                    activation=activation, center=center, workspace=workspace)
@@ -1270,6 +1271,17 @@ def muon_group_norm_backward(dY, X, groups, weight, bias, mean, rstd, gate=None,
                                     _ptr(dbias), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     _check(rc, "muon_group_norm_backward")
     return dX, dgate, dweight, dbias
+
+
+def muon_group_norm_backward_workspace_size(X, groups) -> int:
+    """Workspace bytes of muon_group_norm_backward for X of this shape and dtype (0 where it would refuse them)."""
+    if torch is None:
+        _load_torch()
+    n = X.shape[-1]
+    if groups <= 0 or n % groups != 0:
+        raise ValueError(f"the groups ({groups}) must divide the channels ({n})")
+    _sizes("muon_group_norm_backward_workspace_size", groups, n)
+    return int(lib().muon_group_norm_backward_workspace_size(X.numel() // max(n, 1), groups, n // groups, _type_code(X, "X")))
 
 
 def muon_token_logprobs(logits, tokens=None, scale=1.0, entropy=True, top=0, workspace=None, stream=None):

@@ -33,3 +33,25 @@ def test_the_map_of_ranges_holds_its_offsets(mu, tokens, mapped, vocab, ranges):
     assert not mapped or (((wave + 511) // 512) | 1) * 512 <= 1 << 23
     got = mu.lib().muon_embedding_backward_workspace_size(tokens, vocab, 1)
     assert got == embedding_workspace(tokens, 1, ranges if mapped else 0)
+
+
+@pytest.mark.parametrize("dtype,code", [(torch.bfloat16, 1), (torch.float32, 0)])
+@pytest.mark.parametrize("shape,groups", [((700, 192), 3), ((2, 5, 96), 1), ((96,), 4), ((0, 96), 2), ((16_384, 1536), 1), ((4, 40_002), 1),
+                                          ((2062, 24 * 75), 24)])
+def test_group_norm_backward_workspace(mu, shape, groups, dtype, code):  # noqa: F811
+    """The binding's size is the library's: that of the parts of two sums at least."""
+    X = torch.empty(shape, dtype=dtype)
+    rows, n = X.numel() // shape[-1], shape[-1]
+    got = mu.muon_group_norm_backward_workspace_size(X, groups)
+    assert got == mu.lib().muon_group_norm_backward_workspace_size(rows, groups, n // groups, code) >= 2 * n * 4
+
+
+@pytest.mark.parametrize("call,error", [
+    (lambda m: m.muon_group_norm_backward_workspace_size(torch.empty(3, 8), 3), ValueError),
+    (lambda m: m.muon_group_norm_backward_workspace_size(torch.empty(3, 8), 0), ValueError),
+    (lambda m: m.muon_group_norm_backward_workspace_size(torch.empty(3, 8).half(), 2), TypeError),
+    (lambda m: m.muon_group_norm_backward_workspace_size(torch.empty(0, 1 << 32), 1), RuntimeError),
+])
+def test_group_norm_backward_workspace_refusals(mu, call, error):  # noqa: F811
+    with pytest.raises(error):
+        call(mu)
