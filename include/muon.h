@@ -600,7 +600,8 @@ int muon_group_norm_backward(const void* dY, long long lddy, const void* X, long
  *   L = log sum_j e^{scale (x_j - m)},  log p_j = scale (x_j - m) - L,
  *   H = -sum_j p_j log p_j
  *   X           rows of vocab logits of dtype, ldx elements apart (>= vocab)
- *   scale       > 0, finite (one over the temperature)
+ *   scale       > 0 and below 2.358e38, the largest float32 over log2(e) (one over the
+ *               temperature)
  *   tokens      NULL, or a token a row; one outside [0, vocab) (padding) has log p 0
  *   logprobs    NULL, or float32[rows]: log p of the row's token (tokens needed)
  *   entropy     NULL, or float32[rows]: H

@@ -113,6 +113,8 @@ LogpPlan plan_logp(long long rows, int vocab, int dtype, int top) {
   p.end = std::max(p.ranks + align_up(parts * top * 8, kAlign), kAlign);
   return p;
 }
+// The kernels' exponents are in base 2: their factor has to be finite too.
+bool temper_ok(float scale) { return scale > 0.0f && std::isfinite(scale * 1.44269504f); }
 bool strided_ok(const float* p, long long rows, long long stride) {
   return aligned_to(p, 4) && stride >= 0 && extent_ok({rows - 1}, {stride});
 }
@@ -247,7 +249,7 @@ int muon_token_logprobs(const void* X, long long ldx, int dtype, long long rows,
                         size_t workspace_bytes, void* stream) {
   const int rc = check_logp(dtype, rows, vocab, top);
   if (rc != MUON_OK) return rc;
-  if (!(scale > 0.0f) || !std::isfinite(scale) || !rows_ok(rows, vocab, ldx)) return MUON_EINVAL;
+  if (!temper_ok(scale) || !rows_ok(rows, vocab, ldx)) return MUON_EINVAL;
   if (rows == 0) return MUON_OK;
   const size_t es = dtype_size(dtype), per = static_cast<size_t>(rows) * 4;
   if (X == nullptr || !aligned_to(X, es) || !aligned_to(logprobs, 4) || !aligned_to(entropy, 4) || !aligned_to(stats, 4) ||
@@ -275,7 +277,7 @@ int muon_token_logprobs_backward(const void* X, long long ldx, int dtype, long l
                                  const float* entropy, const float* dentropy, long long sdh, void* dX, long long lddx, void* stream) {
   const int rc = check_logp(dtype, rows, vocab, 0);
   if (rc != MUON_OK) return rc;
-  if (!(scale > 0.0f) || !std::isfinite(scale) || !rows_ok(rows, vocab, ldx) || !rows_ok(rows, vocab, lddx)) return MUON_EINVAL;
+  if (!temper_ok(scale) || !rows_ok(rows, vocab, ldx) || !rows_ok(rows, vocab, lddx)) return MUON_EINVAL;
   if (rows == 0) return MUON_OK;
   const size_t es = dtype_size(dtype), per = static_cast<size_t>(rows) * 4;
   if (X == nullptr || dX == nullptr || stats == nullptr || !aligned_to(X, es) || !aligned_to(dX, es) || !aligned_to(stats, 4) ||

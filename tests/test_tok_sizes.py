@@ -55,3 +55,11 @@ def test_group_norm_backward_workspace(mu, shape, groups, dtype, code):  # noqa:
 def test_group_norm_backward_workspace_refusals(mu, call, error):  # noqa: F811
     with pytest.raises(error):
         call(mu)
+
+
+@pytest.mark.parametrize("scale,status", [(3e38, -1), (2.36e38, -1), (2.35e38, 0), (1e-45, 0)])
+def test_largest_scale(mu, scale, status):  # noqa: F811
+    """Exponents are taken in base 2: past the largest float32 over log2(e) the factor was an infinity, and
+    0 times it, at the largest logit, NaN."""
+    from test_tok_abi import logp, logp_bwd
+    assert logp(mu, rows=0, scale=scale) == status and logp_bwd(mu, rows=0, scale=scale) == status
