@@ -530,14 +530,13 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedGradLaunch A, 
 constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / kWave, kJoinChunks = 4;
 
 template <typename TT, int V>
-__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(EmbedGradLaunch A, int chunk, uint32_t groups, uint32_t slices) {
-  const uint32_t blk = static_cast<uint32_t>(block_of_grid()), slice = blk / groups;   // fewer than 2^26
-  if (slice >= slices) return;
+__global__ void __launch_bounds__(kJoinThreads) embed_join_kernel(EmbedGradLaunch A, int chunk) {
   __shared__ float sums[kJoinWaves][V][kWave];
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-  const int col = (static_cast<int>(slice) * kWave + lane) * V;
+  const int col = (static_cast<int>(blockIdx.z) * kWave + lane) * V;
   const int base = col < A.n - V ? col : A.n - V, first = col - base;
-  const long long c0 = static_cast<long long>(blk - slice * groups) * kJoinChunks;
+  const long long c0 = block_of_grid() * kJoinChunks;
+  if (c0 * chunk >= A.tokens) return;
   const int last = static_cast<int>(A.tokens) - 1;
   const auto id_of = [&](long long p) { return A.sorted[p < 0 ? 0 : p < last ? p : last].y; };
   // the border behind the lane's chunk: spanned, and the one behind it, but not the one before
@@ -660,8 +659,9 @@ hipError_t sums(const EmbedGradLaunch& A, int chunk, hipStream_t st) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || chunks < 3) return e;   // no run spans two borders
   constexpr int W = V < 4 ? V : 4;
-  const uint32_t groups = static_cast<uint32_t>((chunks + kJoinChunks - 1) / kJoinChunks), wide = (A.n + kWave * W - 1) / (kWave * W);
-  hipLaunchKernelGGL((embed_join_kernel<TT, W>), grid_of(static_cast<long long>(groups) * wide), dim3(kJoinThreads), 0, st, A, chunk, groups, wide);
+  dim3 grid = grid_of((chunks + kJoinChunks - 1) / kJoinChunks);
+  grid.z = (A.n + kWave * W - 1) / (kWave * W);   // 2^13 at most
+  hipLaunchKernelGGL((embed_join_kernel<TT, W>), grid, dim3(kJoinThreads), 0, st, A, chunk);
   return hipGetLastError();
 }
 
