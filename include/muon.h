@@ -534,8 +534,8 @@ typedef struct {
 } muon_ids;
 
 /* Token embedding (the tied embedding that "Muon Meets Mamba" leaves to AdamW;
- * Mamba-2 130M: 50,280 rows of 768): Y_t = scale table[id_t], rounded once.  An id
- * outside [0, vocab) (padding) gives a row of zeros.
+ * Mamba-2 130M: 50,280 rows of 768): Y_t = scale table[id_t], the product in float32,
+ * then rounded to dtype.  An id outside [0, vocab) (padding) gives a row of zeros.
  *   table  vocab rows of n elements of table_dtype, ldt elements apart (>= n)
  *   Y      rows of dtype, ldy apart
  * table_dtype and dtype: MUON_F32 or MUON_BF16, in any combination.  tokens and

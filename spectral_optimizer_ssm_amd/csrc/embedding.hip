@@ -14,7 +14,7 @@
 // However often one id occurs, no wave adds more than two chunks.  Measured (bfloat16
 // gradients, a float32 table of 50,280 rows, ids by Zipf's law): 16,384 tokens of 768
 // take 21 + 13 + 6 us, bound by the zeros' 154 MB (7.2 TB/s) and the gathered rows;
-// 131,071 tokens of 515 take 5 (a map of the ids' ranges) + 32 + 59 + 12 us: counting and
+// 131,071 tokens of 515 take 5 (a map of the ids' ranges) + 32 + 59 + 13 us: counting and
 // placing the range of the most frequent id by one workgroup, and 240 MB of rows at odd
 // addresses, sums and parts.  The forward pass of 16,384 tokens takes 10.5 us, 44 MB at
 // 4.2 TB/s.
@@ -127,7 +127,7 @@ __host__ __device__ __forceinline__ uint32_t wave_span(uint32_t tokens, uint32_t
 
 // Many tokens: their ranges are looked up first, 16 bits a token, with counts by blocks
 // of tokens, so that a workgroup looks at eight tokens a lane at once and need not count
-// those below its range (131,071 tokens of 515: 5 + 34 us instead of 52; 50,000 of 768:
+// those below its range (131,071 tokens of 515: 5 + 32 us instead of 52; 50,000 of 768:
 // 68 us in all instead of 77, but 33,000 of 128: 35 instead of 33).  A wave's list holds a
 // token as its place among the wave's, above the kRangeBits of its id: no wave walks more
 // than what those bits hold.
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads) embed_sum_kernel(EmbedGradLaunch A, 
 }
 
 // The long runs' parts: the lanes look for those that start in the workgroup's chunks,
-// then its waves share each one's parts (131,071 tokens of 515: 12 us, 15 with 1,024
+// then its waves share each one's parts (131,071 tokens of 515: 13 us, 15 with 1,024
 // threads for sixteen chunks).
 constexpr int kJoinThreads = 512, kJoinWaves = kJoinThreads / kWave, kJoinChunks = 4;
 
@@ -699,9 +699,9 @@ EmbedMapSizes embed_map_sizes(uint32_t tokens, int vocab) {
   return {padded * sizeof(uint16_t), (padded + kMapBlock - 1) / kMapBlock * ranges * sizeof(int), range};
 }
 
-// Sorted tokens of a chunk: 16,384 tokens of 768 take 15 + 7 us (sums and joins) in
-// chunks of 16, 16 + 11 of 8 and 16 + 7 of 32; 131,071 of 515 take 44 + 13 of 32,
-// 46 + 23 of 16 and 57 + 49 of 8.
+// Sorted tokens of a chunk: 16,384 tokens of 768 take 13 + 6 us (sums and joins) in
+// chunks of 16, 13 + 8 of 8 and 16 + 5 of 32; 131,071 of 515 take 59 + 13 of 32,
+// 61 + 23 of 16 and 71 + 40 of 8.
 int embed_grad_chunk(uint32_t tokens) { return tokens > 1u << 16 ? 32 : 16; }
 
 hipError_t launch_embed(const EmbedLaunch& A, bool table_bf16, bool bf16, hipStream_t st) {

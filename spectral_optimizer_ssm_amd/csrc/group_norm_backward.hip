@@ -308,9 +308,13 @@ hipError_t run_gate(const GroupNormGradLaunch& A, NormGate gate, hipStream_t st)
 // workgroup walks one group; 24 groups of 64: 49 and 58).  At most 512 workgroups, or 256
 // of 512 threads or more: twice as many leave twice the sums (196,608 rows of 128: 47 and
 // 51 us).  Waves that walk three pieces of three tensors have enough in flight alone on
-// their unit (16,384 bfloat16 rows of 1,536 with a gate: 50 us a call with 256 workgroups,
-// 54 with 512; without a gate 40 and 34; two pieces of 1,024 channels 35 either way, of
-// 768 with the gate after 36 and 32).
+// their unit.  With a gate, 256 workgroups and 512, a call in a given workspace: 16,384
+// bfloat16 rows of 1,536 channels 49 and 53 us (gate behind 46 and 48, centered 52 and 58),
+// of 1,032 42 and 45 (40 and 38, 49 and 54), 49,152 of 1,536 141 and 148; 16,384 float32
+// rows of 768 45 and 47, 49,152 140 and 149; 2 to 16 groups of 1,536 5 to 9% less by 256,
+// of 768 float32 6 to 8%; up to 4,096 rows nothing.  Only 16,384 float32 rows of 516 and
+// 600, centered, take more (40 and 37, 42 and 40).  Without a gate 40 and 34; two pieces
+// of 1,024 channels 35 either way, of 768 with the gate after 36 and 32.
 GroupGradPlan group_norm_grad_plan(int rows, int groups, int w, bool bf16, bool gated) {
   const GroupPlan p = grad_plan(w, bf16 ? Vec<bf16_t>::n : Vec<float>::n);
   const int units = p.threads == 0 || p.threads >= kGroupThreads ? 1 : kGroupThreads / p.threads;

@@ -447,7 +447,7 @@ struct EmbedMapSizes {
   int range;                 // ids of a range
 };
 EmbedMapSizes embed_map_sizes(uint32_t tokens, int vocab);   // of no bytes where the map is not used
-int embed_grad_chunk(uint32_t tokens);   // sorted tokens that a thread adds up
+int embed_grad_chunk(uint32_t tokens);   // sorted tokens that a wave adds up, a piece of their columns a lane
 hipError_t launch_embed_grad(const EmbedGradLaunch& A, bool bf16, bool table_bf16, hipStream_t st);
 
 // Group norm (group_norm.hip, group_norm_backward.hip): each group of w channels of a
